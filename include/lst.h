@@ -492,6 +492,143 @@ LST_API lst_status lst_store_step(lst_store* store, void* const* staging, void* 
                                   const lst_adamw_hparams* hparams, int64_t timeout_ms);
 
 /* ------------------------------------------------------------------------
+ * Training operators around the packed blocks: what a step computes before
+ * the update (the embedding block's lookup and gradient, the LM-head block's
+ * loss and gradients, written in the blocks' own formats) and the Muon rule
+ * as another update of the matrices in a block.
+ *
+ * All calls are asynchronous on cuda_stream (null = the legacy default
+ * stream), allocate nothing and keep nothing from one call to the next.
+ * Arguments given by pointer to a struct are read during the call only.
+ * Matrices are device memory with contiguous rows; results are the same on
+ * every run (no atomics on values). Calls that share a workspace must not
+ * overlap on the GPU; a workspace needs no initial contents.
+ * ------------------------------------------------------------------------ */
+typedef enum lst_dtype { LST_BF16 = 0, LST_F32 = 1 } lst_dtype;
+
+/* rows x cols elements; row r starts at data + r * stride elements
+   (stride >= cols). data is aligned to its element. */
+typedef struct lst_matrix {
+  void* data;
+  int64_t rows, cols, stride;
+  int32_t dtype;
+} lst_matrix;
+
+/* count token indices, device memory, signed, 32 or 64 bits each. */
+typedef struct lst_indices {
+  const void* data;
+  int64_t count;
+  int32_t bits;
+} lst_indices;
+
+/* Embedding lookup: out[i] = scale * table[tokens[i]], formed in fp32 and
+   rounded once to out's type. table: vocab x hidden; out: count x hidden,
+   bf16 or fp32 each. A token outside 0..vocab-1 gives a row of NaN (nothing
+   is read). Errors: LST_ERR_INVALID_ARG (null, sizes that do not match,
+   unknown type), LST_ERR_ALIGNMENT (data not aligned to its element),
+   LST_ERR_CUDA. */
+LST_API lst_status lst_embed(const lst_matrix* table, const lst_indices* tokens, const lst_matrix* out, float scale,
+                             void* cuda_stream);
+
+/* Gradient of the lookup: grad[t] = scale * sum of dout[i] over tokens[i] == t,
+   summed in fp32 in order of i within groups of neighbouring occurrences, and
+   rounded once to grad's type; rows of tokens that do not occur become zero.
+   With accumulate, the sums are added to grad (one rounding) and the other
+   rows stay as they are. Tokens outside 0..vocab-1 (a padding index of -1,
+   say) contribute nothing. dout: count x hidden, grad: vocab x hidden, bf16
+   or fp32 each; grad is for instance the embedding tensor's range of a block's
+   G segment. workspace: lst_embed_grad_workspace_bytes() bytes, 256-byte
+   aligned. Errors as lst_embed, plus LST_ERR_INVALID_ARG for a workspace that
+   is too small, count or vocab above 2^30. */
+LST_API int64_t lst_embed_grad_workspace_bytes(int64_t count, int64_t hidden, int64_t vocab);
+LST_API lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* tokens, const lst_matrix* grad,
+                                  float scale, int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                                  void* cuda_stream);
+
+/* Softmax cross entropy of tokens against a vocabulary without the matrix of
+   logits: l = x w^T (x: count x hidden, w: vocab x hidden, both bf16, fp32
+   accumulation), lse_i = log sum_v exp(l_iv), loss_i = lse_i - l_i,targets[i],
+   both fp32 [count]. A target equal to ignore_index has loss 0; any other
+   target outside 0..vocab-1 has loss NaN and no gradient.
+   lst_xent_grad also gives mean (fp32, one value) = the mean loss over the
+   targets that are not ignored, and the gradients of grad_scale * mean:
+     dx = grad_scale/N * (softmax(l) - onehot) w      count x hidden, bf16
+     dw = grad_scale/N * (softmax(l) - onehot)^T x    vocab x hidden, bf16
+   (N = targets not ignored; mean, dx and dw are zero where N = 0; dw is added
+   to what it holds, with one rounding, when accumulate_dw is set). dw is for
+   instance the head's range of a block's G segment. Rows of x whose target is
+   ignored do not reach dw, whatever they hold.
+   The vocabulary is worked through in pieces of as many columns as the
+   workspace holds at 2 bytes per token and column; lst_xent_workspace_bytes
+   gives the size for one piece, at most 1 GiB of them, beyond which the
+   logits of all but one piece are formed twice. A smaller workspace makes
+   smaller pieces; LST_ERR_INVALID_ARG where not even 256 columns fit.
+   workspace: 256-byte aligned. Errors otherwise as lst_embed. */
+LST_API int64_t lst_xent_workspace_bytes(int64_t count, int64_t hidden, int64_t vocab, int32_t with_grad);
+LST_API lst_status lst_xent_loss(const lst_matrix* x, const lst_matrix* w, const lst_indices* targets,
+                                 int64_t ignore_index, float* loss, float* lse, void* workspace,
+                                 int64_t workspace_bytes, void* cuda_stream);
+LST_API lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, const lst_indices* targets,
+                                 int64_t ignore_index, float grad_scale, float* loss, float* lse, float* mean,
+                                 const lst_matrix* dx, const lst_matrix* dw, int32_t accumulate_dw, void* workspace,
+                                 int64_t workspace_bytes, void* cuda_stream);
+
+/* Newton-Schulz orthogonalisation (the update rule of the Muon optimizer):
+   X_0 = U / (|U|_F + eps), then `steps` times X <- a X + (b A + c A^2) X with
+   A = X X^T and (a, b, c) = (3.4445, -4.7750, 2.0315), which takes every
+   singular value of U that is not negligible to about 1 and keeps the singular
+   vectors. Products are formed from fp16 values scaled by powers of two, with
+   fp32 sums; see lst_muon.cu. in[i], out[i]: `count` matrices of one shape;
+   in bf16 or fp32 (all the same), out bf16. A zero matrix gives zero; a matrix
+   with a NaN or infinity, or whose |U|_F overflows fp32, gives values of no
+   meaning for itself only. 1 <= steps <= 20, eps > 0.
+   workspace: lst_orthogonalize_workspace_bytes() bytes, 256-byte aligned; a
+   smaller one is used for fewer matrices at a time, LST_ERR_INVALID_ARG where
+   it does not hold one. Errors otherwise as lst_embed. */
+typedef struct lst_ns_params {
+  int32_t steps;
+  float eps;
+} lst_ns_params;
+LST_API int64_t lst_orthogonalize_workspace_bytes(int32_t count, int64_t rows, int64_t cols);
+LST_API lst_status lst_orthogonalize(int32_t count, const lst_matrix* in, const lst_matrix* out,
+                                     const lst_ns_params* params, void* workspace, int64_t workspace_bytes,
+                                     void* cuda_stream);
+
+/* One Muon step over device-resident blocks. For every matrix it applies to:
+     m = momentum*m + g;  u = g + momentum*m (nesterov) or m;
+     O = lst_orthogonalize of u (ns_steps, eps);
+     w = w*(1 - lr*weight_decay) - lr*s*O,
+     s = rms_scale*sqrt(max(rows, cols)), or sqrt(max(1, rows/cols)) where
+     rms_scale = 0
+   (m and the update in fp32; w is the master in the mixed layout, and W is
+   derived from it; the V segment is neither read nor written). use_muon: host
+   array, one entry per tensor of the layout in its order, nonzero for tensors
+   of two dimensions that take the Muon rule; NULL: every tensor of two
+   dimensions (pass an array to leave embeddings and heads out). The other
+   tensors take lst_adamw_step's update with `adamw`, bit for bit, or are left
+   alone when adamw is NULL. Padding is not touched.
+   workspace: lst_muon_workspace_bytes() bytes, 256-byte aligned; a smaller one
+   means fewer matrices at a time, LST_ERR_INVALID_ARG where the largest does
+   not fit. dev_blocks as in lst_adamw_step. Errors as lst_adamw_step, plus
+   LST_ERR_INVALID_ARG for muon hyperparameters outside their domain (lr,
+   weight_decay finite, 0 <= momentum < 1, rms_scale >= 0, eps > 0,
+   1 <= ns_steps <= 20) or a use_muon entry on a tensor that is not a matrix. */
+typedef struct lst_muon_hparams {
+  float lr, momentum, weight_decay, rms_scale, eps;
+  int32_t nesterov, ns_steps;
+} lst_muon_hparams;
+LST_API int64_t lst_muon_workspace_bytes(const lst_layout* layout);
+LST_API lst_status lst_muon_step(const lst_layout* layout, void* const* dev_blocks, const lst_muon_hparams* muon,
+                                 const lst_adamw_hparams* adamw, const uint8_t* use_muon, void* workspace,
+                                 int64_t workspace_bytes, void* cuda_stream);
+
+/* LST_ERR_TIMEOUT if a wait inside one of the matrix kernels of these
+   operators ran out (2 s) since the last call on the current device: the
+   results of the calls since then are not valid. LST_OK otherwise.
+   Synchronises the device. */
+LST_API lst_status lst_operator_status(void);
+
+/* ------------------------------------------------------------------------
  * Utilities.
  * ------------------------------------------------------------------------ */
 

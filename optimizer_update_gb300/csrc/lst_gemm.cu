@@ -1,0 +1,597 @@
+// Tensor-core products of the training operators: one persistent kernel,
+// instantiated for the operand layouts and epilogues of lst_gemm.h.
+//
+// A CTA pair (cluster of 2, tcgen05 cta_group::2) forms a 256 x 256 tile of
+// C = A * B with fp32 accumulators in tensor memory: each CTA holds 128 rows
+// of the tile, loads its 128 rows of A and its half of B, and the pair's MMAs
+// read both halves of B, so a 64-deep K step costs each SM 32 KB of shared
+// memory instead of the 48 KB a lone CTA would read for the same rows. Per CTA:
+//   warp 0     one thread issues the TMA loads (six 32 KB stages),
+//   warp 1     one thread of the leading CTA issues the MMAs,
+//   warps 2-9  take finished accumulators from tensor memory: two warps per 32
+//              rows, one for each half of the tile's columns.
+// Two accumulators of 256 columns alternate, so the epilogue of a tile runs
+// under the main loop of the next. Tiles are dealt to the pairs in a fixed
+// order: every result is formed by one pair in one order of additions.
+#include "lst_gemm.h"
+
+#include <mutex>
+
+#include "lst_tc.cuh"
+
+namespace lst {
+
+namespace {
+
+constexpr int kTileK = 64;
+constexpr int kStages = 6;
+constexpr int kOperandBytes = 128 * kTileK * 2;   // one CTA's share of A or of B
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kBarriers = 2 * kStages + 4;
+constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 8 * kBarriers + 16;
+constexpr uint32_t kTmemColumns = 512;
+
+__device__ int g_gemm_error;
+
+struct Shape {
+  int32_t m, n;
+  int32_t k_blocks, k_per_split, splits;
+  int32_t tiles_m, tiles_n, tiles;  // tiles: of one matrix and one split
+  int32_t symmetric;
+  int32_t first_tile;
+};
+
+template <class Params>
+struct Args {
+  CUtensorMap a[kGemmMaxProblems], b[kGemmMaxProblems];
+  Shape shape[kGemmMaxProblems];
+  Params epi[kGemmMaxProblems];
+  int32_t count, total_tiles;
+};
+
+struct Tile {
+  int problem, batch, split, tm, tn, kb0, kb1;
+};
+
+// Tiles of a matrix go down groups of 8 tile rows, column by column: the tiles
+// in flight share 8 row panels of A and a few column panels of B, which stay
+// in L2. A symmetric result has the tiles of its upper triangle, row by row.
+template <class Params>
+__device__ __forceinline__ Tile decode(const Args<Params>& g, int t) {
+  Tile r;
+  int p = 0;
+  while (p + 1 < g.count && t >= g.shape[p + 1].first_tile) ++p;
+  const Shape& s = g.shape[p];
+  int i = t - s.first_tile;
+  const int matrix = i / s.tiles;
+  i -= matrix * s.tiles;
+  r.problem = p;
+  r.batch = matrix / s.splits;
+  r.split = matrix - r.batch * s.splits;
+  if (s.symmetric) {
+    int row = 0;
+    while (i >= s.tiles_n - row) {
+      i -= s.tiles_n - row;
+      ++row;
+    }
+    r.tm = row;
+    r.tn = row + i;
+  } else {
+    const int per_group = 8 * s.tiles_n;
+    const int group = i / per_group;
+    const int rows = min(8, s.tiles_m - group * 8);
+    i -= group * per_group;
+    r.tm = group * 8 + i % rows;
+    r.tn = i / rows;
+  }
+  r.kb0 = r.split * s.k_per_split;
+  r.kb1 = min(s.k_blocks, r.kb0 + s.k_per_split);
+  return r;
+}
+
+// ---- epilogues ---------------------------------------------------------------
+// Each warp calls run() with its accumulator address (32 lanes = 32 rows, 128
+// columns); `release` must be called once, by all lanes, when the accumulator
+// has been read.
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ float unpack16(uint16_t u, bool bf16) {
+  return bf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u));
+}
+
+// 32 consecutive 16-bit values of one row, `left` of them inside the matrix.
+__device__ __forceinline__ void store_row32(uint16_t* p, const uint32_t (&w)[16], int left, int vec) {
+  if (left >= 32 && vec >= 16) {
+    if (vec >= 32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + 16 * i), "r"(w[8 * i]),
+                     "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]),
+                     "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
+                     : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < left) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+struct StoreEpilogue {
+  using Params = StoreParams;
+  static __device__ __forceinline__ void store(const Params& e, const Shape& s, const Tile& t, uint16_t* out,
+                                               const uint16_t* c, bool bf16, bool mirror, int row, int col,
+                                               float (&v)[32]) {
+    const int left = s.n - col;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = v[i] * e.alpha;
+    if (c) {
+      const uint16_t* q = c + static_cast<int64_t>(row) * e.ld + col;
+      if (left >= 32 && e.vec >= 16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 u = *reinterpret_cast<const uint4*>(q + 8 * j);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[8 * j + i] = __fmaf_rn(e.beta, unpack16(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))), bf16), v[8 * j + i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < left) v[i] = __fmaf_rn(e.beta, unpack16(q[i], bf16), v[i]);
+      }
+    }
+    if (e.diag != 0.0f) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i == row) v[i] += e.diag;
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack16(v[2 * i], v[2 * i + 1], bf16);
+    if (!e.transposed) store_row32(out + static_cast<int64_t>(row) * e.ld + col, w, left, e.vec);
+    if (e.transposed || mirror) {
+      uint16_t* q = out + static_cast<int64_t>(col) * e.ld + row;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < left) q[static_cast<int64_t>(i) * e.ld] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+  template <class Release>
+  static __device__ __forceinline__ void run(const Params& e, const Shape& s, const Tile& t, int row, int col0,
+                                             uint32_t tmem, Release release) {
+    const bool bf16 = e.bf16 != 0;
+    const bool mirror = s.symmetric && t.tm != t.tn;
+    uint16_t* const out = static_cast<uint16_t*>(e.out) + t.batch * e.batch_stride;
+    const uint16_t* const c = e.c ? static_cast<const uint16_t*>(e.c) + t.batch * e.batch_stride : nullptr;
+#pragma unroll 1
+    for (int chunk = 0; chunk < 4; ++chunk) {
+      const int col = col0 + 32 * chunk;
+      if (col >= s.n) break;
+      float v[32];
+      __syncwarp();
+      tc::tmem_ld32(tmem + 32 * chunk, v);
+      tc::tmem_ld_wait();
+      if (row < s.m) store(e, s, t, out, c, bf16, mirror, row, col, v);
+    }
+    release();
+  }
+};
+
+struct PartialEpilogue {
+  using Params = PartialParams;
+  template <class Release>
+  static __device__ __forceinline__ void run(const Params& e, const Shape& s, const Tile& t, int row, int col0,
+                                             uint32_t tmem, Release release) {
+    float* const out = e.out + t.split * e.split_stride + static_cast<int64_t>(row) * e.ld;
+#pragma unroll 1
+    for (int chunk = 0; chunk < 4; ++chunk) {
+      const int col = col0 + 32 * chunk;
+      if (col >= s.n) break;
+      float v[32];
+      tc::tmem_ld32(tmem + 32 * chunk, v);
+      tc::tmem_ld_wait();
+      if (row < s.m) {
+        // ld is a multiple of 32, so a row's tail may be written past column n
+  #pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float4* p = reinterpret_cast<float4*>(out + col) + j;
+          float4 x = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          if (e.accumulate) {
+            const float4 y = *p;
+            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+          }
+          *p = x;
+        }
+      }
+      __syncwarp();
+    }
+    release();
+  }
+};
+
+// One row's logits of 128 vocabulary entries: their maximum M, the sum of
+// exp(l - M), the target's logit where it is among them, and (for the
+// gradient) q = (M - l) * 2^11 in 16 bits. q keeps l to 2^-12 over the 32
+// below M, where rounding l itself to bf16 would keep a logit of 16 only to
+// 2^-5; an entry further below (a probability under 1e-14 of its group's
+// largest) saturates.
+struct XentEpilogue {
+  using Params = XentParams;
+  template <class Release>
+  static __device__ __forceinline__ void run(const Params& e, const Shape& s, const Tile& t, int row, int col0,
+                                             uint32_t tmem, Release release) {
+    if (col0 >= s.n) {
+      release();
+      return;
+    }
+    float v[128];
+#pragma unroll
+    for (int chunk = 0; chunk < 4; ++chunk) tc::tmem_ld32(tmem + 32 * chunk, v + 32 * chunk);
+    tc::tmem_ld_wait();
+    release();
+    const int left = s.n - col0;
+    const float ninf = __int_as_float(0xff800000);
+    if (left < 128) {
+#pragma unroll
+      for (int i = 0; i < 128; ++i)
+        if (i >= left) v[i] = ninf;
+    }
+    float m4[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll
+    for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], v[i]);
+    const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+    // all -inf: the sum is 0, or NaN where a logit is (max passes over NaN)
+    const float base = top == ninf ? 0.0f : top;
+    float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 128; ++i) s4[i & 3] += tc::exp2_approx((v[i] - base) * 1.4426950408889634f);
+    const bool inside = row < s.m;
+    int64_t target = -1;
+    if (inside) {
+      e.stats[(e.first_group + (col0 >> 7)) * e.stat_ld + row] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+      target = e.index_bytes == 8 ? static_cast<const int64_t*>(e.targets)[row] : static_cast<const int32_t*>(e.targets)[row];
+      target -= e.first_column + col0;
+    }
+    const bool hit = target >= 0 && target < 128 && target < left;
+    if (__any_sync(0xffffffffu, hit)) {
+      float x = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 128; ++i)
+        x += i == static_cast<int>(target) ? v[i] : 0.0f;
+      if (hit) e.target_logit[row] = x;
+    }
+    if (e.q && inside) {
+      uint16_t* const out = e.q + static_cast<int64_t>(row) * e.q_ld + col0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float lo = fminf((top - v[32 * j + 2 * i]) * 2048.0f, 65535.0f);
+          const float hi = fminf((top - v[32 * j + 2 * i + 1]) * 2048.0f, 65535.0f);
+          w[i] = __float2uint_rn(lo) | (__float2uint_rn(hi) << 16);
+        }
+        store_row32(out + 32 * j, w, 32, 32);  // q_ld is a multiple of 128
+      }
+    }
+  }
+};
+
+// ---- the kernel ----------------------------------------------------------------
+template <class Epi, bool kBf16, bool kAMn, bool kBMn>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gemm_kernel(const __grid_constant__ Args<typename Epi::Params> g) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
+  const uint32_t bars = base + kStages * kStageBytes;
+  const uint32_t full = bars, empty = bars + 8 * kStages, tfull = bars + 16 * kStages, tempty = tfull + 16;
+  const uint32_t tmem_slot = tempty + 16;
+  const uint32_t abort_slot = tmem_slot + 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_rank();
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(full + 8 * i, 1);
+      tc::mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tfull + 8 * i, 1);
+      tc::mbar_init(tempty + 8 * i, 2 * kEpiWarps);
+    }
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort_slot), "r"(0) : "memory");
+    tc::mbar_init_fence();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc::tmem_alloc_pair(tmem_slot, kTmemColumns);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after();
+  uint32_t tmem;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
+
+  bool ok = true;
+  if (warp == 0) {
+    if (tc::elect_one()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int t = cluster; t < g.total_tiles && ok; t += clusters) {
+        const Tile tile = decode(g, t);
+        const CUtensorMap* ma = &g.a[tile.problem];
+        const CUtensorMap* mb = &g.b[tile.problem];
+        const int m0 = tile.tm * kGemmTile + 128 * static_cast<int>(rank);
+        const int n0 = tile.tn * kGemmTile + 128 * static_cast<int>(rank);
+        for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
+          ok = tc::mbar_wait(empty + 8 * stage, phase ^ 1);
+          if (!ok) break;
+          const uint32_t sa = base + stage * kStageBytes, sb = sa + kOperandBytes;
+          if (rank == 0) tc::mbar_expect_tx(full + 8 * stage, 2 * kStageBytes);
+          const uint32_t bar = tc::map_to_rank(full + 8 * stage, 0);
+          if (kAMn) {
+            tc::tma_load_3d_pair(sa, ma, bar, m0, kb * kTileK, tile.batch);
+            tc::tma_load_3d_pair(sa + kOperandBytes / 2, ma, bar, m0 + 64, kb * kTileK, tile.batch);
+          } else {
+            tc::tma_load_3d_pair(sa, ma, bar, kb * kTileK, m0, tile.batch);
+          }
+          if (kBMn) {
+            tc::tma_load_3d_pair(sb, mb, bar, n0, kb * kTileK, tile.batch);
+            tc::tma_load_3d_pair(sb + kOperandBytes / 2, mb, bar, n0 + 64, kb * kTileK, tile.batch);
+          } else {
+            tc::tma_load_3d_pair(sb, mb, bar, kb * kTileK, n0, tile.batch);
+          }
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && tc::elect_one()) {
+      constexpr uint32_t idesc = tc::instr_desc(kGemmTile, kGemmTile, kBf16, kAMn, kBMn);
+      // one MMA is 16 deep in K: 32 bytes along a K-major row, 16 rows of 128
+      // bytes in the MN-major order (descriptor units of 16 bytes)
+      constexpr uint64_t step_a = kAMn ? 128 : 2, step_b = kBMn ? 128 : 2;
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, tphase = 0;
+      for (int t = cluster; t < g.total_tiles && ok; t += clusters) {
+        const Tile tile = decode(g, t);
+        ok = tc::mbar_wait(tempty + 8 * buf, tphase ^ 1);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t d = tmem + kGemmTile * buf;
+        for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
+          ok = tc::mbar_wait(full + 8 * stage, phase);
+          if (!ok) break;
+          tc::fence_after();
+          const uint32_t sa = base + stage * kStageBytes;
+          const uint64_t da = tc::smem_desc(sa, kAMn), db = tc::smem_desc(sa + kOperandBytes, kBMn);
+#pragma unroll
+          for (int k = 0; k < kTileK / 16; ++k)
+            tc::mma_f16_pair(d, da + step_a * k, db + step_b * k, idesc, kb != tile.kb0 || k != 0);
+          tc::mma_commit_pair(empty + 8 * stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (ok) tc::mma_commit_pair(tfull + 8 * buf);
+        buf ^= 1;
+        if (buf == 0) tphase ^= 1;
+      }
+    }
+  } else {
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    int buf = 0;
+    uint32_t tphase = 0;
+    for (int t = cluster; t < g.total_tiles; t += clusters) {
+      const Tile tile = decode(g, t);
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(tfull + 8 * buf, tphase));
+      if (!ok) break;
+      tc::fence_after();
+      const int row = tile.tm * kGemmTile + 128 * static_cast<int>(rank) + 32 * quad + lane;
+      const int col0 = tile.tn * kGemmTile + 128 * half;
+      const uint32_t addr = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kGemmTile * buf + 128 * half;
+      const uint32_t bar = tempty + 8 * buf;
+      Epi::run(g.epi[tile.problem], g.shape[tile.problem], tile, row, col0, addr, [&]() {
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(bar, 0));
+      });
+      buf ^= 1;
+      if (buf == 0) tphase ^= 1;
+    }
+  }
+  if (!ok) {
+    atomicExch(&g_gemm_error, 1);
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort_slot), "r"(1) : "memory");
+  }
+  __syncthreads();
+  uint32_t aborted;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(aborted) : "r"(abort_slot));
+  // after a wait that ran out, give loads and MMAs in flight time to land
+  if (aborted)
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc::tmem_free_pair(tmem, kTmemColumns);
+  }
+}
+
+// ---- host ------------------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeTiled>(nullptr);
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// Tile of 64 contiguous elements x 128 rows (K-major: 64 deep in K, 128 rows)
+// or x 64 rows (MN-major: 64 wide, 64 deep in K).
+bool make_map(CUtensorMap* map, const GemmOperand& o, bool bf16, bool mn_major) {
+  EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.inner), static_cast<cuuint64_t>(o.outer),
+                              static_cast<cuuint64_t>(o.batch)};
+  const cuuint64_t pitch = static_cast<cuuint64_t>(o.pitch) * 2;
+  const cuuint64_t strides[2] = {pitch, o.batch > 1 ? static_cast<cuuint64_t>(o.batch_pitch) * 2 : pitch};
+  const cuuint32_t box[3] = {64u, mn_major ? 64u : 128u, 1u};
+  const cuuint32_t one[3] = {1u, 1u, 1u};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void*>(o.ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// CTA pairs of this kernel that can be resident at once; 0 when the query fails.
+template <class Epi, bool kBf16, bool kAMn, bool kBMn>
+int resident_pairs() {
+  auto kernel = gemm_kernel<Epi, kBf16, kAMn, kBMn>;
+  constexpr int kMaxDevices = 16;
+  static std::mutex mu;
+  static int cached[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cached[dev]) return cached[dev];
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return 0;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {2, 1, 1};
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int pairs = 0;
+  if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess) return 0;
+  return cached[dev] = pairs;
+}
+
+template <class Epi>
+const typename Epi::Params& params_of(const GemmProblem& p);
+template <>
+const StoreParams& params_of<StoreEpilogue>(const GemmProblem& p) { return p.store; }
+template <>
+const PartialParams& params_of<PartialEpilogue>(const GemmProblem& p) { return p.partial; }
+template <>
+const XentParams& params_of<XentEpilogue>(const GemmProblem& p) { return p.xent; }
+
+template <class Epi, bool kBf16, bool kAMn, bool kBMn>
+cudaError_t launch(const GemmProblem* problems, int count, cudaStream_t stream) {
+  auto kernel = gemm_kernel<Epi, kBf16, kAMn, kBMn>;
+  const int pairs = resident_pairs<Epi, kBf16, kAMn, kBMn>();
+  if (pairs <= 0) {
+    const cudaError_t err = cudaGetLastError();
+    return err != cudaSuccess ? err : cudaErrorInvalidDevice;
+  }
+  Args<typename Epi::Params> g;
+  int64_t total = 0;
+  int used = 0;
+  for (int i = 0; i < count; ++i) {
+    const GemmProblem& p = problems[i];
+    if (p.m <= 0 || p.n <= 0 || p.k <= 0 || p.batch <= 0) continue;
+    Shape& s = g.shape[used];
+    s.m = static_cast<int32_t>(p.m);
+    s.n = static_cast<int32_t>(p.n);
+    s.k_blocks = static_cast<int32_t>(ceil_div(p.k, kTileK));
+    s.k_per_split = static_cast<int32_t>(ceil_div(s.k_blocks, p.splits));
+    s.splits = static_cast<int32_t>(ceil_div(s.k_blocks, s.k_per_split));
+    s.tiles_m = static_cast<int32_t>(ceil_div(p.m, kGemmTile));
+    s.tiles_n = static_cast<int32_t>(ceil_div(p.n, kGemmTile));
+    s.symmetric = p.symmetric;
+    s.tiles = p.symmetric ? s.tiles_n * (s.tiles_n + 1) / 2 : s.tiles_m * s.tiles_n;
+    s.first_tile = static_cast<int32_t>(total);
+    total += static_cast<int64_t>(s.tiles) * s.splits * p.batch;
+    if (total > INT32_MAX / 2) return cudaErrorInvalidValue;
+    if (!make_map(&g.a[used], p.a, kBf16, kAMn) || !make_map(&g.b[used], p.b, kBf16, kBMn))
+      return cudaErrorInvalidPitchValue;
+    g.epi[used] = params_of<Epi>(p);
+    ++used;
+  }
+  if (used == 0) return cudaSuccess;
+  g.count = used;
+  g.total_tiles = static_cast<int32_t>(total);
+  const unsigned grid = 2u * static_cast<unsigned>(total < pairs ? total : pairs);
+  kernel<<<grid, kThreads, kSmemBytes, stream>>>(g);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gemm(GemmKind kind, const GemmProblem* p, int count, cudaStream_t stream) {
+  if (count > kGemmMaxProblems) return cudaErrorInvalidValue;
+  switch (kind) {
+    case GEMM_NS_SYM: return launch<StoreEpilogue, false, false, false>(p, count, stream);
+    case GEMM_NS_APPLY: return launch<StoreEpilogue, false, false, true>(p, count, stream);
+    case GEMM_LOGITS: return launch<XentEpilogue, true, false, false>(p, count, stream);
+    case GEMM_DX: return launch<StoreEpilogue, true, false, true>(p, count, stream);
+    case GEMM_DX_SPLIT: return launch<PartialEpilogue, true, false, true>(p, count, stream);
+    case GEMM_DW: return launch<StoreEpilogue, true, true, true>(p, count, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+// A split costs each tile its pipeline's ramp and, in fp32, a partial sum to
+// write and read: about 3 K steps for a whole tile, 12 for a part of one. Taken:
+// the count with the shortest run of rounds over the 76 pairs of 152 SMs.
+int gemm_splits(int64_t tiles, int64_t k) {
+  const int64_t blocks = ceil_div(k, kTileK);
+  int64_t best = 1, best_cost = 0;
+  for (int64_t s = 1; s <= 32 && s <= blocks; ++s) {
+    const int64_t per = ceil_div(blocks, s);
+    const int64_t real = ceil_div(blocks, per);
+    if (real != s) continue;
+    const int64_t cost = ceil_div(tiles * s, 76) * (per + (s > 1 ? 12 : 3));
+    if (s == 1 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return static_cast<int>(best);
+}
+
+cudaError_t gemm_take_error(int* out) {
+  cudaError_t err = cudaMemcpyFromSymbol(out, g_gemm_error, sizeof(int));
+  if (err != cudaSuccess || *out == 0) return err;
+  const int zero = 0;
+  return cudaMemcpyToSymbol(g_gemm_error, &zero, sizeof(int));
+}
+
+}  // namespace lst

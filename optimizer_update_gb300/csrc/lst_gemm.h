@@ -1,0 +1,81 @@
+// Host interface of the tensor-core product kernel (lst_gemm.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace lst {
+
+// A 16-bit operand in device memory: `inner` contiguous elements, `outer` rows
+// `pitch` elements apart, `batch` such matrices `batch_pitch` elements apart.
+// Base and pitches are multiples of 16 bytes (a rule of the tile loads).
+struct GemmOperand {
+  const void* ptr;
+  int64_t inner, outer, pitch;
+  int64_t batch = 1, batch_pitch = 0;
+};
+
+// out = alpha * acc + beta * c (+ diag on the main diagonal), rounded to fp16
+// or bf16; c has out's shape, pitch and type. `vec`: bytes a store may be
+// wide (32, 16 or 2) by out's alignment.
+struct StoreParams {
+  void* out;
+  const void* c;
+  int64_t ld, batch_stride;
+  float alpha, beta, diag;
+  int32_t bf16, transposed, vec;
+};
+
+// fp32 partial sums of a K range: out[split][row][col], added to what is there
+// when `accumulate` is set.
+struct PartialParams {
+  float* out;
+  int64_t ld, split_stride;
+  int32_t accumulate;
+};
+
+// Logits of tokens (rows) against a piece of the vocabulary (columns), reduced
+// on the spot; see lst_xent.cu.
+struct XentParams {
+  const void* targets;
+  float2* stats;    // [128-column group][row]: (max, sum of exp(l - max))
+  float* target_logit;
+  uint16_t* q;      // [row][column]: (max - l) in steps of 2^-11, or null
+  int64_t q_ld, stat_ld, first_group, first_column;
+  int32_t index_bytes;
+};
+
+enum GemmKind {
+  GEMM_NS_SYM,    // fp16, A [m,k] and B [n,k] both K-contiguous, StoreParams
+  GEMM_NS_APPLY,  // fp16, A [m,k] K-contiguous, B [k,n] n-contiguous, StoreParams
+  GEMM_LOGITS,    // bf16, A [m,k], B [n,k] K-contiguous, XentParams
+  GEMM_DX,        // bf16, A [m,k] K-contiguous, B [k,n] n-contiguous, StoreParams
+  GEMM_DX_SPLIT,  // the same, PartialParams
+  GEMM_DW,        // bf16, A [k,m] m-contiguous, B [k,n] n-contiguous, StoreParams
+};
+
+struct GemmProblem {
+  GemmOperand a, b;
+  int64_t m, n, k, batch = 1;
+  bool symmetric = false;  // the result is symmetric: form one triangle of tiles and mirror it
+  int splits = 1;          // K ranges (GEMM_DX_SPLIT)
+  StoreParams store{};
+  PartialParams partial{};
+  XentParams xent{};
+};
+
+constexpr int kGemmMaxProblems = 8;
+constexpr int kGemmTile = 256;
+
+// One launch over up to kGemmMaxProblems independent products of one kind.
+cudaError_t launch_gemm(GemmKind kind, const GemmProblem* problems, int count, cudaStream_t stream);
+
+// K ranges that fill the GPU for `tiles` output tiles of `k` elements each.
+int gemm_splits(int64_t tiles, int64_t k);
+
+// Whether some wait of a matrix kernel ran out since the last call on this
+// device (synchronises the device).
+cudaError_t gemm_take_error(int* out);
+
+}  // namespace lst

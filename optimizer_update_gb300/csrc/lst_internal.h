@@ -44,6 +44,8 @@ struct Tensor {
   int64_t layer = 0;
   int64_t elem_off = 0;
   int64_t numel = 0;
+  int32_t ndim = 0;
+  int64_t dims[4] = {0, 0, 0, 0};
 };
 
 struct Engine;  // streamed-step resources (streams, events), per device

@@ -108,6 +108,8 @@ extern "C" lst_status lst_layout_create(int32_t n_tensors, const int32_t* ndim, 
     t.layer = l;
     t.elem_off = cursor[(size_t)l];
     t.numel = n;
+    t.ndim = ndim[i];
+    for (int k = 0; k < ndim[i]; ++k) t.dims[k] = dims[4 * (int64_t)i + k];
     cursor[(size_t)l] += round_up(n, kTensorAlign);
     if (cursor[(size_t)l] > kMaxBlockElems) {
       delete L;

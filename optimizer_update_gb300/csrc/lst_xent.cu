@@ -1,0 +1,481 @@
+// Softmax cross entropy of a large vocabulary without the matrix of logits,
+// and its gradients.
+//
+// Mathematics. l = x w^T; lse_i = log sum_v exp(l_iv); loss_i = lse_i - l_i,t;
+// with p = exp(l - lse) and g = grad_scale / N the gradient with respect to
+// the logits is d_iv = g (p_iv - [v = t_i]), and dx = d w, dw = d^T x.
+//
+// Order. Logits are formed 256 x 256 at a time on the tensor cores
+// (lst_gemm.cu); a tile leaves, for each row and 128 columns, the maximum M
+// and the sum of exp(l - M), from which a second kernel joins lse. For the
+// gradient the tile also leaves (M - l) in 16 bits of fixed point, steps of
+// 2^-11: the workspace holds as many columns of those ("a piece") as fit, and
+// d is written over them in bf16 once lse is known. That one rounding (and
+// the 2^-12 of the fixed point, eight times smaller) is all that d loses;
+// keeping exp(l - M) in bf16 instead and rescaling it would round twice. A
+// bf16 d is what the tensor cores take next to the bf16 x and w; its error is
+// that of the results' own rounding.
+//   One piece: 2 N V H operations for the logits, 4 N V H for dx and dw.
+//   More pieces: first the statistics of all of them; then each piece's logits
+//   are formed again (except those of the one formed last, still there), 8 N V H in all.
+// dx sums over the vocabulary: where its tiles do not fill the GPU the sum is
+// split, and partial sums are added in a fixed order in fp32, which also
+// carries them over the pieces.
+//
+// Bound by the tensor cores from about 300 tokens on; below by reading w.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "lst_gemm.h"
+#include "lst_ops.h"
+
+namespace lst {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int64_t kMaxPieceBytes = int64_t(1) << 30;
+
+__device__ __forceinline__ int64_t target_at(const void* t, int wide, int64_t i) {
+  return wide ? static_cast<const int64_t*>(t)[i] : static_cast<const int32_t*>(t)[i];
+}
+
+// lse and loss of 32 rows from the statistics of all 128-column groups: 32
+// threads per row take every 32nd group each, with the running maximum and sum.
+__global__ void __launch_bounds__(1024)
+    join_kernel(const float2* __restrict__ stats, int64_t stat_ld, int groups, const float* __restrict__ target_logit,
+                const void* __restrict__ targets, int wide, int64_t ignore, int64_t vocab, int rows,
+                float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float2 part[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * 32 + lane;
+  const float ninf = __int_as_float(0xff800000);
+  float top = ninf, sum = 0.0f;
+  if (row < rows) {
+    for (int g = warp; g < groups; g += 32) {
+      const float2 s = stats[g * stat_ld + row];
+      const float m = fmaxf(top, s.x);
+      const float base = m == ninf ? 0.0f : m;
+      sum = sum * exp2f((top - base) * kLog2e) + s.y * exp2f((s.x - base) * kLog2e);
+      top = m;
+    }
+  }
+  part[warp][lane] = make_float2(top, sum);
+  __syncthreads();
+  // warp w joins row w of the block
+  const float2 s = part[lane][warp];
+  float m = s.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == ninf ? 0.0f : m;
+  float z = s.y * exp2f((s.x - base) * kLog2e);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  const int r = blockIdx.x * 32 + warp;
+  if (lane == 0 && r < rows) {
+    const float l = base + logf(z);
+    const int64_t t = target_at(targets, wide, r);
+    lse[r] = l;
+    loss[r] = t == ignore ? 0.0f : (t >= 0 && t < vocab) ? l - target_logit[r] : __int_as_float(0x7fc00000);
+  }
+}
+
+// mean loss, and g = grad_scale / N, by one block in a fixed order.
+__global__ void __launch_bounds__(1024)
+    mean_kernel(const float* __restrict__ loss, const void* __restrict__ targets, int wide, int64_t ignore, int rows,
+                float grad_scale, float* __restrict__ mean, float* __restrict__ g) {
+  double sum = 0.0;
+  int count = 0;
+  for (int i = threadIdx.x; i < rows; i += 1024)
+    if (target_at(targets, wide, i) != ignore) {
+      sum += static_cast<double>(loss[i]);
+      ++count;
+    }
+  __shared__ double s[32];
+  __shared__ int c[32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_down_sync(0xffffffffu, sum, o);
+    count += __shfl_down_sync(0xffffffffu, count, o);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    s[threadIdx.x >> 5] = sum;
+    c[threadIdx.x >> 5] = count;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 32; ++i) {
+      sum += s[i];
+      count += c[i];
+    }
+    *mean = count ? static_cast<float>(sum / count) : 0.0f;
+    *g = count ? static_cast<float>(static_cast<double>(grad_scale) / count) : 0.0f;
+  }
+}
+
+// d over q, in place: 8 entries per thread, one row per block of columns.
+__global__ void __launch_bounds__(256)
+    logit_grad_kernel(uint16_t* __restrict__ q, int64_t q_ld, const float2* __restrict__ stats, int64_t stat_ld,
+                      int64_t first_group, int64_t first_column, int columns, const float* __restrict__ lse,
+                      const float* __restrict__ target_logit, const void* __restrict__ targets, int wide,
+                      int64_t ignore, int64_t vocab, const float* __restrict__ gp, int blocks_per_row) {
+  const int row = blockIdx.x / blocks_per_row;
+  const int col = ((blockIdx.x - row * blocks_per_row) * 256 + threadIdx.x) * 8;
+  if (col >= columns) return;
+  uint4* const p = reinterpret_cast<uint4*>(q + static_cast<int64_t>(row) * q_ld + col);
+  const int64_t t = target_at(targets, wide, row);
+  if (t == ignore || t < 0 || t >= vocab) {
+    *p = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const float g = *gp, l = lse[row];
+  const float top = stats[(first_group + (col >> 7)) * stat_ld + row].x;
+  const float base = (top - l) * kLog2e;
+  const uint4 x = *p;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  float d[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float steps = static_cast<float>((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+    float e;
+    const float a = __fmaf_rn(steps, -kLog2e / 2048.0f, base);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a));
+    d[i] = e * g;
+  }
+  const int64_t at = t - first_column - col;
+  if (at >= 0 && at < 8) {
+    // the target's own probability from its fp32 logit: p - 1 cancels when p is near 1
+    const float e = expm1f(target_logit[row] - l) * g;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i == static_cast<int>(at)) d[i] = e;
+  }
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(d[2 * i], d[2 * i + 1]);
+    r[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *p = make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// dx = sum of its parts, in order, rounded to bf16.
+__global__ void __launch_bounds__(256)
+    dx_kernel(const float* __restrict__ parts, int64_t ld, int64_t split_stride, int splits, int rows, int cols,
+              __nv_bfloat16* __restrict__ dx, int64_t dx_ld, int wide_store) {
+  const int quads = (cols + 3) / 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int row = static_cast<int>(i / quads);
+  if (row >= rows) return;
+  const int col = static_cast<int>(i - static_cast<int64_t>(row) * quads) * 4;
+  const float* p = parts + static_cast<int64_t>(row) * ld + col;
+  float4 a = *reinterpret_cast<const float4*>(p);
+  for (int s = 1; s < splits; ++s) {
+    const float4 b = *reinterpret_cast<const float4*>(p + s * split_stride);
+    a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+  }
+  __nv_bfloat16* o = dx + static_cast<int64_t>(row) * dx_ld + col;
+  const float v[4] = {a.x, a.y, a.z, a.w};
+  if (wide_store) {
+    const __nv_bfloat162 h0 = __floats2bfloat162_rn(v[0], v[1]), h1 = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(o) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+  } else {
+    for (int k = 0; k < 4 && col + k < cols; ++k) o[k] = __float2bfloat16_rn(v[k]);
+  }
+}
+
+// Rows at a pitch that is a multiple of 16 bytes, for operands that are not
+// laid out so (a rule of the tile loads). `ignore_rows`: rows whose target is
+// ignored become zero, so that nothing they hold reaches a sum over rows.
+__global__ void __launch_bounds__(256)
+    pack_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t* __restrict__ dst,
+                int64_t dst_ld) {
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int c = threadIdx.x; c < cols; c += 256) dst[r * dst_ld + c] = src[r * ld + c];
+}
+
+// Whether any ignored row holds a value that is not finite is not known without
+// reading x, so x is copied with its ignored rows zeroed for the product d^T x:
+// 0 * infinity would reach dw.
+__global__ void __launch_bounds__(256)
+    mask_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t* __restrict__ dst,
+                     int64_t dst_ld, const void* __restrict__ targets, int wide, int64_t ignore, int64_t vocab,
+                     int vec) {
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int64_t t = target_at(targets, wide, r);
+    const bool keep = t != ignore && t >= 0 && t < vocab;
+    if (vec) {
+      for (int c = threadIdx.x * 8; c < cols; c += 2048)
+        *reinterpret_cast<uint4*>(dst + r * dst_ld + c) =
+            keep ? *reinterpret_cast<const uint4*>(src + r * ld + c) : make_uint4(0, 0, 0, 0);
+    } else {
+      for (int c = threadIdx.x; c < cols; c += 256) dst[r * dst_ld + c] = keep ? src[r * ld + c] : 0;
+    }
+  }
+}
+
+bool tile_ready(const lst_matrix* m) {
+  return reinterpret_cast<uintptr_t>(m->data) % 16 == 0 && (m->stride * 2) % 16 == 0;
+}
+
+struct Plan {
+  int64_t n_pad, groups, piece, pieces, splits;
+  int64_t packed_ld, x_ld, part_ld;
+  int64_t scalar_off, tlogit_off, stats_off, xm_off, xpack_off, wpack_off, part_off, q_off;
+  int64_t fixed;  // bytes before the pieces
+  int64_t bytes;
+};
+
+// Layout of the workspace; `bytes` < 0: for one piece, at most 1 GiB of it.
+// Returns false when not even one tile of columns fits.
+bool make_plan(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool pack_w, int64_t bytes, Plan* p) {
+  p->n_pad = ops_round_up(n, 64);
+  p->groups = ops_ceil_div(v, 128);
+  p->packed_ld = ops_round_up(h, 8);
+  int64_t at = 0;
+  auto take = [&](int64_t size) {
+    const int64_t off = at;
+    at += ops_round_up(size, 256);
+    return off;
+  };
+  p->scalar_off = take(256);
+  p->tlogit_off = take(n * 4);
+  p->stats_off = take(p->groups * p->n_pad * 8);
+  p->xpack_off = take(pack_x ? n * p->packed_ld * 2 : 0);
+  p->wpack_off = take(pack_w ? v * p->packed_ld * 2 : 0);
+  p->piece = p->pieces = 0;
+  p->splits = 1;
+  if (grad) {
+    p->xm_off = take(n * p->packed_ld * 2);
+    p->part_ld = ops_round_up(h, 32);
+    const int64_t tiles = ops_ceil_div(n, kGemmTile) * ops_ceil_div(h, kGemmTile);
+    const int64_t whole = ops_round_up(v, kGemmTile);
+    const int64_t most = std::max<int64_t>(kGemmTile, kMaxPieceBytes / (2 * n) / kGemmTile * kGemmTile);
+    auto parts = [&](int64_t piece) {
+      const int64_t splits = gemm_splits(tiles, std::min(piece, v));
+      return splits > 1 || piece < v ? splits * n * p->part_ld * 4 + 256 : 0;
+    };
+    int64_t piece = std::min(whole, most);
+    if (bytes >= 0)
+      while (piece > 0 && at + ops_round_up(parts(piece), 256) + n * piece * 2 > bytes)
+        piece = piece > 4 * kGemmTile ? piece / 2 / kGemmTile * kGemmTile : piece - kGemmTile;
+    if (piece <= 0) return false;
+    p->piece = piece;
+    p->pieces = ops_ceil_div(v, piece);
+    p->splits = gemm_splits(tiles, std::min(piece, v));
+    p->part_off = take(parts(piece));
+    p->q_off = take(n * piece * 2);
+  }
+  p->bytes = at;
+  return bytes < 0 || at <= bytes;
+}
+
+GemmOperand rows_operand(const void* ptr, int64_t rows, int64_t cols, int64_t ld) { return {ptr, cols, rows, ld}; }
+
+int store_width(const lst_matrix* m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(m->data) | static_cast<uintptr_t>(m->stride * 2);
+  return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 2;
+}
+
+lst_status check_xw(const lst_matrix* x, const lst_matrix* w, const lst_indices* targets, const char* who) {
+  LST_TRY(check_matrix(x, "x", who));
+  LST_TRY(check_matrix(w, "w", who));
+  LST_TRY(check_indices(targets, "targets", who));
+  if (x->dtype != LST_BF16 || w->dtype != LST_BF16) return fail(LST_ERR_INVALID_ARG, "%s: x and w must be bf16", who);
+  if (x->rows != targets->count || x->cols != w->cols)
+    return fail(LST_ERR_INVALID_ARG, "%s: x must be targets x hidden, w vocabulary x hidden", who);
+  if (w->rows == 0 || w->cols == 0) return fail(LST_ERR_INVALID_ARG, "%s: empty vocabulary or hidden size", who);
+  if (x->rows > (int64_t(1) << 24)) return fail(LST_ERR_INVALID_ARG, "%s: more than 2^24 targets", who);
+  return LST_OK;
+}
+
+struct Call {
+  const char* who;
+  const lst_matrix *x, *w;
+  const lst_indices* targets;
+  int64_t ignore;
+  float *loss, *lse;
+  char* ws;
+  cudaStream_t stream;
+  Plan p;
+  const void *xp, *wp;
+  int64_t x_ld, w_ld;
+  int wide;
+
+  // The operands of the products, packed first where their rows are not on 16 bytes.
+  cudaError_t operands() {
+    xp = x->data, wp = w->data, x_ld = x->stride, w_ld = w->stride;
+    auto pack = [&](const lst_matrix* m, int64_t off, const void** ptr, int64_t* ld) {
+      const unsigned grid = static_cast<unsigned>(std::min<int64_t>(m->rows, 8192));
+      pack_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(m->data), m->stride, m->rows,
+                                            static_cast<int>(m->cols), reinterpret_cast<uint16_t*>(ws + off),
+                                            p.packed_ld);
+      *ptr = ws + off;
+      *ld = p.packed_ld;
+      return cudaGetLastError();
+    };
+    cudaError_t err = cudaSuccess;
+    if (!tile_ready(x)) err = pack(x, p.xpack_off, &xp, &x_ld);
+    if (err == cudaSuccess && !tile_ready(w)) err = pack(w, p.wpack_off, &wp, &w_ld);
+    return err;
+  }
+
+  cudaError_t logits(int64_t v0, int64_t columns, bool keep) {
+    GemmProblem g;
+    g.a = rows_operand(xp, x->rows, x->cols, x_ld);
+    g.b = rows_operand(static_cast<const uint16_t*>(wp) + v0 * w_ld, columns, w->cols, w_ld);
+    g.m = x->rows;
+    g.n = columns;
+    g.k = x->cols;
+    g.xent = {targets->data, reinterpret_cast<float2*>(ws + p.stats_off), reinterpret_cast<float*>(ws + p.tlogit_off),
+              keep ? reinterpret_cast<uint16_t*>(ws + p.q_off) : nullptr, p.piece, p.n_pad, v0 / 128, v0,
+              targets->bits / 8};
+    return launch_gemm(GEMM_LOGITS, &g, 1, stream);
+  }
+
+  cudaError_t join() {
+    join_kernel<<<static_cast<unsigned>(ops_ceil_div(x->rows, 32)), 1024, 0, stream>>>(
+        reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, static_cast<int>(p.groups),
+        reinterpret_cast<const float*>(ws + p.tlogit_off), targets->data, wide, ignore, w->rows,
+        static_cast<int>(x->rows), loss, lse);
+    return cudaGetLastError();
+  }
+};
+
+}  // namespace
+}  // namespace lst
+
+using namespace lst;
+
+extern "C" int64_t lst_xent_workspace_bytes(int64_t count, int64_t hidden, int64_t vocab, int32_t with_grad) {
+  if (count <= 0 || hidden <= 0 || vocab <= 0 || count > (int64_t(1) << 24) || vocab > INT32_MAX || hidden > INT32_MAX)
+    return 0;
+  Plan p;
+  // rows of an odd size have to be packed; others may be, when they start off 16 bytes
+  const bool pack = hidden % 8 != 0;
+  make_plan(count, hidden, vocab, with_grad != 0, pack, pack, -1, &p);
+  return p.bytes;
+}
+
+extern "C" lst_status lst_xent_loss(const lst_matrix* x, const lst_matrix* w, const lst_indices* targets,
+                                    int64_t ignore_index, float* loss, float* lse, void* workspace,
+                                    int64_t workspace_bytes, void* cuda_stream) {
+  clear_error();
+  const char* who = "lst_xent_loss";
+  LST_TRY(check_xw(x, w, targets, who));
+  if (x->rows == 0) return LST_OK;
+  if (!loss || !lse) return fail(LST_ERR_INVALID_ARG, "%s: loss or lse is null", who);
+  if (reinterpret_cast<uintptr_t>(loss) % 4 || reinterpret_cast<uintptr_t>(lse) % 4)
+    return fail(LST_ERR_ALIGNMENT, "%s: loss or lse not 4-byte aligned", who);
+  Call c{who, x, w, targets, ignore_index, loss, lse, static_cast<char*>(workspace),
+         static_cast<cudaStream_t>(cuda_stream), {}, nullptr, nullptr, 0, 0, targets->bits == 64};
+  make_plan(x->rows, x->cols, w->rows, false, !tile_ready(x), !tile_ready(w), -1, &c.p);
+  LST_TRY(check_workspace(workspace, workspace_bytes, c.p.bytes, who));
+  LST_TRY_CUDA(c.operands(), who);
+  LST_TRY_CUDA(c.logits(0, w->rows, false), who);
+  LST_TRY_CUDA(c.join(), who);
+  return LST_OK;
+}
+
+extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, const lst_indices* targets,
+                                    int64_t ignore_index, float grad_scale, float* loss, float* lse, float* mean,
+                                    const lst_matrix* dx, const lst_matrix* dw, int32_t accumulate_dw, void* workspace,
+                                    int64_t workspace_bytes, void* cuda_stream) {
+  clear_error();
+  const char* who = "lst_xent_grad";
+  LST_TRY(check_xw(x, w, targets, who));
+  LST_TRY(check_matrix(dx, "dx", who));
+  LST_TRY(check_matrix(dw, "dw", who));
+  if (dx->dtype != LST_BF16 || dw->dtype != LST_BF16) return fail(LST_ERR_INVALID_ARG, "%s: dx and dw must be bf16", who);
+  if (dx->rows != x->rows || dx->cols != x->cols || dw->rows != w->rows || dw->cols != w->cols)
+    return fail(LST_ERR_INVALID_ARG, "%s: dx and dw must have the shapes of x and w", who);
+  if (!std::isfinite(grad_scale)) return fail(LST_ERR_INVALID_ARG, "%s: grad_scale not finite", who);
+  if (!mean) return fail(LST_ERR_INVALID_ARG, "%s: mean is null", who);
+  if (x->rows > 0 && (!loss || !lse)) return fail(LST_ERR_INVALID_ARG, "%s: loss or lse is null", who);
+  if (reinterpret_cast<uintptr_t>(loss) % 4 || reinterpret_cast<uintptr_t>(lse) % 4 ||
+      reinterpret_cast<uintptr_t>(mean) % 4)
+    return fail(LST_ERR_ALIGNMENT, "%s: loss, lse or mean not 4-byte aligned", who);
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  if (x->rows == 0) {
+    LST_TRY_CUDA(cudaMemsetAsync(mean, 0, 4, stream), who);
+    if (!accumulate_dw)
+      LST_TRY_CUDA(cudaMemset2DAsync(dw->data, (size_t)dw->stride * 2, 0, (size_t)dw->cols * 2, (size_t)dw->rows, stream),
+                   who);
+    return LST_OK;
+  }
+  Call c{who, x, w, targets, ignore_index, loss, lse, static_cast<char*>(workspace), stream, {}, nullptr, nullptr,
+         0, 0, targets->bits == 64};
+  const bool px = !tile_ready(x), pw = !tile_ready(w);
+  if (!make_plan(x->rows, x->cols, w->rows, true, px, pw, workspace_bytes < 0 ? 0 : workspace_bytes, &c.p))
+    return fail(LST_ERR_INVALID_ARG, "%s: workspace of %lld bytes holds no piece of 256 columns", who,
+                (long long)workspace_bytes);
+  const Plan& p = c.p;
+  LST_TRY(check_workspace(workspace, workspace_bytes, p.bytes, who));
+  char* ws = c.ws;
+  const int64_t n = x->rows, h = x->cols, v = w->rows;
+  float* g = reinterpret_cast<float*>(ws + p.scalar_off);
+  uint16_t* xm = reinterpret_cast<uint16_t*>(ws + p.xm_off);
+  uint16_t* q = reinterpret_cast<uint16_t*>(ws + p.q_off);
+
+  LST_TRY_CUDA(c.operands(), who);
+  mask_rows_kernel<<<static_cast<unsigned>(std::min<int64_t>(n, 8192)), 256, 0, stream>>>(
+      static_cast<const uint16_t*>(c.xp), c.x_ld, n, static_cast<int>(h), xm, p.packed_ld, targets->data, c.wide,
+      ignore_index, v, h % 8 == 0);
+  LST_TRY_CUDA(cudaGetLastError(), who);
+  for (int64_t k = p.pieces - 1; k >= 0; --k) {
+    const int64_t v0 = k * p.piece;
+    LST_TRY_CUDA(c.logits(v0, std::min(p.piece, v - v0), k == 0), who);
+  }
+  LST_TRY_CUDA(c.join(), who);
+  mean_kernel<<<1, 1024, 0, stream>>>(loss, targets->data, c.wide, ignore_index, static_cast<int>(n), grad_scale, mean, g);
+  LST_TRY_CUDA(cudaGetLastError(), who);
+  const bool parts = p.splits > 1 || p.pieces > 1;
+  // the first piece sets every partial sum of dx: only the last can be shorter,
+  // with fewer splits
+  for (int64_t k = 0; k < p.pieces; ++k) {
+    const int64_t v0 = k * p.piece, columns = std::min(p.piece, v - v0);
+    if (k > 0) LST_TRY_CUDA(c.logits(v0, columns, true), who);
+    const int blocks = static_cast<int>(ops_ceil_div(columns, 2048));
+    logit_grad_kernel<<<static_cast<unsigned>(n * blocks), 256, 0, stream>>>(
+        q, p.piece, reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, v0 / 128, v0, static_cast<int>(columns),
+        lse, reinterpret_cast<const float*>(ws + p.tlogit_off), targets->data, c.wide, ignore_index, v, g, blocks);
+    LST_TRY_CUDA(cudaGetLastError(), who);
+    // dw of the piece = d^T x
+    GemmProblem d;
+    d.a = rows_operand(q, n, columns, p.piece);
+    d.b = rows_operand(xm, n, h, p.packed_ld);
+    d.m = columns;
+    d.n = h;
+    d.k = n;
+    uint16_t* dwp = static_cast<uint16_t*>(dw->data) + v0 * dw->stride;
+    d.store = {dwp, accumulate_dw ? dwp : nullptr, dw->stride, 0, 1.0f, 1.0f, 0.0f, 1, 0, store_width(dw)};
+    LST_TRY_CUDA(launch_gemm(GEMM_DW, &d, 1, stream), who);
+    // dx += d w
+    GemmProblem e;
+    e.a = rows_operand(q, n, columns, p.piece);
+    e.b = rows_operand(static_cast<const uint16_t*>(c.wp) + v0 * c.w_ld, columns, h, c.w_ld);
+    e.m = n;
+    e.n = h;
+    e.k = columns;
+    if (parts) {
+      e.splits = static_cast<int>(p.splits);
+      e.partial = {reinterpret_cast<float*>(ws + p.part_off), p.part_ld, n * p.part_ld, k > 0};
+      LST_TRY_CUDA(launch_gemm(GEMM_DX_SPLIT, &e, 1, stream), who);
+    } else {
+      e.store = {dx->data, nullptr, dx->stride, 0, 1.0f, 0.0f, 0.0f, 1, 0, store_width(dx)};
+      LST_TRY_CUDA(launch_gemm(GEMM_DX, &e, 1, stream), who);
+    }
+  }
+  if (parts) {
+    const int64_t quads = ops_ceil_div(h, 4) * n;
+    const bool wide_store = h % 4 == 0 && dx->stride % 4 == 0 && reinterpret_cast<uintptr_t>(dx->data) % 8 == 0;
+    dx_kernel<<<static_cast<unsigned>(ops_ceil_div(quads, 256)), 256, 0, stream>>>(
+        reinterpret_cast<const float*>(ws + p.part_off), p.part_ld, n * p.part_ld, static_cast<int>(p.splits),
+        static_cast<int>(n), static_cast<int>(h), static_cast<__nv_bfloat16*>(dx->data), dx->stride, wide_store);
+    LST_TRY_CUDA(cudaGetLastError(), who);
+  }
+  return LST_OK;
+}

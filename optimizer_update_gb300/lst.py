@@ -63,6 +63,67 @@ class lst_step_options(ctypes.Structure):
                 ("workspace", ctypes.c_void_p)]
 
 
+class lst_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("stride", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class lst_indices(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("count", ctypes.c_int64), ("bits", ctypes.c_int32)]
+
+
+class lst_ns_params(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class lst_muon_hparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("rms_scale", ctypes.c_float), ("eps", ctypes.c_float), ("nesterov", ctypes.c_int32),
+                ("ns_steps", ctypes.c_int32)]
+
+
+# lst_dtype
+LST_BF16 = 0
+LST_F32 = 1
+
+
+def matrix(t) -> lst_matrix:
+    """An lst_matrix over a torch tensor of two dimensions (bf16, bf16 bit
+    patterns as int16, or fp32) with contiguous rows. The tensor has to outlive
+    the calls that use it."""
+    import torch
+    if t.dim() != 2:
+        raise ValueError("a matrix has two dimensions")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError("rows must be contiguous")
+    if t.dtype == torch.float32:
+        dtype = LST_F32
+    elif t.dtype in (torch.bfloat16, torch.int16):
+        dtype = LST_BF16
+    else:
+        raise ValueError(f"unsupported type {t.dtype}")
+    return lst_matrix(t.data_ptr(), rows, cols, max(cols, t.stride(0)) if rows > 1 else cols, dtype)
+
+
+def indices(t) -> lst_indices:
+    """An lst_indices over a contiguous torch tensor of int32 or int64."""
+    import torch
+    if t.dtype not in (torch.int32, torch.int64):
+        raise ValueError("indices are int32 or int64")
+    if not t.is_contiguous():
+        raise ValueError("indices must be contiguous")
+    return lst_indices(t.data_ptr(), t.numel(), 64 if t.dtype == torch.int64 else 32)
+
+
+def ns_params(steps=5, eps=1e-7):
+    return lst_ns_params(steps, eps)
+
+
+def muon_hparams(lr=1e-4, momentum=0.95, weight_decay=0.01, rms_scale=0.2, eps=1e-7, nesterov=True, ns_steps=5):
+    return lst_muon_hparams(lr, momentum, weight_decay, rms_scale, eps, 1 if nesterov else 0, ns_steps)
+
+
 def step_options(block_steps=None, skip=None, grad_sq: int = 0, workspace: int = 0):
     """Per-block options. block_steps / skip: sequences (host) of n_layers ints,
     or None; grad_sq / workspace: device pointers (ints) or 0. The returned
@@ -139,6 +200,19 @@ def lib() -> ctypes.CDLL:
             "lst_store_read": ([vp, i64, vp], ctypes.c_int),
             "lst_store_write": ([vp, i64, vp, i64], ctypes.c_int),
             "lst_store_step": ([vp, P(vp), vp, vp, P(lst_adamw_hparams), i64], ctypes.c_int),
+            "lst_embed": ([P(lst_matrix), P(lst_indices), P(lst_matrix), f32, vp], ctypes.c_int),
+            "lst_embed_grad_workspace_bytes": ([i64, i64, i64], i64),
+            "lst_embed_grad": ([P(lst_matrix), P(lst_indices), P(lst_matrix), f32, i32, vp, i64, vp], ctypes.c_int),
+            "lst_xent_workspace_bytes": ([i64, i64, i64, i32], i64),
+            "lst_xent_loss": ([P(lst_matrix), P(lst_matrix), P(lst_indices), i64, vp, vp, vp, i64, vp], ctypes.c_int),
+            "lst_xent_grad": ([P(lst_matrix), P(lst_matrix), P(lst_indices), i64, f32, vp, vp, vp, P(lst_matrix),
+                               P(lst_matrix), i32, vp, i64, vp], ctypes.c_int),
+            "lst_orthogonalize_workspace_bytes": ([i32, i64, i64], i64),
+            "lst_orthogonalize": ([i32, P(lst_matrix), P(lst_matrix), P(lst_ns_params), vp, i64, vp], ctypes.c_int),
+            "lst_muon_workspace_bytes": ([vp], i64),
+            "lst_muon_step": ([vp, P(vp), P(lst_muon_hparams), P(lst_adamw_hparams), P(ctypes.c_uint8), vp, i64, vp],
+                              ctypes.c_int),
+            "lst_operator_status": ([], ctypes.c_int),
             "lst_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "lst_last_error": ([], ctypes.c_char_p),
             "lst_test_inject": ([i32, i64], ctypes.c_int),
@@ -351,6 +425,72 @@ def lst_store_write(store: int, layer: int, host_src: int, step: int) -> None:
 def lst_store_step(store: int, staging: Sequence[int], dev_buf0: int, dev_buf1: int, hparams: lst_adamw_hparams,
                    timeout_ms: int = 0) -> None:
     _check(lib().lst_store_step(store, _ptr_array(staging), dev_buf0, dev_buf1, ctypes.byref(hparams), timeout_ms))
+
+
+# training operators: matrices as lst_matrix (see matrix()), tokens and targets
+# as lst_indices (see indices()), other device memory as pointers
+def lst_embed(table: lst_matrix, tokens: lst_indices, out: lst_matrix, scale: float = 1.0, stream: int = 0) -> None:
+    _check(lib().lst_embed(table, tokens, out, scale, stream or None))
+
+
+def lst_embed_grad_workspace_bytes(count: int, hidden: int, vocab: int) -> int:
+    return int(lib().lst_embed_grad_workspace_bytes(count, hidden, vocab))
+
+
+def lst_embed_grad(dout: lst_matrix, tokens: lst_indices, grad: lst_matrix, scale: float, accumulate: bool,
+                   workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(lib().lst_embed_grad(dout, tokens, grad, scale, 1 if accumulate else 0, workspace or None, workspace_bytes,
+                                stream or None))
+
+
+def lst_xent_workspace_bytes(count: int, hidden: int, vocab: int, with_grad: bool) -> int:
+    return int(lib().lst_xent_workspace_bytes(count, hidden, vocab, 1 if with_grad else 0))
+
+
+def lst_xent_loss(x: lst_matrix, w: lst_matrix, targets: lst_indices, ignore_index: int, loss: int, lse: int,
+                  workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(lib().lst_xent_loss(x, w, targets, ignore_index, loss or None, lse or None, workspace or None,
+                               workspace_bytes, stream or None))
+
+
+def lst_xent_grad(x: lst_matrix, w: lst_matrix, targets: lst_indices, ignore_index: int, grad_scale: float, loss: int,
+                  lse: int, mean: int, dx: lst_matrix, dw: lst_matrix, accumulate_dw: bool, workspace: int,
+                  workspace_bytes: int, stream: int = 0) -> None:
+    _check(lib().lst_xent_grad(x, w, targets, ignore_index, grad_scale, loss or None, lse or None, mean or None, dx, dw,
+                               1 if accumulate_dw else 0, workspace or None, workspace_bytes, stream or None))
+
+
+def lst_orthogonalize_workspace_bytes(count: int, rows: int, cols: int) -> int:
+    return int(lib().lst_orthogonalize_workspace_bytes(count, rows, cols))
+
+
+def lst_orthogonalize(inputs: Sequence[lst_matrix], outputs: Sequence[lst_matrix], params: lst_ns_params,
+                      workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    n = len(inputs)
+    if len(outputs) != n:
+        raise ValueError("one output per input")
+    _check(lib().lst_orthogonalize(n, (lst_matrix * max(1, n))(*inputs), (lst_matrix * max(1, n))(*outputs), params,
+                                   workspace or None, workspace_bytes, stream or None))
+
+
+def lst_muon_workspace_bytes(handle: int) -> int:
+    return int(lib().lst_muon_workspace_bytes(handle))
+
+
+def lst_muon_step(handle: int, dev_blocks: Sequence[int], muon: lst_muon_hparams, adamw, use_muon, workspace: int,
+                  workspace_bytes: int, stream: int = 0) -> None:
+    """adamw: hyperparameters of the other tensors, or None to leave them alone;
+    use_muon: one truth value per tensor of the layout, or None for every tensor
+    of two dimensions."""
+    mask = (ctypes.c_uint8 * max(1, len(use_muon)))(*[1 if u else 0 for u in use_muon]) if use_muon is not None else None
+    _check(lib().lst_muon_step(handle, _ptr_array(dev_blocks), muon, adamw, mask, workspace or None, workspace_bytes,
+                               stream or None))
+
+
+def lst_operator_status() -> None:
+    """Raises LstError (LST_ERR_TIMEOUT) if a wait inside a matrix kernel ran
+    out since the last call; synchronises the device."""
+    _check(lib().lst_operator_status())
 
 
 def lst_host_alloc(nbytes: int) -> int:
