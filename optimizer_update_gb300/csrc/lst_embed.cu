@@ -89,6 +89,8 @@ __global__ void __launch_bounds__(256)
     embed_kernel(const TI* __restrict__ table, int64_t table_ld, const void* __restrict__ tokens, int wide,
                  TO* __restrict__ out, int64_t out_ld, int hidden, int64_t vocab, uint32_t units_per_row,
                  uint32_t rows_per_launch, int64_t row_base, float scale) {
+  let_next_start();
+  wait_for_previous();
   const uint64_t unit = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x;
   const uint32_t r = static_cast<uint32_t>(unit / units_per_row);
   if (r >= rows_per_launch) return;
@@ -132,6 +134,8 @@ __device__ __forceinline__ uint32_t remote_u32(const uint32_t* p, uint32_t rank)
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1)
     sort_kernel(const void* __restrict__ tokens, int wide, int n, int vocab, int passes, int digit_bits, uint2* buf0,
                 uint2* buf1, uint32_t* seen) {
+  let_next_start();
+  wait_for_previous();
   extern __shared__ uint32_t sm[];
   const int bins = 1 << digit_bits;
   uint32_t* const count = sm;                        // [warp][bin]
@@ -266,6 +270,8 @@ __global__ void __launch_bounds__(kSumThreads)
     sum_kernel(const TD* __restrict__ dout, int64_t dout_ld, const uint2* __restrict__ sorted, int n, int vocab,
                int hidden, int slices, int sum_blocks, const uint32_t* __restrict__ seen, float* __restrict__ parts,
                int64_t parts_ld, Grad<TG> g) {
+  let_next_start();
+  wait_for_previous();
   if (static_cast<int>(blockIdx.x) >= sum_blocks) {
     const int64_t r0 = static_cast<int64_t>(blockIdx.x - sum_blocks) * kZeroRows;
     float zero[8] = {};
@@ -329,6 +335,8 @@ template <class TG, bool VEC>
 __global__ void __launch_bounds__(kSumThreads)
     join_kernel(const uint2* __restrict__ sorted, int n, int vocab, int hidden, int slices,
                 const float* __restrict__ parts, int64_t parts_ld, Grad<TG> g) {
+  let_next_start();
+  wait_for_previous();
   const int chunk = blockIdx.x / slices;
   const int64_t e0 = static_cast<int64_t>(chunk) * kRun, e1 = e0 + kRun;
   if (e1 >= n) return;
@@ -365,10 +373,9 @@ cudaError_t launch_embed(const lst_matrix* table, const lst_indices* tokens, con
     const int64_t rows = out->rows - r0 < rows_max ? out->rows - r0 : rows_max;
     const unsigned grid = static_cast<unsigned>(ops_ceil_div(rows * units, 256));
     auto k = vec ? embed_kernel<TI, TO, true> : embed_kernel<TI, TO, false>;
-    k<<<grid, 256, 0, stream>>>(static_cast<const TI*>(table->data), table->stride, tokens->data, tokens->bits == 64,
+    const cudaError_t err = launch_chained(k, dim3(grid), dim3(256), 0, stream, static_cast<const TI*>(table->data), table->stride, tokens->data, tokens->bits == 64,
                                 static_cast<TO*>(out->data), out->stride, static_cast<int>(out->cols), table->rows,
                                 static_cast<uint32_t>(units), static_cast<uint32_t>(rows), r0, scale);
-    const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
@@ -417,17 +424,15 @@ cudaError_t launch_grad(const lst_matrix* dout, const lst_matrix* grad, const Gr
   const Grad<TG> g = {static_cast<TG*>(grad->data), grad->stride, scale, accumulate};
   if (sum_blocks + zero_blocks > 0) {
     auto k = vec ? sum_kernel<TD, TG, true> : sum_kernel<TD, TG, false>;
-    k<<<static_cast<unsigned>(sum_blocks + zero_blocks), kSumThreads, 0, stream>>>(
+    const cudaError_t err = launch_chained(k, dim3(static_cast<unsigned>(sum_blocks + zero_blocks)), dim3(kSumThreads), 0, stream, 
         static_cast<const TD*>(dout->data), dout->stride, sorted, n, vocab, hidden, static_cast<int>(slices),
         static_cast<int>(sum_blocks), seen, parts, p.parts_ld, g);
-    const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
   if (p.chunks > 1) {
     auto k = vec ? join_kernel<TG, true> : join_kernel<TG, false>;
-    k<<<static_cast<unsigned>(sum_blocks), kSumThreads, 0, stream>>>(sorted, n, vocab, hidden, static_cast<int>(slices),
+    return launch_chained(k, dim3(static_cast<unsigned>(sum_blocks)), dim3(kSumThreads), 0, stream, sorted, n, vocab, hidden, static_cast<int>(slices),
                                                                      parts, p.parts_ld, g);
-    return cudaGetLastError();
   }
   return cudaSuccess;
 }
@@ -486,12 +491,11 @@ extern "C" lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* 
   // the largest case (10-bit digits) needs 139,264 bytes; a function attribute
   // is per device, so it is set on every call (host only, under a microsecond)
   LST_TRY_CUDA(cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), who);
-  sort_kernel<<<kSortCtas, kSortThreads, smem, s>>>(tokens->data, tokens->bits == 64, static_cast<int>(dout->rows),
+  LST_TRY_CUDA(launch_chained(sort_kernel, dim3(kSortCtas), dim3(kSortThreads), smem, s, tokens->data, tokens->bits == 64, static_cast<int>(dout->rows),
                                                     static_cast<int>(grad->rows), p.passes, p.digit_bits,
                                                     reinterpret_cast<uint2*>(ws + p.buf_off[0]),
                                                     reinterpret_cast<uint2*>(ws + p.buf_off[1]),
-                                                    reinterpret_cast<uint32_t*>(ws + p.seen_off));
-  LST_TRY_CUDA(cudaGetLastError(), who);
+                                                    reinterpret_cast<uint32_t*>(ws + p.seen_off)), who);
   const int kind = (dout->dtype == LST_F32 ? 2 : 0) + (grad->dtype == LST_F32 ? 1 : 0);
   cudaError_t err;
   switch (kind) {

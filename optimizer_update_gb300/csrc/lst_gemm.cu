@@ -10,13 +10,16 @@
 //   warp 1     one thread of the leading CTA issues the MMAs,
 //   warps 2-9  take finished accumulators from tensor memory: two warps per 32
 //              rows, one for each half of the tile's columns.
-// Two accumulators of 256 columns alternate, so the epilogue of a tile runs
-// under the main loop of the next. Tiles are dealt to the pairs in a fixed
+// Two accumulators alternate, so the epilogue of a tile runs under the main
+// loop of the next. Tiles are dealt to the pairs in a fixed
 // order: every result is formed by one pair in one order of additions.
+// Products that have fewer tiles than the GPU has pairs run with tiles of 256 x
+// 128: twice the pairs at work, half the time to a tile's end.
 #include "lst_gemm.h"
 
 #include <mutex>
 
+#include "lst_ops.h"
 #include "lst_tc.cuh"
 
 namespace lst {
@@ -25,13 +28,12 @@ namespace {
 
 constexpr int kTileK = 64;
 constexpr int kStages = 6;
-constexpr int kOperandBytes = 128 * kTileK * 2;   // one CTA's share of A or of B
-constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kABytes = 128 * kTileK * 2;  // one CTA's rows of A
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kBarriers = 2 * kStages + 4;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024 + 8 * kBarriers + 16;
-constexpr uint32_t kTmemColumns = 512;
+__host__ __device__ constexpr int b_bytes(int tile_n) { return tile_n / 2 * kTileK * 2; }  // one CTA's half of B
+__host__ __device__ constexpr int smem_bytes(int tile_n) { return kStages * (kABytes + b_bytes(tile_n)) + 1024 + 8 * kBarriers + 16; }
 
 __device__ int g_gemm_error;
 
@@ -40,14 +42,18 @@ struct Shape {
   int32_t k_blocks, k_per_split, splits;
   int32_t tiles_m, tiles_n, tiles;  // tiles: of one matrix and one split
   int32_t symmetric;
+  int32_t a_mn, b_mn;  // operand is MN-major in memory
   int32_t first_tile;
 };
 
-template <class Params>
+struct Nothing {};
+
+template <class Epi>
 struct Args {
   CUtensorMap a[kGemmMaxProblems], b[kGemmMaxProblems];
   Shape shape[kGemmMaxProblems];
-  Params epi[kGemmMaxProblems];
+  typename Epi::Params epi[kGemmMaxProblems];
+  typename Epi::Table table;
   int32_t count, total_tiles;
 };
 
@@ -58,8 +64,8 @@ struct Tile {
 // Tiles of a matrix go down groups of 8 tile rows, column by column: the tiles
 // in flight share 8 row panels of A and a few column panels of B, which stay
 // in L2. A symmetric result has the tiles of its upper triangle, row by row.
-template <class Params>
-__device__ __forceinline__ Tile decode(const Args<Params>& g, int t) {
+template <int kTileN, class Epi>
+__device__ __forceinline__ Tile decode(const Args<Epi>& g, int t) {
   Tile r;
   int p = 0;
   while (p + 1 < g.count && t >= g.shape[p + 1].first_tile) ++p;
@@ -71,13 +77,14 @@ __device__ __forceinline__ Tile decode(const Args<Params>& g, int t) {
   r.batch = matrix / s.splits;
   r.split = matrix - r.batch * s.splits;
   if (s.symmetric) {
+    constexpr int kAcross = kGemmTile / kTileN;
     int row = 0;
-    while (i >= s.tiles_n - row) {
-      i -= s.tiles_n - row;
+    while (i >= s.tiles_n - kAcross * row) {
+      i -= s.tiles_n - kAcross * row;
       ++row;
     }
     r.tm = row;
-    r.tn = row + i;
+    r.tn = kAcross * row + i;
   } else {
     const int per_group = 8 * s.tiles_n;
     const int group = i / per_group;
@@ -92,8 +99,8 @@ __device__ __forceinline__ Tile decode(const Args<Params>& g, int t) {
 }
 
 // ---- epilogues ---------------------------------------------------------------
-// Each warp calls run() with its accumulator address (32 lanes = 32 rows, 128
-// columns); `release` must be called once, by all lanes, when the accumulator
+// Each warp calls run() with its accumulator address (32 lanes = 32 rows, kCols
+// = half a tile's columns); `release` must be called once, by all lanes, when the accumulator
 // has been read.
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
@@ -132,6 +139,7 @@ __device__ __forceinline__ void store_row32(uint16_t* p, const uint32_t (&w)[16]
 
 struct StoreEpilogue {
   using Params = StoreParams;
+  using Table = Nothing;
   static __device__ __forceinline__ void store(const Params& e, const Shape& s, const Tile& t, uint16_t* out,
                                                const uint16_t* c, bool bf16, bool mirror, int row, int col,
                                                float (&v)[32]) {
@@ -163,23 +171,24 @@ struct StoreEpilogue {
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack16(v[2 * i], v[2 * i + 1], bf16);
-    if (!e.transposed) store_row32(out + static_cast<int64_t>(row) * e.ld + col, w, left, e.vec);
-    if (e.transposed || mirror) {
+    store_row32(out + static_cast<int64_t>(row) * e.ld + col, w, left, e.vec);
+    if (mirror) {
       uint16_t* q = out + static_cast<int64_t>(col) * e.ld + row;
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         if (i < left) q[static_cast<int64_t>(i) * e.ld] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
     }
   }
-  template <class Release>
-  static __device__ __forceinline__ void run(const Params& e, const Shape& s, const Tile& t, int row, int col0,
-                                             uint32_t tmem, Release release) {
+  template <int kCols, class Release>
+  static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
+                                             int col0, uint32_t tmem, Release release) {
     const bool bf16 = e.bf16 != 0;
-    const bool mirror = s.symmetric && t.tm != t.tn;
+    constexpr int kAcross = kGemmTile / (2 * kCols);  // tiles of a diagonal block are formed whole
+    const bool mirror = s.symmetric && t.tn >= kAcross * (t.tm + 1);
     uint16_t* const out = static_cast<uint16_t*>(e.out) + t.batch * e.batch_stride;
     const uint16_t* const c = e.c ? static_cast<const uint16_t*>(e.c) + t.batch * e.batch_stride : nullptr;
 #pragma unroll 1
-    for (int chunk = 0; chunk < 4; ++chunk) {
+    for (int chunk = 0; chunk < kCols / 32; ++chunk) {
       const int col = col0 + 32 * chunk;
       if (col >= s.n) break;
       float v[32];
@@ -188,18 +197,101 @@ struct StoreEpilogue {
       tc::tmem_ld_wait();
       if (row < s.m) store(e, s, t, out, c, bf16, mirror, row, col, v);
     }
+    __syncwarp();
+    release();
+  }
+};
+
+// The Muon update of the weights by a tile of the orthogonalised matrix.
+struct UpdateEpilogue {
+  using Params = UpdateParams;
+  using Table = UpdateTable;
+  static __device__ __forceinline__ void store(const Params& e, float step, void* w, uint16_t* w16, int left,
+                                               const float (&v)[32]) {
+    float x[32];
+    const bool wide = left >= 32 && e.vec >= 16;
+    if (e.format == LST_L12_BF16) {
+      const uint16_t* p = static_cast<const uint16_t*>(w);
+      if (wide) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 u = reinterpret_cast<const uint4*>(p)[j];
+          const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[8 * j + i] = unpack16(static_cast<uint16_t>(q[i >> 1] >> (16 * (i & 1))), true);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = i < left ? unpack16(p[i], true) : 0.0f;
+      }
+    } else {
+      const float* p = static_cast<const float*>(w);
+      if (wide) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 u = reinterpret_cast<const float4*>(p)[j];
+          x[4 * j] = u.x, x[4 * j + 1] = u.y, x[4 * j + 2] = u.z, x[4 * j + 3] = u.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = i < left ? p[i] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __fsub_rn(__fmul_rn(x[i], e.decay), __fmul_rn(step, v[i]));
+    if (e.format != LST_L12_BF16) {
+      float* p = static_cast<float*>(w);
+      if (wide) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          reinterpret_cast<float4*>(p)[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < left) p[i] = x[i];
+      }
+    }
+    if (e.format != LST_L16_FP32) {
+      uint32_t q[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) q[i] = pack16(x[2 * i], x[2 * i + 1], true);
+      store_row32(e.format == LST_L12_BF16 ? static_cast<uint16_t*>(w) : w16, q, left, e.vec);
+    }
+  }
+  template <int kCols, class Release>
+  static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
+                                             int col0, uint32_t tmem, Release release) {
+    char* const w = static_cast<char*>(table.w[e.first + t.batch]);
+    uint16_t* const w16 = table.w16[e.first + t.batch];
+    const float step = table.step[e.first + t.batch];
+    const int size = e.format == LST_L12_BF16 ? 2 : 4;
+#pragma unroll 1
+    for (int chunk = 0; chunk < kCols / 32; ++chunk) {
+      const int col = col0 + 32 * chunk;
+      if (col >= s.n) break;
+      float v[32];
+      __syncwarp();
+      tc::tmem_ld32(tmem + 32 * chunk, v);
+      tc::tmem_ld_wait();
+      if (row < s.m) {
+        const int64_t i = static_cast<int64_t>(row) * e.ld + col;
+        store(e, step, w + i * size, w16 ? w16 + i : nullptr, s.n - col, v);
+      }
+    }
+    __syncwarp();
     release();
   }
 };
 
 struct PartialEpilogue {
   using Params = PartialParams;
-  template <class Release>
-  static __device__ __forceinline__ void run(const Params& e, const Shape& s, const Tile& t, int row, int col0,
-                                             uint32_t tmem, Release release) {
+  using Table = Nothing;
+  template <int kCols, class Release>
+  static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
+                                             int col0, uint32_t tmem, Release release) {
     float* const out = e.out + t.split * e.split_stride + static_cast<int64_t>(row) * e.ld;
 #pragma unroll 1
-    for (int chunk = 0; chunk < 4; ++chunk) {
+    for (int chunk = 0; chunk < kCols / 32; ++chunk) {
       const int col = col0 + 32 * chunk;
       if (col >= s.n) break;
       float v[32];
@@ -232,9 +324,11 @@ struct PartialEpilogue {
 // largest) saturates.
 struct XentEpilogue {
   using Params = XentParams;
-  template <class Release>
-  static __device__ __forceinline__ void run(const Params& e, const Shape& s, const Tile& t, int row, int col0,
-                                             uint32_t tmem, Release release) {
+  using Table = Nothing;
+  template <int kCols, class Release>
+  static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
+                                             int col0, uint32_t tmem, Release release) {
+    static_assert(kCols == 128, "statistics are per 128 columns");
     if (col0 >= s.n) {
       release();
       return;
@@ -293,9 +387,11 @@ struct XentEpilogue {
 };
 
 // ---- the kernel ----------------------------------------------------------------
-template <class Epi, bool kBf16, bool kAMn, bool kBMn>
+template <class Epi, bool kBf16, int kTileN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    gemm_kernel(const __grid_constant__ Args<typename Epi::Params> g) {
+    gemm_kernel(const __grid_constant__ Args<Epi> g) {
+  constexpr int kBBytes = b_bytes(kTileN), kStageBytes = kABytes + kBBytes;
+  constexpr uint32_t kTmemColumns = 2 * kTileN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t bars = base + kStages * kStageBytes;
@@ -305,6 +401,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_rank();
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+
+  let_next_start();
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -328,6 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
+  wait_for_previous();
 
   bool ok = true;
   if (warp == 0) {
@@ -335,26 +434,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       for (int t = cluster; t < g.total_tiles && ok; t += clusters) {
-        const Tile tile = decode(g, t);
+        const Tile tile = decode<kTileN>(g, t);
         const CUtensorMap* ma = &g.a[tile.problem];
         const CUtensorMap* mb = &g.b[tile.problem];
         const int m0 = tile.tm * kGemmTile + 128 * static_cast<int>(rank);
-        const int n0 = tile.tn * kGemmTile + 128 * static_cast<int>(rank);
+        const int n0 = tile.tn * kTileN + kTileN / 2 * static_cast<int>(rank);
+        const bool a_mn = g.shape[tile.problem].a_mn, b_mn = g.shape[tile.problem].b_mn;
         for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
           ok = tc::mbar_wait(empty + 8 * stage, phase ^ 1);
           if (!ok) break;
-          const uint32_t sa = base + stage * kStageBytes, sb = sa + kOperandBytes;
+          const uint32_t sa = base + stage * kStageBytes, sb = sa + kABytes;
           if (rank == 0) tc::mbar_expect_tx(full + 8 * stage, 2 * kStageBytes);
           const uint32_t bar = tc::map_to_rank(full + 8 * stage, 0);
-          if (kAMn) {
+          if (a_mn) {
             tc::tma_load_3d_pair(sa, ma, bar, m0, kb * kTileK, tile.batch);
-            tc::tma_load_3d_pair(sa + kOperandBytes / 2, ma, bar, m0 + 64, kb * kTileK, tile.batch);
+            tc::tma_load_3d_pair(sa + kABytes / 2, ma, bar, m0 + 64, kb * kTileK, tile.batch);
           } else {
             tc::tma_load_3d_pair(sa, ma, bar, kb * kTileK, m0, tile.batch);
           }
-          if (kBMn) {
+          if (b_mn) {
             tc::tma_load_3d_pair(sb, mb, bar, n0, kb * kTileK, tile.batch);
-            tc::tma_load_3d_pair(sb + kOperandBytes / 2, mb, bar, n0 + 64, kb * kTileK, tile.batch);
+            if (kTileN == 256) tc::tma_load_3d_pair(sb + kBBytes / 2, mb, bar, n0 + 64, kb * kTileK, tile.batch);
           } else {
             tc::tma_load_3d_pair(sb, mb, bar, kb * kTileK, n0, tile.batch);
           }
@@ -367,24 +467,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && tc::elect_one()) {
-      constexpr uint32_t idesc = tc::instr_desc(kGemmTile, kGemmTile, kBf16, kAMn, kBMn);
-      // one MMA is 16 deep in K: 32 bytes along a K-major row, 16 rows of 128
-      // bytes in the MN-major order (descriptor units of 16 bytes)
-      constexpr uint64_t step_a = kAMn ? 128 : 2, step_b = kBMn ? 128 : 2;
       int stage = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
       for (int t = cluster; t < g.total_tiles && ok; t += clusters) {
-        const Tile tile = decode(g, t);
+        const Tile tile = decode<kTileN>(g, t);
         ok = tc::mbar_wait(tempty + 8 * buf, tphase ^ 1);
         if (!ok) break;
         tc::fence_after();
-        const uint32_t d = tmem + kGemmTile * buf;
+        const uint32_t d = tmem + kTileN * buf;
+        const bool a_mn = g.shape[tile.problem].a_mn, b_mn = g.shape[tile.problem].b_mn;
+        const uint32_t idesc = tc::instr_desc(kGemmTile, kTileN, kBf16, a_mn, b_mn);
+        // one MMA is 16 deep in K: 32 bytes along a K-major row, 16 rows of 128
+        // bytes in the MN-major order (descriptor units of 16 bytes)
+        const uint64_t step_a = a_mn ? 128 : 2, step_b = b_mn ? 128 : 2;
         for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
           ok = tc::mbar_wait(full + 8 * stage, phase);
           if (!ok) break;
           tc::fence_after();
           const uint32_t sa = base + stage * kStageBytes;
-          const uint64_t da = tc::smem_desc(sa, kAMn), db = tc::smem_desc(sa + kOperandBytes, kBMn);
+          const uint64_t da = tc::smem_desc(sa, a_mn), db = tc::smem_desc(sa + kABytes, b_mn);
 #pragma unroll
           for (int k = 0; k < kTileK / 16; ++k)
             tc::mma_f16_pair(d, da + step_a * k, db + step_b * k, idesc, kb != tile.kb0 || k != 0);
@@ -404,15 +505,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int buf = 0;
     uint32_t tphase = 0;
     for (int t = cluster; t < g.total_tiles; t += clusters) {
-      const Tile tile = decode(g, t);
+      const Tile tile = decode<kTileN>(g, t);
       ok = __all_sync(0xffffffffu, tc::mbar_wait(tfull + 8 * buf, tphase));
       if (!ok) break;
       tc::fence_after();
       const int row = tile.tm * kGemmTile + 128 * static_cast<int>(rank) + 32 * quad + lane;
-      const int col0 = tile.tn * kGemmTile + 128 * half;
-      const uint32_t addr = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kGemmTile * buf + 128 * half;
+      const int col0 = tile.tn * kTileN + kTileN / 2 * half;
+      const uint32_t addr = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kTileN * buf + kTileN / 2 * half;
       const uint32_t bar = tempty + 8 * buf;
-      Epi::run(g.epi[tile.problem], g.shape[tile.problem], tile, row, col0, addr, [&]() {
+      Epi::template run<kTileN / 2>(g.epi[tile.problem], g.table, g.shape[tile.problem], tile, row, col0, addr, [&]() {
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(bar, 0));
@@ -457,16 +558,16 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Tile of 64 contiguous elements x 128 rows (K-major: 64 deep in K, 128 rows)
-// or x 64 rows (MN-major: 64 wide, 64 deep in K).
-bool make_map(CUtensorMap* map, const GemmOperand& o, bool bf16, bool mn_major) {
+// Tile of 64 contiguous elements x `rows` rows (K-major: 64 deep in K) or x 64
+// rows (MN-major: 64 wide, 64 deep in K).
+bool make_map(CUtensorMap* map, const GemmOperand& o, bool bf16, int rows) {
   EncodeTiled fn = encode_tiled();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.inner), static_cast<cuuint64_t>(o.outer),
                               static_cast<cuuint64_t>(o.batch)};
   const cuuint64_t pitch = static_cast<cuuint64_t>(o.pitch) * 2;
   const cuuint64_t strides[2] = {pitch, o.batch > 1 ? static_cast<cuuint64_t>(o.batch_pitch) * 2 : pitch};
-  const cuuint32_t box[3] = {64u, mn_major ? 64u : 128u, 1u};
+  const cuuint32_t box[3] = {64u, o.transposed ? 64u : static_cast<cuuint32_t>(rows), 1u};
   const cuuint32_t one[3] = {1u, 1u, 1u};
   return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
             const_cast<void*>(o.ptr), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -477,9 +578,10 @@ bool make_map(CUtensorMap* map, const GemmOperand& o, bool bf16, bool mn_major) 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // CTA pairs of this kernel that can be resident at once; 0 when the query fails.
-template <class Epi, bool kBf16, bool kAMn, bool kBMn>
+template <class Epi, bool kBf16, int kTileN>
 int resident_pairs() {
-  auto kernel = gemm_kernel<Epi, kBf16, kAMn, kBMn>;
+  auto kernel = gemm_kernel<Epi, kBf16, kTileN>;
+  constexpr int kSmemBytes = smem_bytes(kTileN);
   constexpr int kMaxDevices = 16;
   static std::mutex mu;
   static int cached[kMaxDevices] = {};
@@ -504,24 +606,27 @@ int resident_pairs() {
   return cached[dev] = pairs;
 }
 
-template <class Epi>
-const typename Epi::Params& params_of(const GemmProblem& p);
-template <>
-const StoreParams& params_of<StoreEpilogue>(const GemmProblem& p) { return p.store; }
-template <>
-const PartialParams& params_of<PartialEpilogue>(const GemmProblem& p) { return p.partial; }
-template <>
-const XentParams& params_of<XentEpilogue>(const GemmProblem& p) { return p.xent; }
+void set_params(StoreParams* e, Nothing*, const GemmProblem& p, const UpdateTable*) { *e = p.store; }
+void set_params(PartialParams* e, Nothing*, const GemmProblem& p, const UpdateTable*) { *e = p.partial; }
+void set_params(XentParams* e, Nothing*, const GemmProblem& p, const UpdateTable*) { *e = p.xent; }
+void set_params(UpdateParams* e, UpdateTable* t, const GemmProblem& p, const UpdateTable* updates) {
+  *e = p.update;
+  for (int64_t i = p.update.first; i < p.update.first + p.batch; ++i) {
+    t->w[i] = updates->w[i];
+    t->w16[i] = updates->w16[i];
+    t->step[i] = updates->step[i];
+  }
+}
 
-template <class Epi, bool kBf16, bool kAMn, bool kBMn>
-cudaError_t launch(const GemmProblem* problems, int count, cudaStream_t stream) {
-  auto kernel = gemm_kernel<Epi, kBf16, kAMn, kBMn>;
-  const int pairs = resident_pairs<Epi, kBf16, kAMn, kBMn>();
+template <class Epi, bool kBf16, int kTileN>
+cudaError_t launch(const GemmProblem* problems, int count, cudaStream_t stream, const UpdateTable* updates) {
+  auto kernel = gemm_kernel<Epi, kBf16, kTileN>;
+  const int pairs = resident_pairs<Epi, kBf16, kTileN>();
   if (pairs <= 0) {
     const cudaError_t err = cudaGetLastError();
     return err != cudaSuccess ? err : cudaErrorInvalidDevice;
   }
-  Args<typename Epi::Params> g;
+  Args<Epi> g;
   int64_t total = 0;
   int used = 0;
   for (int i = 0; i < count; ++i) {
@@ -534,36 +639,52 @@ cudaError_t launch(const GemmProblem* problems, int count, cudaStream_t stream) 
     s.k_per_split = static_cast<int32_t>(ceil_div(s.k_blocks, p.splits));
     s.splits = static_cast<int32_t>(ceil_div(s.k_blocks, s.k_per_split));
     s.tiles_m = static_cast<int32_t>(ceil_div(p.m, kGemmTile));
-    s.tiles_n = static_cast<int32_t>(ceil_div(p.n, kGemmTile));
+    s.tiles_n = static_cast<int32_t>(ceil_div(p.n, kTileN));
     s.symmetric = p.symmetric;
-    s.tiles = p.symmetric ? s.tiles_n * (s.tiles_n + 1) / 2 : s.tiles_m * s.tiles_n;
+    s.a_mn = p.a.transposed;
+    s.b_mn = p.b.transposed;
+    s.tiles = s.tiles_m * s.tiles_n;
+    if (p.symmetric) {
+      s.tiles = 0;
+      for (int i = 0; i < s.tiles_m; ++i) s.tiles += s.tiles_n - kGemmTile / kTileN * i;
+    }
     s.first_tile = static_cast<int32_t>(total);
     total += static_cast<int64_t>(s.tiles) * s.splits * p.batch;
     if (total > INT32_MAX / 2) return cudaErrorInvalidValue;
-    if (!make_map(&g.a[used], p.a, kBf16, kAMn) || !make_map(&g.b[used], p.b, kBf16, kBMn))
-      return cudaErrorInvalidPitchValue;
-    g.epi[used] = params_of<Epi>(p);
+    if (!make_map(&g.a[used], p.a, kBf16, 128) || !make_map(&g.b[used], p.b, kBf16, kTileN / 2)) return cudaErrorInvalidPitchValue;
+    set_params(&g.epi[used], &g.table, p, updates);
     ++used;
   }
   if (used == 0) return cudaSuccess;
   g.count = used;
   g.total_tiles = static_cast<int32_t>(total);
   const unsigned grid = 2u * static_cast<unsigned>(total < pairs ? total : pairs);
-  kernel<<<grid, kThreads, kSmemBytes, stream>>>(g);
-  return cudaGetLastError();
+  return launch_chained(kernel, dim3(grid), dim3(kThreads), smem_bytes(kTileN), stream, g);
+}
+
+// Fewer 256 x 256 tiles than pairs: half as wide (see the top of the file).
+template <class Epi, bool kBf16>
+cudaError_t launch_fit(const GemmProblem* problems, int count, cudaStream_t stream, const UpdateTable* updates) {
+  int64_t tiles = 0;
+  for (int i = 0; i < count; ++i) {
+    const GemmProblem& p = problems[i];
+    const int64_t tm = ceil_div(p.m, kGemmTile), tn = ceil_div(p.n, kGemmTile);
+    tiles += (p.symmetric ? tn * (tn + 1) / 2 : tm * tn) * p.batch * p.splits;
+  }
+  return tiles < 76 ? launch<Epi, kBf16, 128>(problems, count, stream, updates)
+                    : launch<Epi, kBf16, 256>(problems, count, stream, updates);
 }
 
 }  // namespace
 
-cudaError_t launch_gemm(GemmKind kind, const GemmProblem* p, int count, cudaStream_t stream) {
+cudaError_t launch_gemm(GemmKind kind, const GemmProblem* p, int count, cudaStream_t stream, const UpdateTable* updates) {
   if (count > kGemmMaxProblems) return cudaErrorInvalidValue;
   switch (kind) {
-    case GEMM_NS_SYM: return launch<StoreEpilogue, false, false, false>(p, count, stream);
-    case GEMM_NS_APPLY: return launch<StoreEpilogue, false, false, true>(p, count, stream);
-    case GEMM_LOGITS: return launch<XentEpilogue, true, false, false>(p, count, stream);
-    case GEMM_DX: return launch<StoreEpilogue, true, false, true>(p, count, stream);
-    case GEMM_DX_SPLIT: return launch<PartialEpilogue, true, false, true>(p, count, stream);
-    case GEMM_DW: return launch<StoreEpilogue, true, true, true>(p, count, stream);
+    case GEMM_F16: return launch_fit<StoreEpilogue, false>(p, count, stream, nullptr);
+    case GEMM_F16_UPDATE: return launch_fit<UpdateEpilogue, false>(p, count, stream, updates);
+    case GEMM_BF16: return launch_fit<StoreEpilogue, true>(p, count, stream, nullptr);
+    case GEMM_BF16_PARTS: return launch<PartialEpilogue, true, 256>(p, count, stream, nullptr);
+    case GEMM_BF16_XENT: return launch<XentEpilogue, true, 256>(p, count, stream, nullptr);
   }
   return cudaErrorInvalidValue;
 }

@@ -9,10 +9,12 @@ namespace lst {
 
 // A 16-bit operand in device memory: `inner` contiguous elements, `outer` rows
 // `pitch` elements apart, `batch` such matrices `batch_pitch` elements apart.
+// The summed dimension is the inner one, or with `transposed` the outer one.
 // Base and pitches are multiples of 16 bytes (a rule of the tile loads).
 struct GemmOperand {
   const void* ptr;
   int64_t inner, outer, pitch;
+  bool transposed = false;
   int64_t batch = 1, batch_pitch = 0;
 };
 
@@ -24,7 +26,22 @@ struct StoreParams {
   const void* c;
   int64_t ld, batch_stride;
   float alpha, beta, diag;
-  int32_t bf16, transposed, vec;
+  int32_t bf16, vec;
+};
+
+// w = w * decay - step * acc for the matrices of the batch, with w, the derived
+// bf16 weight (or null) and step of matrix b at entry first + b of the launch's
+// table. `format`: bf16 w, fp32 w with derived bf16, fp32 w (lst_format).
+constexpr int kGemmMaxUpdates = 64;
+struct UpdateTable {
+  void* w[kGemmMaxUpdates];
+  uint16_t* w16[kGemmMaxUpdates];
+  float step[kGemmMaxUpdates];
+};
+struct UpdateParams {
+  int64_t ld;
+  int32_t first, format, vec;
+  float decay;
 };
 
 // fp32 partial sums of a K range: out[split][row][col], added to what is there
@@ -47,29 +64,30 @@ struct XentParams {
 };
 
 enum GemmKind {
-  GEMM_NS_SYM,    // fp16, A [m,k] and B [n,k] both K-contiguous, StoreParams
-  GEMM_NS_APPLY,  // fp16, A [m,k] K-contiguous, B [k,n] n-contiguous, StoreParams
-  GEMM_LOGITS,    // bf16, A [m,k], B [n,k] K-contiguous, XentParams
-  GEMM_DX,        // bf16, A [m,k] K-contiguous, B [k,n] n-contiguous, StoreParams
-  GEMM_DX_SPLIT,  // the same, PartialParams
-  GEMM_DW,        // bf16, A [k,m] m-contiguous, B [k,n] n-contiguous, StoreParams
+  GEMM_F16,         // fp16 operands, StoreParams
+  GEMM_F16_UPDATE,  // fp16 operands, UpdateParams
+  GEMM_BF16,        // bf16 operands, StoreParams
+  GEMM_BF16_PARTS,  // bf16 operands, PartialParams
+  GEMM_BF16_XENT,   // bf16 operands, XentParams
 };
 
 struct GemmProblem {
   GemmOperand a, b;
   int64_t m, n, k, batch = 1;
   bool symmetric = false;  // the result is symmetric: form one triangle of tiles and mirror it
-  int splits = 1;          // K ranges (GEMM_DX_SPLIT)
+  int splits = 1;          // K ranges (GEMM_BF16_PARTS)
   StoreParams store{};
   PartialParams partial{};
   XentParams xent{};
+  UpdateParams update{};
 };
 
 constexpr int kGemmMaxProblems = 8;
 constexpr int kGemmTile = 256;
 
 // One launch over up to kGemmMaxProblems independent products of one kind.
-cudaError_t launch_gemm(GemmKind kind, const GemmProblem* problems, int count, cudaStream_t stream);
+cudaError_t launch_gemm(GemmKind kind, const GemmProblem* problems, int count, cudaStream_t stream,
+                        const UpdateTable* updates = nullptr);
 
 // K ranges that fill the GPU for `tiles` output tiles of `k` elements each.
 int gemm_splits(int64_t tiles, int64_t k);

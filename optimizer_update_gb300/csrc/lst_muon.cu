@@ -1,7 +1,8 @@
 // Newton-Schulz orthogonalisation and the Muon step over packed blocks.
 //
-// Mathematics. With X_0 = U / (|U|_F + eps) (transposed so that m <= n) a step
-// is X <- Q X, Q = a I + b A + c A^2, A = X X^T. All Q and A are polynomials of
+// Mathematics, for a wide matrix (m rows, n >= m columns; a tall one is the
+// same from the other side, X <- X Q with A = X^T X, in its own row order). With
+// X_0 = U / (|U|_F + eps) a step is X <- Q X, Q = a I + b A + c A^2, A = X X^T. All Q and A are polynomials of
 // X_0 X_0^T: symmetric, and they commute. So two steps can share one Gram
 // matrix: with Q_1 from A, the next Gram matrix is A' = Q_1 A Q_1, Q_2 comes
 // from A', and X <- (Q_2 Q_1) X. A pair so formed costs five m x m products and
@@ -45,26 +46,23 @@ constexpr float kScaleX = 16384.0f, kScaleA = 16384.0f, kScaleQ = 8192.0f, kScal
 
 constexpr int kItemsPerLaunch = 32;
 constexpr int kNormBlocks = 512;   // partial sums per matrix
-constexpr int kTile = 64;
+// Inputs of the matrices whose norms are taken together: their second read, to
+// scale them, then comes from L2 (129 MB) for the most part.
+constexpr int64_t kIngestBytes = int64_t(64) << 20;
 
-// One matrix on its way in (u = its values) and out (its orthogonalised form).
+// One matrix on its way in.
 struct Item {
   const void* g;      // gradient, or the matrix itself
   float* mom;         // momentum, or null
-  void* w;            // weight to update, or null
-  uint16_t* w16;      // derived bf16 weight, or null
-  __half* x;          // m x ldx values
-  const __half* o;    // result
+  __half* x;          // rows x ldx values
   double* part;       // kNormBlocks partial sums of squares
   int64_t rows, cols, ld, ldx;
-  int32_t tall;       // rows > cols: x is the transpose
-  float step;         // lr * update scale / kScaleX
 };
 struct ItemTable {
   Item it[kItemsPerLaunch];
 };
 struct MuonScalars {
-  float momentum, decay, eps;
+  float momentum, eps;
   int32_t nesterov;
 };
 
@@ -72,148 +70,148 @@ __device__ __forceinline__ float load_in(const void* p, int64_t i, bool f32) {
   return f32 ? static_cast<const float*>(p)[i]
              : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
 }
+template <bool F32>
+__device__ __forceinline__ void load_in8(const void* p, int64_t i, float (&v)[8]) {
+  if (F32) {
+    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
+    v[4] = bf16_lo(a.z), v[5] = bf16_hi(a.z), v[6] = bf16_lo(a.w), v[7] = bf16_hi(a.w);
+  }
+}
 
 // u of one element; `m` is the momentum already updated.
 __device__ __forceinline__ float muon_u(float g, float m, const MuonScalars& s) {
   return s.nesterov ? __fadd_rn(g, __fmul_rn(s.momentum, m)) : m;
 }
+__device__ __forceinline__ float new_momentum(float m, float g, const MuonScalars& s) {
+  return __fadd_rn(__fmul_rn(s.momentum, m), g);
+}
 
-// m = momentum m + g in place, and the sum of u^2 (in fp32 over a thread's
-// elements of one stride, in fp64 above that). Bound by memory: reads g and m,
-// writes m.
+// Whether every row of the matrix can be read in vectors of 8.
+template <bool MOM>
+__device__ __forceinline__ bool vector_rows(const Item& it) {
+  return it.cols % 8 == 0 && it.ld % 8 == 0 && (reinterpret_cast<uintptr_t>(it.g) & 15) == 0 &&
+         (!MOM || (reinterpret_cast<uintptr_t>(it.mom) & 15) == 0);
+}
+
+// m = momentum m + g in place, and the sum of u^2: in fp32 over a warp's
+// elements, in fp64 over warps and blocks (fp64 is slow on this GPU: one
+// instruction per SM and 16 clocks for a warp, so few threads use it). Bound by
+// memory: reads g and m, writes m.
 template <bool F32, bool MOM>
 __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ ItemTable t, MuonScalars s) {
+  let_next_start();
+  wait_for_previous();
   const Item& it = t.it[blockIdx.y];
-  double sum = 0.0;
-  const bool flat = it.ld == it.cols && (reinterpret_cast<uintptr_t>(it.g) & 15) == 0 &&
-                    (!MOM || (reinterpret_cast<uintptr_t>(it.mom) & 15) == 0);
-  const int64_t total = it.rows * it.cols;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
-  int64_t tail = 0;
-  if (flat) {
-    const int64_t quads = total / 4;
-    tail = quads * 4;
-    for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < quads; q += stride) {
-      float g[4], u[4];
-      if (F32) {
-        const float4 x = static_cast<const float4*>(it.g)[q];
-        g[0] = x.x, g[1] = x.y, g[2] = x.z, g[3] = x.w;
-      } else {
-        const uint2 x = static_cast<const uint2*>(it.g)[q];
-        g[0] = bf16_lo(x.x), g[1] = bf16_hi(x.x), g[2] = bf16_lo(x.y), g[3] = bf16_hi(x.y);
-      }
+  float sum = 0.0f;
+  if (vector_rows<MOM>(it)) {
+    const uint32_t per_row = static_cast<uint32_t>(it.cols / 8);
+    const int64_t total = it.rows * per_row;
+    const bool flat = it.ld == it.cols;
+#pragma unroll 2
+    for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < total; q += static_cast<int64_t>(gridDim.x) * 256) {
+      const int64_t at = flat ? q * 8 : q / per_row * it.ld + q % per_row * 8;
+      float g[8];
+      load_in8<F32>(it.g, at, g);
       if (MOM) {
-        float4 m = reinterpret_cast<float4*>(it.mom)[q];
-        m.x = __fadd_rn(__fmul_rn(s.momentum, m.x), g[0]);
-        m.y = __fadd_rn(__fmul_rn(s.momentum, m.y), g[1]);
-        m.z = __fadd_rn(__fmul_rn(s.momentum, m.z), g[2]);
-        m.w = __fadd_rn(__fmul_rn(s.momentum, m.w), g[3]);
-        reinterpret_cast<float4*>(it.mom)[q] = m;
-        u[0] = muon_u(g[0], m.x, s), u[1] = muon_u(g[1], m.y, s);
-        u[2] = muon_u(g[2], m.z, s), u[3] = muon_u(g[3], m.w, s);
-      } else {
-        u[0] = g[0], u[1] = g[1], u[2] = g[2], u[3] = g[3];
+        float4* p = reinterpret_cast<float4*>(it.mom) + 2 * q;
+        float4 a = p[0], b = p[1];
+        a = make_float4(new_momentum(a.x, g[0], s), new_momentum(a.y, g[1], s), new_momentum(a.z, g[2], s),
+                        new_momentum(a.w, g[3], s));
+        b = make_float4(new_momentum(b.x, g[4], s), new_momentum(b.y, g[5], s), new_momentum(b.z, g[6], s),
+                        new_momentum(b.w, g[7], s));
+        p[0] = a;
+        p[1] = b;
+        const float m[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = muon_u(g[i], m[i], s);
       }
-      sum += static_cast<double>((u[0] * u[0] + u[1] * u[1]) + (u[2] * u[2] + u[3] * u[3]));
+      float x = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x = __fmaf_rn(g[i], g[i], x);
+      sum += x;
+    }
+  } else {
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < it.rows; r += warps) {
+#pragma unroll 4
+      for (int64_t c = lane; c < it.cols; c += 32) {
+        float u = load_in(it.g, r * it.ld + c, F32);
+        if (MOM) {
+          float* p = it.mom + r * it.cols + c;
+          const float m = new_momentum(*p, u, s);
+          *p = m;
+          u = muon_u(u, m, s);
+        }
+        sum = __fmaf_rn(u, u, sum);
+      }
     }
   }
-  for (int64_t i = tail + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += stride) {
-    const int64_t at = it.ld == it.cols ? i : i / it.cols * it.ld + i % it.cols;
-    float u = load_in(it.g, at, F32);
-    if (MOM) {
-      const float m = __fadd_rn(__fmul_rn(s.momentum, it.mom[i]), u);
-      it.mom[i] = m;
-      u = muon_u(u, m, s);
-    }
-    sum += static_cast<double>(u * u);
-  }
-  __shared__ double red[8];
+  __shared__ float red[8];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
     double x = red[0];
-    for (int i = 1; i < 8; ++i) x += red[i];
+    for (int i = 1; i < 8; ++i) x += static_cast<double>(red[i]);
     it.part[blockIdx.x] = x;
   }
 }
 
-// X_0 = u / (|u|_F + eps), in fp16 times kScaleX, transposed where rows > cols.
+// X_0 = u / (|u|_F + eps), in fp16 times kScaleX.
 template <bool F32, bool MOM>
 __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ ItemTable t, MuonScalars s, int parts) {
+  let_next_start();
+  wait_for_previous();
   const Item& it = t.it[blockIdx.y];
-  const int64_t tiles_c = (it.cols + kTile - 1) / kTile, tiles = (it.rows + kTile - 1) / kTile * tiles_c;
-  if (blockIdx.x >= tiles) return;
-  __shared__ double red[8];
-  __shared__ __half tile[kTile][kTile + 2];
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < parts; i += 256) sum += it.part[i];
+  __shared__ float shared_inv;
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < parts; i += 32) sum += it.part[i];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  sum = red[0];
-  for (int i = 1; i < 8; ++i) sum += red[i];
-  const float inv = static_cast<float>(static_cast<double>(kScaleX) / (sqrt(sum) + static_cast<double>(s.eps)));
-  const int c = threadIdx.x & 63, r4 = threadIdx.x >> 6;
-  for (int64_t b = blockIdx.x; b < tiles; b += gridDim.x) {
-    const int64_t r0 = b / tiles_c * kTile, c0 = b % tiles_c * kTile;
-#pragma unroll 4
-    for (int k = 0; k < kTile / 4; ++k) {
-      const int r = r4 + 4 * k;
-      if (r0 + r >= it.rows || c0 + c >= it.cols) continue;
-      float u = load_in(it.g, (r0 + r) * it.ld + c0 + c, F32);
-      if (MOM) u = muon_u(u, it.mom[(r0 + r) * it.cols + c0 + c], s);
-      const __half h = __float2half_rn(u * inv);
-      if (it.tall)
-        tile[r][c] = h;
-      else
-        it.x[(r0 + r) * it.ldx + c0 + c] = h;
-    }
-    if (it.tall) {
-      __syncthreads();
-#pragma unroll 4
-      for (int k = 0; k < kTile / 4; ++k) {
-        const int col = r4 + 4 * k;  // column of the source
-        if (c0 + col < it.cols && r0 + c < it.rows) it.x[(c0 + col) * it.ldx + r0 + c] = tile[c][col];
-      }
-      __syncthreads();
-    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
+    if (threadIdx.x == 0)
+      shared_inv = static_cast<float>(static_cast<double>(kScaleX) / (sqrt(sum) + static_cast<double>(s.eps)));
   }
-}
-
-// w = w decay - step O (and the derived bf16 W). FMT as in lst_device.cuh.
-template <int FMT>
-__global__ void __launch_bounds__(256) apply_kernel(const __grid_constant__ ItemTable t, MuonScalars s) {
-  const Item& it = t.it[blockIdx.y];
-  const int64_t tiles_c = (it.cols + kTile - 1) / kTile, tiles = (it.rows + kTile - 1) / kTile * tiles_c;
-  __shared__ __half tile[kTile][kTile + 2];
-  const int c = threadIdx.x & 63, r4 = threadIdx.x >> 6;
-  for (int64_t b = blockIdx.x; b < tiles; b += gridDim.x) {
-    const int64_t r0 = b / tiles_c * kTile, c0 = b % tiles_c * kTile;
-    if (it.tall) {
-      __syncthreads();
-#pragma unroll 4
-      for (int k = 0; k < kTile / 4; ++k) {
-        const int col = r4 + 4 * k;
-        if (c0 + col < it.cols && r0 + c < it.rows) tile[c][col] = it.o[(c0 + col) * it.ldx + r0 + c];
+  __syncthreads();
+  const float inv = shared_inv;
+  if (vector_rows<MOM>(it)) {
+    const uint32_t per_row = static_cast<uint32_t>(it.cols / 8);
+    const int64_t total = it.rows * per_row;
+#pragma unroll 2
+    for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < total; q += static_cast<int64_t>(gridDim.x) * 256) {
+      const int64_t r = q / per_row, c = (q - r * per_row) * 8;
+      float u[8];
+      load_in8<F32>(it.g, r * it.ld + c, u);
+      if (MOM) {
+        float m[8];
+        load_in8<true>(it.mom, q * 8, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = muon_u(u[i], m[i], s);
       }
-      __syncthreads();
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(u[2 * i] * inv, u[2 * i + 1] * inv);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(it.x + r * it.ldx + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+  } else {
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < it.rows; r += warps) {
 #pragma unroll 4
-    for (int k = 0; k < kTile / 4; ++k) {
-      const int r = r4 + 4 * k;
-      if (r0 + r >= it.rows || c0 + c >= it.cols) continue;
-      const float o = __half2float(it.tall ? tile[r][c] : it.o[(r0 + r) * it.ldx + c0 + c]);
-      const int64_t i = (r0 + r) * it.cols + c0 + c;
-      float w = FMT == F_L12 ? bf16_lo(static_cast<uint16_t*>(it.w)[i]) : static_cast<float*>(it.w)[i];
-      w = __fsub_rn(__fmul_rn(w, s.decay), __fmul_rn(it.step, o));
-      if (FMT == F_L12) {
-        static_cast<__nv_bfloat16*>(it.w)[i] = __float2bfloat16_rn(w);
-      } else {
-        static_cast<float*>(it.w)[i] = w;
-        if (FMT == F_L16M) reinterpret_cast<__nv_bfloat16*>(it.w16)[i] = __float2bfloat16_rn(w);
+      for (int64_t c = lane; c < it.cols; c += 32) {
+        float u = load_in(it.g, r * it.ld + c, F32);
+        if (MOM) u = muon_u(u, it.mom[r * it.cols + c], s);
+        it.x[r * it.ldx + c] = __float2half_rn(u * inv);
       }
     }
   }
@@ -233,6 +231,8 @@ struct AdamTable {
 };
 template <int FMT>
 __global__ void __launch_bounds__(256) adam_kernel(const __grid_constant__ AdamTable t, Scalars s) {
+  let_next_start();
+  wait_for_previous();
   const AdamItem& it = t.it[blockIdx.y];
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < it.n;
        i += static_cast<int64_t>(gridDim.x) * 256) {
@@ -255,14 +255,22 @@ __global__ void __launch_bounds__(256) adam_kernel(const __grid_constant__ AdamT
 // ---- a batch of matrices: buffers and products -----------------------------------
 
 struct Shape2 {
-  int64_t m, n;  // m <= n
+  int64_t rows, cols;
+  int64_t m() const { return rows < cols ? rows : cols; }
+  int64_t n() const { return rows < cols ? cols : rows; }
+  bool operator==(const Shape2& o) const { return rows == o.rows && cols == o.cols; }
+  bool operator<(const Shape2& o) const {
+    return m() != o.m() ? m() < o.m() : n() != o.n() ? n() < o.n() : rows < o.rows;
+  }
 };
 
-// Matrices sorted by (m, n): `groups` of one shape, `classes` of one m. A class
-// keeps three stacks of m x m matrices, a group two stacks of m x n.
+// Matrices in the order of Shape2: `groups` of one shape, `classes` of one m. A
+// class keeps three stacks of m x m matrices, a group two stacks of its shape.
 struct Batch {
   struct Group {
-    int64_t m, n, ldx, first, count, x_off[2], cls, first_in_class;
+    Shape2 s;
+    int64_t ldx, first, count, x_off[2], cls, first_in_class;
+    int64_t x_elems() const { return s.rows * ldx; }
   };
   struct Class {
     int64_t m, lds, count, s_off[3];
@@ -272,8 +280,8 @@ struct Batch {
   int64_t part_off = 0, bytes = 0;
 
   static int64_t ld(int64_t n) { return ops_round_up(n, 64); }
-  static int64_t item_bytes(const Shape2& s) {  // upper bound of what one more matrix adds
-    return 2 * s.m * ld(s.n) * 2 + 3 * s.m * ld(s.m) * 2 + kNormBlocks * 8 + 8 * 256;
+  static int64_t item_bytes(const Shape2& s) {  // upper bound of what one more matrix adds, tall or wide
+    return 2 * std::max(s.rows * ld(s.cols), s.cols * ld(s.rows)) * 2 + 3 * s.m() * ld(s.m()) * 2 + kNormBlocks * 8 + 8 * 256;
   }
 
   void build(const Shape2* shapes, int64_t count) {
@@ -283,17 +291,17 @@ struct Batch {
     part_off = at;
     at += ops_round_up(count * kNormBlocks * 8, 256);
     for (int64_t i = 0; i < count; ++i) {
-      if (classes.empty() || classes.back().m != shapes[i].m) classes.push_back({shapes[i].m, ld(shapes[i].m), 0, {0, 0, 0}});
-      if (groups.empty() || groups.back().m != shapes[i].m || groups.back().n != shapes[i].n)
-        groups.push_back({shapes[i].m, shapes[i].n, ld(shapes[i].n), i, 0, {0, 0}, (int64_t)classes.size() - 1,
-                          classes.back().count});
+      const int64_t m = shapes[i].m();
+      if (classes.empty() || classes.back().m != m) classes.push_back({m, ld(m), 0, {0, 0, 0}});
+      if (groups.empty() || !(groups.back().s == shapes[i]))
+        groups.push_back({shapes[i], ld(shapes[i].cols), i, 0, {0, 0}, (int64_t)classes.size() - 1, classes.back().count});
       groups.back().count++;
       classes.back().count++;
     }
     for (Group& g : groups)
       for (int k = 0; k < 2; ++k) {
         g.x_off[k] = at;
-        at += ops_round_up(g.count * g.m * g.ldx * 2, 256);
+        at += ops_round_up(g.count * g.x_elems() * 2, 256);
       }
     for (Class& c : classes)
       for (int k = 0; k < 3; ++k) {
@@ -320,35 +328,39 @@ struct Runner {
     return cudaSuccess;
   }
 
-  GemmOperand x_operand(const Batch::Group& g, int k) const {
-    return {ws + g.x_off[k], g.n, g.m, g.ldx, g.count, g.m * g.ldx};
+  // Matrices first .. first + count of a group; `transposed` as in GemmOperand.
+  GemmOperand x_operand(const Batch::Group& g, int k, int64_t first, int64_t count, bool transposed) const {
+    return {ws + g.x_off[k] + first * g.x_elems() * 2, g.s.cols, g.s.rows, g.ldx, transposed, count, g.x_elems()};
   }
   GemmOperand s_operand(const Batch::Class& c, int k, int64_t first, int64_t count) const {
-    return {ws + c.s_off[k] + first * c.m * c.lds * 2, c.m, c.m, c.lds, count, c.m * c.lds};
+    return {ws + c.s_off[k] + first * c.m * c.lds * 2, c.m, c.m, c.lds, false, count, c.m * c.lds};
   }
   static StoreParams s_store(const Batch::Class& c, void* out, const void* cc, float alpha, float beta, float diag) {
-    return {out, cc, c.lds, c.m * c.lds, alpha, beta, diag, 0, 0, 32};
+    return {out, cc, c.lds, c.m * c.lds, alpha, beta, diag, 0, 32};
   }
 
-  // A = X X^T into stack 0
+  // A = X X^T (or X^T X) into stack 0
   cudaError_t gram(int x) {
-    for (const Batch::Group& g : b.groups) {
+    // the longest sums first: the short tiles then even out the pairs' ends
+    for (size_t i = b.groups.size(); i-- > 0;) {
+      const Batch::Group& g = b.groups[i];
       const Batch::Class& c = b.classes[(size_t)g.cls];
       GemmProblem p;
-      p.a = p.b = x_operand(g, x);
-      p.m = p.n = g.m;
-      p.k = g.n;
+      p.a = p.b = x_operand(g, x, 0, g.count, g.s.rows > g.s.cols);
+      p.m = p.n = c.m;
+      p.k = g.s.n();
       p.batch = g.count;
       p.symmetric = true;
       p.store = s_store(c, ws + c.s_off[0] + g.first_in_class * c.m * c.lds * 2, nullptr, kScaleA / (kScaleX * kScaleX),
                         0.0f, 0.0f);
       pending.push_back(p);
     }
-    return flush(GEMM_NS_SYM);
+    return flush(GEMM_F16);
   }
   // out = alpha s1 s2 + beta s3 + diag I, all symmetric and commuting
   cudaError_t product(int out, int s1, int s2, float alpha, int s3 = -1, float beta = 0.0f, float diag = 0.0f) {
-    for (const Batch::Class& c : b.classes) {
+    for (size_t i = b.classes.size(); i-- > 0;) {
+      const Batch::Class& c = b.classes[i];
       GemmProblem p;
       p.a = s_operand(c, s1, 0, c.count);
       p.b = s_operand(c, s2, 0, c.count);
@@ -358,27 +370,33 @@ struct Runner {
       p.store = s_store(c, ws + c.s_off[out], s3 < 0 ? nullptr : ws + c.s_off[s3], alpha, beta, diag);
       pending.push_back(p);
     }
-    return flush(GEMM_NS_SYM);
+    return flush(GEMM_F16);
   }
   // stack `out` = Q of the Gram matrices in stack `a`
   cudaError_t polynomial(int out, int a) {
     return product(out, a, a, kC * kScaleQ / (kScaleA * kScaleA), a, kB * kScaleQ / kScaleA, kA * kScaleQ);
   }
+  // S X (or X S) of matrices first .. first + count of a group, without a destination.
+  GemmProblem applied(const Batch::Group& g, int s, int x, int64_t first, int64_t count) const {
+    const Batch::Class& c = b.classes[(size_t)g.cls];
+    const bool tall = g.s.rows > g.s.cols;
+    GemmProblem p;
+    p.a = tall ? x_operand(g, x, first, count, false) : s_operand(c, s, g.first_in_class + first, count);
+    p.b = tall ? s_operand(c, s, g.first_in_class + first, count) : x_operand(g, x, first, count, true);
+    p.m = g.s.rows;
+    p.n = g.s.cols;
+    p.k = c.m;
+    p.batch = count;
+    return p;
+  }
   // X_out = S X_in, S in stack s stored times `scale`
   cudaError_t apply(int s, float scale, int x_in, int x_out) {
-    for (const Batch::Group& g : b.groups) {
-      const Batch::Class& c = b.classes[(size_t)g.cls];
-      GemmProblem p;
-      p.a = s_operand(c, s, g.first_in_class, g.count);
-      p.b = x_operand(g, x_in);
-      p.m = g.m;
-      p.n = g.n;
-      p.k = g.m;
-      p.batch = g.count;
-      p.store = {ws + g.x_off[x_out], nullptr, g.ldx, g.m * g.ldx, 1.0f / scale, 0.0f, 0.0f, 0, 0, 32};
-      pending.push_back(p);
+    for (size_t i = b.groups.size(); i-- > 0;) {
+      const Batch::Group& g = b.groups[i];
+      pending.push_back(applied(g, s, x_in, 0, g.count));
+      pending.back().store = {ws + g.x_off[x_out], nullptr, g.ldx, g.x_elems(), 1.0f / scale, 0.0f, 0.0f, 0, 32};
     }
-    return flush(GEMM_NS_APPLY);
+    return flush(GEMM_F16);
   }
 
   // `steps` steps from X in buffer 0, as single steps or as 2 + 1 + 2 + 1 + ...
@@ -417,58 +435,40 @@ struct Runner {
 bool use_pairs(const Shape2* s, int64_t count) {
   double single = 0, paired = 0;
   for (int64_t i = 0; i < count; ++i) {
-    const double m = (double)s[i].m, n = (double)s[i].n;
+    const double m = (double)s[i].m(), n = (double)s[i].n();
     single += 15 * m * m * n + 5 * m * m * m;
     paired += 9 * m * m * n + 11 * m * m * m;
   }
   return paired < single;
 }
 
-template <class F>
-cudaError_t for_items(const std::vector<Item>& items, F launch) {
-  for (size_t i = 0; i < items.size(); i += kItemsPerLaunch) {
+// Norms and X_0 of a batch's items, a few at a time (kIngestBytes).
+cudaError_t ingest(const std::vector<Item>& items, bool f32, bool mom, const MuonScalars& s, cudaStream_t stream) {
+  const int64_t size = (f32 ? 4 : 2) + (mom ? 4 : 0);
+  for (size_t i = 0; i < items.size();) {
     ItemTable t;
-    const int n = static_cast<int>(std::min<size_t>(kItemsPerLaunch, items.size() - i));
-    int64_t largest = 0;
-    for (int k = 0; k < n; ++k) {
-      t.it[k] = items[i + k];
-      largest = std::max(largest, t.it[k].rows * t.it[k].cols);
+    int n = 0;
+    int64_t bytes = 0, largest = 0;
+    while (n < kItemsPerLaunch && i < items.size()) {
+      const int64_t z = items[i].rows * items[i].cols;
+      if (n > 0 && bytes + z * size > kIngestBytes) break;
+      bytes += z * size;
+      largest = std::max(largest, z);
+      t.it[n++] = items[i++];
     }
-    launch(t, n, largest);
-    const cudaError_t err = cudaGetLastError();
+    // 8 elements a thread, twice, until the grid is large enough to walk on
+    const int parts = static_cast<int>(std::min<int64_t>(kNormBlocks, ops_ceil_div(largest, 4096)));
+    const dim3 g1(parts, n), g2(static_cast<unsigned>(std::min<int64_t>(1024, ops_ceil_div(largest, 4096))), n);
+    auto norm = f32 ? (mom ? norm_kernel<true, true> : norm_kernel<true, false>)
+                    : (mom ? norm_kernel<false, true> : norm_kernel<false, false>);
+    auto scale = f32 ? (mom ? scale_kernel<true, true> : scale_kernel<true, false>)
+                     : (mom ? scale_kernel<false, true> : scale_kernel<false, false>);
+    cudaError_t err = launch_chained(norm, g1, dim3(256), 0, stream, t, s);
+    if (err == cudaSuccess) err = launch_chained(scale, g2, dim3(256), 0, stream, t, s, parts);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
 }
-
-int norm_blocks(int64_t elements) {
-  return static_cast<int>(std::min<int64_t>(kNormBlocks, std::max<int64_t>(1, elements / 8192)));
-}
-
-// Norms and X_0 of a batch's items.
-cudaError_t ingest(const std::vector<Item>& items, bool f32, bool mom, const MuonScalars& s, cudaStream_t stream) {
-  return for_items(items, [&](const ItemTable& t, int n, int64_t largest) {
-    const int parts = norm_blocks(largest);
-    const unsigned tiles = static_cast<unsigned>(std::min<int64_t>(16384, std::max<int64_t>(1, largest / 2048)));
-    const dim3 g1(parts, n), g2(tiles, n);
-    if (f32 && mom) {
-      norm_kernel<true, true><<<g1, 256, 0, stream>>>(t, s);
-      scale_kernel<true, true><<<g2, 256, 0, stream>>>(t, s, parts);
-    } else if (f32) {
-      norm_kernel<true, false><<<g1, 256, 0, stream>>>(t, s);
-      scale_kernel<true, false><<<g2, 256, 0, stream>>>(t, s, parts);
-    } else if (mom) {
-      norm_kernel<false, true><<<g1, 256, 0, stream>>>(t, s);
-      scale_kernel<false, true><<<g2, 256, 0, stream>>>(t, s, parts);
-    } else {
-      norm_kernel<false, false><<<g1, 256, 0, stream>>>(t, s);
-      scale_kernel<false, false><<<g2, 256, 0, stream>>>(t, s, parts);
-    }
-  });
-}
-
-Shape2 shape_of(int64_t rows, int64_t cols) { return {std::min(rows, cols), std::max(rows, cols)}; }
-bool by_shape(const Shape2& a, const Shape2& b) { return a.m != b.m ? a.m < b.m : a.n < b.n; }
 
 // A workspace for all matrices at once, or for as many as 4 GiB hold, at least one.
 constexpr int64_t kMaxBatchBytes = int64_t(4) << 30;
@@ -480,7 +480,7 @@ using namespace lst;
 
 extern "C" int64_t lst_orthogonalize_workspace_bytes(int32_t count, int64_t rows, int64_t cols) {
   if (count <= 0 || rows <= 0 || cols <= 0) return 0;
-  const Shape2 s = shape_of(rows, cols);
+  const Shape2 s = {rows, cols};
   const int64_t fit = std::max<int64_t>(1, kMaxBatchBytes / Batch::item_bytes(s));
   return std::min<int64_t>(count, fit) * Batch::item_bytes(s);
 }
@@ -505,11 +505,10 @@ extern "C" lst_status lst_orthogonalize(int32_t count, const lst_matrix* in, con
     if (out[i].dtype != LST_BF16) return fail(LST_ERR_INVALID_ARG, "%s: out must be bf16", who);
   }
   if (in[0].rows == 0 || in[0].cols == 0) return LST_OK;
-  const Shape2 shape = shape_of(in[0].rows, in[0].cols);
+  const Shape2 shape = {in[0].rows, in[0].cols};
   LST_TRY(check_workspace(workspace, workspace_bytes, Batch::item_bytes(shape), who));
   const int64_t fit = workspace_bytes / Batch::item_bytes(shape);
-  const bool tall = in[0].rows > in[0].cols;
-  const MuonScalars s = {0.0f, 1.0f, params->eps, 0};
+  const MuonScalars s = {0.0f, params->eps, 0};
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   char* ws = static_cast<char*>(workspace);
   try {
@@ -528,33 +527,24 @@ extern "C" lst_status lst_orthogonalize(int32_t count, const lst_matrix* in, con
         it.rows = src.rows;
         it.cols = src.cols;
         it.ld = src.stride;
-        it.x = reinterpret_cast<__half*>(ws + g.x_off[0]) + i * g.m * g.ldx;
+        it.x = reinterpret_cast<__half*>(ws + g.x_off[0]) + i * g.x_elems();
         it.ldx = g.ldx;
         it.part = reinterpret_cast<double*>(ws + b.part_off) + i * kNormBlocks;
-        it.tall = tall;
       }
       LST_TRY_CUDA(ingest(items, in[0].dtype == LST_F32, false, s, stream), who);
       Runner run{b, ws, stream, {}};
       int si, xi;
       float scale;
       LST_TRY_CUDA(run.iterate(params->steps, use_pairs(shapes.data(), n), &si, &scale, &xi), who);
-      // the last product goes to the caller's matrices, transposed back
+      // the last product goes to the caller's matrices
       for (int64_t i = 0; i < n; ++i) {
         const lst_matrix& dst = out[first + i];
-        GemmProblem p;
-        p.a = run.s_operand(b.classes[0], si, i, 1);
-        p.b = run.x_operand(g, xi);
-        p.b.ptr = ws + g.x_off[xi] + i * g.m * g.ldx * 2;
-        p.b.batch = 1;
-        p.m = g.m;
-        p.n = g.n;
-        p.k = g.m;
         const uintptr_t align = reinterpret_cast<uintptr_t>(dst.data) | static_cast<uintptr_t>(dst.stride * 2);
         const int vec = align % 32 == 0 ? 32 : align % 16 == 0 ? 16 : 2;
-        p.store = {dst.data, nullptr, dst.stride, 0, 1.0f / (scale * kScaleX), 0.0f, 0.0f, 1, tall ? 1 : 0, vec};
-        run.pending.push_back(p);
+        run.pending.push_back(run.applied(g, si, xi, i, 1));
+        run.pending.back().store = {dst.data, nullptr, dst.stride, 0, 1.0f / (scale * kScaleX), 0.0f, 0.0f, 1, vec};
       }
-      LST_TRY_CUDA(run.flush(GEMM_NS_APPLY), who);
+      LST_TRY_CUDA(run.flush(GEMM_F16), who);
     }
   } catch (...) {
     return fail(LST_ERR_OOM, "%s: out of host memory", who);
@@ -567,7 +557,7 @@ extern "C" int64_t lst_muon_workspace_bytes(const lst_layout* L) {
   int64_t all = 0, largest = 0;
   for (const Tensor& t : L->tensors) {
     if (t.ndim != 2 || t.numel == 0) continue;
-    const int64_t z = Batch::item_bytes(shape_of(t.dims[0], t.dims[1]));
+    const int64_t z = Batch::item_bytes({t.dims[0], t.dims[1]});
     all += z;
     largest = std::max(largest, z);
   }
@@ -619,7 +609,7 @@ extern "C" lst_status lst_muon_step(const lst_layout* L, void* const* dev_blocks
       if (use_muon ? use_muon[i] != 0 : matrix) {
         if (t.dims[0] > INT32_MAX || t.dims[1] > INT32_MAX)
           return fail(LST_ERR_INVALID_ARG, "%s: tensor %lld: dimension above 2^31-1", who, (long long)i);
-        picks.push_back({shape_of(t.dims[0], t.dims[1]), i});
+        picks.push_back({{t.dims[0], t.dims[1]}, i});
         largest = std::max(largest, Batch::item_bytes(picks.back().s));
       } else if (adamw) {
         const Run r = run_of(t);
@@ -627,11 +617,11 @@ extern "C" lst_status lst_muon_step(const lst_layout* L, void* const* dev_blocks
       }
     }
     LST_TRY(check_workspace(workspace, workspace_bytes, largest, who));
-    std::stable_sort(picks.begin(), picks.end(), [](const Pick& a, const Pick& b) { return by_shape(a.s, b.s); });
+    std::stable_sort(picks.begin(), picks.end(), [](const Pick& a, const Pick& b) { return a.s < b.s; });
     cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     char* ws = static_cast<char*>(workspace);
-    const MuonScalars ms = {hp->momentum, (float)(1.0 - (double)hp->lr * (double)hp->weight_decay), hp->eps,
-                            hp->nesterov ? 1 : 0};
+    const MuonScalars ms = {hp->momentum, hp->eps, hp->nesterov ? 1 : 0};
+    const float decay = (float)(1.0 - (double)hp->lr * (double)hp->weight_decay);
     const bool f32 = L->fmt == LST_L16_FP32;
 
     for (size_t first = 0; first < picks.size();) {
@@ -648,46 +638,46 @@ extern "C" lst_status lst_muon_step(const lst_layout* L, void* const* dev_blocks
       std::vector<Item> items(shapes.size());
       for (const Batch::Group& g : b.groups)
         for (int64_t k = 0; k < g.count; ++k) {
-          const Tensor& t = L->tensors[(size_t)picks[first + (size_t)(g.first + k)].tensor];
-          const Run r = run_of(t);
-          Item& it = items[(size_t)(g.first + k)];
-          const double rows = (double)t.dims[0], cols = (double)t.dims[1];
-          const double scale = hp->rms_scale > 0.0f ? (double)hp->rms_scale * std::sqrt(std::max(rows, cols))
-                                                    : std::sqrt(std::max(1.0, rows / cols));
-          it = {};
-          it.g = r.g;
-          it.mom = r.m;
-          it.w = r.w;
-          it.w16 = static_cast<uint16_t*>(r.w16);
-          it.rows = t.dims[0];
-          it.cols = it.ld = t.dims[1];
-          it.x = reinterpret_cast<__half*>(ws + g.x_off[0]) + k * g.m * g.ldx;
-          it.ldx = g.ldx;
-          it.part = reinterpret_cast<double*>(ws + b.part_off) + (g.first + k) * kNormBlocks;
-          it.tall = t.dims[0] > t.dims[1];
-          it.step = (float)((double)hp->lr * scale / (double)kScaleX);
+          const Run r = run_of(L->tensors[(size_t)picks[first + (size_t)(g.first + k)].tensor]);
+          items[(size_t)(g.first + k)] = {r.g, r.m, reinterpret_cast<__half*>(ws + g.x_off[0]) + k * g.x_elems(),
+                                          reinterpret_cast<double*>(ws + b.part_off) + (g.first + k) * kNormBlocks,
+                                          g.s.rows, g.s.cols, g.s.cols, g.ldx};
         }
       LST_TRY_CUDA(ingest(items, f32, true, ms, stream), who);
       Runner run{b, ws, stream, {}};
       int si, xi;
       float scale;
       LST_TRY_CUDA(run.iterate(hp->ns_steps, use_pairs(shapes.data(), (int64_t)shapes.size()), &si, &scale, &xi), who);
-      LST_TRY_CUDA(run.apply(si, scale, xi, xi ^ 1), who);
-      for (const Batch::Group& g : b.groups)
-        for (int64_t k = 0; k < g.count; ++k)
-          items[(size_t)(g.first + k)].o = reinterpret_cast<const __half*>(ws + g.x_off[xi ^ 1]) + k * g.m * g.ldx;
-      LST_TRY_CUDA(for_items(items,
-                             [&](const ItemTable& t, int n, int64_t big) {
-                               const dim3 grid(
-                                   static_cast<unsigned>(std::min<int64_t>(16384, std::max<int64_t>(1, big / 2048))), n);
-                               if (L->fmt == LST_L12_BF16)
-                                 apply_kernel<F_L12><<<grid, 256, 0, stream>>>(t, ms);
-                               else if (L->fmt == LST_L16_MIXED)
-                                 apply_kernel<F_L16M><<<grid, 256, 0, stream>>>(t, ms);
-                               else
-                                 apply_kernel<F_L16F><<<grid, 256, 0, stream>>>(t, ms);
-                             }),
-                   who);
+      // the last product updates the weights
+      UpdateTable table;
+      int entries = 0;
+      auto flush = [&]() {
+        const cudaError_t err = launch_gemm(GEMM_F16_UPDATE, run.pending.data(), (int)run.pending.size(), stream, &table);
+        run.pending.clear();
+        entries = 0;
+        return err;
+      };
+      for (size_t i = b.groups.size(); i-- > 0;) {
+        const Batch::Group& g = b.groups[i];
+        const double rows = (double)g.s.rows, cols = (double)g.s.cols;
+        const double s = hp->rms_scale > 0.0f ? (double)hp->rms_scale * std::sqrt(std::max(rows, cols))
+                                              : std::sqrt(std::max(1.0, rows / cols));
+        for (int64_t k = 0; k < g.count;) {
+          if (entries == kGemmMaxUpdates || run.pending.size() == kGemmMaxProblems) LST_TRY_CUDA(flush(), who);
+          const int64_t now = std::min<int64_t>(g.count - k, kGemmMaxUpdates - entries);
+          run.pending.push_back(run.applied(g, si, xi, k, now));
+          // tensors start at multiples of 8 elements: rows of such a length are on 16 bytes in every field
+          run.pending.back().update = {g.s.cols, entries, L->fmt, g.s.cols % 8 == 0 ? 16 : 2, decay};
+          for (int64_t j = 0; j < now; ++j, ++entries) {
+            const Run r = run_of(L->tensors[(size_t)picks[first + (size_t)(g.first + k + j)].tensor]);
+            table.w[entries] = r.w;
+            table.w16[entries] = static_cast<uint16_t*>(r.w16);
+            table.step[entries] = (float)((double)hp->lr * s / ((double)kScaleX * (double)scale));
+          }
+          k += now;
+        }
+      }
+      LST_TRY_CUDA(flush(), who);
       first = last;
     }
     for (size_t i = 0; i < adam.size(); i += kItemsPerLaunch) {
@@ -699,13 +689,10 @@ extern "C" lst_status lst_muon_step(const lst_layout* L, void* const* dev_blocks
         big = std::max(big, t.it[k].n);
       }
       const dim3 grid(static_cast<unsigned>(std::min<int64_t>(4096, ops_ceil_div(big, 1024))), n);
-      if (L->fmt == LST_L12_BF16)
-        adam_kernel<F_L12><<<grid, 256, 0, stream>>>(t, as);
-      else if (L->fmt == LST_L16_MIXED)
-        adam_kernel<F_L16M><<<grid, 256, 0, stream>>>(t, as);
-      else
-        adam_kernel<F_L16F><<<grid, 256, 0, stream>>>(t, as);
-      LST_TRY_CUDA(cudaGetLastError(), who);
+      auto kernel = L->fmt == LST_L12_BF16    ? adam_kernel<F_L12>
+                    : L->fmt == LST_L16_MIXED ? adam_kernel<F_L16M>
+                                              : adam_kernel<F_L16F>;
+      LST_TRY_CUDA(launch_chained(kernel, grid, dim3(256), 0, stream, t, as), who);
     }
   } catch (...) {
     return fail(LST_ERR_OOM, "%s: out of host memory", who);

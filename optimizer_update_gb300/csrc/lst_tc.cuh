@@ -93,10 +93,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
-}
-
 // TMA tile load by one CTA of a pair: the data lands in this CTA's shared
 // memory at `dst`, the bytes are counted on the barrier `cluster_bar` (a
 // cluster address: the leader's barrier).

@@ -48,6 +48,8 @@ __global__ void __launch_bounds__(1024)
     join_kernel(const float2* __restrict__ stats, int64_t stat_ld, int groups, const float* __restrict__ target_logit,
                 const void* __restrict__ targets, int wide, int64_t ignore, int64_t vocab, int rows,
                 float* __restrict__ loss, float* __restrict__ lse) {
+  let_next_start();
+  wait_for_previous();
   __shared__ float2 part[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x * 32 + lane;
@@ -86,6 +88,8 @@ __global__ void __launch_bounds__(1024)
 __global__ void __launch_bounds__(1024)
     mean_kernel(const float* __restrict__ loss, const void* __restrict__ targets, int wide, int64_t ignore, int rows,
                 float grad_scale, float* __restrict__ mean, float* __restrict__ g) {
+  let_next_start();
+  wait_for_previous();
   double sum = 0.0;
   int count = 0;
   for (int i = threadIdx.x; i < rows; i += 1024)
@@ -121,6 +125,8 @@ __global__ void __launch_bounds__(256)
                       int64_t first_group, int64_t first_column, int columns, const float* __restrict__ lse,
                       const float* __restrict__ target_logit, const void* __restrict__ targets, int wide,
                       int64_t ignore, int64_t vocab, const float* __restrict__ gp, int blocks_per_row) {
+  let_next_start();
+  wait_for_previous();
   const int row = blockIdx.x / blocks_per_row;
   const int col = ((blockIdx.x - row * blocks_per_row) * 256 + threadIdx.x) * 8;
   if (col >= columns) return;
@@ -165,6 +171,8 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     dx_kernel(const float* __restrict__ parts, int64_t ld, int64_t split_stride, int splits, int rows, int cols,
               __nv_bfloat16* __restrict__ dx, int64_t dx_ld, int wide_store) {
+  let_next_start();
+  wait_for_previous();
   const int quads = (cols + 3) / 4;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int row = static_cast<int>(i / quads);
@@ -193,6 +201,8 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     pack_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t* __restrict__ dst,
                 int64_t dst_ld) {
+  let_next_start();
+  wait_for_previous();
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
     for (int c = threadIdx.x; c < cols; c += 256) dst[r * dst_ld + c] = src[r * ld + c];
 }
@@ -204,6 +214,8 @@ __global__ void __launch_bounds__(256)
     mask_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t* __restrict__ dst,
                      int64_t dst_ld, const void* __restrict__ targets, int wide, int64_t ignore, int64_t vocab,
                      int vec) {
+  let_next_start();
+  wait_for_previous();
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const int64_t t = target_at(targets, wide, r);
     const bool keep = t != ignore && t >= 0 && t < vocab;
@@ -273,7 +285,10 @@ bool make_plan(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool pac
   return bytes < 0 || at <= bytes;
 }
 
-GemmOperand rows_operand(const void* ptr, int64_t rows, int64_t cols, int64_t ld) { return {ptr, cols, rows, ld}; }
+// A matrix of rows; `transposed`: the product sums over its rows.
+GemmOperand rows_operand(const void* ptr, int64_t rows, int64_t cols, int64_t ld, bool transposed = false) {
+  return {ptr, cols, rows, ld, transposed};
+}
 
 int store_width(const lst_matrix* m) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(m->data) | static_cast<uintptr_t>(m->stride * 2);
@@ -310,12 +325,10 @@ struct Call {
     xp = x->data, wp = w->data, x_ld = x->stride, w_ld = w->stride;
     auto pack = [&](const lst_matrix* m, int64_t off, const void** ptr, int64_t* ld) {
       const unsigned grid = static_cast<unsigned>(std::min<int64_t>(m->rows, 8192));
-      pack_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(m->data), m->stride, m->rows,
-                                            static_cast<int>(m->cols), reinterpret_cast<uint16_t*>(ws + off),
-                                            p.packed_ld);
       *ptr = ws + off;
       *ld = p.packed_ld;
-      return cudaGetLastError();
+      return launch_chained(pack_kernel, dim3(grid), dim3(256), 0, stream, static_cast<const uint16_t*>(m->data), m->stride,
+                            m->rows, static_cast<int>(m->cols), reinterpret_cast<uint16_t*>(ws + off), p.packed_ld);
     };
     cudaError_t err = cudaSuccess;
     if (!tile_ready(x)) err = pack(x, p.xpack_off, &xp, &x_ld);
@@ -333,15 +346,14 @@ struct Call {
     g.xent = {targets->data, reinterpret_cast<float2*>(ws + p.stats_off), reinterpret_cast<float*>(ws + p.tlogit_off),
               keep ? reinterpret_cast<uint16_t*>(ws + p.q_off) : nullptr, p.piece, p.n_pad, v0 / 128, v0,
               targets->bits / 8};
-    return launch_gemm(GEMM_LOGITS, &g, 1, stream);
+    return launch_gemm(GEMM_BF16_XENT, &g, 1, stream);
   }
 
   cudaError_t join() {
-    join_kernel<<<static_cast<unsigned>(ops_ceil_div(x->rows, 32)), 1024, 0, stream>>>(
+    return launch_chained(join_kernel, dim3(static_cast<unsigned>(ops_ceil_div(x->rows, 32))), dim3(1024), 0, stream, 
         reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, static_cast<int>(p.groups),
         reinterpret_cast<const float*>(ws + p.tlogit_off), targets->data, wide, ignore, w->rows,
         static_cast<int>(x->rows), loss, lse);
-    return cudaGetLastError();
   }
 };
 
@@ -421,17 +433,15 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
   uint16_t* q = reinterpret_cast<uint16_t*>(ws + p.q_off);
 
   LST_TRY_CUDA(c.operands(), who);
-  mask_rows_kernel<<<static_cast<unsigned>(std::min<int64_t>(n, 8192)), 256, 0, stream>>>(
+  LST_TRY_CUDA(launch_chained(mask_rows_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(n, 8192))), dim3(256), 0, stream, 
       static_cast<const uint16_t*>(c.xp), c.x_ld, n, static_cast<int>(h), xm, p.packed_ld, targets->data, c.wide,
-      ignore_index, v, h % 8 == 0);
-  LST_TRY_CUDA(cudaGetLastError(), who);
+      ignore_index, v, h % 8 == 0), who);
   for (int64_t k = p.pieces - 1; k >= 0; --k) {
     const int64_t v0 = k * p.piece;
     LST_TRY_CUDA(c.logits(v0, std::min(p.piece, v - v0), k == 0), who);
   }
   LST_TRY_CUDA(c.join(), who);
-  mean_kernel<<<1, 1024, 0, stream>>>(loss, targets->data, c.wide, ignore_index, static_cast<int>(n), grad_scale, mean, g);
-  LST_TRY_CUDA(cudaGetLastError(), who);
+  LST_TRY_CUDA(launch_chained(mean_kernel, dim3(1), dim3(1024), 0, stream, loss, targets->data, c.wide, ignore_index, static_cast<int>(n), grad_scale, mean, g), who);
   const bool parts = p.splits > 1 || p.pieces > 1;
   // the first piece sets every partial sum of dx: only the last can be shorter,
   // with fewer splits
@@ -439,43 +449,41 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
     const int64_t v0 = k * p.piece, columns = std::min(p.piece, v - v0);
     if (k > 0) LST_TRY_CUDA(c.logits(v0, columns, true), who);
     const int blocks = static_cast<int>(ops_ceil_div(columns, 2048));
-    logit_grad_kernel<<<static_cast<unsigned>(n * blocks), 256, 0, stream>>>(
+    LST_TRY_CUDA(launch_chained(logit_grad_kernel, dim3(static_cast<unsigned>(n * blocks)), dim3(256), 0, stream, 
         q, p.piece, reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, v0 / 128, v0, static_cast<int>(columns),
-        lse, reinterpret_cast<const float*>(ws + p.tlogit_off), targets->data, c.wide, ignore_index, v, g, blocks);
-    LST_TRY_CUDA(cudaGetLastError(), who);
+        lse, reinterpret_cast<const float*>(ws + p.tlogit_off), targets->data, c.wide, ignore_index, v, g, blocks), who);
     // dw of the piece = d^T x
     GemmProblem d;
-    d.a = rows_operand(q, n, columns, p.piece);
-    d.b = rows_operand(xm, n, h, p.packed_ld);
+    d.a = rows_operand(q, n, columns, p.piece, true);
+    d.b = rows_operand(xm, n, h, p.packed_ld, true);
     d.m = columns;
     d.n = h;
     d.k = n;
     uint16_t* dwp = static_cast<uint16_t*>(dw->data) + v0 * dw->stride;
-    d.store = {dwp, accumulate_dw ? dwp : nullptr, dw->stride, 0, 1.0f, 1.0f, 0.0f, 1, 0, store_width(dw)};
-    LST_TRY_CUDA(launch_gemm(GEMM_DW, &d, 1, stream), who);
+    d.store = {dwp, accumulate_dw ? dwp : nullptr, dw->stride, 0, 1.0f, 1.0f, 0.0f, 1, store_width(dw)};
+    LST_TRY_CUDA(launch_gemm(GEMM_BF16, &d, 1, stream), who);
     // dx += d w
     GemmProblem e;
     e.a = rows_operand(q, n, columns, p.piece);
-    e.b = rows_operand(static_cast<const uint16_t*>(c.wp) + v0 * c.w_ld, columns, h, c.w_ld);
+    e.b = rows_operand(static_cast<const uint16_t*>(c.wp) + v0 * c.w_ld, columns, h, c.w_ld, true);
     e.m = n;
     e.n = h;
     e.k = columns;
     if (parts) {
       e.splits = static_cast<int>(p.splits);
       e.partial = {reinterpret_cast<float*>(ws + p.part_off), p.part_ld, n * p.part_ld, k > 0};
-      LST_TRY_CUDA(launch_gemm(GEMM_DX_SPLIT, &e, 1, stream), who);
+      LST_TRY_CUDA(launch_gemm(GEMM_BF16_PARTS, &e, 1, stream), who);
     } else {
-      e.store = {dx->data, nullptr, dx->stride, 0, 1.0f, 0.0f, 0.0f, 1, 0, store_width(dx)};
-      LST_TRY_CUDA(launch_gemm(GEMM_DX, &e, 1, stream), who);
+      e.store = {dx->data, nullptr, dx->stride, 0, 1.0f, 0.0f, 0.0f, 1, store_width(dx)};
+      LST_TRY_CUDA(launch_gemm(GEMM_BF16, &e, 1, stream), who);
     }
   }
   if (parts) {
     const int64_t quads = ops_ceil_div(h, 4) * n;
     const bool wide_store = h % 4 == 0 && dx->stride % 4 == 0 && reinterpret_cast<uintptr_t>(dx->data) % 8 == 0;
-    dx_kernel<<<static_cast<unsigned>(ops_ceil_div(quads, 256)), 256, 0, stream>>>(
+    LST_TRY_CUDA(launch_chained(dx_kernel, dim3(static_cast<unsigned>(ops_ceil_div(quads, 256))), dim3(256), 0, stream, 
         reinterpret_cast<const float*>(ws + p.part_off), p.part_ld, n * p.part_ld, static_cast<int>(p.splits),
-        static_cast<int>(n), static_cast<int>(h), static_cast<__nv_bfloat16*>(dx->data), dx->stride, wide_store);
-    LST_TRY_CUDA(cudaGetLastError(), who);
+        static_cast<int>(n), static_cast<int>(h), static_cast<__nv_bfloat16*>(dx->data), dx->stride, wide_store), who);
   }
   return LST_OK;
 }

@@ -91,29 +91,41 @@ def matrix(t) -> lst_matrix:
     """An lst_matrix over a torch tensor of two dimensions (bf16, bf16 bit
     patterns as int16, or fp32) with contiguous rows. The tensor has to outlive
     the calls that use it."""
-    import torch
+    dtype = _matrix_dtype(t.dtype)
     if t.dim() != 2:
         raise ValueError("a matrix has two dimensions")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError("rows must be contiguous")
-    if t.dtype == torch.float32:
-        dtype = LST_F32
-    elif t.dtype in (torch.bfloat16, torch.int16):
-        dtype = LST_BF16
-    else:
-        raise ValueError(f"unsupported type {t.dtype}")
-    return lst_matrix(t.data_ptr(), rows, cols, max(cols, t.stride(0)) if rows > 1 else cols, dtype)
+    return lst_matrix(t.data_ptr(), rows, cols, stride if rows > 1 and stride > cols else cols, dtype)
+
+
+_dtypes = {}  # torch types, filled at their first use: the binding does not import torch by itself
+
+
+def _matrix_dtype(dtype) -> int:
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.float32: LST_F32, torch.bfloat16: LST_BF16, torch.int16: LST_BF16, torch.int32: -32,
+                        torch.int64: -64})
+    code = _dtypes.get(dtype, -1)
+    if code < 0:
+        raise ValueError(f"unsupported type {dtype}")
+    return code
 
 
 def indices(t) -> lst_indices:
     """An lst_indices over a contiguous torch tensor of int32 or int64."""
-    import torch
-    if t.dtype not in (torch.int32, torch.int64):
+    if not _dtypes:
+        import torch
+        _matrix_dtype(torch.float32)
+    bits = -_dtypes.get(t.dtype, 0)
+    if bits < 32:
         raise ValueError("indices are int32 or int64")
     if not t.is_contiguous():
         raise ValueError("indices must be contiguous")
-    return lst_indices(t.data_ptr(), t.numel(), 64 if t.dtype == torch.int64 else 32)
+    return lst_indices(t.data_ptr(), t.numel(), bits)
 
 
 def ns_params(steps=5, eps=1e-7):
