@@ -7,15 +7,18 @@
 // atomics would make the sum's order, and so its last bits, differ from run to
 // run, and would read and write fp32 sums of a large gradient; instead
 //   1. one cluster of 8 CTAs sorts (token, position) pairs, stable, by radix
-//      passes in shared memory, and marks the tokens seen in a bit per token;
-//   2. every 32 consecutive sorted positions and 1024 columns go to a CTA that
+//      passes in shared memory, while the launch's other CTAs zero the gradient
+//      (the rows that step 2 writes too, which costs less than waiting for the
+//      sort to know them);
+//   2. every 32 (or 8) consecutive sorted positions and 1024 columns go to a CTA that
 //      adds up runs of equal tokens in registers and writes the gradient of
 //      every run that ends inside; the parts of runs that cross into another
-//      CTA's positions go to the workspace. Other CTAs of the same launch
-//      zero the rows of tokens that were not seen;
+//      CTA's positions go to the workspace;
 //   3. the crossing runs are added up, part by part in order.
-// Each dout row is read once and each gradient row written once.
+// Each dout row is read once.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "lst_ops.h"
 
@@ -23,59 +26,77 @@ namespace lst {
 
 namespace {
 
-// ---- typed vectors of 8 elements ------------------------------------------------
-// `left` elements are inside the row (8 or more on the vector path, which
-// needs 16-byte aligned rows and a column count that is a multiple of 8).
-template <bool VEC>
-__device__ __forceinline__ void load8(const float* p, int left, float (&v)[8]) {
-  if (VEC) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
-  }
+// ---- 8 elements of a row per thread ------------------------------------------------
+// A group of THREADS threads covers 8 THREADS columns. On the vector path (rows on
+// 16 bytes, a column count that is a multiple of 8) a thread has 8 consecutive
+// ones, otherwise every THREADS-th, so that a warp's accesses stay consecutive.
+// `p` is the row at the group's first column, `left` the columns from there on.
+template <bool VEC, int THREADS>
+__device__ __forceinline__ int column_of(int thread, int i) {
+  return VEC ? thread * 8 + i : thread + i * THREADS;
 }
-template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, int left, float (&v)[8]) {
+template <bool VEC, int THREADS>
+__device__ __forceinline__ void load8(const float* p, int thread, int left, float (&v)[8]) {
   if (VEC) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    const float4* q = reinterpret_cast<const float4*>(p) + 2 * thread;
+    if (thread * 8 < left) {
+      const float4 a = q[0], b = q[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? __bfloat162float(p[i]) : 0.0f;
-  }
-}
-template <bool VEC>
-__device__ __forceinline__ void store8(float* p, int left, const float (&v)[8]) {
-  if (VEC) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4*>(p + 4), make_float4(v[4], v[5], v[6], v[7]));
-  } else {
-#pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = v[i];
+      if (thread + i * THREADS < left) v[i] = p[thread + i * THREADS];
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void store8(__nv_bfloat16* p, int left, const float (&v)[8]) {
+template <bool VEC, int THREADS>
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, int thread, int left, float (&v)[8]) {
   if (VEC) {
-    uint32_t w[4];
+    if (thread * 8 < left) {
+      const uint4 a = reinterpret_cast<const uint4*>(p)[thread];
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
     }
-    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = __float2bfloat16_rn(v[i]);
+      if (thread + i * THREADS < left) v[i] = __bfloat162float(p[thread + i * THREADS]);
+  }
+}
+template <bool VEC, int THREADS>
+__device__ __forceinline__ void store8(float* p, int thread, int left, const float (&v)[8]) {
+  if (VEC) {
+    float4* q = reinterpret_cast<float4*>(p) + 2 * thread;
+    if (thread * 8 < left) {
+      __stcs(q, make_float4(v[0], v[1], v[2], v[3]));
+      __stcs(q + 1, make_float4(v[4], v[5], v[6], v[7]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (thread + i * THREADS < left) p[thread + i * THREADS] = v[i];
+  }
+}
+template <bool VEC, int THREADS>
+__device__ __forceinline__ void store8(__nv_bfloat16* p, int thread, int left, const float (&v)[8]) {
+  if (VEC) {
+    if (thread * 8 < left) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      __stcs(reinterpret_cast<uint4*>(p) + thread, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (thread + i * THREADS < left) p[thread + i * THREADS] = __float2bfloat16_rn(v[i]);
   }
 }
 
@@ -84,35 +105,52 @@ __device__ __forceinline__ int64_t token_at(const void* t, int wide, int64_t i) 
 }
 
 // ---- lookup -----------------------------------------------------------------------
+// A warp takes 256 columns of a row at a time, and two such pieces at once; the
+// CTAs of a launch walk the output from start to end. (A persistent grid whose
+// warps took pieces a grid apart wrote all over the output at once: 281 us for
+// 65536 x 4096 bf16, against PIECES2.)
+constexpr int kPieces = 2;
+
 template <class TI, class TO, bool VEC>
 __global__ void __launch_bounds__(256)
     embed_kernel(const TI* __restrict__ table, int64_t table_ld, const void* __restrict__ tokens, int wide,
-                 TO* __restrict__ out, int64_t out_ld, int hidden, int64_t vocab, uint32_t units_per_row,
-                 uint32_t rows_per_launch, int64_t row_base, float scale) {
+                 TO* __restrict__ out, int64_t out_ld, int hidden, int64_t vocab, uint32_t pieces_per_row, int64_t pieces,
+                 float scale) {
   let_next_start();
   wait_for_previous();
-  const uint64_t unit = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const uint32_t r = static_cast<uint32_t>(unit / units_per_row);
-  if (r >= rows_per_launch) return;
-  const int col = static_cast<int>(unit - static_cast<uint64_t>(r) * units_per_row) * 8;
-  const int64_t row = row_base + r;
-  const int64_t t = token_at(tokens, wide, row);
-  float v[8];
-  if (t >= 0 && t < vocab) {
-    load8<VEC>(table + t * table_ld + col, hidden - col, v);
+  const int lane = threadIdx.x & 31;
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * 8 * kPieces + (threadIdx.x >> 5);
+  float v[kPieces][8];
+  int64_t row[kPieces];
+  int col[kPieces];
+  bool inside[kPieces];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], scale);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __int_as_float(0x7fc00000);
+  for (int k = 0; k < kPieces; ++k) {
+    const int64_t p = p0 + k * 8;
+    inside[k] = false;
+    if (p < pieces) {
+      // 32-bit division where it suffices
+      row[k] = p <= 0xffffffffll ? static_cast<int64_t>(static_cast<uint32_t>(p) / pieces_per_row) : p / pieces_per_row;
+      col[k] = static_cast<int>(p - row[k] * pieces_per_row) * 256;
+      const int64_t t = token_at(tokens, wide, row[k]);
+      inside[k] = t >= 0 && t < vocab;
+      if (inside[k]) load8<VEC, 32>(table + t * table_ld + col[k], lane, hidden - col[k], v[k]);
+    }
   }
-  store8<VEC>(out + row * out_ld + col, hidden - col, v);
+#pragma unroll
+  for (int k = 0; k < kPieces; ++k) {
+    if (p0 + k * 8 >= pieces) break;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[k][i] = inside[k] ? __fmul_rn(v[k][i], scale) : __int_as_float(0x7fc00000);
+    store8<VEC, 32>(out + row[k] * out_ld + col[k], lane, hidden - col[k], v[k]);
+  }
 }
 
 // ---- stable sort of (token, position) ---------------------------------------------
 constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortAhead = 8;  // loads in flight per thread
 
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
@@ -133,9 +171,22 @@ __device__ __forceinline__ uint32_t remote_u32(const uint32_t* p, uint32_t rank)
 // outside the vocabulary get the key `vocab` and sort last.
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1)
     sort_kernel(const void* __restrict__ tokens, int wide, int n, int vocab, int passes, int digit_bits, uint2* buf0,
-                uint2* buf1, uint32_t* seen) {
+                uint2* buf1, char* zero, int64_t zero_pitch, int64_t zero_row, int zero_vec) {
   let_next_start();
   wait_for_previous();
+  if (blockIdx.x >= kSortCtas) {
+    const int64_t first = static_cast<int64_t>(blockIdx.x - kSortCtas) * kSortThreads + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x - kSortCtas) * kSortThreads;
+    if (zero_vec) {  // one range of whole 16-byte words
+#pragma unroll 8
+      for (int64_t i = first; i < zero_row / 16; i += step) reinterpret_cast<uint4*>(zero)[i] = make_uint4(0, 0, 0, 0);
+    } else {  // rows of 2-byte units, a warp at a time
+      const int lane = threadIdx.x & 31;
+      for (int64_t r = first >> 5; r < vocab; r += step >> 5)
+        for (int64_t c = lane; c < zero_row / 2; c += 32) reinterpret_cast<uint16_t*>(zero + r * zero_pitch)[c] = 0;
+    }
+    return;
+  }
   extern __shared__ uint32_t sm[];
   const int bins = 1 << digit_bits;
   uint32_t* const count = sm;                        // [warp][bin]
@@ -149,11 +200,6 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
   const int64_t first = static_cast<int64_t>(cta * kSortWarps + warp) * per_warp;
   const int64_t last = first + per_warp < n ? first + per_warp : n;
 
-  for (int64_t i = static_cast<int64_t>(cta) * kSortThreads + tid; i < (static_cast<int64_t>(vocab) + 31) / 32;
-       i += kSortCtas * kSortThreads)
-    seen[i] = 0;
-  cluster_barrier();
-
   for (int pass = 0; pass < passes; ++pass) {
     const uint2* const src = (pass & 1) ? buf0 : buf1;  // unused in pass 0
     uint2* const dst = (pass & 1) ? buf1 : buf0;
@@ -161,24 +207,26 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     for (int i = tid; i < kSortWarps * bins; i += kSortThreads) count[i] = 0;
     __syncthreads();
     uint32_t* const mine = count + warp * bins;
-    for (int64_t i0 = first; i0 < last; i0 += 32) {
-      const bool in = i0 + lane < last;
-      uint32_t digit = bins;
-      if (in) {
-        uint32_t key;
-        if (pass == 0) {
-          const int64_t t = token_at(tokens, wide, i0 + lane);
-          const bool valid = t >= 0 && t < vocab;
-          key = valid ? static_cast<uint32_t>(t) : static_cast<uint32_t>(vocab);
-          if (valid) atomicOr(seen + (key >> 5), 1u << (key & 31));
-        } else {
-          key = src[i0 + lane].x;
-        }
-        digit = (key >> shift) & (bins - 1);
+    auto item_at = [&](int64_t i) {
+      if (pass > 0) return src[i];
+      const int64_t t = token_at(tokens, wide, i);
+      return make_uint2(t >= 0 && t < vocab ? static_cast<uint32_t>(t) : static_cast<uint32_t>(vocab),
+                        static_cast<uint32_t>(i));
+    };
+    for (int64_t i0 = first; i0 < last; i0 += 32 * kSortAhead) {
+      uint32_t key[kSortAhead];
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j)
+        if (i0 + 32 * j + lane < last) key[j] = item_at(i0 + 32 * j + lane).x;
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j) {
+        if (i0 + 32 * j >= last) break;
+        const bool in = i0 + 32 * j + lane < last;
+        const uint32_t digit = in ? (key[j] >> shift) & (bins - 1) : bins;
+        const uint32_t same = __match_any_sync(0xffffffffu, digit);
+        if (in && (same & below) == 0) mine[digit] += __popc(same);
+        __syncwarp();
       }
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      if (in && (same & below) == 0) mine[digit] += __popc(same);
-      __syncwarp();
     }
     __syncthreads();
     for (int d = tid; d < bins; d += kSortThreads) {
@@ -212,35 +260,31 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     for (int w = 0; w < warp; ++w) before += warp_sum[w];
     if (tid < bins) start[tid] = before + scan - all + lower;
     __syncthreads();
-    for (int64_t i0 = first; i0 < last; i0 += 32) {
-      const bool in = i0 + lane < last;
-      uint32_t digit = bins;
-      uint2 item = make_uint2(0, 0);
-      if (in) {
-        if (pass == 0) {
-          const int64_t t = token_at(tokens, wide, i0 + lane);
-          item = make_uint2(t >= 0 && t < vocab ? static_cast<uint32_t>(t) : static_cast<uint32_t>(vocab),
-                            static_cast<uint32_t>(i0 + lane));
-        } else {
-          item = src[i0 + lane];
-        }
-        digit = (item.x >> shift) & (bins - 1);
+    for (int64_t i0 = first; i0 < last; i0 += 32 * kSortAhead) {
+      uint2 item[kSortAhead];
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j)
+        if (i0 + 32 * j + lane < last) item[j] = item_at(i0 + 32 * j + lane);
+#pragma unroll
+      for (int j = 0; j < kSortAhead; ++j) {
+        if (i0 + 32 * j >= last) break;
+        const bool in = i0 + 32 * j + lane < last;
+        const uint32_t digit = in ? (item[j].x >> shift) & (bins - 1) : bins;
+        const uint32_t same = __match_any_sync(0xffffffffu, digit);
+        if (in) dst[start[digit] + mine[digit] + __popc(same & below)] = item[j];
+        __syncwarp();
+        if (in && (same & below) == 0) mine[digit] += __popc(same);
+        __syncwarp();
       }
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      if (in) dst[start[digit] + mine[digit] + __popc(same & below)] = item;
-      __syncwarp();
-      if (in && (same & below) == 0) mine[digit] += __popc(same);
-      __syncwarp();
     }
     cluster_barrier();  // items placed; totals read by all
   }
 }
 
 // ---- runs of equal tokens -----------------------------------------------------------
-constexpr int kRun = 32;             // sorted positions of a CTA
+constexpr int kMaxRun = 32;          // sorted positions of a CTA, at most
 constexpr int kSumThreads = 128;     // x 8 columns
 constexpr int kSumCols = kSumThreads * 8;
-constexpr int kZeroRows = 16;
 
 template <class TG>
 struct Grad {
@@ -250,60 +294,50 @@ struct Grad {
   int accumulate;
 };
 
+// Row `row` from column `col` on: the thread's 8 sums, scaled.
 template <class TG, bool VEC>
-__device__ __forceinline__ void write_row(const Grad<TG>& g, int64_t row, int col, int left, float (&acc)[8]) {
+__device__ __forceinline__ void write_row(const Grad<TG>& g, int64_t row, int col, int left, const float (&acc)[8]) {
   TG* p = g.data + row * g.ld + col;
-  float v[8];
+  float v[8] = {};
   if (g.accumulate) {
-    load8<VEC>(p, left, v);
+    load8<VEC, kSumThreads>(p, threadIdx.x, left, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __fmaf_rn(acc[i], g.scale, v[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(acc[i], g.scale);
   }
-  store8<VEC>(p, left, v);
+  store8<VEC, kSumThreads>(p, threadIdx.x, left, v);
 }
 
 template <class TD, class TG, bool VEC>
 __global__ void __launch_bounds__(kSumThreads)
     sum_kernel(const TD* __restrict__ dout, int64_t dout_ld, const uint2* __restrict__ sorted, int n, int vocab,
-               int hidden, int slices, int sum_blocks, const uint32_t* __restrict__ seen, float* __restrict__ parts,
-               int64_t parts_ld, Grad<TG> g) {
+               int hidden, int slices, int run, float* __restrict__ parts, int64_t parts_ld, Grad<TG> g) {
   let_next_start();
   wait_for_previous();
-  if (static_cast<int>(blockIdx.x) >= sum_blocks) {
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x - sum_blocks) * kZeroRows;
-    float zero[8] = {};
-    for (int64_t r = r0; r < r0 + kZeroRows && r < vocab; ++r) {
-      if ((seen[r >> 5] >> (r & 31)) & 1) continue;
-      for (int col = threadIdx.x * 8; col < hidden; col += kSumCols) store8<VEC>(g.data + r * g.ld + col, hidden - col, zero);
-    }
-    return;
-  }
   const int chunk = blockIdx.x / slices;
-  const int col = (blockIdx.x - chunk * slices) * kSumCols + threadIdx.x * 8;
-  __shared__ uint32_t key[kRun + 2], pos[kRun];
-  const int64_t e0 = static_cast<int64_t>(chunk) * kRun;
-  const int len = n - e0 < kRun ? static_cast<int>(n - e0) : kRun;
+  const int col = (blockIdx.x - chunk * slices) * kSumCols, left = hidden - col;
+  __shared__ uint32_t key[kMaxRun + 2], pos[kMaxRun];
+  const int64_t e0 = static_cast<int64_t>(chunk) * run;
+  const int len = n - e0 < run ? static_cast<int>(n - e0) : run;
   constexpr uint32_t kNone = 0xffffffffu;
-  if (threadIdx.x < kRun + 2) {
+  if (static_cast<int>(threadIdx.x) < run + 2) {
     const int64_t e = e0 + threadIdx.x - 1;
     const uint2 it = e >= 0 && e < n ? sorted[e] : make_uint2(kNone, 0);
     key[threadIdx.x] = it.x;
-    if (threadIdx.x >= 1 && threadIdx.x <= kRun) pos[threadIdx.x - 1] = it.y;
+    if (threadIdx.x >= 1 && static_cast<int>(threadIdx.x) <= run) pos[threadIdx.x - 1] = it.y;
   }
   __syncthreads();
-  if (col >= hidden) return;
-  const int left = hidden - col;
   float acc[8] = {};
   bool head = key[0] == key[1];
-  constexpr int kBatch = 4;  // rows in flight per thread
+  constexpr int kBatch = VEC && sizeof(TD) == 2 ? 8 : 4;  // rows in flight per thread
   for (int j0 = 0; j0 < len; j0 += kBatch) {
-    float v[kBatch][8];
+    float v[kBatch][8] = {};
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
-      if (j0 + j < len) load8<VEC>(dout + static_cast<int64_t>(pos[j0 + j]) * dout_ld + col, left, v[j]);
+      if (j0 + j < len)
+        load8<VEC, kSumThreads>(dout + static_cast<int64_t>(pos[j0 + j]) * dout_ld + col, threadIdx.x, left, v[j]);
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int e = j0 + j;
@@ -316,8 +350,7 @@ __global__ void __launch_bounds__(kSumThreads)
       if (k < static_cast<uint32_t>(vocab)) {
         if (head || more) {
           float* p = parts + (static_cast<int64_t>(chunk) * 2 + (head ? 0 : 1)) * parts_ld + col;
-          *reinterpret_cast<float4*>(p) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          *reinterpret_cast<float4*>(p + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+          store8<VEC, kSumThreads>(p, threadIdx.x, left, acc);
         } else {
           write_row<TG, VEC>(g, k, col, left, acc);
         }
@@ -333,29 +366,37 @@ __global__ void __launch_bounds__(kSumThreads)
 // following CTAs in order.
 template <class TG, bool VEC>
 __global__ void __launch_bounds__(kSumThreads)
-    join_kernel(const uint2* __restrict__ sorted, int n, int vocab, int hidden, int slices,
+    join_kernel(const uint2* __restrict__ sorted, int n, int vocab, int hidden, int slices, int run, int chunks,
                 const float* __restrict__ parts, int64_t parts_ld, Grad<TG> g) {
   let_next_start();
   wait_for_previous();
   const int chunk = blockIdx.x / slices;
-  const int64_t e0 = static_cast<int64_t>(chunk) * kRun, e1 = e0 + kRun;
+  const int64_t e0 = static_cast<int64_t>(chunk) * run, e1 = e0 + run;
   if (e1 >= n) return;
-  const uint32_t k = sorted[e1 - 1].x;
-  if (k >= static_cast<uint32_t>(vocab) || sorted[e1].x != k) return;
-  if (e0 > 0 && sorted[e0 - 1].x == k) return;  // began earlier (sorted: the whole chunk is this run)
-  const int col = (blockIdx.x - chunk * slices) * kSumCols + threadIdx.x * 8;
-  if (col >= hidden) return;
-  float acc[8];
-  load8<true>(parts + (static_cast<int64_t>(chunk) * 2 + 1) * parts_ld + col, 8, acc);
-  for (int64_t c = chunk + 1;; ++c) {
-    float v[8];
-    load8<true>(parts + c * 2 * parts_ld + col, 8, v);
+  const uint32_t k = sorted[e1 - 1].x, after = sorted[e1].x, before = e0 > 0 ? sorted[e0 - 1].x : 0xffffffffu;
+  // no run that crosses here, or one that began earlier (sorted: all of this CTA's positions are it)
+  if (k >= static_cast<uint32_t>(vocab) || after != k || before == k) return;
+  const int col = (blockIdx.x - chunk * slices) * kSumCols, left = hidden - col;
+  float acc[8] = {};
+  load8<VEC, kSumThreads>(parts + (static_cast<int64_t>(chunk) * 2 + 1) * parts_ld + col, threadIdx.x, left, acc);
+  constexpr int kBatch = 4;  // parts in flight; those past the run's end are not used
+  for (int64_t c0 = chunk + 1;; c0 += kBatch) {
+    float v[kBatch][8] = {};
+    bool part[kBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], v[i]);
-    const int64_t next = (c + 1) * kRun;
-    if (next >= n || sorted[next].x != k) break;
+    for (int j = 0; j < kBatch; ++j) {
+      part[j] = c0 + j < chunks && sorted[(c0 + j) * run].x == k;
+      if (c0 + j < chunks) load8<VEC, kSumThreads>(parts + (c0 + j) * 2 * parts_ld + col, threadIdx.x, left, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (part[j]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], v[j][i]);
+      }
+    if (!part[kBatch - 1]) break;
   }
-  write_row<TG, VEC>(g, k, col, hidden - col, acc);
+  write_row<TG, VEC>(g, k, col, left, acc);
 }
 
 bool vec_rows(const lst_matrix* m) {
@@ -367,24 +408,30 @@ template <class TI, class TO>
 cudaError_t launch_embed(const lst_matrix* table, const lst_indices* tokens, const lst_matrix* out, float scale,
                          cudaStream_t stream) {
   const bool vec = vec_rows(table) && vec_rows(out);
-  const int64_t units = ops_ceil_div(out->cols, 8);
-  const int64_t rows_max = ((int64_t(1) << 31) - 1) / units * 128;
-  for (int64_t r0 = 0; r0 < out->rows; r0 += rows_max) {
-    const int64_t rows = out->rows - r0 < rows_max ? out->rows - r0 : rows_max;
-    const unsigned grid = static_cast<unsigned>(ops_ceil_div(rows * units, 256));
-    auto k = vec ? embed_kernel<TI, TO, true> : embed_kernel<TI, TO, false>;
-    const cudaError_t err = launch_chained(k, dim3(grid), dim3(256), 0, stream, static_cast<const TI*>(table->data), table->stride, tokens->data, tokens->bits == 64,
-                                static_cast<TO*>(out->data), out->stride, static_cast<int>(out->cols), table->rows,
-                                static_cast<uint32_t>(units), static_cast<uint32_t>(rows), r0, scale);
+  const int64_t per_row = ops_ceil_div(out->cols, 256), pieces = out->rows * per_row;
+  const int64_t per_block = 8 * kPieces;
+  // 2^30 rows of 2^23 pieces at most; a launch covers what its grid can count
+  const int64_t most = (int64_t(1) << 30) / per_row * per_row;
+  const int64_t at_once = std::max<int64_t>(per_row, std::min(pieces, most * per_block));
+  const int64_t rows_at_once = at_once / per_row;
+  for (int64_t r = 0; r < out->rows; r += rows_at_once) {
+    const int64_t rows = std::min(rows_at_once, out->rows - r), now = rows * per_row;
+    const cudaError_t err = launch_chained(
+        vec ? embed_kernel<TI, TO, true> : embed_kernel<TI, TO, false>,
+        dim3(static_cast<unsigned>(ops_ceil_div(now, per_block))), dim3(256), 0, stream,
+        static_cast<const TI*>(table->data), table->stride,
+        static_cast<const char*>(tokens->data) + r * (tokens->bits / 8), tokens->bits == 64,
+        static_cast<TO*>(out->data) + r * out->stride, out->stride, static_cast<int>(out->cols), table->rows,
+        static_cast<uint32_t>(per_row), now, scale);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
 }
 
 struct GradPlan {
-  int passes, digit_bits;
+  int passes, digit_bits, run;
   int64_t chunks, parts_ld;
-  int64_t buf_off[2], seen_off, parts_off, bytes;
+  int64_t buf_off[2], parts_off, bytes;
 };
 
 GradPlan grad_plan(int64_t n, int64_t hidden, int64_t vocab) {
@@ -393,15 +440,16 @@ GradPlan grad_plan(int64_t n, int64_t hidden, int64_t vocab) {
   while ((int64_t(1) << bits) <= vocab) ++bits;  // keys 0..vocab
   p.passes = bits <= 10 ? 1 : bits <= 20 ? 2 : 3;
   p.digit_bits = static_cast<int>(ops_ceil_div(bits, p.passes));
-  p.chunks = ops_ceil_div(n, kRun);
+  // 32 positions to a CTA, or 8 where that leaves the GPU short of CTAs: a short
+  // call's time is the latency of a CTA's rows one batch after the other
+  p.run = ops_ceil_div(n, kMaxRun) * ops_ceil_div(hidden, kSumCols) >= 152 * 16 ? kMaxRun : 8;
+  p.chunks = ops_ceil_div(n, p.run);
   p.parts_ld = ops_round_up(hidden, 8);
   int64_t at = 0;
   for (int i = 0; i < 2; ++i) {
     p.buf_off[i] = at;
     at += ops_round_up(n * 8, 256);
   }
-  p.seen_off = at;
-  at += ops_round_up((vocab + 31) / 32 * 4, 256);
   p.parts_off = at;
   at += ops_round_up(p.chunks * 2 * p.parts_ld * 4, 256);
   p.bytes = at;
@@ -415,26 +463,20 @@ cudaError_t launch_grad(const lst_matrix* dout, const lst_matrix* grad, const Gr
   const int n = static_cast<int>(dout->rows), hidden = static_cast<int>(dout->cols);
   const int vocab = static_cast<int>(grad->rows);
   const uint2* sorted = reinterpret_cast<const uint2*>(ws + p.buf_off[(p.passes - 1) & 1]);
-  const uint32_t* seen = reinterpret_cast<const uint32_t*>(ws + p.seen_off);
   float* parts = reinterpret_cast<float*>(ws + p.parts_off);
   const int64_t slices = ops_ceil_div(hidden, kSumCols);
   const int64_t sum_blocks = p.chunks * slices;
-  const int64_t zero_blocks = accumulate ? 0 : ops_ceil_div(vocab, kZeroRows);
-  if (sum_blocks + zero_blocks > INT32_MAX) return cudaErrorInvalidValue;
+  if (sum_blocks == 0) return cudaSuccess;
+  if (sum_blocks > INT32_MAX) return cudaErrorInvalidValue;
   const Grad<TG> g = {static_cast<TG*>(grad->data), grad->stride, scale, accumulate};
-  if (sum_blocks + zero_blocks > 0) {
-    auto k = vec ? sum_kernel<TD, TG, true> : sum_kernel<TD, TG, false>;
-    const cudaError_t err = launch_chained(k, dim3(static_cast<unsigned>(sum_blocks + zero_blocks)), dim3(kSumThreads), 0, stream, 
-        static_cast<const TD*>(dout->data), dout->stride, sorted, n, vocab, hidden, static_cast<int>(slices),
-        static_cast<int>(sum_blocks), seen, parts, p.parts_ld, g);
-    if (err != cudaSuccess) return err;
-  }
-  if (p.chunks > 1) {
-    auto k = vec ? join_kernel<TG, true> : join_kernel<TG, false>;
-    return launch_chained(k, dim3(static_cast<unsigned>(sum_blocks)), dim3(kSumThreads), 0, stream, sorted, n, vocab, hidden, static_cast<int>(slices),
-                                                                     parts, p.parts_ld, g);
-  }
-  return cudaSuccess;
+  const cudaError_t err = launch_chained(
+      vec ? sum_kernel<TD, TG, true> : sum_kernel<TD, TG, false>, dim3(static_cast<unsigned>(sum_blocks)),
+      dim3(kSumThreads), 0, stream, static_cast<const TD*>(dout->data), dout->stride, sorted, n, vocab, hidden,
+      static_cast<int>(slices), p.run, parts, p.parts_ld, g);
+  if (err != cudaSuccess || p.chunks == 1) return err;
+  return launch_chained(vec ? join_kernel<TG, true> : join_kernel<TG, false>, dim3(static_cast<unsigned>(sum_blocks)),
+                        dim3(kSumThreads), 0, stream, sorted, n, vocab, hidden, static_cast<int>(slices), p.run,
+                        static_cast<int>(p.chunks), parts, p.parts_ld, g);
 }
 
 }  // namespace
@@ -491,11 +533,15 @@ extern "C" lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* 
   // the largest case (10-bit digits) needs 139,264 bytes; a function attribute
   // is per device, so it is set on every call (host only, under a microsecond)
   LST_TRY_CUDA(cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), who);
-  LST_TRY_CUDA(launch_chained(sort_kernel, dim3(kSortCtas), dim3(kSortThreads), smem, s, tokens->data, tokens->bits == 64, static_cast<int>(dout->rows),
-                                                    static_cast<int>(grad->rows), p.passes, p.digit_bits,
-                                                    reinterpret_cast<uint2*>(ws + p.buf_off[0]),
-                                                    reinterpret_cast<uint2*>(ws + p.buf_off[1]),
-                                                    reinterpret_cast<uint32_t*>(ws + p.seen_off)), who);
+  const int64_t row = grad->cols * dtype_bytes(grad->dtype), pitch = grad->stride * dtype_bytes(grad->dtype);
+  const bool flat = row == pitch && reinterpret_cast<uintptr_t>(grad->data) % 16 == 0 && row * grad->rows % 16 == 0;
+  // two CTAs per SM; the clusters after the first zero the gradient
+  const unsigned grid = accumulate ? kSortCtas : 2 * 152;
+  LST_TRY_CUDA(launch_chained(sort_kernel, dim3(grid), dim3(kSortThreads), smem, s, tokens->data, tokens->bits == 64,
+                              static_cast<int>(dout->rows), static_cast<int>(grad->rows), p.passes, p.digit_bits,
+                              reinterpret_cast<uint2*>(ws + p.buf_off[0]), reinterpret_cast<uint2*>(ws + p.buf_off[1]),
+                              static_cast<char*>(grad->data), pitch, flat ? row * grad->rows : row, flat ? 1 : 0),
+               who);
   const int kind = (dout->dtype == LST_F32 ? 2 : 0) + (grad->dtype == LST_F32 ? 1 : 0);
   cudaError_t err;
   switch (kind) {

@@ -17,6 +17,7 @@
 // 128: twice the pairs at work, half the time to a tile's end.
 #include "lst_gemm.h"
 
+#include <algorithm>
 #include <mutex>
 
 #include "lst_ops.h"
@@ -139,6 +140,7 @@ __device__ __forceinline__ void store_row32(uint16_t* p, const uint32_t (&w)[16]
 
 struct StoreEpilogue {
   using Params = StoreParams;
+  static __device__ __forceinline__ void begin(const Params&) {}
   using Table = Nothing;
   static __device__ __forceinline__ void store(const Params& e, const Shape& s, const Tile& t, uint16_t* out,
                                                const uint16_t* c, bool bf16, bool mirror, int row, int col,
@@ -205,6 +207,7 @@ struct StoreEpilogue {
 // The Muon update of the weights by a tile of the orthogonalised matrix.
 struct UpdateEpilogue {
   using Params = UpdateParams;
+  static __device__ __forceinline__ void begin(const Params&) {}
   using Table = UpdateTable;
   static __device__ __forceinline__ void store(const Params& e, float step, void* w, uint16_t* w16, int left,
                                                const float (&v)[32]) {
@@ -316,6 +319,24 @@ struct PartialEpilogue {
   }
 };
 
+struct GradParams {
+  StoreParams store;
+  PartialParams partial;
+};
+struct GradEpilogue {
+  using Params = GradParams;
+  static __device__ __forceinline__ void begin(const Params&) {}
+  using Table = Nothing;
+  template <int kCols, class Release>
+  static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
+                                             int col0, uint32_t tmem, Release release) {
+    if (e.partial.out)
+      PartialEpilogue::run<kCols>(e.partial, table, s, t, row, col0, tmem, release);
+    else
+      StoreEpilogue::run<kCols>(e.store, table, s, t, row, col0, tmem, release);
+  }
+};
+
 // One row's logits of 128 vocabulary entries: their maximum M, the sum of
 // exp(l - M), the target's logit where it is among them, and (for the
 // gradient) q = (M - l) * 2^11 in 16 bits. q keeps l to 2^-12 over the 32
@@ -325,6 +346,9 @@ struct PartialEpilogue {
 struct XentEpilogue {
   using Params = XentParams;
   using Table = Nothing;
+  static __device__ __forceinline__ void begin(const Params& e) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *e.counter = 0;
+  }
   template <int kCols, class Release>
   static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
                                              int col0, uint32_t tmem, Release release) {
@@ -427,6 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
   wait_for_previous();
+  Epi::begin(g.epi[0]);
 
   bool ok = true;
   if (warp == 0) {
@@ -607,7 +632,7 @@ int resident_pairs() {
 }
 
 void set_params(StoreParams* e, Nothing*, const GemmProblem& p, const UpdateTable*) { *e = p.store; }
-void set_params(PartialParams* e, Nothing*, const GemmProblem& p, const UpdateTable*) { *e = p.partial; }
+void set_params(GradParams* e, Nothing*, const GemmProblem& p, const UpdateTable*) { *e = {p.store, p.partial}; }
 void set_params(XentParams* e, Nothing*, const GemmProblem& p, const UpdateTable*) { *e = p.xent; }
 void set_params(UpdateParams* e, UpdateTable* t, const GemmProblem& p, const UpdateTable* updates) {
   *e = p.update;
@@ -682,30 +707,20 @@ cudaError_t launch_gemm(GemmKind kind, const GemmProblem* p, int count, cudaStre
   switch (kind) {
     case GEMM_F16: return launch_fit<StoreEpilogue, false>(p, count, stream, nullptr);
     case GEMM_F16_UPDATE: return launch_fit<UpdateEpilogue, false>(p, count, stream, updates);
-    case GEMM_BF16: return launch_fit<StoreEpilogue, true>(p, count, stream, nullptr);
-    case GEMM_BF16_PARTS: return launch<PartialEpilogue, true, 256>(p, count, stream, nullptr);
+    case GEMM_BF16: return launch_fit<GradEpilogue, true>(p, count, stream, nullptr);
     case GEMM_BF16_XENT: return launch<XentEpilogue, true, 256>(p, count, stream, nullptr);
   }
   return cudaErrorInvalidValue;
 }
 
-// A split costs each tile its pipeline's ramp and, in fp32, a partial sum to
-// write and read: about 3 K steps for a whole tile, 12 for a part of one. Taken:
-// the count with the shortest run of rounds over the 76 pairs of 152 SMs.
-int gemm_splits(int64_t tiles, int64_t k) {
-  const int64_t blocks = ceil_div(k, kTileK);
-  int64_t best = 1, best_cost = 0;
-  for (int64_t s = 1; s <= 32 && s <= blocks; ++s) {
-    const int64_t per = ceil_div(blocks, s);
-    const int64_t real = ceil_div(blocks, per);
-    if (real != s) continue;
-    const int64_t cost = ceil_div(tiles * s, 76) * (per + (s > 1 ? 12 : 3));
-    if (s == 1 || cost < best_cost) {
-      best = s;
-      best_cost = cost;
-    }
-  }
-  return static_cast<int>(best);
+// A split costs a partial sum to write and to read, and a whole sum on one pair
+// may outlast everything else in the launch. Taken: the fewest splits with which
+// a tile takes no more than half of a pair's share of the work (76 pairs).
+int gemm_splits(int64_t tiles, int64_t k, int64_t others) {
+  const int64_t blocks = ceil_div(k, kTileK), share = (tiles * blocks + others) / 76;
+  int64_t s = 1;
+  while (s < 32 && ceil_div(blocks, s) > std::max<int64_t>(share / 2, 8)) ++s;
+  return static_cast<int>(ceil_div(blocks, ceil_div(blocks, s)));
 }
 
 cudaError_t gemm_take_error(int* out) {

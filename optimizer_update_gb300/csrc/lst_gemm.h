@@ -45,7 +45,7 @@ struct UpdateParams {
 };
 
 // fp32 partial sums of a K range: out[split][row][col], added to what is there
-// when `accumulate` is set.
+// when `accumulate` is set. Used in place of StoreParams where out is not null.
 struct PartialParams {
   float* out;
   int64_t ld, split_stride;
@@ -58,6 +58,7 @@ struct XentParams {
   const void* targets;
   float2* stats;    // [128-column group][row]: (max, sum of exp(l - max))
   float* target_logit;
+  int32_t* counter; // set to 0
   uint16_t* q;      // [row][column]: (max - l) in steps of 2^-11, or null
   int64_t q_ld, stat_ld, first_group, first_column;
   int32_t index_bytes;
@@ -66,8 +67,7 @@ struct XentParams {
 enum GemmKind {
   GEMM_F16,         // fp16 operands, StoreParams
   GEMM_F16_UPDATE,  // fp16 operands, UpdateParams
-  GEMM_BF16,        // bf16 operands, StoreParams
-  GEMM_BF16_PARTS,  // bf16 operands, PartialParams
+  GEMM_BF16,        // bf16 operands, StoreParams or PartialParams
   GEMM_BF16_XENT,   // bf16 operands, XentParams
 };
 
@@ -75,7 +75,7 @@ struct GemmProblem {
   GemmOperand a, b;
   int64_t m, n, k, batch = 1;
   bool symmetric = false;  // the result is symmetric: form one triangle of tiles and mirror it
-  int splits = 1;          // K ranges (GEMM_BF16_PARTS)
+  int splits = 1;          // K ranges (PartialParams)
   StoreParams store{};
   PartialParams partial{};
   XentParams xent{};
@@ -89,8 +89,9 @@ constexpr int kGemmTile = 256;
 cudaError_t launch_gemm(GemmKind kind, const GemmProblem* problems, int count, cudaStream_t stream,
                         const UpdateTable* updates = nullptr);
 
-// K ranges that fill the GPU for `tiles` output tiles of `k` elements each.
-int gemm_splits(int64_t tiles, int64_t k);
+// K ranges into which `tiles` output tiles with sums over `k` are to be split
+// when they share a launch with products of `others` tile steps of 64 in all.
+int gemm_splits(int64_t tiles, int64_t k, int64_t others);
 
 // Whether some wait of a matrix kernel ran out since the last call on this
 // device (synchronises the device).

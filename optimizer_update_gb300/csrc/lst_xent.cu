@@ -44,10 +44,13 @@ __device__ __forceinline__ int64_t target_at(const void* t, int wide, int64_t i)
 
 // lse and loss of 32 rows from the statistics of all 128-column groups: 32
 // threads per row take every 32nd group each, with the running maximum and sum.
+// With `mean`, the last block to finish also forms the mean loss and g =
+// grad_scale / N from all losses, in a fixed order.
 __global__ void __launch_bounds__(1024)
     join_kernel(const float2* __restrict__ stats, int64_t stat_ld, int groups, const float* __restrict__ target_logit,
-                const void* __restrict__ targets, int wide, int64_t ignore, int64_t vocab, int rows,
-                float* __restrict__ loss, float* __restrict__ lse) {
+                const void* __restrict__ targets, int wide, int64_t ignore, int64_t vocab, int rows, float* loss,
+                float* __restrict__ lse, float grad_scale, float* __restrict__ mean, float* __restrict__ g,
+                int32_t* counter) {
   let_next_start();
   wait_for_previous();
   __shared__ float2 part[32][33];
@@ -56,8 +59,9 @@ __global__ void __launch_bounds__(1024)
   const float ninf = __int_as_float(0xff800000);
   float top = ninf, sum = 0.0f;
   if (row < rows) {
-    for (int g = warp; g < groups; g += 32) {
-      const float2 s = stats[g * stat_ld + row];
+#pragma unroll 8
+    for (int i = warp; i < groups; i += 32) {
+      const float2 s = stats[i * stat_ld + row];
       const float m = fmaxf(top, s.x);
       const float base = m == ninf ? 0.0f : m;
       sum = sum * exp2f((top - base) * kLog2e) + s.y * exp2f((s.x - base) * kLog2e);
@@ -82,68 +86,99 @@ __global__ void __launch_bounds__(1024)
     lse[r] = l;
     loss[r] = t == ignore ? 0.0f : (t >= 0 && t < vocab) ? l - target_logit[r] : __int_as_float(0x7fc00000);
   }
-}
+  if (!mean) return;
 
-// mean loss, and g = grad_scale / N, by one block in a fixed order.
-__global__ void __launch_bounds__(1024)
-    mean_kernel(const float* __restrict__ loss, const void* __restrict__ targets, int wide, int64_t ignore, int rows,
-                float grad_scale, float* __restrict__ mean, float* __restrict__ g) {
-  let_next_start();
-  wait_for_previous();
-  double sum = 0.0;
+  __shared__ int last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(counter, 1) == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double total = 0.0;
   int count = 0;
+#pragma unroll 4
   for (int i = threadIdx.x; i < rows; i += 1024)
     if (target_at(targets, wide, i) != ignore) {
-      sum += static_cast<double>(loss[i]);
+      total += static_cast<double>(__ldcg(loss + i));
       ++count;
     }
-  __shared__ double s[32];
-  __shared__ int c[32];
+  __shared__ double sums[32];
+  __shared__ int counts[32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_down_sync(0xffffffffu, sum, o);
+    total += __shfl_down_sync(0xffffffffu, total, o);
     count += __shfl_down_sync(0xffffffffu, count, o);
   }
-  if ((threadIdx.x & 31) == 0) {
-    s[threadIdx.x >> 5] = sum;
-    c[threadIdx.x >> 5] = count;
+  if (lane == 0) {
+    sums[warp] = total;
+    counts[warp] = count;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < 32; ++i) {
-      sum += s[i];
-      count += c[i];
+      total += sums[i];
+      count += counts[i];
     }
-    *mean = count ? static_cast<float>(sum / count) : 0.0f;
+    *mean = count ? static_cast<float>(total / count) : 0.0f;
     *g = count ? static_cast<float>(static_cast<double>(grad_scale) / count) : 0.0f;
   }
 }
 
-// d over q, in place: 8 entries per thread, one row per block of columns.
+// A row whose target takes part in the gradient.
+__device__ __forceinline__ bool in_gradient(int64_t t, int64_t ignore, int64_t vocab) {
+  return t != ignore && t >= 0 && t < vocab;
+}
+
+// x as the product d^T x reads it: rows without a gradient become zero, since d
+// is zero there but 0 * infinity would reach dw.
+struct MaskedRows {
+  const uint16_t* src;
+  uint16_t* dst;
+  int64_t ld, dst_ld;
+  int32_t rows, cols, vec;
+};
+
+// d over q, in place: 16 entries per thread, one row per block of columns. The
+// blocks after the first `d_blocks` copy x with its rows masked.
 __global__ void __launch_bounds__(256)
     logit_grad_kernel(uint16_t* __restrict__ q, int64_t q_ld, const float2* __restrict__ stats, int64_t stat_ld,
                       int64_t first_group, int64_t first_column, int columns, const float* __restrict__ lse,
                       const float* __restrict__ target_logit, const void* __restrict__ targets, int wide,
-                      int64_t ignore, int64_t vocab, const float* __restrict__ gp, int blocks_per_row) {
+                      int64_t ignore, int64_t vocab, const float* __restrict__ gp, int blocks_per_row, int d_blocks,
+                      MaskedRows x) {
   let_next_start();
   wait_for_previous();
+  if (static_cast<int>(blockIdx.x) >= d_blocks) {
+    for (int64_t r = blockIdx.x - d_blocks; r < x.rows; r += gridDim.x - d_blocks) {
+      const bool keep = in_gradient(target_at(targets, wide, r), ignore, vocab);
+      if (x.vec) {
+        for (int c = threadIdx.x * 8; c < x.cols; c += 2048)
+          *reinterpret_cast<uint4*>(x.dst + r * x.dst_ld + c) =
+              keep ? *reinterpret_cast<const uint4*>(x.src + r * x.ld + c) : make_uint4(0, 0, 0, 0);
+      } else {
+        for (int c = threadIdx.x; c < x.cols; c += 256) x.dst[r * x.dst_ld + c] = keep ? x.src[r * x.ld + c] : 0;
+      }
+    }
+    return;
+  }
   const int row = blockIdx.x / blocks_per_row;
-  const int col = ((blockIdx.x - row * blocks_per_row) * 256 + threadIdx.x) * 8;
+  const int col = ((blockIdx.x - row * blocks_per_row) * 256 + threadIdx.x) * 16;
   if (col >= columns) return;
   uint4* const p = reinterpret_cast<uint4*>(q + static_cast<int64_t>(row) * q_ld + col);
   const int64_t t = target_at(targets, wide, row);
-  if (t == ignore || t < 0 || t >= vocab) {
-    *p = make_uint4(0, 0, 0, 0);
+  if (!in_gradient(t, ignore, vocab)) {
+    p[0] = p[1] = make_uint4(0, 0, 0, 0);
     return;
   }
+  const uint4 x0 = p[0], x1 = p[1];
   const float g = *gp, l = lse[row];
   const float top = stats[(first_group + (col >> 7)) * stat_ld + row].x;
   const float base = (top - l) * kLog2e;
-  const uint4 x = *p;
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float d[8];
+  const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+  float d[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 16; ++i) {
     const float steps = static_cast<float>((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
     float e;
     const float a = __fmaf_rn(steps, -kLog2e / 2048.0f, base);
@@ -151,20 +186,21 @@ __global__ void __launch_bounds__(256)
     d[i] = e * g;
   }
   const int64_t at = t - first_column - col;
-  if (at >= 0 && at < 8) {
+  if (at >= 0 && at < 16) {
     // the target's own probability from its fp32 logit: p - 1 cancels when p is near 1
     const float e = expm1f(target_logit[row] - l) * g;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 16; ++i)
       if (i == static_cast<int>(at)) d[i] = e;
   }
-  uint32_t r[4];
+  uint32_t r[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(d[2 * i], d[2 * i + 1]);
     r[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  *p = make_uint4(r[0], r[1], r[2], r[3]);
+  p[0] = make_uint4(r[0], r[1], r[2], r[3]);
+  p[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
 // dx = sum of its parts, in order, rounded to bf16.
@@ -196,8 +232,7 @@ __global__ void __launch_bounds__(256)
 }
 
 // Rows at a pitch that is a multiple of 16 bytes, for operands that are not
-// laid out so (a rule of the tile loads). `ignore_rows`: rows whose target is
-// ignored become zero, so that nothing they hold reaches a sum over rows.
+// laid out so (a rule of the tile loads).
 __global__ void __launch_bounds__(256)
     pack_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t* __restrict__ dst,
                 int64_t dst_ld) {
@@ -205,28 +240,6 @@ __global__ void __launch_bounds__(256)
   wait_for_previous();
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
     for (int c = threadIdx.x; c < cols; c += 256) dst[r * dst_ld + c] = src[r * ld + c];
-}
-
-// Whether any ignored row holds a value that is not finite is not known without
-// reading x, so x is copied with its ignored rows zeroed for the product d^T x:
-// 0 * infinity would reach dw.
-__global__ void __launch_bounds__(256)
-    mask_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t* __restrict__ dst,
-                     int64_t dst_ld, const void* __restrict__ targets, int wide, int64_t ignore, int64_t vocab,
-                     int vec) {
-  let_next_start();
-  wait_for_previous();
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const int64_t t = target_at(targets, wide, r);
-    const bool keep = t != ignore && t >= 0 && t < vocab;
-    if (vec) {
-      for (int c = threadIdx.x * 8; c < cols; c += 2048)
-        *reinterpret_cast<uint4*>(dst + r * dst_ld + c) =
-            keep ? *reinterpret_cast<const uint4*>(src + r * ld + c) : make_uint4(0, 0, 0, 0);
-    } else {
-      for (int c = threadIdx.x; c < cols; c += 256) dst[r * dst_ld + c] = keep ? src[r * ld + c] : 0;
-    }
-  }
 }
 
 bool tile_ready(const lst_matrix* m) {
@@ -263,11 +276,16 @@ bool make_plan(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool pac
   if (grad) {
     p->xm_off = take(n * p->packed_ld * 2);
     p->part_ld = ops_round_up(h, 32);
-    const int64_t tiles = ops_ceil_div(n, kGemmTile) * ops_ceil_div(h, kGemmTile);
+    const int64_t tiles_h = ops_ceil_div(h, kGemmTile), tiles = ops_ceil_div(n, kGemmTile) * tiles_h;
+    // dx shares its launch with dw, whose sums go over the tokens (and 3 steps for a tile's ramp)
+    auto split = [&](int64_t piece) {
+      const int64_t columns = std::min(piece, v);
+      return gemm_splits(tiles, columns, ops_ceil_div(columns, kGemmTile) * tiles_h * (ops_ceil_div(n, 64) + 3));
+    };
     const int64_t whole = ops_round_up(v, kGemmTile);
     const int64_t most = std::max<int64_t>(kGemmTile, kMaxPieceBytes / (2 * n) / kGemmTile * kGemmTile);
     auto parts = [&](int64_t piece) {
-      const int64_t splits = gemm_splits(tiles, std::min(piece, v));
+      const int64_t splits = split(piece);
       return splits > 1 || piece < v ? splits * n * p->part_ld * 4 + 256 : 0;
     };
     int64_t piece = std::min(whole, most);
@@ -277,7 +295,7 @@ bool make_plan(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool pac
     if (piece <= 0) return false;
     p->piece = piece;
     p->pieces = ops_ceil_div(v, piece);
-    p->splits = gemm_splits(tiles, std::min(piece, v));
+    p->splits = split(piece);
     p->part_off = take(parts(piece));
     p->q_off = take(n * piece * 2);
   }
@@ -344,16 +362,17 @@ struct Call {
     g.n = columns;
     g.k = x->cols;
     g.xent = {targets->data, reinterpret_cast<float2*>(ws + p.stats_off), reinterpret_cast<float*>(ws + p.tlogit_off),
-              keep ? reinterpret_cast<uint16_t*>(ws + p.q_off) : nullptr, p.piece, p.n_pad, v0 / 128, v0,
+              reinterpret_cast<int32_t*>(ws + p.scalar_off) + 1, keep ? reinterpret_cast<uint16_t*>(ws + p.q_off) : nullptr, p.piece, p.n_pad, v0 / 128, v0,
               targets->bits / 8};
     return launch_gemm(GEMM_BF16_XENT, &g, 1, stream);
   }
 
-  cudaError_t join() {
+  cudaError_t join(float grad_scale, float* mean) {
     return launch_chained(join_kernel, dim3(static_cast<unsigned>(ops_ceil_div(x->rows, 32))), dim3(1024), 0, stream, 
         reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, static_cast<int>(p.groups),
         reinterpret_cast<const float*>(ws + p.tlogit_off), targets->data, wide, ignore, w->rows,
-        static_cast<int>(x->rows), loss, lse);
+        static_cast<int>(x->rows), loss, lse, grad_scale, mean, reinterpret_cast<float*>(ws + p.scalar_off),
+        reinterpret_cast<int32_t*>(ws + p.scalar_off) + 1);
   }
 };
 
@@ -388,7 +407,7 @@ extern "C" lst_status lst_xent_loss(const lst_matrix* x, const lst_matrix* w, co
   LST_TRY(check_workspace(workspace, workspace_bytes, c.p.bytes, who));
   LST_TRY_CUDA(c.operands(), who);
   LST_TRY_CUDA(c.logits(0, w->rows, false), who);
-  LST_TRY_CUDA(c.join(), who);
+  LST_TRY_CUDA(c.join(0.0f, nullptr), who);
   return LST_OK;
 }
 
@@ -433,27 +452,30 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
   uint16_t* q = reinterpret_cast<uint16_t*>(ws + p.q_off);
 
   LST_TRY_CUDA(c.operands(), who);
-  LST_TRY_CUDA(launch_chained(mask_rows_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(n, 8192))), dim3(256), 0, stream, 
-      static_cast<const uint16_t*>(c.xp), c.x_ld, n, static_cast<int>(h), xm, p.packed_ld, targets->data, c.wide,
-      ignore_index, v, h % 8 == 0), who);
   for (int64_t k = p.pieces - 1; k >= 0; --k) {
     const int64_t v0 = k * p.piece;
     LST_TRY_CUDA(c.logits(v0, std::min(p.piece, v - v0), k == 0), who);
   }
-  LST_TRY_CUDA(c.join(), who);
-  LST_TRY_CUDA(launch_chained(mean_kernel, dim3(1), dim3(1024), 0, stream, loss, targets->data, c.wide, ignore_index, static_cast<int>(n), grad_scale, mean, g), who);
+  LST_TRY_CUDA(c.join(grad_scale, mean), who);
   const bool parts = p.splits > 1 || p.pieces > 1;
   // the first piece sets every partial sum of dx: only the last can be shorter,
   // with fewer splits
   for (int64_t k = 0; k < p.pieces; ++k) {
     const int64_t v0 = k * p.piece, columns = std::min(p.piece, v - v0);
     if (k > 0) LST_TRY_CUDA(c.logits(v0, columns, true), who);
-    const int blocks = static_cast<int>(ops_ceil_div(columns, 2048));
-    LST_TRY_CUDA(launch_chained(logit_grad_kernel, dim3(static_cast<unsigned>(n * blocks)), dim3(256), 0, stream, 
-        q, p.piece, reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, v0 / 128, v0, static_cast<int>(columns),
-        lse, reinterpret_cast<const float*>(ws + p.tlogit_off), targets->data, c.wide, ignore_index, v, g, blocks), who);
-    // dw of the piece = d^T x
-    GemmProblem d;
+    const int blocks = static_cast<int>(ops_ceil_div(columns, 4096));
+    const int64_t d_blocks = n * blocks, copies = k == 0 ? std::min<int64_t>(n, 2048) : 0;
+    const MaskedRows masked = {static_cast<const uint16_t*>(c.xp), xm, c.x_ld, p.packed_ld, static_cast<int32_t>(n),
+                               static_cast<int32_t>(h), h % 8 == 0};
+    LST_TRY_CUDA(launch_chained(logit_grad_kernel, dim3(static_cast<unsigned>(d_blocks + copies)), dim3(256), 0, stream, q,
+                                p.piece, reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, v0 / 128, v0,
+                                static_cast<int>(columns), lse, reinterpret_cast<const float*>(ws + p.tlogit_off),
+                                targets->data, c.wide, ignore_index, v, g, blocks, static_cast<int>(d_blocks), masked),
+                 who);
+    // dw of the piece = d^T x, and dx += d w, in one launch: the tiles of the longer sums first
+    GemmProblem both[2];
+    GemmProblem& d = both[n > columns / p.splits ? 0 : 1];
+    GemmProblem& e = both[n > columns / p.splits ? 1 : 0];
     d.a = rows_operand(q, n, columns, p.piece, true);
     d.b = rows_operand(xm, n, h, p.packed_ld, true);
     d.m = columns;
@@ -461,9 +483,6 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
     d.k = n;
     uint16_t* dwp = static_cast<uint16_t*>(dw->data) + v0 * dw->stride;
     d.store = {dwp, accumulate_dw ? dwp : nullptr, dw->stride, 0, 1.0f, 1.0f, 0.0f, 1, store_width(dw)};
-    LST_TRY_CUDA(launch_gemm(GEMM_BF16, &d, 1, stream), who);
-    // dx += d w
-    GemmProblem e;
     e.a = rows_operand(q, n, columns, p.piece);
     e.b = rows_operand(static_cast<const uint16_t*>(c.wp) + v0 * c.w_ld, columns, h, c.w_ld, true);
     e.m = n;
@@ -472,11 +491,10 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
     if (parts) {
       e.splits = static_cast<int>(p.splits);
       e.partial = {reinterpret_cast<float*>(ws + p.part_off), p.part_ld, n * p.part_ld, k > 0};
-      LST_TRY_CUDA(launch_gemm(GEMM_BF16_PARTS, &e, 1, stream), who);
     } else {
       e.store = {dx->data, nullptr, dx->stride, 0, 1.0f, 0.0f, 0.0f, 1, store_width(dx)};
-      LST_TRY_CUDA(launch_gemm(GEMM_BF16, &e, 1, stream), who);
     }
+    LST_TRY_CUDA(launch_gemm(GEMM_BF16, both, 2, stream), who);
   }
   if (parts) {
     const int64_t quads = ops_ceil_div(h, 4) * n;
