@@ -14,7 +14,7 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblst.so")
 
 SOURCES = ["lst_layout.cpp", "lst_api.cpp", "lst_stream.cpp", "lst_store.cpp", "lst_kernels.cu", "lst_kernels_ex.cu", "lst_noalloc.cu", "lst_copy.cu",
-           "lst_gemm.cu", "lst_embed.cu", "lst_xent.cu", "lst_muon.cu"]
+           "lst_gemm.cu", "lst_embed.cu", "lst_xent.cu", "lst_muon.cu", "lst_ns_small.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -34,15 +34,12 @@
 
 #include "lst_device.cuh"
 #include "lst_gemm.h"
+#include "lst_ns.h"
 #include "lst_ops.h"
 
 namespace lst {
 
 namespace {
-
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-// power-of-two scales of the stored fp16 values
-constexpr float kScaleX = 16384.0f, kScaleA = 16384.0f, kScaleQ = 8192.0f, kScaleQA = 16384.0f, kScaleR = 4096.0f;
 
 constexpr int kItemsPerLaunch = 32;
 constexpr int kNormBlocks = 512;   // partial sums per matrix
@@ -61,11 +58,6 @@ struct Item {
 struct ItemTable {
   Item it[kItemsPerLaunch];
 };
-struct MuonScalars {
-  float momentum, eps;
-  int32_t nesterov;
-};
-
 __device__ __forceinline__ float load_in(const void* p, int64_t i, bool f32) {
   return f32 ? static_cast<const float*>(p)[i]
              : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
@@ -83,14 +75,6 @@ __device__ __forceinline__ void load_in8(const void* p, int64_t i, float (&v)[8]
   }
 }
 
-// u of one element; `m` is the momentum already updated.
-__device__ __forceinline__ float muon_u(float g, float m, const MuonScalars& s) {
-  return s.nesterov ? __fadd_rn(g, __fmul_rn(s.momentum, m)) : m;
-}
-__device__ __forceinline__ float new_momentum(float m, float g, const MuonScalars& s) {
-  return __fadd_rn(__fmul_rn(s.momentum, m), g);
-}
-
 // Whether every row of the matrix can be read in vectors of 8.
 template <bool MOM>
 __device__ __forceinline__ bool vector_rows(const Item& it) {
@@ -103,7 +87,7 @@ __device__ __forceinline__ bool vector_rows(const Item& it) {
 // instruction per SM and 16 clocks for a warp, so few threads use it). Bound by
 // memory: reads g and m, writes m.
 template <bool F32, bool MOM>
-__global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ ItemTable t, MuonScalars s) {
+__global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ ItemTable t, NsMomentum s) {
   let_next_start();
   wait_for_previous();
   const Item& it = t.it[blockIdx.y];
@@ -166,7 +150,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ ItemT
 
 // X_0 = u / (|u|_F + eps), in fp16 times kScaleX.
 template <bool F32, bool MOM>
-__global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ ItemTable t, MuonScalars s, int parts) {
+__global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ ItemTable t, NsMomentum s, int parts) {
   let_next_start();
   wait_for_previous();
   const Item& it = t.it[blockIdx.y];
@@ -374,7 +358,7 @@ struct Runner {
   }
   // stack `out` = Q of the Gram matrices in stack `a`
   cudaError_t polynomial(int out, int a) {
-    return product(out, a, a, kC * kScaleQ / (kScaleA * kScaleA), a, kB * kScaleQ / kScaleA, kA * kScaleQ);
+    return product(out, a, a, kNsC * kScaleQ / (kScaleA * kScaleA), a, kNsB * kScaleQ / kScaleA, kNsA * kScaleQ);
   }
   // S X (or X S) of matrices first .. first + count of a group, without a destination.
   GemmProblem applied(const Batch::Group& g, int s, int x, int64_t first, int64_t count) const {
@@ -443,7 +427,7 @@ bool use_pairs(const Shape2* s, int64_t count) {
 }
 
 // Norms and X_0 of a batch's items, a few at a time (kIngestBytes).
-cudaError_t ingest(const std::vector<Item>& items, bool f32, bool mom, const MuonScalars& s, cudaStream_t stream) {
+cudaError_t ingest(const std::vector<Item>& items, bool f32, bool mom, const NsMomentum& s, cudaStream_t stream) {
   const int64_t size = (f32 ? 4 : 2) + (mom ? 4 : 0);
   for (size_t i = 0; i < items.size();) {
     ItemTable t;
@@ -507,8 +491,19 @@ extern "C" lst_status lst_orthogonalize(int32_t count, const lst_matrix* in, con
   if (in[0].rows == 0 || in[0].cols == 0) return LST_OK;
   const Shape2 shape = {in[0].rows, in[0].cols};
   LST_TRY(check_workspace(workspace, workspace_bytes, Batch::item_bytes(shape), who));
+  if (ns_small_fits(shape.rows, shape.cols)) {
+    const NsSmallCall call = {shape.rows, shape.cols, in[0].dtype == LST_F32, -1, params->steps, 1.0f, {0.0f, params->eps, 0}};
+    NsSmallItem items[kNsSmallItems];
+    for (int32_t first = 0; first < count; first += kNsSmallItems) {
+      const int now = std::min(kNsSmallItems, count - first);
+      for (int i = 0; i < now; ++i)
+        items[i] = {in[first + i].data, nullptr, out[first + i].data, nullptr, in[first + i].stride, out[first + i].stride, 0.0f};
+      LST_TRY_CUDA(ns_small(items, now, call, static_cast<cudaStream_t>(cuda_stream)), who);
+    }
+    return LST_OK;
+  }
   const int64_t fit = workspace_bytes / Batch::item_bytes(shape);
-  const MuonScalars s = {0.0f, params->eps, 0};
+  const NsMomentum s = {0.0f, params->eps, 0};
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   char* ws = static_cast<char*>(workspace);
   try {
@@ -620,9 +615,33 @@ extern "C" lst_status lst_muon_step(const lst_layout* L, void* const* dev_blocks
     std::stable_sort(picks.begin(), picks.end(), [](const Pick& a, const Pick& b) { return a.s < b.s; });
     cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
     char* ws = static_cast<char*>(workspace);
-    const MuonScalars ms = {hp->momentum, hp->eps, hp->nesterov ? 1 : 0};
+    const NsMomentum ms = {hp->momentum, hp->eps, hp->nesterov ? 1 : 0};
     const float decay = (float)(1.0 - (double)hp->lr * (double)hp->weight_decay);
     const bool f32 = L->fmt == LST_L16_FP32;
+
+    auto step_of = [&](const Shape2& z) {
+      const double rows = (double)z.rows, cols = (double)z.cols;
+      return (double)hp->lr * (hp->rms_scale > 0.0f ? (double)hp->rms_scale * std::sqrt(std::max(rows, cols))
+                                                    : std::sqrt(std::max(1.0, rows / cols)));
+    };
+    // small matrices: one kernel for those of a shape
+    std::vector<Pick> large;
+    std::vector<NsSmallItem> small;
+    for (size_t i = 0; i < picks.size(); ++i) {
+      const Shape2& z = picks[i].s;
+      if (!ns_small_fits(z.rows, z.cols)) {
+        large.push_back(picks[i]);
+        continue;
+      }
+      const Run r = run_of(L->tensors[(size_t)picks[i].tensor]);
+      small.push_back({r.g, r.m, r.w, static_cast<uint16_t*>(r.w16), z.cols, z.cols, (float)step_of(z)});
+      if (i + 1 == picks.size() || !(picks[i + 1].s == z)) {
+        const NsSmallCall call = {z.rows, z.cols, f32, L->fmt, hp->ns_steps, decay, ms};
+        LST_TRY_CUDA(ns_small(small.data(), (int)small.size(), call, stream), who);
+        small.clear();
+      }
+    }
+    picks.swap(large);
 
     for (size_t first = 0; first < picks.size();) {
       std::vector<Shape2> shapes;
@@ -659,9 +678,6 @@ extern "C" lst_status lst_muon_step(const lst_layout* L, void* const* dev_blocks
       };
       for (size_t i = b.groups.size(); i-- > 0;) {
         const Batch::Group& g = b.groups[i];
-        const double rows = (double)g.s.rows, cols = (double)g.s.cols;
-        const double s = hp->rms_scale > 0.0f ? (double)hp->rms_scale * std::sqrt(std::max(rows, cols))
-                                              : std::sqrt(std::max(1.0, rows / cols));
         for (int64_t k = 0; k < g.count;) {
           if (entries == kGemmMaxUpdates || run.pending.size() == kGemmMaxProblems) LST_TRY_CUDA(flush(), who);
           const int64_t now = std::min<int64_t>(g.count - k, kGemmMaxUpdates - entries);
@@ -672,7 +688,7 @@ extern "C" lst_status lst_muon_step(const lst_layout* L, void* const* dev_blocks
             const Run r = run_of(L->tensors[(size_t)picks[first + (size_t)(g.first + k + j)].tensor]);
             table.w[entries] = r.w;
             table.w16[entries] = static_cast<uint16_t*>(r.w16);
-            table.step[entries] = (float)((double)hp->lr * s / ((double)kScaleX * (double)scale));
+            table.step[entries] = (float)(step_of(g.s) / ((double)kScaleX * (double)scale));
           }
           k += now;
         }
@@ -705,6 +721,8 @@ extern "C" lst_status lst_operator_status(void) {
   int err = 0;
   LST_TRY_CUDA(cudaDeviceSynchronize(), "lst_operator_status");
   LST_TRY_CUDA(gemm_take_error(&err), "lst_operator_status");
-  if (err) return fail(LST_ERR_TIMEOUT, "a wait inside a matrix kernel ran out");
+  int small = 0;
+  LST_TRY_CUDA(ns_small_take_error(&small), "lst_operator_status");
+  if (err || small) return fail(LST_ERR_TIMEOUT, "a wait inside a matrix kernel ran out");
   return LST_OK;
 }

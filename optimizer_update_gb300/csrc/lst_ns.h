@@ -1,0 +1,54 @@
+// Newton-Schulz constants and the one-kernel form for small matrices.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace lst {
+
+// The quintic's coefficients, and the powers of two by which fp16 values of each
+// kind are stored (lst_muon.cu says why these).
+constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
+constexpr float kScaleX = 16384.0f, kScaleA = 16384.0f, kScaleQ = 8192.0f, kScaleQA = 16384.0f, kScaleR = 4096.0f;
+
+struct NsMomentum {
+  float momentum, eps;
+  int32_t nesterov;
+};
+
+// u of one element from its gradient and updated momentum.
+__device__ __forceinline__ float muon_u(float g, float m, const NsMomentum& s) {
+  return s.nesterov ? __fadd_rn(g, __fmul_rn(s.momentum, m)) : m;
+}
+__device__ __forceinline__ float new_momentum(float m, float g, const NsMomentum& s) {
+  return __fadd_rn(__fmul_rn(s.momentum, m), g);
+}
+
+// One matrix of a launch: the input (a gradient with its momentum, or the matrix
+// itself), and where the result goes: a bf16 matrix, or a weight to update.
+struct NsSmallItem {
+  const void* g;
+  float* mom;      // null: g is the matrix
+  void* out;       // bf16 result, or the weight
+  uint16_t* w16;   // derived bf16 weight (mixed layout)
+  int64_t ld, out_ld;
+  float step;      // lr * update scale (weights)
+};
+constexpr int kNsSmallItems = 48;
+struct NsSmallCall {
+  int64_t rows, cols;
+  int32_t f32;      // g is fp32
+  int32_t format;   // lst_format of the weight, or -1: bf16 result
+  int32_t steps;
+  float decay;
+  NsMomentum s;
+};
+
+// Whether matrices of this shape run in one kernel.
+bool ns_small_fits(int64_t rows, int64_t cols);
+cudaError_t ns_small(const NsSmallItem* items, int count, const NsSmallCall& call, cudaStream_t stream);
+// Whether one of its waits ran out since the last call (synchronises).
+cudaError_t ns_small_take_error(int* out);
+
+}  // namespace lst

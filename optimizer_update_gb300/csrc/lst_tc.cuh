@@ -134,6 +134,29 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
       : "memory");
 }
 
+// ---- tcgen05, one CTA (cta_group::1) -------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Makes shared-memory writes of this thread visible to the tensor cores and TMA.
+__device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
 // 32 accumulator columns of this warp's 32 lanes: thread i gets row i.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
   uint32_t r[32];
@@ -149,6 +172,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -161,11 +196,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // Shared-memory operand in 128-byte-swizzled atoms of 8 rows x 128 bytes.
 // K-major (K contiguous): 8-row groups 1024 bytes apart (stride offset).
 // MN-major (the other dimension contiguous): a 64-element chunk of it is
-// 8192 bytes (64 K rows x 128 bytes) from the next (leading offset), groups of
+// `chunk` bytes (K rows x 128 bytes) from the next (leading offset), groups of
 // 8 K rows 1024 bytes apart (stride offset).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn_major) {
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn_major, uint32_t chunk = 8192) {
   uint64_t d = (addr >> 4) & 0x3FFF;
-  d |= static_cast<uint64_t>(mn_major ? (8192 >> 4) : 1) << 16;
+  d |= static_cast<uint64_t>(mn_major ? (chunk >> 4) : 1) << 16;
   d |= static_cast<uint64_t>(1024 >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;  // sm_100 descriptor version
   d |= static_cast<uint64_t>(2) << 61;  // 128-byte swizzle
