@@ -35,7 +35,8 @@ constexpr int kM = 128;                       // rows held, zero beyond m
 constexpr int kChunk = kM * 128;              // bytes of 64 columns
 constexpr int kMaxChunks = 8;                 // of X per CTA
 constexpr int kMatrix = 2 * kChunk;           // bytes of an m x m matrix
-constexpr int kSmallThreads = 256;
+constexpr int kSmallThreads = 512;
+constexpr int kSmallWarps = kSmallThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kSmallSmem = kMaxChunks * kChunk + 3 * kMatrix + 1024 + 256;
 
@@ -79,14 +80,18 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
 struct Small {
   uint32_t x, s0, s1, s2, part, bar, tmem;
   uint32_t parity;
-  int rank, ranks, warp, lane, row, half;  // row: of the accumulator, half: of its columns
+  int rank, ranks, warp, lane;
+  int row, quarter;  // of the accumulator: the thread's row, the warp's quarter of 128 columns
+  int depth;         // m rounded up to 16: the rows and columns of S that are used
   bool ok;
+
+  __device__ __forceinline__ uint32_t lanes() const { return tmem + (static_cast<uint32_t>(row & ~31) << 16); }
 
   // Operands written and visible, then `issue` by one thread, then everyone
   // waits for its products.
   template <class Issue>
   __device__ __forceinline__ void multiply(Issue issue) {
-    tc::fence_async_proxy();
+    tc::fence_async_proxy_cta();
     tc::fence_before();
     __syncthreads();
     if (warp == 0) {
@@ -103,23 +108,28 @@ struct Small {
     __syncwarp();
   }
 
-  // out = alpha a b + beta a + diag I, in fp16
+  // out = alpha a b + beta a + diag I, in fp16. Rows beyond `depth` hold what
+  // they will: a row of a product depends on no other row of its first factor,
+  // and sums and columns end at `depth`.
   __device__ __forceinline__ void product(uint32_t out, uint32_t a, uint32_t b, float alpha, float beta, float diag) {
     const uint32_t d = tmem;
+    const int steps = depth / 16;
     multiply([=]() {
-      constexpr uint32_t idesc = tc::instr_desc(kM, kM, false, false, false);
-#pragma unroll
-      for (int k = 0; k < kM / 16; ++k) {
+      const uint32_t idesc = tc::instr_desc(kM, 16 * steps, false, false, false);
+#pragma unroll 1
+      for (int k = 0; k < steps; ++k) {
         const uint32_t off = (k >> 2) * kChunk + (k & 3) * 32;
         tc::mma_f16(d, tc::smem_desc(a + off, false), tc::smem_desc(b + off, false), idesc, k != 0);
       }
     });
-#pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-      const int col0 = half * 64 + j * 16;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int col0 = quarter * 32 + j * 16;
+      if (col0 >= depth) break;
       float v[16];
-      tc::tmem_ld16(tmem + (static_cast<uint32_t>(row & ~31) << 16) + col0, v);
-      const uint32_t at0 = half * kChunk + chunk_at(row, j * 16), at1 = half * kChunk + chunk_at(row, j * 16 + 8);
+      tc::tmem_ld16(lanes() + col0, v);
+      const uint32_t at0 = (quarter >> 1) * kChunk + chunk_at(row, (quarter & 1) * 32 + j * 16);
+      const uint32_t at1 = (quarter >> 1) * kChunk + chunk_at(row, (quarter & 1) * 32 + j * 16 + 8);
       const uint4 y0 = ld_shared_v4(a + at0), y1 = ld_shared_v4(a + at1);
       const uint32_t y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
       tc::tmem_ld_wait();
@@ -136,32 +146,63 @@ struct Small {
     }
   }
 
+  // Adds up the partial Gram matrices of C CTAs and gives s0 to all of them: CTA
+  // `rank` takes every C-th row.
+  template <int C>
+  __device__ __forceinline__ void exchange(float alpha) {
+    constexpr int kRounds = kM / C / kSmallWarps;
+    float4 v[kRounds][C];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int r = (warp + i * kSmallWarps) * C + rank;
+      if (r < depth && 4 * lane < depth)
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[i][c] = ld_cluster_v4(tc::map_to_rank(part + part_at(r, lane), c));
+    }
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int r = (warp + i * kSmallWarps) * C + rank;
+      if (r < depth && 4 * lane < depth) {
+        float4 sum = v[i][0];
+#pragma unroll
+        for (int c = 1; c < C; ++c)
+          sum = make_float4(sum.x + v[i][c].x, sum.y + v[i][c].y, sum.z + v[i][c].z, sum.w + v[i][c].w);
+        const uint32_t lo = half2_bits(sum.x * alpha, sum.y * alpha), hi = half2_bits(sum.z * alpha, sum.w * alpha);
+        const uint32_t at = s0 + (lane >> 4) * kChunk + chunk_at(r, (lane & 15) * 4);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          asm volatile("st.shared::cluster.v2.b32 [%0], {%1,%2};" ::"r"(tc::map_to_rank(at, c)), "r"(lo), "r"(hi));
+      }
+    }
+  }
+
   // s0 = X X^T summed over the cluster. Uses the space of s1 and s2.
   __device__ __forceinline__ void gram(int chunks) {
     const uint32_t xs = x, d = tmem;
+    const int columns = depth;
     multiply([=]() {
-      constexpr uint32_t idesc = tc::instr_desc(kM, kM, false, false, false);
+      const uint32_t idesc = tc::instr_desc(kM, columns, false, false, false);
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t o = tc::smem_desc(xs + c * kChunk + k * 32, false);
-          tc::mma_f16(d, o, o, idesc, c != 0 || k != 0);
-        }
+      for (int c = 0; c < 4 * chunks; ++c) {
+        const uint64_t o = tc::smem_desc(xs + (c >> 2) * kChunk + (c & 3) * 32, false);
+        tc::mma_f16(d, o, o, idesc, c != 0);
+      }
     });
     constexpr float alpha = kScaleA / (kScaleX * kScaleX);
-#pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-      const int col0 = half * 64 + j * 16;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int col0 = quarter * 32 + j * 16;
+      if (col0 >= depth) break;
       float v[16];
-      tc::tmem_ld16(tmem + (static_cast<uint32_t>(row & ~31) << 16) + col0, v);
+      tc::tmem_ld16(lanes() + col0, v);
       tc::tmem_ld_wait();
       if (ranks == 1) {
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = half2_bits(v[2 * i] * alpha, v[2 * i + 1] * alpha);
-        st_shared_v4(s0 + half * kChunk + chunk_at(row, j * 16), w[0], w[1], w[2], w[3]);
-        st_shared_v4(s0 + half * kChunk + chunk_at(row, j * 16 + 8), w[4], w[5], w[6], w[7]);
+        const uint32_t at = s0 + (quarter >> 1) * kChunk;
+        st_shared_v4(at + chunk_at(row, (quarter & 1) * 32 + j * 16), w[0], w[1], w[2], w[3]);
+        st_shared_v4(at + chunk_at(row, (quarter & 1) * 32 + j * 16 + 8), w[4], w[5], w[6], w[7]);
       } else {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -170,40 +211,26 @@ struct Small {
       }
     }
     if (ranks == 1) return;
+    __syncwarp();
     tc::cluster_sync();
-    const int rows = kM / ranks;  // 2, 4 or 8 ranks
-#pragma unroll 1
-    for (int i = threadIdx.x; i < rows * 32; i += kSmallThreads) {
-      const int r = rank * rows + (i >> 5), quad = i & 31;
-      float4 v[kMaxCluster];
-#pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c)
-        if (c < ranks) v[c] = ld_cluster_v4(tc::map_to_rank(part + part_at(r, quad), c));
-      float4 sum = v[0];
-#pragma unroll
-      for (int c = 1; c < kMaxCluster; ++c)
-        if (c < ranks) sum = make_float4(sum.x + v[c].x, sum.y + v[c].y, sum.z + v[c].z, sum.w + v[c].w);
-      const uint32_t lo = half2_bits(sum.x * alpha, sum.y * alpha), hi = half2_bits(sum.z * alpha, sum.w * alpha);
-      const uint32_t at = s0 + (quad >> 4) * kChunk + chunk_at(r, (quad & 15) * 4);
-#pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c)
-        if (c < ranks)
-          asm volatile("st.shared::cluster.v2.b32 [%0], {%1,%2};" ::"r"(tc::map_to_rank(at, c)), "r"(lo), "r"(hi));
-    }
+    if (ranks == 2) exchange<2>(alpha);
+    if (ranks == 4) exchange<4>(alpha);
+    if (ranks == 8) exchange<8>(alpha);
     tc::fence_async_proxy();
+    __syncwarp();
     tc::cluster_sync();
   }
 
   // tensor memory = sa X, all columns of the slice
   __device__ __forceinline__ void apply(uint32_t sa, int chunks) {
     const uint32_t xs = x, d = tmem;
+    const int steps = depth / 16;
     multiply([=]() {
 #pragma unroll 1
       for (int c = 0; c < chunks; c += 4) {
-        const int n = min(4, chunks - c) * 64;
-        const uint32_t idesc = tc::instr_desc(kM, n, false, false, true);
-#pragma unroll
-        for (int k = 0; k < kM / 16; ++k)
+        const uint32_t idesc = tc::instr_desc(kM, min(4, chunks - c) * 64, false, false, true);
+#pragma unroll 1
+        for (int k = 0; k < steps; ++k)
           tc::mma_f16(d + c * 64, tc::smem_desc(sa + (k >> 2) * kChunk + (k & 3) * 32, false),
                       tc::smem_desc(xs + c * kChunk + k * 2048, true, kChunk), idesc, k != 0);
       }
@@ -248,7 +275,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   k.warp = threadIdx.x >> 5;
   k.lane = threadIdx.x & 31;
   k.row = 32 * (k.warp & 3) + k.lane;
-  k.half = k.warp >> 2;
+  k.quarter = k.warp >> 2;
   k.rank = static_cast<int>(tc::cluster_rank());
   k.ranks = ranks;
   k.parity = 0;
@@ -273,6 +300,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const int rows = static_cast<int>(call.rows), cols = static_cast<int>(call.cols);
   const bool tall = rows > cols;
   const int m = tall ? cols : rows, n = tall ? rows : cols;
+  k.depth = (m + 15) & ~15;
   const int width = chunks * 64, n0 = k.rank * width;
   const int mine = max(0, min(width, n - n0));  // columns of X (rows of a tall matrix) held here
   // the matrix elements held here: `outer` rows of `inner` contiguous ones
@@ -280,25 +308,25 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const int64_t first = tall ? static_cast<int64_t>(n0) * it.ld : n0;
   const int64_t first_m = tall ? static_cast<int64_t>(n0) * cols : n0;  // momentum: rows of `cols`
 
-  // a warp takes 4 rows x 128 columns at a time, their 16 loads in flight together
+  // 128 rows x 32 columns at a time, a warp's 8 loads in flight together
   auto for_values = [&](auto visit) {
 #pragma unroll 1
-    for (int r0 = 4 * k.warp; r0 < outer; r0 += 4 * kSmallThreads / 32)
+    for (int r0 = k.warp; r0 < outer; r0 += 8 * kSmallWarps)
 #pragma unroll 1
-      for (int c0 = k.lane; c0 < inner; c0 += 128) {
-        float g[16], mom[16];
+      for (int c = k.lane; c < inner; c += 32) {
+        float g[8], mom[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int r = r0 + (j >> 2), c = c0 + 32 * (j & 3);
-          if (r < outer && c < inner) {
+        for (int j = 0; j < 8; ++j) {
+          const int r = r0 + j * kSmallWarps;
+          if (r < outer) {
             g[j] = load_value<F32>(it.g, first + r * it.ld + c);
             if (MOM) mom[j] = it.mom[first_m + static_cast<int64_t>(r) * cols + c];
           }
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int r = r0 + (j >> 2), c = c0 + 32 * (j & 3);
-          if (r < outer && c < inner) visit(r, c, g[j], mom[j]);
+        for (int j = 0; j < 8; ++j) {
+          const int r = r0 + j * kSmallWarps;
+          if (r < outer) visit(r, c, g[j], mom[j]);
         }
       }
   };
@@ -315,26 +343,28 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
-  __shared__ float warp_sum[kSmallThreads / 32];
+  __shared__ float warp_sum[kSmallWarps];
   __shared__ float shared_inv;
   if (k.lane == 0) warp_sum[k.warp] = sum;
   // rows and columns beyond the matrix are zero
   for (int i = threadIdx.x; i < chunks * kChunk / 16; i += kSmallThreads) st_shared_v4(k.x + 16 * i, 0, 0, 0, 0);
   __syncthreads();
   if (threadIdx.x < ranks) {
-    double x = 0.0;
-    for (int i = 0; i < kSmallThreads / 32; ++i) x += static_cast<double>(warp_sum[i]);
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(tc::map_to_rank(sums + 8 * k.rank, threadIdx.x)), "d"(x) : "memory");
+    float x = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kSmallWarps; ++i) x += warp_sum[i];
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::map_to_rank(sums + 4 * k.rank, threadIdx.x)), "f"(x));
   }
+  __syncwarp();
   tc::cluster_sync();
   if (threadIdx.x == 0) {
-    double x = 0.0;
+    float x = 0.0f;
     for (int i = 0; i < ranks; ++i) {
-      double y;
-      asm volatile("ld.shared.f64 %0, [%1];" : "=d"(y) : "r"(sums + 8 * i) : "memory");
+      float y;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(sums + 4 * i));
       x += y;
     }
-    shared_inv = static_cast<float>(static_cast<double>(kScaleX) / (sqrt(x) + static_cast<double>(call.s.eps)));
+    shared_inv = kScaleX / (sqrtf(x) + call.s.eps);
   }
   __syncthreads();
   const float inv = shared_inv;
@@ -370,14 +400,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     const bool final = done >= call.steps;
     const float back = final ? 1.0f / (scale * kScaleX) : 1.0f / scale;
 #pragma unroll 1
-    for (int c = k.half; c < 4 * chunks; c += 2) {  // 16 columns at a time
+    for (int c = k.quarter; c < 4 * chunks; c += 4) {  // 16 columns at a time
       float v[16];
       __syncwarp();
-      tc::tmem_ld16(k.tmem + (static_cast<uint32_t>(k.row & ~31) << 16) + 16 * c, v);
+      tc::tmem_ld16(k.lanes() + 16 * c, v);
       tc::tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] *= back;
       if (!final) {
+        if (k.row >= k.depth) continue;  // X stays zero there
         const uint32_t at = k.x + (c >> 2) * kChunk;
         st_shared_v4(at + chunk_at(k.row, (c & 3) * 16), half2_bits(v[0], v[1]), half2_bits(v[2], v[3]),
                      half2_bits(v[4], v[5]), half2_bits(v[6], v[7]));
