@@ -116,88 +116,86 @@ __device__ __forceinline__ float unpack16(uint16_t u, bool bf16) {
   return bf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u));
 }
 
-// 32 consecutive 16-bit values of one row, `left` of them inside the matrix.
-__device__ __forceinline__ void store_row32(uint16_t* p, const uint32_t (&w)[16], int left, int vec) {
-  if (left >= 32 && vec >= 16) {
-    if (vec >= 32) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p + 16 * i), "r"(w[8 * i]),
-                     "r"(w[8 * i + 1]), "r"(w[8 * i + 2]), "r"(w[8 * i + 3]), "r"(w[8 * i + 4]), "r"(w[8 * i + 5]),
-                     "r"(w[8 * i + 6]), "r"(w[8 * i + 7])
-                     : "memory");
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    }
+// Epilogues go through a row 16 columns at a time in loops that are not unrolled:
+// a launch of few tiles runs this code once, and fetching long unrolled code took
+// longer (4 us for a 256 x 128 tile) than running it. What a group reads from
+// memory is fetched one group ahead.
+
+// 16 consecutive 16-bit values of one row, `left` of them inside the matrix.
+__device__ __forceinline__ void store_row16(uint16_t* p, const uint32_t (&w)[8], int left, int vec) {
+  if (left >= 16 && vec >= 32) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else if (left >= 16 && vec >= 16) {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < 16; ++i)
       if (i < left) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+__device__ __forceinline__ void load_row16(const uint16_t* p, uint32_t (&w)[8], int left, int vec) {
+  if (left >= 16 && vec >= 16) {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = (2 * i < left ? p[2 * i] : 0u) | ((2 * i + 1 < left ? static_cast<uint32_t>(p[2 * i + 1]) : 0u) << 16);
   }
 }
 
 struct StoreEpilogue {
   using Params = StoreParams;
-  static __device__ __forceinline__ void begin(const Params&) {}
   using Table = Nothing;
-  static __device__ __forceinline__ void store(const Params& e, const Shape& s, const Tile& t, uint16_t* out,
-                                               const uint16_t* c, bool bf16, bool mirror, int row, int col,
-                                               float (&v)[32]) {
-    const int left = s.n - col;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = v[i] * e.alpha;
-    if (c) {
-      const uint16_t* q = c + static_cast<int64_t>(row) * e.ld + col;
-      if (left >= 32 && e.vec >= 16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 u = *reinterpret_cast<const uint4*>(q + 8 * j);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            v[8 * j + i] = __fmaf_rn(e.beta, unpack16(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))), bf16), v[8 * j + i]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i < left) v[i] = __fmaf_rn(e.beta, unpack16(q[i], bf16), v[i]);
-      }
-    }
-    if (e.diag != 0.0f) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col + i == row) v[i] += e.diag;
-    }
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack16(v[2 * i], v[2 * i + 1], bf16);
-    store_row32(out + static_cast<int64_t>(row) * e.ld + col, w, left, e.vec);
-    if (mirror) {
-      uint16_t* q = out + static_cast<int64_t>(col) * e.ld + row;
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < left) q[static_cast<int64_t>(i) * e.ld] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-    }
-  }
+  static __device__ __forceinline__ void begin(const Params&) {}
   template <int kCols, class Release>
-  static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
+  static __device__ __forceinline__ void run(const Params& e, const Table&, const Shape& s, const Tile& t, int row,
                                              int col0, uint32_t tmem, Release release) {
-    const bool bf16 = e.bf16 != 0;
+    const bool bf16 = e.bf16 != 0, inside = row < s.m;
     constexpr int kAcross = kGemmTile / (2 * kCols);  // tiles of a diagonal block are formed whole
     const bool mirror = s.symmetric && t.tn >= kAcross * (t.tm + 1);
-    uint16_t* const out = static_cast<uint16_t*>(e.out) + t.batch * e.batch_stride;
-    const uint16_t* const c = e.c ? static_cast<const uint16_t*>(e.c) + t.batch * e.batch_stride : nullptr;
+    const int64_t at = t.batch * e.batch_stride + static_cast<int64_t>(row) * e.ld + col0;
+    uint16_t* out = static_cast<uint16_t*>(e.out) + at;
+    uint16_t* across = static_cast<uint16_t*>(e.out) + t.batch * e.batch_stride + static_cast<int64_t>(col0) * e.ld + row;
+    const uint16_t* c = e.c && inside ? static_cast<const uint16_t*>(e.c) + at : nullptr;
+    uint32_t next[8];
+    if (c) load_row16(c, next, s.n - col0, e.vec);
 #pragma unroll 1
-    for (int chunk = 0; chunk < kCols / 32; ++chunk) {
-      const int col = col0 + 32 * chunk;
-      if (col >= s.n) break;
-      float v[32];
+    for (int g = 0; g < kCols / 16; ++g) {
+      const int left = s.n - col0 - 16 * g;
+      if (left <= 0) break;
+      float v[16];
       __syncwarp();
-      tc::tmem_ld32(tmem + 32 * chunk, v);
+      tc::tmem_ld16(tmem + 16 * g, v);
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = next[i];
+      if (c && left > 16 && g + 1 < kCols / 16) load_row16(c + 16 * (g + 1), next, left - 16, e.vec);
       tc::tmem_ld_wait();
-      if (row < s.m) store(e, s, t, out, c, bf16, mirror, row, col, v);
+      if (!inside) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = v[i] * e.alpha;
+      if (c) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          v[i] = __fmaf_rn(e.beta, unpack16(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))), bf16), v[i]);
+      }
+      const int diag = row - col0 - 16 * g;
+      if (e.diag != 0.0f && diag >= 0 && diag < 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += i == diag ? e.diag : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack16(v[2 * i], v[2 * i + 1], bf16);
+      store_row16(out + 16 * g, w, left, e.vec);
+      if (mirror) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < left) across[static_cast<int64_t>(16 * g + i) * e.ld] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+      }
     }
     __syncwarp();
     release();
@@ -207,78 +205,70 @@ struct StoreEpilogue {
 // The Muon update of the weights by a tile of the orthogonalised matrix.
 struct UpdateEpilogue {
   using Params = UpdateParams;
-  static __device__ __forceinline__ void begin(const Params&) {}
   using Table = UpdateTable;
-  static __device__ __forceinline__ void store(const Params& e, float step, void* w, uint16_t* w16, int left,
-                                               const float (&v)[32]) {
-    float x[32];
-    const bool wide = left >= 32 && e.vec >= 16;
-    if (e.format == LST_L12_BF16) {
-      const uint16_t* p = static_cast<const uint16_t*>(w);
-      if (wide) {
+  static __device__ __forceinline__ void begin(const Params&) {}
+  // 16 weights of a row, as 8 words of bf16 pairs or 16 of fp32
+  static __device__ __forceinline__ void load(const char* w, bool bf16, uint32_t (&x)[16], int left, int vec) {
+    if (bf16) {
+      uint32_t h[8];
+      load_row16(reinterpret_cast<const uint16_t*>(w), h, left, vec);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint4 u = reinterpret_cast<const uint4*>(p)[j];
-          const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+      for (int i = 0; i < 8; ++i) x[i] = h[i];
+    } else if (left >= 16 && vec >= 16) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[8 * j + i] = unpack16(static_cast<uint16_t>(q[i >> 1] >> (16 * (i & 1))), true);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = i < left ? unpack16(p[i], true) : 0.0f;
+      for (int i = 0; i < 4; ++i) {
+        const uint4 u = reinterpret_cast<const uint4*>(w)[i];
+        x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
       }
     } else {
-      const float* p = static_cast<const float*>(w);
-      if (wide) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 u = reinterpret_cast<const float4*>(p)[j];
-          x[4 * j] = u.x, x[4 * j + 1] = u.y, x[4 * j + 2] = u.z, x[4 * j + 3] = u.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = i < left ? p[i] : 0.0f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = __fsub_rn(__fmul_rn(x[i], e.decay), __fmul_rn(step, v[i]));
-    if (e.format != LST_L12_BF16) {
-      float* p = static_cast<float*>(w);
-      if (wide) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          reinterpret_cast<float4*>(p)[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i < left) p[i] = x[i];
-      }
-    }
-    if (e.format != LST_L16_FP32) {
-      uint32_t q[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) q[i] = pack16(x[2 * i], x[2 * i + 1], true);
-      store_row32(e.format == LST_L12_BF16 ? static_cast<uint16_t*>(w) : w16, q, left, e.vec);
+      for (int i = 0; i < 16; ++i) x[i] = i < left ? reinterpret_cast<const uint32_t*>(w)[i] : 0u;
     }
   }
   template <int kCols, class Release>
   static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
                                              int col0, uint32_t tmem, Release release) {
-    char* const w = static_cast<char*>(table.w[e.first + t.batch]);
-    uint16_t* const w16 = table.w16[e.first + t.batch];
+    const bool bf16 = e.format == LST_L12_BF16, inside = row < s.m && col0 < s.n;
+    const int size = bf16 ? 2 : 4;
     const float step = table.step[e.first + t.batch];
-    const int size = e.format == LST_L12_BF16 ? 2 : 4;
+    const int64_t at = static_cast<int64_t>(row) * e.ld + col0;
+    char* w = static_cast<char*>(table.w[e.first + t.batch]) + at * size;
+    uint16_t* w16 = bf16 ? reinterpret_cast<uint16_t*>(w) : table.w16[e.first + t.batch] + at;
+    uint32_t next[16];
+    if (inside) load(w, bf16, next, s.n - col0, e.vec);
 #pragma unroll 1
-    for (int chunk = 0; chunk < kCols / 32; ++chunk) {
-      const int col = col0 + 32 * chunk;
-      if (col >= s.n) break;
-      float v[32];
+    for (int g = 0; g < kCols / 16; ++g) {
+      const int left = s.n - col0 - 16 * g;
+      if (left <= 0) break;
+      float v[16];
       __syncwarp();
-      tc::tmem_ld32(tmem + 32 * chunk, v);
+      tc::tmem_ld16(tmem + 16 * g, v);
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        x[i] = bf16 ? unpack16(static_cast<uint16_t>(next[i >> 1] >> (16 * (i & 1))), true) : __uint_as_float(next[i]);
+      if (inside && left > 16 && g + 1 < kCols / 16) load(w + 16 * (g + 1) * size, bf16, next, left - 16, e.vec);
       tc::tmem_ld_wait();
-      if (row < s.m) {
-        const int64_t i = static_cast<int64_t>(row) * e.ld + col;
-        store(e, step, w + i * size, w16 ? w16 + i : nullptr, s.n - col, v);
+      if (!inside) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __fsub_rn(__fmul_rn(x[i], e.decay), __fmul_rn(step, v[i]));
+      if (!bf16) {
+        float* p = reinterpret_cast<float*>(w) + 16 * g;
+        if (left >= 16 && e.vec >= 16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (i < left) p[i] = x[i];
+        }
+      }
+      if (e.format != LST_L16_FP32) {
+        uint32_t q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = pack16(x[2 * i], x[2 * i + 1], true);
+        store_row16(w16 + 16 * g, q, left, e.vec);
       }
     }
     __syncwarp();
@@ -290,21 +280,21 @@ struct PartialEpilogue {
   using Params = PartialParams;
   using Table = Nothing;
   template <int kCols, class Release>
-  static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
+  static __device__ __forceinline__ void run(const Params& e, const Table&, const Shape& s, const Tile& t, int row,
                                              int col0, uint32_t tmem, Release release) {
-    float* const out = e.out + t.split * e.split_stride + static_cast<int64_t>(row) * e.ld;
+    float* const out = e.out + t.split * e.split_stride + static_cast<int64_t>(row) * e.ld + col0;
 #pragma unroll 1
-    for (int chunk = 0; chunk < kCols / 32; ++chunk) {
-      const int col = col0 + 32 * chunk;
-      if (col >= s.n) break;
-      float v[32];
-      tc::tmem_ld32(tmem + 32 * chunk, v);
+    for (int g = 0; g < kCols / 16; ++g) {
+      if (col0 + 16 * g >= s.n) break;
+      float v[16];
+      __syncwarp();
+      tc::tmem_ld16(tmem + 16 * g, v);
       tc::tmem_ld_wait();
       if (row < s.m) {
         // ld is a multiple of 32, so a row's tail may be written past column n
-  #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float4* p = reinterpret_cast<float4*>(out + col) + j;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float4* p = reinterpret_cast<float4*>(out + 16 * g) + j;
           float4 x = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           if (e.accumulate) {
             const float4 y = *p;
@@ -313,8 +303,8 @@ struct PartialEpilogue {
           *p = x;
         }
       }
-      __syncwarp();
     }
+    __syncwarp();
     release();
   }
 };
@@ -396,15 +386,15 @@ struct XentEpilogue {
     if (e.q && inside) {
       uint16_t* const out = e.q + static_cast<int64_t>(row) * e.q_ld + col0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t w[16];
+      for (int j = 0; j < 8; ++j) {
+        uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float lo = fminf((top - v[32 * j + 2 * i]) * 2048.0f, 65535.0f);
-          const float hi = fminf((top - v[32 * j + 2 * i + 1]) * 2048.0f, 65535.0f);
+        for (int i = 0; i < 8; ++i) {
+          const float lo = fminf((top - v[16 * j + 2 * i]) * 2048.0f, 65535.0f);
+          const float hi = fminf((top - v[16 * j + 2 * i + 1]) * 2048.0f, 65535.0f);
           w[i] = __float2uint_rn(lo) | (__float2uint_rn(hi) << 16);
         }
-        store_row32(out + 32 * j, w, 32, 32);  // q_ld is a multiple of 128
+        store_row16(out + 16 * j, w, 16, 32);  // q_ld is a multiple of 128
       }
     }
   }
@@ -421,7 +411,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t bars = base + kStages * kStageBytes;
   const uint32_t full = bars, empty = bars + 8 * kStages, tfull = bars + 16 * kStages, tempty = tfull + 16;
   const uint32_t tmem_slot = tempty + 16;
-  const uint32_t abort_slot = tmem_slot + 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_rank();
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
@@ -437,7 +426,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_init(tfull + 8 * i, 1);
       tc::mbar_init(tempty + 8 * i, 2 * kEpiWarps);
     }
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort_slot), "r"(0) : "memory");
     tc::mbar_init_fence();
   }
   if (warp == 1) {
@@ -450,6 +438,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::fence_after();
   uint32_t tmem;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
+  // while the launch before runs on: the first tile's parameters and tensor maps,
+  // whose first reads take about 0.5 us
+  const Tile first = decode<kTileN>(g, cluster);
+  if (warp == 0 && lane == 0) {
+    tc::prefetch_map(&g.a[first.problem]);
+    tc::prefetch_map(&g.b[first.problem]);
+  }
+  const int32_t* words = reinterpret_cast<const int32_t*>(&g.epi[first.problem]);
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(typename Epi::Params) / 4); i += 8) asm volatile("" ::"r"(words[i]));
   wait_for_previous();
   Epi::begin(g.epi[0]);
 
@@ -459,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       for (int t = cluster; t < g.total_tiles && ok; t += clusters) {
-        const Tile tile = decode<kTileN>(g, t);
+        const Tile tile = t == cluster ? first : decode<kTileN>(g, t);
         const CUtensorMap* ma = &g.a[tile.problem];
         const CUtensorMap* mb = &g.b[tile.problem];
         const int m0 = tile.tm * kGemmTile + 128 * static_cast<int>(rank);
@@ -495,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int stage = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
       for (int t = cluster; t < g.total_tiles && ok; t += clusters) {
-        const Tile tile = decode<kTileN>(g, t);
+        const Tile tile = t == cluster ? first : decode<kTileN>(g, t);
         ok = tc::mbar_wait(tempty + 8 * buf, tphase ^ 1);
         if (!ok) break;
         tc::fence_after();
@@ -530,7 +528,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int buf = 0;
     uint32_t tphase = 0;
     for (int t = cluster; t < g.total_tiles; t += clusters) {
-      const Tile tile = decode<kTileN>(g, t);
+      const Tile tile = t == cluster ? first : decode<kTileN>(g, t);
       ok = __all_sync(0xffffffffu, tc::mbar_wait(tfull + 8 * buf, tphase));
       if (!ok) break;
       tc::fence_after();
@@ -541,22 +539,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Epi::template run<kTileN / 2>(g.epi[tile.problem], g.table, g.shape[tile.problem], tile, row, col0, addr, [&]() {
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(bar, 0));
+        if (lane == 0) tc::mbar_arrive_cluster_relaxed(tc::map_to_rank(bar, 0));
       });
       buf ^= 1;
       if (buf == 0) tphase ^= 1;
     }
   }
   if (!ok) {
+    // a wait ran out: loads and MMAs in flight get time to land before the CTA ends
     atomicExch(&g_gemm_error, 1);
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort_slot), "r"(1) : "memory");
-  }
-  __syncthreads();
-  uint32_t aborted;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(aborted) : "r"(abort_slot));
-  // after a wait that ran out, give loads and MMAs in flight time to land
-  if (aborted)
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  }
   tc::fence_before();
   __syncthreads();
   tc::cluster_sync();
