@@ -34,7 +34,10 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kBarriers = 2 * kStages + 4;
 __host__ __device__ constexpr int b_bytes(int tile_n) { return tile_n / 2 * kTileK * 2; }  // one CTA's half of B
-__host__ __device__ constexpr int smem_bytes(int tile_n) { return kStages * (kABytes + b_bytes(tile_n)) + 1024 + 8 * kBarriers + 16; }
+constexpr int kTurnBytes = 32 * 33 * 4;  // a warp's 32 x 32 values on their way from rows to columns
+__host__ __device__ constexpr int smem_bytes(int tile_n) {
+  return kStages * (kABytes + b_bytes(tile_n)) + 1024 + 8 * kBarriers + 16 + kEpiWarps * kTurnBytes;
+}
 
 __device__ int g_gemm_error;
 
@@ -101,7 +104,7 @@ __device__ __forceinline__ Tile decode(const Args<Epi>& g, int t) {
 
 // ---- epilogues ---------------------------------------------------------------
 // Each warp calls run() with its accumulator address (32 lanes = 32 rows, kCols
-// = half a tile's columns); `release` must be called once, by all lanes, when the accumulator
+// = half a tile's columns); prepare() runs before the tile is complete. `release` must be called once, by all lanes, when the accumulator
 // has been read.
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
@@ -120,6 +123,21 @@ __device__ __forceinline__ float unpack16(uint16_t u, bool bf16) {
 // a launch of few tiles runs this code once, and fetching long unrolled code took
 // longer (4 us for a 256 x 128 tile) than running it. What a group reads from
 // memory is fetched one group ahead.
+
+// 32 accumulator columns with the lanes turned from rows to columns, through the
+// warp's words at `turn`: v[i] becomes row i of the lane's column. What is then
+// read and written is consecutive over the lanes.
+__device__ __forceinline__ void load_turned(uint32_t tmem, uint32_t turn, float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  tc::tmem_ld32(tmem, v);
+  tc::tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("st.shared.f32 [%0], %1;" ::"r"(turn + (lane * 33 + i) * 4), "f"(v[i]));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(turn + (i * 33 + lane) * 4));
+}
 
 // 16 consecutive 16-bit values of one row, `left` of them inside the matrix.
 __device__ __forceinline__ void store_row16(uint16_t* p, const uint32_t (&w)[8], int left, int vec) {
@@ -148,12 +166,50 @@ __device__ __forceinline__ void load_row16(const uint16_t* p, uint32_t (&w)[8], 
 }
 
 struct StoreEpilogue {
+  template <int kCols, class... Rest>
+  static __device__ __forceinline__ void prepare(const Rest&...) {}
   using Params = StoreParams;
   using Table = Nothing;
   static __device__ __forceinline__ void begin(const Params&) {}
+  // Rows that are not on 16 bytes (a caller's matrix: not symmetric, no diagonal).
+  template <int kCols>
+  static __device__ __forceinline__ void turned(const Params& e, const Shape& s, const Tile& t, int row, int col0, uint32_t tmem,
+                                                uint32_t turn) {
+    const bool bf16 = e.bf16 != 0;
+    const int row0 = row & ~31, lane = row & 31, rows = s.m - row0;
+    const int64_t first = t.batch * e.batch_stride + static_cast<int64_t>(row0) * e.ld + col0 + lane;
+#pragma unroll 1
+    for (int g = 0; g < kCols / 32; ++g) {
+      if (col0 + 32 * g >= s.n) break;
+      const bool inside = col0 + 32 * g + lane < s.n;
+      const int64_t at = first + 32 * g;
+      uint16_t old[32];
+      if (e.c) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (inside && i < rows) old[i] = static_cast<const uint16_t*>(e.c)[at + i * e.ld];
+      }
+      float v[32];
+      load_turned(tmem + 32 * g, turn, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (inside && i < rows) {
+          float y = v[i] * e.alpha;
+          if (e.c) y = __fmaf_rn(e.beta, unpack16(old[i], bf16), y);
+          static_cast<uint16_t*>(e.out)[at + i * e.ld] = static_cast<uint16_t>(pack16(y, 0.0f, bf16));
+        }
+      }
+    }
+  }
   template <int kCols, class Release>
   static __device__ __forceinline__ void run(const Params& e, const Table&, const Shape& s, const Tile& t, int row,
-                                             int col0, uint32_t tmem, Release release) {
+                                             int col0, uint32_t tmem, uint32_t turn, Release release) {
+    if (e.vec < 16) {
+      turned<kCols>(e, s, t, row, col0, tmem, turn);
+      __syncwarp();
+      release();
+      return;
+    }
     const bool bf16 = e.bf16 != 0, inside = row < s.m;
     constexpr int kAcross = kGemmTile / (2 * kCols);  // tiles of a diagonal block are formed whole
     const bool mirror = s.symmetric && t.tn >= kAcross * (t.tm + 1);
@@ -207,68 +263,106 @@ struct UpdateEpilogue {
   using Params = UpdateParams;
   using Table = UpdateTable;
   static __device__ __forceinline__ void begin(const Params&) {}
-  // 16 weights of a row, as 8 words of bf16 pairs or 16 of fp32
-  static __device__ __forceinline__ void load(const char* w, bool bf16, uint32_t (&x)[16], int left, int vec) {
-    if (bf16) {
-      uint32_t h[8];
-      load_row16(reinterpret_cast<const uint16_t*>(w), h, left, vec);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = h[i];
-    } else if (left >= 16 && vec >= 16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 u = reinterpret_cast<const uint4*>(w)[i];
-        x[4 * i] = u.x, x[4 * i + 1] = u.y, x[4 * i + 2] = u.z, x[4 * i + 3] = u.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = i < left ? reinterpret_cast<const uint32_t*>(w)[i] : 0u;
-    }
+  // The tile's weights to L2 while its main loop runs, a row's columns in one request.
+  template <int kCols>
+  static __device__ __forceinline__ void prepare(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
+                                                 int col0) {
+    if (row >= s.m || col0 >= s.n || e.vec < 16) return;
+    const int size = e.format == LST_L12_BF16 ? 2 : 4, bytes = (min(kCols, s.n - col0) * size) & ~15;
+    const char* w = static_cast<const char*>(table.w[e.first + t.batch]) + (static_cast<int64_t>(row) * e.ld + col0) * size;
+    if (bytes > 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(w), "r"(bytes) : "memory");
   }
-  template <int kCols, class Release>
-  static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
-                                             int col0, uint32_t tmem, Release release) {
-    const bool bf16 = e.format == LST_L12_BF16, inside = row < s.m && col0 < s.n;
-    const int size = bf16 ? 2 : 4;
-    const float step = table.step[e.first + t.batch];
-    const int64_t at = static_cast<int64_t>(row) * e.ld + col0;
-    char* w = static_cast<char*>(table.w[e.first + t.batch]) + at * size;
-    uint16_t* w16 = bf16 ? reinterpret_cast<uint16_t*>(w) : table.w16[e.first + t.batch] + at;
-    uint32_t next[16];
-    if (inside) load(w, bf16, next, s.n - col0, e.vec);
+  // Either a row of fp32 weights per lane, 64 bytes at a time, or the lanes along
+  // the columns. The last product of a TinyLlama layer by the two, at 97 us of
+  // MMA: mixed layout 181 and 205 us, fp32 157 and 182, 12 B layout 305 and 183
+  // (32 bytes of each of 32 rows do not get through L1 in time). So bf16 weights
+  // and rows that are not on 16 bytes take the second way.
+  template <int kCols>
+  static __device__ __forceinline__ void rows(const Params& e, float step, float* w, uint16_t* w16, bool inside, int columns,
+                                              uint32_t tmem) {
+    float4 next[4];
+    if (inside)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * i < columns) next[i] = reinterpret_cast<const float4*>(w)[i];
 #pragma unroll 1
-    for (int g = 0; g < kCols / 16; ++g) {
-      const int left = s.n - col0 - 16 * g;
-      if (left <= 0) break;
-      float v[16];
+    for (int g = 0; g < kCols / 16; ++g, w += 16, w16 += 16, columns -= 16) {
+      if (columns <= 0) break;
+      float v[16], x[16];
       __syncwarp();
       tc::tmem_ld16(tmem + 16 * g, v);
-      float x[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        x[i] = bf16 ? unpack16(static_cast<uint16_t>(next[i >> 1] >> (16 * (i & 1))), true) : __uint_as_float(next[i]);
-      if (inside && left > 16 && g + 1 < kCols / 16) load(w + 16 * (g + 1) * size, bf16, next, left - 16, e.vec);
+      for (int i = 0; i < 4; ++i) x[4 * i] = next[i].x, x[4 * i + 1] = next[i].y, x[4 * i + 2] = next[i].z, x[4 * i + 3] = next[i].w;
+      if (inside && g + 1 < kCols / 16)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (16 + 4 * i < columns) next[i] = reinterpret_cast<const float4*>(w + 16)[i];
       tc::tmem_ld_wait();
       if (!inside) continue;
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = __fsub_rn(__fmul_rn(x[i], e.decay), __fmul_rn(step, v[i]));
-      if (!bf16) {
-        float* p = reinterpret_cast<float*>(w) + 16 * g;
-        if (left >= 16 && e.vec >= 16) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        } else {
+      for (int i = 0; i < 4; ++i)
+        if (4 * i < columns) reinterpret_cast<float4*>(w)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      if (e.format == LST_L16_MIXED) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (i < left) p[i] = x[i];
-        }
+        for (int i = 0; i < 2; ++i)  // a row's columns are a multiple of 8
+          if (8 * i < columns)
+            reinterpret_cast<uint4*>(w16)[i] = make_uint4(pack16(x[8 * i], x[8 * i + 1], true), pack16(x[8 * i + 2], x[8 * i + 3], true),
+                                                          pack16(x[8 * i + 4], x[8 * i + 5], true), pack16(x[8 * i + 6], x[8 * i + 7], true));
       }
-      if (e.format != LST_L16_FP32) {
-        uint32_t q[8];
+    }
+  }
+  template <int kCols, class Release>
+  static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
+                                             int col0, uint32_t tmem, uint32_t turn, Release release) {
+    const bool bf16 = e.format == LST_L12_BF16;
+    const float step = table.step[e.first + t.batch];
+    const int row0 = row & ~31, lane = row & 31, rows = s.m - row0;
+    const int64_t first = static_cast<int64_t>(row0) * e.ld + col0 + lane;
+    char* const weights = static_cast<char*>(table.w[e.first + t.batch]);
+    uint16_t* const w16 = bf16 ? reinterpret_cast<uint16_t*>(weights) : table.w16[e.first + t.batch];
+    if (!bf16 && e.vec >= 16) {
+      const int64_t at = static_cast<int64_t>(row) * e.ld + col0;
+      UpdateEpilogue::rows<kCols>(e, step, reinterpret_cast<float*>(weights) + at, w16 + at, row < s.m, s.n - col0, tmem);
+      __syncwarp();
+      release();
+      return;
+    }
+    float next[32];
+    auto fetch = [&](int g) {
+      const int64_t at = first + 32 * g;
+      const bool inside = col0 + 32 * g + lane < s.n;
+      if (bf16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = pack16(x[2 * i], x[2 * i + 1], true);
-        store_row16(w16 + 16 * g, q, left, e.vec);
+        for (int i = 0; i < 32; ++i)
+          if (inside && i < rows) next[i] = __uint_as_float(__ldcg(reinterpret_cast<const uint16_t*>(weights) + at + i * e.ld));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (inside && i < rows) next[i] = __ldcg(reinterpret_cast<const float*>(weights) + at + i * e.ld);
+      }
+    };
+    fetch(0);
+#pragma unroll 1
+    for (int g = 0; g < kCols / 32; ++g) {
+      if (col0 + 32 * g >= s.n) break;
+      const bool inside = col0 + 32 * g + lane < s.n;
+      const int64_t at = first + 32 * g;
+      float v[32], x[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = next[i];
+      if (g + 1 < kCols / 32) fetch(g + 1);
+      load_turned(tmem + 32 * g, turn, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (inside && i < rows) {
+          if (bf16) x[i] = unpack16(static_cast<uint16_t>(__float_as_uint(x[i])), true);
+          const float y = __fsub_rn(__fmul_rn(x[i], e.decay), __fmul_rn(step, v[i]));
+          if (!bf16) reinterpret_cast<float*>(weights)[at + i * e.ld] = y;
+          if (e.format != LST_L16_FP32)
+            reinterpret_cast<__nv_bfloat16*>(w16)[at + i * e.ld] = __float2bfloat16_rn(y);
+        }
       }
     }
     __syncwarp();
@@ -281,7 +375,7 @@ struct PartialEpilogue {
   using Table = Nothing;
   template <int kCols, class Release>
   static __device__ __forceinline__ void run(const Params& e, const Table&, const Shape& s, const Tile& t, int row,
-                                             int col0, uint32_t tmem, Release release) {
+                                             int col0, uint32_t tmem, uint32_t turn, Release release) {
     float* const out = e.out + t.split * e.split_stride + static_cast<int64_t>(row) * e.ld + col0;
 #pragma unroll 1
     for (int g = 0; g < kCols / 16; ++g) {
@@ -314,16 +408,18 @@ struct GradParams {
   PartialParams partial;
 };
 struct GradEpilogue {
+  template <int kCols, class... Rest>
+  static __device__ __forceinline__ void prepare(const Rest&...) {}
   using Params = GradParams;
   static __device__ __forceinline__ void begin(const Params&) {}
   using Table = Nothing;
   template <int kCols, class Release>
   static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
-                                             int col0, uint32_t tmem, Release release) {
+                                             int col0, uint32_t tmem, uint32_t turn, Release release) {
     if (e.partial.out)
-      PartialEpilogue::run<kCols>(e.partial, table, s, t, row, col0, tmem, release);
+      PartialEpilogue::run<kCols>(e.partial, table, s, t, row, col0, tmem, turn, release);
     else
-      StoreEpilogue::run<kCols>(e.store, table, s, t, row, col0, tmem, release);
+      StoreEpilogue::run<kCols>(e.store, table, s, t, row, col0, tmem, turn, release);
   }
 };
 
@@ -334,6 +430,8 @@ struct GradEpilogue {
 // 2^-5; an entry further below (a probability under 1e-14 of its group's
 // largest) saturates.
 struct XentEpilogue {
+  template <int kCols, class... Rest>
+  static __device__ __forceinline__ void prepare(const Rest&...) {}
   using Params = XentParams;
   using Table = Nothing;
   static __device__ __forceinline__ void begin(const Params& e) {
@@ -341,7 +439,7 @@ struct XentEpilogue {
   }
   template <int kCols, class Release>
   static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
-                                             int col0, uint32_t tmem, Release release) {
+                                             int col0, uint32_t tmem, uint32_t turn, Release release) {
     static_assert(kCols == 128, "statistics are per 128 columns");
     if (col0 >= s.n) {
       release();
@@ -529,14 +627,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t tphase = 0;
     for (int t = cluster; t < g.total_tiles; t += clusters) {
       const Tile tile = t == cluster ? first : decode<kTileN>(g, t);
+      const int row = tile.tm * kGemmTile + 128 * static_cast<int>(rank) + 32 * quad + lane;
+      const int col0 = tile.tn * kTileN + kTileN / 2 * half;
+      Epi::template prepare<kTileN / 2>(g.epi[tile.problem], g.table, g.shape[tile.problem], tile, row, col0);
       ok = __all_sync(0xffffffffu, tc::mbar_wait(tfull + 8 * buf, tphase));
       if (!ok) break;
       tc::fence_after();
-      const int row = tile.tm * kGemmTile + 128 * static_cast<int>(rank) + 32 * quad + lane;
-      const int col0 = tile.tn * kTileN + kTileN / 2 * half;
       const uint32_t addr = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kTileN * buf + kTileN / 2 * half;
       const uint32_t bar = tempty + 8 * buf;
-      Epi::template run<kTileN / 2>(g.epi[tile.problem], g.table, g.shape[tile.problem], tile, row, col0, addr, [&]() {
+      const uint32_t turn = tmem_slot + 16 + (warp - 2) * kTurnBytes;
+      Epi::template run<kTileN / 2>(g.epi[tile.problem], g.table, g.shape[tile.problem], tile, row, col0, addr, turn, [&]() {
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_cluster_relaxed(tc::map_to_rank(bar, 0));
