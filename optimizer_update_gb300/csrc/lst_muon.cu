@@ -42,7 +42,7 @@ namespace lst {
 namespace {
 
 constexpr int kItemsPerLaunch = 32;
-constexpr int kNormBlocks = 512;   // partial sums per matrix
+constexpr int kNormBlocks = 1024;  // partial sums per matrix
 // Inputs of the matrices whose norms are taken together: their second read, to
 // scale them, then comes from L2 (129 MB) for the most part.
 constexpr int64_t kIngestBytes = int64_t(64) << 20;
@@ -52,7 +52,7 @@ struct Item {
   const void* g;      // gradient, or the matrix itself
   float* mom;         // momentum, or null
   __half* x;          // rows x ldx values
-  double* part;       // kNormBlocks partial sums of squares
+  float* part;        // kNormBlocks partial sums of squares
   int64_t rows, cols, ld, ldx;
 };
 struct ItemTable {
@@ -82,10 +82,17 @@ __device__ __forceinline__ bool vector_rows(const Item& it) {
          (!MOM || (reinterpret_cast<uintptr_t>(it.mom) & 15) == 0);
 }
 
-// m = momentum m + g in place, and the sum of u^2: in fp32 over a warp's
-// elements, in fp64 over warps and blocks (fp64 is slow on this GPU: one
-// instruction per SM and 16 clocks for a warp, so few threads use it). Bound by
-// memory: reads g and m, writes m.
+// Row and first column of vector q of 8, with 32-bit division where it suffices.
+__device__ __forceinline__ void vector_at(int64_t q, uint32_t per_row, int64_t* r, int64_t* c) {
+  *r = q <= 0xffffffffll ? static_cast<int64_t>(static_cast<uint32_t>(q) / per_row) : q / per_row;
+  *c = (q - *r * per_row) * 8;
+}
+
+// m = momentum m + g in place, and the sum of u^2 in fp32: over a thread's
+// elements, a warp, a block and at last the blocks (each level adds at most a
+// few hundred terms, an error under 1e-5 of the norm in the worst case, against
+// the 5e-4 of the fp16 that it scales; fp64 would cost more than the loads do).
+// Bound by memory: reads g and m, writes m.
 template <bool F32, bool MOM>
 __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ ItemTable t, NsMomentum s) {
   let_next_start();
@@ -96,9 +103,11 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ ItemT
     const uint32_t per_row = static_cast<uint32_t>(it.cols / 8);
     const int64_t total = it.rows * per_row;
     const bool flat = it.ld == it.cols;
-#pragma unroll 2
+#pragma unroll 4
     for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < total; q += static_cast<int64_t>(gridDim.x) * 256) {
-      const int64_t at = flat ? q * 8 : q / per_row * it.ld + q % per_row * 8;
+      int64_t r = 0, c = q * 8;
+      if (!flat) vector_at(q, per_row, &r, &c);
+      const int64_t at = r * it.ld + c;
       float g[8];
       load_in8<F32>(it.g, at, g);
       if (MOM) {
@@ -142,8 +151,8 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ ItemT
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
-    double x = red[0];
-    for (int i = 1; i < 8; ++i) x += static_cast<double>(red[i]);
+    float x = red[0];
+    for (int i = 1; i < 8; ++i) x += red[i];
     it.part[blockIdx.x] = x;
   }
 }
@@ -154,23 +163,24 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Item
   let_next_start();
   wait_for_previous();
   const Item& it = t.it[blockIdx.y];
-  __shared__ float shared_inv;
-  if (threadIdx.x < 32) {
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < parts; i += 32) sum += it.part[i];
+  __shared__ float red[8];
+  float sum = 0.0f;
+  for (int i = threadIdx.x; i < parts; i += 256) sum += it.part[i];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
-    if (threadIdx.x == 0)
-      shared_inv = static_cast<float>(static_cast<double>(kScaleX) / (sqrt(sum) + static_cast<double>(s.eps)));
-  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
   __syncthreads();
-  const float inv = shared_inv;
+  sum = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) sum += red[i];
+  const float inv = kScaleX / (sqrtf(sum) + s.eps);
   if (vector_rows<MOM>(it)) {
     const uint32_t per_row = static_cast<uint32_t>(it.cols / 8);
     const int64_t total = it.rows * per_row;
-#pragma unroll 2
+#pragma unroll 4
     for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < total; q += static_cast<int64_t>(gridDim.x) * 256) {
-      const int64_t r = q / per_row, c = (q - r * per_row) * 8;
+      int64_t r, c;
+      vector_at(q, per_row, &r, &c);
       float u[8];
       load_in8<F32>(it.g, r * it.ld + c, u);
       if (MOM) {
@@ -265,7 +275,7 @@ struct Batch {
 
   static int64_t ld(int64_t n) { return ops_round_up(n, 64); }
   static int64_t item_bytes(const Shape2& s) {  // upper bound of what one more matrix adds, tall or wide
-    return 2 * std::max(s.rows * ld(s.cols), s.cols * ld(s.rows)) * 2 + 3 * s.m() * ld(s.m()) * 2 + kNormBlocks * 8 + 8 * 256;
+    return 2 * std::max(s.rows * ld(s.cols), s.cols * ld(s.rows)) * 2 + 3 * s.m() * ld(s.m()) * 2 + kNormBlocks * 4 + 8 * 256;
   }
 
   void build(const Shape2* shapes, int64_t count) {
@@ -273,7 +283,7 @@ struct Batch {
     classes.clear();
     int64_t at = 0;
     part_off = at;
-    at += ops_round_up(count * kNormBlocks * 8, 256);
+    at += ops_round_up(count * kNormBlocks * 4, 256);
     for (int64_t i = 0; i < count; ++i) {
       const int64_t m = shapes[i].m();
       if (classes.empty() || classes.back().m != m) classes.push_back({m, ld(m), 0, {0, 0, 0}});
@@ -524,7 +534,7 @@ extern "C" lst_status lst_orthogonalize(int32_t count, const lst_matrix* in, con
         it.ld = src.stride;
         it.x = reinterpret_cast<__half*>(ws + g.x_off[0]) + i * g.x_elems();
         it.ldx = g.ldx;
-        it.part = reinterpret_cast<double*>(ws + b.part_off) + i * kNormBlocks;
+        it.part = reinterpret_cast<float*>(ws + b.part_off) + i * kNormBlocks;
       }
       LST_TRY_CUDA(ingest(items, in[0].dtype == LST_F32, false, s, stream), who);
       Runner run{b, ws, stream, {}};
@@ -659,7 +669,7 @@ extern "C" lst_status lst_muon_step(const lst_layout* L, void* const* dev_blocks
         for (int64_t k = 0; k < g.count; ++k) {
           const Run r = run_of(L->tensors[(size_t)picks[first + (size_t)(g.first + k)].tensor]);
           items[(size_t)(g.first + k)] = {r.g, r.m, reinterpret_cast<__half*>(ws + g.x_off[0]) + k * g.x_elems(),
-                                          reinterpret_cast<double*>(ws + b.part_off) + (g.first + k) * kNormBlocks,
+                                          reinterpret_cast<float*>(ws + b.part_off) + (g.first + k) * kNormBlocks,
                                           g.s.rows, g.s.cols, g.s.cols, g.ldx};
         }
       LST_TRY_CUDA(ingest(items, f32, true, ms, stream), who);
