@@ -445,55 +445,67 @@ struct XentEpilogue {
       release();
       return;
     }
-    float v[128];
-#pragma unroll
-    for (int chunk = 0; chunk < 4; ++chunk) tc::tmem_ld32(tmem + 32 * chunk, v + 32 * chunk);
-    tc::tmem_ld_wait();
-    release();
-    const int left = s.n - col0;
+    const int left = min(s.n - col0, 128);
     const float ninf = __int_as_float(0xff800000);
-    if (left < 128) {
+    float top = ninf;
+#pragma unroll 1
+    for (int g = 0; g < 8; ++g) {
+      float v[16];
+      __syncwarp();
+      tc::tmem_ld16(tmem + 16 * g, v);
+      tc::tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 128; ++i)
-        if (i >= left) v[i] = ninf;
+      for (int i = 0; i < 16; ++i)
+        if (16 * g + i < left) top = fmaxf(top, v[i]);
     }
-    float m4[4] = {ninf, ninf, ninf, ninf};
-#pragma unroll
-    for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], v[i]);
-    const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+    const bool inside = row < s.m;
+    int target = -1;
+    if (inside) {
+      int64_t t64 = e.index_bytes == 8 ? static_cast<const int64_t*>(e.targets)[row] : static_cast<const int32_t*>(e.targets)[row];
+      t64 -= e.first_column + col0;
+      if (t64 >= 0 && t64 < left) target = static_cast<int>(t64);
+    }
     // all -inf: the sum is 0, or NaN where a logit is (max passes over NaN)
     const float base = top == ninf ? 0.0f : top;
-    float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float sum0 = 0.0f, sum1 = 0.0f, at_target = 0.0f;
+    uint16_t* const out = e.q && inside ? e.q + static_cast<int64_t>(row) * e.q_ld + col0 : nullptr;
+#pragma unroll 1
+    for (int g = 0; g < 8; ++g) {
+      float v[16];
+      __syncwarp();
+      tc::tmem_ld16(tmem + 16 * g, v);
+      tc::tmem_ld_wait();
+      if (16 * g + 16 > left) {
 #pragma unroll
-    for (int i = 0; i < 128; ++i) s4[i & 3] += tc::exp2_approx((v[i] - base) * 1.4426950408889634f);
-    const bool inside = row < s.m;
-    int64_t target = -1;
-    if (inside) {
-      e.stats[(e.first_group + (col0 >> 7)) * e.stat_ld + row] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
-      target = e.index_bytes == 8 ? static_cast<const int64_t*>(e.targets)[row] : static_cast<const int32_t*>(e.targets)[row];
-      target -= e.first_column + col0;
-    }
-    const bool hit = target >= 0 && target < 128 && target < left;
-    if (__any_sync(0xffffffffu, hit)) {
-      float x = 0.0f;
+        for (int i = 0; i < 16; ++i)
+          if (16 * g + i >= left) v[i] = ninf;
+      }
 #pragma unroll
-      for (int i = 0; i < 128; ++i)
-        x += i == static_cast<int>(target) ? v[i] : 0.0f;
-      if (hit) e.target_logit[row] = x;
-    }
-    if (e.q && inside) {
-      uint16_t* const out = e.q + static_cast<int64_t>(row) * e.q_ld + col0;
+      for (int i = 0; i < 16; i += 2) {
+        sum0 += tc::exp2_approx((v[i] - base) * 1.4426950408889634f);
+        sum1 += tc::exp2_approx((v[i + 1] - base) * 1.4426950408889634f);
+      }
+      if (target >> 4 == g) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+        for (int i = 0; i < 16; ++i)
+          if (i == (target & 15)) at_target = v[i];
+      }
+      if (out) {
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float lo = fminf((top - v[16 * j + 2 * i]) * 2048.0f, 65535.0f);
-          const float hi = fminf((top - v[16 * j + 2 * i + 1]) * 2048.0f, 65535.0f);
+          const float lo = fminf((top - v[2 * i]) * 2048.0f, 65535.0f);
+          const float hi = fminf((top - v[2 * i + 1]) * 2048.0f, 65535.0f);
           w[i] = __float2uint_rn(lo) | (__float2uint_rn(hi) << 16);
         }
-        store_row16(out + 16 * j, w, 16, 32);  // q_ld is a multiple of 128
+        store_row16(out + 16 * g, w, 16, 32);  // q_ld is a multiple of 128
       }
+    }
+    __syncwarp();
+    release();
+    if (inside) {
+      e.stats[(e.first_group + (col0 >> 7)) * e.stat_ld + row] = make_float2(top, sum0 + sum1);
+      if (target >= 0) e.target_logit[row] = at_target;
     }
   }
 };

@@ -38,6 +38,12 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int64_t kMaxPieceBytes = int64_t(1) << 30;
 
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ int64_t target_at(const void* t, int wide, int64_t i) {
   return wide ? static_cast<const int64_t*>(t)[i] : static_cast<const int32_t*>(t)[i];
 }
@@ -64,7 +70,7 @@ __global__ void __launch_bounds__(1024)
       const float2 s = stats[i * stat_ld + row];
       const float m = fmaxf(top, s.x);
       const float base = m == ninf ? 0.0f : m;
-      sum = sum * exp2f((top - base) * kLog2e) + s.y * exp2f((s.x - base) * kLog2e);
+      sum = sum * exp2_approx((top - base) * kLog2e) + s.y * exp2_approx((s.x - base) * kLog2e);
       top = m;
     }
   }
@@ -76,7 +82,7 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float base = m == ninf ? 0.0f : m;
-  float z = s.y * exp2f((s.x - base) * kLog2e);
+  float z = s.y * exp2_approx((s.x - base) * kLog2e);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   const int r = blockIdx.x * 32 + warp;
@@ -88,22 +94,28 @@ __global__ void __launch_bounds__(1024)
   }
   if (!mean) return;
 
-  __shared__ int last;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(counter, 1) == static_cast<int>(gridDim.x) - 1;
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  double total = 0.0;
+  if (gridDim.x > 1) {
+    __shared__ int last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(counter, 1) == static_cast<int>(gridDim.x) - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+  } else {
+    __syncthreads();
+  }
+  // fp64 for a thread's share (one in 1024 of the rows), fp32 for the tree above
+  double mine = 0.0;
   int count = 0;
 #pragma unroll 4
   for (int i = threadIdx.x; i < rows; i += 1024)
     if (target_at(targets, wide, i) != ignore) {
-      total += static_cast<double>(__ldcg(loss + i));
+      mine += static_cast<double>(__ldcg(loss + i));
       ++count;
     }
-  __shared__ double sums[32];
+  float total = static_cast<float>(mine);
+  __shared__ float sums[32];
   __shared__ int counts[32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -115,13 +127,18 @@ __global__ void __launch_bounds__(1024)
     counts[warp] = count;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < 32; ++i) {
-      total += sums[i];
-      count += counts[i];
+  if (warp == 0) {
+    total = sums[lane];
+    count = counts[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      total += __shfl_down_sync(0xffffffffu, total, o);
+      count += __shfl_down_sync(0xffffffffu, count, o);
     }
-    *mean = count ? static_cast<float>(total / count) : 0.0f;
-    *g = count ? static_cast<float>(static_cast<double>(grad_scale) / count) : 0.0f;
+    if (lane == 0) {
+      *mean = count ? total / static_cast<float>(count) : 0.0f;
+      *g = count ? grad_scale / static_cast<float>(count) : 0.0f;
+    }
   }
 }
 
@@ -180,10 +197,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float steps = static_cast<float>((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-    float e;
-    const float a = __fmaf_rn(steps, -kLog2e / 2048.0f, base);
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a));
-    d[i] = e * g;
+    d[i] = exp2_approx(__fmaf_rn(steps, -kLog2e / 2048.0f, base)) * g;
   }
   const int64_t at = t - first_column - col;
   if (at >= 0 && at < 16) {
@@ -216,6 +230,7 @@ __global__ void __launch_bounds__(256)
   const int col = static_cast<int>(i - static_cast<int64_t>(row) * quads) * 4;
   const float* p = parts + static_cast<int64_t>(row) * ld + col;
   float4 a = *reinterpret_cast<const float4*>(p);
+#pragma unroll 8
   for (int s = 1; s < splits; ++s) {
     const float4 b = *reinterpret_cast<const float4*>(p + s * split_stride);
     a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
