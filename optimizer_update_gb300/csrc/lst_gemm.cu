@@ -485,11 +485,8 @@ struct XentEpilogue {
         sum0 += tc::exp2_approx((v[i] - base) * 1.4426950408889634f);
         sum1 += tc::exp2_approx((v[i + 1] - base) * 1.4426950408889634f);
       }
-      if (target >> 4 == g) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i == (target & 15)) at_target = v[i];
-      }
+      for (int i = 0; i < 16; ++i) at_target = 16 * g + i == target ? v[i] : at_target;
       if (out) {
         uint32_t w[8];
 #pragma unroll

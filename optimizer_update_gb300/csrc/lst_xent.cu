@@ -217,22 +217,30 @@ __global__ void __launch_bounds__(256)
   p[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// dx = sum of its parts, in order, rounded to bf16.
+// dx = sum of its parts, in a fixed order, rounded to bf16: a block takes 128
+// columns of a row, its warps every eighth part each.
 __global__ void __launch_bounds__(256)
-    dx_kernel(const float* __restrict__ parts, int64_t ld, int64_t split_stride, int splits, int rows, int cols,
-              __nv_bfloat16* __restrict__ dx, int64_t dx_ld, int wide_store) {
+    dx_kernel(const float* __restrict__ parts, int64_t ld, int64_t split_stride, int splits, int cols,
+              __nv_bfloat16* __restrict__ dx, int64_t dx_ld, int wide_store, int slices) {
   let_next_start();
   wait_for_previous();
-  const int quads = (cols + 3) / 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int row = static_cast<int>(i / quads);
-  if (row >= rows) return;
-  const int col = static_cast<int>(i - static_cast<int64_t>(row) * quads) * 4;
+  __shared__ float4 sums[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x / slices, col = (blockIdx.x - row * slices) * 128 + 4 * lane;
   const float* p = parts + static_cast<int64_t>(row) * ld + col;
-  float4 a = *reinterpret_cast<const float4*>(p);
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (col < cols) {
 #pragma unroll 8
-  for (int s = 1; s < splits; ++s) {
-    const float4 b = *reinterpret_cast<const float4*>(p + s * split_stride);
+    for (int s = warp; s < splits; s += 8) {
+      const float4 b = *reinterpret_cast<const float4*>(p + s * split_stride);
+      a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+    }
+  }
+  sums[warp][lane] = a;
+  __syncthreads();
+  if (warp != 0 || col >= cols) return;
+  for (int w = 1; w < 8 && w < splits; ++w) {
+    const float4 b = sums[w][lane];
     a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
   }
   __nv_bfloat16* o = dx + static_cast<int64_t>(row) * dx_ld + col;
@@ -382,6 +390,15 @@ struct Call {
     return launch_gemm(GEMM_BF16_XENT, &g, 1, stream);
   }
 
+  cudaError_t sum_dx(const lst_matrix* dx) {
+    const int64_t slices = ops_ceil_div(dx->cols, 128);
+    const bool wide_store = dx->cols % 4 == 0 && dx->stride % 4 == 0 && reinterpret_cast<uintptr_t>(dx->data) % 8 == 0;
+    return launch_chained(dx_kernel, dim3(static_cast<unsigned>(dx->rows * slices)), dim3(256), 0, stream,
+                          reinterpret_cast<const float*>(ws + p.part_off), p.part_ld, dx->rows * p.part_ld,
+                          static_cast<int>(p.splits), static_cast<int>(dx->cols), static_cast<__nv_bfloat16*>(dx->data),
+                          dx->stride, wide_store, static_cast<int>(slices));
+  }
+
   cudaError_t join(float grad_scale, float* mean) {
     return launch_chained(join_kernel, dim3(static_cast<unsigned>(ops_ceil_div(x->rows, 32))), dim3(1024), 0, stream, 
         reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, static_cast<int>(p.groups),
@@ -511,12 +528,6 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
     }
     LST_TRY_CUDA(launch_gemm(GEMM_BF16, both, 2, stream), who);
   }
-  if (parts) {
-    const int64_t quads = ops_ceil_div(h, 4) * n;
-    const bool wide_store = h % 4 == 0 && dx->stride % 4 == 0 && reinterpret_cast<uintptr_t>(dx->data) % 8 == 0;
-    LST_TRY_CUDA(launch_chained(dx_kernel, dim3(static_cast<unsigned>(ops_ceil_div(quads, 256))), dim3(256), 0, stream, 
-        reinterpret_cast<const float*>(ws + p.part_off), p.part_ld, n * p.part_ld, static_cast<int>(p.splits),
-        static_cast<int>(n), static_cast<int>(h), static_cast<__nv_bfloat16*>(dx->data), dx->stride, wide_store), who);
-  }
+  if (parts) LST_TRY_CUDA(c.sum_dx(dx), who);
   return LST_OK;
 }
