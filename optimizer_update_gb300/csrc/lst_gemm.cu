@@ -139,30 +139,19 @@ __device__ __forceinline__ void load_turned(uint32_t tmem, uint32_t turn, float 
   for (int i = 0; i < 32; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(turn + (i * 33 + lane) * 4));
 }
 
-// 16 consecutive 16-bit values of one row, `left` of them inside the matrix.
-__device__ __forceinline__ void store_row16(uint16_t* p, const uint32_t (&w)[8], int left, int vec) {
-  if (left >= 16 && vec >= 32) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else if (left >= 16 && vec >= 16) {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  } else {
+// The first `left` < 8 values of 8.
+__device__ __forceinline__ uint4 load_tail(const uint16_t* p, int left) {
+  uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < left) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-  }
+  for (int i = 0; i < 7; ++i)
+    if (i < left) w[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void load_row16(const uint16_t* p, uint32_t (&w)[8], int left, int vec) {
-  if (left >= 16 && vec >= 16) {
-    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-  } else {
+__device__ __forceinline__ void store_tail(uint16_t* p, const uint4& v, int left) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i] = (2 * i < left ? p[2 * i] : 0u) | ((2 * i + 1 < left ? static_cast<uint32_t>(p[2 * i + 1]) : 0u) << 16);
-  }
+  for (int i = 0; i < 7; ++i)
+    if (i < left) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
 }
 
 struct StoreEpilogue {
@@ -210,47 +199,88 @@ struct StoreEpilogue {
       release();
       return;
     }
-    const bool bf16 = e.bf16 != 0, inside = row < s.m;
+    // 64 columns at a time through the warp's words, row by row in, four whole
+    // 128-byte rows an instruction out: a lane per row would touch 32 lines with
+    // every store (a 256 x 256 product of depth 256: 5.2 us, STORE_US so).
+    const bool bf16 = e.bf16 != 0;
     constexpr int kAcross = kGemmTile / (2 * kCols);  // tiles of a diagonal block are formed whole
     const bool mirror = s.symmetric && t.tn >= kAcross * (t.tm + 1);
-    const int64_t at = t.batch * e.batch_stride + static_cast<int64_t>(row) * e.ld + col0;
-    uint16_t* out = static_cast<uint16_t*>(e.out) + at;
-    uint16_t* across = static_cast<uint16_t*>(e.out) + t.batch * e.batch_stride + static_cast<int64_t>(col0) * e.ld + row;
-    const uint16_t* c = e.c && inside ? static_cast<const uint16_t*>(e.c) + at : nullptr;
-    uint32_t next[8];
-    if (c) load_row16(c, next, s.n - col0, e.vec);
+    const int lane = row & 31, row0 = row & ~31, rows = s.m - row0;
+    const int64_t matrix = t.batch * e.batch_stride;
+    uint16_t* const out = static_cast<uint16_t*>(e.out) + matrix;
+    const uint16_t* const c = e.c ? static_cast<const uint16_t*>(e.c) + matrix : nullptr;
+    const int unit = lane & 7;                              // 8 columns, of rows 4 i + lane / 8
+    auto word = [&](int r, int u) { return turn + r * 128 + ((u ^ (r & 7)) << 4); };
 #pragma unroll 1
-    for (int g = 0; g < kCols / 16; ++g) {
-      const int left = s.n - col0 - 16 * g;
+    for (int h = 0; h < kCols / 64; ++h) {
+      const int col = col0 + 64 * h, left = s.n - col;
       if (left <= 0) break;
-      float v[16];
       __syncwarp();
-      tc::tmem_ld16(tmem + 16 * g, v);
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = next[i];
-      if (c && left > 16 && g + 1 < kCols / 16) load_row16(c + 16 * (g + 1), next, left - 16, e.vec);
-      tc::tmem_ld_wait();
-      if (!inside) continue;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = v[i] * e.alpha;
       if (c) {
+        uint4 w[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          v[i] = __fmaf_rn(e.beta, unpack16(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))), bf16), v[i]);
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          const uint16_t* p = c + static_cast<int64_t>(row0 + r) * e.ld + col + 8 * unit;
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (r < rows && 8 * unit + 8 <= left)
+            w[i] = *reinterpret_cast<const uint4*>(p);
+          else if (r < rows && 8 * unit < left)
+            w[i] = load_tail(p, left - 8 * unit);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t a = word(4 * i + (lane >> 3), unit);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[i].x), "r"(w[i].y), "r"(w[i].z), "r"(w[i].w));
+        }
+        __syncwarp();
       }
-      const int diag = row - col0 - 16 * g;
-      if (e.diag != 0.0f && diag >= 0 && diag < 16) {
+#pragma unroll 1
+      for (int g = 0; g < 4; ++g) {
+        float v[16];
+        __syncwarp();
+        tc::tmem_ld16(tmem + 64 * h + 16 * g, v);
+        const uint32_t a0 = word(lane, 2 * g), a1 = word(lane, 2 * g + 1);
+        uint32_t w[8];
+        if (c) {
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a0));
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "r"(a1));
+        }
+        tc::tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] += i == diag ? e.diag : 0.0f;
+        for (int i = 0; i < 16; ++i) v[i] = v[i] * e.alpha;
+        if (c) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            v[i] = __fmaf_rn(e.beta, unpack16(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))), bf16), v[i]);
+        }
+        const int diag = row - col - 16 * g;
+        if (e.diag != 0.0f && diag >= 0 && diag < 16) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += i == diag ? e.diag : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack16(v[2 * i], v[2 * i + 1], bf16);
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a0), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]));
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a1), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]));
+        if (mirror && lane < rows) {
+          uint16_t* across = out + static_cast<int64_t>(col + 16 * g) * e.ld + row;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (16 * g + i < left) across[static_cast<int64_t>(i) * e.ld] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+        }
       }
+      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pack16(v[2 * i], v[2 * i + 1], bf16);
-      store_row16(out + 16 * g, w, left, e.vec);
-      if (mirror) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < left) across[static_cast<int64_t>(16 * g + i) * e.ld] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+      for (int i = 0; i < 8; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        uint4 w;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(word(r, unit)));
+        uint16_t* p = out + static_cast<int64_t>(row0 + r) * e.ld + col + 8 * unit;
+        if (r < rows && 8 * unit + 8 <= left)
+          *reinterpret_cast<uint4*>(p) = w;
+        else if (r < rows && 8 * unit < left)
+          store_tail(p, w, left - 8 * unit);
       }
     }
     __syncwarp();
@@ -376,26 +406,18 @@ struct PartialEpilogue {
   template <int kCols, class Release>
   static __device__ __forceinline__ void run(const Params& e, const Table&, const Shape& s, const Tile& t, int row,
                                              int col0, uint32_t tmem, uint32_t turn, Release release) {
-    float* const out = e.out + t.split * e.split_stride + static_cast<int64_t>(row) * e.ld + col0;
+    const int lane = row & 31, row0 = row & ~31, rows = s.m - row0;
+    float* const out = e.out + t.split * e.split_stride + static_cast<int64_t>(row0) * e.ld + col0 + lane;
 #pragma unroll 1
-    for (int g = 0; g < kCols / 16; ++g) {
-      if (col0 + 16 * g >= s.n) break;
-      float v[16];
-      __syncwarp();
-      tc::tmem_ld16(tmem + 16 * g, v);
-      tc::tmem_ld_wait();
-      if (row < s.m) {
-        // ld is a multiple of 32, so a row's tail may be written past column n
+    for (int g = 0; g < kCols / 32; ++g) {
+      if (col0 + 32 * g >= s.n) break;
+      const bool inside = col0 + 32 * g + lane < s.n;
+      float v[32];
+      load_turned(tmem + 32 * g, turn, v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float4* p = reinterpret_cast<float4*>(out + 16 * g) + j;
-          float4 x = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          if (e.accumulate) {
-            const float4 y = *p;
-            x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-          }
-          *p = x;
-        }
+      for (int i = 0; i < 32; ++i) {
+        float* p = out + i * e.ld + 32 * g;
+        if (inside && i < rows) *p = e.accumulate ? *p + v[i] : v[i];
       }
     }
     __syncwarp();
@@ -495,7 +517,9 @@ struct XentEpilogue {
           const float hi = fminf((top - v[2 * i + 1]) * 2048.0f, 65535.0f);
           w[i] = __float2uint_rn(lo) | (__float2uint_rn(hi) << 16);
         }
-        store_row16(out + 16 * g, w, 16, 32);  // q_ld is a multiple of 128
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(out + 16 * g), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");  // q_ld is a multiple of 256
       }
     }
     __syncwarp();
