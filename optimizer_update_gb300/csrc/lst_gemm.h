@@ -19,7 +19,8 @@ struct GemmOperand {
 };
 
 // out = alpha * acc + beta * c (+ diag on the main diagonal), rounded to fp16
-// or bf16; c has out's shape, pitch and type. `vec`: bytes a store may be
+// or bf16; c has out's shape, pitch and type; alpha times *scale where that is
+// not null (device memory). `vec`: bytes a store may be
 // wide (32, 16 or 2) by out's alignment.
 struct StoreParams {
   void* out;
@@ -27,6 +28,7 @@ struct StoreParams {
   int64_t ld, batch_stride;
   float alpha, beta, diag;
   int32_t bf16, vec;
+  const float* scale = nullptr;
 };
 
 // w = w * decay - step * acc for the matrices of the batch, with w, the derived

@@ -10,11 +10,14 @@
 // and the sum of exp(l - M), from which a second kernel joins lse. For the
 // gradient the tile also leaves (M - l) in 16 bits of fixed point, steps of
 // 2^-11: the workspace holds as many columns of those ("a piece") as fit, and
-// d is written over them in bf16 once lse is known. That one rounding (and
+// d / g is written over them in bf16 once lse is known. That one rounding (and
 // the 2^-12 of the fixed point, eight times smaller) is all that d loses;
 // keeping exp(l - M) in bf16 instead and rescaling it would round twice. A
 // bf16 d is what the tensor cores take next to the bf16 x and w; its error is
-// that of the results' own rounding.
+// that of the results' own rounding. g multiplies the fp32 results: inside d,
+// -g would round alike for every token with an unlikely target, a common factor
+// up to 2^-8 off on dx and dw (measured 3.3e-3 from the 64-bit gradient instead
+// of 1.9e-3).
 //   One piece: 2 N V H operations for the logits, 4 N V H for dx and dw.
 //   More pieces: first the statistics of all of them; then each piece's logits
 //   are formed again (except those of the one formed last, still there), 8 N V H in all.
@@ -50,12 +53,18 @@ __device__ __forceinline__ int64_t target_at(const void* t, int wide, int64_t i)
 
 // lse and loss of 32 rows from the statistics of all 128-column groups: 32
 // threads per row take every 32nd group each, with the running maximum and sum.
+// The target's logit is formed again as a plain fp32 dot product: the tensor
+// cores' sums round towards zero, by up to 1e-5 for a logit of 10, and unlike the
+// errors of the other logits this one does not average out of the loss. With
+// delta = (dot product - tensor-core logit), lse moves by p delta to first order,
+// so that a certain target (p = 1) keeps a loss of zero.
 // With `mean`, the last block to finish also forms the mean loss and g =
 // grad_scale / N from all losses, in a fixed order.
 __global__ void __launch_bounds__(1024)
-    join_kernel(const float2* __restrict__ stats, int64_t stat_ld, int groups, const float* __restrict__ target_logit,
-                const void* __restrict__ targets, int wide, int64_t ignore, int64_t vocab, int rows, float* loss,
-                float* __restrict__ lse, float grad_scale, float* __restrict__ mean, float* __restrict__ g,
+    join_kernel(const float2* __restrict__ stats, int64_t stat_ld, int groups, float* __restrict__ target_logit,
+                const void* __restrict__ targets, int wide, int64_t ignore, int64_t vocab, int rows,
+                const uint16_t* __restrict__ x, int64_t x_ld, const uint16_t* __restrict__ w, int64_t w_ld, int hidden,
+                float* loss, float* __restrict__ lse, float grad_scale, float* __restrict__ mean, float* __restrict__ g,
                 int32_t* counter) {
   let_next_start();
   wait_for_previous();
@@ -75,8 +84,33 @@ __global__ void __launch_bounds__(1024)
     }
   }
   part[warp][lane] = make_float2(top, sum);
+  // warp w has row w of the block
+  const int r = blockIdx.x * 32 + warp;
+  const int64_t t = r < rows ? target_at(targets, wide, r) : ignore;
+  const bool with_target = t != ignore && t >= 0 && t < vocab;
+  float dot = 0.0f;
+  if (with_target) {
+    const uint16_t* a = x + r * x_ld;
+    const uint16_t* b = w + t * w_ld;
+    if (hidden % 8 == 0) {  // rows are on 16 bytes
+#pragma unroll 4
+      for (int k = 8 * lane; k < hidden; k += 256) {
+        const uint4 u = *reinterpret_cast<const uint4*>(a + k), v = *reinterpret_cast<const uint4*>(b + k);
+        const uint32_t p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dot = __fmaf_rn(__uint_as_float(p[i] << 16), __uint_as_float(q[i] << 16), dot);
+          dot = __fmaf_rn(__uint_as_float(p[i] & 0xffff0000u), __uint_as_float(q[i] & 0xffff0000u), dot);
+        }
+      }
+    } else {
+      for (int k = lane; k < hidden; k += 32)
+        dot = __fmaf_rn(__uint_as_float(static_cast<uint32_t>(a[k]) << 16), __uint_as_float(static_cast<uint32_t>(b[k]) << 16), dot);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
   __syncthreads();
-  // warp w joins row w of the block
   const float2 s = part[lane][warp];
   float m = s.x;
 #pragma unroll
@@ -85,12 +119,15 @@ __global__ void __launch_bounds__(1024)
   float z = s.y * exp2_approx((s.x - base) * kLog2e);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  const int r = blockIdx.x * 32 + warp;
   if (lane == 0 && r < rows) {
-    const float l = base + logf(z);
-    const int64_t t = target_at(targets, wide, r);
+    float l = base + logf(z);
+    if (with_target) {
+      const float old = target_logit[r], delta = dot - old;
+      l += delta * exp2_approx((old - l) * kLog2e);
+      target_logit[r] = dot;
+    }
     lse[r] = l;
-    loss[r] = t == ignore ? 0.0f : (t >= 0 && t < vocab) ? l - target_logit[r] : __int_as_float(0x7fc00000);
+    loss[r] = with_target ? l - dot : t == ignore ? 0.0f : __int_as_float(0x7fc00000);
   }
   if (!mean) return;
 
@@ -156,13 +193,13 @@ struct MaskedRows {
   int32_t rows, cols, vec;
 };
 
-// d over q, in place: 16 entries per thread, one row per block of columns. The
+// d / g over q, in place: 16 entries per thread, one row per block of columns. The
 // blocks after the first `d_blocks` copy x with its rows masked.
 __global__ void __launch_bounds__(256)
     logit_grad_kernel(uint16_t* __restrict__ q, int64_t q_ld, const float2* __restrict__ stats, int64_t stat_ld,
                       int64_t first_group, int64_t first_column, int columns, const float* __restrict__ lse,
                       const float* __restrict__ target_logit, const void* __restrict__ targets, int wide,
-                      int64_t ignore, int64_t vocab, const float* __restrict__ gp, int blocks_per_row, int d_blocks,
+                      int64_t ignore, int64_t vocab, int blocks_per_row, int d_blocks,
                       MaskedRows x) {
   let_next_start();
   wait_for_previous();
@@ -189,7 +226,7 @@ __global__ void __launch_bounds__(256)
     return;
   }
   const uint4 x0 = p[0], x1 = p[1];
-  const float g = *gp, l = lse[row];
+  const float l = lse[row];
   const float top = stats[(first_group + (col >> 7)) * stat_ld + row].x;
   const float base = (top - l) * kLog2e;
   const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
@@ -197,12 +234,12 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float steps = static_cast<float>((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-    d[i] = exp2_approx(__fmaf_rn(steps, -kLog2e / 2048.0f, base)) * g;
+    d[i] = exp2_approx(__fmaf_rn(steps, -kLog2e / 2048.0f, base));
   }
   const int64_t at = t - first_column - col;
   if (at >= 0 && at < 16) {
     // the target's own probability from its fp32 logit: p - 1 cancels when p is near 1
-    const float e = expm1f(target_logit[row] - l) * g;
+    const float e = expm1f(target_logit[row] - l);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (i == static_cast<int>(at)) d[i] = e;
@@ -217,11 +254,11 @@ __global__ void __launch_bounds__(256)
   p[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// dx = sum of its parts, in a fixed order, rounded to bf16: a block takes 128
+// dx = g times the sum of its parts, in a fixed order, rounded to bf16: a block takes 128
 // columns of a row, its warps every eighth part each.
 __global__ void __launch_bounds__(256)
     dx_kernel(const float* __restrict__ parts, int64_t ld, int64_t split_stride, int splits, int cols,
-              __nv_bfloat16* __restrict__ dx, int64_t dx_ld, int wide_store, int slices) {
+              __nv_bfloat16* __restrict__ dx, int64_t dx_ld, int wide_store, int slices, const float* __restrict__ gp) {
   let_next_start();
   wait_for_previous();
   __shared__ float4 sums[8][32];
@@ -244,7 +281,7 @@ __global__ void __launch_bounds__(256)
     a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
   }
   __nv_bfloat16* o = dx + static_cast<int64_t>(row) * dx_ld + col;
-  const float v[4] = {a.x, a.y, a.z, a.w};
+  const float g = *gp, v[4] = {a.x * g, a.y * g, a.z * g, a.w * g};
   if (wide_store) {
     const __nv_bfloat162 h0 = __floats2bfloat162_rn(v[0], v[1]), h1 = __floats2bfloat162_rn(v[2], v[3]);
     *reinterpret_cast<uint2*>(o) =
@@ -396,14 +433,16 @@ struct Call {
     return launch_chained(dx_kernel, dim3(static_cast<unsigned>(dx->rows * slices)), dim3(256), 0, stream,
                           reinterpret_cast<const float*>(ws + p.part_off), p.part_ld, dx->rows * p.part_ld,
                           static_cast<int>(p.splits), static_cast<int>(dx->cols), static_cast<__nv_bfloat16*>(dx->data),
-                          dx->stride, wide_store, static_cast<int>(slices));
+                          dx->stride, wide_store, static_cast<int>(slices),
+                          reinterpret_cast<const float*>(ws + p.scalar_off));
   }
 
   cudaError_t join(float grad_scale, float* mean) {
     return launch_chained(join_kernel, dim3(static_cast<unsigned>(ops_ceil_div(x->rows, 32))), dim3(1024), 0, stream, 
         reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, static_cast<int>(p.groups),
-        reinterpret_cast<const float*>(ws + p.tlogit_off), targets->data, wide, ignore, w->rows,
-        static_cast<int>(x->rows), loss, lse, grad_scale, mean, reinterpret_cast<float*>(ws + p.scalar_off),
+        reinterpret_cast<float*>(ws + p.tlogit_off), targets->data, wide, ignore, w->rows,
+        static_cast<int>(x->rows), static_cast<const uint16_t*>(xp), x_ld, static_cast<const uint16_t*>(wp), w_ld,
+        static_cast<int>(x->cols), loss, lse, grad_scale, mean, reinterpret_cast<float*>(ws + p.scalar_off),
         reinterpret_cast<int32_t*>(ws + p.scalar_off) + 1);
   }
 };
@@ -502,7 +541,7 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
     LST_TRY_CUDA(launch_chained(logit_grad_kernel, dim3(static_cast<unsigned>(d_blocks + copies)), dim3(256), 0, stream, q,
                                 p.piece, reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, v0 / 128, v0,
                                 static_cast<int>(columns), lse, reinterpret_cast<const float*>(ws + p.tlogit_off),
-                                targets->data, c.wide, ignore_index, v, g, blocks, static_cast<int>(d_blocks), masked),
+                                targets->data, c.wide, ignore_index, v, blocks, static_cast<int>(d_blocks), masked),
                  who);
     // dw of the piece = d^T x, and dx += d w, in one launch: the tiles of the longer sums first
     GemmProblem both[2];
@@ -514,7 +553,7 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
     d.n = h;
     d.k = n;
     uint16_t* dwp = static_cast<uint16_t*>(dw->data) + v0 * dw->stride;
-    d.store = {dwp, accumulate_dw ? dwp : nullptr, dw->stride, 0, 1.0f, 1.0f, 0.0f, 1, store_width(dw)};
+    d.store = {dwp, accumulate_dw ? dwp : nullptr, dw->stride, 0, 1.0f, 1.0f, 0.0f, 1, store_width(dw), g};
     e.a = rows_operand(q, n, columns, p.piece);
     e.b = rows_operand(static_cast<const uint16_t*>(c.wp) + v0 * c.w_ld, columns, h, c.w_ld, true);
     e.m = n;
@@ -524,7 +563,7 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
       e.splits = static_cast<int>(p.splits);
       e.partial = {reinterpret_cast<float*>(ws + p.part_off), p.part_ld, n * p.part_ld, k > 0};
     } else {
-      e.store = {dx->data, nullptr, dx->stride, 0, 1.0f, 0.0f, 0.0f, 1, store_width(dx)};
+      e.store = {dx->data, nullptr, dx->stride, 0, 1.0f, 0.0f, 0.0f, 1, store_width(dx), g};
     }
     LST_TRY_CUDA(launch_gemm(GEMM_BF16, both, 2, stream), who);
   }
