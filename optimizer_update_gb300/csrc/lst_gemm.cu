@@ -527,7 +527,7 @@ struct XentEpilogue {
     __syncwarp();
     release();
     if (inside) {
-      e.stats[(e.first_group + (col0 >> 7)) * e.stat_ld + row] = make_float2(top, sum0 + sum1);
+      e.stats[row * e.stat_ld + e.first_group + (col0 >> 7)] = make_float2(top, sum0 + sum1);
       if (target >= 0) e.target_logit[row] = at_target;
     }
   }

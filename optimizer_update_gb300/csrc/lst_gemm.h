@@ -58,7 +58,7 @@ struct PartialParams {
 // on the spot; see lst_xent.cu.
 struct XentParams {
   const void* targets;
-  float2* stats;    // [128-column group][row]: (max, sum of exp(l - max))
+  float2* stats;    // [row][128-column group]: (max, sum of exp(l - max))
   float* target_logit;
   int32_t* counter; // set to 0
   uint16_t* q;      // [row][column]: (max - l) in steps of 2^-11, or null

@@ -51,8 +51,10 @@ __device__ __forceinline__ int64_t target_at(const void* t, int wide, int64_t i)
   return wide ? static_cast<const int64_t*>(t)[i] : static_cast<const int32_t*>(t)[i];
 }
 
-// lse and loss of 32 rows from the statistics of all 128-column groups: 32
-// threads per row take every 32nd group each, with the running maximum and sum.
+// lse and loss of a row from the statistics of its 128-column groups, a block per
+// row: short chains of dependent loads, and short code. Whole training calls of
+// 1023 tokens of 32000 took 316 us with it, 329 with a warp per row, 335 with a
+// warp per row and its loops unrolled, 326 with blocks that take several rows.
 // The target's logit is formed again as a plain fp32 dot product: the tensor
 // cores' sums round towards zero, by up to 1e-5 for a logit of 10, and unlike the
 // errors of the other logits this one does not average out of the loss. With
@@ -60,7 +62,8 @@ __device__ __forceinline__ int64_t target_at(const void* t, int wide, int64_t i)
 // so that a certain target (p = 1) keeps a loss of zero.
 // With `mean`, the last block to finish also forms the mean loss and g =
 // grad_scale / N from all losses, in a fixed order.
-__global__ void __launch_bounds__(1024)
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const float2* __restrict__ stats, int64_t stat_ld, int groups, float* __restrict__ target_logit,
                 const void* __restrict__ targets, int wide, int64_t ignore, int64_t vocab, int rows,
                 const uint16_t* __restrict__ x, int64_t x_ld, const uint16_t* __restrict__ w, int64_t w_ld, int hidden,
@@ -68,33 +71,17 @@ __global__ void __launch_bounds__(1024)
                 int32_t* counter) {
   let_next_start();
   wait_for_previous();
-  __shared__ float2 part[32][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x;
   const float ninf = __int_as_float(0xff800000);
-  float top = ninf, sum = 0.0f;
-  if (row < rows) {
-#pragma unroll 8
-    for (int i = warp; i < groups; i += 32) {
-      const float2 s = stats[i * stat_ld + row];
-      const float m = fmaxf(top, s.x);
-      const float base = m == ninf ? 0.0f : m;
-      sum = sum * exp2_approx((top - base) * kLog2e) + s.y * exp2_approx((s.x - base) * kLog2e);
-      top = m;
-    }
-  }
-  part[warp][lane] = make_float2(top, sum);
-  // warp w has row w of the block
-  const int r = blockIdx.x * 32 + warp;
-  const int64_t t = r < rows ? target_at(targets, wide, r) : ignore;
+  const int64_t t = target_at(targets, wide, r);
   const bool with_target = t != ignore && t >= 0 && t < vocab;
-  float dot = 0.0f;
+  float dot = 0.0f, top = ninf, sum = 0.0f;
   if (with_target) {
     const uint16_t* a = x + r * x_ld;
     const uint16_t* b = w + t * w_ld;
     if (hidden % 8 == 0) {  // rows are on 16 bytes
-#pragma unroll 4
-      for (int k = 8 * lane; k < hidden; k += 256) {
+#pragma unroll 1
+      for (int k = 8 * threadIdx.x; k < hidden; k += 8 * kJoinThreads) {
         const uint4 u = *reinterpret_cast<const uint4*>(a + k), v = *reinterpret_cast<const uint4*>(b + k);
         const uint32_t p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -104,30 +91,49 @@ __global__ void __launch_bounds__(1024)
         }
       }
     } else {
-      for (int k = lane; k < hidden; k += 32)
+#pragma unroll 1
+      for (int k = threadIdx.x; k < hidden; k += kJoinThreads)
         dot = __fmaf_rn(__uint_as_float(static_cast<uint32_t>(a[k]) << 16), __uint_as_float(static_cast<uint32_t>(b[k]) << 16), dot);
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-  __syncthreads();
-  const float2 s = part[lane][warp];
-  float m = s.x;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float base = m == ninf ? 0.0f : m;
-  float z = s.y * exp2_approx((s.x - base) * kLog2e);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  if (lane == 0 && r < rows) {
-    float l = base + logf(z);
-    if (with_target) {
-      const float old = target_logit[r], delta = dot - old;
-      l += delta * exp2_approx((old - l) * kLog2e);
-      target_logit[r] = dot;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < groups; i += kJoinThreads) {
+    const float2 s = stats[r * stat_ld + i];
+    const float m = fmaxf(top, s.x), base = m == ninf ? 0.0f : m;
+    sum = sum * exp2_approx((top - base) * kLog2e) + s.y * exp2_approx((s.x - base) * kLog2e);
+    top = m;
+  }
+  __shared__ float3 part[kJoinThreads / 32];
+  auto join = [&](int width) {  // over `width` lanes
+    float m = top;
+#pragma unroll 1
+    for (int o = width / 2; o > 0; o >>= 1) {
+      dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
-    lse[r] = l;
-    loss[r] = with_target ? l - dot : t == ignore ? 0.0f : __int_as_float(0x7fc00000);
+    const float base = m == ninf ? 0.0f : m;
+    sum *= exp2_approx((top - base) * kLog2e);
+    top = m;
+#pragma unroll 1
+    for (int o = width / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  };
+  join(32);
+  if (lane == 0) part[warp] = make_float3(top, sum, dot);
+  __syncthreads();
+  if (warp == 0) {
+    const float3 p = part[lane & (kJoinThreads / 32 - 1)];
+    top = p.x, sum = p.y, dot = p.z;
+    join(kJoinThreads / 32);
+    if (lane == 0) {
+      float l = (top == ninf ? 0.0f : top) + logf(sum);
+      if (with_target) {
+        const float old = target_logit[r], delta = dot - old;
+        l += delta * exp2_approx((old - l) * kLog2e);
+        target_logit[r] = dot;
+      }
+      lse[r] = l;
+      loss[r] = with_target ? l - dot : t == ignore ? 0.0f : __int_as_float(0x7fc00000);
+    }
   }
   if (!mean) return;
 
@@ -142,18 +148,28 @@ __global__ void __launch_bounds__(1024)
   } else {
     __syncthreads();
   }
-  // fp64 for a thread's share (one in 1024 of the rows), fp32 for the tree above
+  // fp64 for a thread's share of the rows, fp32 for the tree above
   double mine = 0.0;
   int count = 0;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < rows; i += 1024)
-    if (target_at(targets, wide, i) != ignore) {
-      mine += static_cast<double>(__ldcg(loss + i));
-      ++count;
+  for (int i0 = threadIdx.x; i0 < rows; i0 += 4 * kJoinThreads) {
+    int64_t of[4];
+    float each[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * kJoinThreads;
+      of[j] = i < rows ? target_at(targets, wide, i) : ignore;
+      each[j] = i < rows ? __ldcg(loss + i) : 0.0f;
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (of[j] != ignore) {
+        mine += static_cast<double>(each[j]);
+        ++count;
+      }
+  }
   float total = static_cast<float>(mine);
-  __shared__ float sums[32];
-  __shared__ int counts[32];
+  __shared__ float sums[kJoinThreads / 32];
+  __shared__ int counts[kJoinThreads / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     total += __shfl_down_sync(0xffffffffu, total, o);
@@ -165,8 +181,8 @@ __global__ void __launch_bounds__(1024)
   }
   __syncthreads();
   if (warp == 0) {
-    total = sums[lane];
-    count = counts[lane];
+    total = lane < kJoinThreads / 32 ? sums[lane] : 0.0f;
+    count = lane < kJoinThreads / 32 ? counts[lane] : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       total += __shfl_down_sync(0xffffffffu, total, o);
@@ -227,7 +243,7 @@ __global__ void __launch_bounds__(256)
   }
   const uint4 x0 = p[0], x1 = p[1];
   const float l = lse[row];
-  const float top = stats[(first_group + (col >> 7)) * stat_ld + row].x;
+  const float top = stats[row * stat_ld + first_group + (col >> 7)].x;
   const float base = (top - l) * kLog2e;
   const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
   float d[16];
@@ -254,31 +270,26 @@ __global__ void __launch_bounds__(256)
   p[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// dx = g times the sum of its parts, in a fixed order, rounded to bf16: a block takes 128
-// columns of a row, its warps every eighth part each.
+// dx = g times the sum of its parts, in a fixed order, rounded to bf16.
 __global__ void __launch_bounds__(256)
-    dx_kernel(const float* __restrict__ parts, int64_t ld, int64_t split_stride, int splits, int cols,
-              __nv_bfloat16* __restrict__ dx, int64_t dx_ld, int wide_store, int slices, const float* __restrict__ gp) {
+    dx_kernel(const float* __restrict__ parts, int64_t ld, int64_t split_stride, int splits, int rows, int cols,
+              __nv_bfloat16* __restrict__ dx, int64_t dx_ld, int wide_store, const float* __restrict__ gp) {
   let_next_start();
   wait_for_previous();
-  __shared__ float4 sums[8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x / slices, col = (blockIdx.x - row * slices) * 128 + 4 * lane;
+  const int quads = (cols + 3) / 4;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int row = static_cast<int>(i / quads);
+  if (row >= rows) return;
+  const int col = static_cast<int>(i - static_cast<int64_t>(row) * quads) * 4;
   const float* p = parts + static_cast<int64_t>(row) * ld + col;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (col < cols) {
-#pragma unroll 8
-    for (int s = warp; s < splits; s += 8) {
-      const float4 b = *reinterpret_cast<const float4*>(p + s * split_stride);
-      a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-    }
-  }
-  sums[warp][lane] = a;
-  __syncthreads();
-  if (warp != 0 || col >= cols) return;
-  for (int w = 1; w < 8 && w < splits; ++w) {
-    const float4 b = sums[w][lane];
-    a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+  for (int s0 = 0; s0 < splits; s0 += 8) {  // eight parts in flight
+    float4 b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      b[j] = s0 + j < splits ? *reinterpret_cast<const float4*>(p + (s0 + j) * split_stride) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = make_float4(a.x + b[j].x, a.y + b[j].y, a.z + b[j].z, a.w + b[j].w);
   }
   __nv_bfloat16* o = dx + static_cast<int64_t>(row) * dx_ld + col;
   const float g = *gp, v[4] = {a.x * g, a.y * g, a.z * g, a.w * g};
@@ -307,7 +318,7 @@ bool tile_ready(const lst_matrix* m) {
 }
 
 struct Plan {
-  int64_t n_pad, groups, piece, pieces, splits;
+  int64_t groups, piece, pieces, splits;
   int64_t packed_ld, x_ld, part_ld;
   int64_t scalar_off, tlogit_off, stats_off, xm_off, xpack_off, wpack_off, part_off, q_off;
   int64_t fixed;  // bytes before the pieces
@@ -317,7 +328,6 @@ struct Plan {
 // Layout of the workspace; `bytes` < 0: for one piece, at most 1 GiB of it.
 // Returns false when not even one tile of columns fits.
 bool make_plan(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool pack_w, int64_t bytes, Plan* p) {
-  p->n_pad = ops_round_up(n, 64);
   p->groups = ops_ceil_div(v, 128);
   p->packed_ld = ops_round_up(h, 8);
   int64_t at = 0;
@@ -328,7 +338,7 @@ bool make_plan(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool pac
   };
   p->scalar_off = take(256);
   p->tlogit_off = take(n * 4);
-  p->stats_off = take(p->groups * p->n_pad * 8);
+  p->stats_off = take(n * p->groups * 8);
   p->xpack_off = take(pack_x ? n * p->packed_ld * 2 : 0);
   p->wpack_off = take(pack_w ? v * p->packed_ld * 2 : 0);
   p->piece = p->pieces = 0;
@@ -422,24 +432,23 @@ struct Call {
     g.n = columns;
     g.k = x->cols;
     g.xent = {targets->data, reinterpret_cast<float2*>(ws + p.stats_off), reinterpret_cast<float*>(ws + p.tlogit_off),
-              reinterpret_cast<int32_t*>(ws + p.scalar_off) + 1, keep ? reinterpret_cast<uint16_t*>(ws + p.q_off) : nullptr, p.piece, p.n_pad, v0 / 128, v0,
+              reinterpret_cast<int32_t*>(ws + p.scalar_off) + 1, keep ? reinterpret_cast<uint16_t*>(ws + p.q_off) : nullptr, p.piece, p.groups, v0 / 128, v0,
               targets->bits / 8};
     return launch_gemm(GEMM_BF16_XENT, &g, 1, stream);
   }
 
   cudaError_t sum_dx(const lst_matrix* dx) {
-    const int64_t slices = ops_ceil_div(dx->cols, 128);
     const bool wide_store = dx->cols % 4 == 0 && dx->stride % 4 == 0 && reinterpret_cast<uintptr_t>(dx->data) % 8 == 0;
-    return launch_chained(dx_kernel, dim3(static_cast<unsigned>(dx->rows * slices)), dim3(256), 0, stream,
-                          reinterpret_cast<const float*>(ws + p.part_off), p.part_ld, dx->rows * p.part_ld,
-                          static_cast<int>(p.splits), static_cast<int>(dx->cols), static_cast<__nv_bfloat16*>(dx->data),
-                          dx->stride, wide_store, static_cast<int>(slices),
+    return launch_chained(dx_kernel, dim3(static_cast<unsigned>(ops_ceil_div(ops_ceil_div(dx->cols, 4) * dx->rows, 256))),
+                          dim3(256), 0, stream, reinterpret_cast<const float*>(ws + p.part_off), p.part_ld,
+                          dx->rows * p.part_ld, static_cast<int>(p.splits), static_cast<int>(dx->rows),
+                          static_cast<int>(dx->cols), static_cast<__nv_bfloat16*>(dx->data), dx->stride, wide_store,
                           reinterpret_cast<const float*>(ws + p.scalar_off));
   }
 
   cudaError_t join(float grad_scale, float* mean) {
-    return launch_chained(join_kernel, dim3(static_cast<unsigned>(ops_ceil_div(x->rows, 32))), dim3(1024), 0, stream, 
-        reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, static_cast<int>(p.groups),
+    return launch_chained(join_kernel, dim3(static_cast<unsigned>(x->rows)), dim3(kJoinThreads), 0, stream, 
+        reinterpret_cast<const float2*>(ws + p.stats_off), p.groups, static_cast<int>(p.groups),
         reinterpret_cast<float*>(ws + p.tlogit_off), targets->data, wide, ignore, w->rows,
         static_cast<int>(x->rows), static_cast<const uint16_t*>(xp), x_ld, static_cast<const uint16_t*>(wp), w_ld,
         static_cast<int>(x->cols), loss, lse, grad_scale, mean, reinterpret_cast<float*>(ws + p.scalar_off),
@@ -539,7 +548,7 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
     const MaskedRows masked = {static_cast<const uint16_t*>(c.xp), xm, c.x_ld, p.packed_ld, static_cast<int32_t>(n),
                                static_cast<int32_t>(h), h % 8 == 0};
     LST_TRY_CUDA(launch_chained(logit_grad_kernel, dim3(static_cast<unsigned>(d_blocks + copies)), dim3(256), 0, stream, q,
-                                p.piece, reinterpret_cast<const float2*>(ws + p.stats_off), p.n_pad, v0 / 128, v0,
+                                p.piece, reinterpret_cast<const float2*>(ws + p.stats_off), p.groups, v0 / 128, v0,
                                 static_cast<int>(columns), lse, reinterpret_cast<const float*>(ws + p.tlogit_off),
                                 targets->data, c.wide, ignore_index, v, blocks, static_cast<int>(d_blocks), masked),
                  who);
