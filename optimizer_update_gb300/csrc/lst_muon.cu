@@ -403,10 +403,18 @@ struct Runner {
       const int now = pair && steps - done >= 2 ? 2 : 1;
       cudaError_t err;
       if ((err = gram(at)) != cudaSuccess) return err;
-      if ((err = polynomial(1, 0)) != cudaSuccess) return err;
-      *s = 1;
-      *scale = kScaleQ;
-      if (now == 2) {
+      if (now == 2 && b.classes.back().m <= kNsChain) {  // the largest m
+        for (const Batch::Class& c : b.classes)
+          if ((err = ns_chain(reinterpret_cast<__half*>(ws + c.s_off[0]), c.m, c.lds, c.m * c.lds, c.count, stream)) != cudaSuccess)
+            return err;
+        *s = 0;
+        *scale = kScaleR;
+      } else if ((err = polynomial(1, 0)) != cudaSuccess) {
+        return err;
+      } else if (now == 1) {
+        *s = 1;
+        *scale = kScaleQ;
+      } else {
         if ((err = product(2, 1, 0, kScaleQA / (kScaleQ * kScaleA))) != cudaSuccess) return err;   // Q A
         if ((err = product(0, 2, 1, kScaleA / (kScaleQA * kScaleQ))) != cudaSuccess) return err;   // A' = (Q A) Q
         if ((err = polynomial(2, 0)) != cudaSuccess) return err;                                   // Q'

@@ -1,6 +1,7 @@
 // Newton-Schulz constants and the one-kernel form for small matrices.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -48,7 +49,12 @@ struct NsSmallCall {
 // Whether matrices of this shape run in one kernel.
 bool ns_small_fits(int64_t rows, int64_t cols);
 cudaError_t ns_small(const NsSmallItem* items, int count, const NsSmallCall& call, cudaStream_t stream);
-// Whether one of its waits ran out since the last call (synchronises).
+// For m x m Gram matrices with m at most kNsChain: what two steps make of them
+// (s <- Q' Q, stored times kScaleR; s holds A times kScaleA), `count` matrices
+// `pitch` elements apart with rows `ld` apart (a multiple of 64), on 16 bytes.
+constexpr int kNsChain = 256;
+cudaError_t ns_chain(__half* s, int64_t m, int64_t ld, int64_t pitch, int64_t count, cudaStream_t stream);
+// Whether one of these kernels' waits ran out since the last call (synchronises).
 cudaError_t ns_small_take_error(int* out);
 
 }  // namespace lst

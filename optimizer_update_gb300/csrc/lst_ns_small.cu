@@ -455,6 +455,164 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   }
 }
 
+// ---- two steps of a Gram matrix of up to 256 rows -------------------------------------
+// The five products between A and Q' Q of one matrix, by a CTA pair with the
+// matrices in shared memory: CTA r holds rows 128 r .. 128 r + 127, which are its
+// rows of every first factor and, all being symmetric, its half of every second
+// one. As five launches of the tiled kernel they cost 5 us each whatever their size.
+constexpr int kHalf = 4 * kChunk;  // bytes of 128 rows x 256 columns
+constexpr int kChainSmem = 3 * kHalf + 1024 + 64;
+
+struct Chain {
+  uint32_t s0, s1, s2, ready, bar, tmem, parity;
+  int rank, warp, lane, row, quarter, depth;
+  bool ok;
+
+  __device__ __forceinline__ void product(uint32_t out, uint32_t a, uint32_t b, float alpha, float beta, float diag) {
+    tc::fence_async_proxy_cta();
+    tc::fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) tc::mbar_arrive_cluster(tc::map_to_rank(ready, 0));
+    if (warp == 0) {
+      __syncwarp();
+      if (rank == 0) {
+        ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(ready, parity));
+        tc::fence_async_proxy();
+        tc::fence_after();
+        if (ok && tc::elect_one()) {
+          constexpr uint32_t idesc = tc::instr_desc(256, 256, false, false, false);
+#pragma unroll 1
+          for (int k = 0; k < depth / 16; ++k) {
+            const uint32_t off = (k >> 2) * kChunk + (k & 3) * 32;
+            tc::mma_f16_pair(tmem, tc::smem_desc(a + off, false), tc::smem_desc(b + off, false), idesc, k != 0);
+          }
+          tc::mma_commit_pair(bar);
+        }
+        __syncwarp();
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(bar, parity));
+    parity ^= 1;
+    tc::fence_after();
+    __syncwarp();
+    const int row_global = 128 * rank + row;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      const int col0 = quarter * 64 + j * 16;
+      if (col0 >= depth) break;
+      float v[16];
+      tc::tmem_ld16(tmem + (static_cast<uint32_t>(row & ~31) << 16) + col0, v);
+      const uint32_t at0 = quarter * kChunk + chunk_at(row, j * 16), at1 = quarter * kChunk + chunk_at(row, j * 16 + 8);
+      const uint4 y0 = ld_shared_v4(a + at0), y1 = ld_shared_v4(a + at1);
+      const uint32_t y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+      tc::tmem_ld_wait();
+      const int at_diag = row_global - col0;
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[i]));
+        w[i] = half2_bits(__fmaf_rn(beta, f.x, v[2 * i] * alpha) + (at_diag == 2 * i ? diag : 0.0f),
+                          __fmaf_rn(beta, f.y, v[2 * i + 1] * alpha) + (at_diag == 2 * i + 1 ? diag : 0.0f));
+      }
+      st_shared_v4(out + at0, w[0], w[1], w[2], w[3]);
+      st_shared_v4(out + at1, w[4], w[5], w[6], w[7]);
+    }
+  }
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1)
+    ns_chain_kernel(__half* s, int m, int64_t ld, int64_t pitch) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
+  Chain k;
+  k.s0 = base;
+  k.s1 = base + kHalf;
+  k.s2 = base + 2 * kHalf;
+  k.ready = base + 3 * kHalf;
+  k.bar = k.ready + 8;
+  const uint32_t slot = k.bar + 8;
+  k.warp = threadIdx.x >> 5;
+  k.lane = threadIdx.x & 31;
+  k.row = 32 * (k.warp & 3) + k.lane;
+  k.quarter = k.warp >> 2;
+  k.rank = static_cast<int>(tc::cluster_rank());
+  k.depth = (m + 15) & ~15;
+  k.parity = 0;
+  k.ok = true;
+  let_next_start();
+  if (threadIdx.x == 0) {
+    tc::mbar_init(k.ready, 2);
+    tc::mbar_init(k.bar, 1);
+    tc::mbar_init_fence();
+  }
+  if (k.warp == 1) {
+    __syncwarp();
+    tc::tmem_alloc_pair(slot, 256);
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after();
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(k.tmem) : "r"(slot));
+  wait_for_previous();
+
+  // 128 rows x 32 pieces of 16 bytes; what lies beyond m is zero
+  __half* const mine = s + static_cast<int64_t>(blockIdx.x >> 1) * pitch;
+  const int piece = k.lane;
+  uint4 v[kM / kSmallWarps];
+#pragma unroll
+  for (int i = 0; i < kM / kSmallWarps; ++i) {
+    const int r = 128 * k.rank + k.warp + i * kSmallWarps;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r < m && 8 * piece < m) {
+      v[i] = *reinterpret_cast<const uint4*>(mine + r * ld + 8 * piece);
+      uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      if (8 * piece + 8 > m)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (8 * piece + e >= m) w[e >> 1] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+      v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kM / kSmallWarps; ++i)
+    st_shared_v4(k.s0 + (piece >> 3) * kChunk + chunk_at(k.warp + i * kSmallWarps, (piece & 7) * 8), v[i].x, v[i].y, v[i].z, v[i].w);
+
+  // Q = s1 from A = s0, Q A = s2, A' = s0, Q' = s2, Q' Q = s0
+#pragma unroll 1
+  for (int op = 0; op < 5; ++op) {
+    const bool poly = op == 0 || op == 3;
+    const uint32_t out = op == 0 ? k.s1 : op == 1 || op == 3 ? k.s2 : k.s0;
+    const uint32_t a = poly ? k.s0 : op == 1 ? k.s1 : k.s2;
+    const uint32_t b = poly || op == 1 ? k.s0 : k.s1;
+    const float alpha = poly      ? kNsC * kScaleQ / (kScaleA * kScaleA)
+                        : op == 1 ? kScaleQA / (kScaleQ * kScaleA)
+                        : op == 2 ? kScaleA / (kScaleQA * kScaleQ)
+                                  : kScaleR / (kScaleQ * kScaleQ);
+    k.product(out, a, b, alpha, poly ? kNsB * kScaleQ / kScaleA : 0.0f, poly ? kNsA * kScaleQ : 0.0f);
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int i = 0; i < kM / kSmallWarps; ++i) {
+    const int r = k.warp + i * kSmallWarps, row = 128 * k.rank + r;
+    if (row < m && 8 * piece < m) {  // ld is a multiple of 64: a last piece may reach past m
+      const uint4 w = ld_shared_v4(k.s0 + (piece >> 3) * kChunk + chunk_at(r, (piece & 7) * 8));
+      *reinterpret_cast<uint4*>(mine + row * ld + 8 * piece) = w;
+    }
+  }
+  if (!k.ok) {
+    atomicExch(&g_ns_small_error, 1);
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);  // products in flight land
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::cluster_sync();
+  if (k.warp == 1) {
+    __syncwarp();
+    tc::tmem_free_pair(k.tmem, 256);
+  }
+}
+
 }  // namespace
 
 bool ns_small_fits(int64_t rows, int64_t cols) {
@@ -506,6 +664,17 @@ cudaError_t ns_small(const NsSmallItem* items, int count, const NsSmallCall& cal
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
+}
+
+cudaError_t ns_chain(__half* s, int64_t m, int64_t ld, int64_t pitch, int64_t count, cudaStream_t stream) {
+  // per device, host only, under a microsecond
+  cudaError_t err = cudaFuncSetAttribute(ns_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kChainSmem);
+  for (int64_t first = 0; err == cudaSuccess && first < count; first += 1 << 20) {
+    const int64_t now = std::min<int64_t>(count - first, 1 << 20);
+    err = launch_chained(ns_chain_kernel, dim3(static_cast<unsigned>(2 * now)), dim3(kSmallThreads), kChainSmem, stream,
+                         s + first * pitch, static_cast<int>(m), ld, pitch);
+  }
+  return err;
 }
 
 cudaError_t ns_small_take_error(int* out) {
