@@ -108,7 +108,7 @@ __device__ __forceinline__ int64_t token_at(const void* t, int wide, int64_t i) 
 // A warp takes 256 columns of a row at a time, and two such pieces at once; the
 // CTAs of a launch walk the output from start to end. (A persistent grid whose
 // warps took pieces a grid apart wrote all over the output at once: 281 us for
-// 65536 x 4096 bf16, against PIECES2.)
+// 65536 x 4096 bf16, against 144. Four pieces at once: 198.)
 constexpr int kPieces = 2;
 
 template <class TI, class TO, bool VEC>
