@@ -32,10 +32,6 @@ namespace {
 // ones, otherwise every THREADS-th, so that a warp's accesses stay consecutive.
 // `p` is the row at the group's first column, `left` the columns from there on.
 template <bool VEC, int THREADS>
-__device__ __forceinline__ int column_of(int thread, int i) {
-  return VEC ? thread * 8 + i : thread + i * THREADS;
-}
-template <bool VEC, int THREADS>
 __device__ __forceinline__ void load8(const float* p, int thread, int left, float (&v)[8]) {
   if (VEC) {
     const float4* q = reinterpret_cast<const float4*>(p) + 2 * thread;

@@ -10,9 +10,9 @@
 //   warp 1     one thread of the leading CTA issues the MMAs,
 //   warps 2-9  take finished accumulators from tensor memory: two warps per 32
 //              rows, one for each half of the tile's columns.
-// Two accumulators alternate, so the epilogue of a tile runs under the main
-// loop of the next. Tiles are dealt to the pairs in a fixed
-// order: every result is formed by one pair in one order of additions.
+// Two accumulators alternate, so the epilogue of a tile runs under the main loop
+// of the next. Tiles are dealt to the pairs in a fixed order: every result is
+// formed by one pair in one order of additions.
 // Products that have fewer tiles than the GPU has pairs run with tiles of 256 x
 // 128: twice the pairs at work, half the time to a tile's end.
 #include "lst_gemm.h"
@@ -104,8 +104,8 @@ __device__ __forceinline__ Tile decode(const Args<Epi>& g, int t) {
 
 // ---- epilogues ---------------------------------------------------------------
 // Each warp calls run() with its accumulator address (32 lanes = 32 rows, kCols
-// = half a tile's columns); prepare() runs before the tile is complete. `release` must be called once, by all lanes, when the accumulator
-// has been read.
+// = half a tile's columns); prepare() runs before the tile is complete. `release`
+// must be called once, by all lanes, when the accumulator has been read.
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool bf16) {
   if (bf16) {
