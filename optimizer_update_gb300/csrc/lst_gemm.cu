@@ -452,7 +452,7 @@ struct GradEpilogue {
 // gradient) q = (M - l) * 2^11 in 16 bits. q keeps l to 2^-12 over the 32
 // below M, where rounding l itself to bf16 would keep a logit of 16 only to
 // 2^-5; an entry further below (a probability under 1e-14 of its group's
-// largest) saturates.
+// largest, or zero at a logit of -inf) saturates and counts as zero.
 struct XentEpilogue {
   template <int kCols, class... Rest>
   static __device__ __forceinline__ void prepare(const Rest&...) {}
@@ -484,7 +484,7 @@ struct XentEpilogue {
     }
     const bool inside = row < s.m;
     int target = -1;
-    if (inside) {
+    if (inside && e.targets) {
       int64_t t64 = e.index_bytes == 8 ? static_cast<const int64_t*>(e.targets)[row] : static_cast<const int32_t*>(e.targets)[row];
       t64 -= e.first_column + col0;
       if (t64 >= 0 && t64 < left) target = static_cast<int>(t64);

@@ -57,7 +57,7 @@ struct PartialParams {
 // Logits of tokens (rows) against a piece of the vocabulary (columns), reduced
 // on the spot; see lst_xent.cu.
 struct XentParams {
-  const void* targets;
+  const void* targets;  // null: leave target_logit
   float2* stats;    // [row][128-column group]: (max, sum of exp(l - max))
   float* target_logit;
   int32_t* counter; // set to 0

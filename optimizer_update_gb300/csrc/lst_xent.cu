@@ -59,7 +59,8 @@ __device__ __forceinline__ int64_t target_at(const void* t, int wide, int64_t i)
 // cores' sums round towards zero, by up to 1e-5 for a logit of 10, and unlike the
 // errors of the other logits this one does not average out of the loss. With
 // delta = (dot product - tensor-core logit), lse moves by p delta to first order,
-// so that a certain target (p = 1) keeps a loss of zero.
+// so that a certain target (p = 1) keeps a loss of zero. A target at -inf (p = 0)
+// has no delta: its loss is inf, its row's lse and gradient stay finite.
 // With `mean`, the last block to finish also forms the mean loss and g =
 // grad_scale / N from all losses, in a fixed order.
 constexpr int kJoinThreads = 256;
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kJoinThreads)
       float l = (top == ninf ? 0.0f : top) + logf(sum);
       if (with_target) {
         const float old = target_logit[r], delta = dot - old;
-        l += delta * exp2_approx((old - l) * kLog2e);
+        if (fabsf(delta) <= 3.402823466e38f) l += delta * exp2_approx((old - l) * kLog2e);
         target_logit[r] = dot;
       }
       lse[r] = l;
@@ -249,7 +250,8 @@ __global__ void __launch_bounds__(256)
   float d[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float steps = static_cast<float>((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+    const uint32_t q16 = (w[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+    const float steps = q16 == 0xffffu ? __int_as_float(0x7f800000) : static_cast<float>(q16);
     d[i] = exp2_approx(__fmaf_rn(steps, -kLog2e / 2048.0f, base));
   }
   const int64_t at = t - first_column - col;
@@ -431,7 +433,8 @@ struct Call {
     g.m = x->rows;
     g.n = columns;
     g.k = x->cols;
-    g.xent = {targets->data, reinterpret_cast<float2*>(ws + p.stats_off), reinterpret_cast<float*>(ws + p.tlogit_off),
+    // pieces formed again leave the target logits: they hold fp32 dot products by then
+    g.xent = {v0 > 0 && keep ? nullptr : targets->data, reinterpret_cast<float2*>(ws + p.stats_off), reinterpret_cast<float*>(ws + p.tlogit_off),
               reinterpret_cast<int32_t*>(ws + p.scalar_off) + 1, keep ? reinterpret_cast<uint16_t*>(ws + p.q_off) : nullptr, p.piece, p.groups, v0 / 128, v0,
               targets->bits / 8};
     return launch_gemm(GEMM_BF16_XENT, &g, 1, stream);

@@ -367,6 +367,39 @@ def test_xent_non_finite_rows_stay_in_their_rows():
     assert torch.isnan(r["dx"][~ok]).any(1).all() and not torch.isnan(xent_call(x, w, t, grad=False)["loss"][ok]).any()
 
 
+@pytest.mark.parametrize("pieces", [1, 2])
+def test_xent_logits_of_minus_infinity(pieces):
+    """A vocabulary row whose logits pass below the type's range: probability 0, gradient 0 except where it is the target."""
+    n, hidden, vocab, gone = 40, 64, 300, 7
+    x, w, t = xent_inputs(n, hidden, vocab, seed=17, ignored=0.0)
+    x = x.abs() + 0.5
+    others = torch.arange(vocab, device="cuda") != gone
+    t = torch.where(t == gone, gone + 1, t)
+    e = xent_exact(x, w[others], t - (t > gone).long())
+    w[gone] = torch.finfo(torch.bfloat16).min
+    t[0] = gone
+    scale = 1.0 / n
+    z = x.double() @ w[others].double().T
+    d = torch.zeros(n, vocab, dtype=torch.float64, device="cuda")
+    d[:, others] = torch.softmax(z, 1) * scale
+    d[torch.arange(n), t] -= scale
+    dd = torch.zeros_like(d)
+    dd[:, others] = e["dd"]
+    dd[torch.arange(n), t] += U16 * scale
+    dx, dw = d @ w.double(), d.T @ x.double()
+    bx = dd @ w.double().abs() + 2 * vocab * U32 * (d.abs() @ w.double().abs())
+    bw = dd.T @ x.double().abs() + 2 * n * U32 * (d.abs().T @ x.double().abs())
+    size = lst.lst_xent_workspace_bytes(n, hidden, vocab, True)
+    r = xent_call(x, w, t, ws_bytes=size if pieces == 1 else size - 1)
+    assert torch.isinf(r["loss"][0]) and float(r["mean"]) == math.inf
+    within(r["lse"], e["lse"], e["dlse"], "lse")
+    within(r["loss"][1:], e["loss"][1:], e["dloss"][1:], "loss")
+    within(r["dx"], dx, bx + U16 * (dx.abs() + bx), "dx")
+    within(r["dw"], dw, bw + U16 * (dw.abs() + bw), "dw")
+    only = xent_call(x, w, t, grad=False)
+    assert torch.equal(only["loss"], r["loss"]) and torch.equal(only["lse"], r["lse"])
+
+
 def test_xent_scale_and_accumulate():
     n, hidden, vocab = 200, 104, 900
     x, w, t = xent_inputs(n, hidden, vocab, seed=13)
