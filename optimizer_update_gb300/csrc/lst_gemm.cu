@@ -159,7 +159,6 @@ struct StoreEpilogue {
   static __device__ __forceinline__ void prepare(const Rest&...) {}
   using Params = StoreParams;
   using Table = Nothing;
-  static __device__ __forceinline__ void begin(const Params&) {}
   // Rows that are not on 16 bytes (a caller's matrix: not symmetric, no diagonal).
   template <int kCols>
   static __device__ __forceinline__ void turned(const Params& e, const Shape& s, const Tile& t, int row, int col0, uint32_t tmem,
@@ -294,7 +293,6 @@ struct StoreEpilogue {
 struct UpdateEpilogue {
   using Params = UpdateParams;
   using Table = UpdateTable;
-  static __device__ __forceinline__ void begin(const Params&) {}
   // The tile's weights to L2 while its main loop runs, a row's columns in one request.
   template <int kCols>
   static __device__ __forceinline__ void prepare(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
@@ -435,7 +433,6 @@ struct GradEpilogue {
   template <int kCols, class... Rest>
   static __device__ __forceinline__ void prepare(const Rest&...) {}
   using Params = GradParams;
-  static __device__ __forceinline__ void begin(const Params&) {}
   using Table = Nothing;
   template <int kCols, class Release>
   static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
@@ -458,9 +455,6 @@ struct XentEpilogue {
   static __device__ __forceinline__ void prepare(const Rest&...) {}
   using Params = XentParams;
   using Table = Nothing;
-  static __device__ __forceinline__ void begin(const Params& e) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) *e.counter = 0;
-  }
   template <int kCols, class Release>
   static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
                                              int col0, uint32_t tmem, uint32_t turn, Release release) {
@@ -484,7 +478,7 @@ struct XentEpilogue {
     }
     const bool inside = row < s.m;
     int target = -1;
-    if (inside && e.targets) {
+    if (inside) {
       int64_t t64 = e.index_bytes == 8 ? static_cast<const int64_t*>(e.targets)[row] : static_cast<const int32_t*>(e.targets)[row];
       t64 -= e.first_column + col0;
       if (t64 >= 0 && t64 < left) target = static_cast<int>(t64);
@@ -582,8 +576,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(typename Epi::Params) / 4); i += 8) asm volatile("" ::"r"(words[i]));
   wait_for_previous();
-  Epi::begin(g.epi[0]);
-
   bool ok = true;
   if (warp == 0) {
     if (tc::elect_one()) {

@@ -57,10 +57,9 @@ struct PartialParams {
 // Logits of tokens (rows) against a piece of the vocabulary (columns), reduced
 // on the spot; see lst_xent.cu.
 struct XentParams {
-  const void* targets;  // null: leave target_logit
+  const void* targets;
   float2* stats;    // [row][128-column group]: (max, sum of exp(l - max))
   float* target_logit;
-  int32_t* counter; // set to 0
   uint16_t* q;      // [row][column]: (max - l) in steps of 2^-11, or null
   int64_t q_ld, stat_ld, first_group, first_column;
   int32_t index_bytes;
