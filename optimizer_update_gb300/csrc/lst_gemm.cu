@@ -139,6 +139,29 @@ __device__ __forceinline__ void load_turned(uint32_t tmem, uint32_t turn, float 
   for (int i = 0; i < 32; ++i) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(turn + (i * 33 + lane) * 4));
 }
 
+// The same in units of kUnit = 4 or 8 consecutive columns a lane. Units of 4: v[i] is
+// columns 4 (lane % 8) .. of row 4 i + lane / 8; of 8: v[2 i] and v[2 i + 1] are
+// columns 8 (lane % 4) .. of row 8 i + lane / 4. 16-byte accesses, no bank conflicts.
+template <int kUnit>
+__device__ __forceinline__ void load_units(uint32_t tmem, uint32_t turn, float4 (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+  auto word = [&](int r, int u) { return turn + r * 128 + ((u ^ (r & 7)) << 4); };
+  float a[32];
+  __syncwarp();
+  tc::tmem_ld32(tmem, a);
+  tc::tmem_ld_wait();
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(word(lane, u)), "f"(a[4 * u]), "f"(a[4 * u + 1]),
+                 "f"(a[4 * u + 2]), "f"(a[4 * u + 3]));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t from = kUnit == 4 ? word(4 * i + (lane >> 3), lane & 7) : word(8 * (i >> 1) + (lane >> 2), 2 * (lane & 3) + (i & 1));
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v[i].x), "=f"(v[i].y), "=f"(v[i].z), "=f"(v[i].w) : "r"(from));
+  }
+}
+
 // The first `left` < 8 values of 8.
 __device__ __forceinline__ uint4 load_tail(const uint16_t* p, int left) {
   uint32_t w[4] = {0, 0, 0, 0};
@@ -302,44 +325,59 @@ struct UpdateEpilogue {
     const char* w = static_cast<const char*>(table.w[e.first + t.batch]) + (static_cast<int64_t>(row) * e.ld + col0) * size;
     if (bytes > 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(w), "r"(bytes) : "memory");
   }
-  // Either a row of fp32 weights per lane, 64 bytes at a time, or the lanes along
-  // the columns. The last product of a TinyLlama layer by the two, at 97 us of
-  // MMA: mixed layout 181 and 205 us, fp32 157 and 182, 12 B layout 305 and 183
-  // (32 bytes of each of 32 rows do not get through L1 in time). So bf16 weights
-  // and rows that are not on 16 bytes take the second way.
-  template <int kCols>
-  static __device__ __forceinline__ void rows(const Params& e, float step, float* w, uint16_t* w16, bool inside, int columns,
-                                              uint32_t tmem) {
-    float4 next[4];
-    if (inside)
+  // Rows on 16 bytes: 32 columns of 32 rows at a time, 16 bytes a lane, whole rows
+  // (128 bytes of fp32, 64 of bf16) an instruction. UPDATE_FIGS
+  template <bool kBf16, int kCols>
+  static __device__ __forceinline__ void units(const Params& e, float step, char* w, uint16_t* w16, int rows, int left,
+                                               uint32_t tmem, uint32_t turn) {
+    constexpr int kUnit = kBf16 ? 8 : 4, kAcross = 32 / kUnit, kDown = 32 / kAcross, kLoads = 32 / kDown;
+    constexpr int kSize = kBf16 ? 2 : 4, kAhead = kBf16 ? 2 : 1, kGroups = kCols / 32;
+    const int lane = threadIdx.x & 31, r0 = lane / kAcross, c0 = kUnit * (lane % kAcross);
+    const int64_t at = r0 * e.ld + c0, down = kDown * e.ld;  // elements
+    uint4 next[kAhead][kLoads];
+    auto fetch = [&](uint4 (&x)[kLoads], int g) {
+      if (g >= kGroups || 32 * g + c0 >= left) return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (4 * i < columns) next[i] = reinterpret_cast<const float4*>(w)[i];
+      for (int i = 0; i < kLoads; ++i)
+        if (kDown * i + r0 < rows) x[i] = __ldcg(reinterpret_cast<const uint4*>(w + (at + i * down + 32 * g) * kSize));
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) fetch(next[k], k);
 #pragma unroll 1
-    for (int g = 0; g < kCols / 16; ++g, w += 16, w16 += 16, columns -= 16) {
-      if (columns <= 0) break;
-      float v[16], x[16];
-      __syncwarp();
-      tc::tmem_ld16(tmem + 16 * g, v);
+    for (int g = 0; g < kGroups; ++g) {
+      if (32 * g >= left) break;
+      uint4 x[kLoads];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[4 * i] = next[i].x, x[4 * i + 1] = next[i].y, x[4 * i + 2] = next[i].z, x[4 * i + 3] = next[i].w;
-      if (inside && g + 1 < kCols / 16)
+      for (int i = 0; i < kLoads; ++i) {
+        x[i] = next[0][i];
+        if (kAhead == 2) next[0][i] = next[kAhead - 1][i];
+      }
+      fetch(next[kAhead - 1], g + kAhead);
+      float4 v[8];
+      load_units<kUnit>(tmem + 32 * g, turn, v);
+      auto updated = [&](float old, float o) { return __fsub_rn(__fmul_rn(old, e.decay), __fmul_rn(step, o)); };
+      if (32 * g + c0 >= left) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (16 + 4 * i < columns) next[i] = reinterpret_cast<const float4*>(w + 16)[i];
-      tc::tmem_ld_wait();
-      if (!inside) continue;
+      for (int i = 0; i < kLoads; ++i) {
+        if (kDown * i + r0 >= rows) break;
+        const int64_t p = at + i * down + 32 * g;
+        if (kBf16) {
+          const uint32_t o[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          const float4 lo = v[(2 * i) & 7], hi = v[(2 * i + 1) & 7];
+          const float d[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+          uint32_t n[4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fsub_rn(__fmul_rn(x[i], e.decay), __fmul_rn(step, v[i]));
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (4 * i < columns) reinterpret_cast<float4*>(w)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-      if (e.format == LST_L16_MIXED) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)  // a row's columns are a multiple of 8
-          if (8 * i < columns)
-            reinterpret_cast<uint4*>(w16)[i] = make_uint4(pack16(x[8 * i], x[8 * i + 1], true), pack16(x[8 * i + 2], x[8 * i + 3], true),
-                                                          pack16(x[8 * i + 4], x[8 * i + 5], true), pack16(x[8 * i + 6], x[8 * i + 7], true));
+          for (int j = 0; j < 4; ++j)
+            n[j] = pack16(updated(__uint_as_float(o[j] << 16), d[2 * j]), updated(__uint_as_float(o[j] & 0xffff0000u), d[2 * j + 1]), true);
+          *reinterpret_cast<uint4*>(w + p * kSize) = make_uint4(n[0], n[1], n[2], n[3]);
+        } else {
+          const float4 d = v[i];
+          const float4 n = make_float4(updated(__uint_as_float(x[i].x), d.x), updated(__uint_as_float(x[i].y), d.y),
+                                       updated(__uint_as_float(x[i].z), d.z), updated(__uint_as_float(x[i].w), d.w));
+          *reinterpret_cast<float4*>(w + p * kSize) = n;
+          if (e.format == LST_L16_MIXED)
+            *reinterpret_cast<uint2*>(w16 + p) = make_uint2(pack16(n.x, n.y, true), pack16(n.z, n.w, true));
+        }
       }
     }
   }
@@ -352,9 +390,12 @@ struct UpdateEpilogue {
     const int64_t first = static_cast<int64_t>(row0) * e.ld + col0 + lane;
     char* const weights = static_cast<char*>(table.w[e.first + t.batch]);
     uint16_t* const w16 = bf16 ? reinterpret_cast<uint16_t*>(weights) : table.w16[e.first + t.batch];
-    if (!bf16 && e.vec >= 16) {
-      const int64_t at = static_cast<int64_t>(row) * e.ld + col0;
-      UpdateEpilogue::rows<kCols>(e, step, reinterpret_cast<float*>(weights) + at, w16 + at, row < s.m, s.n - col0, tmem);
+    if (e.vec >= 16) {
+      const int64_t at = static_cast<int64_t>(row0) * e.ld + col0;
+      if (bf16)
+        units<true, kCols>(e, step, weights + at * 2, w16, rows, s.n - col0, tmem, turn);
+      else
+        units<false, kCols>(e, step, weights + at * 4, w16 + at, rows, s.n - col0, tmem, turn);
       __syncwarp();
       release();
       return;
@@ -403,22 +444,28 @@ struct UpdateEpilogue {
 struct PartialEpilogue {
   using Params = PartialParams;
   using Table = Nothing;
+  // Rows of `out` hold whole units of 4 columns: ld is a multiple of 4.
   template <int kCols, class Release>
   static __device__ __forceinline__ void run(const Params& e, const Table&, const Shape& s, const Tile& t, int row,
                                              int col0, uint32_t tmem, uint32_t turn, Release release) {
-    const int lane = row & 31, row0 = row & ~31, rows = s.m - row0;
-    float* const out = e.out + t.split * e.split_stride + static_cast<int64_t>(row0) * e.ld + col0 + lane;
+    const int lane = row & 31, row0 = row & ~31, rows = s.m - row0, r0 = lane >> 3, c0 = 4 * (lane & 7);
+    float* const out = e.out + t.split * e.split_stride + static_cast<int64_t>(row0 + r0) * e.ld + col0 + c0;
 #pragma unroll 1
     for (int g = 0; g < kCols / 32; ++g) {
       if (col0 + 32 * g >= s.n) break;
-      const bool inside = col0 + 32 * g + lane < s.n;
-      float v[32];
-      load_turned(tmem + 32 * g, turn, v);
+      const bool inside = col0 + 32 * g + c0 < s.n;
+      float4 old[8] = {}, v[8];
+      if (e.accumulate) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float* p = out + i * e.ld + 32 * g;
-        if (inside && i < rows) *p = e.accumulate ? *p + v[i] : v[i];
+        for (int i = 0; i < 8; ++i)
+          if (inside && 4 * i + r0 < rows) old[i] = *reinterpret_cast<const float4*>(out + 4 * i * e.ld + 32 * g);
       }
+      load_units<4>(tmem + 32 * g, turn, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (inside && 4 * i + r0 < rows)
+          *reinterpret_cast<float4*>(out + 4 * i * e.ld + 32 * g) =
+              make_float4(old[i].x + v[i].x, old[i].y + v[i].y, old[i].z + v[i].z, old[i].w + v[i].w);
     }
     __syncwarp();
     release();
