@@ -281,6 +281,13 @@ def test_xent(n, hidden, vocab):
     assert all(torch.equal(again[k], r[k]) for k in r)
 
 
+@pytest.mark.parametrize("n,hidden,vocab", [(700, 264, 7001), (700, 1000, 3500)])
+def test_xent_more_tiles_than_pairs(n, hidden, vocab):
+    """84 tiles of logits, and 112 or 56 of dw with those of dx: a second wave of few tiles, which are formed in halves."""
+    x, w, t = xent_inputs(n, hidden, vocab, seed=42)
+    xent_check(xent_call(x, w, t), xent_exact(x, w, t))
+
+
 @pytest.mark.parametrize("hidden,pad,shift", [(77, 0, 0), (1, 0, 0), (64, 3, 0), (64, 0, 1), (72, 8, 4), (63, 1, 0), (130, 6, 2)])
 def test_xent_strides_and_odd_rows(hidden, pad, shift):
     """Rows that do not start on 16 bytes, padded rows, bases off 16 bytes."""
@@ -519,6 +526,14 @@ def test_orthogonalize_batches_and_strides(count, rows, cols):
         assert all(torch.equal(a, o) for a, o in zip(again, outs))
 
 
+@pytest.mark.parametrize("rows,cols", [(1300, 1700), (1703, 1301)])
+def test_orthogonalize_more_tiles_than_pairs(rows, cols):
+    """21 tiles of a symmetric product and 42 of X by four: a second wave of few tiles, which are formed in halves."""
+    xs = [matrix_like(gen(40 + i), rows, cols).bfloat16() for i in range(4)]
+    for x, o in zip(xs, ns_call(xs)):
+        assert rel(o, ns_exact(x)) <= NS_TOL
+
+
 def test_orthogonalize_zero_tiny_large_and_non_finite():
     g = gen(20)
     good = matrix_like(g, 100, 130)
@@ -626,6 +641,42 @@ def test_muon_step(fmt, nesterov, rms_scale, steps):
         for f in FMT_FIELDS[fmt]:
             assert not got[f][~covered].any(), f                              # padding stays zero
         assert (backing[b][:4096] == 0xA5).all() and (backing[b][-4096:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("fmt", ["L12", "L16M", "L16F"])
+def test_muon_step_more_tiles_than_pairs(fmt):
+    """Matrices of one long side and of two, so that launches hold sums of different lengths and a wave of half tiles."""
+    shapes = [(1304, 1304), (1704, 1304), (1304, 1704), (1304, 1701)]
+    layout = Layout([(f"m{i}", s, 0) for i, s in enumerate(shapes)], fmt)
+    blk = torch.zeros(layout.block_bytes(0), dtype=torch.uint8, device="cuda")
+    v = muon_views(layout, fmt, 0, blk)
+    spans = list(layout.spans(0))
+    field = "MASTER" if fmt == "L16M" else "W"
+    g = gen(41)
+    for (_, off, n), shape in zip(spans, shapes):
+        v[field][off:off + n] = torch.randn(n, generator=g, device="cuda") * 0.02
+        v["G"][off:off + n] = matrix_like(g, *shape).reshape(-1)
+        v["M"][off:off + n] = matrix_like(g, *shape).reshape(-1)
+    old = {f: x.clone() for f, x in v.items()}
+    ws = scratch(lst.lst_muon_workspace_bytes(layout.handle))
+    hp = lst.muon_hparams(lr=2e-2, momentum=0.9, weight_decay=0.1, rms_scale=0.2, nesterov=True)
+    lst.lst_muon_step(layout.handle, [blk.data_ptr()], hp, None, None, ws.data_ptr(), ws.numel(), stream())
+    lst.lst_operator_status()
+    covered = torch.zeros(layout.padded(0), dtype=torch.bool, device="cuda")
+    for (name, off, n), shape in zip(spans, shapes):
+        s = slice(off, off + n)
+        covered[s] = True
+        m = (old["M"][s] * np.float32(0.9)) + old["G"][s].float()
+        assert torch.equal(v["M"][s], m), name
+        o = ns_exact((old["G"][s].double() + float(np.float32(0.9)) * m.double()).view(shape)).reshape(-1)
+        scale, w0 = 0.2 * math.sqrt(max(shape)), old[field][s].double()
+        w = w0 * (1 - 2e-2 * 0.1) - 2e-2 * scale * o
+        limit = NS_TOL * 2e-2 * scale * o.norm() + (4 * U32 * (w0.norm() + w.norm())) + (U16 * w.norm() if fmt == "L12" else 0.0)
+        err = (v[field][s].double() - w).norm()
+        assert float(err) <= float(limit), (name, float(err), float(limit))
+        if fmt == "L16M":
+            assert torch.equal(v["W"][s], v["MASTER"][s].bfloat16())
+    assert not v["M"][~covered].any() and not v[field][~covered].any()
 
 
 def test_muon_mask_and_no_adamw():
