@@ -583,6 +583,75 @@ struct XentEpilogue {
   }
 };
 
+// The same for few tokens, with the vocabulary in the rows and the tokens in the
+// columns: a tile is 256 x 32 or 256 x 64, so that the MMAs of 16 tokens take an
+// eighth of the time and the launch is bound by reading w. Per token and 32
+// vocabulary entries, 16 tokens at a time: a lane takes 16 entries of a token, the
+// other 16 are its partner's (lane ^ 16).
+struct XentFewEpilogue {
+  template <int kCols, class... Rest>
+  static __device__ __forceinline__ void prepare(const Rest&...) {}
+  using Params = XentParams;
+  using Table = Nothing;
+  template <int kCols, class Release>
+  static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
+                                             int col0, uint32_t tmem, uint32_t turn, Release release) {
+    const int lane = row & 31, row0 = row & ~31, left = s.m - row0, first = lane & 16;
+    if (left <= 0 || col0 >= s.n) {
+      release();
+      return;
+    }
+    const float ninf = __int_as_float(0xff800000);
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 16) {
+      float v[16];
+      __syncwarp();
+      tc::tmem_ld16(tmem + c, v);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) asm volatile("st.shared.f32 [%0], %1;" ::"r"(turn + (lane * 17 + i) * 4), "f"(v[i]));
+      __syncwarp();
+      if (c + 16 == kCols) release();
+      const int token = col0 + c + (lane & 15);
+      float top = ninf;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(turn + ((first + i) * 17 + (lane & 15)) * 4));
+        if (first + i >= left) v[i] = ninf;
+        top = fmaxf(top, v[i]);
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      const float base = top == ninf ? 0.0f : top;  // as above
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum += tc::exp2_approx((v[i] - base) * 1.4426950408889634f);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      if (token >= s.n) continue;
+      if (e.q) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float lo = fminf((top - v[2 * i]) * 2048.0f, 65535.0f);
+          const float hi = fminf((top - v[2 * i + 1]) * 2048.0f, 65535.0f);
+          w[i] = __float2uint_rn(lo) | (__float2uint_rn(hi) << 16);
+        }
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(e.q + token * e.q_ld + row0 + first), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+      }
+      if (first == 0) e.stats[token * e.stat_ld + e.first_group + (row0 >> 5)] = make_float2(top, sum);
+      int64_t at = e.index_bytes == 8 ? static_cast<const int64_t*>(e.targets)[token] : static_cast<const int32_t*>(e.targets)[token];
+      at -= e.first_column + row0 + first;
+      if (at >= 0 && at < 16 && at < left - first) {
+        float logit = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) logit = i == static_cast<int>(at) ? v[i] : logit;
+        e.target_logit[token] = logit;
+      }
+    }
+  }
+};
+
 // ---- the kernel ----------------------------------------------------------------
 template <class Epi, bool kBf16, int kTileN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -907,6 +976,9 @@ cudaError_t launch_gemm(GemmKind kind, const GemmProblem* p, int count, cudaStre
     case GEMM_F16_UPDATE: return launch_fit<UpdateEpilogue, false>(p, count, stream, updates);
     case GEMM_BF16: return launch_fit<GradEpilogue, true>(p, count, stream, nullptr);
     case GEMM_BF16_XENT: return launch<XentEpilogue, true, 256>(p, count, stream, nullptr);
+    case GEMM_BF16_XENT_FEW:
+      return p->n <= 32 ? launch<XentFewEpilogue, true, 32>(p, count, stream, nullptr)
+                        : launch<XentFewEpilogue, true, 64>(p, count, stream, nullptr);
   }
   return cudaErrorInvalidValue;
 }

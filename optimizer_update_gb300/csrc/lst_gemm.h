@@ -54,13 +54,13 @@ struct PartialParams {
   int32_t accumulate;
 };
 
-// Logits of tokens (rows) against a piece of the vocabulary (columns), reduced
-// on the spot; see lst_xent.cu.
+// Logits of tokens (rows) against a piece of the vocabulary (columns; the other
+// way round for GEMM_BF16_XENT_FEW), reduced on the spot; see lst_xent.cu.
 struct XentParams {
   const void* targets;
-  float2* stats;    // [row][128-column group]: (max, sum of exp(l - max))
+  float2* stats;    // [token][group of 128, or 32]: (max, sum of exp(l - max))
   float* target_logit;
-  uint16_t* q;      // [row][column]: (max - l) in steps of 2^-11, or null
+  uint16_t* q;      // [token][entry]: (max - l) in steps of 2^-11, or null
   int64_t q_ld, stat_ld, first_group, first_column;
   int32_t index_bytes;
 };
@@ -70,6 +70,7 @@ enum GemmKind {
   GEMM_F16_UPDATE,  // fp16 operands, UpdateParams
   GEMM_BF16,        // bf16 operands, StoreParams or PartialParams
   GEMM_BF16_XENT,   // bf16 operands, XentParams
+  GEMM_BF16_XENT_FEW,
 };
 
 struct GemmProblem {

@@ -6,7 +6,8 @@
 // the logits is d_iv = g (p_iv - [v = t_i]), and dx = d w, dw = d^T x.
 //
 // Order. Logits are formed 256 x 256 at a time on the tensor cores
-// (lst_gemm.cu); a tile leaves, for each row and 128 columns, the maximum M
+// (lst_gemm.cu); a tile leaves, for each row and 128 columns (32 where few tokens
+// are the columns of the tiles), the maximum M
 // and the sum of exp(l - M), from which a second kernel joins lse. For the
 // gradient the tile also leaves (M - l) in 16 bits of fixed point, steps of
 // 2^-11: the workspace holds as many columns of those ("a piece") as fit, and
@@ -25,7 +26,8 @@
 // split, and partial sums are added in a fixed order in fp32, which also
 // carries them over the pieces.
 //
-// Bound by the tensor cores from about 300 tokens on; below by reading w.
+// Bound by the tensor cores from about 300 tokens on; below by reading w, for which
+// few tokens have a form of their own (kFewTokens).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -40,6 +42,10 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int64_t kMaxPieceBytes = int64_t(1) << 30;
+// Up to these the logits are formed with the tokens as the columns of narrow tiles:
+// the loss over w of 32000 x 2048 takes 28 us for 16 tokens and 29 for 64, with tiles
+// of 256 x 256 36 and 31 (but 32 for 128 tokens, where two narrow tiles take 40).
+constexpr int64_t kFewTokens = 64;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -51,7 +57,7 @@ __device__ __forceinline__ int64_t target_at(const void* t, int wide, int64_t i)
   return wide ? static_cast<const int64_t*>(t)[i] : static_cast<const int32_t*>(t)[i];
 }
 
-// lse and loss of a row from the statistics of its 128-column groups, a block per
+// lse and loss of a row from the statistics of its groups of columns, a block per
 // row: short chains of dependent loads, and short code.
 // The target's logit is formed again as a plain fp32 dot product: the tensor
 // cores' sums round towards zero, by up to 1e-5 for a logit of 10, and unlike the
@@ -202,7 +208,7 @@ struct MaskedRows {
 // them forms the mean loss and g.
 __global__ void __launch_bounds__(256)
     logit_grad_kernel(uint16_t* __restrict__ q, int64_t q_ld, const float2* __restrict__ stats, int64_t stat_ld,
-                      int64_t first_group, int64_t first_column, int columns, const float* __restrict__ lse,
+                      int64_t first_group, int group_shift, int64_t first_column, int columns, const float* __restrict__ lse,
                       const float* __restrict__ loss, const void* __restrict__ targets, int wide,
                       int64_t ignore, int64_t vocab, int blocks_per_row, int d_blocks,
                       MaskedRows x, float grad_scale, float* __restrict__ mean, float* __restrict__ g) {
@@ -236,7 +242,7 @@ __global__ void __launch_bounds__(256)
   }
   const uint4 x0 = p[0], x1 = p[1];
   const float l = lse[row];
-  const float top = stats[row * stat_ld + first_group + (col >> 7)].x;
+  const float top = stats[row * stat_ld + first_group + (col >> group_shift)].x;
   const float base = (top - l) * kLog2e;
   const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
   float d[16];
@@ -313,6 +319,7 @@ bool tile_ready(const lst_matrix* m) {
 
 struct Plan {
   int64_t groups, piece, pieces, splits;
+  int group_shift;  // log2 of the vocabulary entries of a group of statistics
   int64_t packed_ld, x_ld, part_ld;
   int64_t scalar_off, tlogit_off, stats_off, xm_off, xpack_off, wpack_off, part_off, q_off;
   int64_t fixed;  // bytes before the pieces
@@ -322,7 +329,8 @@ struct Plan {
 // Layout of the workspace; `bytes` < 0: for one piece, at most 1 GiB of it.
 // Returns false when not even one tile of columns fits.
 bool make_plan(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool pack_w, int64_t bytes, Plan* p) {
-  p->groups = ops_ceil_div(v, 128);
+  p->group_shift = n <= kFewTokens ? 5 : 7;
+  p->groups = ops_ceil_div(v, int64_t(1) << p->group_shift);
   p->packed_ld = ops_round_up(h, 8);
   int64_t at = 0;
   auto take = [&](int64_t size) {
@@ -419,16 +427,19 @@ struct Call {
   }
 
   cudaError_t logits(int64_t v0, int64_t columns, bool keep) {
+    const GemmOperand tokens = rows_operand(xp, x->rows, x->cols, x_ld);
+    const GemmOperand entries = rows_operand(static_cast<const uint16_t*>(wp) + v0 * w_ld, columns, w->cols, w_ld);
+    const bool few = x->rows <= kFewTokens;
     GemmProblem g;
-    g.a = rows_operand(xp, x->rows, x->cols, x_ld);
-    g.b = rows_operand(static_cast<const uint16_t*>(wp) + v0 * w_ld, columns, w->cols, w_ld);
-    g.m = x->rows;
-    g.n = columns;
+    g.a = few ? entries : tokens;
+    g.b = few ? tokens : entries;
+    g.m = few ? columns : x->rows;
+    g.n = few ? x->rows : columns;
     g.k = x->cols;
     g.xent = {targets->data, reinterpret_cast<float2*>(ws + p.stats_off), reinterpret_cast<float*>(ws + p.tlogit_off),
-              keep ? reinterpret_cast<uint16_t*>(ws + p.q_off) : nullptr, p.piece, p.groups, v0 / 128, v0,
+              keep ? reinterpret_cast<uint16_t*>(ws + p.q_off) : nullptr, p.piece, p.groups, v0 >> p.group_shift, v0,
               targets->bits / 8};
-    return launch_gemm(GEMM_BF16_XENT, &g, 1, stream);
+    return launch_gemm(few ? GEMM_BF16_XENT_FEW : GEMM_BF16_XENT, &g, 1, stream);
   }
 
   cudaError_t sum_dx(const lst_matrix* dx) {
@@ -541,7 +552,7 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
     const MaskedRows masked = {static_cast<const uint16_t*>(c.xp), xm, c.x_ld, p.packed_ld, static_cast<int32_t>(n),
                                static_cast<int32_t>(h), h % 8 == 0};
     LST_TRY_CUDA(launch_chained(logit_grad_kernel, dim3(static_cast<unsigned>(d_blocks + copies)), dim3(256), 0, stream, q,
-                                p.piece, reinterpret_cast<const float2*>(ws + p.stats_off), p.groups, v0 / 128, v0,
+                                p.piece, reinterpret_cast<const float2*>(ws + p.stats_off), p.groups, v0 >> p.group_shift, p.group_shift, v0,
                                 static_cast<int>(columns), lse, loss, targets->data, c.wide, ignore_index, v, blocks, static_cast<int>(d_blocks), masked,
                                 grad_scale, mean, g),
                  who);

@@ -288,6 +288,18 @@ def test_xent_more_tiles_than_pairs(n, hidden, vocab):
     xent_check(xent_call(x, w, t), xent_exact(x, w, t))
 
 
+@pytest.mark.parametrize("n", [1, 15, 17, 32, 48, 63, 64, 65])
+def test_xent_few_tokens(n):
+    """Tokens as the columns of narrow tiles (up to 64), more tiles than pairs, a vocabulary that ends inside one."""
+    x, w, t = xent_inputs(n, 136, 40021, seed=n, ignored=0.0)
+    t[-1] = 40020
+    e = xent_exact(x, w, t)
+    r = xent_call(x, w, t)
+    xent_check(r, e)
+    only = xent_call(x, w, t, grad=False)
+    assert torch.equal(only["loss"], r["loss"]) and torch.equal(only["lse"], r["lse"])
+
+
 @pytest.mark.parametrize("hidden,pad,shift", [(77, 0, 0), (1, 0, 0), (64, 3, 0), (64, 0, 1), (72, 8, 4), (63, 1, 0), (130, 6, 2)])
 def test_xent_strides_and_odd_rows(hidden, pad, shift):
     """Rows that do not start on 16 bytes, padded rows, bases off 16 bytes."""
