@@ -82,10 +82,11 @@ __device__ __forceinline__ Tile decode(const Args<Epi>& g, int t) {
   while (p + 1 < g.count && t >= g.shape[p + 1].first_tile) ++p;
   const Shape& s = g.shape[p];
   int i = t - s.first_tile;
-  const int matrix = i / s.tiles;
+  // divisions (some 20 dependent instructions) only where they are needed
+  const int matrix = i < s.tiles ? 0 : i / s.tiles;
   i -= matrix * s.tiles;
   r.problem = p;
-  r.batch = matrix / s.splits;
+  r.batch = s.splits == 1 ? matrix : matrix / s.splits;
   r.split = matrix - r.batch * s.splits;
   if (s.symmetric) {
     constexpr int kAcross = kGemmTile / kTileN;
@@ -101,8 +102,9 @@ __device__ __forceinline__ Tile decode(const Args<Epi>& g, int t) {
     const int group = i / per_group;
     const int rows = min(8, s.tiles_m - group * 8);
     i -= group * per_group;
-    r.tm = group * 8 + i % rows;
-    r.tn = i / rows;
+    const int across = rows == 8 ? i >> 3 : i / rows;
+    r.tm = group * 8 + i - across * rows;
+    r.tn = across;
   }
   r.kb0 = r.split * s.k_per_split;
   r.kb1 = min(s.k_blocks, r.kb0 + s.k_per_split);
@@ -220,7 +222,7 @@ struct StoreEpilogue {
       }
     }
   }
-  template <int kCols, class Release>
+  template <int kCols, bool kOnlyBf16 = false, class Release>
   static __device__ __forceinline__ void run(const Params& e, const Table&, const Shape& s, const Tile& t, int row,
                                              int col0, uint32_t tmem, uint32_t turn, Release release) {
     if (e.vec < 16) {
@@ -232,7 +234,7 @@ struct StoreEpilogue {
     // 64 columns at a time through the warp's words, row by row in, four whole
     // 128-byte rows an instruction out: a lane per row would touch 32 lines with
     // every store (five symmetric products of 2048: 41.2 us that way, 36.6 so).
-    const bool bf16 = e.bf16 != 0;
+    const bool bf16 = kOnlyBf16 || e.bf16 != 0;
     const float alpha = e.scale ? e.alpha * *e.scale : e.alpha;
     constexpr int kAcross = kGemmTile / (2 * kCols);  // tiles of a diagonal block are formed whole
     const bool mirror = s.symmetric && t.tn >= kAcross * (t.tm + 1);
@@ -302,12 +304,12 @@ struct StoreEpilogue {
         }
       }
       __syncwarp();
+      uint16_t* p = out + static_cast<int64_t>(row0 + (lane >> 3)) * e.ld + col + 8 * unit;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 8; ++i, p += 4 * e.ld) {
         const int r = 4 * i + (lane >> 3);
         uint4 w;
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(word(r, unit)));
-        uint16_t* p = out + static_cast<int64_t>(row0 + r) * e.ld + col + 8 * unit;
         if (r < rows && 8 * unit + 8 <= left)
           *reinterpret_cast<uint4*>(p) = w;
         else if (r < rows && 8 * unit < left)
@@ -496,7 +498,7 @@ struct GradEpilogue {
     if (e.partial.out)
       PartialEpilogue::run<kCols>(e.partial, table, s, t, row, col0, tmem, turn, release);
     else
-      StoreEpilogue::run<kCols>(e.store, table, s, t, row, col0, tmem, turn, release);
+      StoreEpilogue::run<kCols, true>(e.store, table, s, t, row, col0, tmem, turn, release);
   }
 };
 
