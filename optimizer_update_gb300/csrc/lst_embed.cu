@@ -6,7 +6,7 @@
 // Gradient: grad[t] = scale * sum_{i : t_i = t} dout[i]. Adding rows with
 // atomics would make the sum's order, and so its last bits, differ from run to
 // run, and would read and write fp32 sums of a large gradient; instead
-//   1. one cluster of 8 CTAs sorts (token, position) pairs, stable, by radix
+//   1. one cluster of 8 or 16 CTAs sorts (token, position) pairs, stable, by radix
 //      passes in shared memory, while the launch's other CTAs zero the gradient
 //      (the rows that step 2 writes too, which costs less than waiting for the
 //      sort to know them);
@@ -143,7 +143,6 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---- stable sort of (token, position) ---------------------------------------------
-constexpr int kSortCtas = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortAhead = 8;  // loads in flight per thread
@@ -165,6 +164,7 @@ __device__ __forceinline__ uint32_t remote_u32(const uint32_t* p, uint32_t rank)
 // each pass is stable: count digits per warp, place the warps' counts one after
 // the other (over the cluster by distributed shared memory), scatter. Tokens
 // outside the vocabulary get the key `vocab` and sort last.
+template <int kSortCtas>
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1)
     sort_kernel(const void* __restrict__ tokens, int wide, int n, int vocab, int passes, int digit_bits, uint2* buf0,
                 uint2* buf1, char* zero, int64_t zero_pitch, int64_t zero_row, int zero_vec) {
@@ -424,6 +424,13 @@ cudaError_t launch_embed(const lst_matrix* table, const lst_indices* tokens, con
   return cudaSuccess;
 }
 
+// The sort takes 16 CTAs instead of 8 where it is the longer part of its launch: from
+// 16384 tokens on (whole gradients of 65521 tokens, 256 columns, added: 72 us against
+// 85; of 16384 29.8 and 31.4; of 4096 22 and 21), unless more is to be zeroed than it
+// leaves time for (65521 tokens, 32000 rows of 2 KB: 119 and 132 us; of 8 KB: 231 and
+// 226, since fewer CTAs in clusters of 16 are resident).
+bool wide_sort(int64_t n, int64_t zeroed_bytes) { return n >= 16384 && zeroed_bytes <= 2000 * n; }
+
 struct GradPlan {
   int passes, digit_bits, run;
   int64_t chunks, parts_ld;
@@ -526,18 +533,25 @@ extern "C" lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* 
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const int bins = 1 << p.digit_bits;
   const int smem = (kSortWarps + 2) * bins * 4;
-  // the largest case (10-bit digits) needs 139,264 bytes; a function attribute
-  // is per device, so it is set on every call (host only, under a microsecond)
-  LST_TRY_CUDA(cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), who);
   const int64_t row = grad->cols * dtype_bytes(grad->dtype), pitch = grad->stride * dtype_bytes(grad->dtype);
   const bool flat = row == pitch && reinterpret_cast<uintptr_t>(grad->data) % 16 == 0 && row * grad->rows % 16 == 0;
+  auto sort = [&](auto kernel, unsigned grid) {
+    return launch_chained(kernel, dim3(grid), dim3(kSortThreads), smem, s, tokens->data, tokens->bits == 64,
+                          static_cast<int>(dout->rows), static_cast<int>(grad->rows), p.passes, p.digit_bits,
+                          reinterpret_cast<uint2*>(ws + p.buf_off[0]), reinterpret_cast<uint2*>(ws + p.buf_off[1]),
+                          static_cast<char*>(grad->data), pitch, flat ? row * grad->rows : row, flat ? 1 : 0);
+  };
   // two CTAs per SM; the clusters after the first zero the gradient
-  const unsigned grid = accumulate ? kSortCtas : 2 * 152;
-  LST_TRY_CUDA(launch_chained(sort_kernel, dim3(grid), dim3(kSortThreads), smem, s, tokens->data, tokens->bits == 64,
-                              static_cast<int>(dout->rows), static_cast<int>(grad->rows), p.passes, p.digit_bits,
-                              reinterpret_cast<uint2*>(ws + p.buf_off[0]), reinterpret_cast<uint2*>(ws + p.buf_off[1]),
-                              static_cast<char*>(grad->data), pitch, flat ? row * grad->rows : row, flat ? 1 : 0),
-               who);
+  // the largest case (10-bit digits) needs 139,264 bytes; a function attribute
+  // is per device, so it is set on every call (host only, under a microsecond)
+  if (wide_sort(dout->rows, accumulate ? 0 : row * grad->rows)) {
+    LST_TRY_CUDA(cudaFuncSetAttribute(sort_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), who);
+    LST_TRY_CUDA(cudaFuncSetAttribute(sort_kernel<16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), who);
+    LST_TRY_CUDA(sort(sort_kernel<16>, accumulate ? 16 : 2 * 152), who);
+  } else {
+    LST_TRY_CUDA(cudaFuncSetAttribute(sort_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), who);
+    LST_TRY_CUDA(sort(sort_kernel<8>, accumulate ? 8 : 2 * 152), who);
+  }
   const int kind = (dout->dtype == LST_F32 ? 2 : 0) + (grad->dtype == LST_F32 ? 1 : 0);
   cudaError_t err;
   switch (kind) {

@@ -159,6 +159,24 @@ def test_embed_grad(n, hidden, vocab, kind, src, dst, accumulate, pad):
     assert torch.equal(call(), grad)  # the same order of additions on every run
 
 
+@pytest.mark.parametrize("n", [16383, 16384, 40001])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad_many_tokens(n, accumulate):
+    """Around the number of tokens from which the sort takes more CTAs: 0.25-steps, sums exact in any order."""
+    vocab, hidden = 5003, 24
+    g = gen(n)
+    t = (torch.rand(n, generator=g, device="cuda") ** 3 * (vocab + 1)).long().to(torch.int32)  # vocab itself is outside
+    dout = (torch.randint(-8, 9, (n, hidden), generator=g, device="cuda") * 0.25).float()
+    before = torch.randint(-8, 9, (vocab, hidden), generator=g, device="cuda").float()
+    grad = before.clone()
+    ws = scratch(lst.lst_embed_grad_workspace_bytes(n, hidden, vocab))
+    lst.lst_embed_grad(lst.matrix(dout), lst.indices(t), lst.matrix(grad), 0.5, accumulate, ws.data_ptr(), ws.numel(), stream())
+    exact = torch.zeros(vocab + 1, hidden, dtype=torch.float64, device="cuda").index_add_(0, t.long(), dout.double())[:vocab] * 0.5
+    if accumulate:
+        exact += before.double()
+    assert torch.equal(grad.double(), exact)
+
+
 def test_embed_grad_empty_and_non_finite():
     grad = torch.ones(50, 16, device="cuda")
     none = torch.empty(0, 16, device="cuda")
