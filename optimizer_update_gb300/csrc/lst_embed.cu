@@ -327,7 +327,11 @@ __global__ void __launch_bounds__(kSumThreads)
   __syncthreads();
   float acc[8] = {};
   bool head = key[0] == key[1];
-  constexpr int kBatch = VEC && sizeof(TD) == 2 ? 8 : 4;  // rows in flight per thread
+  // Rows in flight per thread. More cost registers, and so resident CTAs. 65521 rows,
+  // added to 32000: 4096 bf16 in vectors 186 us by two, 196 by one, 206 by four, 255 by
+  // eight; 4096 fp32 in vectors 275 by four, 276 by two, 280 by one; 4095 without
+  // vectors, bf16 (written) 219 by one, 269 by two, 317 by four, fp32 308, 311, 316.
+  constexpr int kBatch = !VEC ? 1 : sizeof(TD) == 2 ? 2 : 4;
   for (int j0 = 0; j0 < len; j0 += kBatch) {
     float v[kBatch][8] = {};
 #pragma unroll
