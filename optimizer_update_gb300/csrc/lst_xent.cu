@@ -203,7 +203,7 @@ struct MaskedRows {
   int32_t rows, cols, vec;
 };
 
-// d / g over q, in place: 4096 entries of a row per block, twice 8 per thread. The
+// d / g over q, in place: 16 entries per thread, one row per block of columns. The
 // blocks after the first `d_blocks` copy x with its rows masked, and the first of
 // them forms the mean loss and g.
 __global__ void __launch_bounds__(256)
@@ -232,49 +232,42 @@ __global__ void __launch_bounds__(256)
     return;
   }
   const int row = blockIdx.x / blocks_per_row;
-  const int col0 = ((blockIdx.x - row * blocks_per_row) * 512 + threadIdx.x) * 8;
-  uint16_t* const at_row = q + static_cast<int64_t>(row) * q_ld;
+  const int col = ((blockIdx.x - row * blocks_per_row) * 256 + threadIdx.x) * 16;
+  if (col >= columns) return;
+  uint4* const p = reinterpret_cast<uint4*>(q + static_cast<int64_t>(row) * q_ld + col);
   const int64_t t = target_at(targets, wide, row);
-  const bool keep = in_gradient(t, ignore, vocab);
-  uint4 in[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (keep && col0 + 2048 * k < columns) in[k] = *reinterpret_cast<const uint4*>(at_row + col0 + 2048 * k);
-  const float l = lse[row];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int col = col0 + 2048 * k;
-    if (col >= columns) return;
-    if (!keep) {
-      *reinterpret_cast<uint4*>(at_row + col) = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    const float top = stats[row * stat_ld + first_group + (col >> group_shift)].x;
-    const float base = (top - l) * kLog2e;
-    const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
-    float d[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t q16 = (w[i >> 1] >> (16 * (i & 1))) & 0xffffu;
-      const float steps = q16 == 0xffffu ? __int_as_float(0x7f800000) : static_cast<float>(q16);
-      d[i] = exp2_approx(__fmaf_rn(steps, -kLog2e / 2048.0f, base));
-    }
-    const int64_t at = t - first_column - col;
-    if (at >= 0 && at < 8) {
-      // p - 1 of the target cancels when p is near 1; p = exp(-loss)
-      const float e = expm1f(-loss[row]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i == static_cast<int>(at)) d[i] = e;
-    }
-    uint32_t r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(d[2 * i], d[2 * i + 1]);
-      r[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(at_row + col) = make_uint4(r[0], r[1], r[2], r[3]);
+  if (!in_gradient(t, ignore, vocab)) {
+    p[0] = p[1] = make_uint4(0, 0, 0, 0);
+    return;
   }
+  const uint4 x0 = p[0], x1 = p[1];
+  const float l = lse[row];
+  const float top = stats[row * stat_ld + first_group + (col >> group_shift)].x;
+  const float base = (top - l) * kLog2e;
+  const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+  float d[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t q16 = (w[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+    const float steps = q16 == 0xffffu ? __int_as_float(0x7f800000) : static_cast<float>(q16);
+    d[i] = exp2_approx(__fmaf_rn(steps, -kLog2e / 2048.0f, base));
+  }
+  const int64_t at = t - first_column - col;
+  if (at >= 0 && at < 16) {
+    // p - 1 of the target cancels when p is near 1; p = exp(-loss)
+    const float e = expm1f(-loss[row]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i == static_cast<int>(at)) d[i] = e;
+  }
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(d[2 * i], d[2 * i + 1]);
+    r[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  p[0] = make_uint4(r[0], r[1], r[2], r[3]);
+  p[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
 // dx = g times the sum of its parts, in a fixed order, rounded to bf16.
