@@ -549,7 +549,9 @@ LST_API lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* tok
    logits: l = x w^T (x: count x hidden, w: vocab x hidden, both bf16, fp32
    accumulation), lse_i = log sum_v exp(l_iv), loss_i = lse_i - l_i,targets[i],
    both fp32 [count]. A target equal to ignore_index has loss 0; any other
-   target outside 0..vocab-1 has loss NaN and no gradient.
+   target outside 0..vocab-1 has loss NaN and no gradient. A logit of -inf has
+   probability 0, as a target loss inf; infinities above and NaN make their own
+   row's results NaN.
    lst_xent_grad also gives mean (fp32, one value) = the mean loss over the
    targets that are not ignored, and the gradients of grad_scale * mean:
      dx = grad_scale/N * (softmax(l) - onehot) w      count x hidden, bf16
