@@ -89,7 +89,8 @@ LST_F32 = 1
 
 def matrix(t) -> lst_matrix:
     """An lst_matrix over a torch tensor of two dimensions (bf16, bf16 bit
-    patterns as int16, or fp32) with contiguous rows. The tensor has to outlive
+    patterns as int16, or fp32) with contiguous rows that do not overlap (an
+    expanded tensor has to be made contiguous first). The tensor has to outlive
     the calls that use it."""
     dtype = _matrix_dtype(t.dtype)
     if t.dim() != 2:
@@ -98,7 +99,11 @@ def matrix(t) -> lst_matrix:
     stride, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError("rows must be contiguous")
-    return lst_matrix(t.data_ptr(), rows, cols, stride if rows > 1 and stride > cols else cols, dtype)
+    if rows <= 1:
+        stride = cols  # there is no next row
+    elif stride < cols:
+        raise ValueError("rows overlap: the row stride is below the column count")
+    return lst_matrix(t.data_ptr(), rows, cols, stride, dtype)
 
 
 _dtypes = {}  # torch types, filled at their first use: the binding does not import torch by itself

@@ -137,6 +137,28 @@ def test_tensor_arguments(L):
             L.indices(bad)
 
 
+def test_tensor_arguments_overlapping_rows(L):
+    """Rows that share memory (an expanded gradient, a sliding window) are no matrix: their stride is below the column
+    count, and a stride of the column count would reach past the storage."""
+    import torch
+    for bad in (torch.zeros(1, 4).expand(3, 4), torch.zeros(4).expand(3, 4), torch.zeros(9).as_strided((3, 4), (2, 1)),
+                torch.zeros(1, 1).expand(3, 1), torch.zeros(3, 1, dtype=torch.bfloat16).expand(3, 4)):
+        with pytest.raises(ValueError):
+            L.matrix(bad)
+    # one row, or none: the stride means nothing
+    m = L.matrix(torch.zeros(1, 4).expand(1, 4))
+    assert (m.rows, m.cols, m.stride) == (1, 4, 4)
+    m = L.matrix(torch.zeros(5, 9)[2:3, 1:4])
+    assert (m.rows, m.cols) == (1, 3) and m.stride >= 3
+    m = L.matrix(torch.zeros(0, 4))
+    assert (m.rows, m.cols) == (0, 4) and m.stride >= 4
+    m = L.matrix(torch.zeros(7, 1)[::2])
+    assert (m.rows, m.cols, m.stride) == (4, 1, 2)
+    # a row stride is what the tensor says, also where rows are one element
+    m = L.matrix(torch.zeros(4, 6)[:, 2:3])
+    assert (m.rows, m.cols, m.stride) == (4, 1, 6)
+
+
 STRUCTS = {"lst_matrix": ("data", "rows", "cols", "stride", "dtype"), "lst_indices": ("data", "count", "bits"),
            "lst_ns_params": ("steps", "eps"),
            "lst_muon_hparams": ("lr", "momentum", "weight_decay", "rms_scale", "eps", "nesterov", "ns_steps")}
