@@ -66,10 +66,12 @@ class lst_step_options(ctypes.Structure):
 class lst_matrix(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("stride", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+    host = False  # made from a tensor in host memory
 
 
 class lst_indices(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("count", ctypes.c_int64), ("bits", ctypes.c_int32)]
+    host = False
 
 
 class lst_ns_params(ctypes.Structure):
@@ -91,7 +93,7 @@ def matrix(t) -> lst_matrix:
     """An lst_matrix over a torch tensor of two dimensions (bf16, bf16 bit
     patterns as int16, or fp32) with contiguous rows that do not overlap (an
     expanded tensor has to be made contiguous first). The tensor has to outlive
-    the calls that use it."""
+    the calls that use it; operators take tensors in device memory only."""
     dtype = _matrix_dtype(t.dtype)
     if t.dim() != 2:
         raise ValueError("a matrix has two dimensions")
@@ -103,7 +105,10 @@ def matrix(t) -> lst_matrix:
         stride = cols  # there is no next row
     elif stride < cols:
         raise ValueError("rows overlap: the row stride is below the column count")
-    return lst_matrix(t.data_ptr(), rows, cols, stride, dtype)
+    m = lst_matrix(t.data_ptr(), rows, cols, stride, dtype)
+    if not t.is_cuda:
+        m.host = True
+    return m
 
 
 _dtypes = {}  # torch types, filled at their first use: the binding does not import torch by itself
@@ -130,7 +135,16 @@ def indices(t) -> lst_indices:
         raise ValueError("indices are int32 or int64")
     if not t.is_contiguous():
         raise ValueError("indices must be contiguous")
-    return lst_indices(t.data_ptr(), t.numel(), bits)
+    i = lst_indices(t.data_ptr(), t.numel(), bits)
+    if not t.is_cuda:
+        i.host = True
+    return i
+
+
+def _on_device(*operands) -> None:
+    for o in operands:
+        if o is not None and o.host:
+            raise ValueError("a matrix or indices in host memory: operators take device memory")
 
 
 def ns_params(steps=5, eps=1e-7):
@@ -447,6 +461,7 @@ def lst_store_step(store: int, staging: Sequence[int], dev_buf0: int, dev_buf1: 
 # training operators: matrices as lst_matrix (see matrix()), tokens and targets
 # as lst_indices (see indices()), other device memory as pointers
 def lst_embed(table: lst_matrix, tokens: lst_indices, out: lst_matrix, scale: float = 1.0, stream: int = 0) -> None:
+    _on_device(table, tokens, out)
     _check(lib().lst_embed(table, tokens, out, scale, stream or None))
 
 
@@ -456,6 +471,7 @@ def lst_embed_grad_workspace_bytes(count: int, hidden: int, vocab: int) -> int:
 
 def lst_embed_grad(dout: lst_matrix, tokens: lst_indices, grad: lst_matrix, scale: float, accumulate: bool,
                    workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _on_device(dout, tokens, grad)
     _check(lib().lst_embed_grad(dout, tokens, grad, scale, 1 if accumulate else 0, workspace or None, workspace_bytes,
                                 stream or None))
 
@@ -466,6 +482,7 @@ def lst_xent_workspace_bytes(count: int, hidden: int, vocab: int, with_grad: boo
 
 def lst_xent_loss(x: lst_matrix, w: lst_matrix, targets: lst_indices, ignore_index: int, loss: int, lse: int,
                   workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _on_device(x, w, targets)
     _check(lib().lst_xent_loss(x, w, targets, ignore_index, loss or None, lse or None, workspace or None,
                                workspace_bytes, stream or None))
 
@@ -473,6 +490,7 @@ def lst_xent_loss(x: lst_matrix, w: lst_matrix, targets: lst_indices, ignore_ind
 def lst_xent_grad(x: lst_matrix, w: lst_matrix, targets: lst_indices, ignore_index: int, grad_scale: float, loss: int,
                   lse: int, mean: int, dx: lst_matrix, dw: lst_matrix, accumulate_dw: bool, workspace: int,
                   workspace_bytes: int, stream: int = 0) -> None:
+    _on_device(x, w, targets, dx, dw)
     _check(lib().lst_xent_grad(x, w, targets, ignore_index, grad_scale, loss or None, lse or None, mean or None, dx, dw,
                                1 if accumulate_dw else 0, workspace or None, workspace_bytes, stream or None))
 
@@ -486,6 +504,7 @@ def lst_orthogonalize(inputs: Sequence[lst_matrix], outputs: Sequence[lst_matrix
     n = len(inputs)
     if len(outputs) != n:
         raise ValueError("one output per input")
+    _on_device(*inputs, *outputs)
     _check(lib().lst_orthogonalize(n, (lst_matrix * max(1, n))(*inputs), (lst_matrix * max(1, n))(*outputs), params,
                                    workspace or None, workspace_bytes, stream or None))
 

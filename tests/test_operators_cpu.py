@@ -159,6 +159,29 @@ def test_tensor_arguments_overlapping_rows(L):
     assert (m.rows, m.cols, m.stride) == (4, 1, 6)
 
 
+def test_host_tensors_are_refused(L):
+    """A tensor in host memory can be described, but no operator takes it: its kernels would read host addresses."""
+    import torch
+    m, w, t, p = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(10, 8, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int64), P
+    x, table, i = L.matrix(m), L.matrix(w), L.indices(t)
+    dx, dw, di = mat(L, 4, 8), mat(L, 10, 8), idx(L, 4)  # stand for device memory
+    big = 1 << 30
+    for fn, args in [(L.lst_embed, (table, di, dx)), (L.lst_embed, (dw, i, dx)), (L.lst_embed, (dw, di, x)),
+                     (L.lst_embed_grad, (x, di, dw, 1.0, False, p, big)), (L.lst_embed_grad, (dx, i, dw, 1.0, False, p, big)),
+                     (L.lst_embed_grad, (dx, di, table, 1.0, False, p, big)),
+                     (L.lst_xent_loss, (x, dw, di, -100, p, p, p, big)), (L.lst_xent_loss, (dx, table, di, -100, p, p, p, big)),
+                     (L.lst_xent_loss, (dx, dw, i, -100, p, p, p, big)),
+                     (L.lst_xent_grad, (x, dw, di, -100, 1.0, p, p, p, dx, dw, False, p, big)),
+                     (L.lst_xent_grad, (dx, table, di, -100, 1.0, p, p, p, dx, dw, False, p, big)),
+                     (L.lst_xent_grad, (dx, dw, i, -100, 1.0, p, p, p, dx, dw, False, p, big)),
+                     (L.lst_xent_grad, (dx, dw, di, -100, 1.0, p, p, p, x, dw, False, p, big)),
+                     (L.lst_xent_grad, (dx, dw, di, -100, 1.0, p, p, p, dx, table, False, p, big)),
+                     (L.lst_orthogonalize, ([dx, x], [dx, dx], L.ns_params(), p, big)),
+                     (L.lst_orthogonalize, ([dx, dx], [dx, x], L.ns_params(), p, big))]:
+        with pytest.raises(ValueError):
+            fn(*args)
+
+
 STRUCTS = {"lst_matrix": ("data", "rows", "cols", "stride", "dtype"), "lst_indices": ("data", "count", "bits"),
            "lst_ns_params": ("steps", "eps"),
            "lst_muon_hparams": ("lr", "momentum", "weight_decay", "rms_scale", "eps", "nesterov", "ns_steps")}
