@@ -518,6 +518,14 @@ def lst_muon_step(handle: int, dev_blocks: Sequence[int], muon: lst_muon_hparams
     """adamw: hyperparameters of the other tensors, or None to leave them alone;
     use_muon: one truth value per tensor of the layout, or None for every tensor
     of two dimensions."""
+    if len(dev_blocks) != lst_layout_info(handle)[0]:
+        raise ValueError("one pointer per block of the layout")
+    if use_muon is not None:
+        def has(t):
+            return lib().lst_layout_tensor(handle, t, LST_FIELD_G, None, None, None) == LST_OK
+
+        if has(len(use_muon)) or (len(use_muon) > 0 and not has(len(use_muon) - 1)):
+            raise ValueError("one truth value per tensor of the layout")
     mask = (ctypes.c_uint8 * max(1, len(use_muon)))(*[1 if u else 0 for u in use_muon]) if use_muon is not None else None
     _check(lib().lst_muon_step(handle, _ptr_array(dev_blocks), muon, adamw, mask, workspace or None, workspace_bytes,
                                stream or None))

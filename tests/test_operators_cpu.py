@@ -182,6 +182,19 @@ def test_host_tensors_are_refused(L):
             fn(*args)
 
 
+def test_muon_arguments_cover_the_layout(L):
+    """The library reads a mask entry per tensor and a pointer per block; a shorter list would be read past its end."""
+    from optimizer_update_gb300 import Layout
+    lay = Layout([("a", (200, 300), 0), ("n", (16,), 0), ("b", (16, 32), 1)], "L12")
+    ws, hp = L.lst_muon_workspace_bytes(lay.handle), L.muon_hparams()
+    for blocks, mask in [([P], None), ([P, P, P], None), ([P, P], [True]), ([P, P], []), ([P, P], [1, 0, 1, 0])]:
+        with pytest.raises(ValueError):
+            L.lst_muon_step(lay.handle, blocks, hp, None, mask, P, ws)
+    # as long as the layout: on to the library, which wants more workspace
+    refused(L, 1, L.lst_muon_step, lay.handle, [P, P], hp, None, [True, False, False], P, 0)
+    refused(L, 1, L.lst_muon_step, lay.handle, [P, P], hp, None, None, P, 0)
+
+
 STRUCTS = {"lst_matrix": ("data", "rows", "cols", "stride", "dtype"), "lst_indices": ("data", "count", "bits"),
            "lst_ns_params": ("steps", "eps"),
            "lst_muon_hparams": ("lr", "momentum", "weight_decay", "rms_scale", "eps", "nesterov", "ns_steps")}
