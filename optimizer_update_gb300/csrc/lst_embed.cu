@@ -146,6 +146,8 @@ __global__ void __launch_bounds__(256)
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortAhead = 8;  // loads in flight per thread
+constexpr int kSortMaxBits = 10;  // of a digit: one bin per thread
+constexpr int sort_smem(int digit_bits) { return (kSortWarps + 2) * (1 << digit_bits) * 4; }
 
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
@@ -535,8 +537,7 @@ extern "C" lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* 
   LST_TRY(check_workspace(workspace, workspace_bytes, p.bytes, who));
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  const int bins = 1 << p.digit_bits;
-  const int smem = (kSortWarps + 2) * bins * 4;
+  const int smem = sort_smem(p.digit_bits);
   const int64_t row = grad->cols * dtype_bytes(grad->dtype), pitch = grad->stride * dtype_bytes(grad->dtype);
   const bool flat = row == pitch && reinterpret_cast<uintptr_t>(grad->data) % 16 == 0 && row * grad->rows % 16 == 0;
   auto sort = [&](auto kernel, unsigned grid) {
@@ -545,15 +546,18 @@ extern "C" lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* 
                           reinterpret_cast<uint2*>(ws + p.buf_off[0]), reinterpret_cast<uint2*>(ws + p.buf_off[1]),
                           static_cast<char*>(grad->data), pitch, flat ? row * grad->rows : row, flat ? 1 : 0);
   };
-  // two CTAs per SM; the clusters after the first zero the gradient
-  // the largest case (10-bit digits) needs 139,264 bytes; a function attribute
-  // is per device, so it is set on every call (host only, under a microsecond)
+  // The clusters after the first zero the gradient: two CTAs per SM (one where digits
+  // of 10 bits take 139,264 bytes a CTA). The function's limit is set to the largest
+  // size on every call, host only and under a microsecond: it is state of the device
+  // that all threads share, and a limit of this call's own size would fail the
+  // launch of another thread's larger one.
+  constexpr int kLimit = sort_smem(kSortMaxBits);
   if (wide_sort(dout->rows, accumulate ? 0 : row * grad->rows)) {
-    LST_TRY_CUDA(cudaFuncSetAttribute(sort_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), who);
+    LST_TRY_CUDA(cudaFuncSetAttribute(sort_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLimit), who);
     LST_TRY_CUDA(cudaFuncSetAttribute(sort_kernel<16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), who);
     LST_TRY_CUDA(sort(sort_kernel<16>, accumulate ? 16 : 2 * 152), who);
   } else {
-    LST_TRY_CUDA(cudaFuncSetAttribute(sort_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), who);
+    LST_TRY_CUDA(cudaFuncSetAttribute(sort_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kLimit), who);
     LST_TRY_CUDA(sort(sort_kernel<8>, accumulate ? 8 : 2 * 152), who);
   }
   const int kind = (dout->dtype == LST_F32 ? 2 : 0) + (grad->dtype == LST_F32 ? 1 : 0);

@@ -11,6 +11,7 @@ from __future__ import annotations
 import math
 import os
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -210,6 +211,36 @@ def test_embed_grad_is_the_gradient_of_embed():
     diff = (f(0.5) - f(-0.5))
     # fp32 sums of at most 500 terms
     assert abs(float((grad.double() * d).sum()) - diff) <= 502 * U32 * 2.0 * float((d[tokens].abs() * dout.abs()).sum())
+
+
+@pytest.mark.parametrize("n", [100, 20000])
+def test_embed_grad_from_two_threads(n):
+    """Sorts with much and with little shared memory, launched by two host threads on streams of their own."""
+    hidden, errors = 16, []
+
+    def work(vocab, seed):
+        try:
+            g = gen(seed)
+            tokens = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+            dout = torch.randint(-4, 5, (n, hidden), generator=g, device="cuda").float()
+            exact = torch.zeros(vocab, hidden, device="cuda").index_add_(0, tokens, dout)  # whole numbers: exact in any order
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                ws, grad = scratch(lst.lst_embed_grad_workspace_bytes(n, hidden, vocab)), torch.empty_like(exact)
+                for _ in range(500):
+                    lst.lst_embed_grad(lst.matrix(dout), lst.indices(tokens), lst.matrix(grad), 1.0, False, ws.data_ptr(),
+                                       ws.numel(), s.cuda_stream)
+                assert torch.equal(grad, exact)
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in ((2, 1), (1000, 2))]  # digits of 2 and of 10 bits
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
 
 
 # ---------------------------------------------------------------------------
