@@ -447,7 +447,7 @@ GradPlan grad_plan(int64_t n, int64_t hidden, int64_t vocab) {
   GradPlan p;
   int bits = 1;
   while ((int64_t(1) << bits) <= vocab) ++bits;  // keys 0..vocab
-  p.passes = bits <= 10 ? 1 : bits <= 20 ? 2 : 3;
+  p.passes = static_cast<int>(ops_ceil_div(bits, kSortMaxBits));  // 4 for 2^30 entries, 31 bits
   p.digit_bits = static_cast<int>(ops_ceil_div(bits, p.passes));
   // 32 positions to a CTA, or 8 where that leaves the GPU short of CTAs: a short
   // call's time is the latency of a CTA's rows one batch after the other

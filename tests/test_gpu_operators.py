@@ -213,6 +213,19 @@ def test_embed_grad_is_the_gradient_of_embed():
     assert abs(float((grad.double() * d).sum()) - diff) <= 502 * U32 * 2.0 * float((d[tokens].abs() * dout.abs()).sum())
 
 
+@pytest.mark.parametrize("vocab", [(1 << 30) - 1, 1 << 30])
+def test_embed_grad_largest_vocabulary(vocab):
+    """Keys 0..vocab of 30 and of 31 bits; 2^30 entries is the limit."""
+    tokens = torch.tensor([vocab - 1, 5, 1 << 20, vocab - 1, 1023, vocab, -1, 1 << 10, 1 << 29], device="cuda")
+    dout = torch.arange(1.0, 10.0, device="cuda")[:, None].bfloat16()
+    grad = torch.ones(vocab, 1, dtype=torch.bfloat16, device="cuda")
+    ws = scratch(lst.lst_embed_grad_workspace_bytes(9, 1, vocab))
+    lst.lst_embed_grad(lst.matrix(dout), lst.indices(tokens), lst.matrix(grad), 1.0, False, ws.data_ptr(), ws.numel(), stream())
+    seen = torch.tensor([vocab - 1, 5, 1 << 20, 1023, 1 << 10, 1 << 29], device="cuda")
+    assert grad[seen, 0].tolist() == [5.0, 2.0, 3.0, 5.0, 8.0, 9.0]
+    assert int(torch.count_nonzero(grad)) == 6
+
+
 @pytest.mark.parametrize("n", [100, 20000])
 def test_embed_grad_from_two_threads(n):
     """Sorts with much and with little shared memory, launched by two host threads on streams of their own."""
