@@ -538,8 +538,9 @@ LST_API lst_status lst_embed(const lst_matrix* table, const lst_indices* tokens,
    say) contribute nothing. dout: count x hidden, grad: vocab x hidden, bf16
    or fp32 each; grad is for instance the embedding tensor's range of a block's
    G segment. workspace: lst_embed_grad_workspace_bytes() bytes, 256-byte
-   aligned. Errors as lst_embed, plus LST_ERR_INVALID_ARG for a workspace that
-   is too small, count or vocab above 2^30. */
+   aligned; that size serves smaller counts as well. Errors as lst_embed, plus
+   LST_ERR_INVALID_ARG for a workspace that is too small, count or vocab above
+   2^30. */
 LST_API int64_t lst_embed_grad_workspace_bytes(int64_t count, int64_t hidden, int64_t vocab);
 LST_API lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* tokens, const lst_matrix* grad,
                                   float scale, int32_t accumulate, void* workspace, int64_t workspace_bytes,

@@ -443,15 +443,17 @@ struct GradPlan {
   int64_t buf_off[2], parts_off, bytes;
 };
 
+// 32 positions to a CTA, or 8 where that leaves the GPU short of CTAs: a short
+// call's time is the latency of a CTA's rows one batch after the other.
+constexpr int64_t kManyCtas = 152 * 16;
+
 GradPlan grad_plan(int64_t n, int64_t hidden, int64_t vocab) {
   GradPlan p;
   int bits = 1;
   while ((int64_t(1) << bits) <= vocab) ++bits;  // keys 0..vocab
   p.passes = static_cast<int>(ops_ceil_div(bits, kSortMaxBits));  // 4 for 2^30 entries, 31 bits
   p.digit_bits = static_cast<int>(ops_ceil_div(bits, p.passes));
-  // 32 positions to a CTA, or 8 where that leaves the GPU short of CTAs: a short
-  // call's time is the latency of a CTA's rows one batch after the other
-  p.run = ops_ceil_div(n, kMaxRun) * ops_ceil_div(hidden, kSumCols) >= 152 * 16 ? kMaxRun : 8;
+  p.run = ops_ceil_div(n, kMaxRun) * ops_ceil_div(hidden, kSumCols) >= kManyCtas ? kMaxRun : 8;
   p.chunks = ops_ceil_div(n, p.run);
   p.parts_ld = ops_round_up(hidden, 8);
   int64_t at = 0;
@@ -518,7 +520,11 @@ extern "C" lst_status lst_embed(const lst_matrix* table, const lst_indices* toke
 
 extern "C" int64_t lst_embed_grad_workspace_bytes(int64_t count, int64_t hidden, int64_t vocab) {
   if (count < 0 || hidden < 0 || vocab < 0 || count > (int64_t(1) << 30) || vocab > (int64_t(1) << 30)) return 0;
-  return grad_plan(count, hidden, vocab).bytes;
+  const GradPlan p = grad_plan(count, hidden, vocab);
+  if (p.run != kMaxRun) return p.bytes;
+  // fewer tokens in runs of 8 leave more parts: the most that do
+  const int64_t most = (kManyCtas - 1) / ops_ceil_div(hidden, kSumCols) * kMaxRun;
+  return std::max(p.bytes, grad_plan(most, hidden, vocab).bytes);
 }
 
 extern "C" lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* tokens, const lst_matrix* grad,

@@ -122,6 +122,19 @@ def test_workspace_sizes(L):
     assert L.lst_embed_grad_workspace_bytes(-1, 8, 8) == 0
 
 
+@pytest.mark.parametrize("hidden", [1, 1024, 2048, 4095, 3000000])
+def test_embed_grad_workspace_serves_smaller_counts(L, hidden):
+    """A workspace sized for the largest batch is enough for a shorter one, whatever the kernels do with few tokens."""
+    counts = sorted({k + d for k in [2 ** i for i in range(18)] + [2432 * 32 // s for s in (1, 2, 4)] for d in (-31, -1, 0, 1, 32)
+                     if k + d > 0})
+    sizes = [L.lst_embed_grad_workspace_bytes(n, hidden, 32000) for n in counts]
+    assert sizes == sorted(sizes)
+    # and no less than the call itself asks for: one byte less than its own need is refused
+    args = [mat(L, 9, hidden), idx(L, 9), mat(L, 32000, hidden), 1.0, False, P]
+    need = L.lst_embed_grad_workspace_bytes(9, hidden, 32000)
+    refused(L, 1, L.lst_embed_grad, *args, need - 257 if hidden < 3000000 else 1000)
+
+
 def test_tensor_arguments(L):
     import torch
     x = torch.zeros(6, 10)
