@@ -566,8 +566,14 @@ LST_API lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* tok
    gives the size for one piece, at most 1 GiB of them, beyond which the
    logits of all but one piece are formed twice. A smaller workspace makes
    smaller pieces; LST_ERR_INVALID_ARG where not even 256 columns fit.
+   Rows of x or w that do not all start on 16 bytes (an odd hidden size, a
+   padded stride, a view) are copied to the workspace first.
+   lst_xent_workspace_bytes counts the copies of contiguous rows of that hidden
+   size; lst_xent_workspace_bytes_for gives the size for x and w as they lie,
+   with any data pointer and stride (0 for sizes that the calls refuse).
    workspace: 256-byte aligned. Errors otherwise as lst_embed. */
 LST_API int64_t lst_xent_workspace_bytes(int64_t count, int64_t hidden, int64_t vocab, int32_t with_grad);
+LST_API int64_t lst_xent_workspace_bytes_for(const lst_matrix* x, const lst_matrix* w, int32_t with_grad);
 LST_API lst_status lst_xent_loss(const lst_matrix* x, const lst_matrix* w, const lst_indices* targets,
                                  int64_t ignore_index, float* loss, float* lse, void* workspace,
                                  int64_t workspace_bytes, void* cuda_stream);

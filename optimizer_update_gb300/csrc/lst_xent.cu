@@ -375,6 +375,12 @@ bool make_plan(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool pac
   return bytes < 0 || at <= bytes;
 }
 
+int64_t plan_bytes(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool pack_w) {
+  Plan p;
+  make_plan(n, h, v, grad, pack_x, pack_w, -1, &p);
+  return p.bytes;
+}
+
 // A matrix of rows; `transposed`: the product sums over its rows.
 GemmOperand rows_operand(const void* ptr, int64_t rows, int64_t cols, int64_t ld, bool transposed = false) {
   return {ptr, cols, rows, ld, transposed};
@@ -468,11 +474,15 @@ using namespace lst;
 extern "C" int64_t lst_xent_workspace_bytes(int64_t count, int64_t hidden, int64_t vocab, int32_t with_grad) {
   if (count <= 0 || hidden <= 0 || vocab <= 0 || count > (int64_t(1) << 24) || vocab > INT32_MAX || hidden > INT32_MAX)
     return 0;
-  Plan p;
-  // rows of an odd size have to be packed; others may be, when they start off 16 bytes
-  const bool pack = hidden % 8 != 0;
-  make_plan(count, hidden, vocab, with_grad != 0, pack, pack, -1, &p);
-  return p.bytes;
+  const bool pack = hidden % 8 != 0;  // contiguous rows of such a length are off 16 bytes
+  return plan_bytes(count, hidden, vocab, with_grad != 0, pack, pack);
+}
+
+extern "C" int64_t lst_xent_workspace_bytes_for(const lst_matrix* x, const lst_matrix* w, int32_t with_grad) {
+  if (!x || !w || x->rows <= 0 || w->rows <= 0 || x->cols <= 0 || x->cols != w->cols || x->rows > (int64_t(1) << 24) ||
+      w->rows > INT32_MAX || x->cols > INT32_MAX)
+    return 0;
+  return plan_bytes(x->rows, x->cols, w->rows, with_grad != 0, !tile_ready(x), !tile_ready(w));
 }
 
 extern "C" lst_status lst_xent_loss(const lst_matrix* x, const lst_matrix* w, const lst_indices* targets,
@@ -525,8 +535,9 @@ extern "C" lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, co
          0, 0, targets->bits == 64};
   const bool px = !tile_ready(x), pw = !tile_ready(w);
   if (!make_plan(x->rows, x->cols, w->rows, true, px, pw, workspace_bytes < 0 ? 0 : workspace_bytes, &c.p))
-    return fail(LST_ERR_INVALID_ARG, "%s: workspace of %lld bytes holds no piece of 256 columns", who,
-                (long long)workspace_bytes);
+    return fail(LST_ERR_INVALID_ARG,
+                "%s: workspace of %lld bytes holds no piece of 256 columns (lst_xent_workspace_bytes_for: %lld for all)", who,
+                (long long)workspace_bytes, (long long)plan_bytes(x->rows, x->cols, w->rows, true, px, pw));
   const Plan& p = c.p;
   LST_TRY(check_workspace(workspace, workspace_bytes, p.bytes, who));
   char* ws = c.ws;

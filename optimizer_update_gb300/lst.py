@@ -235,6 +235,7 @@ def lib() -> ctypes.CDLL:
             "lst_embed_grad_workspace_bytes": ([i64, i64, i64], i64),
             "lst_embed_grad": ([P(lst_matrix), P(lst_indices), P(lst_matrix), f32, i32, vp, i64, vp], ctypes.c_int),
             "lst_xent_workspace_bytes": ([i64, i64, i64, i32], i64),
+            "lst_xent_workspace_bytes_for": ([P(lst_matrix), P(lst_matrix), i32], i64),
             "lst_xent_loss": ([P(lst_matrix), P(lst_matrix), P(lst_indices), i64, vp, vp, vp, i64, vp], ctypes.c_int),
             "lst_xent_grad": ([P(lst_matrix), P(lst_matrix), P(lst_indices), i64, f32, vp, vp, vp, P(lst_matrix),
                                P(lst_matrix), i32, vp, i64, vp], ctypes.c_int),
@@ -478,6 +479,11 @@ def lst_embed_grad(dout: lst_matrix, tokens: lst_indices, grad: lst_matrix, scal
 
 def lst_xent_workspace_bytes(count: int, hidden: int, vocab: int, with_grad: bool) -> int:
     return int(lib().lst_xent_workspace_bytes(count, hidden, vocab, 1 if with_grad else 0))
+
+
+def lst_xent_workspace_bytes_for(x: lst_matrix, w: lst_matrix, with_grad: bool) -> int:
+    """The size for x and w as they lie: rows that do not start on 16 bytes take more."""
+    return int(lib().lst_xent_workspace_bytes_for(x, w, 1 if with_grad else 0))
 
 
 def lst_xent_loss(x: lst_matrix, w: lst_matrix, targets: lst_indices, ignore_index: int, loss: int, lse: int,

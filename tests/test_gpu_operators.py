@@ -373,6 +373,23 @@ def test_xent_strides_and_odd_rows(hidden, pad, shift):
     xent_check(r, e)
 
 
+@pytest.mark.parametrize("n,hidden,vocab,pad,shift", [(130, 64, 300, 3, 0), (130, 64, 300, 0, 1), (16, 2048, 5000, 0, 1),
+                                                      (16, 256, 5000, 4, 0), (130, 72, 300, 8, 4), (130, 77, 300, 0, 0),
+                                                      (300, 64, 4000, 1, 3), (33, 104, 1000, 8, 0)])
+@pytest.mark.parametrize("which", ["x", "w", "xw"])
+def test_xent_workspace_for_strides(n, hidden, vocab, pad, shift, which):
+    """Operands off 16 bytes in a workspace of exactly the size that is given for them: one piece, the results of
+    contiguous operands bit for bit."""
+    x, w, t = xent_inputs(n, hidden, vocab, seed=hidden + n)
+    ref = xent_call(x, w, t)
+    xs = strided(x, pad, shift) if "x" in which else x
+    ws = strided(w, pad, shift) if "w" in which else w
+    r = xent_call(xs, ws, t, ws_bytes=lst.lst_xent_workspace_bytes_for(lst.matrix(xs), lst.matrix(ws), True))
+    assert all(torch.equal(r[k], ref[k]) for k in ref)
+    only = xent_call(xs, ws, t, grad=False, ws_bytes=lst.lst_xent_workspace_bytes_for(lst.matrix(xs), lst.matrix(ws), False))
+    assert torch.equal(only["loss"], ref["loss"]) and torch.equal(only["lse"], ref["lse"])
+
+
 @pytest.mark.parametrize("n,hidden,vocab", [(300, 264, 5003), (40, 64, 3000), (1030, 96, 1500)])
 def test_xent_small_workspaces(n, hidden, vocab):
     """Down to pieces of 256 columns: the same loss bit for bit, gradients within the same bounds."""

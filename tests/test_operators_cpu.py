@@ -78,6 +78,29 @@ def test_xent_refusals(L):
         refused(L, status, L.lst_xent_grad, *[change.get(i, a) for i, a in enumerate(ok)])
 
 
+@pytest.mark.parametrize("n,h,v,xs,ws,xo,wo", [(512, 2048, 32000, 3, 0, 0, 0), (512, 2048, 32000, 0, 0, 0, 2),
+                                               (16, 2048, 32000, 0, 0, 0, 2), (16, 2048, 32000, 4, 4, 0, 0),
+                                               (300, 64, 300, 0, 0, 6, 0), (300, 63, 300, 1, 1, 0, 0), (300, 63, 300, 0, 0, 0, 0),
+                                               (270, 72, 500, 8, 16, 0, 0)])
+def test_xent_workspace_for_the_operands(L, n, h, v, xs, ws, xo, wo):
+    """The size for operands as they lie is what the loss asks for: enough, and not a granule less."""
+    x, w, t = mat(L, n, h, stride=h + xs, data=P + xo), mat(L, v, h, stride=h + ws, data=P + wo), idx(L, n)
+    off = any((m.data | m.stride * 2) % 16 for m in (x, w))
+    for grad in (False, True):
+        need = L.lst_xent_workspace_bytes_for(x, w, grad)
+        plain = L.lst_xent_workspace_bytes_for(mat(L, n, (h + 7) // 8 * 8), mat(L, v, (h + 7) // 8 * 8), grad)
+        assert need > plain if off else need >= plain - 4096
+        if h % 8 == 0:
+            assert plain == L.lst_xent_workspace_bytes(n, h, v, grad)
+    need = L.lst_xent_workspace_bytes_for(x, w, False)
+    refused(L, L.LST_ERR_INVALID_ARG, L.lst_xent_loss, x, w, t, -100, P, P, P, need - 1)
+    # one row's copy more than the sizes alone give is not enough for a w off 16 bytes
+    if ws % 8 or wo:
+        refused(L, L.LST_ERR_INVALID_ARG, L.lst_xent_loss, x, w, t, -100, P, P, P, need - v * h * 2)
+    for bad in ((None, w), (x, None), (x, mat(L, v, h + 1)), (mat(L, 0, h), w), (mat(L, (1 << 24) + 1, h), w)):
+        assert L.lst_xent_workspace_bytes_for(*bad, True) == 0
+
+
 def test_orthogonalize_refusals(L):
     ws = L.lst_orthogonalize_workspace_bytes(2, 16, 32)
     a, o, p = mat(L, 16, 32), mat(L, 16, 32), L.ns_params()
