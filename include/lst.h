@@ -570,7 +570,8 @@ LST_API lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* tok
    padded stride, a view) are copied to the workspace first.
    lst_xent_workspace_bytes counts the copies of contiguous rows of that hidden
    size; lst_xent_workspace_bytes_for gives the size for x and w as they lie,
-   with any data pointer and stride (0 for sizes that the calls refuse).
+   with any data pointer and stride (0 for sizes that the calls refuse). Either
+   size serves smaller counts as well.
    workspace: 256-byte aligned. Errors otherwise as lst_embed. */
 LST_API int64_t lst_xent_workspace_bytes(int64_t count, int64_t hidden, int64_t vocab, int32_t with_grad);
 LST_API int64_t lst_xent_workspace_bytes_for(const lst_matrix* x, const lst_matrix* w, int32_t with_grad);

@@ -322,7 +322,6 @@ struct Plan {
   int group_shift;  // log2 of the vocabulary entries of a group of statistics
   int64_t packed_ld, x_ld, part_ld;
   int64_t scalar_off, tlogit_off, stats_off, xm_off, xpack_off, wpack_off, part_off, q_off;
-  int64_t fixed;  // bytes before the pieces
   int64_t bytes;
 };
 
@@ -375,10 +374,25 @@ bool make_plan(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool pac
   return bytes < 0 || at <= bytes;
 }
 
+// What the calls report: enough for one piece (at most 1 GiB of it) of this many tokens
+// or of any fewer, so that a workspace sized for the largest batch serves all. What
+// make_plan takes is not monotone in n:
+//   statistics are per 32 entries up to kFewTokens tokens, per 128 above;
+//   a piece is rounded down to tiles, so that 1 GiB is not always filled;
+//   few tokens split dx more often. gemm_splits takes s > 1 ranges only where
+//   blocks / (s - 1) > max(share / 2, 8), with share >= (tiles blocks + others) / 76 - 1,
+//   tiles >= tiles_h n / 256 and others >= blocks tiles_h n / 256: it follows that
+//   (s - 1) n < 171 * 128 / tiles_h, and s is at most 32. One piece has parts for s > 1 only.
 int64_t plan_bytes(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool pack_w) {
-  Plan p;
-  make_plan(n, h, v, grad, pack_x, pack_w, -1, &p);
-  return p.bytes;
+  const int64_t ld = ops_round_up(h, 8), few = std::min(n, kFewTokens);
+  auto size = [](int64_t bytes) { return ops_round_up(bytes, 256); };
+  int64_t bytes = 256 + size(n * 4) + size(std::max(n * ops_ceil_div(v, 128), few * ops_ceil_div(v, 32)) * 8) +
+                  size(pack_x ? n * ld * 2 : 0) + size(pack_w ? v * ld * 2 : 0);
+  if (!grad) return bytes;
+  const int64_t all = n * ops_round_up(v, kGemmTile) * 2, most = 171 * 128 / ops_ceil_div(h, kGemmTile);
+  const int64_t rows = std::min(32 * n, most + (all > kMaxPieceBytes ? n : std::min(n, most)));
+  const int64_t q = std::min(all, std::max(kMaxPieceBytes, n * 2 * kGemmTile));
+  return bytes + size(n * ld * 2) + size(rows * ops_round_up(h, 32) * 4 + 256) + size(q);
 }
 
 // A matrix of rows; `transposed`: the product sums over its rows.

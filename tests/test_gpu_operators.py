@@ -411,6 +411,18 @@ def test_xent_small_workspaces(n, hidden, vocab):
     assert tried >= 2
 
 
+@pytest.mark.parametrize("most,n", [(65, 64), (200, 64), (300, 256), (600, 33), (1030, 700), (300, 300)])
+def test_xent_workspace_of_a_larger_batch(most, n):
+    """The workspace for the largest batch serves a shorter one in one piece: the results of its own workspace."""
+    hidden, vocab = 264, 5003
+    x, w, t = xent_inputs(n, hidden, vocab, seed=most + n)
+    ref, large = xent_call(x, w, t), xent_call(x, w, t, ws_bytes=lst.lst_xent_workspace_bytes(most, hidden, vocab, True))
+    assert all(torch.equal(large[k], ref[k]) for k in ref)
+    only = xent_call(x, w, t, grad=False, ws_bytes=lst.lst_xent_workspace_bytes(most, hidden, vocab, False))
+    assert torch.equal(only["loss"], ref["loss"])
+    xent_check(large, xent_exact(x, w, t))
+
+
 def test_xent_ignored_rows_reach_nothing():
     n, hidden, vocab = 300, 128, 1000
     x, w, t = xent_inputs(n, hidden, vocab, seed=8, ignored=0.3)

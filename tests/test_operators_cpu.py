@@ -101,6 +101,20 @@ def test_xent_workspace_for_the_operands(L, n, h, v, xs, ws, xo, wo):
         assert L.lst_xent_workspace_bytes_for(*bad, True) == 0
 
 
+@pytest.mark.parametrize("h,v", [(64, 300), (2048, 32000), (4096, 131072), (77, 50257), (256, 1000)])
+def test_xent_workspace_serves_smaller_counts(L, h, v):
+    """A workspace sized for the largest batch is enough for a shorter one."""
+    counts = sorted({max(1, k + d) for k in [2 ** i for i in range(17)] + [3 * 2 ** i for i in range(6, 14)] for d in (-1, 0, 1, 5)})
+    for grad in (False, True):
+        sizes = [L.lst_xent_workspace_bytes(n, h, v, grad) for n in counts]
+        assert sizes == sorted(sizes)
+    for n in (1, 31, 63, 64, 65, 70, 128, 255, 256, 300):
+        with pytest.raises(L.LstError, match="at least [0-9]+ needed") as e:
+            L.lst_xent_loss(mat(L, n, h), mat(L, v, h), idx(L, n), -100, P, P, P, 256)
+        need = int(str(e.value).split("at least ")[1].split()[0])
+        assert all(L.lst_xent_workspace_bytes(m, h, v, False) >= need for m in counts if m >= n)
+
+
 def test_orthogonalize_refusals(L):
     ws = L.lst_orthogonalize_workspace_bytes(2, 16, 32)
     a, o, p = mat(L, 16, 32), mat(L, 16, 32), L.ns_params()
