@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Item
   sum = red[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) sum += red[i];
-  const float inv = kScaleX / (sqrtf(sum) + s.eps);
+  const NsScale by = ns_scale(sum, s.eps);
   if (vector_rows<MOM>(it)) {
     const uint32_t per_row = static_cast<uint32_t>(it.cols / 8);
     const int64_t total = it.rows * per_row;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Item
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(u[2 * i] * inv, u[2 * i + 1] * inv);
+        const __half2 h = __floats2half2_rn(u[2 * i] * by.pre * by.inv, u[2 * i + 1] * by.pre * by.inv);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
       *reinterpret_cast<uint4*>(it.x + r * it.ldx + c) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Item
       for (int64_t c = lane; c < it.cols; c += 32) {
         float u = load_in(it.g, r * it.ld + c, F32);
         if (MOM) u = muon_u(u, it.mom[r * it.cols + c], s);
-        it.x[r * it.ldx + c] = __float2half_rn(u * inv);
+        it.x[r * it.ldx + c] = __float2half_rn(u * by.pre * by.inv);
       }
     }
   }

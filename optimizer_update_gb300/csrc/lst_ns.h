@@ -26,6 +26,17 @@ __device__ __forceinline__ float new_momentum(float m, float g, const NsMomentum
   return __fadd_rn(__fmul_rn(s.momentum, m), g);
 }
 
+// X_0 = U / (|U|_F + eps) times kScaleX is (u * pre) * inv of every element: `pre` is a
+// power of two, other than 1 where the quotient alone would overflow (a matrix of zeros,
+// or next to nothing, with a small eps).
+struct NsScale {
+  float pre, inv;
+};
+__device__ __forceinline__ NsScale ns_scale(float sum_of_squares, float eps) {
+  const float d = sqrtf(sum_of_squares) + eps, pre = d < 0x1p-64f ? 0x1p100f : 1.0f;
+  return {pre, kScaleX / (d * pre)};
+}
+
 // One matrix of a launch: the input (a gradient with its momentum, or the matrix
 // itself), and where the result goes: a bf16 matrix, or a weight to update.
 struct NsSmallItem {

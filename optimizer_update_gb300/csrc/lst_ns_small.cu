@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
   __shared__ float warp_sum[kSmallWarps];
-  __shared__ float shared_inv;
+  __shared__ NsScale shared_scale;
   if (k.lane == 0) warp_sum[k.warp] = sum;
   // rows and columns beyond the matrix are zero
   for (int i = threadIdx.x; i < chunks * kChunk / 16; i += kSmallThreads) st_shared_v4(k.x + 16 * i, 0, 0, 0, 0);
@@ -364,14 +364,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(sums + 4 * i));
       x += y;
     }
-    shared_inv = kScaleX / (sqrtf(x) + call.s.eps);
+    shared_scale = ns_scale(x, call.s.eps);
   }
   __syncthreads();
-  const float inv = shared_inv;
+  const NsScale by = shared_scale;
   for_values([&](int r, int c, float g, float mom) {
     if (MOM) g = muon_u(g, mom, call.s);
     const int xr = tall ? c : r, xc = tall ? r : c;
-    st_shared16(k.x + (xc >> 6) * kChunk + chunk_at(xr, xc & 63), __half_as_ushort(__float2half_rn(g * inv)));
+    st_shared16(k.x + (xc >> 6) * kChunk + chunk_at(xr, xc & 63), __half_as_ushort(__float2half_rn(g * by.pre * by.inv)));
   });
 
   bool pair = true;

@@ -651,6 +651,17 @@ def test_orthogonalize_zero_tiny_large_and_non_finite():
     assert rel(outs[4], ns_exact(large)) <= NS_TOL
 
 
+@pytest.mark.parametrize("rows,cols", [(100, 130), (300, 1030), (520, 200)])
+@pytest.mark.parametrize("eps", [1e-20, 1e-36, 1e-40, 1e-45])
+def test_orthogonalize_small_eps(rows, cols, eps):
+    """Any eps above zero, the smallest number of fp32 among them: zero stays zero, others do not notice it."""
+    x = matrix_like(gen(50), rows, cols)
+    zero, out, low = ns_call([torch.zeros_like(x), x, x * 2.0 ** -50], eps=eps)
+    assert not zero.any() and torch.isfinite(zero).all()
+    assert rel(out, ns_exact(x, eps=float(np.float32(eps)))) <= NS_TOL
+    assert rel(low, ns_exact(x * 2.0 ** -50, eps=float(np.float32(eps)))) <= NS_TOL
+
+
 def test_orthogonalize_decaying_singular_values():
     """Values falling as 1/i over three decades: the smallest are still growing after five steps, by 3.45 a step, and
     so is their rounding: one more factor of 1.6 in the bound."""
