@@ -589,8 +589,8 @@ LST_API lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, const
    singular value of U that is not negligible to about 1 and keeps the singular
    vectors. Products are formed from fp16 values scaled by powers of two, with
    fp32 sums; see lst_muon.cu. in[i], out[i]: `count` matrices of one shape;
-   in bf16 or fp32 (all the same), out bf16. A zero matrix gives zero; a matrix
-   with a NaN or infinity, or whose |U|_F overflows fp32, gives values of no
+   in bf16 or fp32 (all the same), out bf16. Entries may be of any finite size.
+   A zero matrix gives zero; a matrix with a NaN or infinity gives values of no
    meaning for itself only. 1 <= steps <= 20, eps > 0.
    workspace: lst_orthogonalize_workspace_bytes() bytes, 256-byte aligned; a
    smaller one is used for fewer matrices at a time, LST_ERR_INVALID_ARG where

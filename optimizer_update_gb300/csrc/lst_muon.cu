@@ -52,7 +52,7 @@ struct Item {
   const void* g;      // gradient, or the matrix itself
   float* mom;         // momentum, or null
   __half* x;          // rows x ldx values
-  float* part;        // kNormBlocks partial sums of squares
+  float2* part;       // kNormBlocks partial sums of (u * pre)^2, and pre
   int64_t rows, cols, ld, ldx;
 };
 struct ItemTable {
@@ -88,22 +88,16 @@ __device__ __forceinline__ void vector_at(int64_t q, uint32_t per_row, int64_t* 
   *c = (q - *r * per_row) * 8;
 }
 
-// m = momentum m + g in place, and the sum of u^2 in fp32: over a thread's
-// elements, a warp, a block and at last the blocks (each level adds at most a
-// few hundred terms, an error under 1e-5 of the norm in the worst case, against
-// the 5e-4 of the fp16 that it scales; fp64 would cost more than the loads do).
-// Bound by memory: reads g and m, writes m.
-template <bool F32, bool MOM>
-__global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ ItemTable t, NsMomentum s) {
-  let_next_start();
-  wait_for_previous();
-  const Item& it = t.it[blockIdx.y];
+// A block's share of the sum of (u * pre)^2, by thread. kFirst: with m = momentum m + g in
+// place, and pre = 1.
+template <bool F32, bool MOM, bool kFirst>
+__device__ __forceinline__ float squares(const Item& it, const NsMomentum& s, float pre) {
   float sum = 0.0f;
   if (vector_rows<MOM>(it)) {
     const uint32_t per_row = static_cast<uint32_t>(it.cols / 8);
     const int64_t total = it.rows * per_row;
     const bool flat = it.ld == it.cols;
-#pragma unroll 4
+#pragma unroll (kFirst ? 4 : 1)
     for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < total; q += static_cast<int64_t>(gridDim.x) * 256) {
       int64_t r = 0, c = q * 8;
       if (!flat) vector_at(q, per_row, &r, &c);
@@ -113,48 +107,78 @@ __global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ ItemT
       if (MOM) {
         float4* p = reinterpret_cast<float4*>(it.mom) + 2 * q;
         float4 a = p[0], b = p[1];
-        a = make_float4(new_momentum(a.x, g[0], s), new_momentum(a.y, g[1], s), new_momentum(a.z, g[2], s),
-                        new_momentum(a.w, g[3], s));
-        b = make_float4(new_momentum(b.x, g[4], s), new_momentum(b.y, g[5], s), new_momentum(b.z, g[6], s),
-                        new_momentum(b.w, g[7], s));
-        p[0] = a;
-        p[1] = b;
+        if (kFirst) {
+          a = make_float4(new_momentum(a.x, g[0], s), new_momentum(a.y, g[1], s), new_momentum(a.z, g[2], s),
+                          new_momentum(a.w, g[3], s));
+          b = make_float4(new_momentum(b.x, g[4], s), new_momentum(b.y, g[5], s), new_momentum(b.z, g[6], s),
+                          new_momentum(b.w, g[7], s));
+          p[0] = a;
+          p[1] = b;
+        }
         const float m[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = muon_u(g[i], m[i], s);
       }
       float x = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x = __fmaf_rn(g[i], g[i], x);
+      for (int i = 0; i < 8; ++i) {
+        if (!kFirst) g[i] *= pre;
+        x = __fmaf_rn(g[i], g[i], x);
+      }
       sum += x;
     }
   } else {
     const int lane = threadIdx.x & 31;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
     for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < it.rows; r += warps) {
-#pragma unroll 4
+#pragma unroll (kFirst ? 4 : 1)
       for (int64_t c = lane; c < it.cols; c += 32) {
         float u = load_in(it.g, r * it.ld + c, F32);
         if (MOM) {
           float* p = it.mom + r * it.cols + c;
-          const float m = new_momentum(*p, u, s);
-          *p = m;
+          float m = *p;
+          if (kFirst) *p = m = new_momentum(m, u, s);
           u = muon_u(u, m, s);
         }
+        if (!kFirst) u *= pre;
         sum = __fmaf_rn(u, u, sum);
       }
     }
   }
-  __shared__ float red[8];
+  return sum;
+}
+
+// The sum over the block's threads, in all of them.
+__device__ __forceinline__ float block_sum(float sum, float (&red)[8]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float x = red[0];
-    for (int i = 1; i < 8; ++i) x += red[i];
-    it.part[blockIdx.x] = x;
+  sum = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) sum += red[i];
+  return sum;
+}
+
+// m = momentum m + g in place, and the sum of u^2 in fp32: over a thread's
+// elements, a warp, a block and at last the blocks (each level adds at most a
+// few hundred terms, an error under 1e-5 of the norm in the worst case, against
+// the 5e-4 of the fp16 that it scales; fp64 would cost more than the loads do).
+// A block whose sum is out of range reads its share again (from L2), scaled.
+// Bound by memory: reads g and m, writes m.
+template <bool F32, bool MOM>
+__global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ ItemTable t, NsMomentum s) {
+  let_next_start();
+  wait_for_previous();
+  const Item& it = t.it[blockIdx.y];
+  __shared__ float red[2][8];
+  float pre = 1.0f, sum = block_sum(squares<F32, MOM, true>(it, s, 1.0f), red[0]);
+  if (!ordinary_sum(sum)) {
+    pre = other_pre(sum);
+    sum = block_sum(squares<F32, MOM, false>(it, s, pre), red[1]);
+    if (sum == 0.0f) pre = 1.0f;  // nothing but zeros, or nothing at all
   }
+  if (threadIdx.x == 0) it.part[blockIdx.x] = make_float2(sum, pre);
 }
 
 // X_0 = u / (|u|_F + eps), in fp16 times kScaleX.
@@ -163,17 +187,41 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Item
   let_next_start();
   wait_for_previous();
   const Item& it = t.it[blockIdx.y];
-  __shared__ float red[8];
-  float sum = 0.0f;
-  for (int i = threadIdx.x; i < parts; i += 256) sum += it.part[i];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+  __shared__ float red[3][8];
+  __shared__ int scaled;
+  if (threadIdx.x == 0) scaled = 0;
   __syncthreads();
-  sum = red[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) sum += red[i];
-  const NsScale by = ns_scale(sum, s.eps);
+  float sum = 0.0f, pre = 1.0f;
+  for (int i = threadIdx.x; i < parts; i += 256) {
+    const float2 p = it.part[i];
+    if (p.y == 1.0f)
+      sum += p.x;
+    else
+      scaled = 1;
+  }
+  sum = block_sum(sum, red[0]);
+  if (scaled) {  // join the three ranges: the largest there is sets `pre`
+    float small = 0.0f, large = 0.0f;
+    for (int i = threadIdx.x; i < parts; i += 256) {
+      const float2 p = it.part[i];
+      if (p.y == kSmallPre) small += p.x;
+      if (p.y == kLargePre) large += p.x;
+    }
+    small = block_sum(small, red[1]);
+    large = block_sum(large, red[2]);
+    if (large != 0.0f) {  // or NaN
+      pre = kLargePre;
+      sum = large + sum * kLargePre * kLargePre;
+    } else if (sum > 0.0f) {
+      sum += small / kSmallPre / kSmallPre;
+    } else {
+      pre = kSmallPre;
+      sum = small;
+    }
+  } else if (sum == 0.0f) {
+    pre = kSmallPre;
+  }
+  const float inv = ns_inv(sum, pre, s.eps);
   if (vector_rows<MOM>(it)) {
     const uint32_t per_row = static_cast<uint32_t>(it.cols / 8);
     const int64_t total = it.rows * per_row;
@@ -192,7 +240,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Item
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(u[2 * i] * by.pre * by.inv, u[2 * i + 1] * by.pre * by.inv);
+        const __half2 h = __floats2half2_rn(u[2 * i] * pre * inv, u[2 * i + 1] * pre * inv);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
       *reinterpret_cast<uint4*>(it.x + r * it.ldx + c) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -205,7 +253,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const __grid_constant__ Item
       for (int64_t c = lane; c < it.cols; c += 32) {
         float u = load_in(it.g, r * it.ld + c, F32);
         if (MOM) u = muon_u(u, it.mom[r * it.cols + c], s);
-        it.x[r * it.ldx + c] = __float2half_rn(u * by.pre * by.inv);
+        it.x[r * it.ldx + c] = __float2half_rn(u * pre * inv);
       }
     }
   }
@@ -275,7 +323,7 @@ struct Batch {
 
   static int64_t ld(int64_t n) { return ops_round_up(n, 64); }
   static int64_t item_bytes(const Shape2& s) {  // upper bound of what one more matrix adds, tall or wide
-    return 2 * std::max(s.rows * ld(s.cols), s.cols * ld(s.rows)) * 2 + 3 * s.m() * ld(s.m()) * 2 + kNormBlocks * 4 + 8 * 256;
+    return 2 * std::max(s.rows * ld(s.cols), s.cols * ld(s.rows)) * 2 + 3 * s.m() * ld(s.m()) * 2 + kNormBlocks * 8 + 8 * 256;
   }
 
   void build(const Shape2* shapes, int64_t count) {
@@ -283,7 +331,7 @@ struct Batch {
     classes.clear();
     int64_t at = 0;
     part_off = at;
-    at += ops_round_up(count * kNormBlocks * 4, 256);
+    at += ops_round_up(count * kNormBlocks * 8, 256);
     for (int64_t i = 0; i < count; ++i) {
       const int64_t m = shapes[i].m();
       if (classes.empty() || classes.back().m != m) classes.push_back({m, ld(m), 0, {0, 0, 0}});
@@ -542,7 +590,7 @@ extern "C" lst_status lst_orthogonalize(int32_t count, const lst_matrix* in, con
         it.ld = src.stride;
         it.x = reinterpret_cast<__half*>(ws + g.x_off[0]) + i * g.x_elems();
         it.ldx = g.ldx;
-        it.part = reinterpret_cast<float*>(ws + b.part_off) + i * kNormBlocks;
+        it.part = reinterpret_cast<float2*>(ws + b.part_off) + i * kNormBlocks;
       }
       LST_TRY_CUDA(ingest(items, in[0].dtype == LST_F32, false, s, stream), who);
       Runner run{b, ws, stream, {}};
@@ -677,7 +725,7 @@ extern "C" lst_status lst_muon_step(const lst_layout* L, void* const* dev_blocks
         for (int64_t k = 0; k < g.count; ++k) {
           const Run r = run_of(L->tensors[(size_t)picks[first + (size_t)(g.first + k)].tensor]);
           items[(size_t)(g.first + k)] = {r.g, r.m, reinterpret_cast<__half*>(ws + g.x_off[0]) + k * g.x_elems(),
-                                          reinterpret_cast<float*>(ws + b.part_off) + (g.first + k) * kNormBlocks,
+                                          reinterpret_cast<float2*>(ws + b.part_off) + (g.first + k) * kNormBlocks,
                                           g.s.rows, g.s.cols, g.s.cols, g.ldx};
         }
       LST_TRY_CUDA(ingest(items, f32, true, ms, stream), who);

@@ -26,16 +26,19 @@ __device__ __forceinline__ float new_momentum(float m, float g, const NsMomentum
   return __fadd_rn(__fmul_rn(s.momentum, m), g);
 }
 
-// X_0 = U / (|U|_F + eps) times kScaleX is (u * pre) * inv of every element: `pre` is a
-// power of two, other than 1 where the quotient alone would overflow (a matrix of zeros,
-// or next to nothing, with a small eps).
-struct NsScale {
-  float pre, inv;
-};
-__device__ __forceinline__ NsScale ns_scale(float sum_of_squares, float eps) {
-  const float d = sqrtf(sum_of_squares) + eps, pre = d < 0x1p-64f ? 0x1p100f : 1.0f;
-  return {pre, kScaleX / (d * pre)};
-}
+// Squares in fp32 leave its range from |u| = 1.8e19 on and lose their last bits below
+// 1e-23. Where a sum of squares is outside kLeastSum .. kMostSum it is taken again over
+// u * pre, with `pre` one of two powers of two; matrices in the ordinary range do not notice.
+constexpr float kLeastSum = 0x1p-100f, kMostSum = 0x1p100f;
+constexpr float kSmallPre = 0x1p100f;  // of sums below: u is under 2^-50
+constexpr float kLargePre = 0x1p-80f;  // of sums above, infinite or NaN
+__device__ __forceinline__ bool ordinary_sum(float sum) { return sum >= kLeastSum && sum <= kMostSum; }
+__device__ __forceinline__ float other_pre(float sum) { return sum < kLeastSum ? kSmallPre : kLargePre; }
+
+// X_0 = U / (|U|_F + eps) times kScaleX is (u * pre) * inv of every element, from the sum of
+// (u * pre)^2. The divisor is 2^-50 at least, or with kSmallPre (zero matrices
+// among them) 2^100 times the smallest eps: `inv` is finite.
+__device__ __forceinline__ float ns_inv(float sum, float pre, float eps) { return kScaleX / (sqrtf(sum) + eps * pre); }
 
 // One matrix of a launch: the input (a gradient with its momentum, or the matrix
 // itself), and where the result goes: a bf16 matrix, or a weight to update.

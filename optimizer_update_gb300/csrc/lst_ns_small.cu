@@ -331,47 +331,60 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       }
   };
 
-  // momentum, and the sum of squares
-  float sum = 0.0f;
-  for_values([&](int r, int c, float g, float mom) {
-    if (MOM) {
-      mom = new_momentum(mom, g, call.s);
-      it.mom[first_m + static_cast<int64_t>(r) * cols + c] = mom;
-      g = muon_u(g, mom, call.s);
-    }
-    sum = __fmaf_rn(g, g, sum);
-  });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
+  // momentum, and the sum of squares; once more over scaled values where the sum is out
+  // of range (all CTAs of the cluster see the same sum)
   __shared__ float warp_sum[kSmallWarps];
-  __shared__ NsScale shared_scale;
-  if (k.lane == 0) warp_sum[k.warp] = sum;
-  // rows and columns beyond the matrix are zero
-  for (int i = threadIdx.x; i < chunks * kChunk / 16; i += kSmallThreads) st_shared_v4(k.x + 16 * i, 0, 0, 0, 0);
-  __syncthreads();
-  if (threadIdx.x < ranks) {
-    float x = 0.0f;
+  __shared__ float shared_sum;
+  float pre = 1.0f, total;
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+    float sum = 0.0f;
+    for_values([&](int r, int c, float g, float mom) {
+      if (MOM) {
+        if (pass == 0) {
+          mom = new_momentum(mom, g, call.s);
+          it.mom[first_m + static_cast<int64_t>(r) * cols + c] = mom;
+        }
+        g = muon_u(g, mom, call.s);
+      }
+      g *= pre;
+      sum = __fmaf_rn(g, g, sum);
+    });
 #pragma unroll
-    for (int i = 0; i < kSmallWarps; ++i) x += warp_sum[i];
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::map_to_rank(sums + 4 * k.rank, threadIdx.x)), "f"(x));
-  }
-  __syncwarp();
-  tc::cluster_sync();
-  if (threadIdx.x == 0) {
-    float x = 0.0f;
-    for (int i = 0; i < ranks; ++i) {
-      float y;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(sums + 4 * i));
-      x += y;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
+    if (k.lane == 0) warp_sum[k.warp] = sum;
+    // rows and columns beyond the matrix are zero
+    if (pass == 0)
+      for (int i = threadIdx.x; i < chunks * kChunk / 16; i += kSmallThreads) st_shared_v4(k.x + 16 * i, 0, 0, 0, 0);
+    __syncthreads();
+    const uint32_t now = sums + 4 * kMaxCluster * pass;
+    if (threadIdx.x < ranks) {
+      float x = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kSmallWarps; ++i) x += warp_sum[i];
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::map_to_rank(now + 4 * k.rank, threadIdx.x)), "f"(x));
     }
-    shared_scale = ns_scale(x, call.s.eps);
+    __syncwarp();
+    tc::cluster_sync();
+    if (threadIdx.x == 0) {
+      float x = 0.0f;
+      for (int i = 0; i < ranks; ++i) {
+        float y;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(now + 4 * i));
+        x += y;
+      }
+      shared_sum = x;
+    }
+    __syncthreads();
+    total = shared_sum;
+    if (pass == 1 || ordinary_sum(total)) break;
+    pre = other_pre(total);
   }
-  __syncthreads();
-  const NsScale by = shared_scale;
+  const float inv = ns_inv(total, pre, call.s.eps);
   for_values([&](int r, int c, float g, float mom) {
     if (MOM) g = muon_u(g, mom, call.s);
     const int xr = tall ? c : r, xc = tall ? r : c;
-    st_shared16(k.x + (xc >> 6) * kChunk + chunk_at(xr, xc & 63), __half_as_ushort(__float2half_rn(g * by.pre * by.inv)));
+    st_shared16(k.x + (xc >> 6) * kChunk + chunk_at(xr, xc & 63), __half_as_ushort(__float2half_rn(g * pre * inv)));
   });
 
   bool pair = true;

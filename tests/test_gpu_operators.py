@@ -662,6 +662,64 @@ def test_orthogonalize_small_eps(rows, cols, eps):
     assert rel(low, ns_exact(x * 2.0 ** -50, eps=float(np.float32(eps)))) <= NS_TOL
 
 
+@pytest.mark.parametrize("rows,cols", [(100, 130), (128, 4000), (300, 1030), (1031, 301), (640, 512)])
+@pytest.mark.parametrize("scale,eps", [(2.0 ** 69, 1e-7), (2.0 ** 110, 1e-7), (2.0 ** 130, 1e-7), (2.0 ** -78, 1e-37),
+                                       (2.0 ** -105, 1e-45), (2.0 ** -90, 2.0 ** -95), (2.0 ** 100, 2.0 ** 100)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_orthogonalize_far_from_one(rows, cols, scale, eps, dtype):
+    """Entries whose squares leave the range of fp32 at either end; at 2^130 |U|_F leaves it too."""
+    x = (matrix_like(gen(51), rows, cols).double() * scale).to(DT[dtype])
+    assert torch.isfinite(x).all() and int(torch.count_nonzero(x)) > 0.99 * x.numel()
+    out, zero = ns_call([x, torch.zeros_like(x)], eps=eps)
+    assert rel(out, ns_exact(x, eps=float(np.float32(eps)))) <= NS_TOL and not zero.any()
+
+
+@pytest.mark.parametrize("rows,cols", [(90, 700), (700, 600)])
+def test_orthogonalize_of_mixed_magnitudes(rows, cols):
+    """Rows whose squares overflow, rows in the ordinary range, rows whose squares underflow, in one matrix; and
+    matrices of each kind in one call."""
+    x = matrix_like(gen(52), rows, cols)
+    third = rows // 3
+    parts = torch.ones(rows, 1, device="cuda")
+    parts[:third], parts[2 * third:] = 2.0 ** 80, 2.0 ** -80
+    mixed, low, high = x * parts, x.clone(), x.clone()
+    low[:third] *= 2.0 ** -70
+    high[0] *= 2.0 ** 75
+    xs = [mixed, low, high, x, x * 2.0 ** -110, x * 2.0 ** 90]
+    for got, a in zip(ns_call(xs, eps=1e-40), xs):
+        assert rel(got, ns_exact(a, eps=float(np.float32(1e-40)))) <= NS_TOL
+
+
+@pytest.mark.parametrize("fmt", ["L12", "L16F"])
+@pytest.mark.parametrize("scale", [2.0 ** 75, 2.0 ** -75])
+def test_muon_step_far_from_one(fmt, scale):
+    """Gradients and momentum far from one in matrices of the one-kernel form and of the tiled one."""
+    shapes = [(24, 96), (300, 403), (400, 304)]
+    layout = Layout([(f"m{i}", s, 0) for i, s in enumerate(shapes)], fmt)
+    blk = torch.zeros(layout.block_bytes(0), dtype=torch.uint8, device="cuda")
+    v = muon_views(layout, fmt, 0, blk)
+    g = gen(53)
+    for (_, off, n), shape in zip(layout.spans(0), shapes):
+        v["W"][off:off + n] = torch.randn(n, generator=g, device="cuda") * 0.02
+        for f in ("G", "M"):
+            v[f][off:off + n] = (matrix_like(g, *shape) * scale).reshape(-1)
+    old = {f: x.clone() for f, x in v.items()}
+    ws = scratch(lst.lst_muon_workspace_bytes(layout.handle))
+    hp = lst.muon_hparams(lr=2e-2, momentum=0.9, weight_decay=0.1, rms_scale=0.2, eps=1e-40)
+    lst.lst_muon_step(layout.handle, [blk.data_ptr()], hp, None, None, ws.data_ptr(), ws.numel(), stream())
+    lst.lst_operator_status()
+    for (name, off, n), shape in zip(layout.spans(0), shapes):
+        s = slice(off, off + n)
+        m = (old["M"][s] * np.float32(0.9)) + old["G"][s].float()
+        assert torch.equal(v["M"][s], m), name  # once, although its sum of squares is taken twice
+        u = old["G"][s].double() + float(np.float32(0.9)) * m.double()
+        o = ns_exact(u.view(shape), eps=float(np.float32(1e-40))).reshape(-1)
+        rms, w0 = 0.2 * math.sqrt(max(shape)), old["W"][s].double()
+        w = w0 * (1 - 2e-2 * 0.1) - 2e-2 * rms * o
+        limit = NS_TOL * 2e-2 * rms * o.norm() + 4 * U32 * (w0.norm() + w.norm()) + (U16 * w.norm() if fmt == "L12" else 0.0)
+        assert float((v["W"][s].double() - w).norm()) <= float(limit), name
+
+
 def test_orthogonalize_decaying_singular_values():
     """Values falling as 1/i over three decades: the smallest are still growing after five steps, by 3.45 a step, and
     so is their rounding: one more factor of 1.6 in the bound."""
