@@ -226,6 +226,23 @@ def test_embed_grad_largest_vocabulary(vocab):
     assert int(torch.count_nonzero(grad)) == 6
 
 
+@pytest.mark.parametrize("n", [16384, 65521])
+@pytest.mark.parametrize("vocab", [511, 512, 600, 1023, 262143, 262144, 300000, 1048575])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad_wide_digits(n, vocab, accumulate):
+    """Digits of 9 and 10 bits, one or two passes, in the sort of many tokens: its largest shared memory."""
+    hidden = 8
+    g = gen(n + vocab)
+    t = (torch.rand(n, generator=g, device="cuda", dtype=torch.float64) ** 2 * (vocab + 1)).long()  # vocab itself is outside
+    dout = torch.randint(-8, 9, (n, hidden), generator=g, device="cuda").float()
+    before = torch.randint(-8, 9, (vocab, hidden), generator=g, device="cuda").float()
+    grad = before.clone()
+    ws = scratch(lst.lst_embed_grad_workspace_bytes(n, hidden, vocab))
+    lst.lst_embed_grad(lst.matrix(dout), lst.indices(t), lst.matrix(grad), 1.0, accumulate, ws.data_ptr(), ws.numel(), stream())
+    exact = torch.zeros(vocab + 1, hidden, dtype=torch.float64, device="cuda").index_add_(0, t, dout.double())[:vocab]
+    assert torch.equal(grad.double(), exact + before.double() if accumulate else exact)  # whole numbers
+
+
 @pytest.mark.parametrize("n", [100, 20000])
 def test_embed_grad_from_two_threads(n):
     """Sorts with much and with little shared memory, launched by two host threads on streams of their own."""
@@ -849,6 +866,98 @@ def test_muon_step_more_tiles_than_pairs(fmt):
         if fmt == "L16M":
             assert torch.equal(v["W"][s], v["MASTER"][s].bfloat16())
     assert not v["M"][~covered].any() and not v[field][~covered].any()
+
+
+# Roundings that do not line up add by their squares: a value rounded to fp16 is off by 0.4 uh (rms, over a binade);
+# six such in a step, passed on with a factor of 1.6 from step to step, give 0.4 uh sqrt(6 sum 1.6^2k), k = 0..4, and
+# the result's rounding to bf16 0.4 u16: 4.3e-3, taken as 5e-3.
+NS_TIGHT = 5e-3
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 200), (128, 128), (128, 1000), (200, 64), (136, 144), (256, 256), (256, 1030), (300, 1030),
+                                       (1030, 300), (513, 2049), (1600, 900)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_orthogonalize_coefficients(rows, cols, dtype):
+    """Near enough that a coefficient off by 0.005 would show."""
+    x = matrix_like(gen(60), rows, cols).to(DT[dtype])
+    assert rel(ns_call([x])[0], ns_exact(x)) <= NS_TIGHT
+
+
+def test_orthogonalize_tolerance_tells_coefficients():
+    """What the bound above refuses: the definition in 64 bits with one coefficient changed."""
+    x = matrix_like(gen(60), 300, 1030).cpu()
+    exact = ns_exact(x)
+    global COEF
+    kept = COEF
+    try:
+        for i, d in ((0, 0.005), (0, -0.005), (1, 0.01), (1, -0.01), (2, 0.01), (2, -0.01)):
+            COEF = tuple(c + (d if k == i else 0.0) for k, c in enumerate(kept))
+            assert rel(ns_exact(x), exact) > 2 * NS_TIGHT
+    finally:
+        COEF = kept
+
+
+def muon_shapes(shapes, fmt, seed):
+    layout = Layout([(f"m{i}", s, 0) for i, s in enumerate(shapes)], fmt)
+    blk = torch.zeros(layout.block_bytes(0), dtype=torch.uint8, device="cuda")
+    v = muon_views(layout, fmt, 0, blk)
+    g = gen(seed)
+    for (_, off, n), shape in zip(layout.spans(0), shapes):
+        v["MASTER" if fmt == "L16M" else "W"][off:off + n] = torch.randn(n, generator=g, device="cuda") * 0.02
+        for f in ("G", "M"):
+            v[f][off:off + n] = matrix_like(g, *shape).reshape(-1)
+    return layout, blk
+
+
+def muon_check(layout, fmt, shapes, old_blk, blk):
+    """Weights, momenta and derived weights of a step with lr 0.02, momentum 0.9, decay 0.1, rms scale 0.2, nesterov."""
+    old, new = muon_views(layout, fmt, 0, old_blk), muon_views(layout, fmt, 0, blk)
+    field = "MASTER" if fmt == "L16M" else "W"
+    for (name, off, n), shape in zip(layout.spans(0), shapes):
+        s = slice(off, off + n)
+        m = (old["M"][s] * np.float32(0.9)) + old["G"][s].float()
+        assert torch.equal(new["M"][s], m), name
+        o = ns_exact((old["G"][s].double() + float(np.float32(0.9)) * m.double()).view(shape)).reshape(-1)
+        rms, w0 = 0.2 * math.sqrt(max(shape)), old[field][s].double()
+        w = w0 * (1 - 2e-2 * 0.1) - 2e-2 * rms * o
+        limit = NS_TIGHT * 2e-2 * rms * o.norm() + 4 * U32 * (w0.norm() + w.norm()) + (U16 * w.norm() if fmt == "L12" else 0.0)
+        assert float((new[field][s].double() - w).norm()) <= float(limit), name
+        if fmt == "L16M":
+            assert torch.equal(new["W"][s], new["MASTER"][s].bfloat16())
+
+
+def muon_call(layout, blk, ws_bytes):
+    ws = scratch(ws_bytes)
+    hp = lst.muon_hparams(lr=2e-2, momentum=0.9, weight_decay=0.1, rms_scale=0.2, nesterov=True)
+    lst.lst_muon_step(layout.handle, [blk.data_ptr()], hp, None, None, ws.data_ptr(), ws.numel(), stream())
+    lst.lst_operator_status()
+
+
+@pytest.mark.parametrize("fmt", ["L12", "L16M", "L16F"])
+@pytest.mark.parametrize("shapes", [[(300, 404)] * 3 + [(404, 300)] * 2 + [(300, 403)] * 2 + [(24, 96)] * 3 + [(96, 24)],
+                                    [(136, 144)] * 70 + [(24, 40)] * 60, [(700, 200)] * 2 + [(150, 1700)] * 3])
+def test_muon_several_matrices_of_a_shape(fmt, shapes):
+    """Every matrix of a batch gets its own update: more of a shape than the tables of a launch hold, too."""
+    layout, blk = muon_shapes(shapes, fmt, 61)
+    old = blk.clone()
+    muon_call(layout, blk, lst.lst_muon_workspace_bytes(layout.handle))
+    muon_check(layout, fmt, shapes, old, blk)
+
+
+@pytest.mark.parametrize("fmt", ["L12", "L16M", "L16F"])
+def test_muon_fewer_matrices_at_a_time(fmt):
+    """Tiled matrices in a workspace for one, for some and for all of them; the same workspace gives the same bits."""
+    shapes = [(300, 404)] * 3 + [(404, 300)] * 2 + [(200, 520), (300, 403)]
+    layout, blk = muon_shapes(shapes, fmt, 62)
+    largest = max(lst.lst_orthogonalize_workspace_bytes(1, *s) for s in shapes)
+    full = lst.lst_muon_workspace_bytes(layout.handle)
+    assert full > 4 * largest
+    for size in (largest, 2 * largest + 100, full // 2, full):
+        new, again = blk.clone(), blk.clone()
+        muon_call(layout, new, size)
+        muon_check(layout, fmt, shapes, blk, new)
+        muon_call(layout, again, size)
+        assert torch.equal(new, again)
 
 
 def test_muon_mask_and_no_adamw():
