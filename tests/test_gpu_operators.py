@@ -1046,6 +1046,113 @@ def test_operators_on_a_side_stream_and_in_a_graph():
         assert torch.equal(out, ref_o) and torch.isfinite(emb).all()
 
 
+def bits(t):
+    return t.contiguous().view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32)
+
+
+@pytest.mark.parametrize("pad,shift", [(3, 0), (8, 0), (1, 5), (16, 8)])
+@pytest.mark.parametrize("hidden", [72, 77, 1032])
+def test_results_leave_the_space_between_rows_alone(hidden, pad, shift):
+    """Every result with padded rows, on and off 16 bytes: what lies before, between and behind the rows keeps its bits."""
+    n, vocab = 133, 301
+    x, w, t = xent_inputs(n, hidden, vocab, seed=70)
+    tokens = torch.randint(0, vocab, (n,), generator=gen(71), device="cuda")
+    ws = scratch(max(lst.lst_xent_workspace_bytes(n, hidden, vocab, True), lst.lst_embed_grad_workspace_bytes(n, hidden, vocab),
+                     lst.lst_orthogonalize_workspace_bytes(1, n, hidden)))
+
+    def result(rows, dtype):
+        size = shift + rows * (hidden + pad) + 8
+        buf = torch.full((size,), -7.0, dtype=DT[dtype], device="cuda")
+        inside = torch.zeros(size, dtype=torch.bool, device="cuda")
+        inside[shift:shift + rows * (hidden + pad)].view(rows, hidden + pad)[:, :hidden] = True
+        return buf, buf[shift:shift + rows * (hidden + pad)].view(rows, hidden + pad)[:, :hidden], inside
+
+    def check(made, what):
+        torch.cuda.synchronize()
+        for buf, view, inside in made:
+            assert torch.equal(bits(buf[~inside]), bits(torch.full_like(buf[~inside], -7.0))), what
+            assert torch.isfinite(view).all(), what
+
+    for dtype in ("bf16", "f32"):
+        out, grad = result(n, dtype), result(vocab, dtype)
+        lst.lst_embed(lst.matrix(w), lst.indices(tokens), lst.matrix(out[1]), 1.0, stream())
+        lst.lst_embed_grad(lst.matrix(x), lst.indices(tokens), lst.matrix(grad[1]), 1.0, False, ws.data_ptr(), ws.numel(), stream())
+        check((out, grad), "embed " + dtype)
+        lst.lst_embed_grad(lst.matrix(x), lst.indices(tokens), lst.matrix(grad[1]), 1.0, True, ws.data_ptr(), ws.numel(), stream())
+        check((grad,), "embed, added " + dtype)
+    dx, dw, o = result(n, "bf16"), result(vocab, "bf16"), result(n, "bf16")
+    loss, lse, mean = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda"), torch.zeros(1, device="cuda")
+    for accumulate in (False, True):
+        lst.lst_xent_grad(lst.matrix(x), lst.matrix(w), lst.indices(t), IGNORE, 1.0, loss.data_ptr(), lse.data_ptr(), mean.data_ptr(),
+                          lst.matrix(dx[1]), lst.matrix(dw[1]), accumulate, ws.data_ptr(), ws.numel(), stream())
+        check((dx, dw), f"xent {accumulate}")
+    lst.lst_orthogonalize([lst.matrix(x)], [lst.matrix(o[1])], lst.ns_params(), ws.data_ptr(), ws.numel(), stream())
+    check((o,), "orthogonalize")
+
+
+@pytest.mark.parametrize("ignore", [0, 17, -1, 2 ** 40])
+@pytest.mark.parametrize("n", [50, 200])
+def test_xent_ignore_index_inside_the_vocabulary(n, ignore):
+    """Targets equal to the index are ignored wherever it lies; -100 is then an ordinary target outside the vocabulary."""
+    hidden, vocab = 64, 300
+    x, w, t = xent_inputs(n, hidden, vocab, seed=72, ignored=0.0)
+    t[::5] = ignore
+    # the definition ignores IGNORE
+    e = xent_exact(x, w, torch.where(t == ignore, IGNORE, t))
+    loss, lse, mean = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda"), torch.zeros(1, device="cuda")
+    dx, dw = torch.zeros_like(x), torch.zeros_like(w)
+    ws = scratch(lst.lst_xent_workspace_bytes(n, hidden, vocab, True))
+    lst.lst_xent_grad(lst.matrix(x), lst.matrix(w), lst.indices(t), ignore, 1.0, loss.data_ptr(), lse.data_ptr(), mean.data_ptr(),
+                      lst.matrix(dx), lst.matrix(dw), False, ws.data_ptr(), ws.numel(), stream())
+    xent_check(dict(loss=loss, lse=lse, mean=mean, dx=dx, dw=dw), e)
+    t[1] = -100
+    lst.lst_xent_loss(lst.matrix(x), lst.matrix(w), lst.indices(t), ignore, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(),
+                      stream())
+    assert torch.isnan(loss[1]) and int(torch.isnan(loss).sum()) == 1
+
+
+def test_muon_and_embedding_in_a_graph_and_on_a_side_stream():
+    shapes = [(300, 404), (300, 404), (404, 300), (24, 96), (64,)]
+    layout = Layout([(f"m{i}", s, 0) for i, s in enumerate(shapes)], "L16M")
+    blk = torch.zeros(layout.block_bytes(0), dtype=torch.uint8, device="cuda")
+    v = muon_views(layout, "L16M", 0, blk)
+    g = gen(73)
+    for _, off, n in layout.spans(0):
+        for f in ("MASTER", "G", "M"):
+            v[f][off:off + n] = torch.randn(n, generator=g, device="cuda") * 0.01
+    tokens = torch.randint(0, 50, (20000,), generator=g, device="cuda")
+    table = randn(g, 50, 24, dtype="bf16")
+    ws = scratch(max(lst.lst_muon_workspace_bytes(layout.handle), lst.lst_embed_grad_workspace_bytes(20000, 24, 50)))
+    hp, ahp = lst.muon_hparams(lr=0.02), lst.adamw_hparams(step=3)
+    out, grad = torch.zeros(20000, 24, dtype=torch.bfloat16, device="cuda"), torch.zeros(50, 24, device="cuda")
+
+    def step(block):
+        lst.lst_muon_step(layout.handle, [block.data_ptr()], hp, ahp, None, ws.data_ptr(), ws.numel(), stream())
+        lst.lst_embed(lst.matrix(table), lst.indices(tokens), lst.matrix(out), 0.5, stream())
+        lst.lst_embed_grad(lst.matrix(out), lst.indices(tokens), lst.matrix(grad), 0.5, False, ws.data_ptr(), ws.numel(), stream())
+
+    ref = blk.clone()
+    step(ref)
+    ref_out, ref_grad = out.clone(), grad.clone()
+    side, cur = torch.cuda.Stream(), blk.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out.zero_(), grad.zero_()
+        step(cur)
+    side.synchronize()
+    assert torch.equal(cur, ref) and torch.equal(out, ref_out) and torch.equal(grad, ref_grad)
+    cur = blk.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(cur)
+    for _ in range(2):
+        cur.copy_(blk), out.zero_(), grad.zero_(), ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(cur, ref) and torch.equal(out, ref_out) and torch.equal(grad, ref_grad)
+    lst.lst_operator_status()
+
+
 def test_example_trains():
     """The example's loss falls from about ln(1000) to near the noise floor of its data."""
     sys.path.insert(0, os.path.join(ROOT, "examples"))
