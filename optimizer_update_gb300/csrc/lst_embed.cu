@@ -519,7 +519,8 @@ extern "C" lst_status lst_embed(const lst_matrix* table, const lst_indices* toke
 }
 
 extern "C" int64_t lst_embed_grad_workspace_bytes(int64_t count, int64_t hidden, int64_t vocab) {
-  if (count < 0 || hidden < 0 || vocab < 0 || count > (int64_t(1) << 30) || vocab > (int64_t(1) << 30)) return 0;
+  if (count < 0 || hidden < 0 || vocab < 0 || count > (int64_t(1) << 30) || vocab > (int64_t(1) << 30) || hidden > INT32_MAX)
+    return 0;
   const GradPlan p = grad_plan(count, hidden, vocab);
   if (p.run != kMaxRun) return p.bytes;
   // fewer tokens in runs of 8 leave more parts: the most that do

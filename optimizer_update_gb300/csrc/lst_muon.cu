@@ -524,6 +524,8 @@ cudaError_t ingest(const std::vector<Item>& items, bool f32, bool mom, const NsM
   return cudaSuccess;
 }
 
+// No device holds a matrix of more elements; sizes up to here stay within 64 bits.
+constexpr int64_t kMaxElems = int64_t(1) << 40;
 // A workspace for all matrices at once, or for as many as 4 GiB hold, at least one.
 constexpr int64_t kMaxBatchBytes = int64_t(4) << 30;
 
@@ -533,7 +535,7 @@ constexpr int64_t kMaxBatchBytes = int64_t(4) << 30;
 using namespace lst;
 
 extern "C" int64_t lst_orthogonalize_workspace_bytes(int32_t count, int64_t rows, int64_t cols) {
-  if (count <= 0 || rows <= 0 || cols <= 0) return 0;
+  if (count <= 0 || rows <= 0 || cols <= 0 || rows > INT32_MAX || cols > INT32_MAX || rows > kMaxElems / cols) return 0;
   const Shape2 s = {rows, cols};
   const int64_t fit = std::max<int64_t>(1, kMaxBatchBytes / Batch::item_bytes(s));
   return std::min<int64_t>(count, fit) * Batch::item_bytes(s);
@@ -560,6 +562,7 @@ extern "C" lst_status lst_orthogonalize(int32_t count, const lst_matrix* in, con
   }
   if (in[0].rows == 0 || in[0].cols == 0) return LST_OK;
   const Shape2 shape = {in[0].rows, in[0].cols};
+  if (shape.rows > kMaxElems / shape.cols) return fail(LST_ERR_INVALID_ARG, "%s: matrix of more than 2^40 elements", who);
   LST_TRY(check_workspace(workspace, workspace_bytes, Batch::item_bytes(shape), who));
   if (ns_small_fits(shape.rows, shape.cols)) {
     const NsSmallCall call = {shape.rows, shape.cols, in[0].dtype == LST_F32, -1, params->steps, 1.0f, {0.0f, params->eps, 0}};

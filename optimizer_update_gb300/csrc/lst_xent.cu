@@ -395,6 +395,13 @@ int64_t plan_bytes(int64_t n, int64_t h, int64_t v, bool grad, bool pack_x, bool
   return bytes + size(n * ld * 2) + size(rows * ops_round_up(h, 32) * 4 + 256) + size(q);
 }
 
+// Sizes that the calls take (and whose workspace is counted in 64 bits: no device holds a
+// w of more than 2^40 elements).
+bool sizes_fit(int64_t n, int64_t h, int64_t v) {
+  return n > 0 && h > 0 && v > 0 && n <= (int64_t(1) << 24) && v <= INT32_MAX && h <= INT32_MAX && v <= (int64_t(1) << 40) / h &&
+         n <= (int64_t(1) << 40) / h;
+}
+
 // A matrix of rows; `transposed`: the product sums over its rows.
 GemmOperand rows_operand(const void* ptr, int64_t rows, int64_t cols, int64_t ld, bool transposed = false) {
   return {ptr, cols, rows, ld, transposed};
@@ -414,6 +421,8 @@ lst_status check_xw(const lst_matrix* x, const lst_matrix* w, const lst_indices*
     return fail(LST_ERR_INVALID_ARG, "%s: x must be targets x hidden, w vocabulary x hidden", who);
   if (w->rows == 0 || w->cols == 0) return fail(LST_ERR_INVALID_ARG, "%s: empty vocabulary or hidden size", who);
   if (x->rows > (int64_t(1) << 24)) return fail(LST_ERR_INVALID_ARG, "%s: more than 2^24 targets", who);
+  if (x->rows > 0 && !sizes_fit(x->rows, x->cols, w->rows))
+    return fail(LST_ERR_INVALID_ARG, "%s: x or w of more than 2^40 elements", who);
   return LST_OK;
 }
 
@@ -486,16 +495,13 @@ struct Call {
 using namespace lst;
 
 extern "C" int64_t lst_xent_workspace_bytes(int64_t count, int64_t hidden, int64_t vocab, int32_t with_grad) {
-  if (count <= 0 || hidden <= 0 || vocab <= 0 || count > (int64_t(1) << 24) || vocab > INT32_MAX || hidden > INT32_MAX)
-    return 0;
+  if (!sizes_fit(count, hidden, vocab)) return 0;
   const bool pack = hidden % 8 != 0;  // contiguous rows of such a length are off 16 bytes
   return plan_bytes(count, hidden, vocab, with_grad != 0, pack, pack);
 }
 
 extern "C" int64_t lst_xent_workspace_bytes_for(const lst_matrix* x, const lst_matrix* w, int32_t with_grad) {
-  if (!x || !w || x->rows <= 0 || w->rows <= 0 || x->cols <= 0 || x->cols != w->cols || x->rows > (int64_t(1) << 24) ||
-      w->rows > INT32_MAX || x->cols > INT32_MAX)
-    return 0;
+  if (!x || !w || x->cols != w->cols || !sizes_fit(x->rows, x->cols, w->rows)) return 0;
   return plan_bytes(x->rows, x->cols, w->rows, with_grad != 0, !tile_ready(x), !tile_ready(w));
 }
 

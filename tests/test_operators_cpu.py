@@ -172,6 +172,20 @@ def test_embed_grad_workspace_serves_smaller_counts(L, hidden):
     refused(L, 1, L.lst_embed_grad, *args, need - 257 if hidden < 3000000 else 1000)
 
 
+def test_sizes_past_64_bits(L):
+    """Sizes that no memory holds: no workspace of a size that wrapped around, and a refusal instead of a call with it."""
+    top, big = (1 << 31) - 1, 1 << 30
+    for rows, cols in ((1 << 40, 1 << 40), (top, top), (top + 1, 1), (1, top + 1), (1 << 62, 4)):
+        assert L.lst_orthogonalize_workspace_bytes(1, rows, cols) == 0
+    assert L.lst_xent_workspace_bytes(4, top, top, True) == 0 and L.lst_xent_workspace_bytes(4, 8, top + 1, False) == 0
+    assert L.lst_embed_grad_workspace_bytes(4, top + 1, 8) == 0 and L.lst_embed_grad_workspace_bytes(1 << 30, 1 << 62, 8) == 0
+    assert L.lst_orthogonalize_workspace_bytes(1, top, 64) > top * 64 * 2 and L.lst_embed_grad_workspace_bytes(1 << 30, 4096, 8) > 0
+    assert L.lst_xent_workspace_bytes(1 << 24, 4096, 131072, True) > 0
+    m = mat(L, top, top)
+    refused(L, L.LST_ERR_INVALID_ARG, L.lst_orthogonalize, [m], [m], L.ns_params(), P, big)
+    refused(L, L.LST_ERR_INVALID_ARG, L.lst_xent_loss, mat(L, 4, top), m, idx(L, 4), -100, P, P, P, big)
+
+
 def test_tensor_arguments(L):
     import torch
     x = torch.zeros(6, 10)
