@@ -20,8 +20,8 @@ struct GemmOperand {
 
 // out = alpha * acc + beta * c (+ diag on the main diagonal), rounded to fp16
 // or bf16; c has out's shape, pitch and type; alpha times *scale where that is
-// not null (device memory). `vec`: bytes a store may be
-// wide (32, 16 or 2) by out's alignment.
+// not null (device memory). `vec`: 16 where out's and
+// c's rows start on 16 bytes, otherwise 2.
 struct StoreParams {
   void* out;
   const void* c;

@@ -382,7 +382,7 @@ struct Runner {
     return {ws + c.s_off[k] + first * c.m * c.lds * 2, c.m, c.m, c.lds, false, count, c.m * c.lds};
   }
   static StoreParams s_store(const Batch::Class& c, void* out, const void* cc, float alpha, float beta, float diag) {
-    return {out, cc, c.lds, c.m * c.lds, alpha, beta, diag, 0, 32};
+    return {out, cc, c.lds, c.m * c.lds, alpha, beta, diag, 0, 16};
   }
 
   // A = X X^T (or X^T X) into stack 0
@@ -440,7 +440,7 @@ struct Runner {
     for (size_t i = b.groups.size(); i-- > 0;) {
       const Batch::Group& g = b.groups[i];
       pending.push_back(applied(g, s, x_in, 0, g.count));
-      pending.back().store = {ws + g.x_off[x_out], nullptr, g.ldx, g.x_elems(), 1.0f / scale, 0.0f, 0.0f, 0, 32};
+      pending.back().store = {ws + g.x_off[x_out], nullptr, g.ldx, g.x_elems(), 1.0f / scale, 0.0f, 0.0f, 0, 16};
     }
     return flush(GEMM_F16);
   }
@@ -608,7 +608,7 @@ extern "C" lst_status lst_orthogonalize(int32_t count, const lst_matrix* in, con
       for (int64_t i = 0; i < n; ++i) {
         const lst_matrix& dst = out[first + i];
         const uintptr_t align = reinterpret_cast<uintptr_t>(dst.data) | static_cast<uintptr_t>(dst.stride * 2);
-        const int vec = align % 32 == 0 ? 32 : align % 16 == 0 ? 16 : 2;
+        const int vec = align % 16 == 0 ? 16 : 2;
         run.pending.push_back(run.applied(g, si, xi, i, 1));
         run.pending.back().store = {dst.data, nullptr, dst.stride, 0, 1.0f / (scale * kScaleX), 0.0f, 0.0f, 1, vec};
       }

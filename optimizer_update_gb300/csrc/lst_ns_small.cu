@@ -2,7 +2,8 @@
 // on the short side, 4096 on the long one.
 //
 // The tiled path (lst_muon.cu, lst_gemm.cu) takes 11 dependent launches, about
-// 90 us however small the matrix; this kernel 25 to 30. Here a cluster of 1 to 8 CTAs keeps the whole
+// 90 us however small the matrix; this kernel 15 us for 16 x 16, 27 for 64 x 300, 46
+// for 128 x 1000 and 80 for 128 x 4096. Here a cluster of 1 to 8 CTAs keeps the whole
 // matrix and the iteration on chip. With X (m x n, m <= 128 <= n, a tall matrix
 // transposed on its way in and out) each CTA holds a slice of up to 512 columns
 // of X in shared memory, in fp16, and its own copies of the m x m matrices:

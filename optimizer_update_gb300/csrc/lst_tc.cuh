@@ -72,9 +72,9 @@ __device__ __forceinline__ uint64_t global_ns() {
 }
 
 // Every wait of the matrix kernels has an end: after kWaitLimitNs it returns
-// false, the kernel records that in its error word and all its roles leave
-// (see lst_gemm.cuh), so a wrong count can never hang the GPU. The longest
-// legitimate wait is one tile's main loop, well under a millisecond.
+// false, the kernel records that in its error word and all its roles leave (the
+// end of gemm_kernel in lst_gemm.cu), so a wrong count can never hang the GPU. The
+// longest legitimate wait is one tile's main loop, well under a millisecond.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 __device__ __noinline__ inline bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
   const uint64_t start = global_ns();

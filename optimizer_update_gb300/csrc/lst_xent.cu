@@ -409,7 +409,7 @@ GemmOperand rows_operand(const void* ptr, int64_t rows, int64_t cols, int64_t ld
 
 int store_width(const lst_matrix* m) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(m->data) | static_cast<uintptr_t>(m->stride * 2);
-  return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 2;
+  return a % 16 == 0 ? 16 : 2;
 }
 
 lst_status check_xw(const lst_matrix* x, const lst_matrix* w, const lst_indices* targets, const char* who) {
