@@ -506,15 +506,17 @@ LST_API lst_status lst_store_step(lst_store* store, void* const* staging, void* 
  * ------------------------------------------------------------------------ */
 typedef enum lst_dtype { LST_BF16 = 0, LST_F32 = 1 } lst_dtype;
 
-/* rows x cols elements; row r starts at data + r * stride elements
-   (stride >= cols). data is aligned to its element. */
+/* rows x cols elements, each at most 2^31 - 1; row r starts at data + r * stride
+   elements (cols <= stride <= 2^36; rows do not overlap). data is aligned to its
+   element. */
 typedef struct lst_matrix {
   void* data;
   int64_t rows, cols, stride;
   int32_t dtype;
 } lst_matrix;
 
-/* count token indices, device memory, signed, 32 or 64 bits each. */
+/* count (at most 2^30) token indices, device memory, signed, 32 or 64 bits
+   each. */
 typedef struct lst_indices {
   const void* data;
   int64_t count;
@@ -557,10 +559,11 @@ LST_API lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* tok
    targets that are not ignored, and the gradients of grad_scale * mean:
      dx = grad_scale/N * (softmax(l) - onehot) w      count x hidden, bf16
      dw = grad_scale/N * (softmax(l) - onehot)^T x    vocab x hidden, bf16
-   (N = targets not ignored; mean, dx and dw are zero where N = 0; dw is added
-   to what it holds, with one rounding, when accumulate_dw is set). dw is for
-   instance the head's range of a block's G segment. Rows of x whose target is
-   ignored do not reach dw, whatever they hold.
+   (N = targets not ignored; mean, dx and dw are zero where N = 0 and w is
+   finite; the mean is NaN where a loss is; dw is added to what it holds, with
+   one rounding, when accumulate_dw is set). dw is for instance the head's range
+   of a block's G segment. Rows of x whose target is ignored do not reach dw,
+   whatever they hold.
    The vocabulary is worked through in pieces of as many columns as the
    workspace holds at 2 bytes per token and column; lst_xent_workspace_bytes
    gives the size for one piece, at most 1 GiB of them, beyond which the
@@ -572,7 +575,8 @@ LST_API lst_status lst_embed_grad(const lst_matrix* dout, const lst_indices* tok
    size; lst_xent_workspace_bytes_for gives the size for x and w as they lie,
    with any data pointer and stride (0 for sizes that the calls refuse). Either
    size serves smaller counts as well.
-   workspace: 256-byte aligned. Errors otherwise as lst_embed. */
+   workspace: 256-byte aligned. Errors otherwise as lst_embed, plus
+   LST_ERR_INVALID_ARG for more than 2^24 targets. */
 LST_API int64_t lst_xent_workspace_bytes(int64_t count, int64_t hidden, int64_t vocab, int32_t with_grad);
 LST_API int64_t lst_xent_workspace_bytes_for(const lst_matrix* x, const lst_matrix* w, int32_t with_grad);
 LST_API lst_status lst_xent_loss(const lst_matrix* x, const lst_matrix* w, const lst_indices* targets,
@@ -619,10 +623,13 @@ LST_API lst_status lst_orthogonalize(int32_t count, const lst_matrix* in, const 
    alone when adamw is NULL. Padding is not touched.
    workspace: lst_muon_workspace_bytes() bytes, 256-byte aligned; a smaller one
    means fewer matrices at a time, LST_ERR_INVALID_ARG where the largest does
-   not fit. dev_blocks as in lst_adamw_step. Errors as lst_adamw_step, plus
-   LST_ERR_INVALID_ARG for muon hyperparameters outside their domain (lr,
-   weight_decay finite, 0 <= momentum < 1, rms_scale >= 0, eps > 0,
-   1 <= ns_steps <= 20) or a use_muon entry on a tensor that is not a matrix. */
+   not fit (results are the same bits on every run with the same size; another
+   size may round the matrices differently, since steps are paired for those
+   that run together). dev_blocks as in lst_adamw_step. Errors as
+   lst_adamw_step, plus LST_ERR_INVALID_ARG for muon hyperparameters outside
+   their domain (lr, weight_decay finite, 0 <= momentum < 1, rms_scale >= 0,
+   eps > 0, 1 <= ns_steps <= 20) or a use_muon entry on a tensor that is not a
+   matrix. */
 typedef struct lst_muon_hparams {
   float lr, momentum, weight_decay, rms_scale, eps;
   int32_t nesterov, ns_steps;
