@@ -365,7 +365,9 @@ __global__ void __launch_bounds__(kSumThreads)
 }
 
 // A run that leaves the CTA it began in: its first part, then the parts of the
-// following CTAs in order.
+// following CTAs in order. Bound by latency where one token is frequent: all parts of
+// its run are one CTA's per 1024 columns (65521 tokens of 4096 bf16 columns, added:
+// 217 us uniform, 598 with one token on half of them, 879 with one on all).
 template <class TG, bool VEC>
 __global__ void __launch_bounds__(kSumThreads)
     join_kernel(const uint2* __restrict__ sorted, int n, int vocab, int hidden, int slices, int run, int chunks,
