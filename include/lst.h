@@ -592,7 +592,8 @@ LST_API lst_status lst_xent_grad(const lst_matrix* x, const lst_matrix* w, const
    A = X X^T and (a, b, c) = (3.4445, -4.7750, 2.0315), which takes every
    singular value of U that is not negligible to about 1 and keeps the singular
    vectors. Products are formed from fp16 values scaled by powers of two, with
-   fp32 sums; see lst_muon.cu. in[i], out[i]: `count` matrices of one shape;
+   fp32 sums: the result is about 2e-3 from the 64-bit one in the Frobenius norm,
+   a matrix of a few rows now and then some hundredths; see lst_muon.cu. in[i], out[i]: `count` matrices of one shape;
    in bf16 or fp32 (all the same), out bf16. Entries may be of any finite size.
    A zero matrix gives zero; a matrix with a NaN or infinity gives values of no
    meaning for itself only. 1 <= steps <= 20, eps > 0.
