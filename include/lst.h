@@ -640,6 +640,104 @@ LST_API lst_status lst_muon_step(const lst_layout* layout, void* const* dev_bloc
                                  const lst_adamw_hparams* adamw, const uint8_t* use_muon, void* workspace,
                                  int64_t workspace_bytes, void* cuda_stream);
 
+/* ---- between the layers: residual norms and 8-bit activation checkpoints ----
+ *
+ * An activation checkpoint: rows x cols values in 8 bits, kept from the forward
+ * for the backward pass. Row r has its values at data + r * stride, one byte each,
+ * and a byte for every 32 of them at scales + r * scale_stride. A block of 32
+ * stands for value * 2^(byte - 127): signed integers of -127..127, or e4m3 floats
+ * up to 448, with the smallest power of two that holds the block's largest
+ * magnitude (not below 2^-127), rounded to nearest, ties to even. A block that
+ * holds an infinity or NaN has the byte 255 and stands for NaN.
+ * data is 16-byte aligned and stride a multiple of 16 (>= cols); the memory of
+ * the last row, too, reaches to the next multiple of 16 bytes (read, never
+ * written; what it holds does not matter). scales: any address,
+ * scale_stride >= ceil(cols / 32). cols a multiple of 32 apart, columns of a
+ * wider checkpoint can be taken as one of their own. */
+typedef enum lst_checkpoint_format { LST_CHECKPOINT_I8 = 0, LST_CHECKPOINT_E4M3 = 1 } lst_checkpoint_format;
+typedef struct lst_checkpoint {
+  void* data;
+  void* scales;
+  int64_t rows, cols, stride, scale_stride;
+  int32_t format;
+} lst_checkpoint;
+
+/* out = the checkpoint of x (bf16 or fp32), and out = the values c stands for
+   (bf16, where every normal value is exact, or fp32, where every one is). Shapes
+   match; rows may be 0. Errors: LST_ERR_INVALID_ARG, LST_ERR_ALIGNMENT (data not
+   aligned to its element, a checkpoint's rows not on 16 bytes), LST_ERR_CUDA. */
+LST_API lst_status lst_checkpoint_save(const lst_matrix* x, const lst_checkpoint* out, void* cuda_stream);
+LST_API lst_status lst_checkpoint_restore(const lst_checkpoint* c, const lst_matrix* out, void* cuda_stream);
+
+/* The residual stream from one layer to the next, with a norm on either side of
+   the block between them:
+     u = y * rsqrt(mean(y^2) + eps) * w_post      (u = y where w_post is null)
+     h = residual_scale * x + branch_scale * gate * u
+     z = h * rsqrt(mean(h^2) + eps) * w_pre       (means over a row)
+   x, y, h, z: tokens x hidden, all bf16 or all fp32. w_post, w_pre: 1 x hidden,
+   gate: rows x hidden with rows a divisor of the tokens (1: a gate per channel;
+   one per sample; one per token), token i taking row i / (tokens / rows); null for
+   no gate; bf16 or fp32 each.
+   y may be null (no block: h = residual_scale * x; gate, w_post and y8 null too).
+   h may be null where only z or h8 is wanted; z and w_pre are both null or neither.
+   Everything is formed in fp32 and each result rounded once (z from the unrounded
+   h). h may be x, and z may be y (the same memory and stride); other outputs may
+   not overlap anything. Sums of squares are fp32: rows whose mean square leaves
+   its range (an rms above 2^63 or so) give z = 0, as an infinite one would.
+   h8, y8: where not null, the checkpoints of h (as h's type holds it) and of y,
+   bit for bit what lst_checkpoint_save gives.
+   hidden is at most 16384; eps > 0, scales finite. Errors as lst_checkpoint_save. */
+typedef struct lst_residual_params {
+  float residual_scale, branch_scale, eps;
+} lst_residual_params;
+LST_API lst_status lst_residual_norm(const lst_matrix* x, const lst_matrix* y, const lst_matrix* gate,
+                                     const lst_matrix* w_post, const lst_matrix* w_pre,
+                                     const lst_residual_params* params, const lst_matrix* h, const lst_matrix* z,
+                                     const lst_checkpoint* h8, const lst_checkpoint* y8, void* cuda_stream);
+
+/* Its gradients. With dh the gradient that reaches h directly (from the residual
+   stream of the next layer) and dz that of z:
+     D = dh + gradient of the norm of h at dz
+     dx = residual_scale * D;   dy, dgate, dw_post from branch_scale * D;   dw_pre
+   h and y as the forward had them: a matrix (h, y) or a checkpoint (h8, y8), not
+   both. h is needed for dz, y for w_post or dgate. dh or dz may be null (zero; w_pre
+   is null exactly where dz is).
+   Every output may be null. dh, dz, dx, dy, and h and y as matrices, have one type. dgate, dw_post, dw_pre: shapes of gate, w_post, w_pre,
+   bf16 or fp32 each, for instance their range of a block's G segment; with
+   accumulate, added to what they hold (one rounding). Sums over tokens are fp32, in
+   an order that depends on the sizes alone. dx may be dh, dy may be dz.
+   workspace: lst_residual_norm_grad_workspace_bytes(tokens, hidden, gate rows or 0)
+   bytes, 256-byte aligned; that size serves fewer tokens and gate rows as well.
+   Errors otherwise as lst_residual_norm. */
+LST_API int64_t lst_residual_norm_grad_workspace_bytes(int64_t tokens, int64_t hidden, int64_t gate_rows);
+LST_API lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_matrix* dz, const lst_matrix* h,
+                                          const lst_checkpoint* h8, const lst_matrix* y, const lst_checkpoint* y8,
+                                          const lst_matrix* gate, const lst_matrix* w_post, const lst_matrix* w_pre,
+                                          const lst_residual_params* params, const lst_matrix* dx, const lst_matrix* dy,
+                                          const lst_matrix* dgate, const lst_matrix* dw_post, const lst_matrix* dw_pre,
+                                          int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                                          void* cuda_stream);
+
+/* Weight gradient of a linear layer from the checkpoint of its input:
+     dw[o] = sum over tokens t of dy[t,o] * X[t]
+   X = the values c stands for, or with norm_weight (1 x cols, bf16 or fp32) their
+   norm X[t] * rsqrt(mean(X[t]^2) + eps) * norm_weight, recomputed instead of kept.
+   dy: tokens x out, bf16; dw: out x cols, bf16 or fp32, for instance the weight's
+   range of a block's G segment; added to what it holds when accumulate is set (one
+   rounding). Products on the tensor cores with fp32 sums over bf16 operands: exact
+   for values as they are kept; a normed row is rounded to bf16 before its weight,
+   which multiplies the fp32 sums.
+   dw is zero (or as it was) for no tokens. eps > 0 is read only with norm_weight.
+   workspace: lst_checkpoint_wgrad_workspace_bytes() bytes for the operands as they
+   lie (rows of dy that do not all start on 16 bytes are copied there), 256-byte
+   aligned; that size serves fewer tokens as well. 0 for sizes that the call refuses.
+   Errors as lst_checkpoint_save, plus LST_ERR_INVALID_ARG for more than 2^24 tokens
+   or operands of more than 2^40 elements. */
+LST_API int64_t lst_checkpoint_wgrad_workspace_bytes(const lst_matrix* dy, const lst_checkpoint* c, const lst_matrix* dw);
+LST_API lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_checkpoint* c, const lst_matrix* norm_weight,
+                                        float eps, const lst_matrix* dw, int32_t accumulate, void* workspace,
+                                        int64_t workspace_bytes, void* cuda_stream);
+
 /* LST_ERR_TIMEOUT if a wait inside one of the matrix kernels of these
    operators ran out (2 s) since the last call on the current device: the
    results of the calls since then are not valid. LST_OK otherwise.

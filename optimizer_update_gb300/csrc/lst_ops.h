@@ -43,6 +43,24 @@ inline lst_status check_indices(const lst_indices* t, const char* name, const ch
   return LST_OK;
 }
 
+inline lst_status check_checkpoint(const lst_checkpoint* c, const char* name, const char* who) {
+  if (!c) return fail(LST_ERR_INVALID_ARG, "%s: %s is null", who, name);
+  if (c->format != LST_CHECKPOINT_I8 && c->format != LST_CHECKPOINT_E4M3)
+    return fail(LST_ERR_INVALID_ARG, "%s: %s has unknown format %d", who, name, (int)c->format);
+  if (c->rows < 0 || c->cols < 0 || c->rows > (int64_t(1) << 31) - 1 || c->cols > (int64_t(1) << 31) - 1)
+    return fail(LST_ERR_INVALID_ARG, "%s: %s: rows or columns outside 0..2^31-1", who, name);
+  if (c->stride < c->cols || c->scale_stride < ops_ceil_div(c->cols, 32))
+    return fail(LST_ERR_INVALID_ARG, "%s: %s: stride below the count of columns or scales", who, name);
+  if (c->stride > (int64_t(1) << 36) || c->scale_stride > (int64_t(1) << 36))
+    return fail(LST_ERR_INVALID_ARG, "%s: %s: stride above 2^36", who, name);
+  if (c->rows > 0 && c->cols > 0) {
+    if (!c->data || !c->scales) return fail(LST_ERR_INVALID_ARG, "%s: %s: data or scales is null", who, name);
+    if (reinterpret_cast<uintptr_t>(c->data) % 16 || c->stride % 16)
+      return fail(LST_ERR_ALIGNMENT, "%s: %s: rows not on 16 bytes", who, name);
+  }
+  return LST_OK;
+}
+
 inline lst_status check_workspace(const void* ws, int64_t bytes, int64_t need, const char* who) {
   if (need == 0) return LST_OK;
   if (!ws) return fail(LST_ERR_INVALID_ARG, "%s: workspace is null", who);

@@ -74,6 +74,17 @@ class lst_indices(ctypes.Structure):
     host = False
 
 
+class lst_checkpoint(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
+                ("format", ctypes.c_int32)]
+    host = False
+
+
+class lst_residual_params(ctypes.Structure):
+    _fields_ = [("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 class lst_ns_params(ctypes.Structure):
     _fields_ = [("steps", ctypes.c_int32), ("eps", ctypes.c_float)]
 
@@ -139,6 +150,55 @@ def indices(t) -> lst_indices:
     if not t.is_cuda:
         i.host = True
     return i
+
+
+# lst_checkpoint_format
+LST_CHECKPOINT_I8 = 0
+LST_CHECKPOINT_E4M3 = 1
+CHECKPOINT_FORMATS = {"i8": LST_CHECKPOINT_I8, "e4m3": LST_CHECKPOINT_E4M3}
+
+
+def checkpoint(data, scales, fmt="i8") -> lst_checkpoint:
+    """An lst_checkpoint over two torch tensors of two dimensions and one byte an
+    element: the values (rows on 16 bytes; a column count that is no multiple of
+    16 is a view of wider rows) and the scales, one per 32 columns. fmt: "i8" or
+    "e4m3". checkpoint_buffers() makes such tensors."""
+    if data.dim() != 2 or scales.dim() != 2 or data.element_size() != 1 or scales.element_size() != 1:
+        raise ValueError("values and scales have two dimensions and one byte an element")
+    (rows, cols), (stride, inner) = data.shape, data.stride()
+    (scale_rows, blocks), (scale_stride, scale_inner) = scales.shape, scales.stride()
+    if scale_rows != rows or blocks != (cols + 31) // 32:
+        raise ValueError("one scale per row and 32 columns")
+    if (inner != 1 and cols > 1) or (scale_inner != 1 and blocks > 1):
+        raise ValueError("rows must be contiguous")
+    if rows <= 1:
+        stride, scale_stride = (cols + 15) // 16 * 16, blocks  # there is no next row
+    elif stride < cols or scale_stride < blocks:
+        raise ValueError("rows overlap: the row stride is below the column count")
+    if rows and cols % 16 and _bytes_from(data) < (rows - 1) * stride + (cols + 15) // 16 * 16:
+        raise ValueError("the last row's memory ends before the next multiple of 16 bytes")
+    if fmt not in CHECKPOINT_FORMATS:
+        raise ValueError(f"unknown checkpoint format {fmt}")
+    c = lst_checkpoint(data.data_ptr(), scales.data_ptr(), rows, cols, stride, scale_stride, CHECKPOINT_FORMATS[fmt])
+    if not (data.is_cuda and scales.is_cuda):
+        c.host = True
+    return c
+
+
+def _bytes_from(t) -> int:
+    """Bytes of a one-byte tensor's storage from its first element on."""
+    return t.untyped_storage().nbytes() - t.storage_offset()
+
+
+def checkpoint_buffers(rows: int, cols: int, device="cuda"):
+    """(values, scales) for checkpoint(): uint8 tensors, the values' rows on 16 bytes."""
+    import torch
+    values = torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.uint8, device=device)[:, :cols]
+    return values, torch.empty(rows, (cols + 31) // 32, dtype=torch.uint8, device=device)
+
+
+def residual_params(residual_scale=1.0, branch_scale=1.0, eps=1e-5):
+    return lst_residual_params(residual_scale, branch_scale, eps)
 
 
 def _on_device(*operands) -> None:
@@ -244,6 +304,17 @@ def lib() -> ctypes.CDLL:
             "lst_muon_workspace_bytes": ([vp], i64),
             "lst_muon_step": ([vp, P(vp), P(lst_muon_hparams), P(lst_adamw_hparams), P(ctypes.c_uint8), vp, i64, vp],
                               ctypes.c_int),
+            "lst_checkpoint_save": ([P(lst_matrix), P(lst_checkpoint), vp], ctypes.c_int),
+            "lst_checkpoint_restore": ([P(lst_checkpoint), P(lst_matrix), vp], ctypes.c_int),
+            "lst_residual_norm": ([P(lst_matrix)] * 5 + [P(lst_residual_params), P(lst_matrix), P(lst_matrix),
+                                                         P(lst_checkpoint), P(lst_checkpoint), vp], ctypes.c_int),
+            "lst_residual_norm_grad_workspace_bytes": ([i64, i64, i64], i64),
+            "lst_residual_norm_grad": ([P(lst_matrix), P(lst_matrix), P(lst_matrix), P(lst_checkpoint), P(lst_matrix),
+                                        P(lst_checkpoint), P(lst_matrix), P(lst_matrix), P(lst_matrix),
+                                        P(lst_residual_params)] + [P(lst_matrix)] * 5 + [i32, vp, i64, vp], ctypes.c_int),
+            "lst_checkpoint_wgrad_workspace_bytes": ([P(lst_matrix), P(lst_checkpoint), P(lst_matrix)], i64),
+            "lst_checkpoint_wgrad": ([P(lst_matrix), P(lst_checkpoint), P(lst_matrix), f32, P(lst_matrix), i32, vp, i64, vp],
+                                     ctypes.c_int),
             "lst_operator_status": ([], ctypes.c_int),
             "lst_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "lst_last_error": ([], ctypes.c_char_p),
@@ -535,6 +606,51 @@ def lst_muon_step(handle: int, dev_blocks: Sequence[int], muon: lst_muon_hparams
     mask = (ctypes.c_uint8 * max(1, len(use_muon)))(*[1 if u else 0 for u in use_muon]) if use_muon is not None else None
     _check(lib().lst_muon_step(handle, _ptr_array(dev_blocks), muon, adamw, mask, workspace or None, workspace_bytes,
                                stream or None))
+
+
+def lst_checkpoint_save(x: lst_matrix, out: lst_checkpoint, stream: int = 0) -> None:
+    _on_device(x, out)
+    _check(lib().lst_checkpoint_save(x, out, stream or None))
+
+
+def lst_checkpoint_restore(c: lst_checkpoint, out: lst_matrix, stream: int = 0) -> None:
+    _on_device(c, out)
+    _check(lib().lst_checkpoint_restore(c, out, stream or None))
+
+
+def lst_residual_norm(x: lst_matrix, y, gate, w_post, w_pre, params: lst_residual_params, h, z, h8=None, y8=None,
+                      stream: int = 0) -> None:
+    """y, gate, w_post, w_pre, h, z: matrices or None; h8, y8: checkpoints to write, or None."""
+    _on_device(x, y, gate, w_post, w_pre, h, z, h8, y8)
+    _check(lib().lst_residual_norm(x, y, gate, w_post, w_pre, params, h, z, h8, y8, stream or None))
+
+
+def lst_residual_norm_grad_workspace_bytes(tokens: int, hidden: int, gate_rows: int) -> int:
+    return int(lib().lst_residual_norm_grad_workspace_bytes(tokens, hidden, gate_rows))
+
+
+def lst_residual_norm_grad(dh, dz, h, y, gate, w_post, w_pre, params: lst_residual_params, dx, dy, dgate, dw_post, dw_pre,
+                           accumulate: bool, workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    """h and y: the matrices of the forward pass or checkpoints of them, or None."""
+    _on_device(dh, dz, h, y, gate, w_post, w_pre, dx, dy, dgate, dw_post, dw_pre)
+    h8 = isinstance(h, lst_checkpoint)
+    y8 = isinstance(y, lst_checkpoint)
+    _check(lib().lst_residual_norm_grad(dh, dz, None if h8 else h, h if h8 else None, None if y8 else y, y if y8 else None,
+                                        gate, w_post, w_pre, params, dx, dy, dgate, dw_post, dw_pre, 1 if accumulate else 0,
+                                        workspace or None, workspace_bytes, stream or None))
+
+
+def lst_checkpoint_wgrad_workspace_bytes(dy: lst_matrix, c: lst_checkpoint, dw: lst_matrix) -> int:
+    """The size for the operands as they lie: rows of dy that do not start on 16 bytes take more."""
+    return int(lib().lst_checkpoint_wgrad_workspace_bytes(dy, c, dw))
+
+
+def lst_checkpoint_wgrad(dy: lst_matrix, c: lst_checkpoint, norm_weight, eps: float, dw: lst_matrix, accumulate: bool,
+                         workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    """norm_weight: a 1 x cols matrix where the layer's input was the norm of the checkpointed rows, or None."""
+    _on_device(dy, c, norm_weight, dw)
+    _check(lib().lst_checkpoint_wgrad(dy, c, norm_weight, eps, dw, 1 if accumulate else 0, workspace or None,
+                                      workspace_bytes, stream or None))
 
 
 def lst_operator_status() -> None:
