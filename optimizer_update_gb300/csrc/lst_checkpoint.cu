@@ -32,10 +32,16 @@ __global__ void __launch_bounds__(256)
   for (int64_t t = blockIdx.x * 8 + (threadIdx.x >> 5); t < tasks; t += warps) {
     const int64_t row = t / parts;
     const int col = static_cast<int>(t - row * parts) * kWarpColumns;
-    const Cols<VEC, 2> c = {lane, 32, min(cols - col, kWarpColumns)};
-    float v[2][8];
-    c.load(x + row * ld + col, v);
-    c.save(v, out.data + row * out.stride + col, out.scales + row * out.scale_stride + col / kCkptBlock, out.e4m3);
+    const Cols<VEC> c = {lane, 32, min(cols - col, kWarpColumns)};
+    Unit u[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      u[k].fill(0.0f);
+      if (c.has(k)) c.load(x + row * ld + col, k, u[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      c.save(u[k], k, out.data + row * out.stride + col, out.scales + row * out.scale_stride + col / kCkptBlock, out.e4m3);
   }
 }
 
@@ -50,17 +56,19 @@ __global__ void __launch_bounds__(256)
   for (int64_t t = blockIdx.x * 8 + (threadIdx.x >> 5); t < tasks; t += warps) {
     const int64_t row = t / parts;
     const int col = static_cast<int>(t - row * parts) * kWarpColumns;
-    const Cols<VEC, 2> c = {lane, 32, min(cols - col, kWarpColumns)};
-    float v[2][8];
-    c.restore(in.data + row * in.stride + col, in.scales + row * in.scale_stride + col / kCkptBlock, in.e4m3, v);
-    if (rho) {
-      const float r = rho[row];
+    const Cols<VEC> c = {lane, 32, min(cols - col, kWarpColumns)};
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) {
+      if (!c.has(k)) continue;
+      Unit u;
+      c.restore(in.data + row * in.stride + col, in.scales + row * in.scale_stride + col / kCkptBlock, in.e4m3, k, u);
+      if (rho) {
+        const float2 r = both(rho[row]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * r;
+        for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], r);
+      }
+      c.store(out + row * ld + col, k, u);
     }
-    c.store(out + row * ld + col, v);
   }
 }
 
@@ -71,16 +79,19 @@ __global__ void __launch_bounds__(256) rho_kernel(Kept in, int64_t rows, int col
   wait_for_previous();
   const int lane = threadIdx.x & 31;
   for (int64_t row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += static_cast<int64_t>(gridDim.x) * 8) {
-    float s = 0.0f;
+    float2 sums = both(0.0f);
     for (int col = 0; col < cols; col += kWarpColumns) {
-      const Cols<VEC, 2> c = {lane, 32, min(cols - col, kWarpColumns)};
-      float v[2][8];
-      c.restore(in.data + row * in.stride + col, in.scales + row * in.scale_stride + col / kCkptBlock, in.e4m3, v);
+      const Cols<VEC> c = {lane, 32, min(cols - col, kWarpColumns)};
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < 2; ++k) {
+        if (!c.has(k)) continue;
+        Unit u;
+        c.restore(in.data + row * in.stride + col, in.scales + row * in.scale_stride + col / kCkptBlock, in.e4m3, k, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s = __fmaf_rn(v[k][i], v[k][i], s);
+        for (int j = 0; j < 4; ++j) sums = fma2(u.v[j], u.v[j], sums);
+      }
     }
+    float s = sums.x + sums.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) rho[row] = __frsqrt_rn(s / static_cast<float>(cols) + eps);

@@ -34,6 +34,7 @@
 
 #include "lst_device.cuh"
 #include "lst_gemm.h"
+#include "lst_norm.h"
 #include "lst_ns.h"
 #include "lst_ops.h"
 
@@ -796,6 +797,8 @@ extern "C" lst_status lst_operator_status(void) {
   LST_TRY_CUDA(gemm_take_error(&err), "lst_operator_status");
   int small = 0;
   LST_TRY_CUDA(ns_small_take_error(&small), "lst_operator_status");
-  if (err || small) return fail(LST_ERR_TIMEOUT, "a wait inside a matrix kernel ran out");
+  int norm = 0;
+  LST_TRY_CUDA(norm_take_error(&norm), "lst_operator_status");
+  if (err || small || norm) return fail(LST_ERR_TIMEOUT, "a wait inside a matrix or norm kernel ran out");
   return LST_OK;
 }

@@ -3,8 +3,8 @@
 // and the gradients of all that.
 //
 // Forward, row by row: u = y tau w_post (tau = rsqrt(mean y^2 + eps)), h = a x + b g u,
-// z = h rho w_pre (rho = rsqrt(mean h^2 + eps)). A CTA holds a row in registers: it
-// is read once and h, z and the checkpoints are written from there.
+// z = h rho w_pre (rho = rsqrt(mean h^2 + eps)). A row is read once; h, z and the
+// checkpoints are written from registers.
 //
 // Backward: with m = w_pre dz
 //   D  = dh + rho (m - h rho^2 mean(m h)),  dx = a D,  dw_pre = sum dz h rho
@@ -15,11 +15,13 @@
 // workspace once per CTA (A once per gate row) and are added up in order by a second launch.
 //
 // Both are bound by memory: 8 bytes an element forward, 12 backward in bf16 (10 with
-// checkpoints) against some 20 operations.
+// checkpoints) against some 10 and 30 instructions.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
-#include "lst_ckpt.cuh"
+#include "lst_norm.cuh"
+#include "lst_norm.h"
 
 namespace lst {
 
@@ -27,366 +29,263 @@ namespace {
 
 constexpr int64_t kMaxHidden = 16384;
 constexpr int64_t kSms = 152;
+constexpr int64_t kSharedPerSm = 228 * 1024;  // 1 KB of it the system's, per CTA
+constexpr int kMaxShared = 227 * 1024;
 
-struct Rows {
-  void* p;
-  int64_t stride;  // elements
-};
-struct Weights {
-  const void* p;
-  int64_t stride;
-  int32_t f32;
-};
-struct Kept {
-  uint8_t* data;
-  uint8_t* scales;
-  int64_t stride, scale_stride;
-  int32_t e4m3;
-};
-template <class T>
-__device__ __forceinline__ T* row_of(const Rows& m, int64_t r) {
-  return static_cast<T*>(m.p) + r * m.stride;
-}
-__device__ __forceinline__ const void* row_of(const Weights& w, int64_t r) {
-  return static_cast<const char*>(w.p) + r * w.stride * (w.f32 ? 4 : 2);
-}
+__device__ int g_norm_error;
 
-// Sum of each of the M values over the CTA's threads, in every thread. `turn` alternates
-// between the two halves of `words`, so that one barrier a call is enough.
-template <int M>
-__device__ __forceinline__ void cta_sum(float (&v)[M], float (*words)[M][32], int& turn) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-#pragma unroll
-  for (int j = 0; j < M; ++j)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
-  if (warps == 1) return;
-  if (lane == 0) {
-#pragma unroll
-    for (int j = 0; j < M; ++j) words[turn][j][warp] = v[j];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < M; ++j) {
-    v[j] = lane < warps ? words[turn][j][lane] : 0.0f;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
-  }
-  turn ^= 1;
-}
-
+// ---- forward -----------------------------------------------------------------------
+enum NormOperand { NORM_X, NORM_Y, NORM_GATE, NORM_OPS };
 struct NormArgs {
-  Rows x, y, h, z;
+  PipeArgs<NORM_OPS> pipe;
+  Rows h, z;
   Weights gate, w_post, w_pre;
   Kept h8, y8;
-  int64_t tokens, per_gate;  // tokens of a gate row
-  int32_t hidden;
   float alpha, beta, eps;
 };
 
 template <class T, bool VEC, int K>
-__global__ void __launch_bounds__(512) norm_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float words[2][1][32];
+__global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
   let_next_start();
+  Pipe<NORM_OPS, true> p(a.pipe, smem);
   wait_for_previous();
-  const Cols<VEC, K> c = {static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), a.hidden};
-  const float inverse = 1.0f / static_cast<float>(a.hidden);
+  p.start();
+  const int group = threadIdx.x / a.pipe.group, tid = threadIdx.x - group * a.pipe.group, warp = tid >> 5, warps = a.pipe.group >> 5;
+  Cols<VEC> c = {tid, a.pipe.group, a.pipe.hidden};
+  const float inverse = 1.0f / static_cast<float>(a.pipe.hidden);
+  const bool has_y = a.pipe.in[NORM_Y].p != nullptr, per_token = a.pipe.in[NORM_GATE].p != nullptr;
+  float* const words = p.words() + group * warps * 8;
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < a.tokens; row += gridDim.x) {
-    float h[K][8], y[K][8], w[K][8];
-    c.load(row_of<T>(a.x, row), h);
-    if (a.y.p) {
-      c.load(row_of<T>(a.y, row), y);
-      if (a.y8.data)
-        c.save(y, a.y8.data + row * a.y8.stride, a.y8.scales + row * a.y8.scale_stride, a.y8.e4m3);
-      if (a.w_post.p) {
-        float s[1] = {0.0f};
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[0] = __fmaf_rn(y[k][i], y[k][i], s[0]);
-        cta_sum(s, words, turn);
-        const float tau = __frsqrt_rn(s[0] * inverse + a.eps);
-        c.load_any(a.w_post.p, a.w_post.f32, w);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[k][i] = y[k][i] * tau * w[k][i];
-      }
-      if (a.gate.p) {
-        c.load_any(row_of(a.gate, row / a.per_gate), a.gate.f32, w);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[k][i] = y[k][i] * w[k][i];
-      }
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] = a.alpha * h[k][i] + a.beta * y[k][i];
-    } else {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] = a.alpha * h[k][i];
-    }
-    if (a.h.p) c.store(row_of<T>(a.h, row), h);
-    if (a.h8.data) {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[k][i] = round_to(h[k][i], static_cast<const T*>(nullptr));
-      c.save(w, a.h8.data + row * a.h8.stride, a.h8.scales + row * a.h8.scale_stride, a.h8.e4m3);
-    }
-    if (a.z.p) {
-      float s[1] = {0.0f};
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] = __fmaf_rn(h[k][i], h[k][i], s[0]);
-      cta_sum(s, words, turn);
-      const float rho = __frsqrt_rn(s[0] * inverse + a.eps);
-      c.load_any(a.w_pre.p, a.w_pre.f32, w);
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] = h[k][i] * rho * w[k][i];
-      c.store(row_of<T>(a.z, row), h);
-    }
-  }
-}
-
-struct GradArgs {
-  Rows dh, dz, h, y, dx, dy;
-  Kept h8, y8;
-  Weights gate, w_post, w_pre;
-  void* dgate;
-  int64_t dgate_stride;
-  int32_t dgate_f32, accumulate;
-  // sums over a CTA's rows: of dw_pre and dw_post [cta][hidden], of dgate [2 cta + (0: its first gate row)][hidden]
-  float *part_pre, *part_post, *part_gate;
-  int64_t tokens, per_gate;
-  int32_t hidden, ctas;
-  float alpha, beta, eps;
-};
-
-__device__ __forceinline__ void store_sum(void* p, int64_t at, bool f32, bool accumulate, float v) {
-  if (f32) {
-    float* q = static_cast<float*>(p) + at;
-    *q = accumulate ? *q + v : v;
-  } else {
-    __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + at;
-    *q = __float2bfloat16_rn(accumulate ? __bfloat162float(*q) + v : v);
-  }
-}
-
-// First row of CTA c: the rows divided evenly.
-__host__ __device__ __forceinline__ int64_t first_row(int64_t c, int64_t tokens, int64_t ctas) { return c * tokens / ctas; }
-
-template <class T, bool VEC, int K>
-__global__ void __launch_bounds__(512) norm_grad_kernel(const __grid_constant__ GradArgs a) {
-  __shared__ float words[2][2][32];
-  let_next_start();
-  wait_for_previous();
-  const Cols<VEC, K> c = {static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), a.hidden};
-  const float inverse = 1.0f / static_cast<float>(a.hidden);
-  const int64_t cta = blockIdx.x;
-  const int64_t begin = first_row(cta, a.tokens, a.ctas), end = first_row(cta + 1, a.tokens, a.ctas);
-  const bool per_token = a.gate.p && a.per_gate == 1;
-  float sum_pre[K][8] = {}, sum_a[K][8] = {}, sum_post[K][8] = {};
-  int turn = 0;
-  for (int64_t row = begin; row < end; ++row) {
-    float d[K][8], h[K][8], w[K][8], y[K][8], g[K][8];
+  auto sum = [&](float2 s) { return group_sum(s.x + s.y, words, turn, warps, warp, 1 + group, a.pipe.group); };
+  Unit w_pre[K], gw[K];  // gw = gate * w_post
+  if (a.z.p) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[k][i] = 0.0f, g[k][i] = 1.0f;
-    if (a.dh.p) c.load(row_of<T>(a.dh, row), d);
-    if (a.dz.p) {
-      if (a.h8.data)
-        c.restore(a.h8.data + row * a.h8.stride, a.h8.scales + row * a.h8.scale_stride, a.h8.e4m3, h);
-      else
-        c.load(row_of<T>(a.h, row), h);
-      float m[K][8];
-      c.load(row_of<T>(a.dz, row), m);
-      c.load_any(a.w_pre.p, a.w_pre.f32, w);
-      float s[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s[0] = __fmaf_rn(h[k][i], h[k][i], s[0]);
-          s[1] = __fmaf_rn(m[k][i] * w[k][i], h[k][i], s[1]);
-        }
-      cta_sum(s, words, turn);
-      const float rho = __frsqrt_rn(s[0] * inverse + a.eps), back = rho * rho * (s[1] * inverse);
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sum_pre[k][i] = __fmaf_rn(m[k][i], h[k][i] * rho, sum_pre[k][i]);
-          d[k][i] += rho * (m[k][i] * w[k][i] - h[k][i] * back);
-        }
-    }
-    if (a.dx.p) {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[k][i] = a.alpha * d[k][i];
-      c.store(row_of<T>(a.dx, row), w);
-    }
-    if (a.gate.p) c.load_any(row_of(a.gate, row / a.per_gate), a.gate.f32, g);
-    const bool has_y = a.y.p || a.y8.data;
-    float tau = 1.0f;
+      if (c.has(k)) c.load_any(a.w_pre.p, a.w_pre.f32, k, w_pre[k]);
+  }
+  const bool has_post = a.w_post.p != nullptr;
+  while (p.row < p.end) {
+    const int64_t segment = p.segment_end(p.row);
     if (has_y) {
-      if (a.y8.data)
-        c.restore(a.y8.data + row * a.y8.stride, a.y8.scales + row * a.y8.scale_stride, a.y8.e4m3, y);
-      else
-        c.load(row_of<T>(a.y, row), y);
-    }
-    if (a.w_post.p) {
-      c.load_any(a.w_post.p, a.w_post.f32, w);
-      float s[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+      for (int k = 0; k < K; ++k) {
+        if (!c.has(k)) continue;
+        gw[k].fill(1.0f);
+        if (has_post) c.load_any(a.w_post.p, a.w_post.f32, k, gw[k]);
+        if (a.gate.p && !per_token) {
+          Unit g;
+          c.load_any(row_of(a.gate, p.row / a.pipe.per_segment), a.gate.f32, k, g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s[0] = __fmaf_rn(y[k][i], y[k][i], s[0]);
-          s[1] = __fmaf_rn(a.beta * d[k][i] * g[k][i] * w[k][i], y[k][i], s[1]);
+          for (int j = 0; j < 4; ++j) gw[k].v[j] = mul2(gw[k].v[j], g.v[j]);
         }
-      cta_sum(s, words, turn);
-      tau = __frsqrt_rn(s[0] * inverse + a.eps);
-      const float back = tau * tau * (s[1] * inverse);
-      if (a.dy.p) {
-        float e[K][8];
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) e[k][i] = tau * (a.beta * d[k][i] * g[k][i] * w[k][i] - y[k][i] * back);
-        c.store(row_of<T>(a.dy, row), e);
       }
-    } else if (a.dy.p) {
-      float e[K][8];
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[k][i] = a.beta * d[k][i] * g[k][i];
-      c.store(row_of<T>(a.dy, row), e);
     }
-    if (!has_y) continue;
-    if (per_token) {
+    while (p.row < segment) {
+      const int rows = p.rows_of_turn(p.row);
+      if (!VEC) asm volatile("" : "+r"(c.threads));  // columns' offsets are formed again: held, they would spill
+      p.wait();
+      const bool mine = group < rows;
+      const int64_t row = p.row + group;
+      Unit h[K];
+      if (mine) {
+        const T* const y = reinterpret_cast<const T*>(p.at(NORM_Y, group, VEC));
+        const T* const x = reinterpret_cast<const T*>(p.at(NORM_X, group, VEC));
+        if (has_y) {
+          float2 s = both(0.0f);
 #pragma unroll
-      for (int k = 0; k < K; ++k)
+          for (int k = 0; k < K; ++k) {
+            if (!c.has(k)) continue;
+            c.load(y, k, h[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float t = d[k][i] * (y[k][i] * tau);
-          sum_post[k][i] = __fmaf_rn(g[k][i], t, sum_post[k][i]);
-          if (a.dgate && c.in(k, i))
-            store_sum(a.dgate, row * a.dgate_stride + c.at(k, i), a.dgate_f32, a.accumulate,
-                      a.beta * t * (a.w_post.p ? w[k][i] : 1.0f));
+            for (int j = 0; j < 4; ++j) s = fma2(h[k].v[j], h[k].v[j], s);
+          }
+          if (a.y8.data) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+              if (!c.has(k)) h[k].fill(0.0f);
+              c.save(h[k], k, a.y8.data + row * a.y8.stride, a.y8.scales + row * a.y8.scale_stride, a.y8.e4m3);
+            }
+          }
+          float2 f = both(a.beta);
+          if (has_post) f = both(a.beta * __frsqrt_rn(sum(s) * inverse + a.eps));
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            if (!c.has(k)) continue;
+            Unit u;
+            if (per_token) {
+              if (a.gate.f32)
+                c.load(reinterpret_cast<const float*>(p.at(NORM_GATE, group, VEC)), k, u);
+              else
+                c.load(reinterpret_cast<const __nv_bfloat16*>(p.at(NORM_GATE, group, VEC)), k, u);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) h[k].v[j] = mul2(h[k].v[j], u.v[j]);
+            }
+            c.load(x, k, u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[k].v[j] = fma2(u.v[j], both(a.alpha), mul2(mul2(h[k].v[j], gw[k].v[j]), f));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            if (!c.has(k)) continue;
+            c.load(x, k, h[k]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[k].v[j] = mul2(h[k].v[j], both(a.alpha));
+          }
         }
-      continue;
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum_a[k][i] = __fmaf_rn(d[k][i], y[k][i] * tau, sum_a[k][i]);
-    // the last row of a gate row, or of the CTA
-    const int64_t group = a.gate.p ? row / a.per_gate : 0;
-    if (row + 1 < end && (!a.gate.p || (row + 1) / a.per_gate == group)) continue;
-    const bool whole = group * a.per_gate >= begin && (group + 1) * a.per_gate <= end;
-    const int64_t slot = 2 * cta + (group == begin / a.per_gate ? 0 : 1);
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sum_post[k][i] = __fmaf_rn(g[k][i], sum_a[k][i], sum_post[k][i]);
-        if (a.dgate && c.in(k, i)) {
-          const float t = a.beta * sum_a[k][i] * (a.w_post.p ? w[k][i] : 1.0f);
-          if (whole)
-            store_sum(a.dgate, group * a.dgate_stride + c.at(k, i), a.dgate_f32, a.accumulate, t);
-          else
-            a.part_gate[slot * a.hidden + c.at(k, i)] = t;
-        }
-        sum_a[k][i] = 0.0f;
       }
+      p.release();
+      p.refill(false);
+      if (mine) {
+        float2 s = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (!c.has(k)) continue;
+          if (a.h.p) c.store(row_of<T>(a.h, row), k, h[k]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s = fma2(h[k].v[j], h[k].v[j], s);
+        }
+        if (a.h8.data) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            Unit r;
+            r.fill(0.0f);
+            if (c.has(k)) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) r.at(i) = round_to(h[k].at(i), static_cast<const T*>(nullptr));
+            }
+            c.save(r, k, a.h8.data + row * a.h8.stride, a.h8.scales + row * a.h8.scale_stride, a.h8.e4m3);
+          }
+        }
+        if (a.z.p) {
+          const float2 rho = both(__frsqrt_rn(sum(s) * inverse + a.eps));
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            if (!c.has(k)) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[k].v[j] = mul2(mul2(h[k].v[j], rho), w_pre[k].v[j]);
+            c.store(row_of<T>(a.z, row), k, h[k]);
+          }
+        }
+      }
+      p.next(rows);
+    }
   }
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c.in(k, i)) {
-        if (a.part_pre) a.part_pre[cta * a.hidden + c.at(k, i)] = sum_pre[k][i];
-        if (a.part_post) a.part_post[cta * a.hidden + c.at(k, i)] = a.beta * sum_post[k][i];
-      }
+  p.finish(&g_norm_error);
 }
 
-// Adds up the CTAs' sums: blockIdx.y 0: dw_pre, 1: dw_post, 2 + r: gate row r, unless one
-// CTA had all its rows. 32 columns a CTA, every 8th row of sums to a warp.
+// Adds up the CTAs' sums, 32 columns a CTA: blockIdx.y 0: dw_pre, 1: dw_post; from 2 on the
+// gate rows that more than one CTA worked on, by their number or (where there are more
+// gate rows than CTAs) as the last gate row of CTA blockIdx.y - 2.
 struct JoinArgs {
   const float *pre, *post, *gate;
   void *dw_pre, *dw_post, *dgate;
   int64_t dgate_stride, tokens, per_gate;
-  int32_t pre_f32, post_f32, gate_f32, accumulate, hidden, ctas;
+  int32_t pre_f32, post_f32, gate_f32, accumulate, hidden, ctas, by_row;
 };
-__global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ JoinArgs a) {
-  __shared__ float words[8][33];
+constexpr int kJoinWarps = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const __grid_constant__ JoinArgs a) {
+  __shared__ float words[kJoinWarps][33];
   let_next_start();
   wait_for_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   const bool in = col < a.hidden;
-  auto add = [&](const float* p, int64_t first, int64_t last, void* out, int64_t at, bool f32) {
-    float s = 0.0f;
-    if (in)
-      for (int64_t c = first + warp; c < last; c += 8) s += p[c * a.hidden + col];
-    words[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && in) {
-      s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += words[i][lane];
-      store_sum(out, at + col, f32, a.accumulate, s);
+  const float* part = blockIdx.y == 0 ? a.pre : a.post;
+  void* out = blockIdx.y == 0 ? a.dw_pre : a.dw_post;
+  bool f32 = blockIdx.y == 0 ? a.pre_f32 : a.post_f32;
+  if (blockIdx.y < 2 && !out) return;
+  int64_t at = col, r = -1, first = 0, last = a.ctas;
+  if (blockIdx.y >= 2) {
+    part = a.gate, out = a.dgate, f32 = a.gate_f32;
+    auto owner = [&](int64_t row) {  // the CTA whose rows include `row`
+      int64_t c = row * a.ctas / a.tokens;
+      while (first_row(c + 1, a.tokens, a.ctas) <= row) ++c;
+      return c;
+    };
+    if (a.by_row) {
+      r = blockIdx.y - 2;
+      first = owner(r * a.per_gate);
+    } else {
+      first = blockIdx.y - 2;
+      const int64_t begin = first_row(first, a.tokens, a.ctas), end = first_row(first + 1, a.tokens, a.ctas);
+      r = (end - 1) / a.per_gate;
+      if (begin == end || r * a.per_gate < begin) return;
     }
-    __syncthreads();
-  };
-  const int64_t which = blockIdx.y;
-  if (which == 0) {
-    if (a.dw_pre) add(a.pre, 0, a.ctas, a.dw_pre, 0, a.pre_f32);
-    return;
+    last = owner((r + 1) * a.per_gate - 1) + 1;
+    if (last == first + 1) return;  // its CTA has written it
+    at = r * a.dgate_stride + col;
   }
-  if (which == 1) {
-    if (a.dw_post) add(a.post, 0, a.ctas, a.dw_post, 0, a.post_f32);
-    return;
-  }
-  // gate rows that more than one CTA worked on: CTA c's last one, where it begins in c and ends behind it
-  const int64_t c0 = which - 2, begin = first_row(c0, a.tokens, a.ctas), end = first_row(c0 + 1, a.tokens, a.ctas);
-  if (begin == end) return;
-  const int64_t r = (end - 1) / a.per_gate;
-  if (r * a.per_gate < begin || (r + 1) * a.per_gate <= end) return;
   float s = 0.0f;
-  if (in && warp == 0) {
-    for (int64_t c = c0; c < a.ctas && first_row(c, a.tokens, a.ctas) < (r + 1) * a.per_gate; ++c) {
-      const int64_t b = first_row(c, a.tokens, a.ctas), e = first_row(c + 1, a.tokens, a.ctas);
-      if (b == e) continue;
-      const int64_t slot = 2 * c + (r == b / a.per_gate ? 0 : 1);
-      s += a.gate[slot * a.hidden + col];
+  if (in) {
+#pragma unroll 4
+    for (int64_t c = first + warp; c < last; c += kJoinWarps) {
+      const int64_t slot = r < 0 ? c : 2 * c + (r == first_row(c, a.tokens, a.ctas) / a.per_gate ? 0 : 1);
+      s += part[slot * a.hidden + col];
     }
-    store_sum(a.dgate, r * a.dgate_stride + col, a.gate_f32, a.accumulate, s);
+  }
+  words[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && in) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) v += words[i][lane];
+    store_sum(out, at, f32, a.accumulate, v);
   }
 }
 
 // ---- host ------------------------------------------------------------------------
-// Threads of a row: 8, 16 or 32 columns each.
+// 16 columns a thread (32 of rows above 8192), and short rows several at a time, so that a CTA has about 256 threads, 512 where a row needs them. An SM holds 512 threads of
+// the backward kernel and 768 of the forward one, as many as their registers allow.
 struct Fit {
-  int k, threads;
+  int k, group, groups, per_sm;
+  int threads() const { return group * groups; }
 };
-Fit fit(int64_t hidden) {
-  const int k = hidden <= 2048 ? 1 : hidden <= 8192 ? 2 : 4;
-  return {k, static_cast<int>(ops_round_up(ops_ceil_div(hidden, 8 * k), 32))};
+Fit fit(int64_t hidden, int threads_per_sm) {
+  Fit f;
+  f.k = hidden <= 8192 ? 2 : 4;
+  f.group = static_cast<int>(ops_round_up(ops_ceil_div(hidden, 8 * f.k), 32));
+  f.groups = std::max(1, 256 / f.group);
+  f.per_sm = std::max(1, (f.k == 4 ? 512 : threads_per_sm) / f.threads());
+  return f;
 }
-int64_t grad_ctas(int64_t tokens, int64_t hidden) {
-  return std::min(tokens, kSms * std::max<int64_t>(1, 512 / fit(hidden).threads));
-}
+Fit norm_fit(int64_t hidden) { return fit(hidden, 768); }
+Fit grad_fit(int64_t hidden) { return fit(hidden, 512); }
+int64_t ctas_of(const Fit& f, int64_t tokens) { return std::min(ops_ceil_div(tokens, f.groups), kSms * f.per_sm); }
+
+// Operands in the order of their slots in a staged row.
+template <int OPS>
+struct Operands {
+  PipeArgs<OPS> pipe = {};
+  void range(int op, const void* data, int64_t stride, int64_t bytes) {
+    pipe.in[op] = {static_cast<const uint8_t*>(data), stride, static_cast<int32_t>(bytes), pipe.row_bytes};
+    pipe.row_bytes += static_cast<int32_t>(ops_round_up(bytes + 15, 16));
+  }
+  void matrix(int op, const lst_matrix* m) {
+    if (m) range(op, m->data, m->stride * dtype_bytes(m->dtype), m->cols * dtype_bytes(m->dtype));
+  }
+  // values and scales; returns 1 for integers, 2 for e4m3, 0 for no checkpoint
+  int32_t kept(int op, const lst_checkpoint* c) {
+    if (!c) return 0;
+    range(op, c->data, c->stride, c->cols);
+    range(op + 1, c->scales, c->scale_stride, ops_ceil_div(c->cols, kCkptBlock));
+    return c->format == LST_CHECKPOINT_E4M3 ? 2 : 1;
+  }
+  // `sums`: floats per column that each of several groups leaves in shared memory. Rows are
+  // taken fewer at a time where they would not fit. Returns the shared memory of a CTA.
+  size_t plan(const Fit& f, int64_t tokens, int64_t hidden, int64_t per_segment, int sums) {
+    pipe.tokens = tokens, pipe.per_segment = per_segment, pipe.hidden = static_cast<int32_t>(hidden);
+    pipe.group = f.group, pipe.ctas = static_cast<int32_t>(ctas_of(f, tokens));
+    for (int groups = f.groups;; groups /= 2) {
+      const int64_t stage = static_cast<int64_t>(pipe.row_bytes) * groups, extra = groups > 1 ? groups * sums * hidden * 4 : 0;
+      const int64_t room = std::min<int64_t>(kSharedPerSm / f.per_sm - 1024, kMaxShared) - kPipeHeader - extra;
+      pipe.groups = groups;
+      pipe.stages = static_cast<int32_t>(std::min<int64_t>(kMaxStages, room / stage));
+      if (pipe.stages > 0 || groups == 1) return static_cast<size_t>(kPipeHeader + pipe.stages * stage + extra);
+    }
+  }
+  unsigned threads() const { return static_cast<unsigned>(pipe.group * pipe.groups); }
+};
 
 bool on16(const lst_matrix* m) {
   return !m || (reinterpret_cast<uintptr_t>(m->data) % 16 == 0 && (m->rows <= 1 || m->stride * dtype_bytes(m->dtype) % 16 == 0));
@@ -443,18 +342,9 @@ struct Shape {
   }
 };
 
-template <class Args>
-using Kernel = void (*)(const Args);
-
-template <class T>
-Kernel<NormArgs> norm_of(bool vec, int k) {
-  if (vec) return k == 1 ? norm_kernel<T, true, 1> : k == 2 ? norm_kernel<T, true, 2> : norm_kernel<T, true, 4>;
-  return k == 1 ? norm_kernel<T, false, 1> : k == 2 ? norm_kernel<T, false, 2> : norm_kernel<T, false, 4>;
-}
-template <class T>
-Kernel<GradArgs> norm_grad_of(bool vec, int k) {
-  if (vec) return k == 1 ? norm_grad_kernel<T, true, 1> : k == 2 ? norm_grad_kernel<T, true, 2> : norm_grad_kernel<T, true, 4>;
-  return k == 1 ? norm_grad_kernel<T, false, 1> : k == 2 ? norm_grad_kernel<T, false, 2> : norm_grad_kernel<T, false, 4>;
+template <class T, bool VEC>
+NormKernel<NormArgs> norm_of(int k) {
+  return k == 2 ? norm_kernel<T, VEC, 2> : norm_kernel<T, VEC, 4>;
 }
 
 struct GradPlan {
@@ -462,7 +352,7 @@ struct GradPlan {
 };
 GradPlan grad_plan(int64_t tokens, int64_t hidden, int64_t gate_rows) {
   GradPlan p;
-  p.ctas = grad_ctas(tokens, hidden);
+  p.ctas = ctas_of(grad_fit(hidden), tokens);
   const int64_t each = ops_round_up(p.ctas * hidden * 4, 256);
   p.pre_off = 0;
   p.post_off = each;
@@ -479,6 +369,20 @@ cudaError_t zero_rows(const lst_matrix* m, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t norm_take_error(int* out) {
+  int err[3] = {};
+  cudaError_t st = cudaMemcpyFromSymbol(&err[0], g_norm_error, sizeof(int));
+  if (st == cudaSuccess && err[0]) {
+    const int zero = 0;
+    st = cudaMemcpyToSymbol(g_norm_error, &zero, sizeof(int));
+  }
+  if (st == cudaSuccess) st = norm_grad_bf16_take_error(&err[1]);
+  if (st == cudaSuccess) st = norm_grad_f32_take_error(&err[2]);
+  *out = err[0] | err[1] | err[2];
+  return st;
+}
+
 }  // namespace lst
 
 using namespace lst;
@@ -504,14 +408,21 @@ extern "C" lst_status lst_residual_norm(const lst_matrix* x, const lst_matrix* y
   if (!z != !w_pre) return fail(LST_ERR_INVALID_ARG, "%s: z and w_pre go together", who);
   if (!h && !z && !h8) return fail(LST_ERR_INVALID_ARG, "%s: none of h, z and h8", who);
   if (s.tokens == 0) return LST_OK;
-  const bool vec = s.hidden % 8 == 0 && on16(x) && on16(y) && on16(h) && on16(z);
-  const Fit f = fit(s.hidden);
-  const NormArgs a = {rows_arg(x), rows_arg(y), rows_arg(h), rows_arg(z), weights_arg(gate), weights_arg(w_post),
-                      weights_arg(w_pre), kept_arg(h8), kept_arg(y8), s.tokens, gate ? s.tokens / gate->rows : s.tokens,
-                      static_cast<int32_t>(s.hidden), params->residual_scale, params->branch_scale, params->eps};
-  const unsigned grid = static_cast<unsigned>(std::min(s.tokens, kSms * std::max<int64_t>(1, 1024 / f.threads)));
-  const Kernel<NormArgs> kernel = s.dtype == LST_F32 ? norm_of<float>(vec, f.k) : norm_of<__nv_bfloat16>(vec, f.k);
-  LST_TRY_CUDA(launch_chained(kernel, dim3(grid), dim3(static_cast<unsigned>(f.threads)), 0,
+  const bool token = gate && gate->rows == s.tokens && s.tokens > 1;
+  const bool vec = s.hidden % 8 == 0 && on16(x) && on16(y) && on16(h) && on16(z) && (!token || on16(gate));
+  const Fit f = norm_fit(s.hidden);
+  Operands<NORM_OPS> o;
+  o.matrix(NORM_X, x);
+  o.matrix(NORM_Y, y);
+  if (token) o.matrix(NORM_GATE, gate);
+  const size_t smem = o.plan(f, s.tokens, s.hidden, gate && !token ? s.tokens / gate->rows : s.tokens, 0);
+  const NormArgs a = {o.pipe, rows_arg(h), rows_arg(z), weights_arg(gate), weights_arg(w_post), weights_arg(w_pre), kept_arg(h8),
+                      kept_arg(y8), params->residual_scale, params->branch_scale, params->eps};
+  const NormKernel<NormArgs> kernel = s.dtype == LST_F32 ? (vec ? norm_of<float, true>(f.k) : norm_of<float, false>(f.k))
+                                  : vec              ? norm_of<__nv_bfloat16, true>(f.k)
+                                                     : norm_of<__nv_bfloat16, false>(f.k);
+  LST_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared), who);
+  LST_TRY_CUDA(launch_chained(kernel, dim3(static_cast<unsigned>(o.pipe.ctas)), dim3(o.threads()), smem,
                               static_cast<cudaStream_t>(cuda_stream), a),
                who);
   return LST_OK;
@@ -568,30 +479,41 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   LST_TRY(check_workspace(workspace, workspace_bytes, sums ? p.bytes : 0, who));
   char* ws = static_cast<char*>(workspace);
   const lst_matrix *h_in = dz ? h : nullptr, *y_in = need_y ? y : nullptr;
-  const bool vec = s.hidden % 8 == 0 && on16(dh) && on16(dz) && on16(h_in) && on16(y_in) && on16(dx) && on16(dy);
-  const Fit f = fit(s.hidden);
   const int64_t per_gate = gate ? s.tokens / gate->rows : s.tokens;
+  const bool token = per_gate == 1 && s.tokens > 1;
+  const bool vec = s.hidden % 8 == 0 && on16(dh) && on16(dz) && on16(h_in) && on16(y_in) && on16(dx) && on16(dy) && (!token || on16(gate));
+  const Fit f = grad_fit(s.hidden);
+  Operands<GRAD_OPS> o;
   GradArgs a = {};
-  a.dh = rows_arg(dh), a.dz = rows_arg(dz), a.h = rows_arg(h_in), a.y = rows_arg(y_in), a.dx = rows_arg(dx), a.dy = rows_arg(dy);
-  a.h8 = kept_arg(dz ? h8 : nullptr), a.y8 = kept_arg(need_y ? y8 : nullptr);
+  o.matrix(GRAD_DH, dh), o.matrix(GRAD_DZ, dz), o.matrix(GRAD_H, h_in), o.matrix(GRAD_Y, y_in);
+  a.h_kept = o.kept(GRAD_H, dz ? h8 : nullptr);
+  a.y_kept = o.kept(GRAD_Y, need_y ? y8 : nullptr);
+  if (token) o.matrix(GRAD_GATE, gate);
+  size_t smem = o.plan(f, s.tokens, s.hidden, token ? s.tokens : per_gate, 2);
+  if (f.k == 4) o.pipe.stages = 0, smem = kPipeHeader;  // these read rows where they are
+  a.pipe = o.pipe;
+  a.dx = rows_arg(dx), a.dy = rows_arg(dy);
   a.gate = weights_arg(gate), a.w_post = weights_arg(w_post), a.w_pre = weights_arg(w_pre);
   if (dgate) a.dgate = dgate->data, a.dgate_stride = dgate->stride, a.dgate_f32 = dgate->dtype == LST_F32;
-  a.accumulate = accumulate != 0;
+  a.per_gate = per_gate, a.accumulate = accumulate != 0;
   a.part_pre = dw_pre ? reinterpret_cast<float*>(ws + p.pre_off) : nullptr;
   a.part_post = dw_post ? reinterpret_cast<float*>(ws + p.post_off) : nullptr;
   a.part_gate = dgate ? reinterpret_cast<float*>(ws + p.gate_off) : nullptr;
-  a.tokens = s.tokens, a.per_gate = per_gate, a.hidden = static_cast<int32_t>(s.hidden), a.ctas = static_cast<int32_t>(p.ctas);
   a.alpha = params->residual_scale, a.beta = params->branch_scale, a.eps = params->eps;
-  const Kernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_of<float>(vec, f.k) : norm_grad_of<__nv_bfloat16>(vec, f.k);
-  LST_TRY_CUDA(launch_chained(kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(static_cast<unsigned>(f.threads)), 0, stream, a), who);
+  const bool all = dh && dz && dx && dy && !token && (w_post ? a.h_kept == a.y_kept : !need_y);
+  const int form = !all ? 0 : 1 + a.h_kept + (w_post ? 0 : 3);
+  const NormKernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_f32(vec, f.k == 4) : norm_grad_bf16(vec, f.k == 4, form);
+  LST_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared), who);
+  LST_TRY_CUDA(launch_chained(kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(o.threads()), smem, stream, a), who);
   if (!sums) return LST_OK;
-  JoinArgs j = {a.part_pre, a.part_post, a.part_gate, dw_pre ? dw_pre->data : nullptr, dw_post ? dw_post->data : nullptr,
-                a.dgate, a.dgate_stride, s.tokens, per_gate, dw_pre && dw_pre->dtype == LST_F32,
-                dw_post && dw_post->dtype == LST_F32, a.dgate_f32, a.accumulate, a.hidden, a.ctas};
-  const bool shared_gates = dgate && per_gate > 1;
+  const int64_t gate_rows = dgate && !token ? gate->rows : 0;
+  const JoinArgs j = {a.part_pre, a.part_post, a.part_gate, dw_pre ? dw_pre->data : nullptr, dw_post ? dw_post->data : nullptr,
+                      a.dgate, a.dgate_stride, s.tokens, per_gate, dw_pre && dw_pre->dtype == LST_F32,
+                      dw_post && dw_post->dtype == LST_F32, a.dgate_f32, a.accumulate, static_cast<int32_t>(s.hidden),
+                      static_cast<int32_t>(p.ctas), gate_rows <= p.ctas};
   LST_TRY_CUDA(launch_chained(norm_join_kernel,
-                              dim3(static_cast<unsigned>(ops_ceil_div(s.hidden, 32)), static_cast<unsigned>(2 + (shared_gates ? p.ctas : 0))),
-                              dim3(256), 0, stream, j),
+                              dim3(static_cast<unsigned>(ops_ceil_div(s.hidden, 32)), static_cast<unsigned>(2 + std::min(gate_rows, p.ctas))),
+                              dim3(32 * kJoinWarps), 0, stream, j),
                who);
   return LST_OK;
 }

@@ -1,0 +1,289 @@
+// What the residual-norm kernels share (lst_norm.cu, lst_norm_grad.cuh): arguments, the
+// pipe that brings rows to shared memory, sums over a row.
+#pragma once
+
+#include "lst_ckpt.cuh"
+#include "lst_tc.cuh"
+
+namespace lst {
+
+struct Rows {
+  void* p;
+  int64_t stride;  // elements
+};
+struct Weights {
+  const void* p;
+  int64_t stride;
+  int32_t f32;
+};
+struct Kept {
+  uint8_t* data;
+  uint8_t* scales;
+  int64_t stride, scale_stride;
+  int32_t e4m3;
+};
+template <class T>
+__device__ __forceinline__ T* row_of(const Rows& m, int64_t r) {
+  return static_cast<T*>(m.p) + r * m.stride;
+}
+__device__ __forceinline__ const void* row_of(const Weights& w, int64_t r) {
+  return static_cast<const char*>(w.p) + r * w.stride * (w.f32 ? 4 : 2);
+}
+__device__ __forceinline__ float weight_at(const Weights& w, int64_t r, int64_t col) {
+  const void* p = row_of(w, r);
+  return w.f32 ? static_cast<const float*>(p)[col] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[col]);
+}
+
+// f(column, value) for the columns of a unit
+template <bool VEC, class F>
+__device__ __forceinline__ void for_each(const Cols<VEC>& c, int k, const Unit& u, F f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c.in(k, i)) f(c.at(k, i), u.at(i));
+}
+
+// ---- rows through shared memory ----------------------------------------------------
+// A CTA takes consecutive rows, `groups` at a time (a turn), each by a group of `group`
+// threads. What a row reads are ranges of bytes (a checkpoint's values and scales are
+// two); they come to shared memory by bulk copies some turns ahead of their use, which
+// holds more bytes in flight than registers can.
+struct Range {
+  const uint8_t* p;  // row 0, or null
+  int64_t stride;    // bytes
+  int32_t bytes, slot;  // of a row; where it lies in a staged row
+};
+template <int OPS>
+struct PipeArgs {
+  Range in[OPS];
+  int64_t tokens, per_segment;  // no turn holds rows of two segments (gate rows)
+  int32_t hidden, ctas, group, groups, row_bytes, stages;
+};
+
+// First row of CTA c: the rows divided evenly.
+__host__ __device__ __forceinline__ int64_t first_row(int64_t c, int64_t tokens, int64_t ctas) { return c * tokens / ctas; }
+
+// Bulk copies go from and to 16-byte boundaries; up to 15 bytes at either end of a range
+// are copied by lanes. A range keeps its offset from such a boundary.
+struct Piece {
+  const uint8_t* src;
+  uint32_t dst;
+  int head, mid, tail;
+};
+__device__ __forceinline__ Piece piece_of(const Range& r, int64_t row, uint32_t slot) {
+  Piece p = {nullptr, 0, 0, 0, 0};
+  if (!r.p) return p;
+  p.src = r.p + row * r.stride;
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p.src) & 15);
+  p.dst = slot + r.slot + off;
+  p.head = min(r.bytes, (16 - off) & 15);
+  p.tail = (r.bytes - p.head) & 15;
+  p.mid = r.bytes - p.head - p.tail;
+  return p;
+}
+
+constexpr int kMaxStages = 4;
+constexpr int kPipeHeader = 64 + 2 * 16 * 8 * 4;  // barriers; two turns of 16 warps' sums
+
+// With STAGED false (rows that do not fit in shared memory) rows are read where they are.
+template <int OPS, bool STAGED>
+struct Pipe {
+  const PipeArgs<OPS>& a;
+  uint8_t* smem;
+  uint32_t full, empty;
+  int64_t begin, end, row, ahead;  // rows of this CTA; of this turn; of the next turn to be filled
+  int stage_bytes, stage, into;
+  uint32_t phase;
+  bool ok;
+
+  __device__ __forceinline__ Pipe(const PipeArgs<OPS>& args, uint8_t* shared) : a(args), smem(shared) {
+    full = tc::smem_addr(smem), empty = full + 8 * kMaxStages;
+    stage_bytes = a.row_bytes * a.groups;
+    stage = into = 0, phase = 0, ok = true;
+    if (STAGED) {
+      if (threadIdx.x == 0) {
+        for (int i = 0; i < a.stages; ++i) {
+          tc::mbar_init(full + 8 * i, 2);
+          tc::mbar_init(empty + 8 * i, blockDim.x >> 5);
+        }
+        tc::mbar_init_fence();
+      }
+      __syncthreads();
+    }
+    begin = row = ahead = first_row(blockIdx.x, a.tokens, a.ctas);
+    end = first_row(blockIdx.x + 1, a.tokens, a.ctas);
+  }
+  __device__ __forceinline__ int64_t segment_end(int64_t r) const { return min(end, (r / a.per_segment + 1) * a.per_segment); }
+  __device__ __forceinline__ int rows_of_turn(int64_t r) const {
+    return static_cast<int>(min(static_cast<int64_t>(a.groups), segment_end(r) - r));
+  }
+  // Warp 0 fills stage `into` with the next turn's rows. `full` takes two arrivals: the
+  // first with the bytes of the bulk copies, the second when the lanes' bytes are there.
+  __device__ __forceinline__ void fill() {
+    const int lane = threadIdx.x & 31, rows = rows_of_turn(ahead), pieces = rows * OPS;
+    const uint32_t to = tc::smem_addr(smem + kPipeHeader) + into * stage_bytes, bar = full + 8 * into;
+    int bytes = 0;
+    bool edges = false;
+    for (int i = lane; i < pieces; i += 32) {
+      const Piece p = piece_of(a.in[i % OPS], ahead + i / OPS, to + (i / OPS) * a.row_bytes);
+      bytes += p.mid;
+      edges |= p.head + p.tail > 0;
+    }
+    bytes = __reduce_add_sync(0xffffffffu, bytes);
+    edges = __any_sync(0xffffffffu, edges);
+    if (edges) tc::fence_async_proxy_cta();  // lanes' bytes of the stage's last use before this one's copies
+    if (lane == 0) tc::mbar_expect_tx(bar, bytes);
+    __syncwarp();
+    for (int i = lane; i < pieces; i += 32) {
+      const Piece p = piece_of(a.in[i % OPS], ahead + i / OPS, to + (i / OPS) * a.row_bytes);
+      if (p.mid > 0) tc::bulk_load(p.dst + p.head, p.src + p.head, p.mid, bar);
+    }
+    if (edges) {
+      for (int r = 0; r < rows; ++r) {
+        uint32_t v[OPS], at[OPS];
+#pragma unroll
+        for (int j = 0; j < OPS; ++j) {
+          const Piece p = piece_of(a.in[j], ahead + r, to + r * a.row_bytes);
+          const int k = lane & 15, from = lane < 16 ? k : p.head + p.mid + k;
+          at[j] = k < (lane < 16 ? p.head : p.tail) ? p.dst + from : 0u;
+          if (at[j]) v[j] = p.src[from];
+        }
+#pragma unroll
+        for (int j = 0; j < OPS; ++j)
+          if (at[j]) asm volatile("st.shared.u8 [%0], %1;" ::"r"(at[j]), "r"(v[j]) : "memory");
+      }
+    }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar);
+    ahead += rows;
+    if (++into == a.stages) into = 0;
+  }
+  __device__ __forceinline__ void start() {
+    if (STAGED && threadIdx.x < 32)
+      for (int i = 0; i < a.stages && ahead < end; ++i) fill();
+  }
+  // Warp 0, while a turn is under way: the stage of the turn before is filled again (a
+  // warp for that alone would cost the others an eighth of their registers). A lone
+  // stage is filled again at its turn's end.
+  __device__ __forceinline__ void refill(bool lone) {
+    if (!STAGED || threadIdx.x >= 32 || ahead >= end || lone != (a.stages == 1) || (!lone && row == begin)) return;
+    const uint32_t parity = lone || stage > 0 ? phase : phase ^ 1;
+    ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(empty + 8 * into, parity));
+    if (ok) fill();
+  }
+  __device__ __forceinline__ void wait() {
+    if (STAGED) ok = ok && tc::mbar_wait(full + 8 * stage, phase);
+  }
+  // Operand `op` of the row that group `g` has in this turn; `aligned`: its rows are on 16 bytes.
+  __device__ __forceinline__ const uint8_t* at(int op, int g, bool aligned) const {
+    if (!STAGED) return a.in[op].p + (row + g) * a.in[op].stride;
+    const uint8_t* const to = smem + kPipeHeader + stage * stage_bytes + g * a.row_bytes + a.in[op].slot;
+    if (aligned) return to;
+    const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(a.in[op].p)) +
+                         static_cast<uint32_t>(row + g) * static_cast<uint32_t>(a.in[op].stride);
+    return to + (low & 15);
+  }
+  // This warp has read the turn's rows.
+  __device__ __forceinline__ void release() {
+    if (!STAGED) return;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(empty + 8 * stage);
+  }
+  __device__ __forceinline__ void next(int rows) {
+    refill(true);
+    if (STAGED && ++stage == a.stages) stage = 0, phase ^= 1;
+    row += rows;
+  }
+  // A wait ran out (all later ones are passed over): copies in flight get time to land before the CTA ends.
+  __device__ __forceinline__ void finish(int* error) {
+    if (STAGED && !ok) {
+      atomicExch(error, 1);
+      for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    }
+  }
+  __device__ __forceinline__ float* words() const { return reinterpret_cast<float*>(smem + 64); }
+};
+
+// Sum of v over the threads of a row's group, in each of them. Calls take alternate halves
+// of `words` (`turn`), so that one barrier is enough.
+__device__ __forceinline__ float group_sum(float v, float* words, int& turn, int warps, int warp, int bar, int threads) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (warps == 1) return v;
+  words += turn * 128;
+  turn ^= 1;
+  if (lane == 0) words[warp] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+  v = lane < warps ? words[lane] : 0.0f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+// The same for 8 values: lanes exchange halves, quarters and eighths of them (9 shuffles
+// instead of 40).
+__device__ __forceinline__ void group_sum8(float (&v)[8], float* words, int& turn, int warps, int warp, int bar, int threads) {
+  const int lane = threadIdx.x & 31;
+  float u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float mine = lane & 16 ? v[j + 4] : v[j], other = lane & 16 ? v[j] : v[j + 4];
+    u[j] = mine + __shfl_xor_sync(0xffffffffu, other, 16);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float mine = lane & 8 ? u[j + 2] : u[j], other = lane & 8 ? u[j] : u[j + 2];
+    u[j] = mine + __shfl_xor_sync(0xffffffffu, other, 8);
+  }
+  float s = (lane & 4 ? u[1] : u[0]) + __shfl_xor_sync(0xffffffffu, lane & 4 ? u[0] : u[1], 4);
+  s += __shfl_xor_sync(0xffffffffu, s, 2);
+  s += __shfl_xor_sync(0xffffffffu, s, 1);  // value lane / 4
+  if (warps > 1) {
+    words += turn * 128;
+    turn ^= 1;
+    if ((lane & 3) == 0) words[warp * 8 + (lane >> 2)] = s;
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+    s = 0.0f;
+    for (int w = lane & 3; w < warps; w += 4) s += words[w * 8 + (lane >> 2)];
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = __shfl_sync(0xffffffffu, s, 4 * j);
+}
+
+// ---- backward ----------------------------------------------------------------------
+enum GradOperand { GRAD_DH, GRAD_DZ, GRAD_H, GRAD_H_SCALES, GRAD_Y, GRAD_Y_SCALES, GRAD_GATE, GRAD_OPS };
+struct GradArgs {
+  PipeArgs<GRAD_OPS> pipe;
+  Rows dx, dy;
+  Weights gate, w_post, w_pre;
+  void* dgate;
+  int64_t dgate_stride, per_gate;
+  int32_t dgate_f32, accumulate, h_kept, y_kept;  // kept: 0 a matrix; 1 integers, 2 e4m3
+  // sums over a CTA's rows: of dw_pre and dw_post [cta][hidden], of dgate [2 cta + (0: its first gate row)][hidden]
+  float *part_pre, *part_post, *part_gate;
+  float alpha, beta, eps;
+};
+
+// One value of a parameter gradient.
+__device__ __forceinline__ void store_sum(void* p, int64_t at, bool f32, bool accumulate, float v) {
+  if (f32) {
+    float* q = static_cast<float*>(p) + at;
+    *q = accumulate ? *q + v : v;
+  } else {
+    __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + at;
+    *q = __float2bfloat16_rn(accumulate ? __bfloat162float(*q) + v : v);
+  }
+}
+
+template <class Args>
+using NormKernel = void (*)(const Args);
+// The backward kernel for activations of a type (lst_norm_grad_bf16.cu, lst_norm_grad_f32.cu),
+// 16 columns a thread, or 32 for rows above 8192 (`wide`), and the word that its waits
+// set when one runs out. `form`: see lst_norm_grad.cuh.
+NormKernel<GradArgs> norm_grad_bf16(bool vec, bool wide, int form);
+NormKernel<GradArgs> norm_grad_f32(bool vec, bool wide);
+cudaError_t norm_grad_bf16_take_error(int* out);
+cudaError_t norm_grad_f32_take_error(int* out);
+
+}  // namespace lst
