@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(256)
   for (int64_t t = blockIdx.x * 8 + (threadIdx.x >> 5); t < tasks; t += warps) {
     const int64_t row = t / parts;
     const int col = static_cast<int>(t - row * parts) * kWarpColumns;
-    const Cols<VEC> c = {lane, 32, min(cols - col, kWarpColumns)};
+    const Cols<VEC> c = {static_cast<uint32_t>(lane), 32u, static_cast<uint32_t>(min(cols - col, kWarpColumns))};
     Unit u[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(256)
   for (int64_t t = blockIdx.x * 8 + (threadIdx.x >> 5); t < tasks; t += warps) {
     const int64_t row = t / parts;
     const int col = static_cast<int>(t - row * parts) * kWarpColumns;
-    const Cols<VEC> c = {lane, 32, min(cols - col, kWarpColumns)};
+    const Cols<VEC> c = {static_cast<uint32_t>(lane), 32u, static_cast<uint32_t>(min(cols - col, kWarpColumns))};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!c.has(k)) continue;
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256) rho_kernel(Kept in, int64_t rows, int col
   for (int64_t row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += static_cast<int64_t>(gridDim.x) * 8) {
     float2 sums = both(0.0f);
     for (int col = 0; col < cols; col += kWarpColumns) {
-      const Cols<VEC> c = {lane, 32, min(cols - col, kWarpColumns)};
+      const Cols<VEC> c = {static_cast<uint32_t>(lane), 32u, static_cast<uint32_t>(min(cols - col, kWarpColumns))};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (!c.has(k)) continue;

@@ -114,8 +114,8 @@ struct Unit {
 // vector path units are whole or not there at all: callers pass over those (`has`).
 template <bool VEC>
 struct Cols {
-  int tid, threads, cols;
-  __device__ __forceinline__ int at(int k, int i) const {
+  uint32_t tid, threads, cols;
+  __device__ __forceinline__ uint32_t at(int k, int i) const {
     return VEC ? (tid + k * threads) * 8 + i : tid + (8 * k + i) * threads;
   }
   __device__ __forceinline__ bool in(int k, int i) const { return at(k, VEC ? 0 : i) < cols; }

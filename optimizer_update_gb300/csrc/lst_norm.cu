@@ -45,14 +45,14 @@ struct NormArgs {
 };
 
 template <class T, bool VEC, int K>
-__global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __maxnreg__(128) norm_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   let_next_start();
   Pipe<NORM_OPS, true> p(a.pipe, smem);
   wait_for_previous();
   p.start();
   const int group = threadIdx.x / a.pipe.group, tid = threadIdx.x - group * a.pipe.group, warp = tid >> 5, warps = a.pipe.group >> 5;
-  Cols<VEC> c = {tid, a.pipe.group, a.pipe.hidden};
+  Cols<VEC> c = {static_cast<uint32_t>(tid), static_cast<uint32_t>(a.pipe.group), static_cast<uint32_t>(a.pipe.hidden)};
   const float inverse = 1.0f / static_cast<float>(a.pipe.hidden);
   const bool has_y = a.pipe.in[NORM_Y].p != nullptr, per_token = a.pipe.in[NORM_GATE].p != nullptr;
   float* const words = p.words() + group * warps * 8;
@@ -65,8 +65,7 @@ __global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant
       if (c.has(k)) c.load_any(a.w_pre.p, a.w_pre.f32, k, w_pre[k]);
   }
   const bool has_post = a.w_post.p != nullptr;
-  while (p.row < p.end) {
-    const int64_t segment = p.segment_end(p.row);
+  do {
     if (has_y) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -81,16 +80,18 @@ __global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant
         }
       }
     }
-    while (p.row < segment) {
-      const int rows = p.rows_of_turn(p.row);
+    int rows;
+    do {
+      rows = p.rows();
       if (!VEC) asm volatile("" : "+r"(c.threads));  // columns' offsets are formed again: held, they would spill
       p.wait();
       const bool mine = group < rows;
       const int64_t row = p.row + group;
       Unit h[K];
       if (mine) {
-        const T* const y = reinterpret_cast<const T*>(p.at(NORM_Y, group, VEC));
-        const T* const x = reinterpret_cast<const T*>(p.at(NORM_X, group, VEC));
+        const uint8_t* const staged = p.staged(group);
+        const T* const y = reinterpret_cast<const T*>(p.at(NORM_Y, group, staged, VEC));
+        const T* const x = reinterpret_cast<const T*>(p.at(NORM_X, group, staged, VEC));
         if (has_y) {
           float2 s = both(0.0f);
 #pragma unroll
@@ -108,16 +109,16 @@ __global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant
             }
           }
           float2 f = both(a.beta);
-          if (has_post) f = both(a.beta * __frsqrt_rn(sum(s) * inverse + a.eps));
+          if (has_post) f = both(a.beta * rsqrtf(sum(s) * inverse + a.eps));
 #pragma unroll
           for (int k = 0; k < K; ++k) {
             if (!c.has(k)) continue;
             Unit u;
             if (per_token) {
               if (a.gate.f32)
-                c.load(reinterpret_cast<const float*>(p.at(NORM_GATE, group, VEC)), k, u);
+                c.load(reinterpret_cast<const float*>(p.at(NORM_GATE, group, staged, VEC)), k, u);
               else
-                c.load(reinterpret_cast<const __nv_bfloat16*>(p.at(NORM_GATE, group, VEC)), k, u);
+                c.load(reinterpret_cast<const __nv_bfloat16*>(p.at(NORM_GATE, group, staged, VEC)), k, u);
 #pragma unroll
               for (int j = 0; j < 4; ++j) h[k].v[j] = mul2(h[k].v[j], u.v[j]);
             }
@@ -159,7 +160,7 @@ __global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant
           }
         }
         if (a.z.p) {
-          const float2 rho = both(__frsqrt_rn(sum(s) * inverse + a.eps));
+          const float2 rho = both(rsqrtf(sum(s) * inverse + a.eps));
 #pragma unroll
           for (int k = 0; k < K; ++k) {
             if (!c.has(k)) continue;
@@ -169,9 +170,8 @@ __global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant
           }
         }
       }
-      p.next(rows);
-    }
-  }
+    } while (p.next(rows));
+  } while (p.next_segment());
   p.finish(&g_norm_error);
 }
 
@@ -249,7 +249,7 @@ Fit fit(int64_t hidden, int threads_per_sm) {
   f.per_sm = std::max(1, (f.k == 4 ? 512 : threads_per_sm) / f.threads());
   return f;
 }
-Fit norm_fit(int64_t hidden) { return fit(hidden, 768); }
+Fit norm_fit(int64_t hidden) { return fit(hidden, 512); }
 Fit grad_fit(int64_t hidden) { return fit(hidden, 512); }
 int64_t ctas_of(const Fit& f, int64_t tokens) { return std::min(ops_ceil_div(tokens, f.groups), kSms * f.per_sm); }
 
@@ -271,17 +271,25 @@ struct Operands {
     range(op + 1, c->scales, c->scale_stride, ops_ceil_div(c->cols, kCkptBlock));
     return c->format == LST_CHECKPOINT_E4M3 ? 2 : 1;
   }
-  // `sums`: floats per column that each of several groups leaves in shared memory. Rows are
-  // taken fewer at a time where they would not fit. Returns the shared memory of a CTA.
-  size_t plan(const Fit& f, int64_t tokens, int64_t hidden, int64_t per_segment, int sums) {
-    pipe.tokens = tokens, pipe.per_segment = per_segment, pipe.hidden = static_cast<int32_t>(hidden);
+  // `sums`: floats per column that each of several groups leaves in shared memory; `held`: that
+  // the CTA keeps there. Where not even one stage fits, rows are taken fewer at a time, then
+  // fewer CTAs to an SM. Returns the shared memory of a CTA.
+  size_t plan(const Fit& f, int64_t tokens, int64_t hidden, int64_t per_segment, int sums, int held) {
+    pipe.tokens = static_cast<int32_t>(tokens), pipe.per_segment = static_cast<int32_t>(per_segment);
+    pipe.hidden = static_cast<int32_t>(hidden);
     pipe.group = f.group, pipe.ctas = static_cast<int32_t>(ctas_of(f, tokens));
-    for (int groups = f.groups;; groups /= 2) {
-      const int64_t stage = static_cast<int64_t>(pipe.row_bytes) * groups, extra = groups > 1 ? groups * sums * hidden * 4 : 0;
-      const int64_t room = std::min<int64_t>(kSharedPerSm / f.per_sm - 1024, kMaxShared) - kPipeHeader - extra;
+    int groups = f.groups, per_sm = f.per_sm;
+    for (;;) {
+      const int64_t stage = static_cast<int64_t>(pipe.row_bytes) * groups, columns = ops_round_up(hidden, 8);
+      const int64_t extra = ((groups > 1 ? groups * sums : 0) + held) * columns * 4;
+      const int64_t room = std::min<int64_t>(kSharedPerSm / per_sm - 1024, kMaxShared) - kPipeHeader - extra;
       pipe.groups = groups;
-      pipe.stages = static_cast<int32_t>(std::min<int64_t>(kMaxStages, room / stage));
-      if (pipe.stages > 0 || groups == 1) return static_cast<size_t>(kPipeHeader + pipe.stages * stage + extra);
+      pipe.stages = room < stage ? 0 : static_cast<int32_t>(std::min<int64_t>(kMaxStages, room / stage));
+      if (pipe.stages > 0 || (groups == 1 && per_sm == 1)) return static_cast<size_t>(kPipeHeader + pipe.stages * stage + extra);
+      if (groups > 1)
+        groups /= 2;
+      else
+        --per_sm;
     }
   }
   unsigned threads() const { return static_cast<unsigned>(pipe.group * pipe.groups); }
@@ -415,7 +423,7 @@ extern "C" lst_status lst_residual_norm(const lst_matrix* x, const lst_matrix* y
   o.matrix(NORM_X, x);
   o.matrix(NORM_Y, y);
   if (token) o.matrix(NORM_GATE, gate);
-  const size_t smem = o.plan(f, s.tokens, s.hidden, gate && !token ? s.tokens / gate->rows : s.tokens, 0);
+  const size_t smem = o.plan(f, s.tokens, s.hidden, gate && !token ? s.tokens / gate->rows : s.tokens, 0, 0);
   const NormArgs a = {o.pipe, rows_arg(h), rows_arg(z), weights_arg(gate), weights_arg(w_post), weights_arg(w_pre), kept_arg(h8),
                       kept_arg(y8), params->residual_scale, params->branch_scale, params->eps};
   const NormKernel<NormArgs> kernel = s.dtype == LST_F32 ? (vec ? norm_of<float, true>(f.k) : norm_of<float, false>(f.k))
@@ -489,13 +497,13 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   a.h_kept = o.kept(GRAD_H, dz ? h8 : nullptr);
   a.y_kept = o.kept(GRAD_Y, need_y ? y8 : nullptr);
   if (token) o.matrix(GRAD_GATE, gate);
-  size_t smem = o.plan(f, s.tokens, s.hidden, token ? s.tokens : per_gate, 2);
+  size_t smem = o.plan(f, s.tokens, s.hidden, token ? s.tokens : per_gate, 2, f.k == 2 ? 2 : 0);
   if (f.k == 4) o.pipe.stages = 0, smem = kPipeHeader;  // these read rows where they are
   a.pipe = o.pipe;
   a.dx = rows_arg(dx), a.dy = rows_arg(dy);
   a.gate = weights_arg(gate), a.w_post = weights_arg(w_post), a.w_pre = weights_arg(w_pre);
   if (dgate) a.dgate = dgate->data, a.dgate_stride = dgate->stride, a.dgate_f32 = dgate->dtype == LST_F32;
-  a.per_gate = per_gate, a.accumulate = accumulate != 0;
+  a.per_gate = static_cast<int32_t>(per_gate), a.accumulate = accumulate != 0;
   a.part_pre = dw_pre ? reinterpret_cast<float*>(ws + p.pre_off) : nullptr;
   a.part_post = dw_post ? reinterpret_cast<float*>(ws + p.post_off) : nullptr;
   a.part_gate = dgate ? reinterpret_cast<float*>(ws + p.gate_off) : nullptr;

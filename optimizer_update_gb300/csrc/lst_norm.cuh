@@ -55,7 +55,7 @@ struct Range {
 template <int OPS>
 struct PipeArgs {
   Range in[OPS];
-  int64_t tokens, per_segment;  // no turn holds rows of two segments (gate rows)
+  int32_t tokens, per_segment;  // no turn holds rows of two segments (gate rows)
   int32_t hidden, ctas, group, groups, row_bytes, stages;
 };
 
@@ -90,7 +90,8 @@ struct Pipe {
   const PipeArgs<OPS>& a;
   uint8_t* smem;
   uint32_t full, empty;
-  int64_t begin, end, row, ahead;  // rows of this CTA; of this turn; of the next turn to be filled
+  int begin, end, row, segment;   // rows of this CTA, of this turn, and where its segment ends
+  int ahead, ahead_segment;       // the next turn to be filled
   int stage_bytes, stage, into;
   uint32_t phase;
   bool ok;
@@ -109,17 +110,18 @@ struct Pipe {
       }
       __syncthreads();
     }
-    begin = row = ahead = first_row(blockIdx.x, a.tokens, a.ctas);
-    end = first_row(blockIdx.x + 1, a.tokens, a.ctas);
+    begin = row = ahead = static_cast<int>(first_row(blockIdx.x, a.tokens, a.ctas));
+    end = static_cast<int>(first_row(blockIdx.x + 1, a.tokens, a.ctas));
+    segment = ahead_segment = segment_end(begin);
   }
-  __device__ __forceinline__ int64_t segment_end(int64_t r) const { return min(end, (r / a.per_segment + 1) * a.per_segment); }
-  __device__ __forceinline__ int rows_of_turn(int64_t r) const {
-    return static_cast<int>(min(static_cast<int64_t>(a.groups), segment_end(r) - r));
+  __device__ __forceinline__ int segment_end(int r) const {
+    return static_cast<int>(min(static_cast<int64_t>(end), (r / a.per_segment + int64_t(1)) * a.per_segment));
   }
+  __device__ __forceinline__ int rows() const { return min(a.groups, segment - row); }
   // Warp 0 fills stage `into` with the next turn's rows. `full` takes two arrivals: the
   // first with the bytes of the bulk copies, the second when the lanes' bytes are there.
   __device__ __forceinline__ void fill() {
-    const int lane = threadIdx.x & 31, rows = rows_of_turn(ahead), pieces = rows * OPS;
+    const int lane = threadIdx.x & 31, n = min(a.groups, ahead_segment - ahead), pieces = n * OPS;
     const uint32_t to = tc::smem_addr(smem + kPipeHeader) + into * stage_bytes, bar = full + 8 * into;
     int bytes = 0;
     bool edges = false;
@@ -138,7 +140,7 @@ struct Pipe {
       if (p.mid > 0) tc::bulk_load(p.dst + p.head, p.src + p.head, p.mid, bar);
     }
     if (edges) {
-      for (int r = 0; r < rows; ++r) {
+      for (int r = 0; r < n; ++r) {
         uint32_t v[OPS], at[OPS];
 #pragma unroll
         for (int j = 0; j < OPS; ++j) {
@@ -154,7 +156,8 @@ struct Pipe {
     }
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(bar);
-    ahead += rows;
+    ahead += n;
+    if (ahead == ahead_segment && ahead < end) ahead_segment = segment_end(ahead);
     if (++into == a.stages) into = 0;
   }
   __device__ __forceinline__ void start() {
@@ -173,14 +176,16 @@ struct Pipe {
   __device__ __forceinline__ void wait() {
     if (STAGED) ok = ok && tc::mbar_wait(full + 8 * stage, phase);
   }
-  // Operand `op` of the row that group `g` has in this turn; `aligned`: its rows are on 16 bytes.
-  __device__ __forceinline__ const uint8_t* at(int op, int g, bool aligned) const {
-    if (!STAGED) return a.in[op].p + (row + g) * a.in[op].stride;
-    const uint8_t* const to = smem + kPipeHeader + stage * stage_bytes + g * a.row_bytes + a.in[op].slot;
-    if (aligned) return to;
+  // The staged row of group `g` in this turn, and operand `op` of it; `aligned`: its rows are on 16 bytes.
+  __device__ __forceinline__ const uint8_t* staged(int g) const {
+    return smem + kPipeHeader + stage * stage_bytes + g * a.row_bytes;
+  }
+  __device__ __forceinline__ const uint8_t* at(int op, int g, const uint8_t* staged_row, bool aligned) const {
+    if (!STAGED) return a.in[op].p + static_cast<int64_t>(row + g) * a.in[op].stride;
+    if (aligned) return staged_row + a.in[op].slot;
     const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(a.in[op].p)) +
                          static_cast<uint32_t>(row + g) * static_cast<uint32_t>(a.in[op].stride);
-    return to + (low & 15);
+    return staged_row + a.in[op].slot + (low & 15);
   }
   // This warp has read the turn's rows.
   __device__ __forceinline__ void release() {
@@ -188,10 +193,18 @@ struct Pipe {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) tc::mbar_arrive(empty + 8 * stage);
   }
-  __device__ __forceinline__ void next(int rows) {
+  // The next turn; false behind the last of a segment.
+  __device__ __forceinline__ bool next(int n) {
     refill(true);
     if (STAGED && ++stage == a.stages) stage = 0, phase ^= 1;
-    row += rows;
+    row += n;
+    return row < segment;
+  }
+  // The next segment; false behind the last.
+  __device__ __forceinline__ bool next_segment() {
+    if (row >= end) return false;
+    segment = segment_end(row);
+    return true;
   }
   // A wait ran out (all later ones are passed over): copies in flight get time to land before the CTA ends.
   __device__ __forceinline__ void finish(int* error) {
@@ -258,7 +271,8 @@ struct GradArgs {
   Rows dx, dy;
   Weights gate, w_post, w_pre;
   void* dgate;
-  int64_t dgate_stride, per_gate;
+  int64_t dgate_stride;
+  int32_t per_gate;
   int32_t dgate_f32, accumulate, h_kept, y_kept;  // kept: 0 a matrix; 1 integers, 2 e4m3
   // sums over a CTA's rows: of dw_pre and dw_post [cta][hidden], of dgate [2 cta + (0: its first gate row)][hidden]
   float *part_pre, *part_post, *part_gate;

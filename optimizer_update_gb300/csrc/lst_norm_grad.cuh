@@ -18,7 +18,7 @@ __device__ __forceinline__ void store_sums(void* p, int64_t at, bool f32, bool a
     else
       c.store(static_cast<__nv_bfloat16*>(p) + at, k, u);
   } else {
-    for_each(c, k, u, [&](int col, float v) { store_sum(p, at + col, f32, accumulate, v); });
+    for_each(c, k, u, [&](uint32_t col, float v) { store_sum(p, at + col, f32, accumulate, v); });
   }
 }
 
@@ -39,7 +39,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
   p.start();
   const int group = threadIdx.x / a.pipe.group, tid = threadIdx.x - group * a.pipe.group, warp = tid >> 5, warps = a.pipe.group >> 5;
   const int64_t cta = blockIdx.x;
-  Cols<VEC> c = {tid, a.pipe.group, a.pipe.hidden};
+  Cols<VEC> c = {static_cast<uint32_t>(tid), static_cast<uint32_t>(a.pipe.group), static_cast<uint32_t>(a.pipe.hidden)};
   const int hidden = a.pipe.hidden;
   const float inverse = 1.0f / static_cast<float>(hidden);
   const bool has_dh = FORM ? true : a.pipe.in[GRAD_DH].p != nullptr, has_z = FORM ? true : a.pipe.in[GRAD_DZ].p != nullptr;
@@ -49,13 +49,18 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
   const bool token = FORM ? false : a.pipe.in[GRAD_GATE].p != nullptr;  // a gate per token
   float* const words = p.words() + group * warps * 8;
   int turn = 0;
-  constexpr bool kHold = K <= 2;  // weights in registers; K = 4 reads them again for every row
-  Unit held_pre[kHold ? K : 1], held_gw[kHold ? K : 1], sum_pre[K], sum_a[K];
+  // weights as fp32 in shared memory, where registers would spill; K = 4 reads them again for every row
+  constexpr bool kHold = K <= 2;
+  const int columns = (hidden + 7) & ~7;
+  float* const group_sums = reinterpret_cast<float*>(smem + kPipeHeader + a.pipe.stages * p.stage_bytes);
+  float* const held_pre = group_sums + (a.pipe.groups > 1 ? a.pipe.groups * 2 * columns : 0);
+  float* const held_gw = held_pre + columns;
+  Unit sum_pre[K], sum_a[K];
   // w_pre and gate * w_post of unit k (a gate per token comes with the row)
   auto load_pre = [&](int k, Unit& u) {
     if (has_z) c.load_any(a.w_pre.p, a.w_pre.f32, k, u);
   };
-  auto load_gw = [&](int64_t row, int k, Unit& u) {
+  auto load_gw = [&](int row, int k, Unit& u) {
     u.fill(1.0f);
     if (has_post) c.load_any(a.w_post.p, a.w_post.f32, k, u);
     if (!token && a.gate.p) {
@@ -68,42 +73,55 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
 #pragma unroll
   for (int k = 0; k < K; ++k) sum_pre[k].fill(0.0f), sum_a[k].fill(0.0f);
   bool first_flush = true;
-  while (p.row < p.end) {
-    const int64_t segment = p.segment_end(p.row);
+  do {
     if (kHold) {
+      // each thread the columns that it reads itself, or one group for all
+      if (a.pipe.groups > 1) asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
+      if (group == 0) {
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (c.has(k)) load_pre(k, held_pre[kHold ? k : 0]), load_gw(p.row, k, held_gw[kHold ? k : 0]);
+        for (int k = 0; k < K; ++k) {
+          if (!c.has(k)) continue;
+          Unit u;
+          if (has_z) load_pre(k, u), c.store(held_pre, k, u);
+          load_gw(p.row, k, u);
+          c.store(held_gw, k, u);
+        }
+      }
+      if (a.pipe.groups > 1) asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
     }
-    while (p.row < segment) {
-      const int rows = p.rows_of_turn(p.row);
+    int rows;
+    do {
+      rows = p.rows();
       if (!VEC) asm volatile("" : "+r"(c.threads));  // columns' offsets are formed again: held, they would spill
       p.wait();
       if (group < rows) {
         const int64_t row = p.row + group;
-        auto weights = [&](int k, Unit& pre, Unit& gw) {
-          if (kHold) {
-            pre = held_pre[kHold ? k : 0], gw = held_gw[kHold ? k : 0];
-          } else {
-            load_pre(k, pre);
-            load_gw(row, k, gw);
-          }
+        auto pre_unit = [&](int k, Unit& u) {
+          if (kHold)
+            c.load(held_pre, k, u);
+          else
+            load_pre(k, u);
         };
-        const T* const dh_row = reinterpret_cast<const T*>(p.at(GRAD_DH, group, VEC));
-        const T* const dz_row = reinterpret_cast<const T*>(p.at(GRAD_DZ, group, VEC));
+        auto gw_unit = [&](int k, Unit& u) {
+          if (kHold)
+            c.load(held_gw, k, u);
+          else
+            load_gw(p.row + group, k, u);
+        };
+        const uint8_t* const staged = p.staged(group);
+        const T* const dh_row = reinterpret_cast<const T*>(p.at(GRAD_DH, group, staged, VEC));
+        const T* const dz_row = reinterpret_cast<const T*>(p.at(GRAD_DZ, group, staged, VEC));
         auto either = [&](int op, int kept, int k, Unit& u) {
           if (kept == 0)
-            c.load(reinterpret_cast<const T*>(p.at(op, group, VEC)), k, u);
-          else if (kept == 1)
-            c.restore(p.at(op, group, true), p.at(op + 1, group, false), false, k, u);
+            c.load(reinterpret_cast<const T*>(p.at(op, group, staged, VEC)), k, u);
           else
-            c.restore(p.at(op, group, true), p.at(op + 1, group, false), true, k, u);
+            c.restore(p.at(op, group, staged, true), p.at(op + 1, group, staged, false), kept == 2, k, u);
         };
         auto gate_unit = [&](int k, Unit& u) {
           if (a.gate.f32)
-            c.load(reinterpret_cast<const float*>(p.at(GRAD_GATE, group, VEC)), k, u);
+            c.load(reinterpret_cast<const float*>(p.at(GRAD_GATE, group, staged, VEC)), k, u);
           else
-            c.load(reinterpret_cast<const __nv_bfloat16*>(p.at(GRAD_GATE, group, VEC)), k, u);
+            c.load(reinterpret_cast<const __nv_bfloat16*>(p.at(GRAD_GATE, group, staged, VEC)), k, u);
         };
         Unit m, h, y, g;
         float s[8] = {};
@@ -114,25 +132,26 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
 #pragma unroll
           for (int k = 0; k < K; ++k) {
             if (!c.has(k)) continue;
-            Unit pre, gw, d;
-            weights(k, pre, gw);
+            Unit w, d;
             if (has_z) {
+              pre_unit(k, w);
               c.load(dz_row, k, m);
               either(GRAD_H, h_kept, k, h);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                m.v[j] = mul2(m.v[j], pre.v[j]);
+                m.v[j] = mul2(m.v[j], w.v[j]);
                 s2[0] = fma2(h.v[j], h.v[j], s2[0]);
                 s2[1] = fma2(m.v[j], h.v[j], s2[1]);
               }
             }
             if (has_post) {
               either(GRAD_Y, y_kept, k, y);
+              gw_unit(k, w);
               if (token) gate_unit(k, g);
               if (has_dh) c.load(dh_row, k, d);
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                float2 q = mul2(gw.v[j], y.v[j]);
+                float2 q = mul2(w.v[j], y.v[j]);
                 if (token) q = mul2(q, g.v[j]);
                 s2[2] = fma2(y.v[j], y.v[j], s2[2]);
                 if (has_dh) s2[3] = fma2(d.v[j], q, s2[3]);
@@ -148,27 +167,27 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
           group_sum8(s, words, turn, warps, warp, 1 + group, a.pipe.group);
         }
         p.refill(false);
-        const float rho = has_z ? __frsqrt_rn(s[0] * inverse + a.eps) : 0.0f, back = rho * rho * (s[1] * inverse);
-        const float tau = has_post ? __frsqrt_rn(s[2] * inverse + a.eps) : 1.0f;
+        const float rho = has_z ? rsqrtf(s[0] * inverse + a.eps) : 0.0f, back = rho * rho * (s[1] * inverse);
+        const float tau = has_post ? rsqrtf(s[2] * inverse + a.eps) : 1.0f;
         const float back_y = has_post ? tau * tau * (a.beta * (s[3] + rho * (s[4] - back * s[5])) * inverse) : 0.0f;
         const float2 rho2 = both(rho), of_h = both(-rho * back), alpha = both(a.alpha), tau_beta = both(tau * a.beta), of_y = both(-tau * back_y);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           if (!c.has(k)) continue;
-          Unit pre, gw, d, out;
-          weights(k, pre, gw);
+          Unit w, d, out;
           if (has_dh)
             c.load(dh_row, k, d);
           else
             d.fill(0.0f);
           if (has_z) {
+            pre_unit(k, w);
             c.load(dz_row, k, m);
             either(GRAD_H, h_kept, k, h);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const float2 t = mul2(m.v[j], rho2);
               sum_pre[k].v[j] = fma2(t, h.v[j], sum_pre[k].v[j]);
-              d.v[j] = fma2(h.v[j], of_h, fma2(t, pre.v[j], d.v[j]));
+              d.v[j] = fma2(h.v[j], of_h, fma2(t, w.v[j], d.v[j]));
             }
           }
           if (has_dx) {
@@ -177,13 +196,14 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
             c.store(row_of<T>(a.dx, row), k, out);
           }
           if (has_y) either(GRAD_Y, y_kept, k, y);
+          gw_unit(k, w);
           if (token) gate_unit(k, g);
 #pragma unroll
           for (int j = 0; j < 4; ++j) d.v[j] = mul2(d.v[j], tau_beta);
           if (has_dy) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              out.v[j] = mul2(d.v[j], gw.v[j]);
+              out.v[j] = mul2(d.v[j], w.v[j]);
               if (token) out.v[j] = mul2(out.v[j], g.v[j]);
               if (has_post) out.v[j] = fma2(y.v[j], of_y, out.v[j]);
             }
@@ -195,7 +215,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
               if (token) {
                 const float2 v = mul2(d.v[j], y.v[j]);
                 sum_a[k].v[j] = fma2(g.v[j], v, sum_a[k].v[j]);
-                out.v[j] = mul2(v, gw.v[j]);
+                out.v[j] = mul2(v, w.v[j]);
               } else {
                 sum_a[k].v[j] = fma2(d.v[j], y.v[j], sum_a[k].v[j]);
               }
@@ -205,11 +225,10 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
         }
       }
       p.release();
-      p.next(rows);
-    }
+    } while (p.next(rows));
     // the sums of a gate row, or of all of the CTA's rows
     const bool last = p.row >= p.end;
-    const int64_t gate_row = (segment - 1) / a.per_gate;
+    const int64_t gate_row = (p.segment - 1) / a.per_gate;
     const bool whole = gate_row * a.per_gate >= p.begin && (gate_row + 1) * a.per_gate <= p.end;
     float* const gate_sums = a.part_gate + (2 * cta + (gate_row == p.begin / a.per_gate ? 0 : 1)) * hidden;
     float *const post = a.part_post + cta * hidden, *const pre = a.part_pre + cta * hidden;
@@ -249,18 +268,17 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
       }
     } else {
       // the groups' sums, added up in order
-      float* const buffer = reinterpret_cast<float*>(smem + kPipeHeader + a.pipe.stages * p.stage_bytes);
-      float* const mine = buffer + group * 2 * hidden;
+      float* const mine = group_sums + group * 2 * columns;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (!c.has(k)) continue;
-        for_each(c, k, sum_a[k], [&](int col, float v) { mine[col] = v; });
-        for_each(c, k, sum_pre[k], [&](int col, float v) { mine[hidden + col] = v; });
+        for_each(c, k, sum_a[k], [&](uint32_t col, float v) { mine[col] = v; });
+        for_each(c, k, sum_pre[k], [&](uint32_t col, float v) { mine[columns + col] = v; });
       }
       asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
       for (int col = threadIdx.x; col < hidden; col += blockDim.x) {
         float sa = 0.0f, sp = 0.0f;
-        for (int r = 0; r < a.pipe.groups; ++r) sa += buffer[r * 2 * hidden + col], sp += buffer[(r * 2 + 1) * hidden + col];
+        for (int r = 0; r < a.pipe.groups; ++r) sa += group_sums[r * 2 * columns + col], sp += group_sums[(r * 2 + 1) * columns + col];
         if (posts) {
           const float v = gated ? weight_at(a.gate, gate_row, col) * sa : sa;
           post[col] = first_flush ? v : post[col] + v;
@@ -279,7 +297,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
 #pragma unroll
     for (int k = 0; k < K; ++k) sum_a[k].fill(0.0f);
     first_flush = false;
-  }
+  } while (p.next_segment());
   p.finish(&g_norm_grad_error);
 }
 
