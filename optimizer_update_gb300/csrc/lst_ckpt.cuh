@@ -92,8 +92,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float2 v) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ float round_to(float v, const float*) { return v; }
-__device__ __forceinline__ float round_to(float v, const __nv_bfloat16*) { return __bfloat162float(__float2bfloat16_rn(v)); }
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ float2 round_to(float2 v, const float*) { return v; }
+__device__ __forceinline__ float2 round_to(float2 v, const __nv_bfloat16*) { return unpack_bf16(pack_bf16(v)); }
 
 // Eight values of a row in a thread.
 struct Unit {
@@ -135,7 +136,7 @@ struct Cols {
       const uint4 a = *reinterpret_cast<const uint4*>(p + at(k, 0));
       const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u.v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+      for (int j = 0; j < 4; ++j) u.v[j] = unpack_bf16(w[j]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) u.at(i) = in(k, i) ? __bfloat162float(p[at(k, i)]) : 0.0f;
@@ -188,7 +189,11 @@ struct Cols {
       most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
       const uint32_t byte = ckpt_scale_byte(most, e4m3);
       const float2 r = both(ckpt_inverse(min(byte, 254u)));
-      uint2 w = make_uint2(ckpt_encode4(mul2(u.v[0], r), mul2(u.v[1], r), e4m3), ckpt_encode4(mul2(u.v[2], r), mul2(u.v[3], r), e4m3));
+      uint2 w;
+      if (e4m3)
+        w = make_uint2(ckpt_encode4(mul2(u.v[0], r), mul2(u.v[1], r), true), ckpt_encode4(mul2(u.v[2], r), mul2(u.v[3], r), true));
+      else
+        w = make_uint2(ckpt_encode4(mul2(u.v[0], r), mul2(u.v[1], r), false), ckpt_encode4(mul2(u.v[2], r), mul2(u.v[3], r), false));
       if (byte == 255u) w = make_uint2(0, 0);
       if (in(k, 0)) {
         *reinterpret_cast<uint2*>(data + at(k, 0)) = w;
@@ -210,7 +215,7 @@ struct Cols {
   __device__ __forceinline__ void restore(const uint8_t* data, const uint8_t* scales, bool e4m3, int k, Unit& u) const {
     if (VEC) {
       const uint2 w = *reinterpret_cast<const uint2*>(data + at(k, 0));
-      const float step = ckpt_step(scales[at(k, 0) / kCkptBlock]);
+      const float step = has(k) ? ckpt_step(scales[at(k, 0) / kCkptBlock]) : 0.0f;  // a byte behind the row may be anything
       ckpt_decode4(w.x, e4m3, u.v[0], u.v[1]);
       ckpt_decode4(w.y, e4m3, u.v[2], u.v[3]);
 #pragma unroll

@@ -45,40 +45,59 @@ struct NormArgs {
 };
 
 template <class T, bool VEC, int K>
-__global__ void __maxnreg__(128) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   let_next_start();
   Pipe<NORM_OPS, true> p(a.pipe, smem);
   wait_for_previous();
-  p.start();
+  p.start(VEC && a.pipe.pad);
   const int group = threadIdx.x / a.pipe.group, tid = threadIdx.x - group * a.pipe.group, warp = tid >> 5, warps = a.pipe.group >> 5;
   Cols<VEC> c = {static_cast<uint32_t>(tid), static_cast<uint32_t>(a.pipe.group), static_cast<uint32_t>(a.pipe.hidden)};
   const float inverse = 1.0f / static_cast<float>(a.pipe.hidden);
   const bool has_y = a.pipe.in[NORM_Y].p != nullptr, per_token = a.pipe.in[NORM_GATE].p != nullptr;
+  const bool has_post = a.w_post.p != nullptr, has_h = a.h.p != nullptr, has_z = a.z.p != nullptr;
   float* const words = p.words() + group * warps * 8;
+  // w_pre and beta * gate * w_post as fp32 in shared memory (registers would allow half as many
+  // warps); K = 4 reads them again for every row
+  constexpr bool kHold = K <= 2;
+  const int columns = VEC ? 8 * K * a.pipe.group : a.pipe.hidden;
+  float* const held_pre = reinterpret_cast<float*>(smem + kPipeHeader + a.pipe.stages * p.stage_bytes);
+  float* const held_gw = held_pre + columns;
+  auto load_pre = [&](int k, Unit& u) {
+    u.fill(0.0f);
+    if (has_z && c.has(k)) c.load_any(a.w_pre.p, a.w_pre.f32, k, u);
+  };
+  auto load_gw = [&](int k, Unit& u) {
+    Unit g;
+    u.fill(c.has(k) ? a.beta : 0.0f);
+    if (has_post && c.has(k)) {
+      c.load_any(a.w_post.p, a.w_post.f32, k, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], g.v[j]);
+    }
+    if (a.gate.p && !per_token && c.has(k)) {
+      c.load_any(row_of(a.gate, p.row / a.pipe.per_segment), a.gate.f32, k, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], g.v[j]);
+    }
+  };
   int turn = 0;
   auto sum = [&](float2 s) { return group_sum(s.x + s.y, words, turn, warps, warp, 1 + group, a.pipe.group); };
-  Unit w_pre[K], gw[K];  // gw = gate * w_post
-  if (a.z.p) {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (c.has(k)) c.load_any(a.w_pre.p, a.w_pre.f32, k, w_pre[k]);
-  }
-  const bool has_post = a.w_post.p != nullptr;
   do {
-    if (has_y) {
+    if (kHold) {
+      // each thread the columns that it reads itself, or one group for all
+      if (a.pipe.groups > 1) asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
+      if (group == 0) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (!c.has(k)) continue;
-        gw[k].fill(1.0f);
-        if (has_post) c.load_any(a.w_post.p, a.w_post.f32, k, gw[k]);
-        if (a.gate.p && !per_token) {
-          Unit g;
-          c.load_any(row_of(a.gate, p.row / a.pipe.per_segment), a.gate.f32, k, g);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) gw[k].v[j] = mul2(gw[k].v[j], g.v[j]);
+        for (int k = 0; k < K; ++k) {
+          Unit u;
+          load_pre(k, u);
+          c.store(held_pre, k, u);
+          load_gw(k, u);
+          c.store(held_gw, k, u);
         }
       }
+      if (a.pipe.groups > 1) asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
     }
     int rows;
     do {
@@ -90,30 +109,31 @@ __global__ void __maxnreg__(128) norm_kernel(const __grid_constant__ NormArgs a)
       Unit h[K];
       if (mine) {
         const uint8_t* const staged = p.staged(group);
-        const T* const y = reinterpret_cast<const T*>(p.at(NORM_Y, group, staged, VEC));
         const T* const x = reinterpret_cast<const T*>(p.at(NORM_X, group, staged, VEC));
         if (has_y) {
+          const T* const y = reinterpret_cast<const T*>(p.at(NORM_Y, group, staged, VEC));
           float2 s = both(0.0f);
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            if (!c.has(k)) continue;
             c.load(y, k, h[k]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) s = fma2(h[k].v[j], h[k].v[j], s);
           }
           if (a.y8.data) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-              if (!c.has(k)) h[k].fill(0.0f);
+            for (int k = 0; k < K; ++k)
               c.save(h[k], k, a.y8.data + row * a.y8.stride, a.y8.scales + row * a.y8.scale_stride, a.y8.e4m3);
-            }
           }
-          float2 f = both(a.beta);
-          if (has_post) f = both(a.beta * rsqrtf(sum(s) * inverse + a.eps));
+          const float2 tau = both(has_post ? rsqrtf(sum(s) * inverse + a.eps) : 1.0f);
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            if (!c.has(k)) continue;
             Unit u;
+            if (kHold)
+              c.load(held_gw, k, u);
+            else
+              load_gw(k, u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[k].v[j] = mul2(mul2(h[k].v[j], tau), u.v[j]);
             if (per_token) {
               if (a.gate.f32)
                 c.load(reinterpret_cast<const float*>(p.at(NORM_GATE, group, staged, VEC)), k, u);
@@ -124,12 +144,11 @@ __global__ void __maxnreg__(128) norm_kernel(const __grid_constant__ NormArgs a)
             }
             c.load(x, k, u);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[k].v[j] = fma2(u.v[j], both(a.alpha), mul2(mul2(h[k].v[j], gw[k].v[j]), f));
+            for (int j = 0; j < 4; ++j) h[k].v[j] = fma2(u.v[j], both(a.alpha), h[k].v[j]);
           }
         } else {
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            if (!c.has(k)) continue;
             c.load(x, k, h[k]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) h[k].v[j] = mul2(h[k].v[j], both(a.alpha));
@@ -140,10 +159,10 @@ __global__ void __maxnreg__(128) norm_kernel(const __grid_constant__ NormArgs a)
       p.refill(false);
       if (mine) {
         float2 s = both(0.0f);
+        T* const to = row_of<T>(a.h, row);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (!c.has(k)) continue;
-          if (a.h.p) c.store(row_of<T>(a.h, row), k, h[k]);
+          if (has_h && c.has(k)) c.store(to, k, h[k]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) s = fma2(h[k].v[j], h[k].v[j], s);
         }
@@ -151,22 +170,24 @@ __global__ void __maxnreg__(128) norm_kernel(const __grid_constant__ NormArgs a)
 #pragma unroll
           for (int k = 0; k < K; ++k) {
             Unit r;
-            r.fill(0.0f);
-            if (c.has(k)) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) r.at(i) = round_to(h[k].at(i), static_cast<const T*>(nullptr));
-            }
+            for (int j = 0; j < 4; ++j) r.v[j] = round_to(h[k].v[j], static_cast<const T*>(nullptr));
             c.save(r, k, a.h8.data + row * a.h8.stride, a.h8.scales + row * a.h8.scale_stride, a.h8.e4m3);
           }
         }
-        if (a.z.p) {
+        if (has_z) {
           const float2 rho = both(rsqrtf(sum(s) * inverse + a.eps));
+          T* const out = row_of<T>(a.z, row);
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            if (!c.has(k)) continue;
+            Unit u;
+            if (kHold)
+              c.load(held_pre, k, u);
+            else
+              load_pre(k, u);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[k].v[j] = mul2(mul2(h[k].v[j], rho), w_pre[k].v[j]);
-            c.store(row_of<T>(a.z, row), k, h[k]);
+            for (int j = 0; j < 4; ++j) h[k].v[j] = mul2(mul2(h[k].v[j], rho), u.v[j]);
+            if (c.has(k)) c.store(out, k, h[k]);
           }
         }
       }
@@ -218,11 +239,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const __grid
   }
   float s = 0.0f;
   if (in) {
+    // a gate row that more CTAs share begins in the first one (its first gate row, or its last) and is the first of the others
+    const int64_t step = r < 0 ? 1 : 2;
+    const int64_t odd = r >= 0 && r != first_row(first, a.tokens, a.ctas) / a.per_gate;
+    const float* p = part + col;
 #pragma unroll 4
-    for (int64_t c = first + warp; c < last; c += kJoinWarps) {
-      const int64_t slot = r < 0 ? c : 2 * c + (r == first_row(c, a.tokens, a.ctas) / a.per_gate ? 0 : 1);
-      s += part[slot * a.hidden + col];
-    }
+    for (int64_t c = first + warp; c < last; c += kJoinWarps) s += p[(step * c + (c == first ? odd : 0)) * a.hidden];
   }
   words[warp][lane] = s;
   __syncthreads();
@@ -249,7 +271,7 @@ Fit fit(int64_t hidden, int threads_per_sm) {
   f.per_sm = std::max(1, (f.k == 4 ? 512 : threads_per_sm) / f.threads());
   return f;
 }
-Fit norm_fit(int64_t hidden) { return fit(hidden, 512); }
+Fit norm_fit(int64_t hidden) { return fit(hidden, 768); }
 Fit grad_fit(int64_t hidden) { return fit(hidden, 512); }
 int64_t ctas_of(const Fit& f, int64_t tokens) { return std::min(ops_ceil_div(tokens, f.groups), kSms * f.per_sm); }
 
@@ -257,30 +279,33 @@ int64_t ctas_of(const Fit& f, int64_t tokens) { return std::min(ops_ceil_div(tok
 template <int OPS>
 struct Operands {
   PipeArgs<OPS> pipe = {};
-  void range(int op, const void* data, int64_t stride, int64_t bytes) {
+  int64_t columns;  // of a staged row: all that its threads hold where it is read unit by unit
+  Operands(const Fit& f, bool vec, int64_t hidden) : columns(vec ? int64_t(8) * f.k * f.group : hidden) {}
+  void range(int op, const void* data, int64_t stride, int64_t bytes, int64_t place) {
     pipe.in[op] = {static_cast<const uint8_t*>(data), stride, static_cast<int32_t>(bytes), pipe.row_bytes};
-    pipe.row_bytes += static_cast<int32_t>(ops_round_up(bytes + 15, 16));
+    pipe.row_bytes += static_cast<int32_t>(ops_round_up(place + 15, 16));
   }
   void matrix(int op, const lst_matrix* m) {
-    if (m) range(op, m->data, m->stride * dtype_bytes(m->dtype), m->cols * dtype_bytes(m->dtype));
+    if (m) range(op, m->data, m->stride * dtype_bytes(m->dtype), m->cols * dtype_bytes(m->dtype), columns * dtype_bytes(m->dtype));
   }
   // values and scales; returns 1 for integers, 2 for e4m3, 0 for no checkpoint
   int32_t kept(int op, const lst_checkpoint* c) {
     if (!c) return 0;
-    range(op, c->data, c->stride, c->cols);
-    range(op + 1, c->scales, c->scale_stride, ops_ceil_div(c->cols, kCkptBlock));
+    range(op, c->data, c->stride, c->cols, columns);
+    range(op + 1, c->scales, c->scale_stride, ops_ceil_div(c->cols, kCkptBlock), ops_ceil_div(columns, kCkptBlock));
     return c->format == LST_CHECKPOINT_E4M3 ? 2 : 1;
   }
   // `sums`: floats per column that each of several groups leaves in shared memory; `held`: that
   // the CTA keeps there. Where not even one stage fits, rows are taken fewer at a time, then
   // fewer CTAs to an SM. Returns the shared memory of a CTA.
   size_t plan(const Fit& f, int64_t tokens, int64_t hidden, int64_t per_segment, int sums, int held) {
+    pipe.pad = columns > hidden;
     pipe.tokens = static_cast<int32_t>(tokens), pipe.per_segment = static_cast<int32_t>(per_segment);
     pipe.hidden = static_cast<int32_t>(hidden);
     pipe.group = f.group, pipe.ctas = static_cast<int32_t>(ctas_of(f, tokens));
     int groups = f.groups, per_sm = f.per_sm;
     for (;;) {
-      const int64_t stage = static_cast<int64_t>(pipe.row_bytes) * groups, columns = ops_round_up(hidden, 8);
+      const int64_t stage = static_cast<int64_t>(pipe.row_bytes) * groups;
       const int64_t extra = ((groups > 1 ? groups * sums : 0) + held) * columns * 4;
       const int64_t room = std::min<int64_t>(kSharedPerSm / per_sm - 1024, kMaxShared) - kPipeHeader - extra;
       pipe.groups = groups;
@@ -419,11 +444,11 @@ extern "C" lst_status lst_residual_norm(const lst_matrix* x, const lst_matrix* y
   const bool token = gate && gate->rows == s.tokens && s.tokens > 1;
   const bool vec = s.hidden % 8 == 0 && on16(x) && on16(y) && on16(h) && on16(z) && (!token || on16(gate));
   const Fit f = norm_fit(s.hidden);
-  Operands<NORM_OPS> o;
+  Operands<NORM_OPS> o(f, vec, s.hidden);
   o.matrix(NORM_X, x);
   o.matrix(NORM_Y, y);
   if (token) o.matrix(NORM_GATE, gate);
-  const size_t smem = o.plan(f, s.tokens, s.hidden, gate && !token ? s.tokens / gate->rows : s.tokens, 0, 0);
+  const size_t smem = o.plan(f, s.tokens, s.hidden, gate && !token ? s.tokens / gate->rows : s.tokens, 0, f.k == 2 ? 2 : 0);
   const NormArgs a = {o.pipe, rows_arg(h), rows_arg(z), weights_arg(gate), weights_arg(w_post), weights_arg(w_pre), kept_arg(h8),
                       kept_arg(y8), params->residual_scale, params->branch_scale, params->eps};
   const NormKernel<NormArgs> kernel = s.dtype == LST_F32 ? (vec ? norm_of<float, true>(f.k) : norm_of<float, false>(f.k))
@@ -491,7 +516,7 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   const bool token = per_gate == 1 && s.tokens > 1;
   const bool vec = s.hidden % 8 == 0 && on16(dh) && on16(dz) && on16(h_in) && on16(y_in) && on16(dx) && on16(dy) && (!token || on16(gate));
   const Fit f = grad_fit(s.hidden);
-  Operands<GRAD_OPS> o;
+  Operands<GRAD_OPS> o(f, vec && f.k == 2, s.hidden);
   GradArgs a = {};
   o.matrix(GRAD_DH, dh), o.matrix(GRAD_DZ, dz), o.matrix(GRAD_H, h_in), o.matrix(GRAD_Y, y_in);
   a.h_kept = o.kept(GRAD_H, dz ? h8 : nullptr);

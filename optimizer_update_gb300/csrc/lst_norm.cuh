@@ -56,7 +56,7 @@ template <int OPS>
 struct PipeArgs {
   Range in[OPS];
   int32_t tokens, per_segment;  // no turn holds rows of two segments (gate rows)
-  int32_t hidden, ctas, group, groups, row_bytes, stages;
+  int32_t hidden, ctas, group, groups, row_bytes, stages, pad;
 };
 
 // First row of CTA c: the rows divided evenly.
@@ -93,6 +93,7 @@ struct Pipe {
   int begin, end, row, segment;   // rows of this CTA, of this turn, and where its segment ends
   int ahead, ahead_segment;       // the next turn to be filled
   int stage_bytes, stage, into;
+  const uint8_t* current;  // the stage of this turn
   uint32_t phase;
   bool ok;
 
@@ -100,6 +101,7 @@ struct Pipe {
     full = tc::smem_addr(smem), empty = full + 8 * kMaxStages;
     stage_bytes = a.row_bytes * a.groups;
     stage = into = 0, phase = 0, ok = true;
+    current = smem + kPipeHeader;
     if (STAGED) {
       if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
@@ -160,7 +162,14 @@ struct Pipe {
     if (ahead == ahead_segment && ahead < end) ahead_segment = segment_end(ahead);
     if (++into == a.stages) into = 0;
   }
-  __device__ __forceinline__ void start() {
+  // With `pad`, ranges are shorter than their places in a stage, where zeros stand behind them.
+  __device__ __forceinline__ void start(bool pad) {
+    if (STAGED && pad) {
+      uint4* const p = reinterpret_cast<uint4*>(smem + kPipeHeader);
+      for (int i = threadIdx.x; i < a.stages * stage_bytes / 16; i += blockDim.x) p[i] = make_uint4(0, 0, 0, 0);
+      tc::fence_async_proxy_cta();
+      __syncthreads();
+    }
     if (STAGED && threadIdx.x < 32)
       for (int i = 0; i < a.stages && ahead < end; ++i) fill();
   }
@@ -178,7 +187,7 @@ struct Pipe {
   }
   // The staged row of group `g` in this turn, and operand `op` of it; `aligned`: its rows are on 16 bytes.
   __device__ __forceinline__ const uint8_t* staged(int g) const {
-    return smem + kPipeHeader + stage * stage_bytes + g * a.row_bytes;
+    return current + g * a.row_bytes;
   }
   __device__ __forceinline__ const uint8_t* at(int op, int g, const uint8_t* staged_row, bool aligned) const {
     if (!STAGED) return a.in[op].p + static_cast<int64_t>(row + g) * a.in[op].stride;
@@ -196,7 +205,10 @@ struct Pipe {
   // The next turn; false behind the last of a segment.
   __device__ __forceinline__ bool next(int n) {
     refill(true);
-    if (STAGED && ++stage == a.stages) stage = 0, phase ^= 1;
+    if (STAGED) {
+      current += stage_bytes;
+      if (++stage == a.stages) stage = 0, phase ^= 1, current = smem + kPipeHeader;
+    }
     row += n;
     return row < segment;
   }
@@ -233,7 +245,8 @@ __device__ __forceinline__ float group_sum(float v, float* words, int& turn, int
   return __shfl_sync(0xffffffffu, v, 0);
 }
 // The same for 8 values: lanes exchange halves, quarters and eighths of them (9 shuffles
-// instead of 40).
+// instead of 40). The first `kWanted` are given back.
+template <int kWanted>
 __device__ __forceinline__ void group_sum8(float (&v)[8], float* words, int& turn, int warps, int warp, int bar, int threads) {
   const int lane = threadIdx.x & 31;
   float u[4];
@@ -255,13 +268,18 @@ __device__ __forceinline__ void group_sum8(float (&v)[8], float* words, int& tur
     turn ^= 1;
     if ((lane & 3) == 0) words[warp * 8 + (lane >> 2)] = s;
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
-    s = 0.0f;
-    for (int w = lane & 3; w < warps; w += 4) s += words[w * 8 + (lane >> 2)];
+    float t[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int w = (lane & 3) + 4 * j;
+      t[j] = w < warps ? words[w * 8 + (lane >> 2)] : 0.0f;
+    }
+    s = (t[0] + t[1]) + (t[2] + t[3]);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     s += __shfl_xor_sync(0xffffffffu, s, 1);
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = __shfl_sync(0xffffffffu, s, 4 * j);
+  for (int j = 0; j < kWanted; ++j) v[j] = __shfl_sync(0xffffffffu, s, 4 * j);
 }
 
 // ---- backward ----------------------------------------------------------------------

@@ -36,7 +36,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
   let_next_start();
   Pipe<GRAD_OPS, STAGED> p(a.pipe, smem);
   wait_for_previous();
-  p.start();
+  p.start(VEC && a.pipe.pad);
   const int group = threadIdx.x / a.pipe.group, tid = threadIdx.x - group * a.pipe.group, warp = tid >> 5, warps = a.pipe.group >> 5;
   const int64_t cta = blockIdx.x;
   Cols<VEC> c = {static_cast<uint32_t>(tid), static_cast<uint32_t>(a.pipe.group), static_cast<uint32_t>(a.pipe.hidden)};
@@ -51,7 +51,8 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
   int turn = 0;
   // weights as fp32 in shared memory, where registers would spill; K = 4 reads them again for every row
   constexpr bool kHold = K <= 2;
-  const int columns = (hidden + 7) & ~7;
+  constexpr bool kPadded = VEC && STAGED;  // units behind the row are zeros there: only stores pass over them
+  const int columns = kPadded ? 8 * K * a.pipe.group : hidden;
   float* const group_sums = reinterpret_cast<float*>(smem + kPipeHeader + a.pipe.stages * p.stage_bytes);
   float* const held_pre = group_sums + (a.pipe.groups > 1 ? a.pipe.groups * 2 * columns : 0);
   float* const held_gw = held_pre + columns;
@@ -80,10 +81,12 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
       if (group == 0) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (!c.has(k)) continue;
           Unit u;
-          if (has_z) load_pre(k, u), c.store(held_pre, k, u);
-          load_gw(p.row, k, u);
+          u.fill(0.0f);
+          if (has_z && c.has(k)) load_pre(k, u);
+          c.store(held_pre, k, u);
+          u.fill(0.0f);
+          if (c.has(k)) load_gw(p.row, k, u);
           c.store(held_gw, k, u);
         }
       }
@@ -109,6 +112,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
             load_gw(p.row + group, k, u);
         };
         const uint8_t* const staged = p.staged(group);
+        T *const dx_row = row_of<T>(a.dx, row), *const dy_row = row_of<T>(a.dy, row);
         const T* const dh_row = reinterpret_cast<const T*>(p.at(GRAD_DH, group, staged, VEC));
         const T* const dz_row = reinterpret_cast<const T*>(p.at(GRAD_DZ, group, staged, VEC));
         auto either = [&](int op, int kept, int k, Unit& u) {
@@ -131,7 +135,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
           for (int j = 0; j < 6; ++j) s2[j] = both(0.0f);
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            if (!c.has(k)) continue;
+            if (!kPadded && !c.has(k)) continue;
             Unit w, d;
             if (has_z) {
               pre_unit(k, w);
@@ -164,7 +168,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
           }
 #pragma unroll
           for (int j = 0; j < 6; ++j) s[j] = s2[j].x + s2[j].y;
-          group_sum8(s, words, turn, warps, warp, 1 + group, a.pipe.group);
+          group_sum8<6>(s, words, turn, warps, warp, 1 + group, a.pipe.group);
         }
         p.refill(false);
         const float rho = has_z ? rsqrtf(s[0] * inverse + a.eps) : 0.0f, back = rho * rho * (s[1] * inverse);
@@ -173,7 +177,8 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
         const float2 rho2 = both(rho), of_h = both(-rho * back), alpha = both(a.alpha), tau_beta = both(tau * a.beta), of_y = both(-tau * back_y);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (!c.has(k)) continue;
+          const bool there = c.has(k);
+          if (!kPadded && !there) continue;
           Unit w, d, out;
           if (has_dh)
             c.load(dh_row, k, d);
@@ -193,7 +198,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
           if (has_dx) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) out.v[j] = mul2(d.v[j], alpha);
-            c.store(row_of<T>(a.dx, row), k, out);
+            if (there) c.store(dx_row, k, out);
           }
           if (has_y) either(GRAD_Y, y_kept, k, y);
           gw_unit(k, w);
@@ -207,7 +212,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
               if (token) out.v[j] = mul2(out.v[j], g.v[j]);
               if (has_post) out.v[j] = fma2(y.v[j], of_y, out.v[j]);
             }
-            c.store(row_of<T>(a.dy, row), k, out);
+            if (there) c.store(dy_row, k, out);
           }
           if (has_y) {
 #pragma unroll
@@ -220,7 +225,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
                 sum_a[k].v[j] = fma2(d.v[j], y.v[j], sum_a[k].v[j]);
               }
             }
-            if (token && a.dgate) store_sums(a.dgate, row * a.dgate_stride, a.dgate_f32, a.accumulate, c, k, out);
+            if (token && a.dgate && there) store_sums(a.dgate, row * a.dgate_stride, a.dgate_f32, a.accumulate, c, k, out);
           }
         }
       }
