@@ -45,10 +45,9 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// With `rho` (a factor per row) and `weight` (per column, or null): the norm of the row.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(256)
-    restore_kernel(Kept in, T* __restrict__ out, int64_t ld, int64_t rows, int cols, int parts, const float* __restrict__ rho) {
+    restore_kernel(Kept in, T* __restrict__ out, int64_t ld, int64_t rows, int cols, int parts) {
   let_next_start();
   wait_for_previous();
   const int lane = threadIdx.x & 31;
@@ -62,53 +61,112 @@ __global__ void __launch_bounds__(256)
       if (!c.has(k)) continue;
       Unit u;
       c.restore(in.data + row * in.stride + col, in.scales + row * in.scale_stride + col / kCkptBlock, in.e4m3, k, u);
-      if (rho) {
-        const float2 r = both(rho[row]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], r);
-      }
       c.store(out + row * ld + col, k, u);
     }
   }
 }
 
-// rho[row] = rsqrt(mean of the restored row's squares + eps), a warp a row.
-template <bool VEC>
-__global__ void __launch_bounds__(256) rho_kernel(Kept in, int64_t rows, int cols, float eps, float* __restrict__ rho) {
+// The operands of the weight gradient's product. X: the restored rows, or with `norm` those
+// times rsqrt(mean of their squares + eps), as bf16 rows of whole units of 16 columns (what
+// stands behind a row's last column is not read); by `threads` threads a row, 32 or 256.
+// Blocks from `row_blocks` on copy the rows of dy where they are not on 16 bytes.
+//
+// Converting X on its way into the product instead (four warps beside the loads, codes by a
+// ring of their own) kept the tensor cores waiting: a K step takes 512 cycles and 125 of
+// the 128 bytes a cycle that shared memory moves; 8192 x 11008 x 4096 took 1750 us.
+struct OperandArgs {
+  Kept in;
+  uint16_t* x;
+  int64_t x_ld, rows;
+  int32_t cols, norm, threads, row_blocks;
+  float eps;
+  const uint16_t* dy;
+  uint16_t* dy_out;
+  int64_t dy_ld, dy_out_ld;
+  int32_t dy_cols;
+};
+__device__ __forceinline__ void restore16(const uint8_t* data, const uint8_t* scales, bool e4m3, int col, float2 (&v)[8]) {
+  const uint4 q = *reinterpret_cast<const uint4*>(data + col);  // rows reach to the next 16 columns
+  const float2 step = both(ckpt_step(scales[col / kCkptBlock]));
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if (e4m3) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ckpt_decode4(w[j], true, v[2 * j], v[2 * j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ckpt_decode4(w[j], false, v[2 * j], v[2 * j + 1]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = mul2(v[j], step);
+}
+__global__ void __launch_bounds__(256) operand_kernel(const __grid_constant__ OperandArgs a) {
+  __shared__ float words[8];
   let_next_start();
   wait_for_previous();
-  const int lane = threadIdx.x & 31;
-  for (int64_t row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += static_cast<int64_t>(gridDim.x) * 8) {
-    float2 sums = both(0.0f);
-    for (int col = 0; col < cols; col += kWarpColumns) {
-      const Cols<VEC> c = {static_cast<uint32_t>(lane), 32u, static_cast<uint32_t>(min(cols - col, kWarpColumns))};
+  if (blockIdx.x >= a.row_blocks) {
+    const int units = (a.dy_cols + 7) / 8;
+    for (int64_t r = blockIdx.x - a.row_blocks; r < a.rows; r += gridDim.x - a.row_blocks)
+      for (int u = threadIdx.x; u < units; u += 256) {
+        const uint16_t* p = a.dy + r * a.dy_ld + 8 * u;
+        uint32_t v[8];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (!c.has(k)) continue;
-        Unit u;
-        c.restore(in.data + row * in.stride + col, in.scales + row * in.scale_stride + col / kCkptBlock, in.e4m3, k, u);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sums = fma2(u.v[j], u.v[j], sums);
+        for (int i = 0; i < 8; ++i) v[i] = 8 * u + i < a.dy_cols ? p[i] : 0u;
+        *reinterpret_cast<uint4*>(a.dy_out + r * a.dy_out_ld + 8 * u) =
+            make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
       }
-    }
-    float s = sums.x + sums.y;
+    return;
+  }
+  const int tid = threadIdx.x & (a.threads - 1), at_once = 256 / a.threads;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * at_once; first < a.rows; first += static_cast<int64_t>(a.row_blocks) * at_once) {
+    const int64_t row = first + threadIdx.x / a.threads;
+    const bool mine = row < a.rows;  // whole warps; with 256 threads a row all of them
+    const uint8_t *data = a.in.data + row * a.in.stride, *scales = a.in.scales + row * a.in.scale_stride;
+    float2 rho = both(1.0f);
+    if (a.norm) {
+      float2 sums = both(0.0f);
+      if (mine) {
+#pragma unroll 4
+        for (int col = 16 * tid; col < a.cols; col += 16 * a.threads) {
+          float2 v[8];
+          restore16(data, scales, a.in.e4m3, col, v);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) rho[row] = __frsqrt_rn(s / static_cast<float>(cols) + eps);
+          for (int j = 0; j < 8; ++j) {
+            if (col + 2 * j >= a.cols) v[j].x = 0.0f;  // what lies behind the row may be anything
+            if (col + 2 * j + 1 >= a.cols) v[j].y = 0.0f;
+            sums = fma2(v[j], v[j], sums);
+          }
+        }
+      }
+      float s = sums.x + sums.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (a.threads == 256) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = s;
+        __syncthreads();
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += words[i];
+      }
+      rho = both(rsqrtf(s / static_cast<float>(a.cols) + a.eps));
+    }
+    if (!mine) continue;
+#pragma unroll 4
+    for (int col = 16 * tid; col < a.cols; col += 16 * a.threads) {
+      float2 v[8];
+      restore16(data, scales, a.in.e4m3, col, v);
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = pack_bf16(mul2(v[j], rho));
+      uint4* const to = reinterpret_cast<uint4*>(a.x + row * a.x_ld + col);
+      to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
   }
 }
 
-// Rows of dy at a pitch that is a multiple of 16 bytes.
-__global__ void __launch_bounds__(256)
-    pack_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int cols, uint16_t* __restrict__ dst,
-                     int64_t dst_ld) {
-  let_next_start();
-  wait_for_previous();
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int c = threadIdx.x; c < cols; c += 256) dst[r * dst_ld + c] = src[r * ld + c];
-}
-
-// dw = the sum of the products' partial sums, times the weight of the column, added to dw or not.
+// dw = the sum of the products' partial sums, times the weight of the column, added to dw or
+// not; 4 columns a thread.
 struct FinishArgs {
   const float* part;
   int64_t ld, split_stride;
@@ -117,26 +175,49 @@ struct FinishArgs {
   int64_t dw_ld;
   int32_t splits, weight_f32, dw_f32, accumulate, cols;
   int64_t rows;
+  int32_t vec;
 };
 __global__ void __launch_bounds__(256) wgrad_finish_kernel(const __grid_constant__ FinishArgs a) {
   let_next_start();
   wait_for_previous();
-  const int64_t total = a.rows * a.cols;
+  const int quads = (a.cols + 3) / 4;
+  const int64_t total = a.rows * quads;
   for (int64_t t = blockIdx.x * int64_t(256) + threadIdx.x; t < total; t += int64_t(256) * gridDim.x) {
-    const int64_t row = t / a.cols;
-    const int col = static_cast<int>(t - row * a.cols);
-    const float* p = a.part + row * a.ld + col;
-    float s = 0.0f;
-    for (int k = 0; k < a.splits; ++k) s += p[k * a.split_stride];
+    const int64_t row = t / quads;
+    const int col = 4 * static_cast<int>(t - row * quads);
+    const float* p = a.part + row * a.ld + col;  // ld is a multiple of 4
+    float4 s = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+    for (int k = 0; k < a.splits; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(p + k * a.split_stride);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    float d[4] = {s.x, s.y, s.z, s.w};
+    const int n = min(4, a.cols - col);
     if (a.weight)
-      s *= a.weight_f32 ? static_cast<const float*>(a.weight)[col]
-                        : __bfloat162float(static_cast<const __nv_bfloat16*>(a.weight)[col]);
-    if (a.dw_f32) {
-      float* q = static_cast<float*>(a.dw) + row * a.dw_ld + col;
-      *q = a.accumulate ? *q + s : s;
-    } else {
-      __nv_bfloat16* q = static_cast<__nv_bfloat16*>(a.dw) + row * a.dw_ld + col;
-      *q = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*q) + s : s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n)
+          d[j] *= a.weight_f32 ? static_cast<const float*>(a.weight)[col + j]
+                               : __bfloat162float(static_cast<const __nv_bfloat16*>(a.weight)[col + j]);
+    if (n == 4 && a.vec == 16 && !a.accumulate) {
+      if (a.dw_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.dw) + row * a.dw_ld + col) = make_float4(d[0], d[1], d[2], d[3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.dw) + row * a.dw_ld + col) =
+            make_uint2(pack_bf16(make_float2(d[0], d[1])), pack_bf16(make_float2(d[2], d[3])));
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= n) break;
+      if (a.dw_f32) {
+        float* q = static_cast<float*>(a.dw) + row * a.dw_ld + col + j;
+        *q = a.accumulate ? *q + d[j] : d[j];
+      } else {
+        __nv_bfloat16* q = static_cast<__nv_bfloat16*>(a.dw) + row * a.dw_ld + col + j;
+        *q = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*q) + d[j] : d[j]);
+      }
     }
   }
 }
@@ -148,6 +229,8 @@ Kept kept_arg(const lst_checkpoint* c) {
 bool on16(const lst_matrix* m) {
   return reinterpret_cast<uintptr_t>(m->data) % 16 == 0 && (m->rows <= 1 || m->stride * dtype_bytes(m->dtype) % 16 == 0);
 }
+// Rows that tile loads take.
+bool tile_rows(const lst_matrix* m) { return reinterpret_cast<uintptr_t>(m->data) % 16 == 0 && m->stride % 8 == 0; }
 unsigned warp_grid(int64_t tasks) { return static_cast<unsigned>(std::min(ops_ceil_div(tasks, 8), kSms * 8)); }
 
 template <class T>
@@ -158,10 +241,10 @@ cudaError_t launch_save(const lst_matrix* x, const lst_checkpoint* c, bool vec, 
                         static_cast<int>(parts));
 }
 template <class T>
-cudaError_t launch_restore(const lst_checkpoint* c, T* out, int64_t ld, bool vec, const float* rho, cudaStream_t stream) {
+cudaError_t launch_restore(const lst_checkpoint* c, T* out, int64_t ld, bool vec, cudaStream_t stream) {
   const int64_t parts = ops_ceil_div(c->cols, kWarpColumns);
   return launch_chained(vec ? restore_kernel<T, true> : restore_kernel<T, false>, dim3(warp_grid(c->rows * parts)), dim3(256), 0,
-                        stream, kept_arg(c), out, ld, c->rows, static_cast<int>(c->cols), static_cast<int>(parts), rho);
+                        stream, kept_arg(c), out, ld, c->rows, static_cast<int>(c->cols), static_cast<int>(parts));
 }
 
 lst_status check_pair(const lst_matrix* m, const char* name, const lst_checkpoint* c, const char* cname, const char* who) {
@@ -179,27 +262,27 @@ bool wgrad_sizes_fit(int64_t n, int64_t o, int64_t h) {
 }
 
 struct WgradPlan {
-  int64_t splits, part_ld, dy_ld, x_ld, rho_off, dy_off, x_off, part_off, bytes;
+  int64_t splits, part_ld, dy_ld, x_ld, dy_off, x_off, part_off, bytes;
 };
-WgradPlan wgrad_plan(const lst_matrix* dy, const lst_checkpoint* c, const lst_matrix* dw) {
-  (void)dw;
+// Sums are split where whole tiles leave half of the 76 CTA pairs idle, into ranges of at
+// least 8 steps of 64 tokens.
+WgradPlan wgrad_plan(const lst_matrix* dy, const lst_checkpoint* c) {
   WgradPlan p;
   const int64_t n = dy->rows, o = dy->cols, h = c->cols;
   const int64_t blocks = ops_ceil_div(n, 64), tiles = ops_ceil_div(o, kGemmTile) * ops_ceil_div(h, kGemmTile);
-  p.splits = std::max<int64_t>(1, std::min<int64_t>({32, blocks / 8, 152 / tiles}));
+  p.splits = std::max<int64_t>(1, std::min<int64_t>(blocks / 8, 76 / tiles));
   p.part_ld = ops_round_up(h, 32);
   p.dy_ld = ops_round_up(o, 8);
-  p.x_ld = ops_round_up(h, 8);
+  p.x_ld = ops_round_up(h, 16);
   int64_t at = 0;
   auto take = [&](int64_t size) {
     const int64_t off = at;
     at += ops_round_up(size, 256);
     return off;
   };
-  p.rho_off = take(n * 4);
-  p.dy_off = take(on16(dy) && dy->stride % 8 == 0 ? 0 : n * p.dy_ld * 2);
+  p.dy_off = take(tile_rows(dy) ? 0 : n * p.dy_ld * 2);
   p.x_off = take(n * p.x_ld * 2);
-  p.part_off = take(p.splits * o * p.part_ld * 4);
+  p.part_off = take(p.splits > 1 ? p.splits * o * p.part_ld * 4 : 0);
   p.bytes = at;
   return p;
 }
@@ -228,8 +311,8 @@ extern "C" lst_status lst_checkpoint_restore(const lst_checkpoint* c, const lst_
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   const bool vec = out->cols % 8 == 0 && on16(out);
   LST_TRY_CUDA(out->dtype == LST_F32
-                   ? launch_restore<float>(c, static_cast<float*>(out->data), out->stride, vec, nullptr, stream)
-                   : launch_restore<__nv_bfloat16>(c, static_cast<__nv_bfloat16*>(out->data), out->stride, vec, nullptr, stream),
+                   ? launch_restore<float>(c, static_cast<float*>(out->data), out->stride, vec, stream)
+                   : launch_restore<__nv_bfloat16>(c, static_cast<__nv_bfloat16*>(out->data), out->stride, vec, stream),
                who);
   return LST_OK;
 }
@@ -238,7 +321,7 @@ extern "C" int64_t lst_checkpoint_wgrad_workspace_bytes(const lst_matrix* dy, co
   if (!dy || !c || !dw || dy->rows != c->rows || dw->rows != dy->cols || dw->cols != c->cols ||
       !wgrad_sizes_fit(dy->rows, dy->cols, c->cols))
     return 0;
-  return wgrad_plan(dy, c, dw).bytes;
+  return wgrad_plan(dy, c).bytes;
 }
 
 extern "C" lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_checkpoint* c, const lst_matrix* norm_weight,
@@ -271,40 +354,37 @@ extern "C" lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_check
   const int64_t n = dy->rows, o = dy->cols, h = c->cols;
   if (!wgrad_sizes_fit(n, o, h))
     return fail(LST_ERR_INVALID_ARG, "%s: more than 2^24 tokens, or an operand of more than 2^40 elements", who);
-  const WgradPlan p = wgrad_plan(dy, c, dw);
+  const WgradPlan p = wgrad_plan(dy, c);
   LST_TRY(check_workspace(workspace, workspace_bytes, p.bytes, who));
   char* ws = static_cast<char*>(workspace);
-  float* rho = norm_weight ? reinterpret_cast<float*>(ws + p.rho_off) : nullptr;
-  if (rho)
-    LST_TRY_CUDA(launch_chained(h % 8 == 0 ? rho_kernel<true> : rho_kernel<false>, dim3(warp_grid(n)), dim3(256), 0, stream,
-                                kept_arg(c), n, static_cast<int>(h), eps, rho),
-                 who);
-  const void* dyp = dy->data;
-  int64_t dy_ld = dy->stride;
-  if (!(on16(dy) && dy->stride % 8 == 0)) {
-    dyp = ws + p.dy_off;
-    dy_ld = p.dy_ld;
-    LST_TRY_CUDA(launch_chained(pack_rows_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(n, 8192))), dim3(256), 0, stream,
-                                static_cast<const uint16_t*>(dy->data), dy->stride, n, static_cast<int>(o),
-                                reinterpret_cast<uint16_t*>(ws + p.dy_off), p.dy_ld),
-                 who);
-  }
-  __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(ws + p.x_off);
-  LST_TRY_CUDA(launch_restore<__nv_bfloat16>(c, x, p.x_ld, h % 8 == 0, rho, stream), who);
+  const bool pack = !tile_rows(dy);
+  const int threads = n >= kSms * 8 || h <= 1024 ? 32 : 256;  // a warp a row where there are rows for all of them
+  const int64_t row_blocks = std::min(ops_ceil_div(n, 256 / threads), kSms * 8);
+  const OperandArgs x = {kept_arg(c), reinterpret_cast<uint16_t*>(ws + p.x_off), p.x_ld, n, static_cast<int32_t>(h), norm_weight != nullptr,
+                         threads, static_cast<int32_t>(row_blocks), eps, static_cast<const uint16_t*>(dy->data),
+                         reinterpret_cast<uint16_t*>(ws + p.dy_off), dy->stride, p.dy_ld, static_cast<int32_t>(o)};
+  LST_TRY_CUDA(launch_chained(operand_kernel, dim3(static_cast<unsigned>(row_blocks + (pack ? std::min(n, kSms * 8) : 0))), dim3(256), 0, stream, x), who);
   GemmProblem g;
-  g.a = {dyp, o, n, dy_ld, true};
-  g.b = {x, h, n, p.x_ld, true};
+  if (pack)
+    g.a = {x.dy_out, o, n, p.dy_ld, true};
+  else
+    g.a = {dy->data, o, n, dy->stride, true};
+  g.b = {x.x, h, n, p.x_ld, true};
   g.m = o;
   g.n = h;
   g.k = n;
   g.splits = static_cast<int>(p.splits);
-  g.partial = {reinterpret_cast<float*>(ws + p.part_off), p.part_ld, o * p.part_ld, 0};
-  LST_TRY_CUDA(launch_gemm(GEMM_BF16, &g, 1, stream), who);
+  const bool weight_f32 = norm_weight && norm_weight->dtype == LST_F32;
+  const int vec = on16(dw) && dw->stride * dtype_bytes(dw->dtype) % 16 == 0 ? 16 : 2;
+  g.wgrad = {dw->data, dw->stride, norm_weight ? norm_weight->data : nullptr, dw->dtype == LST_F32, weight_f32, accumulate != 0, vec, {}};
+  if (p.splits > 1) g.wgrad.partial = {reinterpret_cast<float*>(ws + p.part_off), p.part_ld, o * p.part_ld, 0};
+  LST_TRY_CUDA(launch_gemm(GEMM_BF16_WGRAD, &g, 1, stream), who);
+  if (p.splits == 1) return LST_OK;
   const int64_t blocks = ops_ceil_div(n, 64), splits = ops_ceil_div(blocks, ops_ceil_div(blocks, p.splits));
-  const FinishArgs f = {g.partial.out, p.part_ld, o * p.part_ld, norm_weight ? norm_weight->data : nullptr, dw->data, dw->stride,
-                        static_cast<int32_t>(splits), norm_weight && norm_weight->dtype == LST_F32, dw->dtype == LST_F32,
-                        accumulate != 0, static_cast<int32_t>(h), o};
-  LST_TRY_CUDA(launch_chained(wgrad_finish_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(ops_ceil_div(o * h, 256), kSms * 8))),
+  const FinishArgs f = {g.wgrad.partial.out, p.part_ld, o * p.part_ld, g.wgrad.weight, dw->data, dw->stride, static_cast<int32_t>(splits),
+                        weight_f32, dw->dtype == LST_F32, accumulate != 0, static_cast<int32_t>(h), o, vec};
+  const int64_t quads = ops_ceil_div(h, 4);
+  LST_TRY_CUDA(launch_chained(wgrad_finish_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(ops_ceil_div(o * quads, 256), kSms * 8))),
                               dim3(256), 0, stream, f),
                who);
   return LST_OK;

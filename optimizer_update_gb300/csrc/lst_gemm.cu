@@ -502,6 +502,140 @@ struct GradEpilogue {
   }
 };
 
+// A weight gradient: the sums times a weight per column, written or added.
+struct WgradEpilogue {
+  using Params = WgradParams;
+  using Table = Nothing;
+  // What the gradient holds comes to L2 while the main loop runs.
+  template <int kCols>
+  static __device__ __forceinline__ void prepare(const Params& e, const Table&, const Shape& s, const Tile&, int row, int col0) {
+    if (!e.accumulate || e.partial.out || row >= s.m || col0 >= s.n || e.vec < 16) return;
+    const int size = e.f32 ? 4 : 2, bytes = (min(kCols, s.n - col0) * size) & ~15;
+    const char* p = static_cast<const char*>(e.out) + (static_cast<int64_t>(row) * e.ld + col0) * size;
+    if (bytes > 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+  }
+  static __device__ __forceinline__ float weight_of(const Params& e, int col) {
+    return e.weight_f32 ? static_cast<const float*>(e.weight)[col] : __bfloat162float(static_cast<const __nv_bfloat16*>(e.weight)[col]);
+  }
+  // Rows on 16 bytes: 32 columns of 32 rows at a time, 16 bytes a lane.
+  template <bool kBf16, int kCols>
+  static __device__ __forceinline__ void units(const Params& e, char* out, int rows, int col0, int left, uint32_t tmem, uint32_t turn) {
+    constexpr int kUnit = kBf16 ? 8 : 4, kAcross = 32 / kUnit, kDown = 32 / kAcross, kLoads = 32 / kDown, kSize = kBf16 ? 2 : 4;
+    const int lane = threadIdx.x & 31, r0 = lane / kAcross, c0 = kUnit * (lane % kAcross);
+#pragma unroll 1
+    for (int g = 0; g < kCols / 32; ++g) {
+      const int mine = left - 32 * g - c0;  // columns from this lane's first on
+      if (32 * g >= left) break;
+      char* const p0 = out + (r0 * e.ld + 32 * g + c0) * kSize;
+      uint4 old[kLoads];
+      if (e.accumulate) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          if (mine >= kUnit && kDown * i + r0 < rows) old[i] = __ldcg(reinterpret_cast<const uint4*>(p0 + kDown * i * e.ld * kSize));
+      }
+      float w[kUnit];
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) w[j] = e.weight && j < mine ? weight_of(e, col0 + 32 * g + c0 + j) : 1.0f;
+      float4 v[8];
+      load_units<kUnit>(tmem + 32 * g, turn, v);
+      if (mine <= 0) continue;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        if (kDown * i + r0 >= rows) break;
+        char* const p = p0 + kDown * i * e.ld * kSize;
+        float d[kUnit];
+        if (kBf16) {
+          const float4 lo = v[(2 * i) & 7], hi = v[(2 * i + 1) & 7];
+          const float t[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int j = 0; j < kUnit; ++j) d[j] = t[j] * w[j];
+        } else {
+          const float t[4] = {v[i & 7].x, v[i & 7].y, v[i & 7].z, v[i & 7].w};
+#pragma unroll
+          for (int j = 0; j < kUnit; ++j) d[j] = t[j & 3] * w[j];
+        }
+        if (mine >= kUnit) {
+          const uint32_t o[4] = {old[i].x, old[i].y, old[i].z, old[i].w};
+          uint4 n;
+          if (kBf16) {
+            if (e.accumulate) {
+#pragma unroll
+              for (int j = 0; j < kUnit; ++j) d[j] += __uint_as_float(j & 1 ? o[(j >> 1) & 3] & 0xffff0000u : o[(j >> 1) & 3] << 16);
+            }
+            n = make_uint4(pack16(d[0], d[1], true), pack16(d[2], d[3], true), pack16(d[4 % kUnit], d[5 % kUnit], true),
+                           pack16(d[6 % kUnit], d[7 % kUnit], true));
+          } else {
+            if (e.accumulate) {
+#pragma unroll
+              for (int j = 0; j < kUnit; ++j) d[j] += __uint_as_float(o[j & 3]);
+            }
+            n = make_uint4(__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]), __float_as_uint(d[3]));
+          }
+          *reinterpret_cast<uint4*>(p) = n;
+        } else {
+#pragma unroll
+          for (int j = 0; j < kUnit; ++j)
+            if (j < mine) put(e, p + j * kSize, d[j]);
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ void put(const Params& e, char* p, float v) {
+    if (e.f32) {
+      float* q = reinterpret_cast<float*>(p);
+      *q = e.accumulate ? *q + v : v;
+    } else {
+      __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(p);
+      *q = __float2bfloat16_rn(e.accumulate ? __bfloat162float(*q) + v : v);
+    }
+  }
+  template <int kCols, class Release>
+  static __device__ __forceinline__ void run(const Params& e, const Table& table, const Shape& s, const Tile& t, int row,
+                                             int col0, uint32_t tmem, uint32_t turn, Release release) {
+    if (e.partial.out) {
+      PartialEpilogue::run<kCols>(e.partial, table, s, t, row, col0, tmem, turn, release);
+      return;
+    }
+    const int row0 = row & ~31, lane = row & 31, rows = s.m - row0, left = s.n - col0, size = e.f32 ? 4 : 2;
+    char* const out = static_cast<char*>(e.out) + (static_cast<int64_t>(row0) * e.ld + col0) * size;
+    if (e.vec >= 16) {
+      if (e.f32)
+        units<false, kCols>(e, out, rows, col0, left, tmem, turn);
+      else
+        units<true, kCols>(e, out, rows, col0, left, tmem, turn);
+    } else {
+#pragma unroll 1
+      for (int g = 0; g < kCols / 32; ++g) {
+        if (32 * g >= left) break;
+        const bool inside = 32 * g + lane < left;
+        const float w = e.weight && inside ? weight_of(e, col0 + 32 * g + lane) : 1.0f;
+        float v[32], old[32];
+        if (e.accumulate) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (inside && i < rows) {
+              const char* p = out + (i * e.ld + 32 * g + lane) * size;
+              old[i] = e.f32 ? *reinterpret_cast<const float*>(p) : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
+            }
+        }
+        load_turned(tmem + 32 * g, turn, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (inside && i < rows) {
+            char* p = out + (i * e.ld + 32 * g + lane) * size;
+            const float y = e.accumulate ? old[i] + v[i] * w : v[i] * w;
+            if (e.f32)
+              *reinterpret_cast<float*>(p) = y;
+            else
+              *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(y);
+          }
+      }
+    }
+    __syncwarp();
+    release();
+  }
+};
+
 // One row's logits of 128 vocabulary entries: their maximum M, the sum of
 // exp(l - M), the target's logit where it is among them, and (for the
 // gradient) q = (M - l) * 2^11 in 16 bits. q keeps l to 2^-12 over the 32
@@ -893,6 +1027,7 @@ int resident_pairs() {
 void set_params(StoreParams* e, Nothing*, const GemmProblem& p, const UpdateTable*) { *e = p.store; }
 void set_params(GradParams* e, Nothing*, const GemmProblem& p, const UpdateTable*) { *e = {p.store, p.partial}; }
 void set_params(XentParams* e, Nothing*, const GemmProblem& p, const UpdateTable*) { *e = p.xent; }
+void set_params(WgradParams* e, Nothing*, const GemmProblem& p, const UpdateTable*) { *e = p.wgrad; }
 void set_params(UpdateParams* e, UpdateTable* t, const GemmProblem& p, const UpdateTable* updates) {
   *e = p.update;
   for (int64_t i = p.update.first; i < p.update.first + p.batch; ++i) {
@@ -977,6 +1112,10 @@ cudaError_t launch_gemm(GemmKind kind, const GemmProblem* p, int count, cudaStre
     case GEMM_F16: return launch_fit<StoreEpilogue, false>(p, count, stream, nullptr);
     case GEMM_F16_UPDATE: return launch_fit<UpdateEpilogue, false>(p, count, stream, updates);
     case GEMM_BF16: return launch_fit<GradEpilogue, true>(p, count, stream, nullptr);
+    // split sums fill the pairs with whole tiles (see lst_checkpoint.cu)
+    case GEMM_BF16_WGRAD:
+      return p->splits > 1 ? launch<WgradEpilogue, true, 256>(p, count, stream, nullptr)
+                           : launch_fit<WgradEpilogue, true>(p, count, stream, nullptr);
     case GEMM_BF16_XENT: return launch<XentEpilogue, true, 256>(p, count, stream, nullptr);
     case GEMM_BF16_XENT_FEW:
       return p->n <= 32 ? launch<XentFewEpilogue, true, 32>(p, count, stream, nullptr)

@@ -65,12 +65,23 @@ struct XentParams {
   int32_t index_bytes;
 };
 
+// out = weight[column] * acc (+ out), bf16 or fp32, on any alignment (`vec`: 16 where its
+// rows start on 16 bytes); or partial sums where partial.out is not null.
+struct WgradParams {
+  void* out;
+  int64_t ld;
+  const void* weight;
+  int32_t f32, weight_f32, accumulate, vec;
+  PartialParams partial;
+};
+
 enum GemmKind {
   GEMM_F16,         // fp16 operands, StoreParams
   GEMM_F16_UPDATE,  // fp16 operands, UpdateParams
   GEMM_BF16,        // bf16 operands, StoreParams or PartialParams
   GEMM_BF16_XENT,   // bf16 operands, XentParams
   GEMM_BF16_XENT_FEW,
+  GEMM_BF16_WGRAD,  // bf16 operands, WgradParams
 };
 
 struct GemmProblem {
@@ -82,6 +93,7 @@ struct GemmProblem {
   PartialParams partial{};
   XentParams xent{};
   UpdateParams update{};
+  WgradParams wgrad{};
 };
 
 constexpr int kGemmMaxProblems = 8;
