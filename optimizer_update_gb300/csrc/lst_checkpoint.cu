@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The operands of the weight gradient's product. X: the restored rows, or with `norm` those
+// The operands of the weight gradient's product. X: the restored rows, or with NORM those
 // times rsqrt(mean of their squares + eps), as bf16 rows of whole units of 16 columns (what
 // stands behind a row's last column is not read); by `threads` threads a row, 32 or 256.
 // Blocks from `row_blocks` on copy the rows of dy where they are not on 16 bytes.
@@ -78,7 +78,7 @@ struct OperandArgs {
   Kept in;
   uint16_t* x;
   int64_t x_ld, rows;
-  int32_t cols, norm, threads, row_blocks;
+  int32_t cols, threads, row_blocks;
   float eps;
   const uint16_t* dy;
   uint16_t* dy_out;
@@ -99,7 +99,8 @@ __device__ __forceinline__ void restore16(const uint8_t* data, const uint8_t* sc
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = mul2(v[j], step);
 }
-__global__ void __launch_bounds__(256) operand_kernel(const __grid_constant__ OperandArgs a) {
+template <bool NORM>
+__global__ void __launch_bounds__(256, 5) operand_kernel(const __grid_constant__ OperandArgs a) {
   __shared__ float words[8];
   let_next_start();
   wait_for_previous();
@@ -122,10 +123,10 @@ __global__ void __launch_bounds__(256) operand_kernel(const __grid_constant__ Op
     const bool mine = row < a.rows;  // whole warps; with 256 threads a row all of them
     const uint8_t *data = a.in.data + row * a.in.stride, *scales = a.in.scales + row * a.in.scale_stride;
     float2 rho = both(1.0f);
-    if (a.norm) {
+    if (NORM) {
       float2 sums = both(0.0f);
       if (mine) {
-#pragma unroll 4
+#pragma unroll 2
         for (int col = 16 * tid; col < a.cols; col += 16 * a.threads) {
           float2 v[8];
           restore16(data, scales, a.in.e4m3, col, v);
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(256) operand_kernel(const __grid_constant__ Op
       rho = both(rsqrtf(s / static_cast<float>(a.cols) + a.eps));
     }
     if (!mine) continue;
-#pragma unroll 4
+#pragma unroll 2
     for (int col = 16 * tid; col < a.cols; col += 16 * a.threads) {
       float2 v[8];
       restore16(data, scales, a.in.e4m3, col, v);
@@ -360,10 +361,10 @@ extern "C" lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_check
   const bool pack = !tile_rows(dy);
   const int threads = n >= kSms * 8 || h <= 1024 ? 32 : 256;  // a warp a row where there are rows for all of them
   const int64_t row_blocks = std::min(ops_ceil_div(n, 256 / threads), kSms * 8);
-  const OperandArgs x = {kept_arg(c), reinterpret_cast<uint16_t*>(ws + p.x_off), p.x_ld, n, static_cast<int32_t>(h), norm_weight != nullptr,
+  const OperandArgs x = {kept_arg(c), reinterpret_cast<uint16_t*>(ws + p.x_off), p.x_ld, n, static_cast<int32_t>(h),
                          threads, static_cast<int32_t>(row_blocks), eps, static_cast<const uint16_t*>(dy->data),
                          reinterpret_cast<uint16_t*>(ws + p.dy_off), dy->stride, p.dy_ld, static_cast<int32_t>(o)};
-  LST_TRY_CUDA(launch_chained(operand_kernel, dim3(static_cast<unsigned>(row_blocks + (pack ? std::min(n, kSms * 8) : 0))), dim3(256), 0, stream, x), who);
+  LST_TRY_CUDA(launch_chained(norm_weight ? operand_kernel<true> : operand_kernel<false>, dim3(static_cast<unsigned>(row_blocks + (pack ? std::min(n, kSms * 8) : 0))), dim3(256), 0, stream, x), who);
   GemmProblem g;
   if (pack)
     g.a = {x.dy_out, o, n, p.dy_ld, true};

@@ -96,16 +96,19 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t w) { return make_float2(_
 __device__ __forceinline__ float2 round_to(float2 v, const float*) { return v; }
 __device__ __forceinline__ float2 round_to(float2 v, const __nv_bfloat16*) { return unpack_bf16(pack_bf16(v)); }
 
-// Eight values of a row in a thread.
-struct Unit {
-  float2 v[4];
+// Values of a row in a thread: a unit of eight, or half of one.
+template <int P>
+struct Part {
+  float2 v[P];
   __device__ __forceinline__ float& at(int i) { return i & 1 ? v[i >> 1].y : v[i >> 1].x; }
   __device__ __forceinline__ float at(int i) const { return i & 1 ? v[i >> 1].y : v[i >> 1].x; }
   __device__ __forceinline__ void fill(float s) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = both(s);
+    for (int j = 0; j < P; ++j) v[j] = both(s);
   }
 };
+using Unit = Part<4>;
+using Half = Part<2>;
 
 // A row of `cols` values held in units by `threads` threads (a multiple of 32). On the
 // vector path (rows on 16 bytes, a multiple of 8 columns) a unit is 8 consecutive
@@ -122,60 +125,76 @@ struct Cols {
   __device__ __forceinline__ bool in(int k, int i) const { return at(k, VEC ? 0 : i) < cols; }
   __device__ __forceinline__ bool has(int k) const { return !VEC || at(k, 0) < cols; }
 
-  __device__ __forceinline__ void load(const float* p, int k, Unit& u) const {
+  // Unit k, or the half of it from its value `i0` on.
+  template <int P>
+  __device__ __forceinline__ void load(const float* p, int k, Part<P>& u, int i0 = 0) const {
     if (VEC) {
-      const float4 a = *reinterpret_cast<const float4*>(p + at(k, 0)), b = *reinterpret_cast<const float4*>(p + at(k, 4));
-      u.v[0] = make_float2(a.x, a.y), u.v[1] = make_float2(a.z, a.w), u.v[2] = make_float2(b.x, b.y), u.v[3] = make_float2(b.z, b.w);
+#pragma unroll
+      for (int j = 0; j < P; j += 2) {
+        const float4 a = *reinterpret_cast<const float4*>(p + at(k, i0 + 2 * j));
+        u.v[j] = make_float2(a.x, a.y), u.v[j + 1] = make_float2(a.z, a.w);
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u.at(i) = in(k, i) ? p[at(k, i)] : 0.0f;
+      for (int i = 0; i < 2 * P; ++i) u.at(i) = in(k, i0 + i) ? p[at(k, i0 + i)] : 0.0f;
     }
   }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, int k, Unit& u) const {
-    if (VEC) {
+  template <int P>
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int k, Part<P>& u, int i0 = 0) const {
+    if (VEC && P == 4) {
       const uint4 a = *reinterpret_cast<const uint4*>(p + at(k, 0));
       const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u.v[j] = unpack_bf16(w[j]);
+      for (int j = 0; j < P; ++j) u.v[j] = unpack_bf16(w[j & 3]);
+    } else if (VEC) {
+      const uint2 a = *reinterpret_cast<const uint2*>(p + at(k, i0));
+      u.v[0] = unpack_bf16(a.x), u.v[1] = unpack_bf16(a.y);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u.at(i) = in(k, i) ? __bfloat162float(p[at(k, i)]) : 0.0f;
+      for (int i = 0; i < 2 * P; ++i) u.at(i) = in(k, i0 + i) ? __bfloat162float(p[at(k, i0 + i)]) : 0.0f;
     }
   }
-  __device__ __forceinline__ void store(float* p, int k, const Unit& u) const {
+  template <int P>
+  __device__ __forceinline__ void store(float* p, int k, const Part<P>& u, int i0 = 0) const {
     if (VEC) {
-      *reinterpret_cast<float4*>(p + at(k, 0)) = make_float4(u.v[0].x, u.v[0].y, u.v[1].x, u.v[1].y);
-      *reinterpret_cast<float4*>(p + at(k, 4)) = make_float4(u.v[2].x, u.v[2].y, u.v[3].x, u.v[3].y);
+#pragma unroll
+      for (int j = 0; j < P; j += 2)
+        *reinterpret_cast<float4*>(p + at(k, i0 + 2 * j)) = make_float4(u.v[j].x, u.v[j].y, u.v[j + 1].x, u.v[j + 1].y);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (in(k, i)) p[at(k, i)] = u.at(i);
+      for (int i = 0; i < 2 * P; ++i)
+        if (in(k, i0 + i)) p[at(k, i0 + i)] = u.at(i);
     }
   }
-  __device__ __forceinline__ void store(__nv_bfloat16* p, int k, const Unit& u) const {
-    if (VEC) {
-      *reinterpret_cast<uint4*>(p + at(k, 0)) = make_uint4(pack_bf16(u.v[0]), pack_bf16(u.v[1]), pack_bf16(u.v[2]), pack_bf16(u.v[3]));
+  template <int P>
+  __device__ __forceinline__ void store(__nv_bfloat16* p, int k, const Part<P>& u, int i0 = 0) const {
+    if (VEC && P == 4) {
+      *reinterpret_cast<uint4*>(p + at(k, 0)) =
+          make_uint4(pack_bf16(u.v[0]), pack_bf16(u.v[1]), pack_bf16(u.v[2 % P]), pack_bf16(u.v[3 % P]));
+    } else if (VEC) {
+      *reinterpret_cast<uint2*>(p + at(k, i0)) = make_uint2(pack_bf16(u.v[0]), pack_bf16(u.v[1]));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (in(k, i)) p[at(k, i)] = __float2bfloat16_rn(u.at(i));
+      for (int i = 0; i < 2 * P; ++i)
+        if (in(k, i0 + i)) p[at(k, i0 + i)] = __float2bfloat16_rn(u.at(i));
     }
   }
   // Weights of either type, on any alignment.
-  template <class T>
-  __device__ __forceinline__ void load_weights(const T* p, int k, Unit& u) const {
+  template <class T, int P>
+  __device__ __forceinline__ void load_weights(const T* p, int k, Part<P>& u, int i0) const {
     if (VEC && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
-      load(p, k, u);
+      load(p, k, u, i0);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u.at(i) = in(k, i) ? static_cast<float>(p[at(k, i)]) : 0.0f;
+      for (int i = 0; i < 2 * P; ++i) u.at(i) = in(k, i0 + i) ? static_cast<float>(p[at(k, i0 + i)]) : 0.0f;
     }
   }
-  __device__ __forceinline__ void load_any(const void* p, bool f32, int k, Unit& u) const {
+  template <int P>
+  __device__ __forceinline__ void load_any(const void* p, bool f32, int k, Part<P>& u, int i0 = 0) const {
     if (f32)
-      load_weights(static_cast<const float*>(p), k, u);
+      load_weights(static_cast<const float*>(p), k, u, i0);
     else
-      load_weights(static_cast<const __nv_bfloat16*>(p), k, u);
+      load_weights(static_cast<const __nv_bfloat16*>(p), k, u, i0);
   }
 
   // Unit k to and from a checkpoint's row. All threads of a warp save together, units that
@@ -212,22 +231,29 @@ struct Cols {
       }
     }
   }
-  __device__ __forceinline__ void restore(const uint8_t* data, const uint8_t* scales, bool e4m3, int k, Unit& u) const {
+  template <int P>
+  __device__ __forceinline__ void restore(const uint8_t* data, const uint8_t* scales, bool e4m3, int k, Part<P>& u, int i0 = 0) const {
     if (VEC) {
-      const uint2 w = *reinterpret_cast<const uint2*>(data + at(k, 0));
+      uint32_t w[2];
+      if (P == 4) {
+        const uint2 q = *reinterpret_cast<const uint2*>(data + at(k, 0));
+        w[0] = q.x, w[1] = q.y;
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(data + at(k, i0));
+      }
       const float step = has(k) ? ckpt_step(scales[at(k, 0) / kCkptBlock]) : 0.0f;  // a byte behind the row may be anything
-      ckpt_decode4(w.x, e4m3, u.v[0], u.v[1]);
-      ckpt_decode4(w.y, e4m3, u.v[2], u.v[3]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], both(step));
+      for (int j = 0; j < P; j += 2) ckpt_decode4(w[j >> 1], e4m3, u.v[j], u.v[j + 1]);
+#pragma unroll
+      for (int j = 0; j < P; ++j) u.v[j] = mul2(u.v[j], both(step));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 2 * P; ++i) {
         u.at(i) = 0.0f;
-        if (in(k, i)) {
+        if (in(k, i0 + i)) {
           float2 a, b;
-          ckpt_decode4(data[at(k, i)], e4m3, a, b);
-          u.at(i) = a.x * ckpt_step(scales[at(k, i) / kCkptBlock]);
+          ckpt_decode4(data[at(k, i0 + i)], e4m3, a, b);
+          u.at(i) = a.x * ckpt_step(scales[at(k, i0 + i) / kCkptBlock]);
         }
       }
     }

@@ -580,6 +580,42 @@ struct WgradEpilogue {
       }
     }
   }
+  // Rows on any alignment: a column a lane.
+  template <class T, int kCols>
+  static __device__ __forceinline__ void turned(const Params& e, char* out, int rows, int col0, int left, uint32_t tmem, uint32_t turn) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int g = 0; g < kCols / 32; ++g) {
+      if (32 * g >= left) break;
+      const bool inside = 32 * g + lane < left;
+      const float w = e.weight && inside ? weight_of(e, col0 + 32 * g + lane) : 1.0f;
+      T* const first = reinterpret_cast<T*>(out) + 32 * g + lane;
+      float v[32];
+      if (e.accumulate) {
+        T old[32];
+        const T* p = first;
+#pragma unroll
+        for (int i = 0; i < 32; ++i, p += e.ld)
+          if (inside && i < rows) old[i] = *p;
+        load_turned(tmem + 32 * g, turn, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = static_cast<float>(old[i]) + v[i] * w;
+      } else {
+        load_turned(tmem + 32 * g, turn, v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = v[i] * w;
+      }
+      T* p = first;
+      if (inside && rows >= 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i, p += e.ld) *p = static_cast<T>(v[i]);
+      } else if (inside) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i, p += e.ld)
+          if (i < rows) *p = static_cast<T>(v[i]);
+      }
+    }
+  }
   static __device__ __forceinline__ void put(const Params& e, char* p, float v) {
     if (e.f32) {
       float* q = reinterpret_cast<float*>(p);
@@ -604,32 +640,10 @@ struct WgradEpilogue {
       else
         units<true, kCols>(e, out, rows, col0, left, tmem, turn);
     } else {
-#pragma unroll 1
-      for (int g = 0; g < kCols / 32; ++g) {
-        if (32 * g >= left) break;
-        const bool inside = 32 * g + lane < left;
-        const float w = e.weight && inside ? weight_of(e, col0 + 32 * g + lane) : 1.0f;
-        float v[32], old[32];
-        if (e.accumulate) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (inside && i < rows) {
-              const char* p = out + (i * e.ld + 32 * g + lane) * size;
-              old[i] = e.f32 ? *reinterpret_cast<const float*>(p) : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
-            }
-        }
-        load_turned(tmem + 32 * g, turn, v);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (inside && i < rows) {
-            char* p = out + (i * e.ld + 32 * g + lane) * size;
-            const float y = e.accumulate ? old[i] + v[i] * w : v[i] * w;
-            if (e.f32)
-              *reinterpret_cast<float*>(p) = y;
-            else
-              *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(y);
-          }
-      }
+if (e.f32)
+        turned<float, kCols>(e, out, rows, col0, left, tmem, turn);
+      else
+        turned<__nv_bfloat16, kCols>(e, out, rows, col0, left, tmem, turn);
     }
     __syncwarp();
     release();

@@ -196,27 +196,26 @@ __global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant
   p.finish(&g_norm_error);
 }
 
-// Adds up the CTAs' sums, 32 columns a CTA: blockIdx.y 0: dw_pre, 1: dw_post; from 2 on the
+// Adds up the CTAs' sums, 128 columns a CTA: blockIdx.y 0: dw_pre, 1: dw_post; from 2 on the
 // gate rows that more than one CTA worked on, by their number or (where there are more
 // gate rows than CTAs) as the last gate row of CTA blockIdx.y - 2.
 struct JoinArgs {
   const float *pre, *post, *gate;
   void *dw_pre, *dw_post, *dgate;
   int64_t dgate_stride, tokens, per_gate;
-  int32_t pre_f32, post_f32, gate_f32, accumulate, hidden, ctas, by_row;
+  int32_t pre_f32, post_f32, gate_f32, accumulate, hidden, ld, ctas, by_row;
 };
 constexpr int kJoinWarps = 16;
 __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const __grid_constant__ JoinArgs a) {
-  __shared__ float words[kJoinWarps][33];
+  __shared__ float4 words[kJoinWarps][32];
   let_next_start();
   wait_for_previous();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
-  const bool in = col < a.hidden;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 128 + 4 * lane;
   const float* part = blockIdx.y == 0 ? a.pre : a.post;
   void* out = blockIdx.y == 0 ? a.dw_pre : a.dw_post;
   bool f32 = blockIdx.y == 0 ? a.pre_f32 : a.post_f32;
   if (blockIdx.y < 2 && !out) return;
-  int64_t at = col, r = -1, first = 0, last = a.ctas;
+  int64_t at = 0, r = -1, first = 0, last = a.ctas;
   if (blockIdx.y >= 2) {
     part = a.gate, out = a.dgate, f32 = a.gate_f32;
     auto owner = [&](int64_t row) {  // the CTA whose rows include `row`
@@ -235,25 +234,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const __grid
     }
     last = owner((r + 1) * a.per_gate - 1) + 1;
     if (last == first + 1) return;  // its CTA has written it
-    at = r * a.dgate_stride + col;
+    at = r * a.dgate_stride;
   }
-  float s = 0.0f;
-  if (in) {
+  float4 s = make_float4(0, 0, 0, 0);
+  if (col < a.ld) {
     // a gate row that more CTAs share begins in the first one (its first gate row, or its last) and is the first of the others
     const int64_t step = r < 0 ? 1 : 2;
     const int64_t odd = r >= 0 && r != first_row(first, a.tokens, a.ctas) / a.per_gate;
     const float* p = part + col;
-#pragma unroll 4
-    for (int64_t c = first + warp; c < last; c += kJoinWarps) s += p[(step * c + (c == first ? odd : 0)) * a.hidden];
+#pragma unroll 8
+    for (int64_t c = first + warp; c < last; c += kJoinWarps) {
+      const float4 v = *reinterpret_cast<const float4*>(p + (step * c + (c == first ? odd : 0)) * a.ld);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
   }
   words[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && in) {
-    float v = 0.0f;
+  const int mine = blockIdx.x * 128 + threadIdx.x;
+  if (threadIdx.x >= 128 || mine >= a.hidden) return;
+  float v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) v += words[i][lane];
-    store_sum(out, at, f32, a.accumulate, v);
-  }
+  for (int i = 0; i < kJoinWarps; ++i) v += reinterpret_cast<const float*>(words[i])[threadIdx.x];
+  store_sum(out, at + mine, f32, a.accumulate, v);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -300,6 +302,12 @@ struct Operands {
   // fewer CTAs to an SM. Returns the shared memory of a CTA.
   size_t plan(const Fit& f, int64_t tokens, int64_t hidden, int64_t per_segment, int sums, int held) {
     pipe.pad = columns > hidden;
+    pipe.simple = 1;
+    for (const Range& r : pipe.in) {
+      if (!r.p) continue;
+      pipe.row_total += r.bytes;
+      if (reinterpret_cast<uintptr_t>(r.p) % 16 || (tokens > 1 && r.stride % 16) || r.bytes % 16) pipe.simple = 0;
+    }
     pipe.tokens = static_cast<int32_t>(tokens), pipe.per_segment = static_cast<int32_t>(per_segment);
     pipe.hidden = static_cast<int32_t>(hidden);
     pipe.group = f.group, pipe.ctas = static_cast<int32_t>(ctas_of(f, tokens));
@@ -310,7 +318,10 @@ struct Operands {
       const int64_t room = std::min<int64_t>(kSharedPerSm / per_sm - 1024, kMaxShared) - kPipeHeader - extra;
       pipe.groups = groups;
       pipe.stages = room < stage ? 0 : static_cast<int32_t>(std::min<int64_t>(kMaxStages, room / stage));
-      if (pipe.stages > 0 || (groups == 1 && per_sm == 1)) return static_cast<size_t>(kPipeHeader + pipe.stages * stage + extra);
+      if (pipe.stages > 0 || (groups == 1 && per_sm == 1)) {
+        pipe.ctas = static_cast<int32_t>(std::min<int64_t>(pipe.ctas, kSms * per_sm));  // all at once
+        return static_cast<size_t>(kPipeHeader + pipe.stages * stage + extra);
+      }
       if (groups > 1)
         groups /= 2;
       else
@@ -380,13 +391,16 @@ NormKernel<NormArgs> norm_of(int k) {
   return k == 2 ? norm_kernel<T, VEC, 2> : norm_kernel<T, VEC, 4>;
 }
 
+// Elements of a row of sums in the workspace.
+int64_t sum_row(int64_t hidden) { return ops_round_up(hidden, 4); }
+
 struct GradPlan {
   int64_t ctas, pre_off, post_off, gate_off, bytes;
 };
 GradPlan grad_plan(int64_t tokens, int64_t hidden, int64_t gate_rows) {
   GradPlan p;
   p.ctas = ctas_of(grad_fit(hidden), tokens);
-  const int64_t each = ops_round_up(p.ctas * hidden * 4, 256);
+  const int64_t each = ops_round_up(p.ctas * sum_row(hidden) * 4, 256);
   p.pre_off = 0;
   p.post_off = each;
   p.gate_off = 2 * each;
@@ -533,19 +547,19 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   a.part_post = dw_post ? reinterpret_cast<float*>(ws + p.post_off) : nullptr;
   a.part_gate = dgate ? reinterpret_cast<float*>(ws + p.gate_off) : nullptr;
   a.alpha = params->residual_scale, a.beta = params->branch_scale, a.eps = params->eps;
-  const bool all = dh && dz && dx && dy && !token && (w_post ? a.h_kept == a.y_kept : !need_y);
+  const bool all = o.pipe.simple && dh && dz && dx && dy && !token && (w_post ? a.h_kept == a.y_kept : !need_y);
   const int form = !all ? 0 : 1 + a.h_kept + (w_post ? 0 : 3);
-  const NormKernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_f32(vec, f.k == 4) : norm_grad_bf16(vec, f.k == 4, form);
+  const NormKernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_f32(vec, f.k == 4) : norm_grad_bf16(vec, f.k == 4, form, o.pipe.groups == 1);
   LST_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared), who);
-  LST_TRY_CUDA(launch_chained(kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(o.threads()), smem, stream, a), who);
+  LST_TRY_CUDA(launch_chained(kernel, dim3(static_cast<unsigned>(o.pipe.ctas)), dim3(o.threads()), smem, stream, a), who);
   if (!sums) return LST_OK;
   const int64_t gate_rows = dgate && !token ? gate->rows : 0;
   const JoinArgs j = {a.part_pre, a.part_post, a.part_gate, dw_pre ? dw_pre->data : nullptr, dw_post ? dw_post->data : nullptr,
                       a.dgate, a.dgate_stride, s.tokens, per_gate, dw_pre && dw_pre->dtype == LST_F32,
                       dw_post && dw_post->dtype == LST_F32, a.dgate_f32, a.accumulate, static_cast<int32_t>(s.hidden),
-                      static_cast<int32_t>(p.ctas), gate_rows <= p.ctas};
+                      static_cast<int32_t>(sum_row(s.hidden)), o.pipe.ctas, gate_rows <= o.pipe.ctas};
   LST_TRY_CUDA(launch_chained(norm_join_kernel,
-                              dim3(static_cast<unsigned>(ops_ceil_div(s.hidden, 32)), static_cast<unsigned>(2 + std::min(gate_rows, p.ctas))),
+                              dim3(static_cast<unsigned>(ops_ceil_div(s.hidden, 128)), static_cast<unsigned>(2 + std::min<int64_t>(gate_rows, o.pipe.ctas))),
                               dim3(32 * kJoinWarps), 0, stream, j),
                who);
   return LST_OK;

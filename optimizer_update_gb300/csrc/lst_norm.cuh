@@ -34,12 +34,12 @@ __device__ __forceinline__ float weight_at(const Weights& w, int64_t r, int64_t 
   return w.f32 ? static_cast<const float*>(p)[col] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[col]);
 }
 
-// f(column, value) for the columns of a unit
-template <bool VEC, class F>
-__device__ __forceinline__ void for_each(const Cols<VEC>& c, int k, const Unit& u, F f) {
+// f(column, value) for the columns of a unit, or of a half of it
+template <bool VEC, int P, class F>
+__device__ __forceinline__ void for_each(const Cols<VEC>& c, int k, const Part<P>& u, F f, int i0 = 0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c.in(k, i)) f(c.at(k, i), u.at(i));
+  for (int i = 0; i < 2 * P; ++i)
+    if (c.in(k, i0 + i)) f(c.at(k, i0 + i), u.at(i));
 }
 
 // ---- rows through shared memory ----------------------------------------------------
@@ -57,6 +57,7 @@ struct PipeArgs {
   Range in[OPS];
   int32_t tokens, per_segment;  // no turn holds rows of two segments (gate rows)
   int32_t hidden, ctas, group, groups, row_bytes, stages, pad;
+  int32_t simple, row_total;  // all ranges on 16 bytes, and their bytes in a row
 };
 
 // First row of CTA c: the rows divided evenly.
@@ -84,8 +85,48 @@ __device__ __forceinline__ Piece piece_of(const Range& r, int64_t row, uint32_t 
 constexpr int kMaxStages = 4;
 constexpr int kPipeHeader = 64 + 2 * 16 * 8 * 4;  // barriers; two turns of 16 warps' sums
 
-// With STAGED false (rows that do not fit in shared memory) rows are read where they are.
-template <int OPS, bool STAGED>
+// The rows from `ahead` on where some range is not on 16 bytes.
+template <int OPS>
+__device__ __forceinline__ void fill_ragged(const PipeArgs<OPS>& a, int ahead, int n, uint32_t to, uint32_t bar) {
+  const int lane = threadIdx.x & 31, pieces = n * OPS;
+  int bytes = 0;
+  bool edges = false;
+  for (int i = lane; i < pieces; i += 32) {
+    const Piece p = piece_of(a.in[i % OPS], ahead + i / OPS, to + (i / OPS) * a.row_bytes);
+    bytes += p.mid;
+    edges |= p.head + p.tail > 0;
+  }
+  bytes = __reduce_add_sync(0xffffffffu, bytes);
+  edges = __any_sync(0xffffffffu, edges);
+  if (edges) tc::fence_async_proxy_cta();  // lanes' bytes of the stage's last use before this one's copies
+  if (lane == 0) tc::mbar_expect_tx(bar, bytes);
+  __syncwarp();
+  for (int i = lane; i < pieces; i += 32) {
+    const Piece p = piece_of(a.in[i % OPS], ahead + i / OPS, to + (i / OPS) * a.row_bytes);
+    if (p.mid > 0) tc::bulk_load(p.dst + p.head, p.src + p.head, p.mid, bar);
+  }
+  if (edges) {
+    for (int r = 0; r < n; ++r) {
+      uint32_t v[OPS], at[OPS];
+#pragma unroll
+      for (int j = 0; j < OPS; ++j) {
+        const Piece p = piece_of(a.in[j], ahead + r, to + r * a.row_bytes);
+        const int k = lane & 15, from = lane < 16 ? k : p.head + p.mid + k;
+        at[j] = k < (lane < 16 ? p.head : p.tail) ? p.dst + from : 0u;
+        if (at[j]) v[j] = p.src[from];
+      }
+#pragma unroll
+      for (int j = 0; j < OPS; ++j)
+        if (at[j]) asm volatile("st.shared.u8 [%0], %1;" ::"r"(at[j]), "r"(v[j]) : "memory");
+    }
+  }
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(bar);
+}
+
+// With STAGED false (rows that do not fit in shared memory) rows are read where they are;
+// with RAGGED false all ranges are on 16 bytes.
+template <int OPS, bool STAGED, bool RAGGED = true>
 struct Pipe {
   const PipeArgs<OPS>& a;
   uint8_t* smem;
@@ -123,41 +164,21 @@ struct Pipe {
   // Warp 0 fills stage `into` with the next turn's rows. `full` takes two arrivals: the
   // first with the bytes of the bulk copies, the second when the lanes' bytes are there.
   __device__ __forceinline__ void fill() {
-    const int lane = threadIdx.x & 31, n = min(a.groups, ahead_segment - ahead), pieces = n * OPS;
+    const int lane = threadIdx.x & 31, n = min(a.groups, ahead_segment - ahead);
     const uint32_t to = tc::smem_addr(smem + kPipeHeader) + into * stage_bytes, bar = full + 8 * into;
-    int bytes = 0;
-    bool edges = false;
-    for (int i = lane; i < pieces; i += 32) {
-      const Piece p = piece_of(a.in[i % OPS], ahead + i / OPS, to + (i / OPS) * a.row_bytes);
-      bytes += p.mid;
-      edges |= p.head + p.tail > 0;
-    }
-    bytes = __reduce_add_sync(0xffffffffu, bytes);
-    edges = __any_sync(0xffffffffu, edges);
-    if (edges) tc::fence_async_proxy_cta();  // lanes' bytes of the stage's last use before this one's copies
-    if (lane == 0) tc::mbar_expect_tx(bar, bytes);
-    __syncwarp();
-    for (int i = lane; i < pieces; i += 32) {
-      const Piece p = piece_of(a.in[i % OPS], ahead + i / OPS, to + (i / OPS) * a.row_bytes);
-      if (p.mid > 0) tc::bulk_load(p.dst + p.head, p.src + p.head, p.mid, bar);
-    }
-    if (edges) {
-      for (int r = 0; r < n; ++r) {
-        uint32_t v[OPS], at[OPS];
-#pragma unroll
-        for (int j = 0; j < OPS; ++j) {
-          const Piece p = piece_of(a.in[j], ahead + r, to + r * a.row_bytes);
-          const int k = lane & 15, from = lane < 16 ? k : p.head + p.mid + k;
-          at[j] = k < (lane < 16 ? p.head : p.tail) ? p.dst + from : 0u;
-          if (at[j]) v[j] = p.src[from];
-        }
-#pragma unroll
-        for (int j = 0; j < OPS; ++j)
-          if (at[j]) asm volatile("st.shared.u8 [%0], %1;" ::"r"(at[j]), "r"(v[j]) : "memory");
+    if (!RAGGED || a.simple) {
+      // whole rows by bulk copies, a lane an operand: all other warps wait for this one
+      if (lane == 0) tc::mbar_expect_tx(bar, n * a.row_total);
+      __syncwarp();
+      if (lane < OPS && a.in[lane].p) {
+        const Range& r = a.in[lane];
+        const uint8_t* src = r.p + ahead * r.stride;
+        for (int i = 0; i < n; ++i) tc::bulk_load(to + i * a.row_bytes + r.slot, src + i * r.stride, r.bytes, bar);
       }
+      if (lane == 0) tc::mbar_arrive(bar);
+    } else {
+      fill_ragged<OPS>(a, ahead, n, to, bar);
     }
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(bar);
     ahead += n;
     if (ahead == ahead_segment && ahead < end) ahead_segment = segment_end(ahead);
     if (++into == a.stages) into = 0;
@@ -312,8 +333,9 @@ template <class Args>
 using NormKernel = void (*)(const Args);
 // The backward kernel for activations of a type (lst_norm_grad_bf16.cu, lst_norm_grad_f32.cu),
 // 16 columns a thread, or 32 for rows above 8192 (`wide`), and the word that its waits
-// set when one runs out. `form`: see lst_norm_grad.cuh.
-NormKernel<GradArgs> norm_grad_bf16(bool vec, bool wide, int form);
+// set when one runs out. `form`: 0 the general kernel; 1 + KEPT that for whole units of
+// bf16, 4 + KEPT without a norm behind the block; `one`: its ONE.
+NormKernel<GradArgs> norm_grad_bf16(bool vec, bool wide, int form, bool one);
 NormKernel<GradArgs> norm_grad_f32(bool vec, bool wide);
 cudaError_t norm_grad_bf16_take_error(int* out);
 cudaError_t norm_grad_f32_take_error(int* out);

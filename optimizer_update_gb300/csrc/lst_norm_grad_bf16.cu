@@ -3,19 +3,24 @@
 
 namespace lst {
 
-NormKernel<GradArgs> norm_grad_bf16(bool vec, bool wide, int form) {
-  if (vec && !wide) {
-    switch (form) {
-      case 1: return norm_grad_kernel<__nv_bfloat16, true, 2, true, 1>;
-      case 2: return norm_grad_kernel<__nv_bfloat16, true, 2, true, 2>;
-      case 3: return norm_grad_kernel<__nv_bfloat16, true, 2, true, 3>;
-      case 4: return norm_grad_kernel<__nv_bfloat16, true, 2, true, 4>;
-      case 5: return norm_grad_kernel<__nv_bfloat16, true, 2, true, 5>;
-      case 6: return norm_grad_kernel<__nv_bfloat16, true, 2, true, 6>;
-    }
+namespace {
+template <bool ONE>
+NormKernel<GradArgs> rows_kernel(int form) {
+  switch (form) {
+    case 1: return norm_grad_rows_kernel<0, true, ONE>;
+    case 2: return norm_grad_rows_kernel<1, true, ONE>;
+    case 3: return norm_grad_rows_kernel<2, true, ONE>;
+    case 4: return norm_grad_rows_kernel<0, false, ONE>;
+    case 5: return norm_grad_rows_kernel<1, false, ONE>;
+    default: return norm_grad_rows_kernel<2, false, ONE>;
   }
-  if (vec) return wide ? norm_grad_kernel<__nv_bfloat16, true, 4, false, 0> : norm_grad_kernel<__nv_bfloat16, true, 2, true, 0>;
-  return wide ? norm_grad_kernel<__nv_bfloat16, false, 4, false, 0> : norm_grad_kernel<__nv_bfloat16, false, 2, true, 0>;
+}
+}  // namespace
+
+NormKernel<GradArgs> norm_grad_bf16(bool vec, bool wide, int form, bool one) {
+  if (vec && !wide && form) return one ? rows_kernel<true>(form) : rows_kernel<false>(form);
+  if (vec) return wide ? norm_grad_kernel<__nv_bfloat16, true, 4, false> : norm_grad_kernel<__nv_bfloat16, true, 2, true>;
+  return wide ? norm_grad_kernel<__nv_bfloat16, false, 4, false> : norm_grad_kernel<__nv_bfloat16, false, 2, true>;
 }
 
 cudaError_t norm_grad_bf16_take_error(int* out) { return take_norm_error(out); }

@@ -4,8 +4,8 @@
 namespace lst {
 
 NormKernel<GradArgs> norm_grad_f32(bool vec, bool wide) {
-  if (vec) return wide ? norm_grad_kernel<float, true, 4, false, 0> : norm_grad_kernel<float, true, 2, true, 0>;
-  return wide ? norm_grad_kernel<float, false, 4, false, 0> : norm_grad_kernel<float, false, 2, true, 0>;
+  if (vec) return wide ? norm_grad_kernel<float, true, 4, false> : norm_grad_kernel<float, true, 2, true>;
+  return wide ? norm_grad_kernel<float, false, 4, false> : norm_grad_kernel<float, false, 2, true>;
 }
 
 cudaError_t norm_grad_f32_take_error(int* out) { return take_norm_error(out); }
