@@ -239,9 +239,11 @@ struct Cols {
         const uint2 q = *reinterpret_cast<const uint2*>(data + at(k, 0));
         w[0] = q.x, w[1] = q.y;
       } else {
-        w[0] = *reinterpret_cast<const uint32_t*>(data + at(k, i0));
+        w[0] = w[1] = *reinterpret_cast<const uint32_t*>(data + at(k, i0));
       }
-      const float step = has(k) ? ckpt_step(scales[at(k, 0) / kCkptBlock]) : 0.0f;  // a byte behind the row may be anything
+      const bool there = has(k);  // bytes behind the row may be anything
+      const float step = there ? ckpt_step(scales[at(k, 0) / kCkptBlock]) : 0.0f;
+      w[0] = there ? w[0] : 0u, w[1] = there ? w[1] : 0u;
 #pragma unroll
       for (int j = 0; j < P; j += 2) ckpt_decode4(w[j >> 1], e4m3, u.v[j], u.v[j + 1]);
 #pragma unroll

@@ -306,6 +306,7 @@ struct Operands {
     for (const Range& r : pipe.in) {
       if (!r.p) continue;
       pipe.row_total += r.bytes;
+      pipe.margin = std::max(pipe.margin, static_cast<int32_t>(ops_ceil_div(15, std::max<int64_t>(1, r.stride))));
       if (reinterpret_cast<uintptr_t>(r.p) % 16 || (tokens > 1 && r.stride % 16) || r.bytes % 16) pipe.simple = 0;
     }
     pipe.tokens = static_cast<int32_t>(tokens), pipe.per_segment = static_cast<int32_t>(per_segment);

@@ -58,6 +58,7 @@ struct PipeArgs {
   int32_t tokens, per_segment;  // no turn holds rows of two segments (gate rows)
   int32_t hidden, ctas, group, groups, row_bytes, stages, pad;
   int32_t simple, row_total;  // all ranges on 16 bytes, and their bytes in a row
+  int32_t margin;             // rows that span 15 bytes in every range
 };
 
 // First row of CTA c: the rows divided evenly.
@@ -85,7 +86,30 @@ __device__ __forceinline__ Piece piece_of(const Range& r, int64_t row, uint32_t 
 constexpr int kMaxStages = 4;
 constexpr int kPipeHeader = 64 + 2 * 16 * 8 * 4;  // barriers; two turns of 16 warps' sums
 
-// The rows from `ahead` on where some range is not on 16 bytes.
+// The rows from `ahead` on where some range is not on 16 bytes, `margin` rows from the first
+// and the last of all, so that the 16-byte pieces around a range's ends lie within the
+// matrix (what else they hold goes to a place's slack and is not used).
+template <int OPS>
+__device__ __forceinline__ void fill_rounded(const PipeArgs<OPS>& a, int ahead, int n, uint32_t to, uint32_t bar) {
+  const int lane = threadIdx.x & 31;
+  const bool mine = lane < OPS && a.in[lane].p;
+  const Range& r = a.in[mine ? lane : 0];
+  int bytes = 0;
+  for (int i = 0; i < n && mine; ++i) {
+    const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(r.p)) + static_cast<uint32_t>(ahead + i) * static_cast<uint32_t>(r.stride);
+    bytes += ((low & 15) + r.bytes + 15) & ~15;
+  }
+  bytes = __reduce_add_sync(0xffffffffu, bytes);
+  if (lane == 0) tc::mbar_expect_tx(bar, bytes);
+  __syncwarp();
+  for (int i = 0; i < n && mine; ++i) {
+    const uint8_t* src = r.p + (ahead + i) * r.stride;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
+    tc::bulk_load(to + i * a.row_bytes + r.slot, src - off, (off + r.bytes + 15) & ~15, bar);
+  }
+  if (lane == 0) tc::mbar_arrive(bar);
+}
+// The same for any rows, byte by byte at a range's ends.
 template <int OPS>
 __device__ __forceinline__ void fill_ragged(const PipeArgs<OPS>& a, int ahead, int n, uint32_t to, uint32_t bar) {
   const int lane = threadIdx.x & 31, pieces = n * OPS;
@@ -176,6 +200,8 @@ struct Pipe {
         for (int i = 0; i < n; ++i) tc::bulk_load(to + i * a.row_bytes + r.slot, src + i * r.stride, r.bytes, bar);
       }
       if (lane == 0) tc::mbar_arrive(bar);
+    } else if (ahead >= a.margin && ahead + n <= a.tokens - a.margin) {
+      fill_rounded<OPS>(a, ahead, n, to, bar);
     } else {
       fill_ragged<OPS>(a, ahead, n, to, bar);
     }

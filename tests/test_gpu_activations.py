@@ -396,6 +396,22 @@ def test_norm_grad_from_checkpoints(n, h, dtype, pad, fmt):
     p.check_backward(p.x.double(), yv, p.backward(p.x, y8))
 
 
+@pytest.mark.parametrize("n,h", [(60, 40), (60, 2056), (700, 8), (900, 1), (40, 3), (333, 17), (50, 1032)])
+def test_norm_grad_of_ragged_rows_beside_other_bytes(n, h):
+    """Rows of checkpoints that end inside 16 bytes, with e4m3 NaN behind them; rows of a byte or a few."""
+    p = Norm(n, h, post=True)
+    kept = []
+    for x in (p.x, p.y):
+        data, scales, fmt = checkpoint(x, "e4m3")
+        wide = torch.full((n, (h + 15) // 16 * 16 + 16), 0x7F, dtype=torch.uint8, device="cuda")
+        wide[:, :h] = data
+        blocks = torch.full((n, scales.shape[1] + 3), 255, dtype=torch.uint8, device="cuda")
+        blocks[:, 1:1 + scales.shape[1]] = scales
+        kept.append((wide[:, :h], blocks[:, 1:1 + scales.shape[1]], fmt))
+    p.check_backward(*(reference_checkpoint(x, "e4m3")[2] for x in (p.x, p.y)), p.backward(*kept))
+    p.check_backward(p.x.double(), p.y.double(), p.backward(p.x, p.y))
+
+
 @pytest.mark.parametrize("h", [264, 333])
 def test_norm_grad_parts(h):
     """Either gradient alone, and outputs left out."""
