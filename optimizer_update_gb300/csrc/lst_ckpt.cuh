@@ -125,6 +125,16 @@ struct Cols {
   __device__ __forceinline__ bool in(int k, int i) const { return at(k, VEC ? 0 : i) < cols; }
   __device__ __forceinline__ bool has(int k) const { return !VEC || at(k, 0) < cols; }
 
+  // f(i, column, inside the row) for the values of a part
+  template <int P, class F>
+  __device__ __forceinline__ void each(int k, int i0, F f) const {
+    uint32_t e = at(k, i0);
+#pragma unroll
+    for (int i = 0; i < 2 * P; ++i) {
+      f(i, e, e < cols);
+      e += VEC ? 1u : threads;
+    }
+  }
   // Unit k, or the half of it from its value `i0` on.
   template <int P>
   __device__ __forceinline__ void load(const float* p, int k, Part<P>& u, int i0 = 0) const {
@@ -135,8 +145,7 @@ struct Cols {
         u.v[j] = make_float2(a.x, a.y), u.v[j + 1] = make_float2(a.z, a.w);
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < 2 * P; ++i) u.at(i) = in(k, i0 + i) ? p[at(k, i0 + i)] : 0.0f;
+      each<P>(k, i0, [&](int i, uint32_t e, bool inside) { u.at(i) = inside ? p[e] : 0.0f; });
     }
   }
   template <int P>
@@ -150,8 +159,7 @@ struct Cols {
       const uint2 a = *reinterpret_cast<const uint2*>(p + at(k, i0));
       u.v[0] = unpack_bf16(a.x), u.v[1] = unpack_bf16(a.y);
     } else {
-#pragma unroll
-      for (int i = 0; i < 2 * P; ++i) u.at(i) = in(k, i0 + i) ? __bfloat162float(p[at(k, i0 + i)]) : 0.0f;
+      each<P>(k, i0, [&](int i, uint32_t e, bool inside) { u.at(i) = inside ? __bfloat162float(p[e]) : 0.0f; });
     }
   }
   template <int P>
@@ -161,9 +169,9 @@ struct Cols {
       for (int j = 0; j < P; j += 2)
         *reinterpret_cast<float4*>(p + at(k, i0 + 2 * j)) = make_float4(u.v[j].x, u.v[j].y, u.v[j + 1].x, u.v[j + 1].y);
     } else {
-#pragma unroll
-      for (int i = 0; i < 2 * P; ++i)
-        if (in(k, i0 + i)) p[at(k, i0 + i)] = u.at(i);
+      each<P>(k, i0, [&](int i, uint32_t e, bool inside) {
+        if (inside) p[e] = u.at(i);
+      });
     }
   }
   template <int P>
@@ -174,9 +182,9 @@ struct Cols {
     } else if (VEC) {
       *reinterpret_cast<uint2*>(p + at(k, i0)) = make_uint2(pack_bf16(u.v[0]), pack_bf16(u.v[1]));
     } else {
-#pragma unroll
-      for (int i = 0; i < 2 * P; ++i)
-        if (in(k, i0 + i)) p[at(k, i0 + i)] = __float2bfloat16_rn(u.at(i));
+      each<P>(k, i0, [&](int i, uint32_t e, bool inside) {
+        if (inside) p[e] = __float2bfloat16_rn(u.at(i));
+      });
     }
   }
   // Weights of either type, on any alignment.
@@ -185,8 +193,7 @@ struct Cols {
     if (VEC && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
       load(p, k, u, i0);
     } else {
-#pragma unroll
-      for (int i = 0; i < 2 * P; ++i) u.at(i) = in(k, i0 + i) ? static_cast<float>(p[at(k, i0 + i)]) : 0.0f;
+      each<P>(k, i0, [&](int i, uint32_t e, bool inside) { u.at(i) = inside ? static_cast<float>(p[e]) : 0.0f; });
     }
   }
   template <int P>
@@ -249,15 +256,15 @@ struct Cols {
 #pragma unroll
       for (int j = 0; j < P; ++j) u.v[j] = mul2(u.v[j], both(step));
     } else {
-#pragma unroll
-      for (int i = 0; i < 2 * P; ++i) {
-        u.at(i) = 0.0f;
-        if (in(k, i0 + i)) {
-          float2 a, b;
-          ckpt_decode4(data[at(k, i0 + i)], e4m3, a, b);
-          u.at(i) = a.x * ckpt_step(scales[at(k, i0 + i) / kCkptBlock]);
+      each<P>(k, i0, [&](int i, uint32_t e, bool inside) {
+        float2 a = both(0.0f), b;
+        float step = 0.0f;
+        if (inside) {
+          ckpt_decode4(data[e], e4m3, a, b);
+          step = ckpt_step(scales[e / kCkptBlock]);
         }
-      }
+        u.at(i) = a.x * step;
+      });
     }
   }
 };

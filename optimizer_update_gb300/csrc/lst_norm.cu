@@ -265,16 +265,19 @@ struct Fit {
   int k, group, groups, per_sm;
   int threads() const { return group * groups; }
 };
-Fit fit(int64_t hidden, int threads_per_sm) {
+Fit fit(int64_t hidden, int threads_per_sm, int k) {
   Fit f;
-  f.k = hidden <= 8192 ? 2 : 4;
+  f.k = k;
   f.group = static_cast<int>(ops_round_up(ops_ceil_div(hidden, 8 * f.k), 32));
   f.groups = std::max(1, 256 / f.group);
   f.per_sm = std::max(1, (f.k == 4 ? 512 : threads_per_sm) / f.threads());
   return f;
 }
-Fit norm_fit(int64_t hidden) { return fit(hidden, 768); }
-Fit grad_fit(int64_t hidden) { return fit(hidden, 512); }
+Fit norm_fit(int64_t hidden) { return fit(hidden, 768, hidden <= 8192 ? 2 : 4); }
+// Backward, rows that are not whole units take 8 columns a thread where 512 threads are enough: code
+// that goes value by value is long, and half of it with twice the warps runs faster (1023 x 4095 in
+// fp32 with a gate per token: 74 us with 16 columns a thread).
+Fit grad_fit(int64_t hidden, bool vec) { return fit(hidden, 512, !vec && hidden <= 4096 ? 1 : hidden <= 8192 ? 2 : 4); }
 int64_t ctas_of(const Fit& f, int64_t tokens) { return std::min(ops_ceil_div(tokens, f.groups), kSms * f.per_sm); }
 
 // Operands in the order of their slots in a staged row.
@@ -400,7 +403,7 @@ struct GradPlan {
 };
 GradPlan grad_plan(int64_t tokens, int64_t hidden, int64_t gate_rows) {
   GradPlan p;
-  p.ctas = ctas_of(grad_fit(hidden), tokens);
+  p.ctas = std::max(ctas_of(grad_fit(hidden, false), tokens), ctas_of(grad_fit(hidden, true), tokens));
   const int64_t each = ops_round_up(p.ctas * sum_row(hidden) * 4, 256);
   p.pre_off = 0;
   p.post_off = each;
@@ -530,14 +533,14 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   const int64_t per_gate = gate ? s.tokens / gate->rows : s.tokens;
   const bool token = per_gate == 1 && s.tokens > 1;
   const bool vec = s.hidden % 8 == 0 && on16(dh) && on16(dz) && on16(h_in) && on16(y_in) && on16(dx) && on16(dy) && (!token || on16(gate));
-  const Fit f = grad_fit(s.hidden);
+  const Fit f = grad_fit(s.hidden, vec);
   Operands<GRAD_OPS> o(f, vec && f.k == 2, s.hidden);
   GradArgs a = {};
   o.matrix(GRAD_DH, dh), o.matrix(GRAD_DZ, dz), o.matrix(GRAD_H, h_in), o.matrix(GRAD_Y, y_in);
   a.h_kept = o.kept(GRAD_H, dz ? h8 : nullptr);
   a.y_kept = o.kept(GRAD_Y, need_y ? y8 : nullptr);
   if (token) o.matrix(GRAD_GATE, gate);
-  size_t smem = o.plan(f, s.tokens, s.hidden, token ? s.tokens : per_gate, 2, f.k == 2 ? 2 : 0);
+  size_t smem = o.plan(f, s.tokens, s.hidden, token ? s.tokens : per_gate, 2, f.k <= 2 ? 2 : 0);
   if (f.k == 4) o.pipe.stages = 0, smem = kPipeHeader;  // these read rows where they are
   a.pipe = o.pipe;
   a.dx = rows_arg(dx), a.dy = rows_arg(dy);
@@ -550,7 +553,7 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   a.alpha = params->residual_scale, a.beta = params->branch_scale, a.eps = params->eps;
   const bool all = o.pipe.simple && dh && dz && dx && dy && !token && (w_post ? a.h_kept == a.y_kept : !need_y);
   const int form = !all ? 0 : 1 + a.h_kept + (w_post ? 0 : 3);
-  const NormKernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_f32(vec, f.k == 4) : norm_grad_bf16(vec, f.k == 4, form, o.pipe.groups == 1);
+  const NormKernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_f32(vec, f.k) : norm_grad_bf16(vec, f.k, form, o.pipe.groups == 1);
   LST_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared), who);
   LST_TRY_CUDA(launch_chained(kernel, dim3(static_cast<unsigned>(o.pipe.ctas)), dim3(o.threads()), smem, stream, a), who);
   if (!sums) return LST_OK;

@@ -37,9 +37,9 @@ __device__ __forceinline__ float weight_at(const Weights& w, int64_t r, int64_t 
 // f(column, value) for the columns of a unit, or of a half of it
 template <bool VEC, int P, class F>
 __device__ __forceinline__ void for_each(const Cols<VEC>& c, int k, const Part<P>& u, F f, int i0 = 0) {
-#pragma unroll
-  for (int i = 0; i < 2 * P; ++i)
-    if (c.in(k, i0 + i)) f(c.at(k, i0 + i), u.at(i));
+  c.template each<P>(k, i0, [&](int i, uint32_t e, bool inside) {
+    if (inside) f(e, u.at(i));
+  });
 }
 
 // ---- rows through shared memory ----------------------------------------------------
@@ -358,11 +358,10 @@ __device__ __forceinline__ void store_sum(void* p, int64_t at, bool f32, bool ac
 template <class Args>
 using NormKernel = void (*)(const Args);
 // The backward kernel for activations of a type (lst_norm_grad_bf16.cu, lst_norm_grad_f32.cu),
-// 16 columns a thread, or 32 for rows above 8192 (`wide`), and the word that its waits
-// set when one runs out. `form`: 0 the general kernel; 1 + KEPT that for whole units of
+// 8 k columns a thread, and the word that its waits set when one runs out. `form`: 0 the general kernel; 1 + KEPT that for whole units of
 // bf16, 4 + KEPT without a norm behind the block; `one`: its ONE.
-NormKernel<GradArgs> norm_grad_bf16(bool vec, bool wide, int form, bool one);
-NormKernel<GradArgs> norm_grad_f32(bool vec, bool wide);
+NormKernel<GradArgs> norm_grad_bf16(bool vec, int k, int form, bool one);
+NormKernel<GradArgs> norm_grad_f32(bool vec, int k);
 cudaError_t norm_grad_bf16_take_error(int* out);
 cudaError_t norm_grad_f32_take_error(int* out);
 

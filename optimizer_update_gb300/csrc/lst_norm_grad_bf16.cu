@@ -17,10 +17,10 @@ NormKernel<GradArgs> rows_kernel(int form) {
 }
 }  // namespace
 
-NormKernel<GradArgs> norm_grad_bf16(bool vec, bool wide, int form, bool one) {
-  if (vec && !wide && form) return one ? rows_kernel<true>(form) : rows_kernel<false>(form);
-  if (vec) return wide ? norm_grad_kernel<__nv_bfloat16, true, 4, false> : norm_grad_kernel<__nv_bfloat16, true, 2, true>;
-  return wide ? norm_grad_kernel<__nv_bfloat16, false, 4, false> : norm_grad_kernel<__nv_bfloat16, false, 2, true>;
+NormKernel<GradArgs> norm_grad_bf16(bool vec, int k, int form, bool one) {
+  if (vec && k == 2 && form) return one ? rows_kernel<true>(form) : rows_kernel<false>(form);
+  if (vec) return k == 4 ? norm_grad_kernel<__nv_bfloat16, true, 4, false> : norm_grad_kernel<__nv_bfloat16, true, 2, true>;
+  return k == 4 ? norm_grad_kernel<__nv_bfloat16, false, 4, false> : k == 2 ? norm_grad_kernel<__nv_bfloat16, false, 2, true> : norm_grad_kernel<__nv_bfloat16, false, 1, true>;
 }
 
 cudaError_t norm_grad_bf16_take_error(int* out) { return take_norm_error(out); }
