@@ -13,7 +13,7 @@ namespace lst {
 namespace {
 
 constexpr int64_t kSms = 152;
-constexpr int kWarpColumns = 512;  // of a row, per warp and turn
+constexpr int kWarpColumns = 1024;  // of a row, per warp and turn
 
 struct Kept {
   uint8_t* data;
@@ -33,14 +33,14 @@ __global__ void __launch_bounds__(256)
     const int64_t row = t / parts;
     const int col = static_cast<int>(t - row * parts) * kWarpColumns;
     const Cols<VEC> c = {static_cast<uint32_t>(lane), 32u, static_cast<uint32_t>(min(cols - col, kWarpColumns))};
-    Unit u[2];
+    Unit u[4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < 4; ++k) {
       u[k].fill(0.0f);
       if (c.has(k)) c.load(x + row * ld + col, k, u[k]);
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 4; ++k)
       c.save(u[k], k, out.data + row * out.stride + col, out.scales + row * out.scale_stride + col / kCkptBlock, out.e4m3);
   }
 }
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(256)
     const int col = static_cast<int>(t - row * parts) * kWarpColumns;
     const Cols<VEC> c = {static_cast<uint32_t>(lane), 32u, static_cast<uint32_t>(min(cols - col, kWarpColumns))};
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < 4; ++k) {
       if (!c.has(k)) continue;
       Unit u;
       c.restore(in.data + row * in.stride + col, in.scales + row * in.scale_stride + col / kCkptBlock, in.e4m3, k, u);

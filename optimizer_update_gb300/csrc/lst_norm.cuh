@@ -168,6 +168,7 @@ struct Pipe {
     stage = into = 0, phase = 0, ok = true;
     current = smem + kPipeHeader;
     if (STAGED) {
+      for (int i = threadIdx.x; i < 256; i += blockDim.x) words()[i] = 0.0f;
       if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
           tc::mbar_init(full + 8 * i, 2);
@@ -275,21 +276,26 @@ struct Pipe {
   __device__ __forceinline__ float* words() const { return reinterpret_cast<float*>(smem + 64); }
 };
 
-// Sum of v over the threads of a row's group, in each of them. Calls take alternate halves
-// of `words` (`turn`), so that one barrier is enough.
+// Sum of v over the threads of a row's group, in each of them: `words` holds 16 values of a
+// group, zeros behind its warps'. Calls take alternate halves of them (`turn`), so that one
+// barrier is enough; every thread adds up the warps' sums itself, which takes less time
+// than four exchanges.
 __device__ __forceinline__ float group_sum(float v, float* words, int& turn, int warps, int warp, int bar, int threads) {
-  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (warps == 1) return v;
   words += turn * 128;
   turn ^= 1;
-  if (lane == 0) words[warp] = v;
+  if ((threadIdx.x & 31) == 0) words[warp] = v;
   asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
-  v = lane < warps ? words[lane] : 0.0f;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return __shfl_sync(0xffffffffu, v, 0);
+  const float4* const q = reinterpret_cast<const float4*>(words);
+  const float4 a = q[0], b = q[1];
+  v = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+  if (warps > 8) {
+    const float4 c = q[2], d = q[3];
+    v += ((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w));
+  }
+  return v;
 }
 // The same for 8 values: lanes exchange halves, quarters and eighths of them (9 shuffles
 // instead of 40). The first `kWanted` are given back.
