@@ -85,9 +85,8 @@ struct OperandArgs {
   int64_t dy_ld, dy_out_ld;
   int32_t dy_cols;
 };
-__device__ __forceinline__ void restore16(const uint8_t* data, const uint8_t* scales, bool e4m3, int col, float2 (&v)[8]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(data + col);  // rows reach to the next 16 columns
-  const float2 step = both(ckpt_step(scales[col / kCkptBlock]));
+__device__ __forceinline__ void decode16(const uint4& q, uint32_t byte, bool e4m3, float2 (&v)[8]) {
+  const float2 step = both(ckpt_step(byte));
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
   if (e4m3) {
 #pragma unroll
@@ -99,8 +98,19 @@ __device__ __forceinline__ void restore16(const uint8_t* data, const uint8_t* sc
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = mul2(v[j], step);
 }
+// Rows reach to the next 16 columns.
+__device__ __forceinline__ void restore16(const uint8_t* data, const uint8_t* scales, bool e4m3, int col, float2 (&v)[8]) {
+  decode16(*reinterpret_cast<const uint4*>(data + col), scales[col / kCkptBlock], e4m3, v);
+}
+__device__ __forceinline__ void store16(uint16_t* p, const float2 (&v)[8], float2 rho) {
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = pack_bf16(mul2(v[j], rho));
+  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
 template <bool NORM>
-__global__ void __launch_bounds__(256, 5) operand_kernel(const __grid_constant__ OperandArgs a) {
+__global__ void __launch_bounds__(256, NORM ? 2 : 5) operand_kernel(const __grid_constant__ OperandArgs a) {
   __shared__ float words[8];
   let_next_start();
   wait_for_previous();
@@ -123,19 +133,38 @@ __global__ void __launch_bounds__(256, 5) operand_kernel(const __grid_constant__
     const bool mine = row < a.rows;  // whole warps; with 256 threads a row all of them
     const uint8_t *data = a.in.data + row * a.in.stride, *scales = a.in.scales + row * a.in.scale_stride;
     float2 rho = both(1.0f);
+    const bool once = a.cols <= 64 * a.threads;  // a thread's part of the row stays in registers
+    float2 v[NORM ? 4 : 1][8];
     if (NORM) {
       float2 sums = both(0.0f);
-      if (mine) {
-#pragma unroll 2
-        for (int col = 16 * tid; col < a.cols; col += 16 * a.threads) {
-          float2 v[8];
-          restore16(data, scales, a.in.e4m3, col, v);
+      auto add = [&](int col, float2 (&x)[8]) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (col + 2 * j >= a.cols) v[j].x = 0.0f;  // what lies behind the row may be anything
-            if (col + 2 * j + 1 >= a.cols) v[j].y = 0.0f;
-            sums = fma2(v[j], v[j], sums);
+        for (int j = 0; j < 8; ++j) {
+          if (col + 2 * j >= a.cols) x[j].x = 0.0f;  // what lies behind the row may be anything
+          if (col + 2 * j + 1 >= a.cols) x[j].y = 0.0f;
+          sums = fma2(x[j], x[j], sums);
+        }
+      };
+      if (mine && once) {
+        uint4 q[4];
+        uint8_t s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = 16 * (tid + i * a.threads);
+          if (col < a.cols) q[i] = *reinterpret_cast<const uint4*>(data + col), s[i] = scales[col / kCkptBlock];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = 16 * (tid + i * a.threads);
+          if (col < a.cols) {
+            decode16(q[i], s[i], a.in.e4m3, v[NORM ? i : 0]);
+            add(col, v[NORM ? i : 0]);
           }
+        }
+      } else if (mine) {
+        for (int col = 16 * tid; col < a.cols; col += 16 * a.threads) {
+          restore16(data, scales, a.in.e4m3, col, v[0]);
+          add(col, v[0]);
         }
       }
       float s = sums.x + sums.y;
@@ -150,18 +179,20 @@ __global__ void __launch_bounds__(256, 5) operand_kernel(const __grid_constant__
         for (int i = 0; i < 8; ++i) s += words[i];
       }
       rho = both(rsqrtf(s / static_cast<float>(a.cols) + a.eps));
+      if (mine && once) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = 16 * (tid + i * a.threads);
+          if (col < a.cols) store16(a.x + row * a.x_ld + col, v[NORM ? i : 0], rho);
+        }
+        continue;
+      }
     }
     if (!mine) continue;
 #pragma unroll 2
     for (int col = 16 * tid; col < a.cols; col += 16 * a.threads) {
-      float2 v[8];
-      restore16(data, scales, a.in.e4m3, col, v);
-      uint32_t w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = pack_bf16(mul2(v[j], rho));
-      uint4* const to = reinterpret_cast<uint4*>(a.x + row * a.x_ld + col);
-      to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      restore16(data, scales, a.in.e4m3, col, v[0]);
+      store16(a.x + row * a.x_ld + col, v[0], rho);
     }
   }
 }
@@ -265,12 +296,12 @@ bool wgrad_sizes_fit(int64_t n, int64_t o, int64_t h) {
 struct WgradPlan {
   int64_t splits, part_ld, dy_ld, x_ld, dy_off, x_off, part_off, bytes;
 };
-// Sums are split where whole tiles leave half of the 76 CTA pairs idle, into ranges of at
-// least 8 steps of 64 tokens.
+// Sums are split where tiles of 128 columns leave half of the 76 CTA pairs idle, into ranges of
+// at least 8 steps of 64 tokens.
 WgradPlan wgrad_plan(const lst_matrix* dy, const lst_checkpoint* c) {
   WgradPlan p;
   const int64_t n = dy->rows, o = dy->cols, h = c->cols;
-  const int64_t blocks = ops_ceil_div(n, 64), tiles = ops_ceil_div(o, kGemmTile) * ops_ceil_div(h, kGemmTile);
+  const int64_t blocks = ops_ceil_div(n, 64), tiles = ops_ceil_div(o, kGemmTile) * ops_ceil_div(h, kGemmTile / 2);
   p.splits = std::max<int64_t>(1, std::min<int64_t>(blocks / 8, 76 / tiles));
   p.part_ld = ops_round_up(h, 32);
   p.dy_ld = ops_round_up(o, 8);
@@ -359,7 +390,8 @@ extern "C" lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_check
   LST_TRY(check_workspace(workspace, workspace_bytes, p.bytes, who));
   char* ws = static_cast<char*>(workspace);
   const bool pack = !tile_rows(dy);
-  const int threads = n >= kSms * 8 || h <= 1024 ? 32 : 256;  // a warp a row where there are rows for all of them
+  // a warp a row where there are rows for all of them, but normed rows are to stay in registers
+  const int threads = h <= 1024 || (n >= kSms * 8 && (!norm_weight || h <= 2048)) ? 32 : 256;
   const int64_t row_blocks = std::min(ops_ceil_div(n, 256 / threads), kSms * 8);
   const OperandArgs x = {kept_arg(c), reinterpret_cast<uint16_t*>(ws + p.x_off), p.x_ld, n, static_cast<int32_t>(h),
                          threads, static_cast<int32_t>(row_blocks), eps, static_cast<const uint16_t*>(dy->data),

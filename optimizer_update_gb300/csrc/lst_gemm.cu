@@ -1126,9 +1126,9 @@ cudaError_t launch_gemm(GemmKind kind, const GemmProblem* p, int count, cudaStre
     case GEMM_F16: return launch_fit<StoreEpilogue, false>(p, count, stream, nullptr);
     case GEMM_F16_UPDATE: return launch_fit<UpdateEpilogue, false>(p, count, stream, updates);
     case GEMM_BF16: return launch_fit<GradEpilogue, true>(p, count, stream, nullptr);
-    // split sums fill the pairs with whole tiles (see lst_checkpoint.cu)
+    // split sums fill the pairs with tiles of 128 columns (see lst_checkpoint.cu)
     case GEMM_BF16_WGRAD:
-      return p->splits > 1 ? launch<WgradEpilogue, true, 256>(p, count, stream, nullptr)
+      return p->splits > 1 ? launch<WgradEpilogue, true, 128>(p, count, stream, nullptr)
                            : launch_fit<WgradEpilogue, true>(p, count, stream, nullptr);
     case GEMM_BF16_XENT: return launch<XentEpilogue, true, 256>(p, count, stream, nullptr);
     case GEMM_BF16_XENT_FEW:

@@ -443,6 +443,7 @@ struct Operands {
       pipe.stages = room < stage ? 0 : static_cast<int32_t>(std::min<int64_t>(kMaxStages, room / stage));
       if (pipe.stages > 0 || (groups == 1 && per_sm == 1)) {
         pipe.ctas = static_cast<int32_t>(std::min<int64_t>(pipe.ctas, kSms * per_sm));  // all at once
+        if (per_segment == tokens) pipe.step = pipe.ctas * groups;
         return static_cast<size_t>(kPipeHeader + pipe.stages * stage + extra);
       }
       if (groups > 1)

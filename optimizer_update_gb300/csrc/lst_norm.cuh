@@ -59,6 +59,7 @@ struct PipeArgs {
   int32_t hidden, ctas, group, groups, row_bytes, stages, pad;
   int32_t simple, row_total;  // all ranges on 16 bytes, and their bytes in a row
   int32_t margin;             // rows that span 15 bytes in every range
+  int32_t step;               // from a turn's first row to the next one's where CTAs take turns of rows (one segment only), or 0
 };
 
 // First row of CTA c: the rows divided evenly.
@@ -178,8 +179,8 @@ struct Pipe {
       }
       __syncthreads();
     }
-    begin = row = ahead = static_cast<int>(first_row(blockIdx.x, a.tokens, a.ctas));
-    end = static_cast<int>(first_row(blockIdx.x + 1, a.tokens, a.ctas));
+    begin = row = ahead = a.step ? static_cast<int>(blockIdx.x) * a.groups : static_cast<int>(first_row(blockIdx.x, a.tokens, a.ctas));
+    end = a.step ? a.tokens : static_cast<int>(first_row(blockIdx.x + 1, a.tokens, a.ctas));
     segment = ahead_segment = segment_end(begin);
   }
   __device__ __forceinline__ int segment_end(int r) const {
@@ -206,7 +207,7 @@ struct Pipe {
     } else {
       fill_ragged<OPS>(a, ahead, n, to, bar);
     }
-    ahead += n;
+    ahead = static_cast<int>(min(static_cast<int64_t>(ahead) + (a.step ? a.step : n), int64_t(INT32_MAX)));
     if (ahead == ahead_segment && ahead < end) ahead_segment = segment_end(ahead);
     if (++into == a.stages) into = 0;
   }
@@ -257,7 +258,7 @@ struct Pipe {
       current += stage_bytes;
       if (++stage == a.stages) stage = 0, phase ^= 1, current = smem + kPipeHeader;
     }
-    row += n;
+    row = static_cast<int>(min(static_cast<int64_t>(row) + (a.step ? a.step : n), int64_t(INT32_MAX)));
     return row < segment;
   }
   // The next segment; false behind the last.

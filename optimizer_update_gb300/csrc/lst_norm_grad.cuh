@@ -32,8 +32,8 @@ __device__ __forceinline__ void flush_sums(const GradArgs& a, const P& p, const 
   const int64_t cta = blockIdx.x;
   const bool last = p.row >= p.end;
   const int64_t gate_row = (p.segment - 1) / a.per_gate;
-  const bool whole = gate_row * a.per_gate >= p.begin && (gate_row + 1) * a.per_gate <= p.end;
-  float* const gate_sums = a.part_gate + (2 * cta + (gate_row == p.begin / a.per_gate ? 0 : 1)) * ld;
+  const bool whole = a.pipe.step ? a.pipe.ctas == 1 : gate_row * a.per_gate >= p.begin && (gate_row + 1) * a.per_gate <= p.end;
+  float* const gate_sums = a.part_gate + (2 * cta + (a.pipe.step || gate_row == p.begin / a.per_gate ? 0 : 1)) * ld;
   float *const post = a.part_post + cta * ld, *const pre = a.part_pre + cta * ld;
   const bool gated = !token && a.gate.p, gates = !token && has_y && a.dgate, posts = has_y && a.part_post, pres = last && a.part_pre;
   if (ONE || a.pipe.groups == 1) {
