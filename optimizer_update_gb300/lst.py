@@ -162,7 +162,8 @@ def checkpoint(data, scales, fmt="i8") -> lst_checkpoint:
     """An lst_checkpoint over two torch tensors of two dimensions and one byte an
     element: the values (rows on 16 bytes; a column count that is no multiple of
     16 is a view of wider rows) and the scales, one per 32 columns. fmt: "i8" or
-    "e4m3". checkpoint_buffers() makes such tensors."""
+    "e4m3". checkpoint_buffers() makes such tensors. Like matrix(), this keeps no
+    reference to them: they have to outlive the calls that use it."""
     if data.dim() != 2 or scales.dim() != 2 or data.element_size() != 1 or scales.element_size() != 1:
         raise ValueError("values and scales have two dimensions and one byte an element")
     (rows, cols), (stride, inner) = data.shape, data.stride()

@@ -728,3 +728,48 @@ def test_results_leave_the_space_between_rows_alone(h, pad, shift):
         keep[shift:].view(t.shape[0], h + pad)[:, :h] = False
         assert (whole[keep] == 7.0).all()
         assert torch.isfinite(t).all() and t.any()
+
+
+def example():
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    try:
+        import train_checkpointed_layers
+    finally:
+        sys.path.pop(0)
+    return train_checkpointed_layers
+
+
+def test_example_runs():
+    means = example().train(3, log=None)
+    assert len(means) == 3 and all(m == m and 0.0 < m < 100.0 for m in means)
+
+
+def test_example_gradients():
+    """Against the same model in 64 bits by autograd. Expected: integers keep values to 0.7 % (RMS), which enters a
+    gradient twice, 1 %; bf16 roundings of 0.1 to 0.2 % each, some twenty in a row, 1 %; one in some 700 of the MLP's
+    inner values lies so near zero that the rounded sum has the other sign, which replaces as many entries of its
+    gradient, sqrt(1 / 700) = 4 %. Sum 6 %, bound 10 %."""
+    e = example()
+    model = e.Model(7)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    for name, w in model.w.items():  # norms and gates other than one
+        if w.shape[0] == 1:
+            w.mul_(1 + 0.2 * torch.randn(w.shape, generator=g, device="cuda"))
+    tokens, targets = (torch.randint(0, e.VOCAB, (e.TOKENS,), generator=g, device="cuda") for _ in range(2))
+    mean = model.gradients(tokens, targets)
+    lst.lst_operator_status()
+    w = {k: v.double().requires_grad_() for k, v in model.w.items()}
+
+    def norm(x, weight):
+        return x / (x.square().mean(1, keepdim=True) + e.EPS).sqrt() * weight
+
+    x = w["embed_tokens"][tokens]
+    for i in range(e.LAYERS):
+        out = torch.relu(norm(x, w[f"norm_{i}"]) @ w[f"up_{i}"].T) @ w[f"down_{i}"].T
+        x = x + e.BRANCH * w[f"gate_{i}"] * norm(out, w[f"post_norm_{i}"])
+    loss = torch.nn.functional.cross_entropy(norm(x, w["final_norm"]) @ w["lm_head"].T, targets)
+    loss.backward()
+    assert abs(float(mean) - loss.item()) <= 0.01 * loss.item()
+    for name, v in w.items():
+        off = float((model.g[name].double() - v.grad).norm() / v.grad.norm())
+        assert off <= 0.1, f"{name}: {off:.3f}"
