@@ -84,6 +84,7 @@ struct OperandArgs {
   uint16_t* dy_out;
   int64_t dy_ld, dy_out_ld;
   int32_t dy_cols;
+  int32_t parts;  // 2: X as a sum of two bf16 parts, the second `rows` rows behind the first, and dy twice
 };
 __device__ __forceinline__ void decode16(const uint4& q, uint32_t byte, bool e4m3, float2 (&v)[8]) {
   const float2 step = both(ckpt_step(byte));
@@ -102,12 +103,21 @@ __device__ __forceinline__ void decode16(const uint4& q, uint32_t byte, bool e4m
 __device__ __forceinline__ void restore16(const uint8_t* data, const uint8_t* scales, bool e4m3, int col, float2 (&v)[8]) {
   decode16(*reinterpret_cast<const uint4*>(data + col), scales[col / kCkptBlock], e4m3, v);
 }
-__device__ __forceinline__ void store16(uint16_t* p, const float2 (&v)[8], float2 rho) {
-  uint32_t w[8];
+// v rho as bf16; with `rest`, what that leaves as bf16 there.
+__device__ __forceinline__ void store16(uint16_t* p, const float2 (&v)[8], float2 rho, uint16_t* rest) {
+  uint32_t w[8], l[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = pack_bf16(mul2(v[j], rho));
+  for (int j = 0; j < 8; ++j) {
+    const float2 x = mul2(v[j], rho);
+    w[j] = pack_bf16(x);
+    const float2 hi = unpack_bf16(w[j]);
+    l[j] = pack_bf16(make_float2(x.x - hi.x, x.y - hi.y));
+  }
   reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
   reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (!rest) return;
+  reinterpret_cast<uint4*>(rest)[0] = make_uint4(l[0], l[1], l[2], l[3]);
+  reinterpret_cast<uint4*>(rest)[1] = make_uint4(l[4], l[5], l[6], l[7]);
 }
 template <bool NORM>
 __global__ void __launch_bounds__(256, NORM ? 2 : 5) operand_kernel(const __grid_constant__ OperandArgs a) {
@@ -122,8 +132,9 @@ __global__ void __launch_bounds__(256, NORM ? 2 : 5) operand_kernel(const __grid
         uint32_t v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 8 * u + i < a.dy_cols ? p[i] : 0u;
-        *reinterpret_cast<uint4*>(a.dy_out + r * a.dy_out_ld + 8 * u) =
-            make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        for (int part = 0; part < a.parts; ++part)
+          *reinterpret_cast<uint4*>(a.dy_out + (r + part * a.rows) * a.dy_out_ld + 8 * u) =
+              make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
       }
     return;
   }
@@ -132,6 +143,8 @@ __global__ void __launch_bounds__(256, NORM ? 2 : 5) operand_kernel(const __grid
     const int64_t row = first + threadIdx.x / a.threads;
     const bool mine = row < a.rows;  // whole warps; with 256 threads a row all of them
     const uint8_t *data = a.in.data + row * a.in.stride, *scales = a.in.scales + row * a.in.scale_stride;
+    uint16_t* const x = a.x + row * a.x_ld;
+    uint16_t* const rest = NORM && a.parts > 1 ? x + a.rows * a.x_ld : nullptr;
     float2 rho = both(1.0f);
     const bool once = a.cols <= 64 * a.threads;  // a thread's part of the row stays in registers
     float2 v[NORM ? 4 : 1][8];
@@ -183,7 +196,7 @@ __global__ void __launch_bounds__(256, NORM ? 2 : 5) operand_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int col = 16 * (tid + i * a.threads);
-          if (col < a.cols) store16(a.x + row * a.x_ld + col, v[NORM ? i : 0], rho);
+          if (col < a.cols) store16(x + col, v[NORM ? i : 0], rho, rest ? rest + col : nullptr);
         }
         continue;
       }
@@ -192,7 +205,7 @@ __global__ void __launch_bounds__(256, NORM ? 2 : 5) operand_kernel(const __grid
 #pragma unroll 2
     for (int col = 16 * tid; col < a.cols; col += 16 * a.threads) {
       restore16(data, scales, a.in.e4m3, col, v[0]);
-      store16(a.x + row * a.x_ld + col, v[0], rho);
+      store16(x + col, v[0], rho, rest ? rest + col : nullptr);
     }
   }
 }
@@ -293,16 +306,26 @@ bool wgrad_sizes_fit(int64_t n, int64_t o, int64_t h) {
          o <= most / h;
 }
 
+// Normed rows of up to so many tokens go into the product as sums of two bf16 parts, with dy
+// twice: one part alone leaves 2^-9 (RMS 0.0016) of each row, as much again as the result's
+// own rounding. Averages over more tokens keep both at that; twice the products would be
+// most of their time.
+constexpr int64_t kTwoParts = 512;
+
 struct WgradPlan {
-  int64_t splits, part_ld, dy_ld, x_ld, dy_off, x_off, part_off, bytes;
+  int64_t tokens, splits, part_ld, dy_ld, x_ld, dy_off, x_off, part_off, bytes;  // tokens: rows of the product's operands
 };
 // Sums are split where tiles of 128 columns leave half of the 76 CTA pairs idle, into ranges of
-// at least 8 steps of 64 tokens.
-WgradPlan wgrad_plan(const lst_matrix* dy, const lst_checkpoint* c) {
+// at least 8 steps of 64 tokens. Sizes of memory are those of any smaller count, too.
+int64_t wgrad_splits(int64_t tokens, int64_t o, int64_t h) {
+  const int64_t tiles = ops_ceil_div(o, kGemmTile) * ops_ceil_div(h, kGemmTile / 2);
+  return std::max<int64_t>(1, std::min<int64_t>(ops_ceil_div(tokens, 64) / 8, 76 / tiles));
+}
+WgradPlan wgrad_plan(const lst_matrix* dy, const lst_checkpoint* c, bool norm) {
   WgradPlan p;
   const int64_t n = dy->rows, o = dy->cols, h = c->cols;
-  const int64_t blocks = ops_ceil_div(n, 64), tiles = ops_ceil_div(o, kGemmTile) * ops_ceil_div(h, kGemmTile / 2);
-  p.splits = std::max<int64_t>(1, std::min<int64_t>(blocks / 8, 76 / tiles));
+  p.tokens = norm && n <= kTwoParts ? 2 * n : n;
+  p.splits = wgrad_splits(p.tokens, o, h);
   p.part_ld = ops_round_up(h, 32);
   p.dy_ld = ops_round_up(o, 8);
   p.x_ld = ops_round_up(h, 16);
@@ -312,9 +335,10 @@ WgradPlan wgrad_plan(const lst_matrix* dy, const lst_checkpoint* c) {
     at += ops_round_up(size, 256);
     return off;
   };
-  p.dy_off = take(tile_rows(dy) ? 0 : n * p.dy_ld * 2);
-  p.x_off = take(n * p.x_ld * 2);
-  p.part_off = take(p.splits > 1 ? p.splits * o * p.part_ld * 4 : 0);
+  const int64_t twice = 2 * std::min(n, kTwoParts), most = std::max(n, twice), splits = wgrad_splits(most, o, h);
+  p.dy_off = take((tile_rows(dy) ? twice : most) * p.dy_ld * 2);
+  p.x_off = take(most * p.x_ld * 2);
+  p.part_off = take(splits > 1 ? splits * o * p.part_ld * 4 : 0);
   p.bytes = at;
   return p;
 }
@@ -353,7 +377,7 @@ extern "C" int64_t lst_checkpoint_wgrad_workspace_bytes(const lst_matrix* dy, co
   if (!dy || !c || !dw || dy->rows != c->rows || dw->rows != dy->cols || dw->cols != c->cols ||
       !wgrad_sizes_fit(dy->rows, dy->cols, c->cols))
     return 0;
-  return wgrad_plan(dy, c).bytes;
+  return wgrad_plan(dy, c, false).bytes;
 }
 
 extern "C" lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_checkpoint* c, const lst_matrix* norm_weight,
@@ -386,26 +410,26 @@ extern "C" lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_check
   const int64_t n = dy->rows, o = dy->cols, h = c->cols;
   if (!wgrad_sizes_fit(n, o, h))
     return fail(LST_ERR_INVALID_ARG, "%s: more than 2^24 tokens, or an operand of more than 2^40 elements", who);
-  const WgradPlan p = wgrad_plan(dy, c);
+  const WgradPlan p = wgrad_plan(dy, c, norm_weight != nullptr);
   LST_TRY(check_workspace(workspace, workspace_bytes, p.bytes, who));
   char* ws = static_cast<char*>(workspace);
-  const bool pack = !tile_rows(dy);
+  const bool two = p.tokens > n, pack = two || !tile_rows(dy);
   // a warp a row where there are rows for all of them, but normed rows are to stay in registers
   const int threads = h <= 1024 || (n >= kSms * 8 && (!norm_weight || h <= 2048)) ? 32 : 256;
   const int64_t row_blocks = std::min(ops_ceil_div(n, 256 / threads), kSms * 8);
   const OperandArgs x = {kept_arg(c), reinterpret_cast<uint16_t*>(ws + p.x_off), p.x_ld, n, static_cast<int32_t>(h),
                          threads, static_cast<int32_t>(row_blocks), eps, static_cast<const uint16_t*>(dy->data),
-                         reinterpret_cast<uint16_t*>(ws + p.dy_off), dy->stride, p.dy_ld, static_cast<int32_t>(o)};
+                         reinterpret_cast<uint16_t*>(ws + p.dy_off), dy->stride, p.dy_ld, static_cast<int32_t>(o), two ? 2 : 1};
   LST_TRY_CUDA(launch_chained(norm_weight ? operand_kernel<true> : operand_kernel<false>, dim3(static_cast<unsigned>(row_blocks + (pack ? std::min(n, kSms * 8) : 0))), dim3(256), 0, stream, x), who);
   GemmProblem g;
   if (pack)
-    g.a = {x.dy_out, o, n, p.dy_ld, true};
+    g.a = {x.dy_out, o, p.tokens, p.dy_ld, true};
   else
     g.a = {dy->data, o, n, dy->stride, true};
-  g.b = {x.x, h, n, p.x_ld, true};
+  g.b = {x.x, h, p.tokens, p.x_ld, true};
   g.m = o;
   g.n = h;
-  g.k = n;
+  g.k = p.tokens;
   g.splits = static_cast<int>(p.splits);
   const bool weight_f32 = norm_weight && norm_weight->dtype == LST_F32;
   const int vec = on16(dw) && dw->stride * dtype_bytes(dw->dtype) % 16 == 0 ? 16 : 2;
@@ -413,7 +437,7 @@ extern "C" lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_check
   if (p.splits > 1) g.wgrad.partial = {reinterpret_cast<float*>(ws + p.part_off), p.part_ld, o * p.part_ld, 0};
   LST_TRY_CUDA(launch_gemm(GEMM_BF16_WGRAD, &g, 1, stream), who);
   if (p.splits == 1) return LST_OK;
-  const int64_t blocks = ops_ceil_div(n, 64), splits = ops_ceil_div(blocks, ops_ceil_div(blocks, p.splits));
+  const int64_t blocks = ops_ceil_div(p.tokens, 64), splits = ops_ceil_div(blocks, ops_ceil_div(blocks, p.splits));
   const FinishArgs f = {g.wgrad.partial.out, p.part_ld, o * p.part_ld, g.wgrad.weight, dw->data, dw->stride, static_cast<int32_t>(splits),
                         weight_f32, dw->dtype == LST_F32, accumulate != 0, static_cast<int32_t>(h), o, vec};
   const int64_t quads = ops_ceil_div(h, 4);

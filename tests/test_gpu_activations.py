@@ -567,6 +567,27 @@ def test_wgrad_forms(kw, n, o, h):
     check_wgrad(n, o, h, **kw)
 
 
+@pytest.mark.parametrize("n,o,h", [(1, 40, 300), (3, 256, 2048), (512, 300, 264), (513, 300, 264), (511, 64, 17000)])
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+def test_wgrad_normed(n, o, h, fmt):
+    check_wgrad(n, o, h, fmt, norm="f32")
+    check_wgrad(n, o, h, fmt, norm="bf16", out="f32", pad=3)
+
+
+def test_wgrad_normed_of_few_tokens_is_near():
+    """Two bf16 parts of a value leave 2^-16 of it (half a step of the rest): with it the statistic's error and the sums'."""
+    n, o, h = 5, 64, 520
+    g = gen(3)
+    dy, x = randn(g, n, o, dtype="bf16"), randn(g, n, h, dtype="bf16")
+    weight = 1 + randn(g, 1, h, std=0.3)
+    c = checkpoint(x, "i8")
+    dw = wgrad(dy, c, weight, torch.empty(o, h, device="cuda"), False)
+    v = reference_checkpoint(x, "i8")[2]
+    v = v * (v.square().mean(1, keepdim=True) + EPS).rsqrt()
+    size = (dy.double().abs().T @ v.abs()) * weight.double().abs()
+    within(dw, (dy.double().T @ v) * weight.double(), (2.0 ** -16 + ROW + 2 * (2 * n + 64) * U32) * size, "dw")
+
+
 @pytest.mark.parametrize("n,o,h,norm", [(200, 4096, 5120, None), (1100, 5000, 4000, "bf16"), (70, 20000, 1300, None)])
 def test_wgrad_more_tiles_than_pairs(n, o, h, norm):
     check_wgrad(n, o, h, norm=norm)
@@ -578,9 +599,11 @@ def test_wgrad_workspace_of_more_tokens():
     c = checkpoint(x, "i8")
     dw = torch.empty(256, 520, dtype=torch.bfloat16, device="cuda")
     ws = scratch(lst.lst_checkpoint_wgrad_workspace_bytes(mat(dy), lst.checkpoint(*c), mat(dw)))
-    for n in (1, 64, 100, 511, 513, 1024, 2049, 4999):
-        a = wgrad(dy[:n], (c[0][:n], c[1][:n], "i8"), None, torch.empty_like(dw), False, ws)
-        assert torch.equal(a, wgrad(dy[:n], (c[0][:n], c[1][:n], "i8"), None, dw, False))
+    weight = torch.ones(1, 520, device="cuda")
+    for n in (1, 64, 100, 511, 512, 513, 1024, 2049, 4999):
+        for w in (None, weight):
+            a = wgrad(dy[:n], (c[0][:n], c[1][:n], "i8"), w, torch.empty_like(dw), False, ws)
+            assert torch.equal(a, wgrad(dy[:n], (c[0][:n], c[1][:n], "i8"), w, dw, False))
 
 
 def test_wgrad_of_no_tokens():
