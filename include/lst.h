@@ -494,8 +494,10 @@ LST_API lst_status lst_store_step(lst_store* store, void* const* staging, void* 
 /* ------------------------------------------------------------------------
  * Training operators around the packed blocks: what a step computes before
  * the update (the embedding block's lookup and gradient, the LM-head block's
- * loss and gradients, written in the blocks' own formats) and the Muon rule
- * as another update of the matrices in a block.
+ * loss and gradients, written in the blocks' own formats), what stands between
+ * the layers (norms with gate and residual scales, 8-bit checkpoints and the
+ * weight gradients from them) and the Muon rule as another update of the
+ * matrices in a block.
  *
  * All calls are asynchronous on cuda_stream (null = the legacy default
  * stream), allocate nothing and keep nothing from one call to the next.
@@ -738,7 +740,7 @@ LST_API lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_checkpoi
                                         float eps, const lst_matrix* dw, int32_t accumulate, void* workspace,
                                         int64_t workspace_bytes, void* cuda_stream);
 
-/* LST_ERR_TIMEOUT if a wait inside one of the matrix kernels of these
+/* LST_ERR_TIMEOUT if a wait inside one of the matrix or norm kernels of these
    operators ran out (2 s) since the last call on the current device: the
    results of the calls since then are not valid. LST_OK otherwise.
    Synchronises the device. */

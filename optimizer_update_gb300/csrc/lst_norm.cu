@@ -14,8 +14,10 @@
 // takes consecutive rows and keeps the column sums in registers; they go to the
 // workspace once per CTA (A once per gate row) and are added up in order by a second launch.
 //
-// Both are bound by memory: 8 bytes an element forward, 12 backward in bf16 (10 with
-// checkpoints) against some 10 and 30 instructions.
+// Floors are memory's: 8 bytes an element forward, 12 backward in bf16 (10 with checkpoints).
+// Forward runs at 5.9 TB/s (16384 x 4096 with an 8-bit copy, 114 us). Backward runs at 4.9 TB/s
+// (16381 x 8192 from checkpoints, 273 us and 10 for the sums): some 45 instructions an
+// element and 16 warps an SM, as many as 128 registers and the rows in flight leave.
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
@@ -196,125 +198,6 @@ __global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant
   p.finish(&g_norm_error);
 }
 
-// The same for bf16 rows of up to 8192 columns with everything on 16 bytes, x, y, h and z there,
-// no gate per token and no y8. CKPT: h8 0 not there, 1 integers, 2 e4m3; POST: a norm behind
-// the block; ONE: a row at a time (rows above 2048), whose addresses are then the same in
-// all threads. (The general kernel asks for each operand in every row: 16384 x 4096 with h8
-// 124 us.)
-template <int CKPT, bool POST, bool ONE>
-__global__ void __maxnreg__(80) norm_rows_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int K = 2;
-  using T = __nv_bfloat16;
-  extern __shared__ __align__(16) uint8_t smem[];
-  let_next_start();
-  Pipe<NORM_OPS, true, false> p(a.pipe, smem);
-  wait_for_previous();
-  p.start(a.pipe.pad);
-  const int group = ONE ? 0 : threadIdx.x / a.pipe.group, tid = threadIdx.x - group * a.pipe.group, warp = tid >> 5, warps = a.pipe.group >> 5;
-  const Cols<true> c = {static_cast<uint32_t>(tid), static_cast<uint32_t>(a.pipe.group), static_cast<uint32_t>(a.pipe.hidden)};
-  const float inverse = 1.0f / static_cast<float>(a.pipe.hidden);
-  float* const words = p.words() + group * 16;
-  const int columns = 8 * K * a.pipe.group;
-  float* const held_pre = reinterpret_cast<float*>(smem + kPipeHeader + a.pipe.stages * p.stage_bytes);
-  float* const held_gw = held_pre + columns;
-  bool there[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k) there[k] = c.has(k);
-  int turn = 0;
-  auto sum = [&](float2 s) { return group_sum(s.x + s.y, words, turn, warps, warp, 1 + group, a.pipe.group); };
-  do {
-    // each thread the columns that it reads itself, or one group for all
-    if (!ONE) asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
-    if (ONE || group == 0) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        Unit u, g;
-        u.fill(0.0f);
-        if (there[k]) c.load_any(a.w_pre.p, a.w_pre.f32, k, u);
-        c.store(held_pre, k, u);
-        u.fill(there[k] ? a.beta : 0.0f);
-        if (POST && there[k]) {
-          c.load_any(a.w_post.p, a.w_post.f32, k, g);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], g.v[j]);
-        }
-        if (a.gate.p && there[k]) {
-          c.load_any(row_of(a.gate, p.row / a.pipe.per_segment), a.gate.f32, k, g);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) u.v[j] = mul2(u.v[j], g.v[j]);
-        }
-        c.store(held_gw, k, u);
-      }
-    }
-    if (!ONE) asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
-    int rows;
-    do {
-      rows = ONE ? 1 : p.rows();
-      const bool mine = ONE || group < rows;
-      const int64_t row = p.row + group;
-      Unit h[K];
-      float2 s = both(0.0f);
-      p.wait();
-      if (mine) {
-        const uint8_t* const staged = p.staged(group);
-        const T *const x = reinterpret_cast<const T*>(staged + a.pipe.in[NORM_X].slot), *const y = reinterpret_cast<const T*>(staged + a.pipe.in[NORM_Y].slot);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          c.load(y, k, h[k]);
-          if (POST) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s = fma2(h[k].v[j], h[k].v[j], s);
-          }
-        }
-        const float2 tau = both(POST ? rsqrtf(sum(s) * inverse + a.eps) : 1.0f), alpha = both(a.alpha);
-        s = both(0.0f);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          Unit u, g;
-          c.load(x, k, u);
-          c.load(held_gw, k, g);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            h[k].v[j] = fma2(u.v[j], alpha, mul2(POST ? mul2(h[k].v[j], tau) : h[k].v[j], g.v[j]));
-            s = fma2(h[k].v[j], h[k].v[j], s);
-          }
-        }
-      }
-      p.release();
-      if (a.pipe.stages > 1) p.refill(false);
-      if (mine) {
-        T* const to = row_of<T>(a.h, row);
-        uint8_t* const codes = a.h8.data + row * a.h8.stride;
-        uint8_t* const scales = a.h8.scales + row * a.h8.scale_stride;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          uint32_t w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = pack_bf16(h[k].v[j]);
-          if (there[k]) *reinterpret_cast<uint4*>(to + c.at(k, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
-          if (CKPT) {
-            Unit r;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r.v[j] = unpack_bf16(w[j]);
-            c.save(r, k, codes, scales, CKPT == 2);
-          }
-        }
-        const float2 rho = both(rsqrtf(sum(s) * inverse + a.eps));
-        T* const out = row_of<T>(a.z, row);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          Unit u;
-          c.load(held_pre, k, u);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) h[k].v[j] = mul2(mul2(h[k].v[j], rho), u.v[j]);
-          if (there[k]) c.store(out, k, h[k]);
-        }
-      }
-    } while (p.next(rows));
-  } while (p.next_segment());
-  p.finish(&g_norm_error);
-}
-
 // Adds up the CTAs' sums, 128 columns a CTA: blockIdx.y 0: dw_pre, 1: dw_post; from 2 on the
 // gate rows that more than one CTA worked on, by their number or (where there are more
 // gate rows than CTAs) as the last gate row of CTA blockIdx.y - 2.
@@ -378,8 +261,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const __grid
 }
 
 // ---- host ------------------------------------------------------------------------
-// 16 columns a thread (32 of rows above 8192), and short rows several at a time, so that a CTA has about 256 threads, 512 where a row needs them. An SM holds 512 threads of
-// the backward kernel and 768 of the forward one, as many as their registers allow.
+// 16 columns a thread (32 of rows above 8192), and short rows several at a time, so that a CTA
+// has about 256 threads, 512 where a row needs them. An SM holds 512 threads of the backward
+// kernel and 768 of the forward one, as many as their registers allow (forward with 512: 157 us
+// for 16384 x 4096 with a checkpoint and its restore, with 1024 of 64 registers 184, so 155).
 struct Fit {
   int k, group, groups, per_sm;
   int threads() const { return group * groups; }
@@ -395,7 +280,7 @@ Fit fit(int64_t hidden, int threads_per_sm, int k) {
 Fit norm_fit(int64_t hidden) { return fit(hidden, 768, hidden <= 8192 ? 2 : 4); }
 // Backward, rows that are not whole units take 8 columns a thread where 512 threads are enough: code
 // that goes value by value is long, and half of it with twice the warps runs faster (1023 x 4095 in
-// fp32 with a gate per token: 74 us with 16 columns a thread).
+// fp32 with a gate per token: 74 us with 16 columns a thread, 49 with 8).
 Fit grad_fit(int64_t hidden, bool vec) { return fit(hidden, 512, !vec && hidden <= 4096 ? 1 : hidden <= 8192 ? 2 : 4); }
 int64_t ctas_of(const Fit& f, int64_t tokens) { return std::min(ops_ceil_div(tokens, f.groups), kSms * f.per_sm); }
 
@@ -510,14 +395,6 @@ struct Shape {
   }
 };
 
-template <int CKPT>
-NormKernel<NormArgs> norm_rows_of(bool post, bool one) {
-  if (post) return one ? norm_rows_kernel<CKPT, true, true> : norm_rows_kernel<CKPT, true, false>;
-  return one ? norm_rows_kernel<CKPT, false, true> : norm_rows_kernel<CKPT, false, false>;
-}
-NormKernel<NormArgs> norm_rows_of(int ckpt, bool post, bool one) {
-  return ckpt == 0 ? norm_rows_of<0>(post, one) : ckpt == 1 ? norm_rows_of<1>(post, one) : norm_rows_of<2>(post, one);
-}
 template <class T, bool VEC>
 NormKernel<NormArgs> norm_of(int k) {
   return k == 2 ? norm_kernel<T, VEC, 2> : norm_kernel<T, VEC, 4>;
@@ -597,11 +474,7 @@ extern "C" lst_status lst_residual_norm(const lst_matrix* x, const lst_matrix* y
   const size_t smem = o.plan(f, s.tokens, s.hidden, gate && !token ? s.tokens / gate->rows : s.tokens, 0, f.k == 2 ? 2 : 0);
   const NormArgs a = {o.pipe, rows_arg(h), rows_arg(z), weights_arg(gate), weights_arg(w_post), weights_arg(w_pre), kept_arg(h8),
                       kept_arg(y8), params->residual_scale, params->branch_scale, params->eps};
-  // h8 there or not, in its format; without the rest, the general kernel
-  const bool all = s.dtype == LST_BF16 && vec && f.k == 2 && o.pipe.simple && y && h && z && !token && !y8;
-  const int ckpt = !h8 ? 0 : h8->format == LST_CHECKPOINT_E4M3 ? 2 : 1;
-  const NormKernel<NormArgs> kernel = all ? norm_rows_of(ckpt, w_post != nullptr, o.pipe.groups == 1)
-                                  : s.dtype == LST_F32 ? (vec ? norm_of<float, true>(f.k) : norm_of<float, false>(f.k))
+  const NormKernel<NormArgs> kernel = s.dtype == LST_F32 ? (vec ? norm_of<float, true>(f.k) : norm_of<float, false>(f.k))
                                   : vec              ? norm_of<__nv_bfloat16, true>(f.k)
                                                      : norm_of<__nv_bfloat16, false>(f.k);
   LST_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared), who);
@@ -685,7 +558,7 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   a.alpha = params->residual_scale, a.beta = params->branch_scale, a.eps = params->eps;
   const bool all = o.pipe.simple && dh && dz && dx && dy && !token && (w_post ? a.h_kept == a.y_kept : !need_y);
   const int form = !all ? 0 : 1 + a.h_kept + (w_post ? 0 : 3);
-  const NormKernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_f32(vec, f.k) : norm_grad_bf16(vec, f.k, form, o.pipe.groups == 1);
+  const NormKernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_f32(vec, f.k, form, o.pipe.groups == 1) : norm_grad_bf16(vec, f.k, form, o.pipe.groups == 1);
   LST_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared), who);
   LST_TRY_CUDA(launch_chained(kernel, dim3(static_cast<unsigned>(o.pipe.ctas)), dim3(o.threads()), smem, stream, a), who);
   if (!sums) return LST_OK;

@@ -317,16 +317,23 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
   p.finish(&g_norm_grad_error);
 }
 
-// The same for bf16 rows of up to 8192 columns with everything on 16 bytes (scales too), all of dh, dz,
+// Four values as they lie, and two of them as fp32.
+__device__ __forceinline__ uint2 load_raw(const __nv_bfloat16* p) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ float4 load_raw(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float2 pair(const uint2& r, int i) { return unpack_bf16(i ? r.y : r.x); }
+__device__ __forceinline__ float2 pair(const float4& r, int i) { return i ? make_float2(r.z, r.w) : make_float2(r.x, r.y); }
+
+// The same for rows of up to 8192 columns with everything on 16 bytes (scales too), all of dh, dz,
 // dx and dy, no gate per token, and h and y alike: KEPT 0 matrices, 1 integers, 2 e4m3. POST:
 // a norm behind the block; without one, y is not read. h and y stay in registers from the
 // row's sums to its results, dh and dz are read from shared memory again: held too, they
-// would spill, and with all of the shared memory in use local memory lies in L2.
+// would spill, and with all of the shared memory in use local memory lies in L2. (The
+// general kernel, which asks in every unit what there is: 633 us for 16381 x 8192 from
+// checkpoints, this one 283.)
 // ONE: a row at a time (rows above 2048), whose addresses are then the same in all threads.
-template <int KEPT, bool POST, bool ONE>
+template <class T, int KEPT, bool POST, bool ONE>
 __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ GradArgs a) {
   constexpr int K = 2;
-  using T = __nv_bfloat16;
   extern __shared__ __align__(16) uint8_t smem[];
   let_next_start();
   Pipe<GRAD_OPS, true, false> p(a.pipe, smem);
@@ -397,19 +404,19 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
         for (int i = 0; i < 2 * K; ++i) {
           const int k = i >> 1, j0 = 2 * (i & 1), u = (tid + k * c.threads) * 8 + 2 * j0;
           asm volatile("" ::: "memory");
-          const uint2 z = *reinterpret_cast<const uint2*>(dz_row + 2 * u);
+          const auto z = load_raw(reinterpret_cast<const T*>(dz_row + sizeof(T) * u));
           const float4 w = *reinterpret_cast<const float4*>(held_pre + u);
-          const float2 m0 = mul2(unpack_bf16(z.x), make_float2(w.x, w.y)), m1 = mul2(unpack_bf16(z.y), make_float2(w.z, w.w));
+          const float2 m0 = mul2(pair(z, 0), make_float2(w.x, w.y)), m1 = mul2(pair(z, 1), make_float2(w.z, w.w));
           const float2 h0 = h[k].v[j0], h1 = h[k].v[j0 + 1];
           t[0] = fma2(h0, h0, t[0]), t[1] = fma2(m0, h0, t[1]);
           t[0] = fma2(h1, h1, t[0]), t[1] = fma2(m1, h1, t[1]);
           if (POST) {
-            const uint2 d = *reinterpret_cast<const uint2*>(dh_row + 2 * u);
+            const auto d = load_raw(reinterpret_cast<const T*>(dh_row + sizeof(T) * u));
             const float4 g = *reinterpret_cast<const float4*>(held_gw + u);
             const float2 y0 = y[k].v[j0], y1 = y[k].v[j0 + 1];
             const float2 q0 = mul2(make_float2(g.x, g.y), y0), q1 = mul2(make_float2(g.z, g.w), y1);
-            t[2] = fma2(y0, y0, t[2]), t[3] = fma2(unpack_bf16(d.x), q0, t[3]), t[4] = fma2(m0, q0, t[4]), t[5] = fma2(h0, q0, t[5]);
-            t[2] = fma2(y1, y1, t[2]), t[3] = fma2(unpack_bf16(d.y), q1, t[3]), t[4] = fma2(m1, q1, t[4]), t[5] = fma2(h1, q1, t[5]);
+            t[2] = fma2(y0, y0, t[2]), t[3] = fma2(pair(d, 0), q0, t[3]), t[4] = fma2(m0, q0, t[4]), t[5] = fma2(h0, q0, t[5]);
+            t[2] = fma2(y1, y1, t[2]), t[3] = fma2(pair(d, 1), q1, t[3]), t[4] = fma2(m1, q1, t[4]), t[5] = fma2(h1, q1, t[5]);
           }
         }
 #pragma unroll
@@ -432,14 +439,14 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
           for (int j0 = 0; j0 < 4; j0 += 2) {
             const int u = (tid + k * c.threads) * 8 + 2 * j0;
             asm volatile("" ::: "memory");
-            const uint2 z = *reinterpret_cast<const uint2*>(dz_row + 2 * u), d = *reinterpret_cast<const uint2*>(dh_row + 2 * u);
+            const auto z = load_raw(reinterpret_cast<const T*>(dz_row + sizeof(T) * u)), d = load_raw(reinterpret_cast<const T*>(dh_row + sizeof(T) * u));
             const float4 w = *reinterpret_cast<const float4*>(held_pre + u), g = *reinterpret_cast<const float4*>(held_gw + u);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int j = j0 + i;
-              const float2 t = mul2(unpack_bf16(i ? z.y : z.x), rho2);
+              const float2 t = mul2(pair(z, i), rho2);
               sum_pre[k].v[j] = fma2(t, h[k].v[j], sum_pre[k].v[j]);
-              const float2 D = fma2(h[k].v[j], of_h, fma2(t, i ? make_float2(w.z, w.w) : make_float2(w.x, w.y), unpack_bf16(i ? d.y : d.x)));
+              const float2 D = fma2(h[k].v[j], of_h, fma2(t, i ? make_float2(w.z, w.w) : make_float2(w.x, w.y), pair(d, i)));
               dx.v[j] = mul2(D, alpha);
               const float2 e = mul2(D, tau_beta);
               dy.v[j] = mul2(e, i ? make_float2(g.z, g.w) : make_float2(g.x, g.y));

@@ -7,12 +7,12 @@ namespace {
 template <bool ONE>
 NormKernel<GradArgs> rows_kernel(int form) {
   switch (form) {
-    case 1: return norm_grad_rows_kernel<0, true, ONE>;
-    case 2: return norm_grad_rows_kernel<1, true, ONE>;
-    case 3: return norm_grad_rows_kernel<2, true, ONE>;
-    case 4: return norm_grad_rows_kernel<0, false, ONE>;
-    case 5: return norm_grad_rows_kernel<1, false, ONE>;
-    default: return norm_grad_rows_kernel<2, false, ONE>;
+    case 1: return norm_grad_rows_kernel<__nv_bfloat16, 0, true, ONE>;
+    case 2: return norm_grad_rows_kernel<__nv_bfloat16, 1, true, ONE>;
+    case 3: return norm_grad_rows_kernel<__nv_bfloat16, 2, true, ONE>;
+    case 4: return norm_grad_rows_kernel<__nv_bfloat16, 0, false, ONE>;
+    case 5: return norm_grad_rows_kernel<__nv_bfloat16, 1, false, ONE>;
+    default: return norm_grad_rows_kernel<__nv_bfloat16, 2, false, ONE>;
   }
 }
 }  // namespace

@@ -655,7 +655,7 @@ def lst_checkpoint_wgrad(dy: lst_matrix, c: lst_checkpoint, norm_weight, eps: fl
 
 
 def lst_operator_status() -> None:
-    """Raises LstError (LST_ERR_TIMEOUT) if a wait inside a matrix kernel ran
+    """Raises LstError (LST_ERR_TIMEOUT) if a wait inside a matrix or norm kernel ran
     out since the last call; synchronises the device."""
     _check(lib().lst_operator_status())
 

@@ -768,7 +768,7 @@ def test_example_runs():
 
 
 def test_example_gradients():
-    """Against the same model in 64 bits by autograd. Expected: integers keep values to 0.7 % (RMS), which enters a
+    """Against the same model in 64 bits by autograd. Expected: integers keep values to 0.8 % (RMS), which enters a
     gradient twice, 1 %; bf16 roundings of 0.1 to 0.2 % each, some twenty in a row, 1 %; one in some 700 of the MLP's
     inner values lies so near zero that the rounded sum has the other sign, which replaces as many entries of its
     gradient, sqrt(1 / 700) = 4 %. Sum 6 %, bound 10 %."""
