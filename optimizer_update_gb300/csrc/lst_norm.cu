@@ -107,7 +107,7 @@ __global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant
       if (!VEC) asm volatile("" : "+r"(c.threads));  // columns' offsets are formed again: held, they would spill
       p.wait();
       const bool mine = group < rows;
-      const int64_t row = p.row + group;
+      const int64_t row = static_cast<int64_t>(p.row) + group;
       Unit h[K];
       if (mine) {
         const uint8_t* const staged = p.staged(group);
@@ -198,14 +198,16 @@ __global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant
   p.finish(&g_norm_error);
 }
 
-// Adds up the CTAs' sums, 128 columns a CTA: blockIdx.y 0: dw_pre, 1: dw_post; from 2 on the
+// Adds up the CTAs' sums, 128 columns a CTA: blockIdx.y 0: dw_pre, 1: dw_post (with one gate row
+// or none, the sums are A: dw_post from it times the gate, dgate times w_post); from 2 on the
 // gate rows that more than one CTA worked on, by their number or (where there are more
 // gate rows than CTAs) as the last gate row of CTA blockIdx.y - 2.
 struct JoinArgs {
   const float *pre, *post, *gate;
   void *dw_pre, *dw_post, *dgate;
   int64_t dgate_stride, tokens, per_gate;
-  int32_t pre_f32, post_f32, gate_f32, accumulate, hidden, ld, ctas, by_row;
+  int32_t pre_f32, post_f32, gate_f32, accumulate, hidden, ld, ctas, by_row, single;
+  Weights gate_row, w_post;  // factors of A
 };
 constexpr int kJoinWarps = 16;
 __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const __grid_constant__ JoinArgs a) {
@@ -216,7 +218,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const __grid
   const float* part = blockIdx.y == 0 ? a.pre : a.post;
   void* out = blockIdx.y == 0 ? a.dw_pre : a.dw_post;
   bool f32 = blockIdx.y == 0 ? a.pre_f32 : a.post_f32;
-  if (blockIdx.y < 2 && !out) return;
+  const bool both_of_a = blockIdx.y == 1 && a.single;
+  if (blockIdx.y < 2 && !out && !(both_of_a && a.dgate)) return;
   int64_t at = 0, r = -1, first = 0, last = a.ctas;
   if (blockIdx.y >= 2) {
     part = a.gate, out = a.dgate, f32 = a.gate_f32;
@@ -257,7 +260,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const __grid
   float v = 0.0f;
 #pragma unroll
   for (int i = 0; i < kJoinWarps; ++i) v += reinterpret_cast<const float*>(words[i])[threadIdx.x];
-  store_sum(out, at + mine, f32, a.accumulate, v);
+  if (both_of_a && a.dgate) store_sum(a.dgate, mine, a.gate_f32, a.accumulate, a.w_post.p ? v * weight_at(a.w_post, 0, mine) : v);
+  if (both_of_a && a.gate_row.p) v *= weight_at(a.gate_row, 0, mine);
+  if (out) store_sum(out, at + mine, f32, a.accumulate, v);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -553,7 +558,8 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   if (dgate) a.dgate = dgate->data, a.dgate_stride = dgate->stride, a.dgate_f32 = dgate->dtype == LST_F32;
   a.per_gate = static_cast<int32_t>(per_gate), a.accumulate = accumulate != 0;
   a.part_pre = dw_pre ? reinterpret_cast<float*>(ws + p.pre_off) : nullptr;
-  a.part_post = dw_post ? reinterpret_cast<float*>(ws + p.post_off) : nullptr;
+  const bool single = o.pipe.step != 0;  // one gate row, none, or one per token (whose dgate is complete)
+  a.part_post = dw_post || (dgate && single && !token) ? reinterpret_cast<float*>(ws + p.post_off) : nullptr;
   a.part_gate = dgate ? reinterpret_cast<float*>(ws + p.gate_off) : nullptr;
   a.alpha = params->residual_scale, a.beta = params->branch_scale, a.eps = params->eps;
   const bool all = o.pipe.simple && dh && dz && dx && dy && !token && (w_post ? a.h_kept == a.y_kept : !need_y);
@@ -562,11 +568,12 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   LST_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared), who);
   LST_TRY_CUDA(launch_chained(kernel, dim3(static_cast<unsigned>(o.pipe.ctas)), dim3(o.threads()), smem, stream, a), who);
   if (!sums) return LST_OK;
-  const int64_t gate_rows = dgate && !token ? gate->rows : 0;
+  const int64_t gate_rows = dgate && !single ? gate->rows : 0;
   const JoinArgs j = {a.part_pre, a.part_post, a.part_gate, dw_pre ? dw_pre->data : nullptr, dw_post ? dw_post->data : nullptr,
-                      a.dgate, a.dgate_stride, s.tokens, per_gate, dw_pre && dw_pre->dtype == LST_F32,
+                      token ? nullptr : a.dgate, a.dgate_stride, s.tokens, per_gate, dw_pre && dw_pre->dtype == LST_F32,
                       dw_post && dw_post->dtype == LST_F32, a.dgate_f32, a.accumulate, static_cast<int32_t>(s.hidden),
-                      static_cast<int32_t>(sum_row(s.hidden)), o.pipe.ctas, gate_rows <= o.pipe.ctas};
+                      static_cast<int32_t>(sum_row(s.hidden)), o.pipe.ctas, gate_rows <= o.pipe.ctas, single && !token,
+                      token ? Weights{} : a.gate, a.w_post};
   LST_TRY_CUDA(launch_chained(norm_join_kernel,
                               dim3(static_cast<unsigned>(ops_ceil_div(s.hidden, 128)), static_cast<unsigned>(2 + std::min<int64_t>(gate_rows, o.pipe.ctas))),
                               dim3(32 * kJoinWarps), 0, stream, j),

@@ -23,7 +23,8 @@ __device__ __forceinline__ void store_sums(void* p, int64_t at, bool f32, bool a
 }
 
 // The sums of a gate row, or of all of the CTA's rows, to the workspace (or to dgate where
-// the CTA has all of a gate row's tokens).
+// the CTA has all of a gate row's tokens). With one gate row, or none, that is A as it is,
+// from which the join forms dw_post and dgate.
 template <bool VEC, int K, bool ONE, class P>
 __device__ __forceinline__ void flush_sums(const GradArgs& a, const P& p, const Cols<VEC>& c, int group, float* group_sums, int columns,
                                            bool token, bool has_y, bool has_post, bool first_flush, const Unit (&sum_a)[K],
@@ -32,10 +33,11 @@ __device__ __forceinline__ void flush_sums(const GradArgs& a, const P& p, const 
   const int64_t cta = blockIdx.x;
   const bool last = p.row >= p.end;
   const int64_t gate_row = (p.segment - 1) / a.per_gate;
-  const bool whole = a.pipe.step ? a.pipe.ctas == 1 : gate_row * a.per_gate >= p.begin && (gate_row + 1) * a.per_gate <= p.end;
-  float* const gate_sums = a.part_gate + (2 * cta + (a.pipe.step || gate_row == p.begin / a.per_gate ? 0 : 1)) * ld;
+  const bool whole = gate_row * a.per_gate >= p.begin && (gate_row + 1) * a.per_gate <= p.end;
+  float* const gate_sums = a.part_gate + (2 * cta + (gate_row == p.begin / a.per_gate ? 0 : 1)) * ld;
   float *const post = a.part_post + cta * ld, *const pre = a.part_pre + cta * ld;
-  const bool gated = !token && a.gate.p, gates = !token && has_y && a.dgate, posts = has_y && a.part_post, pres = last && a.part_pre;
+  const bool several = !a.pipe.step, gated = several && !token && a.gate.p, gates = several && !token && has_y && a.dgate;
+  const bool posts = has_y && a.part_post, pres = last && a.part_pre;
   if (ONE || a.pipe.groups == 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -172,7 +174,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
       if (!VEC) asm volatile("" : "+r"(c.threads));  // columns' offsets are formed again: held, they would spill
       p.wait();
       if (group < rows) {
-        const int64_t row = p.row + group;
+        const int64_t row = static_cast<int64_t>(p.row) + group;
         auto pre_unit = [&](int k, int i0, Half& u) {
           if (kHold)
             c.load(held_pre, k, u, i0);
@@ -426,7 +428,7 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
       if (a.pipe.stages > 1) p.refill(false);
       asm volatile("" ::: "memory");  // what follows is read again
       if (mine) {
-        const int64_t row = p.row + group;
+        const int64_t row = static_cast<int64_t>(p.row) + group;
         const float rho = rsqrtf(s[0] * inverse + a.eps), back = rho * rho * (s[1] * inverse);
         const float tau = POST ? rsqrtf(s[2] * inverse + a.eps) : 1.0f;
         const float back_y = POST ? tau * tau * (a.beta * (s[3] + rho * (s[4] - back * s[5])) * inverse) : 0.0f;
