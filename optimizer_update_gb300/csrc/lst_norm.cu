@@ -294,6 +294,7 @@ template <int OPS>
 struct Operands {
   PipeArgs<OPS> pipe = {};
   int64_t columns;  // of a staged row: all that its threads hold where it is read unit by unit
+  int scales_only;  // nothing but scales lies off 16 bytes
   Operands(const Fit& f, bool vec, int64_t hidden) : columns(vec ? int64_t(8) * f.k * f.group : hidden) {}
   void range(int op, const void* data, int64_t stride, int64_t bytes, int64_t place) {
     pipe.in[op] = {static_cast<const uint8_t*>(data), stride, static_cast<int32_t>(bytes), pipe.row_bytes};
@@ -305,7 +306,7 @@ struct Operands {
   // values and scales; returns 1 for integers, 2 for e4m3, 0 for no checkpoint
   int32_t kept(int op, const lst_checkpoint* c) {
     if (!c) return 0;
-    range(op, c->data, c->stride, c->cols, columns);
+    range(op, c->data, c->stride, ops_round_up(c->cols, 16), ops_round_up(columns, 16));  // rows reach to there
     range(op + 1, c->scales, c->scale_stride, ops_ceil_div(c->cols, kCkptBlock), ops_ceil_div(columns, kCkptBlock));
     return c->format == LST_CHECKPOINT_E4M3 ? 2 : 1;
   }
@@ -314,12 +315,14 @@ struct Operands {
   // fewer CTAs to an SM. Returns the shared memory of a CTA.
   size_t plan(const Fit& f, int64_t tokens, int64_t hidden, int64_t per_segment, int sums, int held) {
     pipe.pad = columns > hidden;
-    pipe.simple = 1;
-    for (const Range& r : pipe.in) {
+    pipe.simple = scales_only = 1;
+    for (int op = 0; op < OPS; ++op) {
+      const Range& r = pipe.in[op];
       if (!r.p) continue;
       pipe.row_total += r.bytes;
       pipe.margin = std::max(pipe.margin, static_cast<int32_t>(ops_ceil_div(15, std::max<int64_t>(1, r.stride))));
-      if (reinterpret_cast<uintptr_t>(r.p) % 16 || (tokens > 1 && r.stride % 16) || r.bytes % 16) pipe.simple = 0;
+      if (reinterpret_cast<uintptr_t>(r.p) % 16 || (tokens > 1 && r.stride % 16) || r.bytes % 16)
+        pipe.simple = 0, scales_only &= OPS == GRAD_OPS && (op == GRAD_H_SCALES || op == GRAD_Y_SCALES);
     }
     pipe.tokens = static_cast<int32_t>(tokens), pipe.per_segment = static_cast<int32_t>(per_segment);
     pipe.hidden = static_cast<int32_t>(hidden);
@@ -562,7 +565,7 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   a.part_post = dw_post || (dgate && single && !token) ? reinterpret_cast<float*>(ws + p.post_off) : nullptr;
   a.part_gate = dgate ? reinterpret_cast<float*>(ws + p.gate_off) : nullptr;
   a.alpha = params->residual_scale, a.beta = params->branch_scale, a.eps = params->eps;
-  const bool all = o.pipe.simple && dh && dz && dx && dy && !token && (w_post ? a.h_kept == a.y_kept : !need_y);
+  const bool all = o.scales_only && dh && dz && dx && dy && !token && (w_post ? a.h_kept == a.y_kept : !need_y);
   const int form = !all ? 0 : 1 + a.h_kept + (w_post ? 0 : 3);
   const NormKernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_f32(vec, f.k, form, o.pipe.groups == 1) : norm_grad_bf16(vec, f.k, form, o.pipe.groups == 1);
   LST_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared), who);

@@ -149,8 +149,50 @@ __device__ __forceinline__ void fill_ragged(const PipeArgs<OPS>& a, int ahead, i
   if (lane == 0) tc::mbar_arrive(bar);
 }
 
+// The same where only scales (operands 3 and 5 of the backward pass) are not on 16 bytes, in
+// few registers: their rows beside the first and the last of all go byte by byte.
+template <int OPS>
+__device__ __forceinline__ void fill_scales(const PipeArgs<OPS>& a, int ahead, int n, uint32_t to, uint32_t bar) {
+  const int lane = threadIdx.x & 31;
+  const bool mine = lane < OPS && a.in[lane].p, scales = lane == 3 || lane == 5;
+  const Range& r = a.in[mine ? lane : 0];
+  auto inside = [&](int row) { return !scales || (row >= a.margin && row < a.tokens - a.margin); };
+  auto low_bits = [&](const Range& x, int row) {
+    return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x.p)) + static_cast<uint32_t>(row) * static_cast<uint32_t>(x.stride)) & 15;
+  };
+  int bytes = 0;
+#pragma unroll 1
+  for (int i = 0; i < n && mine; ++i)
+    if (inside(ahead + i)) bytes += (low_bits(r, ahead + i) + r.bytes + 15) & ~15;
+  bytes = __reduce_add_sync(0xffffffffu, bytes);
+  tc::fence_async_proxy_cta();  // lanes' bytes of the stage's last use before this one's copies
+  if (lane == 0) tc::mbar_expect_tx(bar, bytes);
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < n && mine; ++i) {
+    if (!inside(ahead + i)) continue;
+    const int off = low_bits(r, ahead + i);
+    tc::bulk_load(to + i * a.row_bytes + r.slot, r.p + static_cast<int64_t>(ahead + i) * r.stride - off, (off + r.bytes + 15) & ~15, bar);
+  }
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    if (ahead + i >= a.margin && ahead + i < a.tokens - a.margin) continue;
+#pragma unroll 1
+    for (int op = 3; op <= 5; op += 2) {
+      const Range& x = a.in[op];
+      if (!x.p) continue;
+      const uint8_t* src = x.p + static_cast<int64_t>(ahead + i) * x.stride;
+      const uint32_t dst = to + i * a.row_bytes + x.slot + low_bits(x, ahead + i);
+#pragma unroll 1
+      for (int b = lane; b < x.bytes; b += 32) asm volatile("st.shared.u8 [%0], %1;" ::"r"(dst + b), "r"(static_cast<uint32_t>(src[b])) : "memory");
+    }
+  }
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(bar);
+}
+
 // With STAGED false (rows that do not fit in shared memory) rows are read where they are;
-// with RAGGED false all ranges are on 16 bytes.
+// with RAGGED false all ranges but scales are on 16 bytes.
 template <int OPS, bool STAGED, bool RAGGED = true>
 struct Pipe {
   const PipeArgs<OPS>& a;
@@ -192,7 +234,7 @@ struct Pipe {
   __device__ __forceinline__ void fill() {
     const int lane = threadIdx.x & 31, n = min(a.groups, ahead_segment - ahead);
     const uint32_t to = tc::smem_addr(smem + kPipeHeader) + into * stage_bytes, bar = full + 8 * into;
-    if (!RAGGED || a.simple) {
+    if (a.simple) {
       // whole rows by bulk copies, a lane an operand: all other warps wait for this one
       if (lane == 0) tc::mbar_expect_tx(bar, n * a.row_total);
       __syncwarp();
@@ -202,6 +244,8 @@ struct Pipe {
         for (int i = 0; i < n; ++i) tc::bulk_load(to + i * a.row_bytes + r.slot, src + i * r.stride, r.bytes, bar);
       }
       if (lane == 0) tc::mbar_arrive(bar);
+    } else if (!RAGGED) {
+      fill_scales<OPS>(a, ahead, n, to, bar);
     } else if (ahead >= a.margin && ahead + n <= a.tokens - a.margin) {
       fill_rounded<OPS>(a, ahead, n, to, bar);
     } else {

@@ -325,13 +325,15 @@ __device__ __forceinline__ float4 load_raw(const float* p) { return *reinterpret
 __device__ __forceinline__ float2 pair(const uint2& r, int i) { return unpack_bf16(i ? r.y : r.x); }
 __device__ __forceinline__ float2 pair(const float4& r, int i) { return i ? make_float2(r.z, r.w) : make_float2(r.x, r.y); }
 
-// The same for rows of up to 8192 columns with everything on 16 bytes (scales too), all of dh, dz,
+// The same for rows of up to 8192 columns with everything but scales on 16 bytes, all of dh, dz,
 // dx and dy, no gate per token, and h and y alike: KEPT 0 matrices, 1 integers, 2 e4m3. POST:
 // a norm behind the block; without one, y is not read. h and y stay in registers from the
 // row's sums to its results, dh and dz are read from shared memory again: held too, they
 // would spill, and with all of the shared memory in use local memory lies in L2. (The
 // general kernel, which asks in every unit what there is: 633 us for 16381 x 8192 from
 // checkpoints, this one 283.)
+// Rows of scales off 16 bytes come with the 16-byte pieces around them: 8192 x 2056 from
+// checkpoints 66 us, with the general kernel 136.
 // ONE: a row at a time (rows above 2048), whose addresses are then the same in all threads.
 template <class T, int KEPT, bool POST, bool ONE>
 __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ GradArgs a) {
@@ -392,8 +394,8 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
             c.load(reinterpret_cast<const T*>(staged + a.pipe.in[GRAD_H].slot), k, h[k]);
             if (POST) c.load(reinterpret_cast<const T*>(staged + a.pipe.in[GRAD_Y].slot), k, y[k]);
           } else {
-            c.restore(staged + a.pipe.in[GRAD_H].slot, staged + a.pipe.in[GRAD_H_SCALES].slot, KEPT == 2, k, h[k]);
-            if (POST) c.restore(staged + a.pipe.in[GRAD_Y].slot, staged + a.pipe.in[GRAD_Y_SCALES].slot, KEPT == 2, k, y[k]);
+            c.restore(staged + a.pipe.in[GRAD_H].slot, p.at(GRAD_H_SCALES, group, staged, false), KEPT == 2, k, h[k]);
+            if (POST) c.restore(staged + a.pipe.in[GRAD_Y].slot, p.at(GRAD_Y_SCALES, group, staged, false), KEPT == 2, k, y[k]);
           }
         }
       }

@@ -396,6 +396,22 @@ def test_norm_grad_from_checkpoints(n, h, dtype, pad, fmt):
     p.check_backward(p.x.double(), yv, p.backward(p.x, y8))
 
 
+@pytest.mark.parametrize("n,h,dtype,kw", [
+    (1, 2056, "bf16", {}), (2, 96, "bf16", {}), (17, 8168, "bf16", {}), (40, 8160, "f32", {}), (1300, 4104, "bf16", dict(gate_rows=0)),
+    (5000, 264, "bf16", dict(gate_rows=4)), (2000, 32, "f32", dict(gate_rows=1000)), (901, 1032, "bf16", dict(post=False)), (64, 8, "bf16", {})])
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+def test_norm_grad_from_two_checkpoints_of_any_scale_rows(n, h, dtype, kw, fmt):
+    """h and y kept alike, with rows of scales off 16 bytes, and their starts, too."""
+    p = Norm(n, h, dtype, **kw)
+    kept = []
+    for x, at in ((p.x, 0), (p.y, 5)):
+        data, scales, _ = checkpoint(x, fmt)
+        blocks = torch.full((n, scales.shape[1] + at), 255, dtype=torch.uint8, device="cuda")
+        blocks[:, at:] = scales
+        kept.append((data, blocks[:, at:], fmt))
+    p.check_backward(*(reference_checkpoint(x, fmt)[2] for x in (p.x, p.y)), p.backward(*kept))
+
+
 @pytest.mark.parametrize("n,h", [(60, 40), (60, 2056), (700, 8), (900, 1), (40, 3), (333, 17), (50, 1032)])
 def test_norm_grad_of_ragged_rows_beside_other_bytes(n, h):
     """Rows of checkpoints that end inside 16 bytes, with e4m3 NaN behind them; rows of a byte or a few."""
