@@ -640,7 +640,7 @@ struct WgradEpilogue {
       else
         units<true, kCols>(e, out, rows, col0, left, tmem, turn);
     } else {
-if (e.f32)
+      if (e.f32)
         turned<float, kCols>(e, out, rows, col0, left, tmem, turn);
       else
         turned<__nv_bfloat16, kCols>(e, out, rows, col0, left, tmem, turn);

@@ -11,8 +11,9 @@
 //   e  = b D g w_post,  dy = tau (e - y tau^2 mean(e y))
 //   A  = sum D tau y over the tokens of a gate row;  dgate = b w_post A,  dw_post = b sum g A
 // so two sums per column (A and dw_pre's) give all three parameter gradients. A CTA
-// takes consecutive rows and keeps the column sums in registers; they go to the
-// workspace once per CTA (A once per gate row) and are added up in order by a second launch.
+// takes consecutive rows (with one gate row, rows in turns) and keeps the column sums in
+// registers; they go to the workspace once per CTA (A once per gate row) and are added up
+// in order by a second launch.
 //
 // Floors are memory's: 8 bytes an element forward, 12 backward in bf16 (10 with checkpoints).
 // Forward runs at 5.9 TB/s (16384 x 4096 with an 8-bit copy, 114 us). Backward runs at 4.9 TB/s
@@ -565,8 +566,8 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   a.part_post = dw_post || (dgate && single && !token) ? reinterpret_cast<float*>(ws + p.post_off) : nullptr;
   a.part_gate = dgate ? reinterpret_cast<float*>(ws + p.gate_off) : nullptr;
   a.alpha = params->residual_scale, a.beta = params->branch_scale, a.eps = params->eps;
-  const bool all = o.scales_only && dh && dz && dx && dy && !token && (w_post ? a.h_kept == a.y_kept : !need_y);
-  const int form = !all ? 0 : 1 + a.h_kept + (w_post ? 0 : 3);
+  const bool whole = o.scales_only && dz && !token && (!need_y || a.h_kept == a.y_kept);
+  const int block = !need_y ? 0 : w_post && dh && dx && dy ? 2 : 1, form = whole ? 1 + a.h_kept + 3 * block : 0;
   const NormKernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_f32(vec, f.k, form, o.pipe.groups == 1) : norm_grad_bf16(vec, f.k, form, o.pipe.groups == 1);
   LST_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared), who);
   LST_TRY_CUDA(launch_chained(kernel, dim3(static_cast<unsigned>(o.pipe.ctas)), dim3(o.threads()), smem, stream, a), who);

@@ -409,8 +409,8 @@ __device__ __forceinline__ void store_sum(void* p, int64_t at, bool f32, bool ac
 template <class Args>
 using NormKernel = void (*)(const Args);
 // The backward kernel for activations of a type (lst_norm_grad_bf16.cu, lst_norm_grad_f32.cu),
-// 8 k columns a thread, and the word that its waits set when one runs out. `form`: 0 the general kernel; 1 + KEPT that for whole units,
-// 4 + KEPT without a norm behind the block; `one`: its ONE.
+// 8 k columns a thread, and the word that its waits set when one runs out. `form`: 0 the general
+// kernel, 1 + KEPT + 3 BLOCK that for whole units; `one`: its ONE.
 NormKernel<GradArgs> norm_grad_bf16(bool vec, int k, int form, bool one);
 NormKernel<GradArgs> norm_grad_f32(bool vec, int k, int form, bool one);
 cudaError_t norm_grad_bf16_take_error(int* out);

@@ -325,9 +325,10 @@ __device__ __forceinline__ float4 load_raw(const float* p) { return *reinterpret
 __device__ __forceinline__ float2 pair(const uint2& r, int i) { return unpack_bf16(i ? r.y : r.x); }
 __device__ __forceinline__ float2 pair(const float4& r, int i) { return i ? make_float2(r.z, r.w) : make_float2(r.x, r.y); }
 
-// The same for rows of up to 8192 columns with everything but scales on 16 bytes, all of dh, dz,
-// dx and dy, no gate per token, and h and y alike: KEPT 0 matrices, 1 integers, 2 e4m3. POST:
-// a norm behind the block; without one, y is not read. h and y stay in registers from the
+// The same for rows of up to 8192 columns with everything but scales on 16 bytes, with dz,
+// no gate per token, and h and y alike: KEPT 0 matrices, 1 integers, 2 e4m3. BLOCK 0: y is
+// not read; 1: it is (for a norm behind the block, or the gate's gradient); 2: there is that norm,
+// and dh, dx and dy (asking whether costs 16384 x 8192 54 us of 393). h and y stay in registers from the
 // row's sums to its results, dh and dz are read from shared memory again: held too, they
 // would spill, and with all of the shared memory in use local memory lies in L2. (The
 // general kernel, which asks in every unit what there is: 633 us for 16381 x 8192 from
@@ -335,7 +336,7 @@ __device__ __forceinline__ float2 pair(const float4& r, int i) { return i ? make
 // Rows of scales off 16 bytes come with the 16-byte pieces around them: 8192 x 2056 from
 // checkpoints 66 us, with the general kernel 136.
 // ONE: a row at a time (rows above 2048), whose addresses are then the same in all threads.
-template <class T, int KEPT, bool POST, bool ONE>
+template <class T, int KEPT, int BLOCK, bool ONE>
 __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ GradArgs a) {
   constexpr int K = 2;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -348,6 +349,8 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
   const float inverse = 1.0f / static_cast<float>(a.pipe.hidden);
   float* const words = p.words() + group * warps * 8;
   int turn = 0;
+  const bool has_dh = BLOCK == 2 || a.pipe.in[GRAD_DH].p, has_dx = BLOCK == 2 || a.dx.p, has_dy = BLOCK == 2 || a.dy.p;
+  const bool has_post = BLOCK == 2 || (BLOCK == 1 && a.w_post.p);
   const int columns = 8 * K * a.pipe.group;
   float* const group_sums = reinterpret_cast<float*>(smem + kPipeHeader + a.pipe.stages * p.stage_bytes);
   float* const held_pre = group_sums + (ONE ? 0 : a.pipe.groups * 2 * columns);
@@ -368,7 +371,7 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
         if (there[k]) c.load_any(a.w_pre.p, a.w_pre.f32, k, u);
         c.store(held_pre, k, u);
         u.fill(there[k] ? 1.0f : 0.0f);
-        if (POST && there[k]) c.load_any(a.w_post.p, a.w_post.f32, k, u);
+        if (has_post && there[k]) c.load_any(a.w_post.p, a.w_post.f32, k, u);
         if (a.gate.p && there[k]) {
           c.load_any(row_of(a.gate, p.row / a.per_gate), a.gate.f32, k, g);
 #pragma unroll
@@ -392,10 +395,10 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
         for (int k = 0; k < K; ++k) {
           if (KEPT == 0) {
             c.load(reinterpret_cast<const T*>(staged + a.pipe.in[GRAD_H].slot), k, h[k]);
-            if (POST) c.load(reinterpret_cast<const T*>(staged + a.pipe.in[GRAD_Y].slot), k, y[k]);
+            if (BLOCK) c.load(reinterpret_cast<const T*>(staged + a.pipe.in[GRAD_Y].slot), k, y[k]);
           } else {
             c.restore(staged + a.pipe.in[GRAD_H].slot, p.at(GRAD_H_SCALES, group, staged, false), KEPT == 2, k, h[k]);
-            if (POST) c.restore(staged + a.pipe.in[GRAD_Y].slot, p.at(GRAD_Y_SCALES, group, staged, false), KEPT == 2, k, y[k]);
+            if (BLOCK) c.restore(staged + a.pipe.in[GRAD_Y].slot, p.at(GRAD_Y_SCALES, group, staged, false), KEPT == 2, k, y[k]);
           }
         }
       }
@@ -414,8 +417,8 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
           const float2 h0 = h[k].v[j0], h1 = h[k].v[j0 + 1];
           t[0] = fma2(h0, h0, t[0]), t[1] = fma2(m0, h0, t[1]);
           t[0] = fma2(h1, h1, t[0]), t[1] = fma2(m1, h1, t[1]);
-          if (POST) {
-            const auto d = load_raw(reinterpret_cast<const T*>(dh_row + sizeof(T) * u));
+          if (BLOCK) {
+            const auto d = has_dh ? load_raw(reinterpret_cast<const T*>(dh_row + sizeof(T) * u)) : decltype(z){};
             const float4 g = *reinterpret_cast<const float4*>(held_gw + u);
             const float2 y0 = y[k].v[j0], y1 = y[k].v[j0 + 1];
             const float2 q0 = mul2(make_float2(g.x, g.y), y0), q1 = mul2(make_float2(g.z, g.w), y1);
@@ -425,15 +428,15 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
         }
 #pragma unroll
         for (int j = 0; j < 6; ++j) s[j] = t[j].x + t[j].y;
-        group_sum8<POST ? 6 : 2>(s, words, turn, warps, warp, 1 + group, a.pipe.group);
+        group_sum8<BLOCK ? 6 : 2>(s, words, turn, warps, warp, 1 + group, a.pipe.group);
       }
       if (a.pipe.stages > 1) p.refill(false);
       asm volatile("" ::: "memory");  // what follows is read again
       if (mine) {
         const int64_t row = static_cast<int64_t>(p.row) + group;
         const float rho = rsqrtf(s[0] * inverse + a.eps), back = rho * rho * (s[1] * inverse);
-        const float tau = POST ? rsqrtf(s[2] * inverse + a.eps) : 1.0f;
-        const float back_y = POST ? tau * tau * (a.beta * (s[3] + rho * (s[4] - back * s[5])) * inverse) : 0.0f;
+        const float tau = has_post ? rsqrtf(s[2] * inverse + a.eps) : 1.0f;
+        const float back_y = has_post ? tau * tau * (a.beta * (s[3] + rho * (s[4] - back * s[5])) * inverse) : 0.0f;
         const float2 rho2 = both(rho), of_h = both(-rho * back), alpha = both(a.alpha), tau_beta = both(tau * a.beta), of_y = both(-tau * back_y);
         T *const dx_out = row_of<T>(a.dx, row), *const dy_out = row_of<T>(a.dy, row);
 #pragma unroll
@@ -443,7 +446,8 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
           for (int j0 = 0; j0 < 4; j0 += 2) {
             const int u = (tid + k * c.threads) * 8 + 2 * j0;
             asm volatile("" ::: "memory");
-            const auto z = load_raw(reinterpret_cast<const T*>(dz_row + sizeof(T) * u)), d = load_raw(reinterpret_cast<const T*>(dh_row + sizeof(T) * u));
+            const auto z = load_raw(reinterpret_cast<const T*>(dz_row + sizeof(T) * u));
+            const auto d = has_dh ? load_raw(reinterpret_cast<const T*>(dh_row + sizeof(T) * u)) : decltype(z){};
             const float4 w = *reinterpret_cast<const float4*>(held_pre + u), g = *reinterpret_cast<const float4*>(held_gw + u);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -454,21 +458,21 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
               dx.v[j] = mul2(D, alpha);
               const float2 e = mul2(D, tau_beta);
               dy.v[j] = mul2(e, i ? make_float2(g.z, g.w) : make_float2(g.x, g.y));
-              if (POST) {
-                dy.v[j] = fma2(y[k].v[j], of_y, dy.v[j]);
+              if (BLOCK) {
+                if (has_post) dy.v[j] = fma2(y[k].v[j], of_y, dy.v[j]);
                 sum_a[k].v[j] = fma2(e, y[k].v[j], sum_a[k].v[j]);
               }
             }
           }
           if (there[k]) {
-            c.store(dx_out, k, dx);
-            c.store(dy_out, k, dy);
+            if (has_dx) c.store(dx_out, k, dx);
+            if (has_dy) c.store(dy_out, k, dy);
           }
         }
       }
       p.release();
     } while (p.next(rows));
-    flush_sums<true, K, ONE>(a, p, c, group, group_sums, columns, false, POST, POST, first_flush, sum_a, sum_pre);
+    flush_sums<true, K, ONE>(a, p, c, group, group_sums, columns, false, BLOCK > 0, has_post, first_flush, sum_a, sum_pre);
 #pragma unroll
     for (int k = 0; k < K; ++k) sum_a[k].fill(0.0f);
     first_flush = false;

@@ -4,21 +4,20 @@
 namespace lst {
 
 namespace {
+template <int BLOCK, bool ONE>
+NormKernel<GradArgs> rows_kernel(int kept) {
+  return kept == 0   ? norm_grad_rows_kernel<float, 0, BLOCK, ONE>
+         : kept == 1 ? norm_grad_rows_kernel<float, 1, BLOCK, ONE>
+                     : norm_grad_rows_kernel<float, 2, BLOCK, ONE>;
+}
 template <bool ONE>
-NormKernel<GradArgs> rows_kernel(int form) {
-  switch (form) {
-    case 1: return norm_grad_rows_kernel<float, 0, true, ONE>;
-    case 2: return norm_grad_rows_kernel<float, 1, true, ONE>;
-    case 3: return norm_grad_rows_kernel<float, 2, true, ONE>;
-    case 4: return norm_grad_rows_kernel<float, 0, false, ONE>;
-    case 5: return norm_grad_rows_kernel<float, 1, false, ONE>;
-    default: return norm_grad_rows_kernel<float, 2, false, ONE>;
-  }
+NormKernel<GradArgs> rows_kernel(int block, int kept) {
+  return block == 0 ? rows_kernel<0, ONE>(kept) : block == 1 ? rows_kernel<1, ONE>(kept) : rows_kernel<2, ONE>(kept);
 }
 }  // namespace
 
 NormKernel<GradArgs> norm_grad_f32(bool vec, int k, int form, bool one) {
-  if (vec && k == 2 && form) return one ? rows_kernel<true>(form) : rows_kernel<false>(form);
+  if (vec && k == 2 && form) return one ? rows_kernel<true>((form - 1) / 3, (form - 1) % 3) : rows_kernel<false>((form - 1) / 3, (form - 1) % 3);
   if (vec) return k == 4 ? norm_grad_kernel<float, true, 4, false> : norm_grad_kernel<float, true, 2, true>;
   return k == 4 ? norm_grad_kernel<float, false, 4, false> : k == 2 ? norm_grad_kernel<float, false, 2, true> : norm_grad_kernel<float, false, 1, true>;
 }

@@ -412,6 +412,23 @@ def test_norm_grad_from_two_checkpoints_of_any_scale_rows(n, h, dtype, kw, fmt):
     p.check_backward(*(reference_checkpoint(x, fmt)[2] for x in (p.x, p.y)), p.backward(*kept))
 
 
+@pytest.mark.parametrize("n,h,dtype", [(301, 264, "bf16"), (90, 4104, "bf16"), (33, 8192, "f32")])
+@pytest.mark.parametrize("fmt", [None, "i8", "e4m3"])
+@pytest.mark.parametrize("kw,dh", [(dict(post=False), True), (dict(post=False), False), (dict(), False), (dict(gate_rows=0, post=False), False),
+                                   (dict(gate_rows=3, post=False), True)])
+def test_norm_grad_forms_of_whole_units(n, h, dtype, fmt, kw, dh):
+    """Rows on 16 bytes without dh, or with a gate's gradient but no norm behind the block; y's infinities stay out of dy there."""
+    p = Norm(n // 3 * 3, h, dtype, **kw)
+    h_in, y_in = (v if fmt is None else checkpoint(v, fmt) for v in (p.x, p.y))
+    hv, yv = (v.double() if fmt is None else reference_checkpoint(v, fmt)[2] for v in (p.x, p.y))
+    got = p.backward(h_in, y_in, dh=dh)
+    p.check_backward(hv, yv, got, dh=dh)
+    if p.w_post is None:
+        p.y[1, 5] = float("inf")
+        dx, dy, *_ = p.backward(h_in, y_in if fmt is None else checkpoint(p.y, fmt), dh=dh)
+        assert torch.equal(dx, got[0]) and torch.equal(dy, got[1])
+
+
 @pytest.mark.parametrize("n,h", [(60, 40), (60, 2056), (700, 8), (900, 1), (40, 3), (333, 17), (50, 1032)])
 def test_norm_grad_of_ragged_rows_beside_other_bytes(n, h):
     """Rows of checkpoints that end inside 16 bytes, with e4m3 NaN behind them; rows of a byte or a few."""
