@@ -108,7 +108,7 @@ __global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant
       if (!VEC) asm volatile("" : "+r"(c.threads));  // columns' offsets are formed again: held, they would spill
       p.wait();
       const bool mine = group < rows;
-      const int64_t row = static_cast<int64_t>(p.row) + group;
+      const int64_t row = static_cast<uint32_t>(p.row) + group;
       Unit h[K];
       if (mine) {
         const uint8_t* const staged = p.staged(group);

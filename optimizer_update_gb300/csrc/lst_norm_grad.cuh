@@ -174,7 +174,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
       if (!VEC) asm volatile("" : "+r"(c.threads));  // columns' offsets are formed again: held, they would spill
       p.wait();
       if (group < rows) {
-        const int64_t row = static_cast<int64_t>(p.row) + group;
+        const int64_t row = static_cast<uint32_t>(p.row) + group;
         auto pre_unit = [&](int k, int i0, Half& u) {
           if (kHold)
             c.load(held_pre, k, u, i0);
@@ -433,7 +433,7 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
       if (a.pipe.stages > 1) p.refill(false);
       asm volatile("" ::: "memory");  // what follows is read again
       if (mine) {
-        const int64_t row = static_cast<int64_t>(p.row) + group;
+        const int64_t row = static_cast<uint32_t>(p.row) + group;
         const float rho = rsqrtf(s[0] * inverse + a.eps), back = rho * rho * (s[1] * inverse);
         const float tau = has_post ? rsqrtf(s[2] * inverse + a.eps) : 1.0f;
         const float back_y = has_post ? tau * tau * (a.beta * (s[3] + rho * (s[4] - back * s[5])) * inverse) : 0.0f;
