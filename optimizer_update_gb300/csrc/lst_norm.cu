@@ -13,7 +13,7 @@
 // so two sums per column (A and dw_pre's) give all three parameter gradients. A CTA
 // takes consecutive rows (with one gate row, rows in turns) and keeps the column sums in
 // registers; they go to the workspace once per CTA (A once per gate row) and are added up
-// in order by a second launch.
+// in order by a second launch. Rows above 8192 columns: lst_norm_split.cuh.
 //
 // Floors are memory's: 8 bytes an element forward, 12 backward in bf16 (10 with checkpoints).
 // Forward runs at 5.9 TB/s (16384 x 4096 with an 8-bit copy, 114 us). Backward runs at 4.9 TB/s
@@ -51,7 +51,7 @@ template <class T, bool VEC, int K>
 __global__ void __maxnreg__(K == 4 ? 128 : 80) norm_kernel(const __grid_constant__ NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   let_next_start();
-  Pipe<NORM_OPS, true> p(a.pipe, smem);
+  Pipe<NORM_OPS> p(a.pipe, smem);
   wait_for_previous();
   p.start(VEC && a.pipe.pad);
   const int group = threadIdx.x / a.pipe.group, tid = threadIdx.x - group * a.pipe.group, warp = tid >> 5, warps = a.pipe.group >> 5;
@@ -287,7 +287,7 @@ Fit norm_fit(int64_t hidden) { return fit(hidden, 768, hidden <= 8192 ? 2 : 4); 
 // Backward, rows that are not whole units take 8 columns a thread where 512 threads are enough: code
 // that goes value by value is long, and half of it with twice the warps runs faster (1023 x 4095 in
 // fp32 with a gate per token: 74 us with 16 columns a thread, 49 with 8).
-Fit grad_fit(int64_t hidden, bool vec) { return fit(hidden, 512, !vec && hidden <= 4096 ? 1 : hidden <= 8192 ? 2 : 4); }
+Fit grad_fit(int64_t hidden, bool vec) { return fit(hidden, 512, !vec && hidden <= 4096 ? 1 : 2); }
 int64_t ctas_of(const Fit& f, int64_t tokens) { return std::min(ops_ceil_div(tokens, f.groups), kSms * f.per_sm); }
 
 // Operands in the order of their slots in a staged row.
@@ -412,17 +412,24 @@ NormKernel<NormArgs> norm_of(int k) {
 // Elements of a row of sums in the workspace.
 int64_t sum_row(int64_t hidden) { return ops_round_up(hidden, 4); }
 
+// Rows above 8192 columns go backward in two launches (lst_norm_split.cuh), by tiles of columns
+// and chunks of rows.
+constexpr int64_t kWide = 8192;
+int64_t split_chunks(int64_t tokens, int64_t hidden, bool vec) { return std::min(tokens, split_ctas(vec) * kSms / ops_ceil_div(hidden, kSplitTile)); }
+
 struct GradPlan {
-  int64_t ctas, pre_off, post_off, gate_off, bytes;
+  int64_t ctas, pre_off, post_off, gate_off, stats_off, bytes;
 };
 GradPlan grad_plan(int64_t tokens, int64_t hidden, int64_t gate_rows) {
   GradPlan p;
-  p.ctas = std::max(ctas_of(grad_fit(hidden, false), tokens), ctas_of(grad_fit(hidden, true), tokens));
+  p.ctas = hidden > kWide ? split_chunks(tokens, hidden, false)
+                          : std::max(ctas_of(grad_fit(hidden, false), tokens), ctas_of(grad_fit(hidden, true), tokens));
   const int64_t each = ops_round_up(p.ctas * sum_row(hidden) * 4, 256);
   p.pre_off = 0;
   p.post_off = each;
   p.gate_off = 2 * each;
-  p.bytes = 2 * each + (gate_rows > 0 ? 2 * each : 0);
+  p.stats_off = 2 * each + (gate_rows > 0 ? 2 * each : 0);
+  p.bytes = p.stats_off + (hidden > kWide ? ops_round_up(tokens * 16, 256) : 0);
   return p;
 }
 
@@ -540,37 +547,51 @@ extern "C" lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_mat
   }
   const bool need_y = w_post || dgate;  // without either, dy is a multiple of D
   const GradPlan p = grad_plan(s.tokens, s.hidden, gate ? gate->rows : 0);
-  const bool sums = dw_pre || dw_post || dgate;
-  LST_TRY(check_workspace(workspace, workspace_bytes, sums ? p.bytes : 0, who));
+  const bool sums = dw_pre || dw_post || dgate, wide = s.hidden > kWide;
+  LST_TRY(check_workspace(workspace, workspace_bytes, sums || wide ? p.bytes : 0, who));
   char* ws = static_cast<char*>(workspace);
   const lst_matrix *h_in = dz ? h : nullptr, *y_in = need_y ? y : nullptr;
   const int64_t per_gate = gate ? s.tokens / gate->rows : s.tokens;
   const bool token = per_gate == 1 && s.tokens > 1;
   const bool vec = s.hidden % 8 == 0 && on16(dh) && on16(dz) && on16(h_in) && on16(y_in) && on16(dx) && on16(dy) && (!token || on16(gate));
   const Fit f = grad_fit(s.hidden, vec);
-  Operands<GRAD_OPS> o(f, vec && f.k == 2, s.hidden);
+  Operands<GRAD_OPS> o(f, vec, s.hidden);
   GradArgs a = {};
   o.matrix(GRAD_DH, dh), o.matrix(GRAD_DZ, dz), o.matrix(GRAD_H, h_in), o.matrix(GRAD_Y, y_in);
   a.h_kept = o.kept(GRAD_H, dz ? h8 : nullptr);
   a.y_kept = o.kept(GRAD_Y, need_y ? y8 : nullptr);
   if (token) o.matrix(GRAD_GATE, gate);
-  size_t smem = o.plan(f, s.tokens, s.hidden, token ? s.tokens : per_gate, 2, f.k <= 2 ? 2 : 0);
-  if (f.k == 4) o.pipe.stages = 0, smem = kPipeHeader;  // these read rows where they are
+  size_t smem = 0;
+  if (wide) {
+    o.pipe.tokens = static_cast<int32_t>(s.tokens), o.pipe.hidden = static_cast<int32_t>(s.hidden);
+    o.pipe.ctas = static_cast<int32_t>(split_chunks(s.tokens, s.hidden, vec));
+  } else {
+    smem = o.plan(f, s.tokens, s.hidden, token ? s.tokens : per_gate, 2, 2);
+  }
   a.pipe = o.pipe;
   a.dx = rows_arg(dx), a.dy = rows_arg(dy);
   a.gate = weights_arg(gate), a.w_post = weights_arg(w_post), a.w_pre = weights_arg(w_pre);
   if (dgate) a.dgate = dgate->data, a.dgate_stride = dgate->stride, a.dgate_f32 = dgate->dtype == LST_F32;
   a.per_gate = static_cast<int32_t>(per_gate), a.accumulate = accumulate != 0;
   a.part_pre = dw_pre ? reinterpret_cast<float*>(ws + p.pre_off) : nullptr;
-  const bool single = o.pipe.step != 0;  // one gate row, none, or one per token (whose dgate is complete)
+  const bool single = token || per_gate == s.tokens;  // one gate row, none, or one per token (whose dgate is complete)
   a.part_post = dw_post || (dgate && single && !token) ? reinterpret_cast<float*>(ws + p.post_off) : nullptr;
   a.part_gate = dgate ? reinterpret_cast<float*>(ws + p.gate_off) : nullptr;
   a.alpha = params->residual_scale, a.beta = params->branch_scale, a.eps = params->eps;
-  const bool whole = o.scales_only && dz && !token && (!need_y || a.h_kept == a.y_kept);
-  const int block = !need_y ? 0 : w_post && dh && dx && dy ? 2 : 1, form = whole ? 1 + a.h_kept + 3 * block : 0;
-  const NormKernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_f32(vec, f.k, form, o.pipe.groups == 1) : norm_grad_bf16(vec, f.k, form, o.pipe.groups == 1);
-  LST_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared), who);
-  LST_TRY_CUDA(launch_chained(kernel, dim3(static_cast<unsigned>(o.pipe.ctas)), dim3(o.threads()), smem, stream, a), who);
+  if (wide) {
+    const SplitKernels kernels = s.dtype == LST_F32 ? norm_split_f32(vec) : norm_split_bf16(vec);
+    a.stats = reinterpret_cast<float4*>(ws + p.stats_off), a.token = token, a.single = single;
+    if (dz || w_post)
+      LST_TRY_CUDA(launch_chained(kernels.stats, dim3(static_cast<unsigned>(std::min(s.tokens, 4 * kSms))), dim3(256), 0, stream, a), who);
+    const dim3 grid(static_cast<unsigned>(ops_ceil_div(s.hidden, kSplitTile)), static_cast<unsigned>(o.pipe.ctas));
+    LST_TRY_CUDA(launch_chained(kernels.apply, grid, dim3(kSplitTile / 8), 0, stream, a), who);
+  } else {
+    const bool whole = vec && o.scales_only && dz && !token && (!need_y || a.h_kept == a.y_kept);
+    const int block = !need_y ? 0 : w_post && dh && dx && dy ? 2 : 1, form = whole ? 1 + a.h_kept + 3 * block : 0;
+    const NormKernel<GradArgs> kernel = s.dtype == LST_F32 ? norm_grad_f32(vec, f.k, form, o.pipe.groups == 1) : norm_grad_bf16(vec, f.k, form, o.pipe.groups == 1);
+    LST_TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared), who);
+    LST_TRY_CUDA(launch_chained(kernel, dim3(static_cast<unsigned>(o.pipe.ctas)), dim3(o.threads()), smem, stream, a), who);
+  }
   if (!sums) return LST_OK;
   const int64_t gate_rows = dgate && !single ? gate->rows : 0;
   const JoinArgs j = {a.part_pre, a.part_post, a.part_gate, dw_pre ? dw_pre->data : nullptr, dw_post ? dw_post->data : nullptr,

@@ -191,9 +191,8 @@ __device__ __forceinline__ void fill_scales(const PipeArgs<OPS>& a, int ahead, i
   if (lane == 0) tc::mbar_arrive(bar);
 }
 
-// With STAGED false (rows that do not fit in shared memory) rows are read where they are;
-// with RAGGED false all ranges but scales are on 16 bytes.
-template <int OPS, bool STAGED, bool RAGGED = true>
+// With RAGGED false all ranges but scales are on 16 bytes.
+template <int OPS, bool RAGGED = true>
 struct Pipe {
   const PipeArgs<OPS>& a;
   uint8_t* smem;
@@ -210,17 +209,15 @@ struct Pipe {
     stage_bytes = a.row_bytes * a.groups;
     stage = into = 0, phase = 0, ok = true;
     current = smem + kPipeHeader;
-    if (STAGED) {
-      for (int i = threadIdx.x; i < 256; i += blockDim.x) words()[i] = 0.0f;
-      if (threadIdx.x == 0) {
-        for (int i = 0; i < a.stages; ++i) {
-          tc::mbar_init(full + 8 * i, 2);
-          tc::mbar_init(empty + 8 * i, blockDim.x >> 5);
-        }
-        tc::mbar_init_fence();
+    for (int i = threadIdx.x; i < 256; i += blockDim.x) words()[i] = 0.0f;
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < a.stages; ++i) {
+        tc::mbar_init(full + 8 * i, 2);
+        tc::mbar_init(empty + 8 * i, blockDim.x >> 5);
       }
-      __syncthreads();
+      tc::mbar_init_fence();
     }
+    __syncthreads();
     begin = row = ahead = a.step ? static_cast<int>(blockIdx.x) * a.groups : static_cast<int>(first_row(blockIdx.x, a.tokens, a.ctas));
     end = a.step ? a.tokens : static_cast<int>(first_row(blockIdx.x + 1, a.tokens, a.ctas));
     segment = ahead_segment = segment_end(begin);
@@ -257,33 +254,32 @@ struct Pipe {
   }
   // With `pad`, ranges are shorter than their places in a stage, where zeros stand behind them.
   __device__ __forceinline__ void start(bool pad) {
-    if (STAGED && pad) {
+    if (pad) {
       uint4* const p = reinterpret_cast<uint4*>(smem + kPipeHeader);
       for (int i = threadIdx.x; i < a.stages * stage_bytes / 16; i += blockDim.x) p[i] = make_uint4(0, 0, 0, 0);
       tc::fence_async_proxy_cta();
       __syncthreads();
     }
-    if (STAGED && threadIdx.x < 32)
+    if (threadIdx.x < 32)
       for (int i = 0; i < a.stages && ahead < end; ++i) fill();
   }
   // Warp 0, while a turn is under way: the stage of the turn before is filled again (a
   // warp for that alone would cost the others an eighth of their registers). A lone
   // stage is filled again at its turn's end.
   __device__ __forceinline__ void refill(bool lone) {
-    if (!STAGED || threadIdx.x >= 32 || ahead >= end || lone != (a.stages == 1) || (!lone && row == begin)) return;
+    if (threadIdx.x >= 32 || ahead >= end || lone != (a.stages == 1) || (!lone && row == begin)) return;
     const uint32_t parity = lone || stage > 0 ? phase : phase ^ 1;
     ok = __all_sync(0xffffffffu, ok && tc::mbar_wait(empty + 8 * into, parity));
     if (ok) fill();
   }
   __device__ __forceinline__ void wait() {
-    if (STAGED) ok = ok && tc::mbar_wait(full + 8 * stage, phase);
+    ok = ok && tc::mbar_wait(full + 8 * stage, phase);
   }
   // The staged row of group `g` in this turn, and operand `op` of it; `aligned`: its rows are on 16 bytes.
   __device__ __forceinline__ const uint8_t* staged(int g) const {
     return current + g * a.row_bytes;
   }
   __device__ __forceinline__ const uint8_t* at(int op, int g, const uint8_t* staged_row, bool aligned) const {
-    if (!STAGED) return a.in[op].p + static_cast<int64_t>(row + g) * a.in[op].stride;
     if (aligned) return staged_row + a.in[op].slot;
     const uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(a.in[op].p)) +
                          static_cast<uint32_t>(row + g) * static_cast<uint32_t>(a.in[op].stride);
@@ -291,17 +287,14 @@ struct Pipe {
   }
   // This warp has read the turn's rows.
   __device__ __forceinline__ void release() {
-    if (!STAGED) return;
     __syncwarp();
     if ((threadIdx.x & 31) == 0) tc::mbar_arrive(empty + 8 * stage);
   }
   // The next turn; false behind the last of a segment.
   __device__ __forceinline__ bool next(int n) {
     refill(true);
-    if (STAGED) {
-      current += stage_bytes;
-      if (++stage == a.stages) stage = 0, phase ^= 1, current = smem + kPipeHeader;
-    }
+    current += stage_bytes;
+    if (++stage == a.stages) stage = 0, phase ^= 1, current = smem + kPipeHeader;
     row = static_cast<int>(min(static_cast<int64_t>(row) + (a.step ? a.step : n), int64_t(INT32_MAX)));
     return row < segment;
   }
@@ -313,7 +306,7 @@ struct Pipe {
   }
   // A wait ran out (all later ones are passed over): copies in flight get time to land before the CTA ends.
   __device__ __forceinline__ void finish(int* error) {
-    if (STAGED && !ok) {
+    if (!ok) {
       atomicExch(error, 1);
       for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     }
@@ -393,6 +386,9 @@ struct GradArgs {
   // sums over a CTA's rows: of dw_pre and dw_post [cta][hidden], of dgate [2 cta + (0: its first gate row)][hidden]
   float *part_pre, *part_post, *part_gate;
   float alpha, beta, eps;
+  // lst_norm_split.cuh: rho and the factors of every row; a gate per token; one gate row or none (or one per token)
+  float4* stats;
+  int32_t token, single;
 };
 
 // One value of a parameter gradient.
@@ -406,6 +402,19 @@ __device__ __forceinline__ void store_sum(void* p, int64_t at, bool f32, bool ac
   }
 }
 
+// A unit of a row of parameter gradients that starts at element `at`.
+template <bool VEC, int P>
+__device__ __forceinline__ void store_sums(void* p, int64_t at, bool f32, bool accumulate, const Cols<VEC>& c, int k, const Part<P>& u, int i0 = 0) {
+  if (VEC && !accumulate && (reinterpret_cast<uintptr_t>(p) + at * (f32 ? 4 : 2)) % 16 == 0) {
+    if (f32)
+      c.store(static_cast<float*>(p) + at, k, u, i0);
+    else
+      c.store(static_cast<__nv_bfloat16*>(p) + at, k, u, i0);
+  } else {
+    for_each(c, k, u, [&](uint32_t col, float v) { store_sum(p, at + col, f32, accumulate, v); }, i0);
+  }
+}
+
 template <class Args>
 using NormKernel = void (*)(const Args);
 // The backward kernel for activations of a type (lst_norm_grad_bf16.cu, lst_norm_grad_f32.cu),
@@ -413,6 +422,15 @@ using NormKernel = void (*)(const Args);
 // kernel, 1 + KEPT + 3 BLOCK that for whole units; `one`: its ONE.
 NormKernel<GradArgs> norm_grad_bf16(bool vec, int k, int form, bool one);
 NormKernel<GradArgs> norm_grad_f32(bool vec, int k, int form, bool one);
+// The two for rows above 8192 columns (lst_norm_split.cuh): columns of a CTA of the second one,
+// 8 a thread, and CTAs of an SM.
+constexpr int kSplitTile = 1024;
+constexpr int split_ctas(bool vec) { return vec ? 4 : 8; }
+struct SplitKernels {
+  NormKernel<GradArgs> stats, apply;
+};
+SplitKernels norm_split_bf16(bool vec);
+SplitKernels norm_split_f32(bool vec);
 cudaError_t norm_grad_bf16_take_error(int* out);
 cudaError_t norm_grad_f32_take_error(int* out);
 

@@ -9,19 +9,6 @@ namespace {
 
 __device__ int g_norm_grad_error;
 
-// A unit of a row of parameter gradients that starts at element `at`.
-template <bool VEC, int P>
-__device__ __forceinline__ void store_sums(void* p, int64_t at, bool f32, bool accumulate, const Cols<VEC>& c, int k, const Part<P>& u, int i0 = 0) {
-  if (VEC && !accumulate && (reinterpret_cast<uintptr_t>(p) + at * (f32 ? 4 : 2)) % 16 == 0) {
-    if (f32)
-      c.store(static_cast<float*>(p) + at, k, u, i0);
-    else
-      c.store(static_cast<__nv_bfloat16*>(p) + at, k, u, i0);
-  } else {
-    for_each(c, k, u, [&](uint32_t col, float v) { store_sum(p, at + col, f32, accumulate, v); }, i0);
-  }
-}
-
 // The sums of a gate row, or of all of the CTA's rows, to the workspace (or to dgate where
 // the CTA has all of a gate row's tokens). With one gate row, or none, that is A as it is,
 // from which the join forms dw_post and dgate.
@@ -105,12 +92,12 @@ __device__ __forceinline__ void flush_sums(const GradArgs& a, const P& p, const 
 // norms' statistics at once, for D is linear in dh, m and h:
 //   sum e y = b (sum dh q + rho (sum m q - rho^2 mean(m h) sum h q)),
 // so a row needs one barrier instead of two. Its roundings are those of D's own terms.
-// This kernel takes whatever the call has.
-template <class T, bool VEC, int K, bool STAGED>
+// This kernel takes whatever the call has, up to 8192 columns.
+template <class T, bool VEC, int K>
 __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   let_next_start();
-  Pipe<GRAD_OPS, STAGED> p(a.pipe, smem);
+  Pipe<GRAD_OPS> p(a.pipe, smem);
   wait_for_previous();
   p.start(VEC && a.pipe.pad);
   const int group = threadIdx.x / a.pipe.group, tid = threadIdx.x - group * a.pipe.group, warp = tid >> 5, warps = a.pipe.group >> 5;
@@ -124,10 +111,9 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
   const bool token = a.pipe.in[GRAD_GATE].p != nullptr;  // a gate per token
   float* const words = p.words() + group * warps * 8;
   int turn = 0;
-  // weights as fp32 in shared memory, where registers would spill; K = 4 reads them again for every row
-  constexpr bool kHold = K <= 2;
-  constexpr bool kPadded = VEC && STAGED;  // units behind the row are zeros there: only stores pass over them
-  const int columns = kPadded ? 8 * K * a.pipe.group : hidden;
+  // weights as fp32 in shared memory, where registers would spill; on the vector path units
+  // behind the row are zeros there: only stores pass over them
+  const int columns = VEC ? 8 * K * a.pipe.group : hidden;
   float* const group_sums = reinterpret_cast<float*>(smem + kPipeHeader + a.pipe.stages * p.stage_bytes);
   float* const held_pre = group_sums + (a.pipe.groups > 1 ? a.pipe.groups * 2 * columns : 0);
   float* const held_gw = held_pre + columns;
@@ -150,24 +136,22 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
   for (int k = 0; k < K; ++k) sum_pre[k].fill(0.0f), sum_a[k].fill(0.0f);
   bool first_flush = true;
   do {
-    if (kHold) {
-      // each thread the columns that it reads itself, or one group for all
-      if (a.pipe.groups > 1) asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
-      if (group == 0) {
+    // each thread the columns that it reads itself, or one group for all
+    if (a.pipe.groups > 1) asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
+    if (group == 0) {
 #pragma unroll
-        for (int q = 0; q < 2 * K; ++q) {
-          const int k = q >> 1, i0 = 4 * (q & 1);
-          Half u;
-          u.fill(0.0f);
-          if (has_z && c.has(k)) load_pre(k, u, i0);
-          c.store(held_pre, k, u, i0);
-          u.fill(0.0f);
-          if (c.has(k)) load_gw(p.row, k, u, i0);
-          c.store(held_gw, k, u, i0);
-        }
+      for (int q = 0; q < 2 * K; ++q) {
+        const int k = q >> 1, i0 = 4 * (q & 1);
+        Half u;
+        u.fill(0.0f);
+        if (has_z && c.has(k)) load_pre(k, u, i0);
+        c.store(held_pre, k, u, i0);
+        u.fill(0.0f);
+        if (c.has(k)) load_gw(p.row, k, u, i0);
+        c.store(held_gw, k, u, i0);
       }
-      if (a.pipe.groups > 1) asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
     }
+    if (a.pipe.groups > 1) asm volatile("bar.sync 15, %0;" ::"r"(blockDim.x) : "memory");
     int rows;
     do {
       rows = p.rows();
@@ -175,18 +159,6 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
       p.wait();
       if (group < rows) {
         const int64_t row = static_cast<uint32_t>(p.row) + group;
-        auto pre_unit = [&](int k, int i0, Half& u) {
-          if (kHold)
-            c.load(held_pre, k, u, i0);
-          else
-            load_pre(k, u, i0);
-        };
-        auto gw_unit = [&](int k, int i0, Half& u) {
-          if (kHold)
-            c.load(held_gw, k, u, i0);
-          else
-            load_gw(p.row + group, k, u, i0);
-        };
         const uint8_t* const staged = p.staged(group);
         T *const dx_row = row_of<T>(a.dx, row), *const dy_row = row_of<T>(a.dy, row);
         const T* const dh_row = reinterpret_cast<const T*>(p.at(GRAD_DH, group, staged, VEC));
@@ -212,11 +184,10 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
 #pragma unroll
           for (int q = 0; q < 2 * K; ++q) {
             const int k = q >> 1, i0 = 4 * (q & 1);
-            if (!kPadded && !c.has(k)) continue;
             if (!VEC) asm volatile("" ::: "memory");  // what is loaded of more columns at once would spill
             Half w, d;
             if (has_z) {
-              pre_unit(k, i0, w);
+              c.load(held_pre, k, w, i0);
               c.load(dz_row, k, m, i0);
               either(GRAD_H, h_kept, k, i0, h);
 #pragma unroll
@@ -228,7 +199,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
             }
             if (has_post) {
               either(GRAD_Y, y_kept, k, i0, y);
-              gw_unit(k, i0, w);
+              c.load(held_gw, k, w, i0);
               if (token) gate_unit(k, i0, g);
               if (has_dh) c.load(dh_row, k, d, i0);
 #pragma unroll
@@ -257,7 +228,6 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
         for (int q = 0; q < 2 * K; ++q) {
           const int k = q >> 1, i0 = 4 * (q & 1), j0 = i0 / 2;
           const bool there = c.has(k);
-          if (!kPadded && !there) continue;
           if (!VEC) asm volatile("" ::: "memory");
           Half w, d, out;
           if (has_dh)
@@ -265,7 +235,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
           else
             d.fill(0.0f);
           if (has_z) {
-            pre_unit(k, i0, w);
+            c.load(held_pre, k, w, i0);
             c.load(dz_row, k, m, i0);
             either(GRAD_H, h_kept, k, i0, h);
 #pragma unroll
@@ -281,7 +251,7 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
             if (there) c.store(dx_row, k, out, i0);
           }
           if (has_y) either(GRAD_Y, y_kept, k, i0, y);
-          gw_unit(k, i0, w);
+          c.load(held_gw, k, w, i0);
           if (token) gate_unit(k, i0, g);
 #pragma unroll
           for (int j = 0; j < 2; ++j) d.v[j] = mul2(d.v[j], tau_beta);
@@ -341,7 +311,7 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
   constexpr int K = 2;
   extern __shared__ __align__(16) uint8_t smem[];
   let_next_start();
-  Pipe<GRAD_OPS, true, false> p(a.pipe, smem);
+  Pipe<GRAD_OPS, false> p(a.pipe, smem);
   wait_for_previous();
   p.start(a.pipe.pad);
   const int group = ONE ? 0 : threadIdx.x / a.pipe.group, tid = threadIdx.x - group * a.pipe.group, warp = tid >> 5, warps = a.pipe.group >> 5;

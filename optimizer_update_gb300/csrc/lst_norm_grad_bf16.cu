@@ -1,5 +1,6 @@
 // The backward kernel of the residual norm for bf16 activations.
 #include "lst_norm_grad.cuh"
+#include "lst_norm_split.cuh"
 
 namespace lst {
 
@@ -17,9 +18,14 @@ NormKernel<GradArgs> rows_kernel(int block, int kept) {
 }  // namespace
 
 NormKernel<GradArgs> norm_grad_bf16(bool vec, int k, int form, bool one) {
-  if (vec && k == 2 && form) return one ? rows_kernel<true>((form - 1) / 3, (form - 1) % 3) : rows_kernel<false>((form - 1) / 3, (form - 1) % 3);
-  if (vec) return k == 4 ? norm_grad_kernel<__nv_bfloat16, true, 4, false> : norm_grad_kernel<__nv_bfloat16, true, 2, true>;
-  return k == 4 ? norm_grad_kernel<__nv_bfloat16, false, 4, false> : k == 2 ? norm_grad_kernel<__nv_bfloat16, false, 2, true> : norm_grad_kernel<__nv_bfloat16, false, 1, true>;
+  if (form) return one ? rows_kernel<true>((form - 1) / 3, (form - 1) % 3) : rows_kernel<false>((form - 1) / 3, (form - 1) % 3);
+  if (vec) return norm_grad_kernel<__nv_bfloat16, true, 2>;
+  return k == 2 ? norm_grad_kernel<__nv_bfloat16, false, 2> : norm_grad_kernel<__nv_bfloat16, false, 1>;
+}
+
+SplitKernels norm_split_bf16(bool vec) {
+  return vec ? SplitKernels{norm_stats_kernel<__nv_bfloat16, true>, norm_apply_kernel<__nv_bfloat16, true>}
+             : SplitKernels{norm_stats_kernel<__nv_bfloat16, false>, norm_apply_kernel<__nv_bfloat16, false>};
 }
 
 cudaError_t norm_grad_bf16_take_error(int* out) { return take_norm_error(out); }

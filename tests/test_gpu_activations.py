@@ -429,6 +429,39 @@ def test_norm_grad_forms_of_whole_units(n, h, dtype, fmt, kw, dh):
         assert torch.equal(dx, got[0]) and torch.equal(dy, got[1])
 
 
+@pytest.mark.parametrize("n,h", [(40, 12), (7, 4100), (9, 8188), (5, 8196)])
+def test_norm_grad_rows_on_16_bytes_of_half_units(n, h):
+    p = Norm(n, h, "f32")
+    p.check_backward(p.x.double(), p.y.double(), p.backward(p.x, p.y))
+
+
+@pytest.mark.parametrize("h", [264, 4104, 9000])
+@pytest.mark.parametrize("fmt", [None, "i8"])
+def test_norm_grad_results_off_16_bytes(h, fmt):
+    """The inputs on 16 bytes, dx and dy not."""
+    p = Norm(40, h)
+    p.pad, p.shift = 3, 1  # of what new() gives
+    h_in, y_in = (v if fmt is None else checkpoint(v, fmt) for v in (p.x, p.y))
+    hv, yv = (v.double() if fmt is None else reference_checkpoint(v, fmt)[2] for v in (p.x, p.y))
+    p.check_backward(hv, yv, p.backward(h_in, y_in))
+
+
+@pytest.mark.parametrize("n,h,dtype,kw,dh", [
+    (700, 8200, "bf16", {}, True), (700, 8193, "bf16", dict(gate_rows=4), True), (160, 12288, "bf16", dict(gate_rows=160), True),
+    (160, 12289, "f32", dict(gate_rows=80, post=False), False), (161, 9000, "f32", dict(gate_rows=0, post=False), True),
+    (33, 16376, "bf16", dict(gate_rows=11), False), (1, 16384, "f32", {}, True), (1, 8201, "bf16", {}, False)])
+@pytest.mark.parametrize("fmt", [None, "i8", "e4m3"])
+def test_norm_grad_wide_rows(n, h, dtype, kw, dh, fmt):
+    p = Norm(n, h, dtype, **kw)
+    h_in, y_in = (v if fmt is None else checkpoint(v, fmt) for v in (p.x, p.y))
+    hv, yv = (v.double() if fmt is None else reference_checkpoint(v, fmt)[2] for v in (p.x, p.y))
+    got = p.backward(h_in, y_in, dh=dh)
+    p.check_backward(hv, yv, got, dh=dh)
+    again = p.backward(h_in, y_in, dh=dh)
+    assert all(a is b or torch.equal(a, b) for a, b in zip(got, again))
+    p.check_backward(None, yv, p.backward(None, y_in, dz=False), dz=False)
+
+
 @pytest.mark.parametrize("n,h", [(60, 40), (60, 2056), (700, 8), (900, 1), (40, 3), (333, 17), (50, 1032)])
 def test_norm_grad_of_ragged_rows_beside_other_bytes(n, h):
     """Rows of checkpoints that end inside 16 bytes, with e4m3 NaN behind them; rows of a byte or a few."""
