@@ -707,7 +707,8 @@ LST_API lst_status lst_residual_norm(const lst_matrix* x, const lst_matrix* y, c
    Every output may be null. dh, dz, dx, dy, and h and y as matrices, have one type. dgate, dw_post, dw_pre: shapes of gate, w_post, w_pre,
    bf16 or fp32 each, for instance their range of a block's G segment; with
    accumulate, added to what they hold (one rounding). Sums over tokens are fp32, in
-   an order that depends on the sizes alone. dx may be dh, dy may be dz.
+   an order that depends on sizes, alignment and the operands given, not on their
+   values or on the run. dx may be dh, dy may be dz.
    workspace: lst_residual_norm_grad_workspace_bytes(tokens, hidden, gate rows or 0)
    bytes, 256-byte aligned; that size serves fewer tokens and gate rows as well.
    Errors otherwise as lst_residual_norm. */
