@@ -84,7 +84,7 @@ struct OperandArgs {
   uint16_t* dy_out;
   int64_t dy_ld, dy_out_ld;
   int32_t dy_cols;
-  int32_t parts;  // 2: X as a sum of two bf16 parts, the second `rows` rows behind the first, and dy twice
+  int32_t parts;  // X as a sum of so many bf16 parts, each `rows` rows behind the one before
 };
 __device__ __forceinline__ void decode16(const uint4& q, uint32_t byte, bool e4m3, float2 (&v)[8]) {
   const float2 step = both(ckpt_step(byte));
@@ -103,21 +103,24 @@ __device__ __forceinline__ void decode16(const uint4& q, uint32_t byte, bool e4m
 __device__ __forceinline__ void restore16(const uint8_t* data, const uint8_t* scales, bool e4m3, int col, float2 (&v)[8]) {
   decode16(*reinterpret_cast<const uint4*>(data + col), scales[col / kCkptBlock], e4m3, v);
 }
-// v rho as bf16; with `rest`, what that leaves as bf16 there.
-__device__ __forceinline__ void store16(uint16_t* p, const float2 (&v)[8], float2 rho, uint16_t* rest) {
-  uint32_t w[8], l[8];
+// v rho as a sum of bf16 parts, `pitch` elements from one to the next.
+__device__ __forceinline__ void store16(uint16_t* p, const float2 (&v)[8], float2 rho, int parts, int64_t pitch) {
+  float2 x[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 x = mul2(v[j], rho);
-    w[j] = pack_bf16(x);
-    const float2 hi = unpack_bf16(w[j]);
-    l[j] = pack_bf16(make_float2(x.x - hi.x, x.y - hi.y));
+  for (int j = 0; j < 8; ++j) x[j] = mul2(v[j], rho);
+  for (;; p += pitch) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = pack_bf16(x[j]);
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (--parts <= 0) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 hi = unpack_bf16(w[j]);
+      x[j] = make_float2(x[j].x - hi.x, x[j].y - hi.y);
+    }
   }
-  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  if (!rest) return;
-  reinterpret_cast<uint4*>(rest)[0] = make_uint4(l[0], l[1], l[2], l[3]);
-  reinterpret_cast<uint4*>(rest)[1] = make_uint4(l[4], l[5], l[6], l[7]);
 }
 template <bool NORM>
 __global__ void __launch_bounds__(256, NORM ? 2 : 5) operand_kernel(const __grid_constant__ OperandArgs a) {
@@ -132,9 +135,8 @@ __global__ void __launch_bounds__(256, NORM ? 2 : 5) operand_kernel(const __grid
         uint32_t v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 8 * u + i < a.dy_cols ? p[i] : 0u;
-        for (int part = 0; part < a.parts; ++part)
-          *reinterpret_cast<uint4*>(a.dy_out + (r + part * a.rows) * a.dy_out_ld + 8 * u) =
-              make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        *reinterpret_cast<uint4*>(a.dy_out + r * a.dy_out_ld + 8 * u) =
+            make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
       }
     return;
   }
@@ -144,7 +146,8 @@ __global__ void __launch_bounds__(256, NORM ? 2 : 5) operand_kernel(const __grid
     const bool mine = row < a.rows;  // whole warps; with 256 threads a row all of them
     const uint8_t *data = a.in.data + row * a.in.stride, *scales = a.in.scales + row * a.in.scale_stride;
     uint16_t* const x = a.x + row * a.x_ld;
-    uint16_t* const rest = NORM && a.parts > 1 ? x + a.rows * a.x_ld : nullptr;
+    const int parts = NORM ? a.parts : 1;
+    const int64_t pitch = a.rows * a.x_ld;
     float2 rho = both(1.0f);
     const bool once = a.cols <= 64 * a.threads;  // a thread's part of the row stays in registers
     float2 v[NORM ? 4 : 1][8];
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(256, NORM ? 2 : 5) operand_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int col = 16 * (tid + i * a.threads);
-          if (col < a.cols) store16(x + col, v[NORM ? i : 0], rho, rest ? rest + col : nullptr);
+          if (col < a.cols) store16(x + col, v[NORM ? i : 0], rho, parts, pitch);
         }
         continue;
       }
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(256, NORM ? 2 : 5) operand_kernel(const __grid
 #pragma unroll 2
     for (int col = 16 * tid; col < a.cols; col += 16 * a.threads) {
       restore16(data, scales, a.in.e4m3, col, v[0]);
-      store16(x + col, v[0], rho, rest ? rest + col : nullptr);
+      store16(x + col, v[0], rho, parts, pitch);
     }
   }
 }
@@ -306,26 +309,29 @@ bool wgrad_sizes_fit(int64_t n, int64_t o, int64_t h) {
          o <= most / h;
 }
 
-// Normed rows of up to so many tokens go into the product as sums of two bf16 parts, with dy
-// twice: one part alone leaves 2^-9 (RMS 0.0016) of each row, as much again as the result's
-// own rounding. Averages over more tokens keep both at that; twice the products would be
-// most of their time.
-constexpr int64_t kTwoParts = 512;
+// Normed rows go into the product as sums of bf16 parts, each with all of dy: two for a bf16
+// result (2^-16 of a value is left, far below the result's own rounding), three for fp32 (all 24
+// bits). One part would leave up to 2^-8 of every value, which no number of tokens averages out
+// of the result's relative error. Values as they are kept are exact in one.
+// 4096 x 256 x 2048: 26 us with two parts and 35 with three, 20 with one, whose bf16 result was
+// off by 0.0024 (0.0017 is its rounding) and whose fp32 one by 0.0017, with three 4e-6 (the sums
+// on the tensor cores); 8192 x 11008 x 4096: 832 and 1304 us, 452 with one.
+int wgrad_parts(bool norm, const lst_matrix* dw) { return !norm ? 1 : dw->dtype == LST_F32 ? 3 : 2; }
 
 struct WgradPlan {
-  int64_t tokens, splits, part_ld, dy_ld, x_ld, dy_off, x_off, part_off, bytes;  // tokens: rows of the product's operands
+  int64_t blocks, splits, part_ld, dy_ld, x_ld, dy_off, x_off, part_off, bytes;  // blocks: steps of 64 tokens of the product
 };
 // Sums are split where tiles of 128 columns leave half of the 76 CTA pairs idle, into ranges of
-// at least 8 steps of 64 tokens. Sizes of memory are those of any smaller count, too.
-int64_t wgrad_splits(int64_t tokens, int64_t o, int64_t h) {
+// at least 8 steps. Sizes of memory are those of any smaller count, too, with or without a norm.
+int64_t wgrad_splits(int64_t blocks, int64_t o, int64_t h) {
   const int64_t tiles = ops_ceil_div(o, kGemmTile) * ops_ceil_div(h, kGemmTile / 2);
-  return std::max<int64_t>(1, std::min<int64_t>(ops_ceil_div(tokens, 64) / 8, 76 / tiles));
+  return std::max<int64_t>(1, std::min<int64_t>(blocks / 8, 76 / tiles));
 }
-WgradPlan wgrad_plan(const lst_matrix* dy, const lst_checkpoint* c, bool norm) {
+WgradPlan wgrad_plan(const lst_matrix* dy, const lst_checkpoint* c, const lst_matrix* dw, bool norm) {
   WgradPlan p;
-  const int64_t n = dy->rows, o = dy->cols, h = c->cols;
-  p.tokens = norm && n <= kTwoParts ? 2 * n : n;
-  p.splits = wgrad_splits(p.tokens, o, h);
+  const int64_t n = dy->rows, o = dy->cols, h = c->cols, most = wgrad_parts(true, dw);
+  p.blocks = wgrad_parts(norm, dw) * ops_ceil_div(n, 64);
+  p.splits = wgrad_splits(p.blocks, o, h);
   p.part_ld = ops_round_up(h, 32);
   p.dy_ld = ops_round_up(o, 8);
   p.x_ld = ops_round_up(h, 16);
@@ -335,9 +341,9 @@ WgradPlan wgrad_plan(const lst_matrix* dy, const lst_checkpoint* c, bool norm) {
     at += ops_round_up(size, 256);
     return off;
   };
-  const int64_t twice = 2 * std::min(n, kTwoParts), most = std::max(n, twice), splits = wgrad_splits(most, o, h);
-  p.dy_off = take((tile_rows(dy) ? twice : most) * p.dy_ld * 2);
-  p.x_off = take(most * p.x_ld * 2);
+  const int64_t splits = wgrad_splits(most * ops_ceil_div(n, 64), o, h);
+  p.dy_off = take(tile_rows(dy) ? 0 : n * p.dy_ld * 2);
+  p.x_off = take(most * n * p.x_ld * 2);
   p.part_off = take(splits > 1 ? splits * o * p.part_ld * 4 : 0);
   p.bytes = at;
   return p;
@@ -377,7 +383,7 @@ extern "C" int64_t lst_checkpoint_wgrad_workspace_bytes(const lst_matrix* dy, co
   if (!dy || !c || !dw || dy->rows != c->rows || dw->rows != dy->cols || dw->cols != c->cols ||
       !wgrad_sizes_fit(dy->rows, dy->cols, c->cols))
     return 0;
-  return wgrad_plan(dy, c, false).bytes;
+  return wgrad_plan(dy, c, dw, false).bytes;
 }
 
 extern "C" lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_checkpoint* c, const lst_matrix* norm_weight,
@@ -410,26 +416,28 @@ extern "C" lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_check
   const int64_t n = dy->rows, o = dy->cols, h = c->cols;
   if (!wgrad_sizes_fit(n, o, h))
     return fail(LST_ERR_INVALID_ARG, "%s: more than 2^24 tokens, or an operand of more than 2^40 elements", who);
-  const WgradPlan p = wgrad_plan(dy, c, norm_weight != nullptr);
+  const WgradPlan p = wgrad_plan(dy, c, dw, norm_weight != nullptr);
+  const int parts = wgrad_parts(norm_weight != nullptr, dw);
   LST_TRY(check_workspace(workspace, workspace_bytes, p.bytes, who));
   char* ws = static_cast<char*>(workspace);
-  const bool two = p.tokens > n, pack = two || !tile_rows(dy);
+  const bool pack = !tile_rows(dy);
   // a warp a row where there are rows for all of them, but normed rows are to stay in registers
   const int threads = h <= 1024 || (n >= kSms * 8 && (!norm_weight || h <= 2048)) ? 32 : 256;
   const int64_t row_blocks = std::min(ops_ceil_div(n, 256 / threads), kSms * 8);
   const OperandArgs x = {kept_arg(c), reinterpret_cast<uint16_t*>(ws + p.x_off), p.x_ld, n, static_cast<int32_t>(h),
                          threads, static_cast<int32_t>(row_blocks), eps, static_cast<const uint16_t*>(dy->data),
-                         reinterpret_cast<uint16_t*>(ws + p.dy_off), dy->stride, p.dy_ld, static_cast<int32_t>(o), two ? 2 : 1};
+                         reinterpret_cast<uint16_t*>(ws + p.dy_off), dy->stride, p.dy_ld, static_cast<int32_t>(o), parts};
   LST_TRY_CUDA(launch_chained(norm_weight ? operand_kernel<true> : operand_kernel<false>, dim3(static_cast<unsigned>(row_blocks + (pack ? std::min(n, kSms * 8) : 0))), dim3(256), 0, stream, x), who);
   GemmProblem g;
   if (pack)
-    g.a = {x.dy_out, o, p.tokens, p.dy_ld, true};
+    g.a = {x.dy_out, o, n, p.dy_ld, true};
   else
     g.a = {dy->data, o, n, dy->stride, true};
-  g.b = {x.x, h, p.tokens, p.x_ld, true};
+  g.b = {x.x, h, n, p.x_ld, true, parts, n * p.x_ld};
   g.m = o;
   g.n = h;
-  g.k = p.tokens;
+  g.k = p.blocks * 64;
+  g.parts = parts;
   g.splits = static_cast<int>(p.splits);
   const bool weight_f32 = norm_weight && norm_weight->dtype == LST_F32;
   const int vec = on16(dw) && dw->stride * dtype_bytes(dw->dtype) % 16 == 0 ? 16 : 2;
@@ -437,7 +445,7 @@ extern "C" lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_check
   if (p.splits > 1) g.wgrad.partial = {reinterpret_cast<float*>(ws + p.part_off), p.part_ld, o * p.part_ld, 0};
   LST_TRY_CUDA(launch_gemm(GEMM_BF16_WGRAD, &g, 1, stream), who);
   if (p.splits == 1) return LST_OK;
-  const int64_t blocks = ops_ceil_div(p.tokens, 64), splits = ops_ceil_div(blocks, ops_ceil_div(blocks, p.splits));
+  const int64_t splits = ops_ceil_div(p.blocks, ops_ceil_div(p.blocks, p.splits));
   const FinishArgs f = {g.wgrad.partial.out, p.part_ld, o * p.part_ld, g.wgrad.weight, dw->data, dw->stride, static_cast<int32_t>(splits),
                         weight_f32, dw->dtype == LST_F32, accumulate != 0, static_cast<int32_t>(h), o, vec};
   const int64_t quads = ops_ceil_div(h, 4);

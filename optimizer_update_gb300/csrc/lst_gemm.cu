@@ -48,6 +48,7 @@ struct Shape {
   int32_t symmetric;
   int32_t a_mn, b_mn;  // operand is MN-major in memory
   int32_t first_tile;
+  int32_t part_blocks;  // K blocks of a part of B
 };
 
 struct Nothing {};
@@ -870,7 +871,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t bytes = 2 * (half ? kStageBytes - kBBytes / 2 : kStageBytes);
         if (half) mb = &g.b_half[tile.problem];
         const bool a_mn = g.shape[tile.problem].a_mn, b_mn = g.shape[tile.problem].b_mn;
-        for (int kb = tile.kb0; kb < tile.kb1; ++kb) {
+        const int part_blocks = g.shape[tile.problem].part_blocks;
+        int kb = tile.kb0, of_b = tile.batch;  // K block, and matrix of B
+        for (; kb >= part_blocks; kb -= part_blocks) ++of_b;
+        for (int left = tile.kb1 - tile.kb0; left > 0; --left) {
           ok = tc::mbar_wait(empty + 8 * stage, phase ^ 1);
           if (!ok) break;
           const uint32_t sa = base + stage * kStageBytes, sb = sa + kABytes;
@@ -883,11 +887,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc::tma_load_3d_pair(sa, ma, bar, kb * kTileK, m0, tile.batch);
           }
           if (b_mn) {
-            tc::tma_load_3d_pair(sb, mb, bar, n0, kb * kTileK, tile.batch);
-            if (kTileN == 256 && !half) tc::tma_load_3d_pair(sb + kBBytes / 2, mb, bar, n0 + 64, kb * kTileK, tile.batch);
+            tc::tma_load_3d_pair(sb, mb, bar, n0, kb * kTileK, of_b);
+            if (kTileN == 256 && !half) tc::tma_load_3d_pair(sb + kBBytes / 2, mb, bar, n0 + 64, kb * kTileK, of_b);
           } else {
-            tc::tma_load_3d_pair(sb, mb, bar, kb * kTileK, n0, tile.batch);
+            tc::tma_load_3d_pair(sb, mb, bar, kb * kTileK, n0, of_b);
           }
+          if (++kb == part_blocks) kb = 0, ++of_b;
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
@@ -1071,6 +1076,7 @@ cudaError_t launch(const GemmProblem* problems, int count, cudaStream_t stream, 
     s.k_blocks = static_cast<int32_t>(ceil_div(p.k, kTileK));
     s.k_per_split = static_cast<int32_t>(ceil_div(s.k_blocks, p.splits));
     s.splits = static_cast<int32_t>(ceil_div(s.k_blocks, s.k_per_split));
+    s.part_blocks = s.k_blocks / p.parts;
     s.tiles_m = static_cast<int32_t>(ceil_div(p.m, kGemmTile));
     s.tiles_n = static_cast<int32_t>(ceil_div(p.n, kTileN));
     s.symmetric = p.symmetric;

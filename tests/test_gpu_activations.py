@@ -654,6 +654,29 @@ def test_wgrad_normed_of_few_tokens_is_near():
     within(dw, (dy.double().T @ v) * weight.double(), (2.0 ** -16 + ROW + 2 * (2 * n + 64) * U32) * size, "dw")
 
 
+@pytest.mark.parametrize("n", [64, 513, 1000, 3001])
+@pytest.mark.parametrize("out,accumulate", [("bf16", False), ("f32", False), ("f32", True)])
+@pytest.mark.parametrize("terms", [1, None])
+def test_wgrad_normed_is_near_for_any_count(n, out, accumulate, terms):
+    """What the parts leave of a value (two 2^-15 at most, three nothing), the statistic's error and the sums' over all
+    parts; then the result's own rounding. With one token per output the sums are three terms and zeros, so that what is
+    left of a value shows."""
+    o, h = 300, 264
+    g = gen(n)
+    dy, x = randn(g, n, o, dtype="bf16"), randn(g, n, h, dtype="bf16")
+    if terms:
+        dy *= torch.arange(n, device="cuda")[:, None] == torch.randint(0, n, (1, o), generator=g, device="cuda")
+    weight, before = 1 + randn(g, 1, h, std=0.3), randn(g, o, h, dtype=out)
+    dw = wgrad(dy, checkpoint(x, "i8"), weight, before.clone(), accumulate)
+    v = reference_checkpoint(x, "i8")[2]
+    v = v * (v.square().mean(1, keepdim=True) + EPS).rsqrt()
+    size, exact = (dy.double().abs().T @ v.abs()) * weight.double().abs(), (dy.double().T @ v) * weight.double()
+    if accumulate:
+        exact = exact + before.double()
+    left = 2.0 ** -15 if out == "bf16" else 0.0
+    within(dw, exact, (left + ROW + 2 * (3 * (terms or n) + 64) * U32) * size + (U[DT[out]] + 2 * U32) * exact.abs(), "dw")
+
+
 @pytest.mark.parametrize("n,o,h,norm", [(200, 4096, 5120, None), (1100, 5000, 4000, "bf16"), (70, 20000, 1300, None)])
 def test_wgrad_more_tiles_than_pairs(n, o, h, norm):
     check_wgrad(n, o, h, norm=norm)
