@@ -729,7 +729,7 @@ LST_API lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_matrix
    range of a block's G segment; added to what it holds when accumulate is set (one
    rounding). Products on the tensor cores with fp32 sums over bf16 operands: exact
    for values as they are kept; a normed row, before its weight, is taken as a sum of
-   bf16 parts, two for a bf16 dw (which leave 2^-16 of a value) and three for fp32
+   bf16 parts, two for a bf16 dw (which leave 2^-15 of a value) and three for fp32
    (which leave nothing), and the weight multiplies the fp32 sums.
    dw is zero (or as it was) for no tokens. eps > 0 is read only with norm_weight.
    workspace: lst_checkpoint_wgrad_workspace_bytes() bytes for the operands as they

@@ -103,22 +103,29 @@ __device__ __forceinline__ void decode16(const uint4& q, uint32_t byte, bool e4m
 __device__ __forceinline__ void restore16(const uint8_t* data, const uint8_t* scales, bool e4m3, int col, float2 (&v)[8]) {
   decode16(*reinterpret_cast<const uint4*>(data + col), scales[col / kCkptBlock], e4m3, v);
 }
-// v rho as a sum of bf16 parts, `pitch` elements from one to the next.
+// v rho as a sum of bf16 parts, `pitch` elements from one to the next: all but the last cut
+// off behind their 8 bits, so that every part has the value's sign. Parts of a value other than
+// zero are none of them zero, either (but 2^-133), so that an infinite dy times the parts is an
+// infinity as the value itself gives it, not inf - inf or inf * 0.
 __device__ __forceinline__ void store16(uint16_t* p, const float2 (&v)[8], float2 rho, int parts, int64_t pitch) {
   float2 x[8];
+  uint32_t w[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = mul2(v[j], rho);
+  for (int j = 0; j < 8; ++j) x[j] = mul2(v[j], rho), w[j] = 0;
   for (;; p += pitch) {
-    uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = pack_bf16(x[j]);
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t cut = __byte_perm(__float_as_uint(x[j].x), __float_as_uint(x[j].y), 0x7632);
+      const uint32_t part = parts > 1 ? cut : pack_bf16(x[j]), before = w[j];
+      w[j] = part | (!(part & 0x7fffu) && (before & 0x7fffu) ? 1u : 0u) | (!(part & 0x7fff0000u) && (before & 0x7fff0000u) ? 0x10000u : 0u);
+    }
     reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
     reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     if (--parts <= 0) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float2 hi = unpack_bf16(w[j]);
-      x[j] = make_float2(x[j].x - hi.x, x[j].y - hi.y);
+      x[j] = make_float2(copysignf(x[j].x - hi.x, x[j].x), copysignf(x[j].y - hi.y, x[j].y));
     }
   }
 }
@@ -310,7 +317,7 @@ bool wgrad_sizes_fit(int64_t n, int64_t o, int64_t h) {
 }
 
 // Normed rows go into the product as sums of bf16 parts, each with all of dy: two for a bf16
-// result (2^-16 of a value is left, far below the result's own rounding), three for fp32 (all 24
+// result (2^-15 of a value is left at most, far below the result's own rounding), three for fp32 (all 24
 // bits). One part would leave up to 2^-8 of every value, which no number of tokens averages out
 // of the result's relative error. Values as they are kept are exact in one.
 // 4096 x 256 x 2048: 26 us with two parts and 35 with three, 20 with one, whose bf16 result was

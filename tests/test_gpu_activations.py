@@ -718,6 +718,31 @@ def test_wgrad_non_finite_blocks_stay_in_their_columns(norm):
     assert torch.isnan(dw[:, bad]).all() and torch.isfinite(dw[:, ~bad]).all()
 
 
+@pytest.mark.parametrize("n", [40, 700])
+@pytest.mark.parametrize("norm,out", [(False, "bf16"), (True, "bf16"), (True, "f32")])
+def test_wgrad_infinities_of_dy(n, norm, out):
+    """An infinity in dy gives what it gives in the formula: infinities of the values' signs, NaN times a zero, NaN
+    where two of them differ."""
+    o, h = 48, 2056
+    g = gen(n)
+    dy, x = randn(g, n, o, dtype="bf16"), randn(g, n, h, dtype="bf16")
+    x[3, 1000:1100] = 0.0
+    dy[3, 5], dy[7, 6], dy[n - 1, 9], dy[2, 9], dy[1, 11] = float("inf"), -float("inf"), float("inf"), float("inf"), float("nan")
+    weight = 1 + 0.1 * torch.rand(1, h, generator=g, device="cuda") if norm else None
+    c = checkpoint(x, "i8")
+    dw = wgrad(dy, c, weight, torch.empty(o, h, dtype=DT[out], device="cuda"), False)
+    v = reference_checkpoint(x, "i8")[2]
+    if norm:
+        v = v * (v.square().mean(1, keepdim=True) + EPS).rsqrt() * weight.double()
+    exact = dy.double().T @ v
+    for bad in (torch.isnan, torch.isposinf, torch.isneginf):
+        assert torch.equal(bad(dw), bad(exact))
+    assert torch.isfinite(dw[[i for i in range(o) if i not in (5, 6, 9, 11)]]).all()
+    zero = checkpoint(torch.zeros_like(x), "i8")  # all parts of a zero are zero
+    dy = torch.full_like(dy, 3.0e38)
+    assert not wgrad(dy, zero, weight, torch.full_like(dw, 7.0), False).any()
+
+
 def test_wgrad_zero_rows_and_largest_values():
     """Rows of zeros; values near the ends of bf16's range, whose products stay in fp32's."""
     n, o, h = 128, 64, 96
