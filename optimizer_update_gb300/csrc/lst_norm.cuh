@@ -101,6 +101,7 @@ __device__ __forceinline__ void fill_rounded(const PipeArgs<OPS>& a, int ahead, 
     bytes += ((low & 15) + r.bytes + 15) & ~15;
   }
   bytes = __reduce_add_sync(0xffffffffu, bytes);
+  tc::fence_async_proxy_cta();  // lanes' bytes of the stage's last use, which may have been fill_ragged's, before these copies
   if (lane == 0) tc::mbar_expect_tx(bar, bytes);
   __syncwarp();
   for (int i = 0; i < n && mine; ++i) {
@@ -123,7 +124,7 @@ __device__ __forceinline__ void fill_ragged(const PipeArgs<OPS>& a, int ahead, i
   }
   bytes = __reduce_add_sync(0xffffffffu, bytes);
   edges = __any_sync(0xffffffffu, edges);
-  if (edges) tc::fence_async_proxy_cta();  // lanes' bytes of the stage's last use before this one's copies
+  tc::fence_async_proxy_cta();  // lanes' bytes of the stage's last use before this one's copies, whether or not it has such bytes itself
   if (lane == 0) tc::mbar_expect_tx(bar, bytes);
   __syncwarp();
   for (int i = lane; i < pieces; i += 32) {

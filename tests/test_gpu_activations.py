@@ -332,6 +332,23 @@ def test_norm_writes_the_checkpoints(n, h, dtype, pad, fmt):
     assert torch.equal(again[0], h8[0]) and torch.equal(again[1], h8[1])
 
 
+@pytest.mark.parametrize("n,h,dtype,kw", [
+    (30000, 33, "bf16", {}), (15000, 777, "bf16", dict(pad=3, shift=1)), (7300, 2047, "f32", {}), (4000, 4095, "bf16", dict(gate_rows=4000)),
+    (20000, 264, "bf16", dict(pad=1)), (15000, 770, "f32", dict(gate_rows=5))])
+def test_norm_odd_rows_over_many_turns(n, h, dtype, kw):
+    """Rows off 16 bytes, eight or more turns of every CTA: its stages are filled again several times, the first rows' and
+    the last ones' byte by byte, those between by whole pieces."""
+    p = Norm(n, h, dtype, **kw)
+    hh, z = p.forward()
+    p.check_forward(hh, z)
+    p.check_backward(p.x.double(), p.y.double(), p.backward(p.x, p.y))
+    h8, y8 = ((*lst.checkpoint_buffers(n, h), f) for f in ("i8", "e4m3"))
+    again, z_again = p.forward(h8, y8)
+    assert torch.equal(again, hh) and torch.equal(z_again, z)
+    for c, source in ((h8, hh), (y8, p.y)):
+        assert all(torch.equal(a, b) for a, b in zip(c[:2], checkpoint(source, c[2])[:2]))
+
+
 def test_norm_in_place():
     p = Norm(50, 300)
     h, z = p.forward()
