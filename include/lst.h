@@ -684,8 +684,9 @@ LST_API lst_status lst_checkpoint_restore(const lst_checkpoint* c, const lst_mat
    h may be null where only z or h8 is wanted; z and w_pre are both null or neither.
    Everything is formed in fp32 and each result rounded once (z from the unrounded
    h). h may be x, and z may be y (the same memory and stride); other outputs may
-   not overlap anything. Sums of squares are fp32: rows whose mean square leaves
-   its range (an rms above 2^63 or so) give z = 0, as an infinite one would.
+   not overlap anything. Sums of squares are fp32: where a row's leaves its range
+   (rms * sqrt(hidden) of 2^64 or more), the norm is zero (z, or u), as if it were
+   infinite.
    h8, y8: where not null, the checkpoints of h (as h's type holds it) and of y,
    bit for bit what lst_checkpoint_save gives.
    hidden is at most 16384; eps > 0, scales finite. Errors as lst_checkpoint_save. */
@@ -708,7 +709,9 @@ LST_API lst_status lst_residual_norm(const lst_matrix* x, const lst_matrix* y, c
    bf16 or fp32 each, for instance their range of a block's G segment; with
    accumulate, added to what they hold (one rounding). Sums over tokens are fp32, in
    an order that depends on sizes, alignment and the operands given, not on their
-   values or on the run. dx may be dh, dy may be dz.
+   values or on the run. dx may be dh, dy may be dz. A norm whose row's sum of squares
+   left fp32's range has the gradient zero. Sums over a row of products of two among h,
+   gate * w_post * y, w_pre * dz and dh are fp32, too, and have to stay in its range.
    workspace: lst_residual_norm_grad_workspace_bytes(tokens, hidden, gate rows or 0)
    bytes, 256-byte aligned; that size serves fewer tokens and gate rows as well.
    Errors otherwise as lst_residual_norm. */

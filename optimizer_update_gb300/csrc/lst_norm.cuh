@@ -392,6 +392,21 @@ struct GradArgs {
   int32_t token, single;
 };
 
+// What the six sums of a row (the top of norm_grad_kernel) give.
+struct RowFactors {
+  float rho, back, tau, back_y;
+};
+__device__ __forceinline__ RowFactors row_factors(const float (&s)[8], float inverse, float eps, float beta, bool has_z, bool has_post) {
+  RowFactors f;
+  f.rho = has_z ? rsqrtf(s[0] * inverse + eps) : 0.0f, f.back = f.rho * f.rho * (s[1] * inverse);
+  f.tau = has_post ? rsqrtf(s[2] * inverse + eps) : 1.0f;
+  // where a sum of squares has overflowed its norm's gradient is zero, and sum h q, which may have
+  // overflowed with it, has no part in it
+  const float of_h = f.back == 0.0f || f.tau == 0.0f ? 0.0f : f.back * s[5];
+  f.back_y = has_post ? f.tau * f.tau * (beta * (s[3] + f.rho * (s[4] - of_h)) * inverse) : 0.0f;
+  return f;
+}
+
 // One value of a parameter gradient.
 __device__ __forceinline__ void store_sum(void* p, int64_t at, bool f32, bool accumulate, float v) {
   if (f32) {

@@ -220,10 +220,8 @@ __global__ void __maxnreg__(128) norm_grad_kernel(const __grid_constant__ GradAr
           group_sum8<6>(s, words, turn, warps, warp, 1 + group, a.pipe.group);
         }
         p.refill(false);
-        const float rho = has_z ? rsqrtf(s[0] * inverse + a.eps) : 0.0f, back = rho * rho * (s[1] * inverse);
-        const float tau = has_post ? rsqrtf(s[2] * inverse + a.eps) : 1.0f;
-        const float back_y = has_post ? tau * tau * (a.beta * (s[3] + rho * (s[4] - back * s[5])) * inverse) : 0.0f;
-        const float2 rho2 = both(rho), of_h = both(-rho * back), alpha = both(a.alpha), tau_beta = both(tau * a.beta), of_y = both(-tau * back_y);
+        const RowFactors f = row_factors(s, inverse, a.eps, a.beta, has_z, has_post);
+        const float2 rho2 = both(f.rho), of_h = both(-f.rho * f.back), alpha = both(a.alpha), tau_beta = both(f.tau * a.beta), of_y = both(-f.tau * f.back_y);
 #pragma unroll
         for (int q = 0; q < 2 * K; ++q) {
           const int k = q >> 1, i0 = 4 * (q & 1), j0 = i0 / 2;
@@ -404,10 +402,8 @@ __global__ void __maxnreg__(128) norm_grad_rows_kernel(const __grid_constant__ G
       asm volatile("" ::: "memory");  // what follows is read again
       if (mine) {
         const int64_t row = static_cast<uint32_t>(p.row) + group;
-        const float rho = rsqrtf(s[0] * inverse + a.eps), back = rho * rho * (s[1] * inverse);
-        const float tau = has_post ? rsqrtf(s[2] * inverse + a.eps) : 1.0f;
-        const float back_y = has_post ? tau * tau * (a.beta * (s[3] + rho * (s[4] - back * s[5])) * inverse) : 0.0f;
-        const float2 rho2 = both(rho), of_h = both(-rho * back), alpha = both(a.alpha), tau_beta = both(tau * a.beta), of_y = both(-tau * back_y);
+        const RowFactors f = row_factors(s, inverse, a.eps, a.beta, true, has_post);
+        const float2 rho2 = both(f.rho), of_h = both(-f.rho * f.back), alpha = both(a.alpha), tau_beta = both(f.tau * a.beta), of_y = both(-f.tau * f.back_y);
         T *const dx_out = row_of<T>(a.dx, row), *const dy_out = row_of<T>(a.dy, row);
 #pragma unroll
         for (int k = 0; k < K; ++k) {

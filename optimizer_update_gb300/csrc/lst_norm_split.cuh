@@ -88,10 +88,8 @@ __global__ void __launch_bounds__(256, 4) norm_stats_kernel(const __grid_constan
     for (int j = 0; j < 6; ++j) s[j] = s2[j].x + s2[j].y;
     group_sum8<6>(s, words, turn, 8, threadIdx.x >> 5, 1, 256);
     if (threadIdx.x == 0) {
-      const float rho = has_z ? rsqrtf(s[0] * inverse + a.eps) : 0.0f, back = rho * rho * (s[1] * inverse);
-      const float tau = has_post ? rsqrtf(s[2] * inverse + a.eps) : 1.0f;
-      const float back_y = has_post ? tau * tau * (a.beta * (s[3] + rho * (s[4] - back * s[5])) * inverse) : 0.0f;
-      a.stats[row] = make_float4(rho, -rho * back, tau * a.beta, -tau * back_y);
+      const RowFactors f = row_factors(s, inverse, a.eps, a.beta, has_z, has_post);
+      a.stats[row] = make_float4(f.rho, -f.rho * f.back, f.tau * a.beta, -f.tau * f.back_y);
     }
   }
 }

@@ -377,6 +377,48 @@ def test_norm_rows_of_zeros_and_non_finite_ones():
     assert torch.isfinite(dx[3]).all() and torch.isfinite(dy[3]).all()
 
 
+@pytest.mark.parametrize("h,dtype,gate_rows", [(4096, "bf16", 0), (4096, "f32", 1), (4096, "bf16", 16), (777, "bf16", 1), (16384, "bf16", 0), (12289, "f32", 1)])
+def test_norm_rows_beyond_fp32_squares(h, dtype, gate_rows):
+    """Rows of sizes 2^0 to 2^62, h and y pointing the same way, so that their product's sum overflows, too. Where a sum of
+    squares is 2^128 or more its norm and that norm's gradient are zero; the other rows are as ever."""
+    sizes = [(i, j) for i in (0, 40, 56, 62) for j in (0, 40, 56, 62)]
+    n = len(sizes)
+    p = Norm(n, h, dtype, gate_rows=gate_rows, beta=0.5)
+    if gate_rows:
+        p.gate.copy_(1 + 0.1 * p.gate.clamp(-4, 4))
+    scale = torch.tensor([[2.0 ** i, 2.0 ** j] for i, j in sizes], device="cuda")
+    p.y.copy_(p.x * scale[:, 1:])
+    p.x.mul_(scale[:, :1])
+
+    def inverse_rms(v):
+        squares = v.square().sum(1, keepdim=True)
+        assert not ((squares > 2.0 ** 127) & (squares < 2.0 ** 129)).any()
+        return torch.where(squares < 2.0 ** 128, (squares / h + EPS).rsqrt(), 0.0)
+
+    x, y, w_post, w_pre, dz, gate = p.x.double(), p.y.double(), p.w_post.double(), p.w_pre.double(), p.dz.double(), p.per_token(p.gate)
+    hh, z = p.forward()
+    u = 0.5 * gate * y * inverse_rms(y) * w_post
+    wide, size = x + u, x.abs() + u.abs()
+    within(hh, wide, U[p.t] * wide.abs() + 2 * ROW * size, "h")
+    rho = inverse_rms(wide)
+    share = 2 * ROW * size.norm(dim=1, keepdim=True) / wide.norm(dim=1, keepdim=True)
+    within(z, wide * rho * w_pre, ((U[p.t] + 2 * ROW + share) * wide.abs() + 2 * ROW * size) * rho * w_pre.abs(), "z")
+    # from x and y as they are
+    dx, dy, dgate, dw_post, dw_pre = p.backward(p.x, p.y)
+    rho, tau, m = inverse_rms(x), inverse_rms(y), dz * w_pre
+    d = p.dh.double() + rho * (m - x * rho * (m * x * rho).mean(1, keepdim=True))
+    size = p.dh.double().abs() + rho * (m.abs() + x.abs() * rho * (m * x * rho).abs().mean(1, keepdim=True))
+    within(dx, d, U[p.t] * d.abs() + 2 * ROW * size, "dx")
+    e, esize = 0.5 * d * gate * w_post, 0.5 * size * (gate * w_post).abs()
+    exact = tau * (e - y * tau * (e * y * tau).mean(1, keepdim=True))
+    esize = tau * (esize + y.abs() * tau * (esize * y.abs() * tau).mean(1, keepdim=True))
+    within(dy, exact, U[p.t] * exact.abs() + 4 * ROW * esize, "dy")
+    for name, g, t, most in (("dw_post", dw_post, 0.5 * d * gate * y * tau, 0.5 * size * gate * (y * tau).abs()), ("dw_pre", dw_pre, dz * x * rho, (dz * x * rho).abs())):
+        exact = t.sum(0, keepdim=True)
+        within(g, exact, (U[g.dtype] + U32) * exact.abs() + (4 * ROW + 2 * (n + 16) * U32) * most.sum(0, keepdim=True), name)
+    assert dgate is None or torch.isfinite(dgate).all()
+
+
 @pytest.mark.parametrize("n,h", SHAPES)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_norm_grad(n, h, dtype):
