@@ -738,8 +738,8 @@ LST_API lst_status lst_residual_norm_grad(const lst_matrix* dh, const lst_matrix
    workspace: lst_checkpoint_wgrad_workspace_bytes() bytes for the operands as they
    lie (rows of dy that do not all start on 16 bytes are copied there), 256-byte
    aligned; that size serves fewer tokens as well. 0 for sizes that the call refuses.
-   Errors as lst_checkpoint_save, plus LST_ERR_INVALID_ARG for more than 2^24 tokens
-   or operands of more than 2^40 elements. */
+   Errors as lst_checkpoint_save, plus LST_ERR_INVALID_ARG for more than 2^24 tokens,
+   dw of more than 2^31 - 2^14 rows or columns, or operands of more than 2^40 elements. */
 LST_API int64_t lst_checkpoint_wgrad_workspace_bytes(const lst_matrix* dy, const lst_checkpoint* c, const lst_matrix* dw);
 LST_API lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_checkpoint* c, const lst_matrix* norm_weight,
                                         float eps, const lst_matrix* dw, int32_t accumulate, void* workspace,

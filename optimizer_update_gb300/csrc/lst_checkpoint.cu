@@ -311,8 +311,9 @@ lst_status check_pair(const lst_matrix* m, const char* name, const lst_checkpoin
 }
 
 bool wgrad_sizes_fit(int64_t n, int64_t o, int64_t h) {
-  const int64_t most = int64_t(1) << 40;
-  return n > 0 && o > 0 && h > 0 && n <= (int64_t(1) << 24) && o <= INT32_MAX && h <= INT32_MAX && o <= most / n && h <= most / n &&
+  // the kernels step past the last column in 32 bits, by at most 16 columns of 256 threads
+  const int64_t most = int64_t(1) << 40, widest = (int64_t(1) << 31) - (1 << 14);
+  return n > 0 && o > 0 && h > 0 && n <= (int64_t(1) << 24) && o <= widest && h <= widest && o <= most / n && h <= most / n &&
          o <= most / h;
 }
 
@@ -422,7 +423,7 @@ extern "C" lst_status lst_checkpoint_wgrad(const lst_matrix* dy, const lst_check
   }
   const int64_t n = dy->rows, o = dy->cols, h = c->cols;
   if (!wgrad_sizes_fit(n, o, h))
-    return fail(LST_ERR_INVALID_ARG, "%s: more than 2^24 tokens, or an operand of more than 2^40 elements", who);
+    return fail(LST_ERR_INVALID_ARG, "%s: more than 2^24 tokens, 2^31 - 2^14 columns or outputs, or 2^40 elements of an operand", who);
   const WgradPlan p = wgrad_plan(dy, c, dw, norm_weight != nullptr);
   const int parts = wgrad_parts(norm_weight != nullptr, dw);
   LST_TRY(check_workspace(workspace, workspace_bytes, p.bytes, who));

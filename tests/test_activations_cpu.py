@@ -127,6 +127,18 @@ def test_wgrad_refusals(L):
     assert L.lst_checkpoint_wgrad_workspace_bytes(mat(L, 1100, o, data=P + 2), many, dw) > L.lst_checkpoint_wgrad_workspace_bytes(mat(L, 1100, o), many, dw)
 
 
+@pytest.mark.parametrize("o,h", [(1, (1 << 31) - 1), (1, (1 << 31) - 4096), (1, (1 << 31) - (1 << 14) + 1), ((1 << 31) - 1, 1), ((1 << 31) - 255, 8)])
+def test_wgrad_refuses_columns_that_32_bits_do_not_step_past(L, o, h):
+    """A thread's next column is up to 4096 further, a tile's last one up to 256, and both are 32-bit numbers."""
+    dy, c, dw = mat(L, 1, o), kept(L, 1, h), mat(L, o, h)
+    assert L.lst_checkpoint_wgrad_workspace_bytes(dy, c, dw) == 0
+    for norm in (None, mat(L, 1, h)):
+        refused(L, BAD, L.lst_checkpoint_wgrad, dy, c, norm, 1e-5, dw, False, P, 1 << 60)
+    widest = (1 << 31) - (1 << 14)
+    o, h = min(o, widest), min(h, widest)
+    assert L.lst_checkpoint_wgrad_workspace_bytes(mat(L, 1, o), kept(L, 1, h), mat(L, o, h)) > 0
+
+
 @pytest.mark.parametrize("o,h", [(1, 1), (256, 2048), (11008, 4096), (300, 777), (16, 12293)])
 def test_wgrad_workspace_serves_fewer_tokens(L, o, h):
     counts = sorted({max(1, (1 << i) + d) for i in range(17) for d in (-1, 0, 1, 100)})
