@@ -571,6 +571,47 @@ def test_norm_grad_accumulates(rows, n, wdtype):
     p.check_backward(p.x.double(), p.y.double(), got, before=before)
 
 
+@pytest.mark.parametrize("n,h,rows", [
+    (300, 2056, 1), (300, 2056, 3), (300, 2056, 300), (900, 2056, 450), (900, 4104, 1), (900, 4104, 300), (300, 4101, 3), (300, 8201, 1), (300, 8201, 3),
+    (300, 8201, 300), (600, 8201, 300), (300, 12288, 1), (300, 12288, 3), (300, 12288, 300), (600, 12288, 300), (90, 16384, 45)])
+@pytest.mark.parametrize("wdtype,fmt,shift", [("bf16", None, 0), ("f32", "i8", 0), ("bf16", "e4m3", 1)])
+def test_norm_grad_accumulates_in_every_form(n, h, rows, wdtype, fmt, shift):
+    """One row a CTA at a time and rows in two launches; gate rows of one CTA, of several, of every token; results on 16
+    bytes and off them."""
+    p = Norm(n, h, gate_rows=rows, wdtype=wdtype)
+    g = gen(9)
+    before = {k: strided(randn(g, r, h, dtype=wdtype, std=10.0), 0, shift) for k, r in (("dgate", rows), ("dw_post", 1), ("dw_pre", 1))}
+    h_in, y_in = (v if fmt is None else checkpoint(v, fmt) for v in (p.x, p.y))
+    hv, yv = (v.double() if fmt is None else reference_checkpoint(v, fmt)[2] for v in (p.x, p.y))
+    grads = [strided(before[k], 0, shift) for k in ("dgate", "dw_post", "dw_pre")]
+    got = p.backward(h_in, y_in, accumulate=True, grads=grads)
+    p.check_backward(hv, yv, got, before=before)
+
+
+@pytest.mark.parametrize("n,h,dtype,kw", [
+    (7000, 2056, "bf16", {}), (7000, 2048, "f32", dict(gate_rows=7)), (4000, 4096, "bf16", {}), (3000, 8192, "bf16", dict(gate_rows=0)),
+    (1600, 12288, "bf16", {}), (1600, 12288, "f32", dict(gate_rows=1600)), (1300, 16384, "bf16", dict(post=False)), (30000, 64, "bf16", dict(gate_rows=15)),
+    (20000, 264, "f32", dict(block=False, post=False, gate_rows=0)), (1500, 9001, "bf16", {})])
+def test_norm_over_many_turns(n, h, dtype, kw):
+    """Every CTA fills its stages again several times, and no two rows are alike; all results, with the checkpoints."""
+    p = Norm(n, h, dtype, **kw)
+    h8 = (*lst.checkpoint_buffers(n, h), "i8")
+    y8 = (*lst.checkpoint_buffers(n, h), "e4m3") if p.y is not None else None
+    hh, z = p.forward(h8, y8)
+    p.check_forward(hh, z)
+    for c, source in ((h8, hh), (y8, p.y)):
+        assert c is None or all(torch.equal(a, b) for a, b in zip(c[:2], checkpoint(source, c[2])[:2]))
+
+
+@pytest.mark.parametrize("n,h,kw", [(9000, 264, {}), (5000, 1032, dict(gate_rows=5)), (3000, 4096, {}), (1500, 8192, dict(gate_rows=3)), (1500, 8200, {}), (9000, 33, {})])
+@pytest.mark.parametrize("fmt", ["i8", "e4m3"])
+def test_norm_grad_of_a_matrix_and_a_checkpoint_over_many_turns(n, h, kw, fmt):
+    p = Norm(n, h, **kw)
+    h8, y8 = checkpoint(p.x, fmt), checkpoint(p.y, fmt)
+    p.check_backward(reference_checkpoint(p.x, fmt)[2], p.y.double(), p.backward(h8, p.y))
+    p.check_backward(p.x.double(), reference_checkpoint(p.y, fmt)[2], p.backward(p.x, y8))
+
+
 def test_norm_grad_in_place_and_again():
     p = Norm(900, 520)
     first = p.backward(p.x, p.y)
@@ -690,6 +731,13 @@ def test_wgrad(n, o, h, fmt):
 @pytest.mark.parametrize("n,o,h", [(100, 200, 264), (300, 333, 301), (3000, 40, 72)])
 def test_wgrad_forms(kw, n, o, h):
     check_wgrad(n, o, h, **kw)
+
+
+@pytest.mark.parametrize("n,o,h,dw_pad", [(300, 333, 301, 3), (900, 520, 301, 3), (300, 5000, 2047, 1), (2500, 300, 77, 3), (300, 333, 300, 4)])
+@pytest.mark.parametrize("kw", [dict(), dict(out="f32"), dict(norm="bf16"), dict(norm="f32", out="f32")])
+def test_wgrad_accumulates_where_rows_on_16_bytes_end_inside_them(n, o, h, dw_pad, kw):
+    check_wgrad(n, o, h, accumulate=True, dw_pad=dw_pad, **kw)
+    check_wgrad(n, o, h, accumulate=False, dw_pad=dw_pad, **kw)
 
 
 @pytest.mark.parametrize("n,o,h", [(1, 40, 300), (3, 256, 2048), (512, 300, 264), (513, 300, 264), (511, 64, 17000)])
