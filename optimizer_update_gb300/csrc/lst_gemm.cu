@@ -19,6 +19,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "lst_ops.h"
 #include "lst_tc.cuh"
@@ -48,7 +49,7 @@ struct Shape {
   int32_t symmetric;
   int32_t a_mn, b_mn;  // operand is MN-major in memory
   int32_t first_tile;
-  int32_t part_blocks;  // K blocks of a part of B
+  int32_t part_blocks;  // K blocks of a part of B (weight gradients)
 };
 
 struct Nothing {};
@@ -808,6 +809,7 @@ template <class Epi, bool kBf16, int kTileN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ Args<Epi> g) {
   constexpr int kBBytes = b_bytes(kTileN), kStageBytes = kABytes + kBBytes;
+  constexpr bool kParts = std::is_same<Epi, WgradEpilogue>::value;  // only weight gradients have B in parts
   constexpr uint32_t kTmemColumns = 2 * kTileN;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (tc::smem_addr(smem_raw) + 1023) & ~1023u;
@@ -871,10 +873,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t bytes = 2 * (half ? kStageBytes - kBBytes / 2 : kStageBytes);
         if (half) mb = &g.b_half[tile.problem];
         const bool a_mn = g.shape[tile.problem].a_mn, b_mn = g.shape[tile.problem].b_mn;
-        const int part_blocks = g.shape[tile.problem].part_blocks;
-        int kb = tile.kb0, of_b = tile.batch;  // K block, and matrix of B
-        for (; kb >= part_blocks; kb -= part_blocks) ++of_b;
-        for (int left = tile.kb1 - tile.kb0; left > 0; --left) {
+        for (int k = tile.kb0; k < tile.kb1; ++k) {
+          int kb = k, of_b = tile.batch;  // K block of both, and matrix of B
+          if (kParts)
+            for (; kb >= g.shape[tile.problem].part_blocks; kb -= g.shape[tile.problem].part_blocks) ++of_b;
           ok = tc::mbar_wait(empty + 8 * stage, phase ^ 1);
           if (!ok) break;
           const uint32_t sa = base + stage * kStageBytes, sb = sa + kABytes;
@@ -892,7 +894,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           } else {
             tc::tma_load_3d_pair(sb, mb, bar, kb * kTileK, n0, of_b);
           }
-          if (++kb == part_blocks) kb = 0, ++of_b;
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;

@@ -89,7 +89,8 @@ struct GemmProblem {
   int64_t m, n, k, batch = 1;
   bool symmetric = false;  // the result is symmetric: form one triangle of tiles and mirror it
   int splits = 1;          // K ranges (PartialParams)
-  int parts = 1;           // B as a sum of so many: k counts all, k / parts (a multiple of 64) each; a is read again for every part, part i of b is matrix i of its batch
+  int parts = 1;           // GEMM_BF16_WGRAD: B as a sum of so many, k / parts (a multiple of 64) deep each; a is
+                           // read again for every part, part i of b is matrix i of its batch
   StoreParams store{};
   PartialParams partial{};
   XentParams xent{};
