@@ -16,8 +16,13 @@
 // in order by a second launch. Rows above 8192 columns: lst_norm_split.cuh.
 //
 // Floors are memory's: 8 bytes an element forward, 12 backward in bf16 (10 with checkpoints).
-// Forward runs at 5.9 TB/s (16384 x 4096 with an 8-bit copy, 114 us). Backward runs at 4.9 TB/s
-// (16381 x 8192 from checkpoints, 273 us and 10 for the sums): some 45 instructions an
+// Forward runs at 5.3 TB/s (16384 x 4096 with an 8-bit copy, 114 us of 90; 5.8 without norm and
+// gate of the block): issue slots are 56 % in use, and what a warp waits for is shared memory (a
+// quarter of its cycles), arithmetic before it (a sixth) and the row's two barriers (another). Rows of
+// 6145 to 8192 columns leave one CTA an SM, whose 13 to 16 warps stand at those barriers together
+// (16384 x 8192: 243 us of 159); rows above hold 32 columns a thread, 9 to 16 warps an SM, and
+// read their weights from L2 for each (4096 x 12288: 171 of 60). Backward runs at 4.8 TB/s
+// (16381 x 8192 from checkpoints, 278 us and 7 for the sums): some 45 instructions an
 // element and 16 warps an SM, as many as 128 registers and the rows in flight leave.
 #include <algorithm>
 #include <cmath>
@@ -268,9 +273,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const __grid
 
 // ---- host ------------------------------------------------------------------------
 // 16 columns a thread (32 of rows above 8192), and short rows several at a time, so that a CTA
-// has about 256 threads, 512 where a row needs them. An SM holds 512 threads of the backward
+// has about 256 threads, 512 where a row needs them. An SM holds up to 512 threads of the backward
 // kernel and 768 of the forward one, as many as their registers allow (forward with 512: 157 us
-// for 16384 x 4096 with a checkpoint and its restore, with 1024 of 64 registers 184, so 155).
+// for 16384 x 4096 with a checkpoint and its restore, with 1024 of 64 registers 184, so 155), in
+// whole CTAs: forward 416 to 512 from 6145 to 8192 columns, 288 to 512 above.
 struct Fit {
   int k, group, groups, per_sm;
   int threads() const { return group * groups; }

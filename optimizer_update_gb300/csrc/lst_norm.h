@@ -5,8 +5,8 @@
 
 namespace lst {
 
-// Whether some wait of the backward kernel ran out since the last call on this
-// device (synchronises the device).
+// Whether some wait of the residual-norm kernels, forward or backward, ran out since
+// the last call on this device (synchronises the device).
 cudaError_t norm_take_error(int* out);
 
 }  // namespace lst

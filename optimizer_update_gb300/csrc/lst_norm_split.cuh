@@ -32,7 +32,8 @@ __device__ __forceinline__ void load_weight(const Weights& w, int64_t row, int c
 template <class T, bool VEC>
 __global__ void __launch_bounds__(256, 4) norm_stats_kernel(const __grid_constant__ GradArgs a) {
   __shared__ float words[256];
-  constexpr int P = VEC && sizeof(T) == 2 ? 4 : 2, kUnroll = P == 4 ? 1 : 2;  // 16 bytes a load; more at once would spill
+  // 16 bytes a load and operand at once, as much as the 64 registers of four CTAs an SM hold (bf16: but 68 bytes)
+  constexpr int P = VEC && sizeof(T) == 2 ? 4 : 2, kUnroll = P == 4 ? 1 : 2;
   let_next_start();
   wait_for_previous();
   const Cols<VEC> c = {threadIdx.x, 256u, static_cast<uint32_t>(a.pipe.hidden)};
@@ -97,7 +98,9 @@ __global__ void __launch_bounds__(256, 4) norm_stats_kernel(const __grid_constan
 // Tile blockIdx.x of the columns, rows first_row(blockIdx.y) on.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(kSplitTile / 8, split_ctas(VEC)) norm_apply_kernel(const __grid_constant__ GradArgs a) {
-  constexpr int P = VEC ? 4 : 2;  // pairs of columns at a time: single values of more would spill
+  // Pairs of columns at a time: whole units, of which 140 bytes a thread spill, or in single values halves of
+  // them, with twice the threads an SM on 64 registers and 544 bytes that spill.
+  constexpr int P = VEC ? 4 : 2;
   let_next_start();
   wait_for_previous();
   const int hidden = a.pipe.hidden, ld = (hidden + 3) & ~3, col0 = blockIdx.x * kSplitTile;
